@@ -88,7 +88,9 @@ extern "C" {
  *    pa_release_blocks, pa_mixed_workspace_size, pa_mixed_attention.
  * 4: pa_prefill_workspace_size, pa_prefill_chunk_balanced,
  *    pa_prefill_balanced_chosen, pa_test_prefill_schedule, pa_decode_append,
- *    pa_mixed_attention_append. */
+ *    pa_mixed_attention_append.
+ *    Added without a new version (nothing before them changed):
+ *    pa_rope_desc, pa_qk_norm_rope, pa_rope_cache_write. */
 #define PA_ABI_VERSION 4
 
 /* Symbols of the shared library; everything else in it stays hidden. */
@@ -238,6 +240,84 @@ PA_API const char *pa_last_error(void);
 PA_API pa_status pa_cache_write(const pa_kv_desc *desc, const void *k, const void *v, void *k_cache,
                          void *v_cache, const int64_t *slot_mapping, int32_t num_tokens,
                          pa_stream_t stream);
+
+/*
+ * Position rotation and per-head norms of queries and keys.  Zero-initialise,
+ * then set the fields; fields are only ever appended.
+ *   cos_sin      : device fp32 [max_position][rotary_dim], 16-byte aligned: row p
+ *                  holds the rotary_dim / 2 cosines, then the rotary_dim / 2
+ *                  sines, of position p.  A scaled rotation (any long-context
+ *                  scheme) is a table with its angles (and its magnitude
+ *                  factor) in it.
+ *   max_position : rows of cos_sin; positions lie in [0, max_position).
+ *   rotary_dim   : dims of a head that rotate, the first ones; a multiple of
+ *                  16, at most head_dim; 0 means head_dim.
+ *   interleaved  : 0: dim i rotates with dim i + rotary_dim / 2; 1: dim 2 i
+ *                  with dim 2 i + 1.
+ *   eps          : added to the mean square; finite and >= 0.
+ *   q_weight, k_weight : device [head_dim] weights of the per-head norms of
+ *                  queries and keys, in the activation type (bf16; fp16 with
+ *                  an fp16 cache), 16-byte aligned.  NULL: that side has no
+ *                  norm.
+ */
+typedef struct {
+  const float *cos_sin;
+  int32_t max_position;
+  int32_t rotary_dim;  /* 0: head_dim */
+  int32_t interleaved; /* 0: half split */
+  float eps;
+  const void *q_weight; /* NULL: no norm */
+  const void *k_weight; /* NULL: no norm */
+} pa_rope_desc;
+
+/*
+ * Per-head RMS norm of queries and keys, and their position rotation, in one
+ * pass (the norm and rotation of the "fused attention preamble" between a
+ * layer's projection and its attention).  Row x of token t and head h
+ * becomes
+ *   y = x * rsqrt(mean(x^2) + eps) * weight     (y = x without a weight)
+ * and its first rotary_dim dims are rotated by the angles of positions[t]:
+ *   y_i' = y_i cos_i - y_j sin_i,  y_j' = y_j cos_i + y_i sin_i
+ * for every pair (i, j) of rope->interleaved.  Arithmetic in fp32, one
+ * rounding to the activation type (bf16; fp16 with an fp16 cache).  The
+ * outputs are what pa_decode_append and pa_mixed_attention_append take as q
+ * and k_new, and the other entry points as q.
+ *   q, k         : [num_tokens][num_q_heads or num_kv_heads][head_dim], the
+ *                  heads of a token contiguous; q_stride / k_stride elements
+ *                  from one token to the next (a multiple of 8, 0: dense), so
+ *                  that both may lie inside one projection's output.
+ *   q_out, k_out : the same shapes, dense.  An output may be its own dense
+ *                  input (in place); it must not overlap the inputs otherwise.
+ *   positions    : int32 [num_tokens]
+ * Either side may be left out (q and q_out, or k and k_out, both NULL).
+ * Uses desc's heads, head_dim, kv_dtype (for the activation type),
+ * error_word and check_indices (a position out of range is reported and
+ * position 0 used).  num_tokens == 0 enqueues nothing and returns PA_OK.
+ */
+PA_API pa_status pa_qk_norm_rope(const pa_kv_desc *desc, const pa_rope_desc *rope, void *q_out, void *k_out,
+                                 const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                 const int32_t *positions, int32_t num_tokens, pa_stream_t stream);
+
+/*
+ * pa_qk_norm_rope with the keys and values going to their slots of the paged
+ * cache on the way (pa_cache_write's scatter): one pass from a projection's
+ * output to rotated queries and a written cache, for the attention calls
+ * that read the new tokens from the cache.
+ *   v            : [num_tokens][num_kv_heads][head_dim], v_stride elements
+ *                  from one token to the next (a multiple of 8, 0: dense);
+ *                  neither normed nor rotated.
+ *   slot_mapping : as in pa_cache_write; a token with a negative slot (padding)
+ *                  writes no cache row, its query is computed all the same.
+ * A 16-bit cache receives what pa_qk_norm_rope followed by pa_cache_write
+ * stores, bit for bit.  An 8-bit cache receives the keys encoded from their
+ * fp32 values (pa_cache_write's encoding, without the rounding to 16 bits
+ * that a k_out in between makes) and the values as pa_cache_write encodes
+ * them.  q and q_out may both be NULL (keys and values only).
+ */
+PA_API pa_status pa_rope_cache_write(const pa_kv_desc *desc, const pa_rope_desc *rope, void *q_out, const void *q,
+                                     int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                                     int64_t v_stride, const int32_t *positions, void *k_cache, void *v_cache,
+                                     const int64_t *slot_mapping, int32_t num_tokens, pa_stream_t stream);
 
 /*
  * Bytes of scratch that pa_decode needs for num_seqs sequences on the current

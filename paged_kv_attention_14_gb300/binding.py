@@ -52,7 +52,7 @@ EXPORTED = ("pa_abi_version", "pa_last_error", "pa_cache_write", "pa_decode_work
             "pa_copy_blocks", "pa_test_stall_pipelines", "pa_bind_blocks", "pa_release_blocks",
             "pa_mixed_workspace_size", "pa_mixed_attention", "pa_prefill_workspace_size",
             "pa_prefill_chunk_balanced", "pa_test_prefill_schedule", "pa_prefill_balanced_chosen",
-            "pa_decode_append", "pa_mixed_attention_append")
+            "pa_decode_append", "pa_mixed_attention_append", "pa_qk_norm_rope", "pa_rope_cache_write")
 
 
 class PaKvDesc(ctypes.Structure):
@@ -74,6 +74,19 @@ class PaKvDesc(ctypes.Structure):
         ("v_scales", ctypes.c_void_p),
         ("error_word", ctypes.c_void_p),
         ("check_indices", ctypes.c_int32),
+    ]
+
+
+class PaRopeDesc(ctypes.Structure):
+    """``pa_rope_desc`` of include/pa.h (field order and types must match)."""
+    _fields_ = [
+        ("cos_sin", ctypes.c_void_p),
+        ("max_position", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("q_weight", ctypes.c_void_p),
+        ("k_weight", ctypes.c_void_p),
     ]
 
 
@@ -105,6 +118,11 @@ def load(path: Optional[str] = None):
         lib.pa_last_error.restype = ctypes.c_char_p
         lib.pa_cache_write.argtypes = [D, P, P, P, P, P, I32, P]
         lib.pa_cache_write.restype = ctypes.c_int
+        R, I64 = ctypes.POINTER(PaRopeDesc), ctypes.c_int64
+        lib.pa_qk_norm_rope.argtypes = [D, R, P, P, P, I64, P, I64, P, I32, P]
+        lib.pa_qk_norm_rope.restype = ctypes.c_int
+        lib.pa_rope_cache_write.argtypes = [D, R, P, P, I64, P, I64, P, I64, P, P, P, P, I32, P]
+        lib.pa_rope_cache_write.restype = ctypes.c_int
         lib.pa_decode_workspace_size.argtypes = [D, I32, I32]
         lib.pa_decode_workspace_size.restype = SZ
         lib.pa_decode.argtypes = [D, P, P, P, P, P, P, I32, P, I32, I32, F, P, SZ, P]
@@ -236,6 +254,121 @@ def pa_cache_write(desc: PaKvDesc, k, v, k_cache, v_cache, slot_mapping, stream=
     _check(load().pa_cache_write(ctypes.byref(desc), _ptr(k, _act(desc), "k"), _ptr(v, _act(desc), "v"),
                                  _ptr(k_cache, _CACHE, "k_cache"), _ptr(v_cache, _CACHE, "v_cache"),
                                  _ptr(slot_mapping, _I64, "slot_mapping"), T, _stream(stream)))
+
+
+def rope_table(max_position: int, rotary_dim: int, base: float = 10000.0, device=None) -> torch.Tensor:
+    """The cos_sin table of plain rotary positions: row p holds cos and sin of
+    p * base^(-2 i / rotary_dim), i < rotary_dim / 2, computed in 64 bits and
+    rounded to fp32 once (fp32 angles of far positions lose their fraction)."""
+    freq = float(base) ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim)
+    ang = torch.arange(max_position, dtype=torch.float64)[:, None] * freq
+    return torch.cat([ang.cos(), ang.sin()], 1).float().to(device or "cuda")
+
+
+def make_rope(cos_sin: torch.Tensor, rotary_dim: int = 0, interleaved: bool = False,
+              q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+              eps: float = 1e-6) -> PaRopeDesc:
+    """The rotation and norms of pa_qk_norm_rope / pa_rope_cache_write.
+    ``cos_sin``: fp32 CUDA ``[max_position, rotary_dim]`` (cosines, then
+    sines); ``rotary_dim`` 0: the table's width; ``q_weight`` / ``k_weight``:
+    ``[head_dim]`` norm weights in the activation type, or None.  The
+    descriptor keeps a reference to the tensors."""
+    if cos_sin.dim() != 2 or (rotary_dim and cos_sin.shape[1] != rotary_dim):
+        raise ValueError("cos_sin must be [max_position, rotary_dim]")
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None and t.dim() != 1:
+            raise ValueError(f"{name} must be one-dimensional")
+    w16 = (torch.bfloat16, torch.float16)
+    r = PaRopeDesc(_ptr(cos_sin, _F32, "cos_sin"), int(cos_sin.shape[0]), int(cos_sin.shape[1]),
+                   1 if interleaved else 0, float(eps), _ptr(q_weight, w16, "q_weight", allow_none=True),
+                   _ptr(k_weight, w16, "k_weight", allow_none=True))
+    r._keep = (cos_sin, q_weight, k_weight)
+    return r
+
+
+def _check_rope(desc: PaKvDesc, rope: PaRopeDesc):
+    """The norm weights against the descriptor: the activation type, one per dim of a head."""
+    act = _act(desc)
+    for t, name in zip(getattr(rope, "_keep", (None,) * 3)[1:], ("q_weight", "k_weight")):
+        if t is not None and (t.dtype not in act or t.shape[0] != desc.head_dim):
+            raise ValueError(f"{name} must hold head_dim elements of {act[0]}")
+
+
+def _rows(t: Optional[torch.Tensor], desc: PaKvDesc, heads: int, tokens: int, name: str, dense: bool = False):
+    """(address, elements from one token to the next) of ``[tokens, heads,
+    head_dim]`` activations whose tokens may lie apart (a slice of a
+    projection's output); (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.dtype not in _act(desc):
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {_act(desc)[0]}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    d = desc.head_dim
+    if tuple(t.shape) != (tokens, heads, d):
+        raise ValueError(f"{name} must be [{tokens}, {heads}, {d}], got {list(t.shape)}")
+    st, sh, se = t.stride()
+    if tokens == 1:
+        st = heads * d  # of one token any stride will do
+    if se != 1 or (heads > 1 and sh != d) or (dense and st != heads * d):
+        raise ValueError(f"{name} must be contiguous" + ("" if dense else " within each token"))
+    return t.data_ptr(), st
+
+
+def _one_device(stream, *tensors):
+    """The launches go to the current device: every tensor has to be there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+    return _stream(stream)
+
+
+def pa_qk_norm_rope(desc: PaKvDesc, rope: PaRopeDesc, q_out, k_out, q, k, positions, stream=None):
+    """Per-head norm and rotation in one pass: q ``[T, Hq, D]`` -> q_out, k
+    ``[T, Hkv, D]`` -> k_out (either pair may be None).  The inputs may be
+    slices of one projection's output, the outputs are dense; an output may
+    be its own input.  ``positions``: int32 ``[T]``."""
+    T = int(positions.shape[0])
+    _check_rope(desc, rope)
+    qp, qs = _rows(q, desc, desc.num_q_heads, T, "q")
+    kp, ks = _rows(k, desc, desc.num_kv_heads, T, "k")
+    qo, _ = _rows(q_out, desc, desc.num_q_heads, T, "q_out", dense=True)
+    ko, _ = _rows(k_out, desc, desc.num_kv_heads, T, "k_out", dense=True)
+    _check(load().pa_qk_norm_rope(ctypes.byref(desc), ctypes.byref(rope), qo, ko, qp, qs, kp, ks,
+                                  _ptr(positions, _I32, "positions"), T,
+                                  _one_device(stream, positions, q, k, q_out, k_out, *getattr(rope, "_keep", ()))))
+
+
+def pa_rope_cache_write(desc: PaKvDesc, rope: PaRopeDesc, q_out, q, k, v, positions, k_cache, v_cache, slot_mapping,
+                        stream=None):
+    """pa_qk_norm_rope with k and v ``[T, Hkv, D]`` going to their cache slots:
+    q -> q_out (both may be None), k normed and rotated, v as it is, both
+    written at ``slot_mapping`` (int64 ``[T]``, negative: no row)."""
+    T = int(slot_mapping.shape[0])
+    _check_rope(desc, rope)
+    if positions.shape[0] != T:
+        raise ValueError("positions and slot_mapping must have one entry per token")
+    qp, qs = _rows(q, desc, desc.num_q_heads, T, "q")
+    kp, ks = _rows(k, desc, desc.num_kv_heads, T, "k")
+    vp, vs = _rows(v, desc, desc.num_kv_heads, T, "v")
+    qo, _ = _rows(q_out, desc, desc.num_q_heads, T, "q_out", dense=True)
+    _check(load().pa_rope_cache_write(ctypes.byref(desc), ctypes.byref(rope), qo, qp, qs, kp, ks, vp, vs,
+                                      _ptr(positions, _I32, "positions"), _cache_ptr(k_cache, desc, "k_cache"),
+                                      _cache_ptr(v_cache, desc, "v_cache"), _ptr(slot_mapping, _I64, "slot_mapping"),
+                                      T, _one_device(stream, positions, q, k, v, q_out, k_cache, v_cache,
+                                                     slot_mapping, *getattr(rope, "_keep", ()))))
+
+
+def _cache_ptr(t, desc: PaKvDesc, name: str):
+    """The address of a cache of the descriptor's type and size."""
+    want = {PA_KV_BF16: (torch.bfloat16,), PA_KV_F16: (torch.float16,),
+            PA_KV_FP8_E4M3: (torch.uint8, torch.float8_e4m3fn),
+            PA_KV_FP8_E5M2: (torch.uint8, torch.float8_e5m2)}[desc.kv_dtype]
+    p = _ptr(t, want, name)
+    if t.numel() != desc.num_blocks * desc.num_kv_heads * 16 * desc.head_dim:
+        raise ValueError(f"{name} must be [num_blocks, num_kv_heads, 16, head_dim]")
+    return p
 
 
 def pa_decode_workspace_size(desc: PaKvDesc, num_seqs: int, max_context_len: int) -> int:

@@ -61,6 +61,36 @@ pa_status check_desc(const pa_kv_desc *d) {
   return PA_OK;
 }
 
+// The checks pa_qk_norm_rope and pa_rope_cache_write share (check_desc has
+// passed).  A side whose input is NULL is left out.
+pa_status check_rope(const pa_kv_desc &d, const pa_rope_desc *r, const void *q, int64_t q_stride, const void *k,
+                     int64_t k_stride, const void *v, int64_t v_stride, const int32_t *positions) {
+  if (!r) return fail(PA_ERR_INVALID_ARG, "rope is NULL%s");
+  if (!r->cos_sin || !aligned16(r->cos_sin))
+    return fail(PA_ERR_INVALID_ARG, "cos_sin must be non-NULL and 16-byte aligned%s");
+  if (r->max_position <= 0) return fail(PA_ERR_INVALID_ARG, "max_position must be positive%s");
+  if (r->rotary_dim < 0 || r->rotary_dim > d.head_dim || r->rotary_dim % 16 != 0)
+    return fail(PA_ERR_INVALID_ARG, "rotary_dim must be a multiple of 16 in [0, head_dim]%s");
+  if (r->interleaved != 0 && r->interleaved != 1)
+    return fail(PA_ERR_INVALID_ARG, "interleaved must be 0 or 1%s");
+  if (!(r->eps >= 0.f) || r->eps > 3.402823466e38f)
+    return fail(PA_ERR_INVALID_ARG, "eps must be finite and >= 0%s");
+  if (!aligned16(r->q_weight) || !aligned16(r->k_weight))
+    return fail(PA_ERR_INVALID_ARG, "q_weight and k_weight must be 16-byte aligned%s");
+  if (!positions || (reinterpret_cast<uintptr_t>(positions) & 3u))
+    return fail(PA_ERR_INVALID_ARG, "positions must be non-NULL and 4-byte aligned%s");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v))
+    return fail(PA_ERR_INVALID_ARG, "q, k and v must be 16-byte aligned%s");
+  const int64_t dq = static_cast<int64_t>(d.num_q_heads) * d.head_dim;
+  const int64_t dk = static_cast<int64_t>(d.num_kv_heads) * d.head_dim;
+  if ((q && q_stride != 0 && (q_stride < dq || q_stride % 8 != 0)) ||
+      (k && k_stride != 0 && (k_stride < dk || k_stride % 8 != 0)) ||
+      (v && v_stride != 0 && (v_stride < dk || v_stride % 8 != 0)))
+    return fail(PA_ERR_INVALID_ARG,
+                "token strides must be 0 or multiples of 8 elements that cover a token's heads%s");
+  return PA_OK;
+}
+
 std::atomic<int> g_test_stall{0};
 std::atomic<unsigned long long> g_test_wait_ns{0};
 std::atomic<int> g_test_schedule{0};  // pa_test_prefill_schedule
@@ -169,6 +199,48 @@ pa_status pa_cache_write(const pa_kv_desc *desc, const void *k, const void *v, v
     return fail(PA_ERR_INVALID_ARG, "slot_mapping must be 8-byte aligned%s");
   const cudaError_t e = pa::launch_cache_write(*desc, k, v, k_cache, v_cache, slot_mapping,
                                                num_tokens, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e);
+}
+
+pa_status pa_qk_norm_rope(const pa_kv_desc *desc, const pa_rope_desc *rope, void *q_out, void *k_out, const void *q,
+                          int64_t q_stride, const void *k, int64_t k_stride, const int32_t *positions,
+                          int32_t num_tokens, pa_stream_t stream) {
+  pa_status st = check_desc(desc);
+  if (st != PA_OK) return st;
+  if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens must be >= 0%s");
+  if (num_tokens == 0) return ok();
+  if ((!q) != (!q_out) || (!k) != (!k_out) || (!q && !k))
+    return fail(PA_ERR_INVALID_ARG, "q with q_out, k with k_out, or both pairs must be given%s");
+  if (!aligned16(q_out) || !aligned16(k_out))
+    return fail(PA_ERR_INVALID_ARG, "q_out and k_out must be 16-byte aligned%s");
+  st = check_rope(*desc, rope, q, q_stride, k, k_stride, nullptr, 0, positions);
+  if (st != PA_OK) return st;
+  const cudaError_t e =
+      pa::launch_rope(*desc, *rope, q_out, k_out, q, q_stride, k, k_stride, nullptr, 0, positions, nullptr, nullptr,
+                      nullptr, num_tokens, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e);
+}
+
+pa_status pa_rope_cache_write(const pa_kv_desc *desc, const pa_rope_desc *rope, void *q_out, const void *q,
+                              int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                              const int32_t *positions, void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                              int32_t num_tokens, pa_stream_t stream) {
+  pa_status st = check_desc(desc);
+  if (st != PA_OK) return st;
+  if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens must be >= 0%s");
+  if (num_tokens == 0) return ok();
+  if ((!q) != (!q_out)) return fail(PA_ERR_INVALID_ARG, "q and q_out must be given together%s");
+  if (!k || !v || !k_cache || !v_cache || !slot_mapping)
+    return fail(PA_ERR_INVALID_ARG, "k, v, k_cache, v_cache and slot_mapping must be non-NULL%s");
+  if (!aligned16(q_out) || !aligned16(k_cache) || !aligned16(v_cache))
+    return fail(PA_ERR_INVALID_ARG, "q_out, k_cache and v_cache must be 16-byte aligned%s");
+  if (reinterpret_cast<uintptr_t>(slot_mapping) & 7u)
+    return fail(PA_ERR_INVALID_ARG, "slot_mapping must be 8-byte aligned%s");
+  st = check_rope(*desc, rope, q, q_stride, k, k_stride, v, v_stride, positions);
+  if (st != PA_OK) return st;
+  const cudaError_t e =
+      pa::launch_rope(*desc, *rope, q_out, nullptr, q, q_stride, k, k_stride, v, v_stride, positions, k_cache, v_cache,
+                      slot_mapping, num_tokens, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ok() : cuda_fail(e);
 }
 

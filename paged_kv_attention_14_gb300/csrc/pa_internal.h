@@ -13,6 +13,14 @@ cudaError_t launch_cache_write(const pa_kv_desc &d, const void *k, const void *v
                                void *v_cache, const int64_t *slot_mapping, int32_t num_tokens,
                                cudaStream_t stream);
 
+// Norm and rotation of q and k (k_cache == NULL: into q_out / k_out; else k
+// and v go to their cache slots and k_out is unused).  q or k may be NULL;
+// a stride of 0 means dense rows.
+cudaError_t launch_rope(const pa_kv_desc &d, const pa_rope_desc &r, void *q_out, void *k_out, const void *q,
+                        int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                        const int32_t *positions, void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                        int32_t num_tokens, cudaStream_t stream);
+
 cudaError_t launch_merge(float *out, float *lse_out, const float *part_o, const float *part_lse,
                          const int32_t *num_parts, int32_t num_seqs, int32_t num_heads,
                          int32_t max_parts, int32_t head_dim, cudaStream_t stream);
