@@ -90,7 +90,8 @@ extern "C" {
  *    pa_prefill_balanced_chosen, pa_test_prefill_schedule, pa_decode_append,
  *    pa_mixed_attention_append.
  *    Added without a new version (nothing before them changed):
- *    pa_rope_desc, pa_qk_norm_rope, pa_rope_cache_write. */
+ *    pa_rope_desc, pa_qk_norm_rope, pa_rope_cache_write,
+ *    pa_decode_shared_workspace_size, pa_decode_shared. */
 #define PA_ABI_VERSION 4
 
 /* Symbols of the shared library; everything else in it stays hidden. */
@@ -564,6 +565,55 @@ PA_API pa_status pa_prefix_attention(const pa_kv_desc *desc, float *out, float *
                                      const int32_t *prefix_lens, int32_t num_groups, int32_t max_q_len,
                                      int32_t max_prefix_len, int32_t num_splits, int32_t out_slots, float scale,
                                      pa_stream_t stream);
+
+/*
+ * Bytes of scratch pa_decode_shared needs for num_seqs sequences in
+ * num_groups groups of at most max_group_size sequences on the current
+ * device (0 if the descriptor or a size is invalid).  It needs no
+ * zero-filling and holds nothing from one call to the next: consecutive
+ * calls on one stream may share it, calls that overlap on the GPU (two
+ * streams, two graphs in flight) need separate ones.
+ */
+PA_API size_t pa_decode_shared_workspace_size(const pa_kv_desc *desc, int32_t num_seqs, int32_t num_groups,
+                                              int32_t max_group_size);
+
+/*
+ * pa_decode for a batch whose sequences share prefixes: the same arguments
+ * and the same results (up to fp32 rounding), with each shared prefix read
+ * once for all the sequences of its group instead of once per sequence
+ * ("Zero-Copy Cache Hits" of "1. Technical Mechanics of the Radix Cache" bind
+ * the sequences of a prefix hit to the same pages).  One call does what
+ * pa_prefix_attention, pa_decode over the own parts and pa_merge_partials do
+ * together.
+ *   group_start : int32 [num_groups + 1], non-decreasing, within [0, num_seqs]:
+ *                 group j is the sequences [group_start[j], group_start[j+1]).
+ *                 Sequences outside every group share nothing.
+ *   prefix_lens : int32 [num_groups]: the block-table rows of group j's
+ *                 sequences name the same blocks for their first
+ *                 prefix_lens[j] tokens.  A prefix is used in whole blocks
+ *                 (rounded down); a sequence may be shorter than its group's
+ *                 prefix or empty, and attends its own context_lens[s] tokens
+ *                 all the same.
+ *   max_group_size : the largest group (host value).  It sizes the tiles and
+ *                 the workspace; larger groups in group_start still give
+ *                 right results.
+ *   max_prefix_len : an upper bound of prefix_lens (host value).
+ *   workspace   : pa_decode_shared_workspace_size() bytes, 16-byte aligned.
+ * num_groups == 0 is a plain decode.  out and lse may be pinned host memory,
+ * as in pa_decode.  With an 8-bit cache the queries are used in fp16: a finite
+ * |q| >= 65520 sets PA_DEVERR_FP16_RANGE in desc->error_word.  With
+ * check_indices the group arrays are checked too (values out of range are
+ * reported and clamped; without it they are clamped in silence).  Errors on
+ * the device are reported in desc->error_word only.
+ * PA_ERR_UNSUPPORTED: local attention, decode_impl PA_DECODE_SIMT, more than
+ * 65535 sequences or groups, a cache of more than 2^31 rows.
+ */
+PA_API pa_status pa_decode_shared(const pa_kv_desc *desc, float *out, float *lse, const void *q, const void *k_cache,
+                                  const void *v_cache, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                  const int32_t *context_lens, int32_t num_seqs, int32_t max_context_len,
+                                  const int32_t *group_start, const int32_t *prefix_lens, int32_t num_groups,
+                                  int32_t max_group_size, int32_t max_prefix_len, float scale, void *workspace,
+                                  size_t workspace_bytes, pa_stream_t stream);
 
 /*
  * Copy-on-write of whole pages: for every i < num_pairs, block dst_blocks[i]

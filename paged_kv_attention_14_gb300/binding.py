@@ -52,7 +52,8 @@ EXPORTED = ("pa_abi_version", "pa_last_error", "pa_cache_write", "pa_decode_work
             "pa_copy_blocks", "pa_test_stall_pipelines", "pa_bind_blocks", "pa_release_blocks",
             "pa_mixed_workspace_size", "pa_mixed_attention", "pa_prefill_workspace_size",
             "pa_prefill_chunk_balanced", "pa_test_prefill_schedule", "pa_prefill_balanced_chosen",
-            "pa_decode_append", "pa_mixed_attention_append", "pa_qk_norm_rope", "pa_rope_cache_write")
+            "pa_decode_append", "pa_mixed_attention_append", "pa_qk_norm_rope", "pa_rope_cache_write",
+            "pa_decode_shared_workspace_size", "pa_decode_shared")
 
 
 class PaKvDesc(ctypes.Structure):
@@ -123,6 +124,10 @@ def load(path: Optional[str] = None):
         lib.pa_qk_norm_rope.restype = ctypes.c_int
         lib.pa_rope_cache_write.argtypes = [D, R, P, P, I64, P, I64, P, I64, P, P, P, P, I32, P]
         lib.pa_rope_cache_write.restype = ctypes.c_int
+        lib.pa_decode_shared_workspace_size.argtypes = [D, I32, I32, I32]
+        lib.pa_decode_shared_workspace_size.restype = SZ
+        lib.pa_decode_shared.argtypes = [D, P, P, P, P, P, P, I32, P, I32, I32, P, P, I32, I32, I32, F, P, SZ, P]
+        lib.pa_decode_shared.restype = ctypes.c_int
         lib.pa_decode_workspace_size.argtypes = [D, I32, I32]
         lib.pa_decode_workspace_size.restype = SZ
         lib.pa_decode.argtypes = [D, P, P, P, P, P, P, I32, P, I32, I32, F, P, SZ, P]
@@ -413,6 +418,48 @@ def pa_decode_append(desc: PaKvDesc, out, q, k_new, v_new, k_cache, v_cache, blo
                                    _ptr(context_lens, _I32, "context_lens"), S, int(max_context_len),
                                    float(scale), _ptr(workspace, (torch.uint8,), "workspace"),
                                    workspace.numel(), _stream(stream)))
+
+
+def pa_decode_shared_workspace_size(desc: PaKvDesc, num_seqs: int, num_groups: int, max_group_size: int) -> int:
+    n = load().pa_decode_shared_workspace_size(ctypes.byref(desc), int(num_seqs), int(num_groups),
+                                               int(max_group_size))
+    if n == 0:
+        raise PaError(PA_ERR_UNSUPPORTED, last_error())
+    return n
+
+
+def decode_shared_workspace(desc: PaKvDesc, num_seqs: int, num_groups: int, max_group_size: int,
+                            device=None) -> torch.Tensor:
+    """A workspace tensor of the size pa_decode_shared needs (any contents will do)."""
+    n = pa_decode_shared_workspace_size(desc, num_seqs, num_groups, max_group_size)
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def pa_decode_shared(desc: PaKvDesc, out, q, k_cache, v_cache, block_tables, context_lens, max_context_len: int,
+                     group_start, prefix_lens, max_group_size: int, max_prefix_len: int, scale: float, workspace,
+                     lse=None, stream=None):
+    """pa_decode of a batch whose sequences share prefixes, each prefix read
+    once for its whole group: group j is the sequences group_start[j] ..
+    group_start[j + 1] - 1 (int32 ``[G + 1]``), whose tables agree on their
+    first prefix_lens[j] tokens (int32 ``[G]``).  ``out`` / ``lse`` may be
+    pinned CPU tensors."""
+    S, G = int(context_lens.shape[0]), int(prefix_lens.shape[0])
+    if group_start.shape[0] != G + 1:
+        raise ValueError("group_start must have one entry more than prefix_lens")
+    heads = (S, desc.num_q_heads)
+    if tuple(q.shape) != (*heads, desc.head_dim) or out.shape != q.shape or block_tables.shape[0] != S or \
+            (lse is not None and tuple(lse.shape) != heads):
+        raise ValueError("q and out must be [S, Hq, D], lse [S, Hq] and block_tables [S, max_blocks]")
+    st = _one_device(stream, q, k_cache, v_cache, block_tables, context_lens, group_start, prefix_lens, workspace,
+                     *(t for t in (out, lse) if t is not None and t.is_cuda))
+    _check(load().pa_decode_shared(ctypes.byref(desc), _ptr(out, _F32, "out", host_ok=True),
+                                   _ptr(lse, _F32, "lse", allow_none=True, host_ok=True), _ptr(q, _act(desc), "q"),
+                                   _cache_ptr(k_cache, desc, "k_cache"), _cache_ptr(v_cache, desc, "v_cache"),
+                                   _ptr(block_tables, _I32, "block_tables"), int(block_tables.shape[1]),
+                                   _ptr(context_lens, _I32, "context_lens"), S, int(max_context_len),
+                                   _ptr(group_start, _I32, "group_start"), _ptr(prefix_lens, _I32, "prefix_lens"), G,
+                                   int(max_group_size), int(max_prefix_len), float(scale),
+                                   _ptr(workspace, (torch.uint8,), "workspace"), workspace.numel(), st))
 
 
 def pa_decode_static(desc: PaKvDesc, out, q, k_cache, v_cache, block_tables, context_lens,

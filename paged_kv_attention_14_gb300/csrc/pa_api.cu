@@ -333,6 +333,67 @@ pa_status pa_decode_append(const pa_kv_desc *desc, float *out, float *lse, const
   return e == cudaSuccess ? ok() : cuda_fail(e);
 }
 
+// What pa_decode_shared and its workspace size ask of the descriptor and the
+// batch's sizes.
+static pa_status check_shared(const pa_kv_desc *desc, int32_t num_seqs, int32_t num_groups, int32_t max_group_size) {
+  const pa_status st = check_desc(desc);
+  if (st != PA_OK) return st;
+  if (num_seqs < 0 || num_groups < 0 || max_group_size < 0)
+    return fail(PA_ERR_INVALID_ARG, "num_seqs, num_groups and max_group_size must be >= 0%s");
+  if (num_seqs > 65535 || num_groups > 65535)
+    return fail(PA_ERR_UNSUPPORTED, "a shared decode takes at most 65535 sequences and groups per call%s");
+  if (desc->sliding_window != 0 || desc->attention_chunk != 0)
+    return fail(PA_ERR_UNSUPPORTED, "local attention does not apply to a shared prefix%s");
+  if (desc->decode_impl != PA_DECODE_AUTO && desc->decode_impl != PA_DECODE_MMA)
+    return fail(PA_ERR_UNSUPPORTED, "pa_decode_shared runs on the tensor cores (decode_impl AUTO or MMA)%s");
+  if (static_cast<int64_t>(desc->num_blocks) * desc->num_kv_heads * 16 > 0x7fffffffLL)
+    return fail(PA_ERR_UNSUPPORTED, "pa_decode_shared addresses at most 2^31 cache rows%s");
+  return PA_OK;
+}
+
+size_t pa_decode_shared_workspace_size(const pa_kv_desc *desc, int32_t num_seqs, int32_t num_groups,
+                                       int32_t max_group_size) {
+  if (check_shared(desc, num_seqs, num_groups, max_group_size) != PA_OK) return 0;
+  return pa::shared_workspace_bytes(*desc, num_seqs, num_groups, max_group_size);
+}
+
+pa_status pa_decode_shared(const pa_kv_desc *desc, float *out, float *lse, const void *q, const void *k_cache,
+                           const void *v_cache, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                           const int32_t *context_lens, int32_t num_seqs, int32_t max_context_len,
+                           const int32_t *group_start, const int32_t *prefix_lens, int32_t num_groups,
+                           int32_t max_group_size, int32_t max_prefix_len, float scale, void *workspace,
+                           size_t workspace_bytes, pa_stream_t stream) {
+  const pa_status st = check_shared(desc, num_seqs, num_groups, max_group_size);
+  if (st != PA_OK) return st;
+  if (num_seqs == 0) return ok();
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens)
+    return fail(PA_ERR_INVALID_ARG,
+                "out, q, k_cache, v_cache, block_tables and context_lens must be non-NULL%s");
+  if (num_groups > 0 && (!group_start || !prefix_lens))
+    return fail(PA_ERR_INVALID_ARG, "group_start and prefix_lens must be non-NULL%s");
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
+    return fail(PA_ERR_INVALID_ARG, "out, q, k_cache and v_cache must be 16-byte aligned%s");
+  if ((reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(context_lens) |
+       reinterpret_cast<uintptr_t>(group_start) | reinterpret_cast<uintptr_t>(prefix_lens) |
+       reinterpret_cast<uintptr_t>(lse)) & 3u)
+    return fail(PA_ERR_INVALID_ARG,
+                "block_tables, context_lens, group_start, prefix_lens and lse must be 4-byte aligned%s");
+  if (max_blocks_per_seq <= 0) return fail(PA_ERR_INVALID_ARG, "max_blocks_per_seq must be positive%s");
+  const int64_t cap = static_cast<int64_t>(max_blocks_per_seq) * 16;
+  if (max_context_len < 0 || max_context_len > cap || max_prefix_len < 0 || max_prefix_len > cap)
+    return fail(PA_ERR_INVALID_ARG,
+                "max_context_len and max_prefix_len must lie in [0, max_blocks_per_seq * block_size]%s");
+  if (!(scale == scale)) return fail(PA_ERR_INVALID_ARG, "scale is NaN%s");
+  if (!workspace || !aligned16(workspace))
+    return fail(PA_ERR_WORKSPACE, "workspace must be non-NULL and 16-byte aligned%s");
+  if (workspace_bytes < pa::shared_workspace_bytes(*desc, num_seqs, num_groups, max_group_size))
+    return fail(PA_ERR_WORKSPACE, "workspace is smaller than pa_decode_shared_workspace_size()%s");
+  const cudaError_t e = pa::launch_shared(*desc, out, lse, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                                          context_lens, num_seqs, group_start, prefix_lens, num_groups,
+                                          max_group_size, scale, workspace, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e);
+}
+
 size_t pa_prefill_workspace_size(const pa_kv_desc *desc, int32_t num_seqs, int32_t max_q_len) {
   if (check_desc(desc) != PA_OK || num_seqs < 0 || max_q_len < 0) return 0;
   const char *why = "";

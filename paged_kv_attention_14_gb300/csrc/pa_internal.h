@@ -55,6 +55,15 @@ cudaError_t launch_decode(const pa_kv_desc &d, const DecodePlan &plan, float *ou
                           void *workspace, cudaStream_t stream, const void *k_new = nullptr,
                           const void *v_new = nullptr);
 
+// pa_decode_shared: the bytes of its workspace on the current device, and
+// its launches.
+size_t shared_workspace_bytes(const pa_kv_desc &d, int32_t num_seqs, int32_t num_groups, int32_t max_group_size);
+cudaError_t launch_shared(const pa_kv_desc &d, float *out, float *lse, const void *q, const void *k_cache,
+                          const void *v_cache, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                          const int32_t *context_lens, int32_t num_seqs, const int32_t *group_start,
+                          const int32_t *prefix_lens, int32_t num_groups, int32_t max_group_size, float scale,
+                          void *workspace, cudaStream_t stream);
+
 pa_status check_prefill(const pa_kv_desc &d, const char **why);
 
 // Every host-side check of pa_prefill_chunk's arguments (num_seqs == 0 or

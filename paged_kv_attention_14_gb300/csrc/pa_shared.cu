@@ -1,0 +1,132 @@
+// pa_shared.cu -- host side of pa_decode_shared: workspace layout and the
+// launches (pa_shared_kernels.cuh has the kernels and their design).
+#include "pa_host_cache.h"
+#include "pa_shared_kernels.cuh"
+
+namespace pa {
+
+namespace {
+
+constexpr size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct Layout {
+  size_t units, groups, seqs, starts, pre_o, pre_lse, own_o, own_lse, cut_o, cut_lse, total;
+};
+
+// Rows of a tile: what the largest group needs, up to the kernel's tile
+int tile_rows_of(const pa_kv_desc &d, int32_t max_group_size) {
+  const int g = d.num_q_heads / d.num_kv_heads;
+  const int cap = shd::MAXROWS / g;  // sequences of a full tile
+  const int n = max_group_size < 1 ? 1 : max_group_size > cap ? cap : max_group_size;
+  return n * g;
+}
+
+Layout layout(const pa_kv_desc &d, int32_t num_seqs, int32_t num_groups, int32_t max_group_size, int ctas) {
+  Layout w;
+  const size_t rows = static_cast<size_t>(num_seqs) * d.num_q_heads;
+  const size_t cut = static_cast<size_t>(ctas) * 2 * tile_rows_of(d, max_group_size);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t x = at;
+    at += up256(bytes);
+    return x;
+  };
+  w.units = take(sizeof(long long));
+  w.groups = take(sizeof(shd::GroupInfo) * num_groups);
+  w.seqs = take(sizeof(shd::SeqInfo) * num_seqs);
+  w.starts = take(sizeof(shd::CtaStart) * ctas);
+  w.pre_o = take(rows * d.head_dim * 4);
+  w.pre_lse = take(rows * 4);
+  w.own_o = take(rows * d.head_dim * 4);
+  w.own_lse = take(rows * 4);
+  w.cut_o = take(cut * d.head_dim * 4);
+  w.cut_lse = take(cut * 4);
+  w.total = at;
+  return w;
+}
+
+}  // namespace
+
+size_t shared_workspace_bytes(const pa_kv_desc &d, int32_t num_seqs, int32_t num_groups, int32_t max_group_size) {
+  return layout(d, num_seqs, num_groups, max_group_size, device_sm_count()).total;
+}
+
+cudaError_t launch_shared(const pa_kv_desc &d, float *out, float *lse, const void *q, const void *k_cache,
+                          const void *v_cache, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                          const int32_t *context_lens, int32_t num_seqs, const int32_t *group_start,
+                          const int32_t *prefix_lens, int32_t num_groups, int32_t max_group_size, float scale,
+                          void *workspace, cudaStream_t stream) {
+  const bool b16 = d.kv_dtype == PA_KV_BF16 || d.kv_dtype == PA_KV_F16;
+  const shd::KernelInfo k = b16 ? shd::pick_attend_16(d.head_dim, d.kv_dtype) : shd::pick_attend_8(d.head_dim, d.kv_dtype);
+  if (prepare_kernel(k.fn, shd::NTHREADS, k.smem) < 1) return cudaErrorInvalidConfiguration;
+  shd::Args a;
+  memset(&a, 0, sizeof a);
+  if (!dec::cache_map(&a.kmap, k_cache, d, 1) || !dec::cache_map(&a.vmap, v_cache, d, 1)) return cudaErrorInvalidValue;
+  a.ctas = device_sm_count();
+  const Layout w = layout(d, num_seqs, num_groups, max_group_size, a.ctas);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  a.out = out;
+  a.lse = lse;
+  a.q = static_cast<const uint16_t *>(q);
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.group_start = group_start;
+  a.prefix_lens = prefix_lens;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_seqs = num_seqs;
+  a.num_groups = num_groups;
+  a.num_kv = d.num_kv_heads;
+  a.num_q = d.num_q_heads;
+  a.g = d.num_q_heads / d.num_kv_heads;
+  a.tile_rows = a.slot_rows = tile_rows_of(d, max_group_size);
+  const float ks = (!b16 && d.k_scale != 0.f) ? d.k_scale : 1.f;
+  a.qscale = scale * ks * shd::kLog2e;
+  a.qscale0 = scale * shd::kLog2e;
+  a.vscale = (!b16 && d.v_scale != 0.f) ? d.v_scale : 1.f;
+  a.k_scales = b16 ? nullptr : d.k_scales;
+  a.v_scales = b16 ? nullptr : d.v_scales;
+  a.num_blocks = d.num_blocks;
+  a.checked = d.check_indices;
+  const TestHooks hooks = test_hooks();
+  a.stall = hooks.stall;
+  a.wait_ns = hooks.wait_ns;
+  a.err = d.error_word;
+  a.units = reinterpret_cast<long long *>(ws + w.units);
+  a.groups = reinterpret_cast<shd::GroupInfo *>(ws + w.groups);
+  a.seqs = reinterpret_cast<shd::SeqInfo *>(ws + w.seqs);
+  a.starts = reinterpret_cast<shd::CtaStart *>(ws + w.starts);
+  a.pre_o = reinterpret_cast<float *>(ws + w.pre_o);
+  a.pre_lse = reinterpret_cast<float *>(ws + w.pre_lse);
+  a.own_o = reinterpret_cast<float *>(ws + w.own_o);
+  a.own_lse = reinterpret_cast<float *>(ws + w.own_lse);
+  a.cut_o = reinterpret_cast<float *>(ws + w.cut_o);
+  a.cut_lse = reinterpret_cast<float *>(ws + w.cut_lse);
+
+  // each launch overlaps the tail of the one before it (programmatic
+  // dependent launch); every kernel waits for that one's writes first
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  void *args[] = {&a};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(shd::PLAN_THREADS);
+  cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(&shd::shared_plan_kernel), args);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(a.ctas);
+  cfg.blockDim = dim3(shd::NTHREADS);
+  cfg.dynamicSmemBytes = k.smem;
+  e = cudaLaunchKernelExC(&cfg, k.fn, args);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(num_seqs) * d.num_q_heads + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  const void *join = d.head_dim == 64 ? reinterpret_cast<const void *>(&shd::shared_join_kernel<64>)
+                                      : reinterpret_cast<const void *>(&shd::shared_join_kernel<128>);
+  return cudaLaunchKernelExC(&cfg, join, args);
+}
+
+}  // namespace pa

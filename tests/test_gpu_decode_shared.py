@@ -1,0 +1,357 @@
+"""pa_decode_shared against the fp64 oracle's plain decode over the whole
+tables.  Slots no sequence may read hold NaN.
+
+Tolerance.  A weight's relative error is the P pair's (2^-18 for bf16 hi + lo,
+less for fp16), the exponential's (2^-22) and its score's: 128 products
+summed in fp32, at worst 128 * 2^-24 * scale * sum |q k| * log2 e, and
+sum |q k| <= 128 * 0.65 for N(0, 1) rows, so 9e-5.  The output is off by at
+most that times max |v|, about 5: 5e-4.  The log-sum-exp is off by the
+scores' error plus the sum's, 2e-4.  An 8-bit cache is widened exactly.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import pa_helpers as H
+from paged_kv_attention_14_gb300 import binding as B
+from paged_kv_attention_14_gb300 import workloads as W
+from paged_kv_attention_14_gb300.step import GraphedStep
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+TOL, LSE_TOL = 5e-4, 2e-4
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from paged_kv_attention_14_gb300 import build
+    B.load(build.build())
+
+
+def _args(b):
+    c = b.meta["cascade"]
+    gs, pre = c["query_start_loc"], c["prefix_lens"]
+    return gs, pre, int((gs[1:] - gs[:-1]).max()), int(pre.max())
+
+
+def _run(b, caches, gs=None, pre=None, max_group=None, lens=None, tables=None, desc=None, out=None, lse=None, ws=None,
+         scale=None, stream=None):
+    g0, p0, mg, mp = _args(b)
+    gs, pre = g0 if gs is None else gs, p0 if pre is None else pre
+    lens = b.context_lens_decode if lens is None else lens
+    tables = b.block_tables_decode if tables is None else tables
+    S = lens.shape[0]
+    d = desc or H.desc_of(b)
+    out = torch.full((S, b.num_q_heads, b.head_dim), float("nan"), device=DEV) if out is None else out
+    lse = torch.full((S, b.num_q_heads), float("nan"), device=DEV) if lse is None else lse
+    ws = B.decode_shared_workspace(d, S, pre.shape[0], mg if max_group is None else max_group) if ws is None else ws
+    B.pa_decode_shared(d, out, b.q_decode, caches[0], caches[1], tables, lens, tables.shape[1] * 16, gs, pre,
+                       mg if max_group is None else max_group, int(pre.max()) if pre.numel() else 0,
+                       b.scale if scale is None else scale, ws, lse=lse, stream=stream)
+    torch.cuda.synchronize()
+    return out, lse
+
+
+def _check(b, out, lse, ocaches=None, rows=None, scale_tol=1.0):
+    S, Hq, D = b.q_decode.shape
+    rows = list(range(S)) if rows is None else rows
+    pairs = [(s, h) for s in rows for h in range(Hq)]
+    o, x = H.oracle_decode(b, ocaches=ocaches, pairs=pairs)
+    H.assert_close(out[rows].reshape(-1, D), o.reshape(-1, D), TOL * scale_tol, "out")
+    H.assert_close(lse[rows].reshape(-1), x, LSE_TOL * scale_tol, "lse")
+
+
+KV = [W.KV_BF16, W.KV_F16, W.KV_FP8, W.KV_FP8_E5M2]
+CASES = [
+    # (group sizes, prefix lens, own lens, q heads, kv heads, head_dim)
+    ([3, 1], [32, 0], [1, 33, 7, 16], 4, 2, 64),
+    ([1], [16], [5], 8, 1, 128),
+    ([2], [16], [1, 1], 4, 4, 128),
+    ([3, 1, 2], [48, 32, 64], [1, 15, 16, 40, 7, 33], 8, 2, 128),       # 12 rows, a single, 8 rows
+    ([5, 2], [256, 0], [3, 100, 17, 1, 64, 9, 250], 32, 8, 128),        # 20 rows: two row groups; nothing shared
+    ([9, 7], [160, 1040], list(range(1, 17)), 40, 8, 128),              # 45 and 35 rows, g 5
+    ([17], [2048], [11 * i + 1 for i in range(17)], 32, 8, 64),         # 68 rows: eight row groups
+    ([33, 3], [512, 4096], [37 * i % 300 + 1 for i in range(36)], 16, 4, 128),   # 132 rows: two tiles
+    ([9], [400], [i + 1 for i in range(9)], 16, 1, 128),                # g 16: 144 rows of one kv head
+    ([40], [96], [3] * 40, 5, 1, 128),                                  # g 5: tiles of 125 rows at most
+]
+
+
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("groups,plens,slens,Hq,Hkv,D", CASES)
+def test_matches_the_oracle(groups, plens, slens, Hq, Hkv, D, kv):
+    b = W.shared_prefix_decode(700 + sum(plens) + D, groups, plens, slens, Hq, Hkv, D, kv_dtype=kv, device=DEV)
+    _check(b, *_run(b, H.gpu_caches(b)), ocaches=H.oracle_caches(b))
+
+
+@pytest.mark.parametrize("kv", [W.KV_BF16, W.KV_FP8])
+def test_wide_group_on_a_long_prefix(kv):
+    """64 sequences on 16384 tokens: 256 rows per kv head, items cut between many CTAs; sampled rows."""
+    g = torch.Generator().manual_seed(8)
+    slens = torch.randint(1, 300, (64,), generator=g).tolist()
+    b = W.shared_prefix_decode(801, [64], [16384], slens, 32, 8, 128, kv_dtype=kv, device=DEV)
+    _check(b, *_run(b, H.gpu_caches(b)), ocaches=H.oracle_caches(b), rows=[0, 1, 31, 32, 63])
+
+
+def test_two_sequences_on_a_very_long_prefix():
+    b = W.shared_prefix_decode(802, [2], [65536], [100, 1], 8, 2, 128, device=DEV)
+    _check(b, *_run(b, H.gpu_caches(b)))
+
+
+def test_no_groups_is_a_plain_decode():
+    b = W.shared_prefix_decode(803, [3, 2], [64, 32], [1, 40, 7, 300, 16], 32, 8, 128, device=DEV)
+    none = torch.zeros(0, dtype=torch.int32, device=DEV)
+    out, lse = _run(b, H.gpu_caches(b), gs=torch.zeros(1, dtype=torch.int32, device=DEV), pre=none, max_group=0)
+    _check(b, out, lse)
+
+
+def test_groups_that_leave_sequences_out_and_prefixes_that_end_inside_a_block():
+    """Group 0 starts at sequence 1, the last sequence belongs to none; a
+    prefix of 16 n + 7 tokens is used up to its whole blocks; the largest
+    group is twice what max_group_size says."""
+    b = W.shared_prefix_decode(804, [6, 5], [96, 208], [9, 50, 1, 16, 33, 17, 8, 2, 300, 31, 90], 32, 8, 128, device=DEV)
+    gs = torch.tensor([1, 6, 10], dtype=torch.int32, device=DEV)
+    pre = torch.tensor([96 + 7, 208 + 15], dtype=torch.int32, device=DEV)
+    _check(b, *_run(b, H.gpu_caches(b), gs=gs, pre=pre, max_group=3))
+
+
+@pytest.mark.parametrize("kv", [W.KV_BF16, W.KV_FP8])
+def test_empty_sequences_and_ones_shorter_than_their_prefix(kv):
+    b = W.shared_prefix_decode(805, [6, 3, 4], [96, 32, 64], [9, 50, 1, 16, 33, 17, 5, 6, 7, 1, 2, 3, 4], 32, 8, 128,
+                               kv_dtype=kv, device=DEV, poison=False)
+    lens = b.context_lens_decode.clone()
+    lens[0], lens[2], lens[3] = 0, 96, 37           # empty; exactly the prefix; inside it
+    lens[6:9] = torch.tensor([0, 20, 1])            # nobody reaches the prefix's end
+    lens[9:13] = 0                                  # a group of padding rows
+    b.context_lens_decode = lens
+    out, lse = _run(b, H.gpu_caches(b))
+    empty = [0, 6, 9, 10, 11, 12]
+    assert (out[empty] == 0).all() and (lse[empty] == float("-inf")).all()
+    _check(b, out, lse, ocaches=H.oracle_caches(b), rows=[s for s in range(13) if s not in empty])
+
+
+def test_padding_rows_read_nothing():
+    """A group whose unread prefix slots hold NaN: all of its sequences but one are empty or shorter."""
+    b = W.shared_prefix_decode(806, [4], [64], [1, 1, 1, 1], 8, 2, 128, device=DEV, poison=False)
+    lens = torch.tensor([0, 21, 0, 5], dtype=torch.int32, device=DEV)
+    kc, vc = b.k_pool.clone(), b.v_pool.clone()
+    blk = int(b.block_tables_decode[1, 1])
+    for c in (kc, vc):  # tokens 21 .. 31 of the prefix and its later blocks
+        c[blk, :, 5:] = float("nan")
+        for j in (2, 3):
+            c[int(b.block_tables_decode[1, j])] = float("nan")
+    b.context_lens_decode, b.k_pool, b.v_pool = lens, kc, vc
+    out, lse = _run(b, (kc, vc))
+    _check(b, out, lse, rows=[1, 3])
+    assert (out[[0, 2]] == 0).all()
+
+
+def test_rising_scores():
+    """Scores that grow along the keys by far more than the raise threshold, up to hundreds."""
+    b = W.shared_prefix_decode(807, [5, 1], [640, 0], [70, 3, 200, 1, 33, 500], 32, 8, 128, device=DEV, poison=False)
+    kc = b.k_pool.float()
+    for s in range(6):
+        n = int(b.context_lens_decode[s])
+        for j in range((n + 15) // 16):
+            blk = int(b.block_tables_decode[s, j])
+            if s in (0, 5) or j >= 40:
+                kc[blk] *= 1 + 0.2 * j
+    b.k_pool = kc.to(torch.bfloat16)
+    # scores (and so their error) are up to 1 + 0.2 * 71 times those of the tolerance's derivation
+    _check(b, *_run(b, (b.k_pool, b.v_pool)), scale_tol=16.0)
+
+
+def test_one_far_larger_score_keeps_the_small_weights():
+    """One key 2^18 times as heavy as each other one; the rest together still weigh: fp16 P must not lose them."""
+    for kv in (W.KV_F16, W.KV_BF16):
+        b = W.shared_prefix_decode(808, [4], [8192], [5, 6, 7, 8], 8, 2, 128, kv_dtype=kv, device=DEV, poison=False)
+        b.q_decode.zero_()
+        b.q_decode[:, :, 0] = 1
+        kc = b.k_pool.clone()
+        kc[..., 0] = 0
+        kc[int(b.block_tables_decode[0, 3]), :, 4, 0] = 12.48 / b.scale  # e^12.48 = 2^18
+        b.k_pool = kc
+        _check(b, *_run(b, (kc, b.v_pool)))
+
+
+def test_nan_and_infinity_stay_in_their_rows():
+    b = W.shared_prefix_decode(809, [5], [160], [9, 50, 1, 16, 33], 32, 8, 128, device=DEV)
+    good, _ = _run(b, H.gpu_caches(b))
+    b.q_decode[2, 5, 3] = float("nan")
+    b.q_decode[4, 31, 7] = float("inf")
+    out, lse = _run(b, H.gpu_caches(b))
+    bad = torch.zeros(5, 32, dtype=torch.bool, device=DEV)
+    bad[2, 5] = bad[4, 31] = True
+    assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad]).all()
+    assert torch.equal(out[~bad], good[~bad])
+
+
+def test_same_bits_every_time_and_from_any_workspace():
+    b = W.shared_prefix_decode(810, [20, 9], [2048, 304], [37 * i % 200 + 1 for i in range(29)], 32, 8, 128, device=DEV)
+    caches = H.gpu_caches(b)
+    a = _run(b, caches)
+    n = B.pa_decode_shared_workspace_size(H.desc_of(b), 29, 2, 20)
+    for fill in (0, 255):
+        ws = torch.full((n,), fill, dtype=torch.uint8, device=DEV)
+        for _ in range(2):
+            x = _run(b, caches, ws=ws)
+            assert torch.equal(x[0], a[0]) and torch.equal(x[1], a[1])
+
+
+def test_per_head_scales():
+    b = W.random_decode(811, [40, 100, 7], 8, 4, 128, kv_dtype=W.KV_FP8, device=DEV, poison=True, per_head_scales=True)
+    gs = torch.tensor([0, 3], dtype=torch.int32, device=DEV)
+    b.meta["cascade"] = dict(query_start_loc=gs, prefix_lens=torch.zeros(1, dtype=torch.int32, device=DEV))
+    out, lse = _run(b, H.gpu_caches(b))
+    o, x = H.oracle_decode(b)
+    # heads of magnitudes up to 2^2: the scores' and the values' errors scale by that
+    H.assert_close(out, o, 4 * TOL, "out")
+    H.assert_close(lse, x, 4 * LSE_TOL, "lse")
+    # a shared block too: the second sequence's first block is the first one's
+    t = b.block_tables_decode.clone()
+    t[1, 0] = t[0, 0]
+    b.block_tables_decode = t
+    pre = torch.tensor([16], dtype=torch.int32, device=DEV)
+    out, lse = _run(b, H.gpu_caches(b), gs=torch.tensor([0, 2], dtype=torch.int32, device=DEV), pre=pre)
+    o, x = H.oracle_decode(b)
+    H.assert_close(out, o, 4 * TOL, "out")
+
+
+def test_checked_indices_are_reported_and_stay_inside():
+    ew = torch.zeros(1, dtype=torch.int32, device=DEV)
+    b = W.shared_prefix_decode(812, [4, 3], [64, 32], [9, 50, 1, 16, 33, 17, 5], 32, 8, 128, device=DEV, poison=False)
+    caches = H.gpu_caches(b)
+    d = B.make_desc(b.num_blocks, 8, 32, 128, error_word=ew, check_indices=True)
+    out, lse = _run(b, caches, desc=d)
+    assert int(ew) == 0
+    _check(b, out, lse)
+    gs, pre, _, _ = _args(b)
+    for what in ("table", "len", "start", "prefix"):
+        ew.zero_()
+        t, n, g2, p2 = b.block_tables_decode.clone(), b.context_lens_decode.clone(), gs.clone(), pre.clone()
+        if what == "table":
+            t[0, 1], t[1, 1], t[2, 1], t[3, 1] = [b.num_blocks + 5] * 4
+        elif what == "len":
+            n[3] = t.shape[1] * 16 + 1
+        elif what == "start":
+            g2[1] = 70000
+        else:
+            p2[0] = -16
+        B.pa_decode_shared(d, out, b.q_decode, caches[0], caches[1], t, n, t.shape[1] * 16, g2, p2, 4, 64, b.scale,
+                           B.decode_shared_workspace(d, 7, 2, 4), lse=lse)
+        torch.cuda.synchronize()
+        assert int(ew) & B.PA_DEVERR_BAD_INDEX, what
+
+
+def test_a_stalled_pipeline_is_reported_and_the_next_call_is_right():
+    ew = torch.zeros(1, dtype=torch.int32, device=DEV)
+    b = W.shared_prefix_decode(813, [20, 3], [512, 32], [9] * 23, 32, 8, 128, device=DEV)
+    caches = H.gpu_caches(b)
+    d = B.make_desc(b.num_blocks, 8, 32, 128, error_word=ew)
+    try:
+        B.pa_test_stall_pipelines(True)
+        _run(b, caches, desc=d)
+    finally:
+        B._check(B.load().pa_test_stall_pipelines(0, 0))
+    assert int(ew) == B.PA_DEVERR_WAIT_TIMEOUT
+    ew.zero_()
+    _check(b, *_run(b, caches, desc=d))
+    assert int(ew) == 0
+
+
+def test_graph_replay_with_other_lengths_and_two_streams_at_once():
+    b = W.shared_prefix_decode(814, [7, 4], [128, 64], [37 * i % 100 + 1 for i in range(11)], 32, 8, 128, device=DEV)
+    caches = H.gpu_caches(b)
+    d = H.desc_of(b)
+    gs, pre, mg, mp = _args(b)
+    S = 11
+    lens = b.context_lens_decode.clone()
+    outs = [torch.zeros(S, 32, 128, device=DEV) for _ in range(3)]
+    wss = [B.decode_shared_workspace(d, S, 2, mg) for _ in range(3)]
+    maxL = b.block_tables_decode.shape[1] * 16
+
+    def issue(i, n, stream=None):
+        B.pa_decode_shared(d, outs[i], b.q_decode, caches[0], caches[1], b.block_tables_decode, n, maxL, gs, pre, mg,
+                           mp, b.scale, wss[i], stream=stream)
+
+    step = GraphedStep(lambda: issue(0, lens))
+    lens.copy_(torch.clamp(lens - 20, min=1))  # the plan is made anew at every replay
+    step()
+    full = b.context_lens_decode
+    b.context_lens_decode = lens
+    o, _ = H.oracle_decode(b)
+    H.assert_close(outs[0], o, TOL, "replay")
+    b.context_lens_decode = full
+    want, _ = _run(b, caches)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i, st in enumerate(streams):
+            issue(1 + i, full, st)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[1], want) and torch.equal(outs[2], want)
+
+
+def test_output_in_pinned_host_memory():
+    b = W.shared_prefix_decode(815, [4, 1], [64, 0], [9, 50, 1, 16, 33], 32, 8, 128, device=DEV)
+    caches = H.gpu_caches(b)
+    want = _run(b, caches)
+    out, lse = torch.zeros(5, 32, 128).pin_memory(), torch.zeros(5, 32).pin_memory()
+    _run(b, caches, out=out, lse=lse)
+    assert torch.equal(out, want[0].cpu()) and torch.equal(lse, want[1].cpu())
+
+
+def test_queries_beyond_fp16_of_an_8bit_cache_are_reported():
+    ew = torch.zeros(1, dtype=torch.int32, device=DEV)
+    b = W.shared_prefix_decode(816, [3], [32], [5, 6, 7], 8, 2, 128, kv_dtype=W.KV_FP8, device=DEV, poison=False)
+    caches = H.gpu_caches(b)
+    d = B.make_desc(b.num_blocks, 2, 8, 128, B.PA_KV_FP8_E4M3, b.k_scale, b.v_scale, error_word=ew)
+    _run(b, caches, desc=d)
+    assert int(ew) == 0
+    b.q_decode[1, 2, 3] = 1e5
+    _run(b, caches, desc=d)
+    assert int(ew) == B.PA_DEVERR_FP16_RANGE
+
+
+def test_misuse_of_the_binding_is_refused():
+    b = W.shared_prefix_decode(817, [3], [32], [5, 6, 7], 8, 2, 128, device=DEV)
+    caches = H.gpu_caches(b)
+    gs, pre, mg, mp = _args(b)
+    with pytest.raises(ValueError, match="group_start"):
+        _run(b, caches, gs=gs[:-1])
+    with pytest.raises(ValueError, match="block_tables"):
+        _run(b, caches, tables=b.block_tables_decode[:2])
+    with pytest.raises(ValueError, match="num_blocks"):
+        _run(b, (caches[0][:-1], caches[1]))
+    with pytest.raises(B.PaError) as e:
+        _run(b, caches, ws=torch.zeros(1024, dtype=torch.uint8, device=DEV))
+    assert e.value.status == B.PA_ERR_WORKSPACE
+
+
+def test_rotated_append_then_shared_decode():
+    """The operators as a step uses them: q, k and v of a projection rotated and
+    written into the cache, then attention over the shared prefix, the own
+    part and the new token, against the oracle on a cache written by hand."""
+    b = W.shared_prefix_decode(818, [6, 2], [160, 48], [9, 50, 1, 16, 33, 17, 5, 100], 32, 8, 128, device=DEV)
+    S, Hq, Hkv, D = 8, 32, 8, 128
+    g = torch.Generator().manual_seed(4)
+    qkv = torch.randn(S, (Hq + 2 * Hkv) * D, generator=g).to(torch.bfloat16).to(DEV)
+    q, k, v = (qkv[:, lo * D:hi * D].view(S, hi - lo, D) for lo, hi in ((0, Hq), (Hq, Hq + Hkv), (Hq + Hkv, 48)))
+    w = (1 + 0.1 * torch.randn(D, generator=g)).to(torch.bfloat16).to(DEV)
+    rope = B.make_rope(B.rope_table(512, D, 1e6, DEV), q_weight=w, k_weight=w)
+    pos = (b.context_lens_decode - 1).to(torch.int32)
+    at = pos.long()
+    slots = b.block_tables_decode.gather(1, (at // 16)[:, None])[:, 0].long() * 16 + at % 16
+    d = H.desc_of(b)
+    kc, vc = b.k_pool.clone(), b.v_pool.clone()
+    q_out = torch.empty(S, Hq, D, dtype=torch.bfloat16, device=DEV)
+    B.pa_rope_cache_write(d, rope, q_out, q, k, v, pos, kc, vc, slots)
+    b.q_decode = q_out
+    out, lse = _run(b, (kc, vc))
+    k_rot = torch.empty(S, Hkv, D, dtype=torch.bfloat16, device=DEV)
+    B.pa_qk_norm_rope(d, rope, None, k_rot, None, k, pos)
+    ok, ov = oracle.cache_write(oracle.KV_BF16, 16, Hkv, D, k_rot.cpu(), v.contiguous().cpu(), slots.cpu(),
+                                b.k_pool.cpu(), b.v_pool.cpu())
+    assert np.array_equal(kc.view(torch.int16).cpu().numpy().view(np.uint16), ok)
+    _check(b, out, lse, ocaches=(oracle.KV_BF16, ok, ov))
