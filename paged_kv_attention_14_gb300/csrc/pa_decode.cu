@@ -158,14 +158,6 @@ pa_status plan_decode(const pa_kv_desc &d, int32_t num_seqs, DecodePlan *plan, c
 
 namespace dec {
 
-bool cache_map(CUtensorMap *map, const void *base, const pa_kv_desc &d, int hg) {
-  KernelInfo k;
-  k.hg = hg;
-  k.swizzle = d.head_dim * ((d.kv_dtype == PA_KV_BF16 || d.kv_dtype == PA_KV_F16) ? 2 : 1) >= 128 ? 128 : 64;
-  k.wide_mode = kWideMode;
-  return make_cache_map(map, base, d, k);
-}
-
 bool make_decode_args(const pa_kv_desc &d, const DecodePlan &plan, float *out, float *lse, const void *q,
                       const void *k_cache, const void *v_cache, const int32_t *block_tables,
                       int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs, float scale,

@@ -1518,10 +1518,6 @@ bool make_decode_args(const pa_kv_desc &d, const DecodePlan &plan, float *out, f
                       int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs, float scale,
                       void *workspace, DecodeArgs *a);
 
-// The tensor map of a cache with boxes of one block of hg kv heads, laid
-// down as swz_off<row bytes, hg> reads it.  pa_decode.cu.
-bool cache_map(CUtensorMap *map, const void *base, const pa_kv_desc &d, int hg);
-
 // Defined in the translation units that instantiate the kernels.
 KernelInfo pick_simt(int head_dim, int kv_dtype, int g);
 KernelInfo pick_mma_bf16(int head_dim, int gq, int hg);

@@ -10,28 +10,61 @@ namespace {
 constexpr size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct Layout {
-  size_t units, groups, seqs, starts, pre_o, pre_lse, own_o, own_lse, cut_o, cut_lse, total;
+  size_t axis, groups, seqs, starts, pre_o, pre_lse, own_o, own_lse, cut_o, cut_lse, total;
 };
 
-// Rows of a tile: what the largest group needs, up to the kernel's tile
-int tile_rows_of(const pa_kv_desc &d, int32_t max_group_size) {
-  const int g = d.num_q_heads / d.num_kv_heads;
-  const int cap = shd::MAXROWS / g;  // sequences of a full tile
-  const int n = max_group_size < 1 ? 1 : max_group_size > cap ? cap : max_group_size;
-  return n * g;
+// Sequences of a tile: what the largest group needs, up to the kernel's rows
+int tile_seqs_of(const pa_kv_desc &d, int32_t max_group_size) {
+  const int cap = shd::MAXROWS / (d.num_q_heads / d.num_kv_heads);
+  return max_group_size < 1 ? 1 : max_group_size > cap ? cap : max_group_size;
+}
+
+// The cache as TMA sees it: rows are (block, kv head, token) triples of
+// head_dim elements; a box is the 16 tokens of one kv head of one block, 64
+// columns of a 16-bit cache (128-byte swizzle, the layout the products
+// read), or the whole rows of an 8-bit one (plain: they are widened).
+bool make_map(CUtensorMap *map, const void *base, const pa_kv_desc &d) {
+  const bool kv8 = d.kv_dtype == PA_KV_FP8_E4M3 || d.kv_dtype == PA_KV_FP8_E5M2;
+  using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                     const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
+                                     CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                     CUtensorMapFloatOOBfill);
+  static EncodeTiledFn enc = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  if (!enc) return false;
+  thread_local MapCache<> cache;
+  const MapKey key = map_key(base, d.num_blocks, d.num_kv_heads, d.head_dim, kv8);
+  if (cache.find(key, map)) return true;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d.head_dim),
+                              static_cast<cuuint64_t>(d.num_blocks) * d.num_kv_heads * 16};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(d.head_dim) * (kv8 ? 1 : 2)};
+  const cuuint32_t box[2] = {kv8 ? static_cast<cuuint32_t>(d.head_dim) : 64u, 16};
+  const cuuint32_t estr[2] = {1, 1};
+  if (enc(map, kv8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(base), dims,
+          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, kv8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return false;
+  cache.put(key, *map);
+  return true;
 }
 
 Layout layout(const pa_kv_desc &d, int32_t num_seqs, int32_t num_groups, int32_t max_group_size, int ctas) {
   Layout w;
   const size_t rows = static_cast<size_t>(num_seqs) * d.num_q_heads;
-  const size_t cut = static_cast<size_t>(ctas) * 2 * tile_rows_of(d, max_group_size);
+  const size_t cut = static_cast<size_t>(ctas) * 2 * tile_seqs_of(d, max_group_size) * (d.num_q_heads / d.num_kv_heads);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t x = at;
     at += up256(bytes);
     return x;
   };
-  w.units = take(sizeof(long long));
+  w.axis = take(sizeof(shd::Axis));
   w.groups = take(sizeof(shd::GroupInfo) * num_groups);
   w.seqs = take(sizeof(shd::SeqInfo) * num_seqs);
   w.starts = take(sizeof(shd::CtaStart) * ctas);
@@ -58,10 +91,10 @@ cudaError_t launch_shared(const pa_kv_desc &d, float *out, float *lse, const voi
                           void *workspace, cudaStream_t stream) {
   const bool b16 = d.kv_dtype == PA_KV_BF16 || d.kv_dtype == PA_KV_F16;
   const shd::KernelInfo k = b16 ? shd::pick_attend_16(d.head_dim, d.kv_dtype) : shd::pick_attend_8(d.head_dim, d.kv_dtype);
-  if (prepare_kernel(k.fn, shd::NTHREADS, k.smem) < 1) return cudaErrorInvalidConfiguration;
+  if (prepare_kernel(k.fn, k.threads, k.smem) < 1) return cudaErrorInvalidConfiguration;
   shd::Args a;
   memset(&a, 0, sizeof a);
-  if (!dec::cache_map(&a.kmap, k_cache, d, 1) || !dec::cache_map(&a.vmap, v_cache, d, 1)) return cudaErrorInvalidValue;
+  if (!make_map(&a.kmap, k_cache, d) || !make_map(&a.vmap, v_cache, d)) return cudaErrorInvalidValue;
   a.ctas = device_sm_count();
   const Layout w = layout(d, num_seqs, num_groups, max_group_size, a.ctas);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -78,7 +111,8 @@ cudaError_t launch_shared(const pa_kv_desc &d, float *out, float *lse, const voi
   a.num_kv = d.num_kv_heads;
   a.num_q = d.num_q_heads;
   a.g = d.num_q_heads / d.num_kv_heads;
-  a.tile_rows = a.slot_rows = tile_rows_of(d, max_group_size);
+  a.tile_seqs = tile_seqs_of(d, max_group_size);
+  a.slot_rows = a.tile_seqs * a.g;
   const float ks = (!b16 && d.k_scale != 0.f) ? d.k_scale : 1.f;
   a.qscale = scale * ks * shd::kLog2e;
   a.qscale0 = scale * shd::kLog2e;
@@ -91,7 +125,7 @@ cudaError_t launch_shared(const pa_kv_desc &d, float *out, float *lse, const voi
   a.stall = hooks.stall;
   a.wait_ns = hooks.wait_ns;
   a.err = d.error_word;
-  a.units = reinterpret_cast<long long *>(ws + w.units);
+  a.axis = reinterpret_cast<shd::Axis *>(ws + w.axis);
   a.groups = reinterpret_cast<shd::GroupInfo *>(ws + w.groups);
   a.seqs = reinterpret_cast<shd::SeqInfo *>(ws + w.seqs);
   a.starts = reinterpret_cast<shd::CtaStart *>(ws + w.starts);
@@ -117,7 +151,7 @@ cudaError_t launch_shared(const pa_kv_desc &d, float *out, float *lse, const voi
   cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(&shd::shared_plan_kernel), args);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(a.ctas);
-  cfg.blockDim = dim3(shd::NTHREADS);
+  cfg.blockDim = dim3(k.threads);
   cfg.dynamicSmemBytes = k.smem;
   e = cudaLaunchKernelExC(&cfg, k.fn, args);
   if (e != cudaSuccess) return e;

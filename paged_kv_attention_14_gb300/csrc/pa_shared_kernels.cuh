@@ -9,29 +9,39 @@
 // normalised by its own sum, with its log-sum-exp) are joined by weights
 // 2^(lse_p - max lse).
 //
-// What bounds it: the K/V bytes (each prefix once per group and kv head, each
-// own part once) while a group has up to about 64 (sequence, head) rows per
-// kv head; with more rows the products of the prefix.
-//
 // Three launches:
 //  * shared_plan_kernel (one CTA) turns the lengths into a list of items --
-//    (group, tile of rows, kv head) over the prefix's blocks, and
-//    (sequence, kv head) over its own blocks -- laid out on one axis of
-//    work units (a block costs more units in a tile of many rows).
-//  * shared_attend_kernel, one persistent CTA per SM: CTA c takes the units
-//    [c U / G, (c + 1) U / G) of that axis, so every CTA has the same work
-//    whatever the lengths.  A producer warp streams the blocks by TMA into a
-//    ring; 8 consumer warps run m16n8k16 MMAs with the rows as M: a tile of
-//    up to 128 rows is RG row groups of 16 x KG = 8 / RG key groups, so one
-//    sequence's few heads spread their keys over all 8 warps and a wide tile
-//    spreads its rows.  P enters P V as a hi + lo pair of 16-bit values
-//    (near-fp32), 8-bit caches are widened to fp16 in registers.
+//    (group, tile of up to 128 rows, kv head) over the prefix's blocks, and
+//    (sequence, kv head) over its own blocks -- laid end to end on one axis
+//    of blocks.
+//  * shared_attend_kernel, one persistent CTA per SM: CTA c takes the blocks
+//    [c n, (c + 1) n) of that axis, so every CTA reads the same bytes
+//    whatever the lengths; an item cut between CTAs leaves a piece in each.
 //  * shared_join_kernel, one warp per (sequence, head): joins the parts.
+//
+// The attention runs on tcgen05 for every item, a sequence's few heads
+// included: an M 128 product costs the tensor cores the same whatever its
+// live rows, 24 products of K 16 per 128 keys (8 for Q K^T, 16 for P V with P
+// as a hi + lo pair) -- about 1,900 cycles, less than the 2,850 in which the
+// SM's share of the measured HBM rate brings those 128 keys (64 KB of bf16).
+// Roles (warps) of the attend kernel:
+//   0  MMA issuer (one thread): Q K^T of step k + 1, then P V of step k, so
+//      that the softmax of step k + 1 runs behind P V of step k;
+//   1  walks the CTA's part of the axis, publishes items, K copies (TMA);
+//   2  V copies;   3  Q tiles (two slots, so that items overlap);
+//   4-11  softmax, two threads per row (64 keys each), and each finished
+//      item's output, one step late so that it hides behind the next item;
+//   12-13 (8-bit caches) widen the landed bytes to fp16 tiles (exact).
+// Scores and outputs are double-buffered in tensor memory (S 2 x 128, O 2 x D
+// columns); P overwrites its scores.  Every wait is bounded.
 #pragma once
 
 #include <cuda.h>
+#include <float.h>
+#include <string.h>
 
-#include "pa_decode_kernels.cuh"
+#include <type_traits>
+
 #include "pa_device.cuh"
 #include "pa_internal.h"
 
@@ -40,23 +50,24 @@ namespace shd {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int NC = 8;            // consumer warps; warp NC produces
-constexpr int NTHREADS = (NC + 1) * 32;
-constexpr int MAXROWS = 16 * NC;  // rows of a tile
-constexpr int kMaxSeqs = 65535;   // sequences of a call (as pa_prefill_chunk)
+constexpr int MAXROWS = 128;     // rows of a tile: one TMEM lane each
+constexpr int KT = 128;          // keys of a step
+constexpr int BPT = KT / 16;     // blocks of a step
 // the running maximum of a row is only raised when a score exceeds it by
 // more than this (log2 units), so that O is rarely rescaled
 constexpr float kRaise = 8.f;
+// fewer blocks than a step are not worth a CTA of their own
+constexpr int kMinBlocks = BPT;
 
-// One group's prefix on the work axis.
+// One group's prefix on the axis of blocks.
 struct __align__(16) GroupInfo {
-  long long base;  // first unit
+  long long base;  // first block
   int first;       // first sequence
   int n;           // sequences
   int nb;          // blocks of the prefix that some sequence reads (0: nothing shared)
   int kend;        // keys of the prefix that some sequence reads
   int tile_seqs;   // sequences of a tile (the last tile may have fewer)
-  int w;           // units of a block
+  int tiles;
   int row;         // a sequence whose table holds all of the prefix that is read
   int pad[3];
 };
@@ -69,19 +80,18 @@ struct __align__(16) SeqInfo {
   int group;  // its group, -1: none
   int pad[2];
 };
-// Where a CTA's range begins.
+// Where a CTA's part of the axis begins.
 struct __align__(16) CtaStart {
   int kind;  // 0 prefix item, 1 own part, 2 nothing to do
   int idx;   // group or sequence
   int sub;   // tile * kv heads + kv head, or kv head
-  int pad;
+  int off;   // first block within the item
 };
-
-constexpr int kOwnUnits = 4;  // units of a block of an own part
-
-// Units of a prefix block in a tile of `rows` rows: the stream bounds tiles of
-// up to 64 rows, their MMAs the wider ones.
-__host__ __device__ constexpr int tile_units(int rows) { return rows <= 64 ? 4 : (rows + 15) / 16; }
+// The whole axis.
+struct __align__(16) Axis {
+  long long blocks;  // U
+  long long per;     // blocks of a CTA
+};
 
 struct Args {
   CUtensorMap kmap;
@@ -99,9 +109,9 @@ struct Args {
   int num_kv;
   int num_q;
   int g;
-  int tile_rows;  // rows a tile may have (a multiple of g, at most MAXROWS)
+  int tile_seqs;  // sequences a tile may have
   int slot_rows;  // rows of a cut item's slot
-  int ctas;       // CTAs that share the work axis
+  int ctas;       // CTAs that share the axis
   float qscale;   // scale * k_scale * log2(e)
   float qscale0;  // scale * log2(e)
   float vscale;
@@ -113,34 +123,22 @@ struct Args {
   unsigned long long wait_ns;
   int32_t *err;
   // workspace
-  long long *units;     // [1] U
+  Axis *axis;
   GroupInfo *groups;
   SeqInfo *seqs;
   CtaStart *starts;
-  float *pre_o;         // [S][Hq][D] prefix parts of uncut items, normalised
-  float *pre_lse;       // [S][Hq], log2 units
-  float *own_o;         // ... own parts
+  float *pre_o;    // [S][Hq][D] prefix parts of uncut items, normalised
+  float *pre_lse;  // [S][Hq], log2 units
+  float *own_o;    // ... own parts
   float *own_lse;
-  float *cut_o;         // [ctas][2][slot_rows][D] pieces of cut items
+  float *cut_o;    // [ctas][2][slot_rows][D] pieces of cut items
   float *cut_lse;
 };
 
-// CTA c's units are [first_unit(c), first_unit(c + 1)); cta_of(u) holds u.
-__device__ __forceinline__ long long first_unit(long long c, long long U, int G) { return c * U / G; }
-__device__ __forceinline__ int cta_of(long long u, long long U, int G) {
-  return static_cast<int>(((u + 1) * G - 1) / U);
-}
-// Blocks [lo, hi) of an item of nb blocks, w units each, from unit u0, that
-// the units [b0, b1) hold: those whose first unit lies there.
-__device__ __forceinline__ void piece_blocks(long long u0, int nb, int w, long long b0, long long b1, int &lo,
-                                             int &hi) {
-  lo = b0 <= u0 ? 0 : static_cast<int>((b0 - u0 + w - 1) / w);
-  hi = static_cast<int>(min((b1 - u0 + w - 1) / w, static_cast<long long>(nb)));
-}
-
 // ------------------------------------------------------------------ planning
 
-constexpr int PLAN_THREADS = 1024;
+constexpr int PLAN_THREADS = 512;
+constexpr int PLAN_CAP = 512;  // sequences / groups planned in shared memory
 
 // Exclusive prefix sum over the CTA's threads; *total gets the sum.
 __device__ __forceinline__ long long scan_exclusive(long long v, long long *total, long long *s_warp) {
@@ -155,6 +153,7 @@ __device__ __forceinline__ long long scan_exclusive(long long v, long long *tota
   if (lane == 31) s_warp[warp] = incl;
   __syncthreads();
   long long before = 0, sum = 0;
+#pragma unroll
   for (int i = 0; i < PLAN_THREADS / 32; ++i) {
     const long long x = s_warp[i];
     if (i < warp) before += x;
@@ -164,25 +163,42 @@ __device__ __forceinline__ long long scan_exclusive(long long v, long long *tota
   return before + incl - v;
 }
 
+// The last entry whose base is <= u (entries of no blocks share the base of
+// the next one, so it is the entry that holds block u).
+template <class T>
+__device__ __forceinline__ int find_base(const T *v, int n, long long u) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (v[mid].base <= u)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
 static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const __grid_constant__ Args a) {
   __shared__ long long s_warp[PLAN_THREADS / 32];
+  __shared__ SeqInfo s_seqs[PLAN_CAP];
+  __shared__ GroupInfo s_groups[PLAN_CAP];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int S = a.num_seqs, G = a.num_groups;
   const int cap = a.max_blocks * 16;
+  SeqInfo *seqs = S <= PLAN_CAP ? s_seqs : a.seqs;
+  GroupInfo *groups = G <= PLAN_CAP ? s_groups : a.groups;
   for (int s = tid; s < S; s += PLAN_THREADS) {
     int L = __ldg(a.context_lens + s);
     if (a.checked) L = checked_len(L, cap, a.err, nullptr);
-    SeqInfo &q = a.seqs[s];
+    SeqInfo q = {};
     q.len = max(L, 0);
-    q.fb = 0;
     q.group = -1;
+    seqs[s] = q;
   }
-  for (int c = tid; c < a.ctas; c += PLAN_THREADS) a.starts[c] = CtaStart{2, 0, 0, 0};
   __syncthreads();
   // one warp per group: its sequences, and how much of the prefix they read
-  const int tile_seqs = a.tile_rows / a.g;
   for (int j = warp; j < G; j += PLAN_THREADS / 32) {
     const int r0 = __ldg(a.group_start + j), r1 = __ldg(a.group_start + j + 1);
     int P = __ldg(a.prefix_lens + j);
@@ -193,253 +209,317 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
     if (s1 - s0 < 2) P = 0;  // nobody to share with
     int mine = -1, row = 0;
     for (int s = s0 + lane; s < s1; s += 32) {
-      const int n = min(a.seqs[s].len, P);
+      const int n = min(seqs[s].len, P);
       if (n > mine) {
         mine = n;
         row = s;
       }
-      a.seqs[s].fb = P >> 4;
-      a.seqs[s].group = j;
+      seqs[s].fb = P >> 4;
+      seqs[s].group = j;
     }
     const int best = __reduce_max_sync(0xffffffffu, mine);
     row = __reduce_min_sync(0xffffffffu, mine == best ? row : 0x7fffffff);
-    const int top = max(best, 0);
     if (lane == 0) {
-      GroupInfo q;
+      GroupInfo q = {};
       q.row = row;
-      q.base = 0;
       q.first = s0;
       q.n = s1 - s0;
-      q.kend = top;
-      q.nb = (top + 15) >> 4;
-      const int tiles = max(1, (q.n + tile_seqs - 1) / tile_seqs);
-      q.tile_seqs = max(1, (q.n + tiles - 1) / tiles);
-      q.w = tile_units(q.tile_seqs * a.g);
-      a.groups[j] = q;
+      q.kend = max(best, 0);
+      q.nb = (q.kend + 15) >> 4;
+      // tiles of equal numbers of sequences
+      q.tiles = max(1, (q.n + a.tile_seqs - 1) / a.tile_seqs);
+      q.tile_seqs = max(1, (q.n + q.tiles - 1) / q.tiles);
+      q.tiles = (q.n + q.tile_seqs - 1) / q.tile_seqs;
+      groups[j] = q;
     }
   }
   __syncthreads();
-  // places on the work axis: prefix items, then own parts
+  // places on the axis: prefix items, then own parts
   long long at = 0;
   for (int j0 = 0; j0 < G; j0 += PLAN_THREADS) {
     const int j = j0 + tid;
-    long long v = 0;
-    if (j < G) {
-      const GroupInfo &q = a.groups[j];
-      const int tiles = (q.n + q.tile_seqs - 1) / q.tile_seqs;
-      v = static_cast<long long>(q.nb) * q.w * tiles * a.num_kv;
-    }
+    const long long v = j < G ? static_cast<long long>(groups[j].nb) * groups[j].tiles * a.num_kv : 0;
     long long sum;
     const long long e = scan_exclusive(v, &sum, s_warp);
-    if (j < G) a.groups[j].base = at + e;
+    if (j < G) groups[j].base = at + e;
     at += sum;
   }
+  const long long own = at;  // first block of the own parts
   for (int s0 = 0; s0 < S; s0 += PLAN_THREADS) {
     const int s = s0 + tid;
-    long long v = 0;
-    int nb = 0;
-    if (s < S) {
-      const SeqInfo &q = a.seqs[s];
-      nb = max(0, ((q.len + 15) >> 4) - q.fb);
-      v = static_cast<long long>(nb) * kOwnUnits * a.num_kv;
-    }
+    const int nb = s < S ? max(0, ((seqs[s].len + 15) >> 4) - seqs[s].fb) : 0;
     long long sum;
-    const long long e = scan_exclusive(v, &sum, s_warp);
+    const long long e = scan_exclusive(static_cast<long long>(nb) * a.num_kv, &sum, s_warp);
     if (s < S) {
-      a.seqs[s].nb = nb;
-      a.seqs[s].base = at + e;
+      seqs[s].nb = nb;
+      seqs[s].base = at + e;
     }
     at += sum;
   }
   const long long U = at;
-  if (tid == 0) *a.units = U;
-  if (U == 0) return;
+  const long long per = max((U + a.ctas - 1) / a.ctas, static_cast<long long>(kMinBlocks));
+  if (tid == 0) *a.axis = Axis{U, per};
   __syncthreads();
-  // each item's owner names it to the CTAs whose first unit it holds
-  auto name = [&](int kind, int idx, long long base, long long item, int items) {
-    if (item == 0) return;
-    const long long end = base + item * items;
-    // the first CTA whose first unit is >= base: floor(c U / G) >= base
-    for (long long c = (base * a.ctas + U - 1) / U; c < a.ctas; ++c) {
-      const long long u = first_unit(c, U, a.ctas);
-      if (u >= end) break;
-      if (u >= base) a.starts[c] = CtaStart{kind, idx, static_cast<int>((u - base) / item), 0};
+  // each CTA's first item
+  for (int c = tid; c < a.ctas; c += PLAN_THREADS) {
+    const long long u = c * per;
+    CtaStart st = {2, 0, 0, 0};
+    if (u < own) {
+      const int j = find_base(groups, G, u);
+      const long long r = u - groups[j].base;
+      st = CtaStart{0, j, static_cast<int>(r / groups[j].nb), static_cast<int>(r % groups[j].nb)};
+    } else if (u < U) {
+      const int s = find_base(seqs, S, u);
+      const long long r = u - seqs[s].base;
+      st = CtaStart{1, s, static_cast<int>(r / seqs[s].nb), static_cast<int>(r % seqs[s].nb)};
     }
-  };
-  for (int j = tid; j < G; j += PLAN_THREADS) {
-    const GroupInfo &q = a.groups[j];
-    name(0, j, q.base, static_cast<long long>(q.nb) * q.w, (q.n + q.tile_seqs - 1) / q.tile_seqs * a.num_kv);
+    a.starts[c] = st;
   }
-  for (int s = tid; s < S; s += PLAN_THREADS)
-    name(1, s, a.seqs[s].base, static_cast<long long>(a.seqs[s].nb) * kOwnUnits, a.num_kv);
+  if (S <= PLAN_CAP)
+    for (int s = tid; s < S; s += PLAN_THREADS) a.seqs[s] = s_seqs[s];
+  if (G <= PLAN_CAP)
+    for (int j = tid; j < G; j += PLAN_THREADS) a.groups[j] = s_groups[j];
 }
 
 // ------------------------------------------------------------------- attend
 
-constexpr int kFirst = 1;  // the stage begins a piece
-constexpr int kLast = 2;   // ... ends it
 constexpr int kToOut = 0;  // a piece's result: the output itself,
 constexpr int kToPre = 1;  // the prefix parts, the own parts,
 constexpr int kToOwn = 2;
 constexpr int kToCut = 3;  // or a cut item's slot
 
-struct __align__(16) Stage {
-  int kind;    // 0 data, 1 end
-  int flags;
+// A piece of an item, as the walking warp hands it to the other roles.
+struct __align__(16) Item {
+  int end;     // 1: nothing follows
   int seq0;    // first sequence of the tile
   int rows;    // rows of the tile (sequences x g)
   int kvh;
-  int key0;    // position of the stage's first token
-  int kend;    // keys from here on are not the item's
-  int blk;     // the stage's first block within the piece
-  int nblk;
+  int key0;    // position of the piece's first token
+  int kend;    // keys from here on are not the piece's
+  int nblk;    // blocks of the piece
+  int table;   // sequence whose block table is read
   int to;
   int slot;    // kToCut: the slot
   int prefix;  // 1: rows have limits of their own (their lengths)
+  int pad;
 };
+
+constexpr int NIQ = 4;  // items in flight between the roles
 
 template <int D_, int KVT_>
 struct Cfg {
   static constexpr int D = D_;
   static constexpr int KVT = KVT_;
-  static constexpr int ESZ = kv16(KVT) ? 2 : 1;
-  static constexpr int ROWB = D * ESZ;
-  static constexpr int TILEB = 16 * ROWB;                // a block of one kv head
-  static constexpr int BPS = 16384 / TILEB;              // blocks of a stage: 16 KB of K, 16 KB of V
-  static constexpr int KVB = BPS * TILEB;
-  static constexpr int STAGEB = 2 * KVB;
-  static constexpr int REDW = (D / 2 + 4) * 32;          // floats of a warp's partial state
-  static constexpr int NRED = NC / 2;                    // warps that write one at a time
-  static constexpr int FIXED = NRED * REDW * 4 + 2048;
-  static constexpr int NS = (230000 - 1024 - FIXED) / STAGEB;
-  static constexpr size_t SMEM = 1024 + size_t(NS) * STAGEB + FIXED;
+  static constexpr bool KV8 = !kv16(KVT);
+  static constexpr bool BF16 = KVT == kKvBf16;  // bf16 products (fp16 otherwise)
+  static constexpr int NCONV = KV8 ? 2 : 0;     // widening warps
+  static constexpr int NTHREADS = (12 + NCONV) * 32;
+  static constexpr int HALVES = D / 64;         // 128-byte column halves of a 16-bit row
+  static constexpr int HB = KT * 128;           // bytes of one half of a K or V tile
+  static constexpr int TB = HALVES * HB;        // a 16-bit K or V tile
+  // where TMA copies land: the tiles themselves, or byte tiles to be widened
+  static constexpr int LB = KV8 ? KT * D : TB;
+  static constexpr int BLOCKB = LB / BPT;       // one 16-token block
+  static constexpr int NT = KV8 ? 2 : (D == 128 ? 3 : 6);      // 16-bit tiles of K, and of V
+  static constexpr int NL = KV8 ? (D == 128 ? 2 : 6) : NT;     // landing slots of K, and of V
+  static constexpr int QHALF = MAXROWS * 128;   // one half of a 128-row Q tile
+  static constexpr int QB = HALVES * QHALF;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = OFF_Q + QB;
+  static constexpr int OFF_V = OFF_K + NT * TB;
+  static constexpr int OFF_LK = KV8 ? OFF_V + NT * TB : OFF_K;
+  static constexpr int OFF_LV = KV8 ? OFF_LK + NL * LB : OFF_V;
+  static constexpr int OFF_X = KV8 ? OFF_LV + NL * LB : OFF_V + NT * TB;  // [2][128] fp32: a row's halves exchange
+  static constexpr int OFF_IQ = OFF_X + 2 * MAXROWS * 4;
+  static constexpr int OFF_BAR = OFF_IQ + NIQ * static_cast<int>(sizeof(Item));
+  static constexpr int BARB = D == 64 ? 640 : 512;
+  static constexpr int SMEM = OFF_BAR + BARB + 1024;  // + alignment slack
+  // an M 128 product reads 128 rows of Q from either slot: past a small
+  // slot's rows it reads whatever follows, which only feeds dead rows
+  static_assert(OFF_Q + QB / 2 + QB / 4 * (HALVES - 1) + QHALF <= OFF_X, "Q reads stay inside shared memory");
+  static_assert(SMEM <= 232448, "shared memory of one CTA");
+  static constexpr uint32_t S_COL = 0;            // two score tiles of KT columns
+  static constexpr uint32_t O_COL = 2 * KT;       // two outputs of D columns
+  static constexpr uint32_t TMEM_COLS = 512;
+  static_assert(O_COL + 2 * D <= TMEM_COLS, "TMEM columns");
+  static constexpr uint32_t IDESC_QK = umma_idesc_bf16(MAXROWS, KT, false, false, !BF16);
+  static constexpr uint32_t IDESC_PV = umma_idesc_bf16(MAXROWS, D, false, true, !BF16);
   // exponent offset of P: fp16 P keeps small probabilities out of its
-  // subnormals; with kRaise the largest P is 2^(8 + 6), below fp16's range
-  static constexpr float PB = KVT == kKvBf16 ? 0.f : 6.f;
-  static_assert(NS >= 3 && SMEM <= 232448, "ring");
+  // subnormals; with kRaise the largest P is 2^(8 + 6), inside fp16's range
+  static constexpr float PB = BF16 ? 0.f : 6.f;
 };
 
 template <class C>
-__device__ void produce(const Args &a, uint8_t *ring, Stage *hdr, uint64_t *full, uint64_t *empty, int lane) {
-  constexpr int BPS = C::BPS;
-  const int me = blockIdx.x, G = a.ctas;
-  const long long U = *a.units;
+struct Bars {
+  uint64_t iq_full[NIQ], iq_empty[NIQ];
+  uint64_t lk_full[C::NL], lk_empty[C::NL], lv_full[C::NL], lv_empty[C::NL];  // landed copies
+  uint64_t k_full[C::NT], k_empty[C::NT], v_full[C::NT], v_empty[C::NT];      // 8-bit: widened tiles
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t drain;
+  uint32_t tmem;
+};
+
+// The Q slot of an item: tiles of up to 64 rows alternate between two
+// half-size slots, larger ones take both.  Every role follows the items in
+// order and so knows the slots and how often each was used.
+struct QSlots {
+  uint32_t uses[2] = {0, 0};
+  int turn = 0;
+  bool big = false;
+  int slot = 0;
+  __device__ __forceinline__ void next(int rows) {
+    big = rows > MAXROWS / 2;
+    if (!big) {
+      slot = turn;
+      turn ^= 1;
+    } else {
+      slot = 0;
+    }
+  }
+  __device__ __forceinline__ bool uses_slot(int i) const { return big || slot == i; }
+  __device__ __forceinline__ void done() {
+    for (int i = 0; i < 2; ++i)
+      if (uses_slot(i)) ++uses[i];
+  }
+};
+
+// Block-table entries of a piece, 32 at a time, the next 32 requested while
+// the current ones are used (one warp).
+struct TableWindow {
+  const int32_t *row;
+  int n, win, cur, nxt;
+  template <class A>
+  __device__ __forceinline__ int entry(const A &a, int e, int lane) const {
+    if (e + lane >= n) return 0;
+    const int v = __ldg(row + e + lane);
+    return a.checked ? checked_block(v, a.num_blocks, a.err, nullptr) : v;
+  }
+  template <class A>
+  __device__ __forceinline__ void begin(const A &a, const int32_t *row_, int n_, int lane) {
+    row = row_;
+    n = n_;
+    win = 0;
+    cur = entry(a, 0, lane);
+    nxt = n > 32 ? entry(a, 32, lane) : 0;
+  }
+  // the block id at b + k, b a multiple of BPT and k < BPT
+  template <class A>
+  __device__ __forceinline__ int at(const A &a, int b, int k, int lane) {
+    if (b - win >= 32) {
+      win += 32;
+      cur = nxt;
+      nxt = win + 32 < n ? entry(a, win + 32, lane) : 0;
+    }
+    return __shfl_sync(0xffffffffu, cur, (b - win + k) & 31);
+  }
+};
+
+// Copies of a piece's K (or V) blocks into the landing slots, a step at a
+// time; `fill` counts the slots filled so far.
+template <class C>
+__device__ bool copy_piece(const Args &a, const CUtensorMap *map, uint8_t *slots, uint64_t *full, uint64_t *empty,
+                           const int32_t *table, int nblk, int kvh, uint32_t &fill, uint64_t pol, int lane) {
+  constexpr int BOXES = C::KV8 ? 1 : C::HALVES;
+  TableWindow tw;
+  tw.begin(a, table, nblk, lane);
+  const int bi = lane / BOXES, hh = lane % BOXES;
+  for (int b = 0; b < nblk; b += BPT) {
+    const int n = min(BPT, nblk - b);
+    const int phys = tw.at(a, b, bi & (BPT - 1), lane);
+    const uint32_t st = fill % C::NL, ph = (fill / C::NL) & 1;
+    if (!mbar_wait(&empty[st], ph ^ 1, a.wait_ns)) return false;
+    if (lane == 0) mbar_arrive_expect_tx(&full[st], n * C::BLOCKB);
+    __syncwarp();
+    if (bi < n) {
+      uint8_t *dst = slots + st * C::LB + (C::KV8 ? bi * C::BLOCKB : hh * C::HB + bi * 2048);
+      tma_load_2d(dst, map, hh * 64, (phys * a.num_kv + kvh) * 16, &full[st], pol);
+    }
+    ++fill;
+  }
+  return true;
+}
+
+// After a failed wait: the copies already issued land before the CTA exits.
+template <class C>
+__device__ void drain_copies(const Args &a, uint64_t *full, uint32_t fill) {
+  for (uint32_t i = fill > C::NL ? fill - C::NL : 0; i < fill; ++i)
+    mbar_wait(&full[i % C::NL], (i / C::NL) & 1, a.wait_ns);
+}
+
+// Warp 1: the CTA's items, and their K copies.
+template <class C>
+__device__ bool walk(const Args &a, uint8_t *smem, Bars<C> &bar, Item *iq, int lane) {
+  const int me = blockIdx.x;
+  const Axis ax = *a.axis;
+  const long long b0 = me * ax.per, b1 = min(b0 + ax.per, ax.blocks);
   const uint64_t pol = l2_evict_first_policy();
+  uint32_t fill = 0, posted = 0;
   bool ok = true;
-  int stage = 0, issued = 0;
-  uint32_t par = 1;  // a fresh barrier counts its preceding phase as complete
-  if (U > 0 && !a.stall) {
-    const long long b0 = first_unit(me, U, G), b1 = first_unit(me + 1, U, G);
+  auto post = [&](const Item &it) {
+    const uint32_t st = posted % NIQ, ph = (posted / NIQ) & 1;
+    if (!mbar_wait(&bar.iq_empty[st], ph ^ 1, a.wait_ns)) return false;
+    if (lane == 0) {
+      iq[st] = it;
+      mbar_arrive(&bar.iq_full[st]);
+    }
+    __syncwarp();
+    ++posted;
+    return true;
+  };
+  if (a.stall) return true;
+  if (b0 < b1) {
     const CtaStart st = a.starts[me];
-    int kind = st.kind, idx = st.idx, sub = st.sub;
-    if (b0 >= b1) kind = 2;
+    int kind = st.kind, idx = st.idx, sub = st.sub, off = st.off;
+    long long left = b1 - b0;
     while (kind < 2 && ok) {
       // the group's or sequence's items, from `sub` on
-      int items, nb, w, fb, kend, seq0 = 0, nseq = 0, tile_seqs = 1, table_row;
-      long long base;
-      bool alone = false;
+      Item it = {};
+      int items, nb, kend, fb = 0, first = 0, n = 1, tile_seqs = 1, whole_to = kToPre;
       if (kind == 0) {
         const GroupInfo q = a.groups[idx];
-        items = q.nb > 0 ? (q.n + q.tile_seqs - 1) / q.tile_seqs * a.num_kv : 0;
+        items = q.tiles * a.num_kv;
         nb = q.nb;
-        w = q.w;
-        fb = 0;
-        kend = q.kend;
-        base = q.base;
-        seq0 = q.first;
-        nseq = q.n;
+        first = q.first;
+        n = q.n;
         tile_seqs = q.tile_seqs;
-        table_row = q.row;
+        kend = q.kend;
+        it.table = q.row;
+        it.prefix = 1;
       } else {
         const SeqInfo q = a.seqs[idx];
-        items = q.nb > 0 ? a.num_kv : 0;
+        items = a.num_kv;
         nb = q.nb;
-        w = kOwnUnits;
         fb = q.fb;
+        first = idx;
         kend = q.len;
-        base = q.base;
-        table_row = idx;
-        alone = q.fb == 0;
+        it.table = idx;
+        whole_to = q.fb == 0 ? kToOut : kToOwn;
       }
-      const int32_t *table = a.block_tables + static_cast<int64_t>(table_row) * a.max_blocks;
-      auto entry = [&](int e) {  // physical block of the item's block e
-        if (e >= nb) return 0;
-        const int v = __ldg(table + fb + e);
-        return a.checked ? checked_block(v, a.num_blocks, a.err, nullptr) : v;
-      };
-      for (; sub < items && ok; ++sub) {
-        const long long u0 = base + static_cast<long long>(sub) * nb * w;
-        const long long u1 = u0 + static_cast<long long>(nb) * w;
-        if (u0 >= b1) {
-          kind = 2;
-          break;
-        }
-        int lo, hi;
-        piece_blocks(u0, nb, w, b0, b1, lo, hi);
-        const bool cut = b0 > u0 || b1 < u1;
-        const int kvh = kind == 0 ? sub % a.num_kv : sub;
+      const int32_t *table = a.block_tables + static_cast<int64_t>(it.table) * a.max_blocks + fb;
+      for (; sub < items && ok && left > 0; ++sub, off = 0) {
         const int t0 = kind == 0 ? sub / a.num_kv * tile_seqs : 0;
-        // this lane's entry of the next 32, and of the 32 after them
-        int win = lo, cur = entry(lo + lane), nxt = 0;
-        if (hi - lo > 32) nxt = entry(lo + 32 + lane);
-        for (int b = lo; b < hi; b += BPS) {
-          const int n = min(BPS, hi - b);
-          if (b - win >= 32) {
-            win += 32;
-            cur = nxt;
-            nxt = win + 32 < hi ? entry(win + 32 + lane) : 0;
-          }
-          // BPS divides 32: a stage's entries are in one window
-          const int phys = __shfl_sync(0xffffffffu, cur, (b - win + (lane % BPS)) & 31);
-          if (!mbar_wait(&empty[stage], par, a.wait_ns)) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) {
-            Stage h;
-            h.kind = 0;
-            h.flags = (b == lo ? kFirst : 0) | (b + BPS >= hi ? kLast : 0);
-            h.seq0 = kind == 0 ? seq0 + t0 : idx;
-            h.rows = (kind == 0 ? min(tile_seqs, nseq - t0) : 1) * a.g;
-            h.kvh = kvh;
-            h.key0 = (fb + b) * 16;
-            h.kend = kend;
-            h.blk = b - lo;
-            h.nblk = n;
-            h.to = cut ? kToCut : kind == 0 ? kToPre : alone ? kToOut : kToOwn;
-            h.slot = me * 2 + (u0 <= b0 ? 0 : 1);
-            h.prefix = kind == 0;
-            hdr[stage] = h;
-            mbar_arrive_expect_tx(&full[stage], 2u * n * C::TILEB);
-          }
-          __syncwarp();
-          uint8_t *sk = ring + static_cast<size_t>(stage) * C::STAGEB;
-          const int row = (phys * a.num_kv + kvh) * 16;
-          // lanes 0 .. BPS - 1 copy K, the next BPS lanes V
-          if (lane % BPS < n && lane < 2 * BPS) {
-            const bool is_v = lane >= BPS;
-            uint8_t *dst = sk + (is_v ? C::KVB : 0) + (lane % BPS) * C::TILEB;
-            const CUtensorMap *map = is_v ? &a.vmap : &a.kmap;
-            if constexpr (C::ROWB > 128)
-              tma_load_3d(dst, map, 0, row, 0, &full[stage], pol);
-            else
-              tma_load_2d(dst, map, 0, row, &full[stage], pol);
-          }
-          ++issued;
-          if (++stage == C::NS) {
-            stage = 0;
-            par ^= 1;
-          }
-        }
+        it.kvh = kind == 0 ? sub % a.num_kv : sub;
+        it.seq0 = first + t0;
+        it.rows = min(tile_seqs, n - t0) * a.g;
+        it.key0 = (fb + off) * 16;
+        it.nblk = static_cast<int>(min(static_cast<long long>(nb - off), left));
+        it.kend = min(kend, it.key0 + it.nblk * 16);  // a cut piece ends before the item
+        const bool whole = it.nblk == nb;
+        it.to = whole ? whole_to : kToCut;
+        // a cut item that begins inside this CTA's range is its last one
+        it.slot = me * 2 + (off == 0 && left < b1 - b0 ? 1 : 0);
+        left -= it.nblk;
+        ok = post(it) && copy_piece<C>(a, &a.kmap, smem + C::OFF_LK, bar.lk_full, bar.lk_empty, table + off, it.nblk,
+                                       it.kvh, fill, pol, lane);
       }
-      if (kind == 2 || !ok) break;
+      if (!ok || left == 0) break;
       // the next group with a prefix, after the last one the sequences with
-      // an own part; the ones without work are passed over 32 at a time
+      // an own part; the ones without blocks are passed over 32 at a time
       sub = 0;
       ++idx;
-      auto next = [&](int n, auto blocks) {
-        while (idx < n) {
-          const unsigned some = __ballot_sync(0xffffffffu, idx + lane < n && blocks(idx + lane) > 0);
+      auto next = [&](int count, auto blocks) {
+        while (idx < count) {
+          const unsigned some = __ballot_sync(0xffffffffu, idx + lane < count && blocks(idx + lane) > 0);
           if (some) {
             idx += __ffs(some) - 1;
             return true;
@@ -455,369 +535,564 @@ __device__ void produce(const Args &a, uint8_t *ring, Stage *hdr, uint64_t *full
       if (kind == 1 && !next(a.num_seqs, [&](int s) { return a.seqs[s].nb; })) kind = 2;
     }
   }
-  if (ok && !a.stall) {
-    if (mbar_wait(&empty[stage], par, a.wait_ns)) {
-      if (lane == 0) {
-        hdr[stage].kind = 1;
-        mbar_arrive(&full[stage]);
-      }
-    } else {
-      ok = false;
-    }
+  if (ok) {
+    Item it = {};
+    it.end = 1;
+    ok = post(it);
   }
-  if (!ok) {
-    if (lane == 0) report_error(a.err, nullptr, kErrWaitTimeout);
-    // the copies already issued land before the CTA can exit
-    for (int i = 1; i <= min(issued, C::NS); ++i) {
-      int st = stage - i;
-      uint32_t p = par ^ 1;  // parity of the fill the ring index `stage` would get next, minus one lap
-      if (st < 0) {
-        st += C::NS;
-        p ^= 1;
+  if (!ok) drain_copies<C>(a, bar.lk_full, fill);
+  return ok;
+}
+
+// The next item for one role (whole warp): false when the wait ran out.
+template <class C>
+__device__ __forceinline__ bool take_item(const Args &a, Bars<C> &bar, const Item *iq, uint32_t &taken, Item &it,
+                                          int lane) {
+  const uint32_t st = taken % NIQ;
+  if (!mbar_wait(&bar.iq_full[st], (taken / NIQ) & 1, a.wait_ns)) return false;
+  it = iq[st];
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&bar.iq_empty[st]);
+  ++taken;
+  return true;
+}
+
+// Warp 2: V copies.
+template <class C>
+__device__ bool copy_v(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq, int lane) {
+  const uint64_t pol = l2_evict_first_policy();
+  uint32_t fill = 0, taken = 0;
+  bool ok = true;
+  Item it;
+  while (ok) {
+    ok = take_item<C>(a, bar, iq, taken, it, lane);
+    if (!ok || it.end) break;
+    const int32_t *table = a.block_tables + static_cast<int64_t>(it.table) * a.max_blocks + (it.key0 >> 4);
+    ok = copy_piece<C>(a, &a.vmap, smem + C::OFF_LV, bar.lv_full, bar.lv_empty, table, it.nblk, it.kvh, fill, pol,
+                       lane);
+  }
+  if (!ok) drain_copies<C>(a, bar.lv_full, fill);
+  return ok;
+}
+
+// Warp 3: Q tiles, [half][row][128 B] with the 128-byte swizzle.  With an
+// 8-bit cache the bf16 queries become fp16 (a finite |q| beyond fp16 does
+// not fit and is reported).
+template <class C>
+__device__ bool load_q(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq, int lane) {
+  constexpr int CH = C::D / 8;  // 16-byte chunks of a row
+  uint32_t taken = 0;
+  QSlots qs;
+  Item it;
+  for (;;) {
+    if (!take_item<C>(a, bar, iq, taken, it, lane)) return false;
+    if (it.end) return true;
+    qs.next(it.rows);
+    for (int i = 0; i < 2; ++i)
+      if (qs.uses_slot(i) && !mbar_wait(&bar.q_empty[i], (qs.uses[i] & 1) ^ 1, a.wait_ns)) return false;
+    uint8_t *base = smem + C::OFF_Q + qs.slot * (C::QB / 2);
+    const int half = qs.big ? C::QHALF : C::QHALF / 2;
+    float big = 0.f;
+    for (int i = lane; i < it.rows * CH; i += 32) {
+      const int R = i / CH, ch = i % CH;
+      const int sq = R / a.g;
+      const uint16_t *src =
+          a.q + (static_cast<int64_t>(it.seq0 + sq) * a.num_q + it.kvh * a.g + (R - sq * a.g)) * C::D + ch * 8;
+      uint8_t *dst = base + (ch >> 3) * half + R * 128 + (((ch & 7) ^ (R & 7)) << 4);
+      if constexpr (C::KV8) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src));
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float f0 = bf16lo(w[e]), f1 = bf16hi(w[e]);
+          const float f = fmaxf(fabsf(f0), fabsf(f1));
+          if (f <= FLT_MAX) big = fmaxf(big, f);
+          o[e] = pack_f16x2(f0, f1);
+        }
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+      } else {
+        cp_async16(dst, src, true);
       }
-      mbar_wait(&full[st], p, a.wait_ns);
+    }
+    if (C::KV8 && big >= 65520.f) report_error(a.err, nullptr, kErrFp16Range);
+    cp_async_commit();
+    cp_async_wait<0>();
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0)
+      for (int i = 0; i < 2; ++i)
+        if (qs.uses_slot(i)) mbar_arrive(&bar.q_full[i]);
+    qs.done();
+  }
+}
+
+// Warps 12-13 (8-bit caches): landed bytes to fp16 tiles, exact; V rows past
+// the item's keys zeroed (they may hold anything, and 0 * NaN is NaN).
+template <class C>
+__device__ bool widen(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq, int ct, int lane) {
+  constexpr int CPR = C::D / 16;  // 16-byte chunks of a row of bytes
+  uint32_t taken = 0, step = 0;
+  Item it;
+  for (;;) {
+    if (!take_item<C>(a, bar, iq, taken, it, lane)) return false;
+    if (it.end) return true;
+    for (int b = 0; b < it.nblk; b += BPT, ++step) {
+      const int rows = min(BPT, it.nblk - b) * 16;
+      const int keep = it.kend - (it.key0 + b * 16);  // rows of the item's keys
+      const uint32_t ls = step % C::NL, lp = (step / C::NL) & 1, ts = step % C::NT, tp = (step / C::NT) & 1;
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        if (!mbar_wait(v ? &bar.lv_full[ls] : &bar.lk_full[ls], lp, a.wait_ns)) return false;
+        if (!mbar_wait(v ? &bar.v_empty[ts] : &bar.k_empty[ts], tp ^ 1, a.wait_ns)) return false;
+        const uint8_t *src = smem + (v ? C::OFF_LV : C::OFF_LK) + ls * C::LB;
+        uint8_t *dst = smem + (v ? C::OFF_V : C::OFF_K) + ts * C::TB;
+        constexpr int ILP = 4;
+        for (int u0 = ct; u0 < rows * CPR; u0 += 64 * ILP) {
+          uint4 x[ILP];
+#pragma unroll
+          for (int k = 0; k < ILP; ++k)
+            if (u0 + 64 * k < rows * CPR) x[k] = *reinterpret_cast<const uint4 *>(src + (u0 + 64 * k) * 16);
+#pragma unroll
+          for (int k = 0; k < ILP; ++k) {
+            const int u = u0 + 64 * k;
+            if (u >= rows * CPR) break;
+            const int r = u / CPR, c = u % CPR;  // dims 16 c .. 16 c + 15 of row r
+            const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            uint32_t o[8];
+            const bool zero = v && r >= keep;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              o[2 * e] = zero ? 0u : fp8x2_to_f16x2<C::KVT>(static_cast<uint16_t>(w[e] & 0xffffu));
+              o[2 * e + 1] = zero ? 0u : fp8x2_to_f16x2<C::KVT>(static_cast<uint16_t>(w[e] >> 16));
+            }
+            uint8_t *row = dst + (c >> 2) * C::HB + r * 128;
+            const int k0 = 2 * (c & 3);
+            *reinterpret_cast<uint4 *>(row + ((k0 ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(row + (((k0 + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(v ? &bar.lv_empty[ls] : &bar.lk_empty[ls]);
+          mbar_arrive(v ? &bar.v_full[ts] : &bar.k_full[ts]);
+        }
+      }
     }
   }
 }
 
-template <class C>
-__device__ void consume(const Args &a, uint8_t *ring, const Stage *hdr, uint64_t *full, uint64_t *empty, float *red,
-                        uint64_t *join_bar, int warp, int lane) {
-  constexpr int D = C::D;
-  constexpr int KVT = C::KVT;
-  constexpr int KS = D / 16;  // k-steps of Q K^T
-  constexpr int NT = D / 8;   // n-tiles of P V
-  const int r = lane >> 2, c = lane & 3;
-  const int lm = lane >> 3, lr = lane & 7;
-  uint32_t qa[KS][4];
-  float o[NT][4];
-  float m[2], l[2];
-  int lim[2];
-  float qsc = 0.f;
-  int rg = 0, kg = 0, RG = 1, KG = 1;
-  bool busy = false;
-  uint32_t joins = 0;  // phases of join_bar so far
-  int stage = 0;
-  uint32_t par = 0;
-  for (;;) {
-    if (!mbar_wait(&full[stage], par, a.wait_ns)) {
-      if (lane == 0) report_error(a.err, nullptr, kErrWaitTimeout);
-      return;
-    }
-    const Stage h = hdr[stage];
-    if (h.kind != 0) return;
-    if (h.flags & kFirst) {
-      RG = h.rows <= 16 ? 1 : h.rows <= 32 ? 2 : h.rows <= 64 ? 4 : 8;
-      KG = NC / RG;
-      rg = warp % RG;
-      kg = warp / RG;
-      busy = rg * 16 < h.rows;
-      qsc = a.k_scales ? a.qscale0 * __ldg(a.k_scales + h.kvh) : a.qscale;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        m[e] = -INFINITY;
-        l[e] = 0.f;
-        lim[e] = h.kend;
-      }
-#pragma unroll
-      for (int t = 0; t < NT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
-      if (busy) {
-        float big = 0.f;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int R = rg * 16 + r + 8 * e;
-          const bool live = R < h.rows;
-          const int s = h.seq0 + (live ? R / a.g : 0);
-          if (h.prefix) lim[e] = live ? min(h.kend, a.seqs[s].len) : 0;
-          const uint16_t *src = a.q + (static_cast<int64_t>(s) * a.num_q + h.kvh * a.g + (live ? R % a.g : 0)) * D;
-#pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            if constexpr (kv16(KVT)) {
-              // fragment columns 2c, 2c + 1 and 2c + 8, 2c + 9 are those dims
-              qa[k][e] = live ? __ldg(reinterpret_cast<const uint32_t *>(src + 16 * k + 2 * c)) : 0u;
-              qa[k][e + 2] = live ? __ldg(reinterpret_cast<const uint32_t *>(src + 16 * k + 2 * c + 8)) : 0u;
-            } else {
-              // an 8-bit K fragment's four bytes are dims 4c .. 4c + 3
-              uint2 x = make_uint2(0, 0);
-              if (live) x = __ldg(reinterpret_cast<const uint2 *>(src + 16 * k + 4 * c));
-              const float f0 = bf16lo(x.x), f1 = bf16hi(x.x), f2 = bf16lo(x.y), f3 = bf16hi(x.y);
-              big = fmaxf(big, fmaxf(fmaxf(fabsf(f0), fabsf(f1)), fmaxf(fabsf(f2), fabsf(f3))));
-              qa[k][e] = pack_f16x2(f0, f1);
-              qa[k][e + 2] = pack_f16x2(f2, f3);
-            }
-          }
-        }
-        // a finite query beyond fp16 does not fit the widened products
-        if (!kv16(KVT) && big >= 65520.f && big <= FLT_MAX) report_error(a.err, nullptr, kErrFp16Range);
-      }
-    }
-    if (busy) {
-      const uint8_t *Ks = ring + static_cast<size_t>(stage) * C::STAGEB;
-      for (int b = 0; b < h.nblk; ++b) {
-        if ((h.blk + b) % KG != kg) continue;
-        const uint32_t kt = smem_u32(Ks + b * C::TILEB);
-        const uint32_t vt = smem_u32(Ks + C::KVB + b * C::TILEB);
-        // ---- S (16 rows x 16 tokens, two n-tiles of 8) = Q K^T
-        float s[2][4];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-        if constexpr (kv16(KVT)) {
-#pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            uint32_t b0, b1, b2, b3;  // (tokens 0-7, dims 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15)
-            ldmatrix_x4(b0, b1, b2, b3, kt + dec::swz_off<C::ROWB, 1>(lr + (lm >> 1) * 8, 2 * k + (lm & 1)));
-            mma16_16816<KVT>(s[0], qa[k][0], qa[k][1], qa[k][2], qa[k][3], b0, b1);
-            mma16_16816<KVT>(s[1], qa[k][0], qa[k][1], qa[k][2], qa[k][3], b2, b3);
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < KS; k += 2) {
-            uint32_t x0, x1, x2, x3;  // 16-byte chunks k and k + 1 of tokens 0-7 and 8-15
-            ldmatrix_x4(x0, x1, x2, x3, kt + dec::swz_off<C::ROWB, 1>(lr + (lm & 1) * 8, k + (lm >> 1)));
-            const uint32_t w[4] = {x0, x1, x2, x3};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t lo = fp8x2_to_f16x2<KVT>(static_cast<uint16_t>(w[i] & 0xffffu));
-              const uint32_t hi = fp8x2_to_f16x2<KVT>(static_cast<uint16_t>(w[i] >> 16));
-              const int kk = k + (i >> 1);
-              mma_f16_16816(s[i & 1], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], lo, hi);
-            }
-          }
-        }
-        // ---- scores in log2 units, keys past a row's limit out
-        const int key = h.key0 + 16 * b;
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[n][e] *= qsc;
-        if (h.prefix || key + 16 > h.kend) {
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (key + 8 * n + 2 * c + (e & 1) >= lim[e >> 1]) s[n][e] = -INFINITY;
-        }
-        // ---- the running maximum: raised only when a score is far above it
-        const float t0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-        const float t1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-        if (__any_sync(0xffffffffu, t0 > m[0] + kRaise || t1 > m[1] + kRaise)) {
-          float x[2] = {t0, t1};
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 1));
-            x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 2));
-            const float mn = fmaxf(m[e], x[e]);
-            const float f = mn == m[e] ? 1.f : exp2f(m[e] - mn);
-            m[e] = mn;
-            l[e] *= f;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              o[t][2 * e] *= f;
-              o[t][2 * e + 1] *= f;
-            }
-          }
-        }
-        // ---- P = 2^(s - m + PB), as a hi + lo pair
-        uint32_t ph[4], pl[4];
-        const float mu0 = (m[0] == -INFINITY ? 0.f : m[0]) - C::PB, mu1 = (m[1] == -INFINITY ? 0.f : m[1]) - C::PB;
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float p0 = ex2_approx(s[n][0] - mu0), p1 = ex2_approx(s[n][1] - mu0);
-          const float p2 = ex2_approx(s[n][2] - mu1), p3 = ex2_approx(s[n][3] - mu1);
-          l[0] += p0 + p1;
-          l[1] += p2 + p3;
-          constexpr int PT = KVT == kKvBf16 ? kKvBf16 : kKvF16;
-          ph[2 * n] = pack16x2<PT>(p0, p1);
-          ph[2 * n + 1] = pack16x2<PT>(p2, p3);
-          pl[2 * n] = pack16x2<PT>(p0 - lo16<PT>(ph[2 * n]), p1 - hi16<PT>(ph[2 * n]));
-          pl[2 * n + 1] = pack16x2<PT>(p2 - lo16<PT>(ph[2 * n + 1]), p3 - hi16<PT>(ph[2 * n + 1]));
-        }
-        // ---- O += P V.  Tokens past the item's keys may hold anything, NaN
-        // included, which a zero probability does not cancel: zeroed in V
-        const int vt0 = h.kend - key;
-        auto keep = [&](int t) { return t < vt0; };
-        uint32_t mk0 = 0xffffffffu, mk1 = 0xffffffffu;
-        if (vt0 < 16) {
-          mk0 = (keep(2 * c) ? 0xffffu : 0u) | (keep(2 * c + 1) ? 0xffff0000u : 0u);
-          mk1 = (keep(2 * c + 8) ? 0xffffu : 0u) | (keep(2 * c + 9) ? 0xffff0000u : 0u);
-        }
-        if constexpr (kv16(KVT)) {
-#pragma unroll
-          for (int t = 0; t < NT; t += 2) {
-            uint32_t b0, b1, b2, b3;  // n-tile t: tokens 0-7, 8-15; n-tile t + 1
-            ldmatrix_x4_trans(b0, b1, b2, b3, vt + dec::swz_off<C::ROWB, 1>(lr + (lm & 1) * 8, t + (lm >> 1)));
-            b0 &= mk0;
-            b1 &= mk1;
-            b2 &= mk0;
-            b3 &= mk1;
-            mma16_16816<KVT>(o[t], ph[0], ph[1], ph[2], ph[3], b0, b1);
-            mma16_16816<KVT>(o[t + 1], ph[0], ph[1], ph[2], ph[3], b2, b3);
-            mma16_16816<KVT>(o[t], pl[0], pl[1], pl[2], pl[3], b0, b1);
-            mma16_16816<KVT>(o[t + 1], pl[0], pl[1], pl[2], pl[3], b2, b3);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < KS; j += 2) {
-            uint32_t x0, x1, x2, x3;  // 16-byte chunks j, j + 1 of tokens 0-7 and 8-15
-            ldmatrix_x4_trans(x0, x1, x2, x3, vt + dec::swz_off<C::ROWB, 1>(lr + (lm & 1) * 8, j + (lm >> 1)));
-            const uint32_t w[4] = {x0, x1, x2, x3};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              // bytes (token 2c: dims 2r, 2r + 1), (token 2c + 1: the same)
-              // to token pairs: dims 16 j + 2r (even n-tile) and 2r + 1 (odd)
-              const uint32_t y0 = __byte_perm(w[2 * i], 0, 0x3120), y1 = __byte_perm(w[2 * i + 1], 0, 0x3120);
-              const uint32_t e0 = fp8x2_to_f16x2<KVT>(static_cast<uint16_t>(y0 & 0xffffu)) & mk0;
-              const uint32_t e1 = fp8x2_to_f16x2<KVT>(static_cast<uint16_t>(y1 & 0xffffu)) & mk1;
-              const uint32_t d0 = fp8x2_to_f16x2<KVT>(static_cast<uint16_t>(y0 >> 16)) & mk0;
-              const uint32_t d1 = fp8x2_to_f16x2<KVT>(static_cast<uint16_t>(y1 >> 16)) & mk1;
-              const int t = 2 * (j + i);
-              mma_f16_16816(o[t], ph[0], ph[1], ph[2], ph[3], e0, e1);
-              mma_f16_16816(o[t + 1], ph[0], ph[1], ph[2], ph[3], d0, d1);
-              mma_f16_16816(o[t], pl[0], pl[1], pl[2], pl[3], e0, e1);
-              mma_f16_16816(o[t + 1], pl[0], pl[1], pl[2], pl[3], d0, d1);
-            }
-          }
-        }
-      }
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[stage]);
-    if (++stage == C::NS) {
-      stage = 0;
-      par ^= 1;
-    }
-    if (!(h.flags & kLast)) continue;
+// Whether the phase of `bar` with the given parity has completed (no waiting).
+__device__ __forceinline__ bool mbar_done(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 
-    // ---- the piece's result
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-    }
-    // the key groups' states join pairwise: of 2 n RG warps the upper half
-    // hands its states to the lower half.  In the first round warp i + n RG
-    // writes slot i; later a warp writes the slot it read in the first round,
-    // so that a slot has no reader when it is written.  Every round ends at
-    // one barrier of all consumer warps, and the next join starts behind the
-    // last one's end.
-    if (KG > 1) {
-      if (joins > 0 && !mbar_wait(join_bar, (joins - 1) & 1, a.wait_ns)) {
-        if (lane == 0) report_error(a.err, nullptr, kErrWaitTimeout);
-        return;
+// Warp 0, one thread: the products, in step order.
+template <class C>
+__device__ bool issue_mma(const Args &a, uint32_t sbase, uint32_t tmem, Bars<C> &bar, const Item *iq) {
+  // 16-bit caches: the landed tiles feed the products
+  uint64_t *k_full = C::KV8 ? bar.k_full : bar.lk_full, *k_empty = C::KV8 ? bar.k_empty : bar.lk_empty;
+  uint64_t *v_full = C::KV8 ? bar.v_full : bar.lv_full, *v_empty = C::KV8 ? bar.v_empty : bar.lv_empty;
+  struct Step {
+    uint32_t k;      // number of the step in the CTA
+    int nblk;
+    int obuf;        // output buffer of its item
+    uint32_t item;   // number of its item
+    bool first, last;
+  };
+  uint32_t taken = 0, steps = 0;
+  int left = 0;             // blocks of the current item not yet in a step
+  bool fresh = false, ended = false;
+  QSlots qs;
+  uint32_t qbase = 0, qhalf = 0;
+  // the next step, once its K (and for an item's first step its Q) is there:
+  // 1 it is, 0 not yet (only if !block), 2 no more steps, -1 a wait ran out
+  auto fetch = [&](Step &s, bool block) -> int {
+    if (ended) return 2;
+    auto there = [&](uint64_t *b, uint32_t ph) {
+      return block ? mbar_wait(b, ph, a.wait_ns) : mbar_done(b, ph);
+    };
+    if (left == 0) {
+      const uint32_t st = taken % NIQ;
+      if (!there(&bar.iq_full[st], (taken / NIQ) & 1)) return block ? -1 : 0;
+      const int end = iq[st].end, rows = iq[st].rows;
+      left = iq[st].nblk;
+      mbar_arrive(&bar.iq_empty[st]);
+      ++taken;
+      if (end) {
+        ended = true;
+        return 2;
       }
-      bool first = true;
-      for (int half = NC / 2; half >= RG; half >>= 1, first = false) {  // half: off * RG warps read
-        if (warp >= half && warp < 2 * half && busy) {
-          float *x = red + (first ? warp - half : warp) * C::REDW + lane;
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[(4 * t + e) * 32] = o[t][e];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            x[(4 * NT + e) * 32] = m[e];
-            x[(4 * NT + 2 + e) * 32] = l[e];
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(join_bar);
-        if (!mbar_wait(join_bar, joins & 1, a.wait_ns)) {
-          if (lane == 0) report_error(a.err, nullptr, kErrWaitTimeout);
-          return;
-        }
-        ++joins;
-        if (warp < half && busy) {
-          const float *x = red + (first ? warp : warp + half) * C::REDW + lane;
-          float f0[2], f1[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float m2 = x[(4 * NT + e) * 32], l2 = x[(4 * NT + 2 + e) * 32];
-            const float mn = fmaxf(m[e], m2);
-            f0[e] = m[e] == mn ? 1.f : exp2f(m[e] - mn);
-            f1[e] = m2 == mn ? 1.f : exp2f(m2 - mn);
-            l[e] = l[e] * f0[e] + l2 * f1[e];
-            m[e] = mn;
-          }
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[t][e] = o[t][e] * f0[e >> 1] + x[(4 * t + e) * 32] * f1[e >> 1];
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(join_bar);
-      ++joins;
+      qs.next(rows);
+      qbase = sbase + C::OFF_Q + qs.slot * (C::QB / 2);
+      qhalf = qs.big ? C::QHALF : C::QHALF / 2;
+      fresh = true;
     }
-    if (kg != 0 || !busy) continue;
+    if (fresh)
+      for (int i = 0; i < 2; ++i)
+        if (qs.uses_slot(i) && !there(&bar.q_full[i], qs.uses[i] & 1)) return block ? -1 : 0;
+    if (!there(&k_full[steps % C::NT], (steps / C::NT) & 1)) return block ? -1 : 0;
+    s.k = steps++;
+    s.nblk = min(left, BPT);
+    left -= s.nblk;
+    s.first = fresh;
+    s.last = left == 0;
+    s.item = taken - 1;
+    s.obuf = s.item & 1;
+    fresh = false;
+    return 1;
+  };
+  auto qk = [&](const Step &s) {
+    tc_fence_after_sync();
+    const uint32_t kbase = sbase + C::OFF_K + (s.k % C::NT) * C::TB;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int R = rg * 16 + r + 8 * e;
-      if (R >= h.rows) continue;
-      const int s = h.seq0 + R / a.g, hd = h.kvh * a.g + R % a.g;
-      const int64_t row = static_cast<int64_t>(s) * a.num_q + hd;
+    for (int kk = 0; kk < C::D / 16; ++kk) {
+      const uint64_t ad = umma_desc_sw128(qbase + (kk >> 2) * qhalf + (kk & 3) * 32, 16, 1024);
+      const uint64_t bd = umma_desc_sw128(kbase + (kk >> 2) * C::HB + (kk & 3) * 32, 16, 1024);
+      umma_bf16_ss(tmem + C::S_COL + (s.k & 1) * KT, ad, bd, C::IDESC_QK, kk > 0 ? 1u : 0u);
+    }
+    umma_commit(&bar.s_full[s.k & 1]);
+    umma_commit(&k_empty[s.k % C::NT]);
+    if (s.last) {
+      for (int i = 0; i < 2; ++i)
+        if (qs.uses_slot(i)) umma_commit(&bar.q_empty[i]);
+      qs.done();
+    }
+  };
+  auto pv = [&](const Step &s) -> bool {
+    if (!mbar_wait_hint(&bar.p_full[s.k & 1], (s.k >> 1) & 1, a.wait_ns)) return false;
+    // an item's first product overwrites the output buffer of the item two before
+    if (s.first && !mbar_wait(&bar.o_empty[s.obuf], ((s.item >> 1) & 1) ^ 1, a.wait_ns)) return false;
+    if (!mbar_wait(&v_full[s.k % C::NT], (s.k / C::NT) & 1, a.wait_ns)) return false;
+    tc_fence_after_sync();
+    const uint32_t vbase = sbase + C::OFF_V + (s.k % C::NT) * C::TB;
+    const uint32_t p = tmem + C::S_COL + (s.k & 1) * KT;
+    for (int kk = 0; kk < s.nblk; ++kk) {
+      // keys 16 kk .. 16 kk + 15: hi at +0, lo at +16 of their 32-column chunk
+      const uint64_t bd = umma_desc_sw128(vbase + kk * 2048, C::HB, 1024);
+      const uint32_t ap = p + (kk >> 1) * 32 + (kk & 1) * 8;
+      umma_bf16_ts(tmem + C::O_COL + s.obuf * C::D, ap, bd, C::IDESC_PV, (s.first && kk == 0) ? 0u : 1u);
+      umma_bf16_ts(tmem + C::O_COL + s.obuf * C::D, ap + 16, bd, C::IDESC_PV, 1u);
+    }
+    umma_commit(&v_empty[s.k % C::NT]);
+    if (s.last) umma_commit(&bar.o_full[s.obuf]);
+    return true;
+  };
+  Step cur, nxt;
+  int r = fetch(cur, true);
+  if (r == 1) qk(cur);
+  while (r == 1) {
+    // the next step's scores first, if its operands are there
+    int n = fetch(nxt, false);
+    if (n == 1) qk(nxt);
+    if (!pv(cur)) return false;
+    if (n == 0) {
+      n = fetch(nxt, true);
+      if (n == 1) qk(nxt);
+    }
+    if (n < 0) return false;
+    cur = nxt;
+    r = n;
+  }
+  return r == 2;
+}
+
+// Warps 4-11: softmax and outputs.  Warps 4-7 take keys 0-63 and warps 8-11
+// keys 64-127 of every step; a thread holds row 32 (warp % 4) + lane (its
+// TMEM lane) and its half h of the keys, later its half of the columns.
+// Partner warps w and w + 4 agree at their named barrier on every wait, so
+// that both go on or both stop.
+template <class C>
+__device__ bool softmax(const Args &a, uint8_t *smem, uint32_t tmem, Bars<C> &bar, const Item *iq, int warp,
+                        int lane) {
+  constexpr int D = C::D;
+  constexpr int PT = C::BF16 ? kKvBf16 : kKvF16;  // type of P
+  const int h = (warp - 4) >> 2;
+  const int row = ((warp & 3) << 5) | lane;
+  const int pair = 1 + (warp & 3);
+  const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+  float *xch = reinterpret_cast<float *>(smem + C::OFF_X);
+  uint64_t *v_full = C::KV8 ? bar.v_full : bar.lv_full, *v_empty = C::KV8 ? bar.v_empty : bar.lv_empty;
+  uint32_t taken = 0, k = 0;
+  bool ok = true;
+  // the finished item whose output waits for the next step to be under way
+  bool pend = false;
+  Item pit;
+  float pm = 0.f, pl = 0.f;
+  uint32_t pnum = 0;
+
+  auto finish = [&]() {
+    pend = false;
+    const int obuf = pnum & 1;
+    const bool mine = (warp & 3) * 32 < pit.rows;  // rows of this warp's lanes live
+    float lsum = pl;
+    if (mine) {
+      named_bar_sync(pair, 64);  // the partner has read the last maxima
+      xch[h * MAXROWS + row] = pl;
+      named_bar_sync(pair, 64);
+      lsum += xch[(h ^ 1) * MAXROWS + row];
+    }
+    ok = mbar_wait(&bar.o_full[obuf], (pnum >> 1) & 1, a.wait_ns) && ok;
+    if (mine && ok) {
+      tc_fence_after_sync();
+      const bool live = row < pit.rows;
+      const int sq = row / a.g;
+      const int64_t orow = static_cast<int64_t>(pit.seq0 + sq) * a.num_q + pit.kvh * a.g + (row - sq * a.g);
       float *dst, *dl;
-      if (h.to == kToCut) {
-        const int64_t x = static_cast<int64_t>(h.slot) * a.slot_rows + R;
+      if (pit.to == kToCut) {
+        const int64_t x = static_cast<int64_t>(pit.slot) * a.slot_rows + row;
         dst = a.cut_o + x * D;
         dl = a.cut_lse + x;
       } else {
-        dst = (h.to == kToOut ? a.out : h.to == kToPre ? a.pre_o : a.own_o) + row * D;
-        dl = h.to == kToOut ? (a.lse ? a.lse + row : nullptr) : (h.to == kToPre ? a.pre_lse : a.own_lse) + row;
+        dst = (pit.to == kToOut ? a.out : pit.to == kToPre ? a.pre_o : a.own_o) + orow * D;
+        dl = pit.to == kToOut ? (a.lse ? a.lse + orow : nullptr) : (pit.to == kToPre ? a.pre_lse : a.own_lse) + orow;
       }
-      // no key (a sequence shorter than the prefix's first block): nothing to weigh
-      const bool none = l[e] == 0.f;
-      float inv = none ? 0.f : 1.f / l[e];
-      if (h.to == kToOut) inv *= a.v_scales ? __ldg(a.v_scales + h.kvh) : a.vscale;
-      const float ls = none ? -INFINITY : m[e] + log2f(l[e]) - C::PB;
-      if (dl && c == 0) *dl = h.to == kToOut ? ls * kLn2 : ls;
-      if constexpr (kv16(KVT)) {
+      // no key (a sequence shorter than the piece's first one): nothing to weigh
+      const bool none = lsum == 0.f;
+      float inv = none ? 0.f : 1.f / lsum;
+      if (pit.to == kToOut) inv *= a.v_scales ? __ldg(a.v_scales + pit.kvh) : a.vscale;
+#pragma unroll 1
+      for (int c0 = h * (D / 2); c0 < (h + 1) * (D / 2); c0 += 32) {
+        float o[32];
+        tmem_ld32(trow + C::O_COL + obuf * D + c0, o);
+        if (live) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-          *reinterpret_cast<float2 *>(dst + 8 * t + 2 * c) =
-              none ? make_float2(0.f, 0.f) : make_float2(o[t][2 * e] * inv, o[t][2 * e + 1] * inv);
-      } else {
-#pragma unroll
-        for (int t = 0; t < NT; t += 2)  // columns 2c, 2c + 1 of the even and odd n-tiles: dims 4c .. 4c + 3
-          *reinterpret_cast<float4 *>(dst + 8 * t + 4 * c) =
-              none ? make_float4(0.f, 0.f, 0.f, 0.f)
-                   : make_float4(o[t][2 * e] * inv, o[t + 1][2 * e] * inv, o[t][2 * e + 1] * inv,
-                                 o[t + 1][2 * e + 1] * inv);
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4 *>(dst + c0 + i) =
+                none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                     : make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
+        }
+      }
+      if (live && h == 0 && dl) {
+        const float ls = none ? -INFINITY : pm + log2f(lsum) - C::PB;
+        *dl = pit.to == kToOut ? ls * kLn2 : ls;
       }
     }
+    tc_fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar.o_empty[obuf]);
+  };
+
+  for (;;) {
+    Item it;
+    const bool got = take_item<C>(a, bar, iq, taken, it, lane);
+    if (!named_bar_and(pair, 64, got && ok)) return false;
+    if (it.end) break;
+    const bool mine = (warp & 3) * 32 < it.rows;
+    const bool live = row < it.rows;
+    int lim = live ? it.kend : 0;  // keys from here on are not the row's
+    if (live && it.prefix) lim = min(lim, a.seqs[it.seq0 + row / a.g].len);
+    float qsc = a.k_scales ? a.qscale0 * __ldg(a.k_scales + it.kvh) : a.qscale;
+    // the maximum is taken of the scores as they are, so a scale that is not
+    // positive goes into them first (and masked scores never meet a 0)
+    const float sgn = qsc < 0.f ? -1.f : 0.f;
+    const bool turn = !(qsc > 0.f);
+    if (turn) qsc = qsc < 0.f ? -qsc : 1.f;
+    float m = -INFINITY, l = 0.f;
+    for (int b = 0; b < it.nblk; b += BPT, ++k) {
+      const int n = min(BPT, it.nblk - b);
+      const int key0 = it.key0 + b * 16;
+      bool there = mbar_wait_hint(&bar.s_full[k & 1], (k >> 1) & 1, a.wait_ns);
+      tc_fence_after_sync();
+      if (!C::KV8 && it.kend < key0 + n * 16) {
+        // V rows past the item's keys may hold anything (0 * NaN is NaN)
+        there = there && mbar_wait(&v_full[k % C::NT], (k / C::NT) & 1, a.wait_ns);
+        const int keep = it.kend - key0;
+        const int i = threadIdx.x - 128;
+        if (there && i < (n * 16 - keep) * C::HALVES * 8) {
+          const int r = keep + i / (C::HALVES * 8), c = i % (C::HALVES * 8);
+          *reinterpret_cast<uint4 *>(smem + C::OFF_V + (k % C::NT) * C::TB + (c >> 3) * C::HB + r * 128 +
+                                     (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
+      if (!named_bar_and(pair, 64, there && ok)) return false;
+      if (mine) {
+        const uint32_t scol = trow + C::S_COL + (k & 1) * KT + 64 * h;
+        uint32_t sc[2][32];
+        tmem_ld32_async(scol, sc[0]);
+        tmem_ld32_async(scol + 32, sc[1]);
+        tmem_wait_ld(sc[0]);
+        tmem_wait_ld(sc[1]);
+        const int kh = key0 + 64 * h;
+        if (turn) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            sc[0][i] = __float_as_uint(__uint_as_float(sc[0][i]) * sgn);
+            sc[1][i] = __float_as_uint(__uint_as_float(sc[1][i]) * sgn);
+          }
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (kh + 32 * c + 32 > lim) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (kh + 32 * c + i >= lim) sc[c][i] = __float_as_uint(-INFINITY);
+          }
+          float t[11];  // a tree of three-input maxima
+#pragma unroll
+          for (int i = 0; i < 10; ++i)
+            t[i] = fmax3(__uint_as_float(sc[c][3 * i]), __uint_as_float(sc[c][3 * i + 1]),
+                         __uint_as_float(sc[c][3 * i + 2]));
+          t[10] = fmaxf(__uint_as_float(sc[c][30]), __uint_as_float(sc[c][31]));
+          mx = fmax3(mx, fmax3(fmax3(t[0], t[1], t[2]), fmax3(t[3], t[4], t[5]), fmax3(t[6], t[7], t[8])),
+                     fmaxf(t[9], t[10]));
+        }
+        // the row's maximum over both halves (the barrier behind the wait above
+        // says that the partner has read the last exchange)
+        xch[h * MAXROWS + row] = mx;
+        named_bar_sync(pair, 64);
+        mx = fmaxf(mx, xch[(h ^ 1) * MAXROWS + row]);
+        mx = mx == -INFINITY ? mx : mx * qsc;
+        const bool raise = mx > m + kRaise;  // m = -inf: any finite score
+        if (__any_sync(0xffffffffu, raise && m != -INFINITY)) {
+          // rare: this half of O's columns takes the new maximum; the product
+          // of the step before, which releases its V tile, is through
+          if (b > 0) ok = mbar_wait(&v_empty[(k - 1) % C::NT], ((k - 1) / C::NT) & 1, a.wait_ns) && ok;
+          tc_fence_after_sync();
+          const float f = (raise && m != -INFINITY) ? exp2f(m - mx) : 1.f;
+          l *= f;
+#pragma unroll 1
+          for (int c0 = h * (D / 2); c0 < (h + 1) * (D / 2); c0 += 32) {
+            float o[32];
+            tmem_ld32(trow + C::O_COL + ((taken - 1) & 1) * D + c0, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= f;
+            tmem_st32(trow + C::O_COL + ((taken - 1) & 1) * D + c0, o);
+          }
+        }
+        if (raise) m = mx;
+        // P = 2^(score - m + PB) in pairs; 32 keys become 16 columns of hi
+        // pairs and 16 of lo pairs over their own, loaded, scores
+        const float off = C::PB - (m == -INFINITY ? 0.f : m);
+        const uint64_t q2 = f2_pack(qsc, qsc), o2 = f2_pack(off, off);
+        uint64_t ls[2] = {0, 0};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 y = f2_unpack(
+                f2_fma(f2_pack(__uint_as_float(sc[c][2 * e]), __uint_as_float(sc[c][2 * e + 1])), q2, o2));
+            const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
+            const uint64_t pp = f2_pack(p0, p1);
+            ls[e & 1] = f2_add(ls[e & 1], pp);
+            hi[e] = pack16x2<PT>(p0, p1);
+            const float2 d = f2_unpack(f2_sub(pp, f2_pack(lo16<PT>(hi[e]), hi16<PT>(hi[e]))));
+            lo[e] = pack16x2<PT>(d.x, d.y);
+          }
+          tmem_st16_async(scol + 32 * c, hi);
+          tmem_st16_async(scol + 32 * c + 16, lo);
+        }
+        const float2 l2 = f2_unpack(f2_add(ls[0], ls[1]));
+        l += l2.x + l2.y;
+        tmem_wait_st();
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.p_full[k & 1]);
+      if (pend) finish();
+    }
+    pend = true;
+    pit = it;
+    pm = m;
+    pl = l;
+    pnum = taken - 1;
   }
+  if (pend) finish();
+  return ok;
 }
 
 template <int D, int KVT>
-__global__ void __launch_bounds__(NTHREADS, 1) shared_attend_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel(const __grid_constant__ Args a) {
   using C = Cfg<D, KVT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *ring = smem;
-  float *red = reinterpret_cast<float *>(smem + static_cast<size_t>(C::NS) * C::STAGEB);
-  Stage *hdr = reinterpret_cast<Stage *>(red + C::NRED * C::REDW);
-  uint64_t *full = reinterpret_cast<uint64_t *>(hdr + C::NS);
-  uint64_t *empty = full + C::NS;
-  uint64_t *join_bar = empty + C::NS;
-  static_assert(C::NS * (sizeof(Stage) + 16) + 8 <= 2048, "headers and barriers");
+  Bars<C> &bar = *reinterpret_cast<Bars<C> *>(smem + C::OFF_BAR);
+  static_assert(sizeof(Bars<C>) <= C::BARB, "barriers");
+  Item *iq = reinterpret_cast<Item *>(smem + C::OFF_IQ);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::NS; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], NC);
+    for (int i = 0; i < NIQ; ++i) {
+      mbar_init(&bar.iq_full[i], 1);
+      mbar_init(&bar.iq_empty[i], 1 + 1 + 1 + 8 + C::NCONV);  // the roles that take items
     }
-    mbar_init(join_bar, NC);
+    for (int i = 0; i < C::NL; ++i) {
+      mbar_init(&bar.lk_full[i], 1);
+      mbar_init(&bar.lk_empty[i], C::KV8 ? C::NCONV : 1);
+      mbar_init(&bar.lv_full[i], 1);
+      mbar_init(&bar.lv_empty[i], C::KV8 ? C::NCONV : 1);
+    }
+    for (int i = 0; i < C::NT; ++i) {
+      mbar_init(&bar.k_full[i], C::KV8 ? C::NCONV : 1);
+      mbar_init(&bar.k_empty[i], 1);
+      mbar_init(&bar.v_full[i], C::KV8 ? C::NCONV : 1);
+      mbar_init(&bar.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.q_full[i], 1);
+      mbar_init(&bar.q_empty[i], 1);
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_full[i], 8);
+      mbar_init(&bar.o_full[i], 1);
+      mbar_init(&bar.o_empty[i], 8);
+    }
+    mbar_init(&bar.drain, 1);
     fence_mbar_init();
   }
+  if (warp == 0) tmem_alloc(&bar.tmem, C::TMEM_COLS);
+  tc_fence_before_sync();
   __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = bar.tmem;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (warp == NC)
-    produce<C>(a, ring, hdr, full, empty, lane);
-  else
-    consume<C>(a, ring, hdr, full, empty, red, join_bar, warp, lane);
+  bool ok = true;
+  if (warp == 0) {
+    if (lane == 0) ok = issue_mma<C>(a, smem_u32(smem), tmem, bar, iq);
+    __syncwarp();
+  } else if (warp == 1) {
+    ok = walk<C>(a, smem, bar, iq, lane);
+  } else if (warp == 2) {
+    ok = copy_v<C>(a, smem, bar, iq, lane);
+  } else if (warp == 3) {
+    ok = load_q<C>(a, smem, bar, iq, lane);
+  } else if (warp < 12) {
+    ok = softmax<C>(a, smem, tmem, bar, iq, warp, lane);
+  } else if constexpr (C::KV8) {
+    ok = widen<C>(a, smem, bar, iq, threadIdx.x - 12 * 32, lane);
+  }
+  if (!ok && lane == 0) report_error(a.err, nullptr, kErrWaitTimeout);
+  // every product issued completes before the tensor memory is given back
+  if (threadIdx.x == 0) {
+    umma_commit(&bar.drain);
+    mbar_wait(&bar.drain, 0, a.wait_ns);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
 }
 
 // --------------------------------------------------------------------- join
+
+// u / n for the axis (32-bit where it fits)
+__device__ __forceinline__ int axis_cta(long long u, const Axis &x) {
+  if (x.blocks < 0x7fffffffLL) return static_cast<int>(static_cast<unsigned>(u) / static_cast<unsigned>(x.per));
+  return static_cast<int>(u / x.per);
+}
 
 // One warp per (sequence, head): the parts' pieces by log-sum-exp weights.
 // Rows that the attention wrote itself (one uncut part) are left alone.
@@ -828,76 +1103,107 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
   if (row >= static_cast<int64_t>(a.num_seqs) * a.num_q) return;
   const int lane = threadIdx.x & 31;
-  const int s = static_cast<int>(row / a.num_q), h = static_cast<int>(row % a.num_q), kvh = h / a.g;
+  const int s = static_cast<int>(row / a.num_q), h = static_cast<int>(row - static_cast<int64_t>(s) * a.num_q);
+  const int kvh = h / a.g;
   const SeqInfo q = a.seqs[s];
-  constexpr int EPL = D / 32;
-  float *out = a.out + row * D + lane * EPL;
-  if (q.len == 0) {
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) out[e] = 0.f;
-    if (a.lse && lane == 0) a.lse[row] = -INFINITY;
-    return;
+  const Axis ax = *a.axis;
+  constexpr int EPL = D / 32;  // elements of a lane
+  using V = typename std::conditional<EPL == 4, float4, float2>::type;
+  V *out = reinterpret_cast<V *>(a.out + row * D) + lane;
+  // the pieces of the prefix part and of the own part: piece i of a part is
+  // CTA c1 + i's slot (1 where the item begins inside that CTA's range), or
+  // the part's own place if one CTA holds it all
+  int p_c1 = 0, p_n = 0, p_s0 = 0, p_r = 0, o_c1 = 0, o_n = 0, o_s0 = 0;
+  bool p_whole = false, o_whole = false;
+  if (q.fb > 0 && q.len > 0) {
+    const GroupInfo gi = a.groups[q.group];
+    const int i = s - gi.first, tile = i / gi.tile_seqs;
+    const long long u0 = gi.base + static_cast<long long>(tile * a.num_kv + kvh) * gi.nb;
+    p_c1 = axis_cta(u0, ax);
+    p_n = axis_cta(u0 + gi.nb - 1, ax) - p_c1 + 1;
+    p_whole = p_n == 1;
+    p_s0 = u0 > p_c1 * ax.per;
+    p_r = (i - tile * gi.tile_seqs) * a.g + h % a.g;
   }
-  const long long U = *a.units;
+  if (q.nb > 0) {
+    const long long u0 = q.base + static_cast<long long>(kvh) * q.nb;
+    o_c1 = axis_cta(u0, ax);
+    o_n = axis_cta(u0 + q.nb - 1, ax) - o_c1 + 1;
+    o_whole = o_n == 1;
+    o_s0 = u0 > o_c1 * ax.per;
+  }
+  if (q.fb == 0 && o_whole) return;
+  const int n = p_n + o_n;
+  // piece i's output row and log-sum-exp
+  auto piece = [&](int i, const float *&o, const float *&x) {
+    const bool pre = i < p_n;
+    if (pre ? p_whole : o_whole) {
+      o = (pre ? a.pre_o : a.own_o) + row * D;
+      x = (pre ? a.pre_lse : a.own_lse) + row;
+      return;
+    }
+    const int k = pre ? i : i - p_n;
+    const int64_t slot = static_cast<int64_t>((pre ? p_c1 : o_c1) + k) * 2 + (k == 0 ? (pre ? p_s0 : o_s0) : 0);
+    const int64_t at = slot * a.slot_rows + (pre ? p_r : h % a.g);
+    o = a.cut_o + at * D;
+    x = a.cut_lse + at;
+  };
   float M = -INFINITY, W = 0.f, acc[EPL];
 #pragma unroll
   for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
-  auto add = [&](const float *o, float x) {
-    if (x == -INFINITY) return;
-    float v[EPL];
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    // 32 pieces' log-sum-exps at once, a lane each
+    const float *po = a.out, *px = nullptr;
+    float x = -INFINITY;
+    if (i0 + lane < n) {
+      piece(i0 + lane, po, px);
+      x = __ldcg(px);
+    }
+    float mn = fmaxf(M, x);
 #pragma unroll
-    for (int e = 0; e < EPL; e += 2) *reinterpret_cast<float2 *>(v + e) = __ldcg(reinterpret_cast<const float2 *>(o + lane * EPL + e));
-    const float mn = fmaxf(M, x);
-    const float f = M == -INFINITY ? 0.f : exp2f(M - mn), w = exp2f(x - mn);
+    for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    const float f = M == mn ? 1.f : exp2f(M - mn);  // 0 for the first pieces
+    const float w = x == -INFINITY ? 0.f : exp2f(x - mn);  // a NaN stays one
+    float ws = w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
+    W = W * f + ws;
     M = mn;
-    W = W * f + w;
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) acc[e] = acc[e] * f + w * v[e];
-  };
-  // an item's pieces: its own place if one CTA holds it, else the CTAs' slots
-  auto pieces = [&](long long u0, int nb, int w, int r, const float *whole_o, const float *whole_lse) {
-    const long long u1 = u0 + static_cast<long long>(nb) * w;
-    const int c1 = cta_of(u0, U, a.ctas), c2 = cta_of(u1 - 1, U, a.ctas);
-    if (c1 == c2) {
-      add(whole_o + row * D, __ldcg(whole_lse + row));
-      return;
+    for (int e = 0; e < EPL; ++e) acc[e] *= f;
+    const int m = min(32, n - i0);
+#pragma unroll 4
+    for (int i = 0; i < m; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const float *oi = reinterpret_cast<const float *>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(po), i));
+      const V v = __ldcg(reinterpret_cast<const V *>(oi) + lane);
+      const float *vf = reinterpret_cast<const float *>(&v);
+      if (wi != 0.f) {
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) acc[e] += wi * vf[e];
+      }
     }
-    for (int cc = c1; cc <= c2; ++cc) {
-      const long long b0 = first_unit(cc, U, a.ctas), b1 = first_unit(cc + 1, U, a.ctas);
-      int lo, hi;
-      piece_blocks(u0, nb, w, b0, b1, lo, hi);
-      if (lo >= hi) continue;  // a range that holds no block's first unit
-      const int64_t x = (static_cast<int64_t>(cc) * 2 + (u0 <= b0 ? 0 : 1)) * a.slot_rows + r;
-      add(a.cut_o + x * D, __ldcg(a.cut_lse + x));
-    }
-  };
-  if (q.fb == 0 && q.nb > 0) {
-    const long long u0 = q.base + static_cast<long long>(kvh) * q.nb * kOwnUnits;
-    if (cta_of(u0, U, a.ctas) == cta_of(u0 + static_cast<long long>(q.nb) * kOwnUnits - 1, U, a.ctas)) return;
   }
-  if (q.fb > 0) {
-    const GroupInfo gi = a.groups[q.group];
-    const int i = s - gi.first, tile = i / gi.tile_seqs;
-    const long long u0 = gi.base + static_cast<long long>(tile * a.num_kv + kvh) * gi.nb * gi.w;
-    pieces(u0, gi.nb, gi.w, (i - tile * gi.tile_seqs) * a.g + h % a.g, a.pre_o, a.pre_lse);
-  }
-  if (q.nb > 0)
-    pieces(q.base + static_cast<long long>(kvh) * q.nb * kOwnUnits, q.nb, kOwnUnits, h % a.g, a.own_o, a.own_lse);
   const float inv = W == 0.f ? 0.f : (a.v_scales ? __ldg(a.v_scales + kvh) : a.vscale) / W;
+  V r;
+  float *rf = reinterpret_cast<float *>(&r);
 #pragma unroll
-  for (int e = 0; e < EPL; e += 2)
-    *reinterpret_cast<float2 *>(out + e) = make_float2(acc[e] * inv, acc[e + 1] * inv);
+  for (int e = 0; e < EPL; ++e) rf[e] = acc[e] * inv;
+  *out = r;
   if (a.lse && lane == 0) a.lse[row] = W == 0.f ? -INFINITY : (M + log2f(W)) * kLn2;
 }
 
-// The attention kernel for a descriptor (pa_shared_bf16.cu and so on).
+// The attention kernel for a descriptor (pa_shared_16.cu, pa_shared_8.cu).
 struct KernelInfo {
   const void *fn;
   size_t smem;
+  int threads;
 };
 template <int D, int KVT>
 KernelInfo attend_info() {
-  return KernelInfo{reinterpret_cast<const void *>(&shared_attend_kernel<D, KVT>), Cfg<D, KVT>::SMEM};
+  return KernelInfo{reinterpret_cast<const void *>(&shared_attend_kernel<D, KVT>), Cfg<D, KVT>::SMEM,
+                    Cfg<D, KVT>::NTHREADS};
 }
 KernelInfo pick_attend_16(int head_dim, int kv_dtype);
 KernelInfo pick_attend_8(int head_dim, int kv_dtype);
