@@ -13,10 +13,11 @@
 //  * shared_plan_kernel (one CTA) turns the lengths into a list of items --
 //    (group, tile of up to 128 rows, kv head) over the prefix's blocks, and
 //    (sequence, kv head) over its own blocks -- laid end to end on one axis
-//    of blocks.
-//  * shared_attend_kernel, one persistent CTA per SM: CTA c takes the blocks
-//    [c n, (c + 1) n) of that axis, so every CTA reads the same bytes
-//    whatever the lengths; an item cut between CTAs leaves a piece in each.
+//    of units, a unit a block, with some units in front of every item for what
+//    it costs besides its blocks.
+//  * shared_attend_kernel, one persistent CTA per SM: CTA c takes the units
+//    [c n, (c + 1) n) of that axis, so every CTA has the same work whatever
+//    the lengths; an item cut between CTAs leaves a piece in each.
 //  * shared_join_kernel, one warp per (sequence, head): joins the parts.
 //
 // The attention runs on tcgen05 for every item, a sequence's few heads
@@ -25,13 +26,15 @@
 // as a hi + lo pair) -- about 1,900 cycles, less than the 2,850 in which the
 // SM's share of the measured HBM rate brings those 128 keys (64 KB of bf16).
 // Roles (warps) of the attend kernel:
-//   0  MMA issuer (one thread): Q K^T of step k + 1, then P V of step k, so
-//      that the softmax of step k + 1 runs behind P V of step k;
-//   1  walks the CTA's part of the axis, publishes items, K copies (TMA);
-//   2  V copies;   3  Q tiles (two slots, so that items overlap);
+//   0  issues Q K^T (one thread), one step ahead of
+//   2  P V (one thread), so that the softmax of one step runs behind the
+//      products of the next;
+//   1  walks the CTA's part of the axis, publishes its items, copies their
+//      K and V (TMA);
+//   3  Q tiles (two slots, so that items overlap);
 //   4-11  softmax, two threads per row (64 keys each), and each finished
 //      item's output, one step late so that it hides behind the next item;
-//   12-13 (8-bit caches) widen the landed bytes to fp16 tiles (exact).
+//   12-15 (8-bit caches) widen the landed bytes to fp16 tiles (exact).
 // Scores and outputs are double-buffered in tensor memory (S 2 x 128, O 2 x D
 // columns); P overwrites its scores.  Every wait is bounded.
 #pragma once
@@ -56,12 +59,15 @@ constexpr int BPT = KT / 16;     // blocks of a step
 // the running maximum of a row is only raised when a score exceeds it by
 // more than this (log2 units), so that O is rarely rescaled
 constexpr float kRaise = 8.f;
-// fewer blocks than a step are not worth a CTA of their own
-constexpr int kMinBlocks = BPT;
+// An item costs its blocks and this many more (its Q tile, its first copies'
+// latency, its output), so the axis gives it that many extra units in front.
+constexpr int kItemUnits = 10;
+// a CTA's share is at least one item of one step
+constexpr int kMinUnits = kItemUnits + BPT;
 
-// One group's prefix on the axis of blocks.
+// One group's prefix on the axis.
 struct __align__(16) GroupInfo {
-  long long base;  // first block
+  long long base;  // first unit
   int first;       // first sequence
   int n;           // sequences
   int nb;          // blocks of the prefix that some sequence reads (0: nothing shared)
@@ -85,12 +91,12 @@ struct __align__(16) CtaStart {
   int kind;  // 0 prefix item, 1 own part, 2 nothing to do
   int idx;   // group or sequence
   int sub;   // tile * kv heads + kv head, or kv head
-  int off;   // first block within the item
+  int off;   // first unit within the item
 };
 // The whole axis.
 struct __align__(16) Axis {
-  long long blocks;  // U
-  long long per;     // blocks of a CTA
+  long long units;  // U
+  long long per;    // units of a CTA
 };
 
 struct Args {
@@ -163,8 +169,11 @@ __device__ __forceinline__ long long scan_exclusive(long long v, long long *tota
   return before + incl - v;
 }
 
-// The last entry whose base is <= u (entries of no blocks share the base of
-// the next one, so it is the entry that holds block u).
+// Units of an item of nb blocks.
+__host__ __device__ __forceinline__ int item_units(int nb) { return nb > 0 ? nb + kItemUnits : 0; }
+
+// The last entry whose base is <= u (entries without work share the base of
+// the next one, so it is the entry that holds unit u).
 template <class T>
 __device__ __forceinline__ int find_base(const T *v, int n, long long u) {
   int lo = 0, hi = n - 1;
@@ -238,18 +247,18 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
   long long at = 0;
   for (int j0 = 0; j0 < G; j0 += PLAN_THREADS) {
     const int j = j0 + tid;
-    const long long v = j < G ? static_cast<long long>(groups[j].nb) * groups[j].tiles * a.num_kv : 0;
+    const long long v = j < G ? static_cast<long long>(item_units(groups[j].nb)) * groups[j].tiles * a.num_kv : 0;
     long long sum;
     const long long e = scan_exclusive(v, &sum, s_warp);
     if (j < G) groups[j].base = at + e;
     at += sum;
   }
-  const long long own = at;  // first block of the own parts
+  const long long own = at;  // first unit of the own parts
   for (int s0 = 0; s0 < S; s0 += PLAN_THREADS) {
     const int s = s0 + tid;
     const int nb = s < S ? max(0, ((seqs[s].len + 15) >> 4) - seqs[s].fb) : 0;
     long long sum;
-    const long long e = scan_exclusive(static_cast<long long>(nb) * a.num_kv, &sum, s_warp);
+    const long long e = scan_exclusive(static_cast<long long>(item_units(nb)) * a.num_kv, &sum, s_warp);
     if (s < S) {
       seqs[s].nb = nb;
       seqs[s].base = at + e;
@@ -257,7 +266,7 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
     at += sum;
   }
   const long long U = at;
-  const long long per = max((U + a.ctas - 1) / a.ctas, static_cast<long long>(kMinBlocks));
+  const long long per = max((U + a.ctas - 1) / a.ctas, static_cast<long long>(kMinUnits));
   if (tid == 0) *a.axis = Axis{U, per};
   __syncthreads();
   // each CTA's first item
@@ -267,11 +276,13 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
     if (u < own) {
       const int j = find_base(groups, G, u);
       const long long r = u - groups[j].base;
-      st = CtaStart{0, j, static_cast<int>(r / groups[j].nb), static_cast<int>(r % groups[j].nb)};
+      const int n = item_units(groups[j].nb);
+      st = CtaStart{0, j, static_cast<int>(r / n), static_cast<int>(r % n)};
     } else if (u < U) {
       const int s = find_base(seqs, S, u);
       const long long r = u - seqs[s].base;
-      st = CtaStart{1, s, static_cast<int>(r / seqs[s].nb), static_cast<int>(r % seqs[s].nb)};
+      const int n = item_units(seqs[s].nb);
+      st = CtaStart{1, s, static_cast<int>(r / n), static_cast<int>(r % n)};
     }
     a.starts[c] = st;
   }
@@ -312,7 +323,7 @@ struct Cfg {
   static constexpr int KVT = KVT_;
   static constexpr bool KV8 = !kv16(KVT);
   static constexpr bool BF16 = KVT == kKvBf16;  // bf16 products (fp16 otherwise)
-  static constexpr int NCONV = KV8 ? 2 : 0;     // widening warps
+  static constexpr int NCONV = KV8 ? 4 : 0;     // widening warps
   static constexpr int NTHREADS = (12 + NCONV) * 32;
   static constexpr int HALVES = D / 64;         // 128-byte column halves of a 16-bit row
   static constexpr int HB = KT * 128;           // bytes of one half of a K or V tile
@@ -354,8 +365,8 @@ struct Bars {
   uint64_t iq_full[NIQ], iq_empty[NIQ];
   uint64_t lk_full[C::NL], lk_empty[C::NL], lv_full[C::NL], lv_empty[C::NL];  // landed copies
   uint64_t k_full[C::NT], k_empty[C::NT], v_full[C::NT], v_empty[C::NT];      // 8-bit: widened tiles
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2];
-  uint64_t drain;
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], p_empty[2], o_full[2], o_empty[2];
+  uint64_t drain[2];
   uint32_t tmem;
 };
 
@@ -414,26 +425,31 @@ struct TableWindow {
   }
 };
 
-// Copies of a piece's K (or V) blocks into the landing slots, a step at a
-// time; `fill` counts the slots filled so far.
+// The copies of a piece's K and V blocks into the landing slots, a step at a
+// time; `fill` counts the slots of each filled so far.
 template <class C>
-__device__ bool copy_piece(const Args &a, const CUtensorMap *map, uint8_t *slots, uint64_t *full, uint64_t *empty,
-                           const int32_t *table, int nblk, int kvh, uint32_t &fill, uint64_t pol, int lane) {
+__device__ bool copy_piece(const Args &a, uint8_t *smem, Bars<C> &bar, const int32_t *table, int nblk, int kvh,
+                           uint32_t &fill, uint64_t pol, int lane) {
   constexpr int BOXES = C::KV8 ? 1 : C::HALVES;
   TableWindow tw;
   tw.begin(a, table, nblk, lane);
   const int bi = lane / BOXES, hh = lane % BOXES;
   for (int b = 0; b < nblk; b += BPT) {
     const int n = min(BPT, nblk - b);
-    const int phys = tw.at(a, b, bi & (BPT - 1), lane);
-    const uint32_t st = fill % C::NL, ph = (fill / C::NL) & 1;
-    if (!mbar_wait(&empty[st], ph ^ 1, a.wait_ns)) return false;
-    if (lane == 0) mbar_arrive_expect_tx(&full[st], n * C::BLOCKB);
+    const int row = (tw.at(a, b, bi & (BPT - 1), lane) * a.num_kv + kvh) * 16;
+    const uint32_t st = fill % C::NL, ph = ((fill / C::NL) & 1) ^ 1;
+    const int off = st * C::LB + (C::KV8 ? bi * C::BLOCKB : hh * C::HB + bi * 2048);
+    if (!mbar_wait(&bar.lk_empty[st], ph, a.wait_ns)) return false;
+    if (lane == 0) mbar_arrive_expect_tx(&bar.lk_full[st], n * C::BLOCKB);
     __syncwarp();
-    if (bi < n) {
-      uint8_t *dst = slots + st * C::LB + (C::KV8 ? bi * C::BLOCKB : hh * C::HB + bi * 2048);
-      tma_load_2d(dst, map, hh * 64, (phys * a.num_kv + kvh) * 16, &full[st], pol);
+    if (bi < n) tma_load_2d(smem + C::OFF_LK + off, &a.kmap, hh * 64, row, &bar.lk_full[st], pol);
+    if (!mbar_wait(&bar.lv_empty[st], ph, a.wait_ns)) {
+      mbar_wait(&bar.lk_full[st], ph ^ 1, a.wait_ns);  // the K copies just issued land
+      return false;
     }
+    if (lane == 0) mbar_arrive_expect_tx(&bar.lv_full[st], n * C::BLOCKB);
+    __syncwarp();
+    if (bi < n) tma_load_2d(smem + C::OFF_LV + off, &a.vmap, hh * 64, row, &bar.lv_full[st], pol);
     ++fill;
   }
   return true;
@@ -441,17 +457,19 @@ __device__ bool copy_piece(const Args &a, const CUtensorMap *map, uint8_t *slots
 
 // After a failed wait: the copies already issued land before the CTA exits.
 template <class C>
-__device__ void drain_copies(const Args &a, uint64_t *full, uint32_t fill) {
-  for (uint32_t i = fill > C::NL ? fill - C::NL : 0; i < fill; ++i)
-    mbar_wait(&full[i % C::NL], (i / C::NL) & 1, a.wait_ns);
+__device__ void drain_copies(const Args &a, Bars<C> &bar, uint32_t fill) {
+  for (uint32_t i = fill > C::NL ? fill - C::NL : 0; i < fill; ++i) {
+    mbar_wait(&bar.lk_full[i % C::NL], (i / C::NL) & 1, a.wait_ns);
+    mbar_wait(&bar.lv_full[i % C::NL], (i / C::NL) & 1, a.wait_ns);
+  }
 }
 
-// Warp 1: the CTA's items, and their K copies.
+// Warp 1: the CTA's items, and their copies.
 template <class C>
 __device__ bool walk(const Args &a, uint8_t *smem, Bars<C> &bar, Item *iq, int lane) {
   const int me = blockIdx.x;
   const Axis ax = *a.axis;
-  const long long b0 = me * ax.per, b1 = min(b0 + ax.per, ax.blocks);
+  const long long b0 = me * ax.per, b1 = min(b0 + ax.per, ax.units);
   const uint64_t pol = l2_evict_first_policy();
   uint32_t fill = 0, posted = 0;
   bool ok = true;
@@ -501,16 +519,20 @@ __device__ bool walk(const Args &a, uint8_t *smem, Bars<C> &bar, Item *iq, int l
         it.kvh = kind == 0 ? sub % a.num_kv : sub;
         it.seq0 = first + t0;
         it.rows = min(tile_seqs, n - t0) * a.g;
-        it.key0 = (fb + off) * 16;
-        it.nblk = static_cast<int>(min(static_cast<long long>(nb - off), left));
+        // the part of the item's units in this CTA's range, and its blocks
+        const int size = item_units(nb);
+        const int take = static_cast<int>(min(static_cast<long long>(size - off), left));
+        const int lo = max(off - kItemUnits, 0);
+        it.nblk = max(off + take - kItemUnits, 0) - lo;
+        it.key0 = (fb + lo) * 16;
         it.kend = min(kend, it.key0 + it.nblk * 16);  // a cut piece ends before the item
         const bool whole = it.nblk == nb;
         it.to = whole ? whole_to : kToCut;
         // a cut item that begins inside this CTA's range is its last one
         it.slot = me * 2 + (off == 0 && left < b1 - b0 ? 1 : 0);
-        left -= it.nblk;
-        ok = post(it) && copy_piece<C>(a, &a.kmap, smem + C::OFF_LK, bar.lk_full, bar.lk_empty, table + off, it.nblk,
-                                       it.kvh, fill, pol, lane);
+        left -= take;
+        if (it.nblk > 0)
+          ok = post(it) && copy_piece<C>(a, smem, bar, table + lo, it.nblk, it.kvh, fill, pol, lane);
       }
       if (!ok || left == 0) break;
       // the next group with a prefix, after the last one the sequences with
@@ -540,7 +562,7 @@ __device__ bool walk(const Args &a, uint8_t *smem, Bars<C> &bar, Item *iq, int l
     it.end = 1;
     ok = post(it);
   }
-  if (!ok) drain_copies<C>(a, bar.lk_full, fill);
+  if (!ok) drain_copies<C>(a, bar, fill);
   return ok;
 }
 
@@ -555,24 +577,6 @@ __device__ __forceinline__ bool take_item(const Args &a, Bars<C> &bar, const Ite
   if (lane == 0) mbar_arrive(&bar.iq_empty[st]);
   ++taken;
   return true;
-}
-
-// Warp 2: V copies.
-template <class C>
-__device__ bool copy_v(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq, int lane) {
-  const uint64_t pol = l2_evict_first_policy();
-  uint32_t fill = 0, taken = 0;
-  bool ok = true;
-  Item it;
-  while (ok) {
-    ok = take_item<C>(a, bar, iq, taken, it, lane);
-    if (!ok || it.end) break;
-    const int32_t *table = a.block_tables + static_cast<int64_t>(it.table) * a.max_blocks + (it.key0 >> 4);
-    ok = copy_piece<C>(a, &a.vmap, smem + C::OFF_LV, bar.lv_full, bar.lv_empty, table, it.nblk, it.kvh, fill, pol,
-                       lane);
-  }
-  if (!ok) drain_copies<C>(a, bar.lv_full, fill);
-  return ok;
 }
 
 // Warp 3: Q tiles, [half][row][128 B] with the 128-byte swizzle.  With an
@@ -627,11 +631,19 @@ __device__ bool load_q(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *i
   }
 }
 
-// Warps 12-13 (8-bit caches): landed bytes to fp16 tiles, exact; V rows past
-// the item's keys zeroed (they may hold anything, and 0 * NaN is NaN).
+// Warps 12-15 (8-bit caches): landed bytes to fp16 tiles, exact; V rows past
+// the piece's keys zeroed (they may hold anything, and 0 * NaN is NaN).  A
+// thread keeps its 16-byte column chunk and its row modulo 8, and with them
+// its places in the swizzled tile, over all its rows.
 template <class C>
 __device__ bool widen(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq, int ct, int lane) {
-  constexpr int CPR = C::D / 16;  // 16-byte chunks of a row of bytes
+  constexpr int CPR = C::D / 16;                  // 16-byte chunks of a row of bytes
+  constexpr int RSTEP = C::NCONV * 32 / CPR;      // rows between a thread's chunks (a multiple of 8)
+  static_assert(RSTEP % 8 == 0 && KT % RSTEP == 0, "a thread's rows agree modulo 8");
+  constexpr int PER = KT / RSTEP;
+  const int c = ct % CPR, r0 = ct / CPR, r7 = r0 & 7;
+  const int put = (c >> 2) * C::HB + r0 * 128;
+  const int x0 = ((2 * (c & 3)) ^ r7) << 4, x1 = ((2 * (c & 3) + 1) ^ r7) << 4;
   uint32_t taken = 0, step = 0;
   Item it;
   for (;;) {
@@ -639,37 +651,35 @@ __device__ bool widen(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq
     if (it.end) return true;
     for (int b = 0; b < it.nblk; b += BPT, ++step) {
       const int rows = min(BPT, it.nblk - b) * 16;
-      const int keep = it.kend - (it.key0 + b * 16);  // rows of the item's keys
-      const uint32_t ls = step % C::NL, lp = (step / C::NL) & 1, ts = step % C::NT, tp = (step / C::NT) & 1;
-#pragma unroll
+      const int keep = it.kend - (it.key0 + b * 16);  // rows of the piece's keys
+      const uint32_t ls = step % C::NL, lp = (step / C::NL) & 1, ts = step % C::NT, tp = ((step / C::NT) & 1) ^ 1;
+#pragma unroll 1
       for (int v = 0; v < 2; ++v) {
         if (!mbar_wait(v ? &bar.lv_full[ls] : &bar.lk_full[ls], lp, a.wait_ns)) return false;
-        if (!mbar_wait(v ? &bar.v_empty[ts] : &bar.k_empty[ts], tp ^ 1, a.wait_ns)) return false;
-        const uint8_t *src = smem + (v ? C::OFF_LV : C::OFF_LK) + ls * C::LB;
-        uint8_t *dst = smem + (v ? C::OFF_V : C::OFF_K) + ts * C::TB;
-        constexpr int ILP = 4;
-        for (int u0 = ct; u0 < rows * CPR; u0 += 64 * ILP) {
+        if (!mbar_wait(v ? &bar.v_empty[ts] : &bar.k_empty[ts], tp, a.wait_ns)) return false;
+        const uint8_t *src = smem + (v ? C::OFF_LV : C::OFF_LK) + ls * C::LB + ct * 16;
+        uint8_t *dst = smem + (v ? C::OFF_V : C::OFF_K) + ts * C::TB + put;
+        const int zero = v ? keep : KT;  // rows from here on become zero
+        constexpr int ILP = PER < 4 ? PER : 4;
+#pragma unroll 1
+        for (int k0 = 0; k0 < PER; k0 += ILP) {
+          if (r0 + k0 * RSTEP >= rows) break;
           uint4 x[ILP];
 #pragma unroll
-          for (int k = 0; k < ILP; ++k)
-            if (u0 + 64 * k < rows * CPR) x[k] = *reinterpret_cast<const uint4 *>(src + (u0 + 64 * k) * 16);
+          for (int k = 0; k < ILP; ++k) x[k] = *reinterpret_cast<const uint4 *>(src + (k0 + k) * RSTEP * C::D);
 #pragma unroll
           for (int k = 0; k < ILP; ++k) {
-            const int u = u0 + 64 * k;
-            if (u >= rows * CPR) break;
-            const int r = u / CPR, c = u % CPR;  // dims 16 c .. 16 c + 15 of row r
-            const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            if (r0 + (k0 + k) * RSTEP >= zero) w[0] = w[1] = w[2] = w[3] = 0;  // the byte 0 is +0
             uint32_t o[8];
-            const bool zero = v && r >= keep;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              o[2 * e] = zero ? 0u : fp8x2_to_f16x2<C::KVT>(static_cast<uint16_t>(w[e] & 0xffffu));
-              o[2 * e + 1] = zero ? 0u : fp8x2_to_f16x2<C::KVT>(static_cast<uint16_t>(w[e] >> 16));
+              o[2 * e] = fp8x2_to_f16x2<C::KVT>(static_cast<uint16_t>(w[e] & 0xffffu));
+              o[2 * e + 1] = fp8x2_to_f16x2<C::KVT>(static_cast<uint16_t>(w[e] >> 16));
             }
-            uint8_t *row = dst + (c >> 2) * C::HB + r * 128;
-            const int k0 = 2 * (c & 3);
-            *reinterpret_cast<uint4 *>(row + ((k0 ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4 *>(row + (((k0 + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+            uint8_t *row = dst + (k0 + k) * RSTEP * 128;
+            *reinterpret_cast<uint4 *>(row + x0) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(row + x1) = make_uint4(o[4], o[5], o[6], o[7]);
           }
         }
         fence_proxy_async_smem();
@@ -683,127 +693,87 @@ __device__ bool widen(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq
   }
 }
 
-// Whether the phase of `bar` with the given parity has completed (no waiting).
-__device__ __forceinline__ bool mbar_done(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
+// One product of 8 or 16 K-steps is issued from descriptors that differ by
+// constants, so that the one issuing thread keeps the tensor pipe fed.
 
-// Warp 0, one thread: the products, in step order.
+// Warp 0, one thread: the scores, S[k % 2] = Q K^T of step k, once the step's
+// K has landed and P V of step k - 2 has read the P that lay there.
 template <class C>
-__device__ bool issue_mma(const Args &a, uint32_t sbase, uint32_t tmem, Bars<C> &bar, const Item *iq) {
+__device__ bool issue_qk(const Args &a, uint32_t sbase, uint32_t tmem, Bars<C> &bar, const Item *iq) {
   // 16-bit caches: the landed tiles feed the products
   uint64_t *k_full = C::KV8 ? bar.k_full : bar.lk_full, *k_empty = C::KV8 ? bar.k_empty : bar.lk_empty;
-  uint64_t *v_full = C::KV8 ? bar.v_full : bar.lv_full, *v_empty = C::KV8 ? bar.v_empty : bar.lv_empty;
-  struct Step {
-    uint32_t k;      // number of the step in the CTA
-    int nblk;
-    int obuf;        // output buffer of its item
-    uint32_t item;   // number of its item
-    bool first, last;
-  };
-  uint32_t taken = 0, steps = 0;
-  int left = 0;             // blocks of the current item not yet in a step
-  bool fresh = false, ended = false;
+  uint32_t taken = 0, k = 0;
   QSlots qs;
-  uint32_t qbase = 0, qhalf = 0;
-  // the next step, once its K (and for an item's first step its Q) is there:
-  // 1 it is, 0 not yet (only if !block), 2 no more steps, -1 a wait ran out
-  auto fetch = [&](Step &s, bool block) -> int {
-    if (ended) return 2;
-    auto there = [&](uint64_t *b, uint32_t ph) {
-      return block ? mbar_wait(b, ph, a.wait_ns) : mbar_done(b, ph);
-    };
-    if (left == 0) {
-      const uint32_t st = taken % NIQ;
-      if (!there(&bar.iq_full[st], (taken / NIQ) & 1)) return block ? -1 : 0;
-      const int end = iq[st].end, rows = iq[st].rows;
-      left = iq[st].nblk;
-      mbar_arrive(&bar.iq_empty[st]);
-      ++taken;
-      if (end) {
-        ended = true;
-        return 2;
-      }
-      qs.next(rows);
-      qbase = sbase + C::OFF_Q + qs.slot * (C::QB / 2);
-      qhalf = qs.big ? C::QHALF : C::QHALF / 2;
-      fresh = true;
-    }
-    if (fresh)
-      for (int i = 0; i < 2; ++i)
-        if (qs.uses_slot(i) && !there(&bar.q_full[i], qs.uses[i] & 1)) return block ? -1 : 0;
-    if (!there(&k_full[steps % C::NT], (steps / C::NT) & 1)) return block ? -1 : 0;
-    s.k = steps++;
-    s.nblk = min(left, BPT);
-    left -= s.nblk;
-    s.first = fresh;
-    s.last = left == 0;
-    s.item = taken - 1;
-    s.obuf = s.item & 1;
-    fresh = false;
-    return 1;
-  };
-  auto qk = [&](const Step &s) {
-    tc_fence_after_sync();
-    const uint32_t kbase = sbase + C::OFF_K + (s.k % C::NT) * C::TB;
+  for (;;) {
+    const uint32_t st = taken % NIQ;
+    if (!mbar_wait(&bar.iq_full[st], (taken / NIQ) & 1, a.wait_ns)) return false;
+    const int end = iq[st].end, rows = iq[st].rows, nblk = iq[st].nblk;
+    mbar_arrive(&bar.iq_empty[st]);
+    ++taken;
+    if (end) return true;
+    qs.next(rows);
+    const uint32_t qhalf = qs.big ? C::QHALF : C::QHALF / 2;
+    const uint64_t qd = umma_desc_sw128(sbase + C::OFF_Q + qs.slot * (C::QB / 2), 16, 1024);
+    for (int i = 0; i < 2; ++i)
+      if (qs.uses_slot(i) && !mbar_wait(&bar.q_full[i], qs.uses[i] & 1, a.wait_ns)) return false;
+    for (int b = 0; b < nblk; b += BPT, ++k) {
+      if (!mbar_wait(&bar.p_empty[k & 1], ((k >> 1) & 1) ^ 1, a.wait_ns)) return false;
+      if (!mbar_wait(&k_full[k % C::NT], (k / C::NT) & 1, a.wait_ns)) return false;
+      tc_fence_after_sync();
+      const uint64_t kd = umma_desc_sw128(sbase + C::OFF_K + (k % C::NT) * C::TB, 16, 1024);
+      const uint32_t s = tmem + C::S_COL + (k & 1) * KT;
 #pragma unroll
-    for (int kk = 0; kk < C::D / 16; ++kk) {
-      const uint64_t ad = umma_desc_sw128(qbase + (kk >> 2) * qhalf + (kk & 3) * 32, 16, 1024);
-      const uint64_t bd = umma_desc_sw128(kbase + (kk >> 2) * C::HB + (kk & 3) * 32, 16, 1024);
-      umma_bf16_ss(tmem + C::S_COL + (s.k & 1) * KT, ad, bd, C::IDESC_QK, kk > 0 ? 1u : 0u);
+      for (int kk = 0; kk < C::D / 16; ++kk)
+        umma_bf16_ss(s, qd + (((kk >> 2) * qhalf + (kk & 3) * 32) >> 4), kd + (((kk >> 2) * C::HB + (kk & 3) * 32) >> 4),
+                     C::IDESC_QK, kk > 0 ? 1u : 0u);
+      umma_commit(&bar.s_full[k & 1]);
+      umma_commit(&k_empty[k % C::NT]);
     }
-    umma_commit(&bar.s_full[s.k & 1]);
-    umma_commit(&k_empty[s.k % C::NT]);
-    if (s.last) {
-      for (int i = 0; i < 2; ++i)
-        if (qs.uses_slot(i)) umma_commit(&bar.q_empty[i]);
-      qs.done();
-    }
-  };
-  auto pv = [&](const Step &s) -> bool {
-    if (!mbar_wait_hint(&bar.p_full[s.k & 1], (s.k >> 1) & 1, a.wait_ns)) return false;
-    // an item's first product overwrites the output buffer of the item two before
-    if (s.first && !mbar_wait(&bar.o_empty[s.obuf], ((s.item >> 1) & 1) ^ 1, a.wait_ns)) return false;
-    if (!mbar_wait(&v_full[s.k % C::NT], (s.k / C::NT) & 1, a.wait_ns)) return false;
-    tc_fence_after_sync();
-    const uint32_t vbase = sbase + C::OFF_V + (s.k % C::NT) * C::TB;
-    const uint32_t p = tmem + C::S_COL + (s.k & 1) * KT;
-    for (int kk = 0; kk < s.nblk; ++kk) {
-      // keys 16 kk .. 16 kk + 15: hi at +0, lo at +16 of their 32-column chunk
-      const uint64_t bd = umma_desc_sw128(vbase + kk * 2048, C::HB, 1024);
-      const uint32_t ap = p + (kk >> 1) * 32 + (kk & 1) * 8;
-      umma_bf16_ts(tmem + C::O_COL + s.obuf * C::D, ap, bd, C::IDESC_PV, (s.first && kk == 0) ? 0u : 1u);
-      umma_bf16_ts(tmem + C::O_COL + s.obuf * C::D, ap + 16, bd, C::IDESC_PV, 1u);
-    }
-    umma_commit(&v_empty[s.k % C::NT]);
-    if (s.last) umma_commit(&bar.o_full[s.obuf]);
-    return true;
-  };
-  Step cur, nxt;
-  int r = fetch(cur, true);
-  if (r == 1) qk(cur);
-  while (r == 1) {
-    // the next step's scores first, if its operands are there
-    int n = fetch(nxt, false);
-    if (n == 1) qk(nxt);
-    if (!pv(cur)) return false;
-    if (n == 0) {
-      n = fetch(nxt, true);
-      if (n == 1) qk(nxt);
-    }
-    if (n < 0) return false;
-    cur = nxt;
-    r = n;
+    for (int i = 0; i < 2; ++i)
+      if (qs.uses_slot(i)) umma_commit(&bar.q_empty[i]);
+    qs.done();
   }
-  return r == 2;
+}
+
+// Warp 2, one thread: O += P V of every step, hi and lo.
+template <class C>
+__device__ bool issue_pv(const Args &a, uint32_t sbase, uint32_t tmem, Bars<C> &bar, const Item *iq) {
+  uint64_t *v_full = C::KV8 ? bar.v_full : bar.lv_full, *v_empty = C::KV8 ? bar.v_empty : bar.lv_empty;
+  uint32_t taken = 0, k = 0;
+  for (;;) {
+    const uint32_t st = taken % NIQ;
+    if (!mbar_wait(&bar.iq_full[st], (taken / NIQ) & 1, a.wait_ns)) return false;
+    const int end = iq[st].end, nblk = iq[st].nblk;
+    mbar_arrive(&bar.iq_empty[st]);
+    const uint32_t item = taken++;
+    if (end) return true;
+    const uint32_t o = tmem + C::O_COL + (item & 1) * C::D;
+    // the item's first product overwrites the output of the item two before
+    if (!mbar_wait(&bar.o_empty[item & 1], ((item >> 1) & 1) ^ 1, a.wait_ns)) return false;
+    for (int b = 0; b < nblk; b += BPT, ++k) {
+      if (!mbar_wait(&v_full[k % C::NT], (k / C::NT) & 1, a.wait_ns)) return false;
+      if (!mbar_wait_hint(&bar.p_full[k & 1], (k >> 1) & 1, a.wait_ns)) return false;
+      tc_fence_after_sync();
+      const uint64_t vd = umma_desc_sw128(sbase + C::OFF_V + (k % C::NT) * C::TB, C::HB, 1024);
+      const uint32_t p = tmem + C::S_COL + (k & 1) * KT;
+      // keys 16 kk .. 16 kk + 15: hi at +0, lo at +16 of their 32-column chunk
+      auto block = [&](int kk) {
+        const uint64_t bd = vd + kk * (2048 >> 4);
+        const uint32_t ap = p + (kk >> 1) * 32 + (kk & 1) * 8;
+        umma_bf16_ts(o, ap, bd, C::IDESC_PV, (kk > 0 || b > 0) ? 1u : 0u);
+        umma_bf16_ts(o, ap + 16, bd, C::IDESC_PV, 1u);
+      };
+      if (nblk - b >= BPT) {
+#pragma unroll
+        for (int kk = 0; kk < BPT; ++kk) block(kk);
+      } else {
+        for (int kk = 0; kk < nblk - b; ++kk) block(kk);
+      }
+      umma_commit(&v_empty[k % C::NT]);
+      umma_commit(&bar.p_empty[k & 1]);
+    }
+    umma_commit(&bar.o_full[item & 1]);
+  }
 }
 
 // Warps 4-11: softmax and outputs.  Warps 4-7 take keys 0-63 and warps 8-11
@@ -918,27 +888,39 @@ __device__ bool softmax(const Args &a, uint8_t *smem, uint32_t tmem, Bars<C> &ba
       if (!named_bar_and(pair, 64, there && ok)) return false;
       if (mine) {
         const uint32_t scol = trow + C::S_COL + (k & 1) * KT + 64 * h;
-        uint32_t sc[2][32];
-        tmem_ld32_async(scol, sc[0]);
-        tmem_ld32_async(scol + 32, sc[1]);
-        tmem_wait_ld(sc[0]);
-        tmem_wait_ld(sc[1]);
         const int kh = key0 + 64 * h;
-        if (turn) {
+        // scores as the softmax takes them: a scale that is not positive
+        // applied, keys past the row's limit out
+        auto ready = [&](int c, uint32_t(&x)[32]) {
+          if (turn) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            sc[0][i] = __float_as_uint(__uint_as_float(sc[0][i]) * sgn);
-            sc[1][i] = __float_as_uint(__uint_as_float(sc[1][i]) * sgn);
+            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * sgn);
           }
-        }
-        float mx = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
           if (kh + 32 * c + 32 > lim) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (kh + 32 * c + i >= lim) sc[c][i] = __float_as_uint(-INFINITY);
+              if (kh + 32 * c + i >= lim) x[i] = __float_as_uint(-INFINITY);
           }
+        };
+        // both chunks of 32 stay in registers, or (8-bit caches, whose 16
+        // warps leave 128 registers a thread) are read again for P
+        constexpr int HOLD = C::KV8 ? 1 : 2;
+        uint32_t sc[HOLD][32];
+        if constexpr (HOLD == 2) {
+          tmem_ld32_async(scol, sc[0]);
+          tmem_ld32_async(scol + 32, sc[1]);
+          tmem_wait_ld(sc[0]);
+          tmem_wait_ld(sc[1]);
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c0 = 0; c0 < 2; ++c0) {
+          const int c = c0 % HOLD;
+          if constexpr (HOLD == 1) {
+            tmem_ld32_async(scol + 32 * c0, sc[0]);
+            tmem_wait_ld(sc[0]);
+          }
+          ready(c0, sc[c]);
           float t[11];  // a tree of three-input maxima
 #pragma unroll
           for (int i = 0; i < 10; ++i)
@@ -978,7 +960,14 @@ __device__ bool softmax(const Args &a, uint8_t *smem, uint32_t tmem, Bars<C> &ba
         const uint64_t q2 = f2_pack(qsc, qsc), o2 = f2_pack(off, off);
         uint64_t ls[2] = {0, 0};
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c0 = 0; c0 < 2; ++c0) {
+          // (with one chunk held: the second is still there)
+          const int c = c0 % HOLD, cc = HOLD == 1 ? 1 - c0 : c0;
+          if (HOLD == 1 && c0 == 1) {
+            tmem_ld32_async(scol, sc[0]);
+            tmem_wait_ld(sc[0]);
+            ready(0, sc[0]);
+          }
           uint32_t hi[16], lo[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -991,8 +980,8 @@ __device__ bool softmax(const Args &a, uint8_t *smem, uint32_t tmem, Bars<C> &ba
             const float2 d = f2_unpack(f2_sub(pp, f2_pack(lo16<PT>(hi[e]), hi16<PT>(hi[e]))));
             lo[e] = pack16x2<PT>(d.x, d.y);
           }
-          tmem_st16_async(scol + 32 * c, hi);
-          tmem_st16_async(scol + 32 * c + 16, lo);
+          tmem_st16_async(scol + 32 * cc, hi);
+          tmem_st16_async(scol + 32 * cc + 16, lo);
         }
         const float2 l2 = f2_unpack(f2_add(ls[0], ls[1]));
         l += l2.x + l2.y;
@@ -1025,7 +1014,7 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
   if (threadIdx.x == 0) {
     for (int i = 0; i < NIQ; ++i) {
       mbar_init(&bar.iq_full[i], 1);
-      mbar_init(&bar.iq_empty[i], 1 + 1 + 1 + 8 + C::NCONV);  // the roles that take items
+      mbar_init(&bar.iq_empty[i], 1 + 1 + 1 + 8 + C::NCONV);  // the warps that take items
     }
     for (int i = 0; i < C::NL; ++i) {
       mbar_init(&bar.lk_full[i], 1);
@@ -1044,10 +1033,11 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
       mbar_init(&bar.q_empty[i], 1);
       mbar_init(&bar.s_full[i], 1);
       mbar_init(&bar.p_full[i], 8);
+      mbar_init(&bar.p_empty[i], 1);
+      mbar_init(&bar.drain[i], 1);
       mbar_init(&bar.o_full[i], 1);
       mbar_init(&bar.o_empty[i], 8);
     }
-    mbar_init(&bar.drain, 1);
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc(&bar.tmem, C::TMEM_COLS);
@@ -1059,12 +1049,13 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
   asm volatile("griddepcontrol.wait;" ::: "memory");
   bool ok = true;
   if (warp == 0) {
-    if (lane == 0) ok = issue_mma<C>(a, smem_u32(smem), tmem, bar, iq);
+    if (lane == 0) ok = issue_qk<C>(a, smem_u32(smem), tmem, bar, iq);
     __syncwarp();
   } else if (warp == 1) {
     ok = walk<C>(a, smem, bar, iq, lane);
   } else if (warp == 2) {
-    ok = copy_v<C>(a, smem, bar, iq, lane);
+    if (lane == 0) ok = issue_pv<C>(a, smem_u32(smem), tmem, bar, iq);
+    __syncwarp();
   } else if (warp == 3) {
     ok = load_q<C>(a, smem, bar, iq, lane);
   } else if (warp < 12) {
@@ -1074,9 +1065,9 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
   }
   if (!ok && lane == 0) report_error(a.err, nullptr, kErrWaitTimeout);
   // every product issued completes before the tensor memory is given back
-  if (threadIdx.x == 0) {
-    umma_commit(&bar.drain);
-    mbar_wait(&bar.drain, 0, a.wait_ns);
+  if ((warp == 0 || warp == 2) && lane == 0) {
+    umma_commit(&bar.drain[warp >> 1]);
+    mbar_wait(&bar.drain[warp >> 1], 0, a.wait_ns);
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -1090,7 +1081,7 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
 
 // u / n for the axis (32-bit where it fits)
 __device__ __forceinline__ int axis_cta(long long u, const Axis &x) {
-  if (x.blocks < 0x7fffffffLL) return static_cast<int>(static_cast<unsigned>(u) / static_cast<unsigned>(x.per));
+  if (x.units < 0x7fffffffLL) return static_cast<int>(static_cast<unsigned>(u) / static_cast<unsigned>(x.per));
   return static_cast<int>(u / x.per);
 }
 
@@ -1112,26 +1103,23 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
   V *out = reinterpret_cast<V *>(a.out + row * D) + lane;
   // the pieces of the prefix part and of the own part: piece i of a part is
   // CTA c1 + i's slot (1 where the item begins inside that CTA's range), or
-  // the part's own place if one CTA holds it all
+  // the part's own place if one CTA holds all its blocks
   int p_c1 = 0, p_n = 0, p_s0 = 0, p_r = 0, o_c1 = 0, o_n = 0, o_s0 = 0;
   bool p_whole = false, o_whole = false;
+  auto pieces = [&](long long u0, int nb, int &c1, int &np, int &s0, bool &whole) {
+    c1 = axis_cta(u0, ax);
+    if ((c1 + 1) * ax.per - u0 <= kItemUnits) ++c1;  // that CTA's range holds none of its blocks
+    np = axis_cta(u0 + item_units(nb) - 1, ax) - c1 + 1;
+    whole = np == 1;
+    s0 = u0 > c1 * ax.per;
+  };
   if (q.fb > 0 && q.len > 0) {
     const GroupInfo gi = a.groups[q.group];
     const int i = s - gi.first, tile = i / gi.tile_seqs;
-    const long long u0 = gi.base + static_cast<long long>(tile * a.num_kv + kvh) * gi.nb;
-    p_c1 = axis_cta(u0, ax);
-    p_n = axis_cta(u0 + gi.nb - 1, ax) - p_c1 + 1;
-    p_whole = p_n == 1;
-    p_s0 = u0 > p_c1 * ax.per;
+    pieces(gi.base + static_cast<long long>(tile * a.num_kv + kvh) * item_units(gi.nb), gi.nb, p_c1, p_n, p_s0, p_whole);
     p_r = (i - tile * gi.tile_seqs) * a.g + h % a.g;
   }
-  if (q.nb > 0) {
-    const long long u0 = q.base + static_cast<long long>(kvh) * q.nb;
-    o_c1 = axis_cta(u0, ax);
-    o_n = axis_cta(u0 + q.nb - 1, ax) - o_c1 + 1;
-    o_whole = o_n == 1;
-    o_s0 = u0 > o_c1 * ax.per;
-  }
+  if (q.nb > 0) pieces(q.base + static_cast<long long>(kvh) * item_units(q.nb), q.nb, o_c1, o_n, o_s0, o_whole);
   if (q.fb == 0 && o_whole) return;
   const int n = p_n + o_n;
   // piece i's output row and log-sum-exp
