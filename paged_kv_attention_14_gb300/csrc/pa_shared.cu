@@ -19,10 +19,11 @@ int tile_seqs_of(const pa_kv_desc &d, int32_t max_group_size) {
   return max_group_size < 1 ? 1 : max_group_size > cap ? cap : max_group_size;
 }
 
-// The cache as TMA sees it: rows are (block, kv head, token) triples of
-// head_dim elements; a box is the 16 tokens of one kv head of one block, 64
-// columns of a 16-bit cache (128-byte swizzle, the layout the products
-// read), or the whole rows of an 8-bit one (plain: they are widened).
+// The cache as TMA sees it.  8-bit: rows of (block, kv head, token) triples, a
+// box is the 16 rows of one block and kv head as they are (they are widened).
+// 16-bit: the rows in groups of 8, each row in halves of 64 columns, a box is
+// a block's two groups as [group][half][8 rows][128 B] (128-byte swizzle),
+// one copy of 4 KB at head_dim 128 where plain rows would take one per half.
 bool make_map(CUtensorMap *map, const void *base, const pa_kv_desc &d) {
   const bool kv8 = d.kv_dtype == PA_KV_FP8_E4M3 || d.kv_dtype == PA_KV_FP8_E5M2;
   using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -41,15 +42,23 @@ bool make_map(CUtensorMap *map, const void *base, const pa_kv_desc &d) {
   thread_local MapCache<> cache;
   const MapKey key = map_key(base, d.num_blocks, d.num_kv_heads, d.head_dim, kv8);
   if (cache.find(key, map)) return true;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d.head_dim),
-                              static_cast<cuuint64_t>(d.num_blocks) * d.num_kv_heads * 16};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(d.head_dim) * (kv8 ? 1 : 2)};
-  const cuuint32_t box[2] = {kv8 ? static_cast<cuuint32_t>(d.head_dim) : 64u, 16};
-  const cuuint32_t estr[2] = {1, 1};
-  if (enc(map, kv8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(base), dims,
-          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, kv8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return false;
+  const cuuint64_t D = d.head_dim, rows = static_cast<cuuint64_t>(d.num_blocks) * d.num_kv_heads * 16;
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r;
+  if (kv8) {
+    const cuuint64_t dims[2] = {D, rows}, strides[1] = {D};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(D), 16};
+    r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  } else {
+    const cuuint64_t dims[4] = {64, 8, D / 64, rows / 8}, strides[3] = {D * 2, 128, D * 16};
+    const cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(D / 64), 2};
+    r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  }
+  if (r != CUDA_SUCCESS) return false;
   cache.put(key, *map);
   return true;
 }

@@ -32,8 +32,9 @@
 //   1  walks the CTA's part of the axis, publishes its items, copies their
 //      K and V (TMA);
 //   3  Q tiles (two slots, so that items overlap);
-//   4-11  softmax, two threads per row (64 keys each), and each finished
-//      item's output, one step late so that it hides behind the next item;
+//   4-11  softmax, two threads per row (64 keys each), and each item's output;
+//      items of up to 32 rows take one quarter of the lanes each, in turn, so
+//      that four of them can be in their softmax or output at once;
 //   12-15 (8-bit caches) widen the landed bytes to fp16 tiles (exact).
 // Scores and outputs are double-buffered in tensor memory (S 2 x 128, O 2 x D
 // columns); P overwrites its scores.  Every wait is bounded.
@@ -326,8 +327,11 @@ struct Cfg {
   static constexpr int NCONV = KV8 ? 4 : 0;     // widening warps
   static constexpr int NTHREADS = (12 + NCONV) * 32;
   static constexpr int HALVES = D / 64;         // 128-byte column halves of a 16-bit row
-  static constexpr int HB = KT * 128;           // bytes of one half of a K or V tile
-  static constexpr int TB = HALVES * HB;        // a 16-bit K or V tile
+  // a 16-bit K or V tile: 8-key groups of [half][8 keys][128 B], 128-byte
+  // swizzle.  A cache block's two groups are one TMA box, and both operand
+  // forms (K: keys as N; V: keys as K) step through it evenly
+  static constexpr int GB = HALVES * 1024;      // bytes of a group
+  static constexpr int TB = KT / 8 * GB;
   // where TMA copies land: the tiles themselves, or byte tiles to be widened
   static constexpr int LB = KV8 ? KT * D : TB;
   static constexpr int BLOCKB = LB / BPT;       // one 16-token block
@@ -335,18 +339,19 @@ struct Cfg {
   static constexpr int NL = KV8 ? (D == 128 ? 2 : 6) : NT;     // landing slots of K, and of V
   static constexpr int QHALF = MAXROWS * 128;   // one half of a 128-row Q tile
   static constexpr int QB = HALVES * QHALF;
-  static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = OFF_Q + QB;
-  static constexpr int OFF_V = OFF_K + NT * TB;
+  static constexpr int OFF_K = 0;
+  static constexpr int OFF_Q = OFF_K + NT * TB;
+  static constexpr int OFF_V = OFF_Q + QB;
   static constexpr int OFF_LK = KV8 ? OFF_V + NT * TB : OFF_K;
   static constexpr int OFF_LV = KV8 ? OFF_LK + NL * LB : OFF_V;
   static constexpr int OFF_X = KV8 ? OFF_LV + NL * LB : OFF_V + NT * TB;  // [2][128] fp32: a row's halves exchange
   static constexpr int OFF_IQ = OFF_X + 2 * MAXROWS * 4;
   static constexpr int OFF_BAR = OFF_IQ + NIQ * static_cast<int>(sizeof(Item));
-  static constexpr int BARB = D == 64 ? 640 : 512;
+  static constexpr int BARB = D == 64 ? 768 : 512;
   static constexpr int SMEM = OFF_BAR + BARB + 1024;  // + alignment slack
-  // an M 128 product reads 128 rows of Q from either slot: past a small
-  // slot's rows it reads whatever follows, which only feeds dead rows
+  // an M 128 product reads 128 rows around a slot's: before and behind them
+  // it reads whatever lies there, which only feeds dead rows
+  static_assert(OFF_Q >= 96 * 128, "Q reads stay inside shared memory");
   static_assert(OFF_Q + QB / 2 + QB / 4 * (HALVES - 1) + QHALF <= OFF_X, "Q reads stay inside shared memory");
   static_assert(SMEM <= 232448, "shared memory of one CTA");
   static constexpr uint32_t S_COL = 0;            // two score tiles of KT columns
@@ -364,17 +369,30 @@ template <class C>
 struct Bars {
   uint64_t iq_full[NIQ], iq_empty[NIQ];
   uint64_t lk_full[C::NL], lk_empty[C::NL], lv_full[C::NL], lv_empty[C::NL];  // landed copies
-  uint64_t k_full[C::NT], k_empty[C::NT], v_full[C::NT], v_empty[C::NT];      // 8-bit: widened tiles
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], p_empty[2], o_full[2], o_empty[2];
+  static constexpr int NW = C::KV8 ? C::NT : 1;
+  uint64_t k_full[NW], k_empty[NW], v_full[NW], v_empty[NW];  // 8-bit: widened tiles
+  uint64_t q_full[2], q_empty[2], p_empty[2];
+  uint64_t sw_full[2], sn_full[4][2];    // scores of wide items, of narrow ones by quarter; [buffer]
+  uint64_t ow_full[2], on_full[4];       // outputs (a quarter's items all use one buffer)
+  uint64_t p_full[2][2], o_empty[2][2];  // [narrow][buffer]
   uint64_t drain[2];
   uint32_t tmem;
 };
+
+// A tile of at most 32 rows needs one quarter of the TMEM lanes, and so only
+// the two softmax warps of that quarter.  Such narrow items take the quarters
+// in turn, so that four of them can be in their softmax or output at once.
+__device__ __forceinline__ bool is_narrow(int rows) { return rows <= 32; }
+// First lane of item number `item` of the CTA
+__device__ __forceinline__ int first_lane(int rows, uint32_t item) {
+  return is_narrow(rows) ? static_cast<int>(item & 3) * 32 : 0;
+}
 
 // The Q slot of an item: tiles of up to 64 rows alternate between two
 // half-size slots, larger ones take both.  Every role follows the items in
 // order and so knows the slots and how often each was used.
 struct QSlots {
-  uint32_t uses[2] = {0, 0};
+  uint32_t par = 0;  // bit = slot: parity of its uses so far
   int turn = 0;
   bool big = false;
   int slot = 0;
@@ -388,10 +406,8 @@ struct QSlots {
     }
   }
   __device__ __forceinline__ bool uses_slot(int i) const { return big || slot == i; }
-  __device__ __forceinline__ void done() {
-    for (int i = 0; i < 2; ++i)
-      if (uses_slot(i)) ++uses[i];
-  }
+  __device__ __forceinline__ uint32_t parity(int i) const { return (par >> i) & 1; }
+  __device__ __forceinline__ void done() { par ^= big ? 3u : 1u << slot; }
 };
 
 // Block-table entries of a piece, 32 at a time, the next 32 requested while
@@ -425,31 +441,45 @@ struct TableWindow {
   }
 };
 
+// One 4-D tile of a tensor map (TMA), completing on `bar`.
+__device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int x, int y, int z, int w, uint64_t *bar,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
 // The copies of a piece's K and V blocks into the landing slots, a step at a
 // time; `fill` counts the slots of each filled so far.
 template <class C>
 __device__ bool copy_piece(const Args &a, uint8_t *smem, Bars<C> &bar, const int32_t *table, int nblk, int kvh,
                            uint32_t &fill, uint64_t pol, int lane) {
-  constexpr int BOXES = C::KV8 ? 1 : C::HALVES;
   TableWindow tw;
   tw.begin(a, table, nblk, lane);
-  const int bi = lane / BOXES, hh = lane % BOXES;
   for (int b = 0; b < nblk; b += BPT) {
     const int n = min(BPT, nblk - b);
-    const int row = (tw.at(a, b, bi & (BPT - 1), lane) * a.num_kv + kvh) * 16;
+    const int tile = tw.at(a, b, lane & (BPT - 1), lane) * a.num_kv + kvh;  // (block, kv head)
     const uint32_t st = fill % C::NL, ph = ((fill / C::NL) & 1) ^ 1;
-    const int off = st * C::LB + (C::KV8 ? bi * C::BLOCKB : hh * C::HB + bi * 2048);
+    const int off = st * C::LB + lane * C::BLOCKB;
+    auto copy = [&](int to, const CUtensorMap *map, uint64_t *full) {
+      if (lane == 0) mbar_arrive_expect_tx(full, n * C::BLOCKB);
+      __syncwarp();
+      if (lane < n) {
+        if constexpr (C::KV8)
+          tma_load_2d(smem + to + off, map, 0, tile * 16, full, pol);
+        else
+          tma_load_4d(smem + to + off, map, 0, 0, 0, tile * 2, full, pol);
+      }
+    };
     if (!mbar_wait(&bar.lk_empty[st], ph, a.wait_ns)) return false;
-    if (lane == 0) mbar_arrive_expect_tx(&bar.lk_full[st], n * C::BLOCKB);
-    __syncwarp();
-    if (bi < n) tma_load_2d(smem + C::OFF_LK + off, &a.kmap, hh * 64, row, &bar.lk_full[st], pol);
+    copy(C::OFF_LK, &a.kmap, &bar.lk_full[st]);
     if (!mbar_wait(&bar.lv_empty[st], ph, a.wait_ns)) {
       mbar_wait(&bar.lk_full[st], ph ^ 1, a.wait_ns);  // the K copies just issued land
       return false;
     }
-    if (lane == 0) mbar_arrive_expect_tx(&bar.lv_full[st], n * C::BLOCKB);
-    __syncwarp();
-    if (bi < n) tma_load_2d(smem + C::OFF_LV + off, &a.vmap, hh * 64, row, &bar.lv_full[st], pol);
+    copy(C::OFF_LV, &a.vmap, &bar.lv_full[st]);
     ++fill;
   }
   return true;
@@ -592,31 +622,50 @@ __device__ bool load_q(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *i
     if (!take_item<C>(a, bar, iq, taken, it, lane)) return false;
     if (it.end) return true;
     qs.next(it.rows);
+#pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (qs.uses_slot(i) && !mbar_wait(&bar.q_empty[i], (qs.uses[i] & 1) ^ 1, a.wait_ns)) return false;
+      if (qs.uses_slot(i) && !mbar_wait(&bar.q_empty[i], qs.parity(i) ^ 1, a.wait_ns)) return false;
     uint8_t *base = smem + C::OFF_Q + qs.slot * (C::QB / 2);
     const int half = qs.big ? C::QHALF : C::QHALF / 2;
     float big = 0.f;
-    for (int i = lane; i < it.rows * CH; i += 32) {
-      const int R = i / CH, ch = i % CH;
-      const int sq = R / a.g;
-      const uint16_t *src =
-          a.q + (static_cast<int64_t>(it.seq0 + sq) * a.num_q + it.kvh * a.g + (R - sq * a.g)) * C::D + ch * 8;
-      uint8_t *dst = base + (ch >> 3) * half + R * 128 + (((ch & 7) ^ (R & 7)) << 4);
-      if constexpr (C::KV8) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src));
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        uint32_t o[4];
+    // a lane keeps its 16-byte column chunk; its rows are RPI apart
+    constexpr int RPI = 32 / CH;
+    const int ch = lane % CH;
+    int R = lane / CH, sq = R / a.g, hd = R - sq * a.g;
+    const uint16_t *src0 = a.q + (static_cast<int64_t>(it.seq0) * a.num_q + it.kvh * a.g) * C::D + ch * 8;
+    uint8_t *dst0 = base + (ch >> 3) * half;
+    const int64_t seq_stride = static_cast<int64_t>(a.num_q) * C::D;
+    while (R < it.rows) {
+      constexpr int ILP = 8;
+      uint4 x[ILP];
+      int at[ILP];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float f0 = bf16lo(w[e]), f1 = bf16hi(w[e]);
-          const float f = fmaxf(fabsf(f0), fabsf(f1));
-          if (f <= FLT_MAX) big = fmaxf(big, f);
-          o[e] = pack_f16x2(f0, f1);
+      for (int k = 0; k < ILP; ++k) {
+        const uint16_t *src = src0 + sq * seq_stride + hd * C::D;
+        at[k] = R < it.rows ? R * 128 + (((ch & 7) ^ (R & 7)) << 4) : -1;
+        if constexpr (C::KV8) {
+          if (at[k] >= 0) x[k] = __ldg(reinterpret_cast<const uint4 *>(src));
+        } else {
+          if (at[k] >= 0) cp_async16(dst0 + at[k], src, true);
         }
-        *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-      } else {
-        cp_async16(dst, src, true);
+        R += RPI;
+        for (hd += RPI; hd >= a.g; hd -= a.g) ++sq;
+      }
+      if constexpr (C::KV8) {
+#pragma unroll
+        for (int k = 0; k < ILP; ++k) {
+          if (at[k] < 0) continue;
+          const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float f0 = bf16lo(w[e]), f1 = bf16hi(w[e]);
+            const float f = fmaxf(fabsf(f0), fabsf(f1));
+            if (f <= FLT_MAX) big = fmaxf(big, f);
+            o[e] = pack_f16x2(f0, f1);
+          }
+          *reinterpret_cast<uint4 *>(dst0 + at[k]) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
       }
     }
     if (C::KV8 && big >= 65520.f) report_error(a.err, nullptr, kErrFp16Range);
@@ -642,7 +691,7 @@ __device__ bool widen(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq
   static_assert(RSTEP % 8 == 0 && KT % RSTEP == 0, "a thread's rows agree modulo 8");
   constexpr int PER = KT / RSTEP;
   const int c = ct % CPR, r0 = ct / CPR, r7 = r0 & 7;
-  const int put = (c >> 2) * C::HB + r0 * 128;
+  const int put = (r0 >> 3) * C::GB + (c >> 2) * 1024 + r7 * 128;
   const int x0 = ((2 * (c & 3)) ^ r7) << 4, x1 = ((2 * (c & 3) + 1) ^ r7) << 4;
   uint32_t taken = 0, step = 0;
   Item it;
@@ -677,7 +726,7 @@ __device__ bool widen(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq
               o[2 * e] = fp8x2_to_f16x2<C::KVT>(static_cast<uint16_t>(w[e] & 0xffffu));
               o[2 * e + 1] = fp8x2_to_f16x2<C::KVT>(static_cast<uint16_t>(w[e] >> 16));
             }
-            uint8_t *row = dst + (k0 + k) * RSTEP * 128;
+            uint8_t *row = dst + (k0 + k) * (RSTEP / 8) * C::GB;
             *reinterpret_cast<uint4 *>(row + x0) = make_uint4(o[0], o[1], o[2], o[3]);
             *reinterpret_cast<uint4 *>(row + x1) = make_uint4(o[4], o[5], o[6], o[7]);
           }
@@ -713,22 +762,26 @@ __device__ bool issue_qk(const Args &a, uint32_t sbase, uint32_t tmem, Bars<C> &
     if (end) return true;
     qs.next(rows);
     const uint32_t qhalf = qs.big ? C::QHALF : C::QHALF / 2;
-    const uint64_t qd = umma_desc_sw128(sbase + C::OFF_Q + qs.slot * (C::QB / 2), 16, 1024);
+    // row 0 of the slot is lane first_lane of the product
+    const uint64_t qd =
+        umma_desc_sw128(sbase + C::OFF_Q + qs.slot * (C::QB / 2) - first_lane(rows, taken - 1) * 128, 16, 1024);
+#pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (qs.uses_slot(i) && !mbar_wait(&bar.q_full[i], qs.uses[i] & 1, a.wait_ns)) return false;
+      if (qs.uses_slot(i) && !mbar_wait(&bar.q_full[i], qs.parity(i), a.wait_ns)) return false;
     for (int b = 0; b < nblk; b += BPT, ++k) {
       if (!mbar_wait(&bar.p_empty[k & 1], ((k >> 1) & 1) ^ 1, a.wait_ns)) return false;
       if (!mbar_wait(&k_full[k % C::NT], (k / C::NT) & 1, a.wait_ns)) return false;
       tc_fence_after_sync();
-      const uint64_t kd = umma_desc_sw128(sbase + C::OFF_K + (k % C::NT) * C::TB, 16, 1024);
+      const uint64_t kd = umma_desc_sw128(sbase + C::OFF_K + (k % C::NT) * C::TB, 16, C::GB);
       const uint32_t s = tmem + C::S_COL + (k & 1) * KT;
 #pragma unroll
       for (int kk = 0; kk < C::D / 16; ++kk)
-        umma_bf16_ss(s, qd + (((kk >> 2) * qhalf + (kk & 3) * 32) >> 4), kd + (((kk >> 2) * C::HB + (kk & 3) * 32) >> 4),
+        umma_bf16_ss(s, qd + (((kk >> 2) * qhalf + (kk & 3) * 32) >> 4), kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
                      C::IDESC_QK, kk > 0 ? 1u : 0u);
-      umma_commit(&bar.s_full[k & 1]);
+      umma_commit(is_narrow(rows) ? &bar.sn_full[(taken - 1) & 3][k & 1] : &bar.sw_full[k & 1]);
       umma_commit(&k_empty[k % C::NT]);
     }
+#pragma unroll
     for (int i = 0; i < 2; ++i)
       if (qs.uses_slot(i)) umma_commit(&bar.q_empty[i]);
     qs.done();
@@ -740,25 +793,39 @@ template <class C>
 __device__ bool issue_pv(const Args &a, uint32_t sbase, uint32_t tmem, Bars<C> &bar, const Item *iq) {
   uint64_t *v_full = C::KV8 ? bar.v_full : bar.lv_full, *v_empty = C::KV8 ? bar.v_empty : bar.lv_empty;
   uint32_t taken = 0, k = 0;
+  // the barriers of P and of O count the warps that work on the item, two for
+  // a narrow one and eight else, so there is one of each kind per buffer:
+  // bit 2 * narrow + buffer is the parity of its next phase
+  uint32_t p_par = 0, o_par = 0;
+  uint32_t used = 0, was = 0;  // bit = buffer: it has held an item; that was a narrow one
   for (;;) {
     const uint32_t st = taken % NIQ;
     if (!mbar_wait(&bar.iq_full[st], (taken / NIQ) & 1, a.wait_ns)) return false;
-    const int end = iq[st].end, nblk = iq[st].nblk;
+    const int end = iq[st].end, nblk = iq[st].nblk, nar = is_narrow(iq[st].rows);
     mbar_arrive(&bar.iq_empty[st]);
     const uint32_t item = taken++;
     if (end) return true;
-    const uint32_t o = tmem + C::O_COL + (item & 1) * C::D;
+    const int ob = item & 1;
+    const uint32_t o = tmem + C::O_COL + ob * C::D;
     // the item's first product overwrites the output of the item two before
-    if (!mbar_wait(&bar.o_empty[item & 1], ((item >> 1) & 1) ^ 1, a.wait_ns)) return false;
+    if ((used >> ob) & 1) {
+      const int kind = (was >> ob) & 1, i = 2 * kind + ob;
+      if (!mbar_wait(&bar.o_empty[kind][ob], (o_par >> i) & 1, a.wait_ns)) return false;
+      o_par ^= 1u << i;
+    }
+    used |= 1u << ob;
+    was = (was & ~(1u << ob)) | (static_cast<uint32_t>(nar) << ob);
     for (int b = 0; b < nblk; b += BPT, ++k) {
       if (!mbar_wait(&v_full[k % C::NT], (k / C::NT) & 1, a.wait_ns)) return false;
-      if (!mbar_wait_hint(&bar.p_full[k & 1], (k >> 1) & 1, a.wait_ns)) return false;
+      const int i = 2 * nar + (k & 1);
+      if (!mbar_wait_hint(&bar.p_full[nar][k & 1], (p_par >> i) & 1, a.wait_ns)) return false;
+      p_par ^= 1u << i;
       tc_fence_after_sync();
-      const uint64_t vd = umma_desc_sw128(sbase + C::OFF_V + (k % C::NT) * C::TB, C::HB, 1024);
+      const uint64_t vd = umma_desc_sw128(sbase + C::OFF_V + (k % C::NT) * C::TB, 1024, C::GB);
       const uint32_t p = tmem + C::S_COL + (k & 1) * KT;
       // keys 16 kk .. 16 kk + 15: hi at +0, lo at +16 of their 32-column chunk
       auto block = [&](int kk) {
-        const uint64_t bd = vd + kk * (2048 >> 4);
+        const uint64_t bd = vd + kk * (2 * C::GB >> 4);
         const uint32_t ap = p + (kk >> 1) * 32 + (kk & 1) * 8;
         umma_bf16_ts(o, ap, bd, C::IDESC_PV, (kk > 0 || b > 0) ? 1u : 0u);
         umma_bf16_ts(o, ap + 16, bd, C::IDESC_PV, 1u);
@@ -772,235 +839,289 @@ __device__ bool issue_pv(const Args &a, uint32_t sbase, uint32_t tmem, Bars<C> &
       umma_commit(&v_empty[k % C::NT]);
       umma_commit(&bar.p_empty[k & 1]);
     }
-    umma_commit(&bar.o_full[item & 1]);
+    umma_commit(nar ? &bar.on_full[item & 3] : &bar.ow_full[ob]);
   }
 }
 
-// Warps 4-11: softmax and outputs.  Warps 4-7 take keys 0-63 and warps 8-11
-// keys 64-127 of every step; a thread holds row 32 (warp % 4) + lane (its
-// TMEM lane) and its half h of the keys, later its half of the columns.
-// Partner warps w and w + 4 agree at their named barrier on every wait, so
-// that both go on or both stop.
-template <class C>
-__device__ bool softmax(const Args &a, uint8_t *smem, uint32_t tmem, Bars<C> &bar, const Item *iq, int warp,
-                        int lane) {
-  constexpr int D = C::D;
-  constexpr int PT = C::BF16 ? kKvBf16 : kKvF16;  // type of P
-  const int h = (warp - 4) >> 2;
-  const int row = ((warp & 3) << 5) | lane;
-  const int pair = 1 + (warp & 3);
-  const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-  float *xch = reinterpret_cast<float *>(smem + C::OFF_X);
-  uint64_t *v_full = C::KV8 ? bar.v_full : bar.lv_full, *v_empty = C::KV8 ? bar.v_empty : bar.lv_empty;
-  uint32_t taken = 0, k = 0;
-  bool ok = true;
-  // the finished item whose output waits for the next step to be under way
-  bool pend = false;
-  Item pit;
-  float pm = 0.f, pl = 0.f;
-  uint32_t pnum = 0;
+// 16 consecutive TMEM columns of this warp's 32 lanes (one lane per thread).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
 
-  auto finish = [&]() {
-    pend = false;
-    const int obuf = pnum & 1;
-    const bool mine = (warp & 3) * 32 < pit.rows;  // rows of this warp's lanes live
-    float lsum = pl;
+// Warps 4-11: softmax and outputs.  Warps 4-7 take keys 0-63 and warps 8-11
+// keys 64-127 of every step; a thread holds lane 32 (warp % 4) + lane of the
+// tile and its half h of the keys, later its half of the columns.  A narrow
+// item's warps are those of its quarter.  Partner warps w and w + 4 agree at their named barrier on every wait, so
+// that both go on or both stop.  The loops over 32 scores are not unrolled
+// further: the roles' code shares the SM's instruction caches.
+template <class C>
+struct Softmax {
+  static constexpr int D = C::D;
+  static constexpr int PT = C::BF16 ? kKvBf16 : kKvF16;  // type of P
+  const Args &a;
+  uint8_t *smem;
+  Bars<C> &bar;
+  uint32_t trow;  // this warp's lanes in tensor memory
+  float *xch;
+  int warp, lane, h, row, pair;
+  bool ok = true;
+  // parities of the next phases of the barriers this warp waits on.  A warp
+  // sees every phase of the wide items' barriers and of its own quarter's,
+  // and no other's, so each parity names one phase.
+  uint32_t sw = 0, sn = 0;  // scores: bit = buffer
+  uint32_t ow = 0, on = 0;  // outputs: bit = buffer; bit 0
+
+  // An item's output, once its last product is through.
+  __device__ __forceinline__ void finish(const Item &it, uint32_t num, float m, float l) {
+    const int ob = num & 1;
+    const int r = row - first_lane(it.rows, num);  // row of the tile
+    const bool live = r >= 0 && r < it.rows;
+    const bool mine = __any_sync(0xffffffffu, live);  // the same for both partners
+    float lsum = l;
     if (mine) {
       named_bar_sync(pair, 64);  // the partner has read the last maxima
-      xch[h * MAXROWS + row] = pl;
+      xch[h * MAXROWS + row] = l;
       named_bar_sync(pair, 64);
       lsum += xch[(h ^ 1) * MAXROWS + row];
     }
-    ok = mbar_wait(&bar.o_full[obuf], (pnum >> 1) & 1, a.wait_ns) && ok;
+    if (is_narrow(it.rows)) {
+      ok = mbar_wait(&bar.on_full[warp & 3], on, a.wait_ns) && ok;
+      on ^= 1;
+    } else {
+      ok = mbar_wait(&bar.ow_full[ob], (ow >> ob) & 1, a.wait_ns) && ok;
+      ow ^= 1u << ob;
+    }
     if (mine && ok) {
       tc_fence_after_sync();
-      const bool live = row < pit.rows;
-      const int sq = row / a.g;
-      const int64_t orow = static_cast<int64_t>(pit.seq0 + sq) * a.num_q + pit.kvh * a.g + (row - sq * a.g);
-      float *dst, *dl;
-      if (pit.to == kToCut) {
-        const int64_t x = static_cast<int64_t>(pit.slot) * a.slot_rows + row;
-        dst = a.cut_o + x * D;
-        dl = a.cut_lse + x;
-      } else {
-        dst = (pit.to == kToOut ? a.out : pit.to == kToPre ? a.pre_o : a.own_o) + orow * D;
-        dl = pit.to == kToOut ? (a.lse ? a.lse + orow : nullptr) : (pit.to == kToPre ? a.pre_lse : a.own_lse) + orow;
-      }
+      const int sq = live ? r / a.g : 0;
+      const int64_t orow = static_cast<int64_t>(it.seq0 + sq) * a.num_q + it.kvh * a.g + (r - sq * a.g);
+      const int64_t srow = static_cast<int64_t>(it.slot) * a.slot_rows + r;
+      float *dst = it.to == kToCut ? a.cut_o + srow * D
+                                   : (it.to == kToOut ? a.out : it.to == kToPre ? a.pre_o : a.own_o) + orow * D;
       // no key (a sequence shorter than the piece's first one): nothing to weigh
       const bool none = lsum == 0.f;
       float inv = none ? 0.f : 1.f / lsum;
-      if (pit.to == kToOut) inv *= a.v_scales ? __ldg(a.v_scales + pit.kvh) : a.vscale;
-#pragma unroll 1
-      for (int c0 = h * (D / 2); c0 < (h + 1) * (D / 2); c0 += 32) {
-        float o[32];
-        tmem_ld32(trow + C::O_COL + obuf * D + c0, o);
-        if (live) {
-#pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4 *>(dst + c0 + i) =
-                none ? make_float4(0.f, 0.f, 0.f, 0.f)
-                     : make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
-        }
+      if (it.to == kToOut) inv *= a.v_scales ? __ldg(a.v_scales + it.kvh) : a.vscale;
+      if (live && h == 0) {
+        const float ls = none ? -INFINITY : m + log2f(lsum) - C::PB;
+        if (it.to == kToCut)
+          a.cut_lse[srow] = ls;
+        else if (it.to != kToOut)
+          (it.to == kToPre ? a.pre_lse : a.own_lse)[orow] = ls;
+        else if (a.lse)
+          a.lse[orow] = ls * kLn2;
       }
-      if (live && h == 0 && dl) {
-        const float ls = none ? -INFINITY : pm + log2f(lsum) - C::PB;
-        *dl = pit.to == kToOut ? ls * kLn2 : ls;
+      // rows of a quad of lanes change places with its column chunks, so that
+      // a store writes 64 consecutive bytes of each of eight rows
+      const int q = lane & 3;
+      float *qdst[4];
+      bool qlive[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int src = (lane & ~3) | j;
+        qdst[j] = reinterpret_cast<float *>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), src));
+        qlive[j] = __shfl_sync(0xffffffffu, static_cast<int>(live), src) != 0;
+      }
+#pragma unroll 1
+      for (int c0 = h * (D / 2); c0 < (h + 1) * (D / 2); c0 += 16) {
+        float o[16];
+        tmem_ld16(trow + C::O_COL + ob * D + c0, o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = none ? 0.f : o[i] * inv;
+        // 4 x 4 transpose of float4s over the quad, in two exchanges
+#pragma unroll
+        for (int bit = 1; bit < 4; bit <<= 1) {
+          const bool up = (q & bit) != 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (j & bit) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float give = up ? o[4 * j + e] : o[4 * (j | bit) + e];
+              const float got = __shfl_xor_sync(0xffffffffu, give, bit);
+              if (up)
+                o[4 * j + e] = got;
+              else
+                o[4 * (j | bit) + e] = got;
+            }
+          }
+        }
+        // o[4 j ..] is now column chunk q of the quad's row j
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (qlive[j])
+            *reinterpret_cast<float4 *>(qdst[j] + c0 + 4 * q) =
+                make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
       }
     }
     tc_fence_before_sync();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&bar.o_empty[obuf]);
-  };
-
-  for (;;) {
-    Item it;
-    const bool got = take_item<C>(a, bar, iq, taken, it, lane);
-    if (!named_bar_and(pair, 64, got && ok)) return false;
-    if (it.end) break;
-    const bool mine = (warp & 3) * 32 < it.rows;
-    const bool live = row < it.rows;
-    int lim = live ? it.kend : 0;  // keys from here on are not the row's
-    if (live && it.prefix) lim = min(lim, a.seqs[it.seq0 + row / a.g].len);
-    float qsc = a.k_scales ? a.qscale0 * __ldg(a.k_scales + it.kvh) : a.qscale;
-    // the maximum is taken of the scores as they are, so a scale that is not
-    // positive goes into them first (and masked scores never meet a 0)
-    const float sgn = qsc < 0.f ? -1.f : 0.f;
-    const bool turn = !(qsc > 0.f);
-    if (turn) qsc = qsc < 0.f ? -qsc : 1.f;
-    float m = -INFINITY, l = 0.f;
-    for (int b = 0; b < it.nblk; b += BPT, ++k) {
-      const int n = min(BPT, it.nblk - b);
-      const int key0 = it.key0 + b * 16;
-      bool there = mbar_wait_hint(&bar.s_full[k & 1], (k >> 1) & 1, a.wait_ns);
-      tc_fence_after_sync();
-      if (!C::KV8 && it.kend < key0 + n * 16) {
-        // V rows past the item's keys may hold anything (0 * NaN is NaN)
-        there = there && mbar_wait(&v_full[k % C::NT], (k / C::NT) & 1, a.wait_ns);
-        const int keep = it.kend - key0;
-        const int i = threadIdx.x - 128;
-        if (there && i < (n * 16 - keep) * C::HALVES * 8) {
-          const int r = keep + i / (C::HALVES * 8), c = i % (C::HALVES * 8);
-          *reinterpret_cast<uint4 *>(smem + C::OFF_V + (k % C::NT) * C::TB + (c >> 3) * C::HB + r * 128 +
-                                     (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-      }
-      if (!named_bar_and(pair, 64, there && ok)) return false;
-      if (mine) {
-        const uint32_t scol = trow + C::S_COL + (k & 1) * KT + 64 * h;
-        const int kh = key0 + 64 * h;
-        // scores as the softmax takes them: a scale that is not positive
-        // applied, keys past the row's limit out
-        auto ready = [&](int c, uint32_t(&x)[32]) {
-          if (turn) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * sgn);
-          }
-          if (kh + 32 * c + 32 > lim) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (kh + 32 * c + i >= lim) x[i] = __float_as_uint(-INFINITY);
-          }
-        };
-        // both chunks of 32 stay in registers, or (8-bit caches, whose 16
-        // warps leave 128 registers a thread) are read again for P
-        constexpr int HOLD = C::KV8 ? 1 : 2;
-        uint32_t sc[HOLD][32];
-        if constexpr (HOLD == 2) {
-          tmem_ld32_async(scol, sc[0]);
-          tmem_ld32_async(scol + 32, sc[1]);
-          tmem_wait_ld(sc[0]);
-          tmem_wait_ld(sc[1]);
-        }
-        float mx = -INFINITY;
-#pragma unroll
-        for (int c0 = 0; c0 < 2; ++c0) {
-          const int c = c0 % HOLD;
-          if constexpr (HOLD == 1) {
-            tmem_ld32_async(scol + 32 * c0, sc[0]);
-            tmem_wait_ld(sc[0]);
-          }
-          ready(c0, sc[c]);
-          float t[11];  // a tree of three-input maxima
-#pragma unroll
-          for (int i = 0; i < 10; ++i)
-            t[i] = fmax3(__uint_as_float(sc[c][3 * i]), __uint_as_float(sc[c][3 * i + 1]),
-                         __uint_as_float(sc[c][3 * i + 2]));
-          t[10] = fmaxf(__uint_as_float(sc[c][30]), __uint_as_float(sc[c][31]));
-          mx = fmax3(mx, fmax3(fmax3(t[0], t[1], t[2]), fmax3(t[3], t[4], t[5]), fmax3(t[6], t[7], t[8])),
-                     fmaxf(t[9], t[10]));
-        }
-        // the row's maximum over both halves (the barrier behind the wait above
-        // says that the partner has read the last exchange)
-        xch[h * MAXROWS + row] = mx;
-        named_bar_sync(pair, 64);
-        mx = fmaxf(mx, xch[(h ^ 1) * MAXROWS + row]);
-        mx = mx == -INFINITY ? mx : mx * qsc;
-        const bool raise = mx > m + kRaise;  // m = -inf: any finite score
-        if (__any_sync(0xffffffffu, raise && m != -INFINITY)) {
-          // rare: this half of O's columns takes the new maximum; the product
-          // of the step before, which releases its V tile, is through
-          if (b > 0) ok = mbar_wait(&v_empty[(k - 1) % C::NT], ((k - 1) / C::NT) & 1, a.wait_ns) && ok;
-          tc_fence_after_sync();
-          const float f = (raise && m != -INFINITY) ? exp2f(m - mx) : 1.f;
-          l *= f;
-#pragma unroll 1
-          for (int c0 = h * (D / 2); c0 < (h + 1) * (D / 2); c0 += 32) {
-            float o[32];
-            tmem_ld32(trow + C::O_COL + ((taken - 1) & 1) * D + c0, o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= f;
-            tmem_st32(trow + C::O_COL + ((taken - 1) & 1) * D + c0, o);
-          }
-        }
-        if (raise) m = mx;
-        // P = 2^(score - m + PB) in pairs; 32 keys become 16 columns of hi
-        // pairs and 16 of lo pairs over their own, loaded, scores
-        const float off = C::PB - (m == -INFINITY ? 0.f : m);
-        const uint64_t q2 = f2_pack(qsc, qsc), o2 = f2_pack(off, off);
-        uint64_t ls[2] = {0, 0};
-#pragma unroll
-        for (int c0 = 0; c0 < 2; ++c0) {
-          // (with one chunk held: the second is still there)
-          const int c = c0 % HOLD, cc = HOLD == 1 ? 1 - c0 : c0;
-          if (HOLD == 1 && c0 == 1) {
-            tmem_ld32_async(scol, sc[0]);
-            tmem_wait_ld(sc[0]);
-            ready(0, sc[0]);
-          }
-          uint32_t hi[16], lo[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 y = f2_unpack(
-                f2_fma(f2_pack(__uint_as_float(sc[c][2 * e]), __uint_as_float(sc[c][2 * e + 1])), q2, o2));
-            const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
-            const uint64_t pp = f2_pack(p0, p1);
-            ls[e & 1] = f2_add(ls[e & 1], pp);
-            hi[e] = pack16x2<PT>(p0, p1);
-            const float2 d = f2_unpack(f2_sub(pp, f2_pack(lo16<PT>(hi[e]), hi16<PT>(hi[e]))));
-            lo[e] = pack16x2<PT>(d.x, d.y);
-          }
-          tmem_st16_async(scol + 32 * cc, hi);
-          tmem_st16_async(scol + 32 * cc + 16, lo);
-        }
-        const float2 l2 = f2_unpack(f2_add(ls[0], ls[1]));
-        l += l2.x + l2.y;
-        tmem_wait_st();
-      }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.p_full[k & 1]);
-      if (pend) finish();
-    }
-    pend = true;
-    pit = it;
-    pm = m;
-    pl = l;
-    pnum = taken - 1;
+    if (lane == 0 && (mine || !is_narrow(it.rows))) mbar_arrive(&bar.o_empty[is_narrow(it.rows)][ob]);
   }
-  if (pend) finish();
-  return ok;
-}
+
+  __device__ bool run(const Item *iq) {
+    uint64_t *v_full = C::KV8 ? bar.v_full : bar.lv_full, *v_empty = C::KV8 ? bar.v_empty : bar.lv_empty;
+    uint32_t taken = 0, k = 0;
+    for (;;) {
+      Item it;
+      const bool got = take_item<C>(a, bar, iq, taken, it, lane);
+      if (!named_bar_and(pair, 64, got && ok)) return false;
+      const uint32_t num = taken - 1;
+      const bool nar = is_narrow(it.rows);
+      if (it.end) return ok;
+      const int r = row - first_lane(it.rows, num);
+      const bool live = r >= 0 && r < it.rows;
+      const bool mine = __any_sync(0xffffffffu, live);
+      const int steps = (it.nblk + BPT - 1) / BPT;
+      if (nar && !mine) {  // another quarter's
+        k += steps;
+        continue;
+      }
+      // keys from here on are not the row's (rows of no sequence take what
+      // comes: nothing reads theirs)
+      int lim = 0x7fffffff;
+      if (live) lim = it.prefix ? min(it.kend, a.seqs[it.seq0 + r / a.g].len) : it.kend;
+      float qsc = a.k_scales ? a.qscale0 * __ldg(a.k_scales + it.kvh) : a.qscale;
+      // the maximum is taken of the scores as they are, so a scale that is not
+      // positive goes into them first (and masked scores never meet a 0)
+      const float sgn = qsc < 0.f ? -1.f : 0.f;
+      const bool turn = !(qsc > 0.f);
+      if (turn) qsc = qsc < 0.f ? -qsc : 1.f;
+      float m = -INFINITY, l = 0.f;
+      for (int b = 0; b < it.nblk; b += BPT, ++k) {
+        const int n = min(BPT, it.nblk - b);
+        const int key0 = it.key0 + b * 16;
+        bool there;
+        if (nar) {
+          there = mbar_wait_hint(&bar.sn_full[warp & 3][k & 1], (sn >> (k & 1)) & 1, a.wait_ns);
+          sn ^= 1u << (k & 1);
+        } else {
+          there = mbar_wait_hint(&bar.sw_full[k & 1], (sw >> (k & 1)) & 1, a.wait_ns);
+          sw ^= 1u << (k & 1);
+        }
+        tc_fence_after_sync();
+        if (!C::KV8 && it.kend < key0 + n * 16) {
+          // V rows past the item's keys may hold anything (0 * NaN is NaN)
+          there = there && mbar_wait(&v_full[k % C::NT], (k / C::NT) & 1, a.wait_ns);
+          const int keep = it.kend - key0;
+          const int threads = nar ? 64 : 256, me = nar ? h * 32 + lane : static_cast<int>(threadIdx.x) - 128;
+          uint8_t *v = smem + C::OFF_V + (k % C::NT) * C::TB;
+          for (int i = me; there && i < (n * 16 - keep) * C::HALVES * 8; i += threads) {
+            const int rr = keep + i / (C::HALVES * 8), c = i % (C::HALVES * 8);
+            *reinterpret_cast<uint4 *>(v + (rr >> 3) * C::GB + (c >> 3) * 1024 + (rr & 7) * 128 + (c & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        if (!named_bar_and(pair, 64, there && ok)) return false;
+        if (mine) step(k, key0, b > 0, lim, live, qsc, turn, sgn, num, v_empty, m, l);
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.p_full[nar][k & 1]);
+      }
+      finish(it, num, m, l);
+    }
+  }
+
+  // One step's scores (in tensor memory) to P over them; m and l follow.
+  __device__ __forceinline__ void step(uint32_t k, int key0, bool later, int lim, bool live, float qsc, bool turn,
+                                       float sgn, uint32_t num, uint64_t *v_empty, float &m, float &l) {
+    const uint32_t scol = trow + C::S_COL + (k & 1) * KT + 64 * h;
+    const int kh = key0 + 64 * h;
+    // 32 scores as the softmax takes them: a scale that is not positive
+    // applied, keys past the row's limit out
+    auto load = [&](int c, uint32_t(&x)[32]) {
+      tmem_ld32_async(scol + 32 * c, x);
+      tmem_wait_ld(x);
+      if (turn) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * sgn);
+      }
+      if (kh + 32 * c + 32 > lim) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (kh + 32 * c + i >= lim) x[i] = __float_as_uint(-INFINITY);
+      }
+    };
+    uint32_t sc[32];
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int c = 1; c >= 0; --c) {
+      load(c, sc);
+      float t[11];  // a tree of three-input maxima
+#pragma unroll
+      for (int i = 0; i < 10; ++i)
+        t[i] = fmax3(__uint_as_float(sc[3 * i]), __uint_as_float(sc[3 * i + 1]), __uint_as_float(sc[3 * i + 2]));
+      t[10] = fmaxf(__uint_as_float(sc[30]), __uint_as_float(sc[31]));
+      mx = fmax3(mx, fmax3(fmax3(t[0], t[1], t[2]), fmax3(t[3], t[4], t[5]), fmax3(t[6], t[7], t[8])),
+                 fmaxf(t[9], t[10]));
+    }
+    // the row's maximum over both halves (the barrier behind the wait above
+    // says that the partner has read the last exchange)
+    xch[h * MAXROWS + row] = mx;
+    named_bar_sync(pair, 64);
+    mx = fmaxf(mx, xch[(h ^ 1) * MAXROWS + row]);
+    mx = mx == -INFINITY ? mx : mx * qsc;
+    const bool raise = live && mx > m + kRaise;  // m = -inf: any finite score
+    if (__any_sync(0xffffffffu, raise && m != -INFINITY)) {
+      // rare: this half of O's columns takes the new maximum; the product of
+      // the step before, which releases its V tile, is through
+      if (later) ok = mbar_wait(&v_empty[(k - 1) % C::NT], ((k - 1) / C::NT) & 1, a.wait_ns) && ok;
+      tc_fence_after_sync();
+      const float f = (raise && m != -INFINITY) ? exp2f(m - mx) : 1.f;
+      l *= f;
+#pragma unroll 1
+      for (int c0 = h * (D / 2); c0 < (h + 1) * (D / 2); c0 += 32) {
+        float o[32];
+        tmem_ld32(trow + C::O_COL + (num & 1) * D + c0, o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] *= f;
+        tmem_st32(trow + C::O_COL + (num & 1) * D + c0, o);
+      }
+    }
+    if (raise) m = mx;
+    // P = 2^(score - m + PB) in pairs; 32 keys become 16 columns of hi pairs
+    // and 16 of lo pairs over their own, loaded, scores (chunk 0's are still
+    // in registers)
+    const float off = C::PB - (m == -INFINITY ? 0.f : m);
+    const uint64_t q2 = f2_pack(qsc, qsc), o2 = f2_pack(off, off);
+    uint64_t ls[2] = {0, 0};
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {
+      if (c == 1) load(1, sc);
+      uint32_t hi[16], lo[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float2 y =
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(sc[2 * e]), __uint_as_float(sc[2 * e + 1])), q2, o2));
+        const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
+        const uint64_t pp = f2_pack(p0, p1);
+        ls[e & 1] = f2_add(ls[e & 1], pp);
+        hi[e] = pack16x2<PT>(p0, p1);
+        const float2 d = f2_unpack(f2_sub(pp, f2_pack(lo16<PT>(hi[e]), hi16<PT>(hi[e]))));
+        lo[e] = pack16x2<PT>(d.x, d.y);
+      }
+      tmem_st16_async(scol + 32 * c, hi);
+      tmem_st16_async(scol + 32 * c + 16, lo);
+    }
+    const float2 l2 = f2_unpack(f2_add(ls[0], ls[1]));
+    l += l2.x + l2.y;
+    tmem_wait_st();
+  }
+};
 
 template <int D, int KVT>
 __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel(const __grid_constant__ Args a) {
@@ -1022,7 +1143,7 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
       mbar_init(&bar.lv_full[i], 1);
       mbar_init(&bar.lv_empty[i], C::KV8 ? C::NCONV : 1);
     }
-    for (int i = 0; i < C::NT; ++i) {
+    for (int i = 0; i < Bars<C>::NW; ++i) {
       mbar_init(&bar.k_full[i], C::KV8 ? C::NCONV : 1);
       mbar_init(&bar.k_empty[i], 1);
       mbar_init(&bar.v_full[i], C::KV8 ? C::NCONV : 1);
@@ -1031,12 +1152,19 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.q_full[i], 1);
       mbar_init(&bar.q_empty[i], 1);
-      mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_full[i], 8);
+      mbar_init(&bar.sw_full[i], 1);
+      mbar_init(&bar.ow_full[i], 1);
+      for (int nar = 0; nar < 2; ++nar) {
+        mbar_init(&bar.p_full[nar][i], nar ? 2 : 8);
+        mbar_init(&bar.o_empty[nar][i], nar ? 2 : 8);
+      }
       mbar_init(&bar.p_empty[i], 1);
       mbar_init(&bar.drain[i], 1);
-      mbar_init(&bar.o_full[i], 1);
-      mbar_init(&bar.o_empty[i], 8);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bar.sn_full[i][0], 1);
+      mbar_init(&bar.sn_full[i][1], 1);
+      mbar_init(&bar.on_full[i], 1);
     }
     fence_mbar_init();
   }
@@ -1059,7 +1187,18 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
   } else if (warp == 3) {
     ok = load_q<C>(a, smem, bar, iq, lane);
   } else if (warp < 12) {
-    ok = softmax<C>(a, smem, tmem, bar, iq, warp, lane);
+    const int h = (warp - 4) >> 2;
+    Softmax<C> sm{a,
+                  smem,
+                  bar,
+                  tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16),
+                  reinterpret_cast<float *>(smem + C::OFF_X),
+                  warp,
+                  lane,
+                  h,
+                  ((warp & 3) << 5) | lane,
+                  1 + (warp & 3)};
+    ok = sm.run(iq);
   } else if constexpr (C::KV8) {
     ok = widen<C>(a, smem, bar, iq, threadIdx.x - 12 * 32, lane);
   }
