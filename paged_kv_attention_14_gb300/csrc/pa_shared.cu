@@ -132,7 +132,7 @@ cudaError_t launch_shared(const pa_kv_desc &d, float *out, float *lse, const voi
   a.checked = d.check_indices;
   const TestHooks hooks = test_hooks();
   a.stall = hooks.stall;
-  a.wait_ns = hooks.wait_ns;
+  a.wait_ns = static_cast<uint32_t>(hooks.wait_ns < 0x7fffffffull ? hooks.wait_ns : 0x7fffffffull);
   a.err = d.error_word;
   a.axis = reinterpret_cast<shd::Axis *>(ws + w.axis);
   a.groups = reinterpret_cast<shd::GroupInfo *>(ws + w.groups);
@@ -164,7 +164,7 @@ cudaError_t launch_shared(const pa_kv_desc &d, float *out, float *lse, const voi
   cfg.dynamicSmemBytes = k.smem;
   e = cudaLaunchKernelExC(&cfg, k.fn, args);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(num_seqs) * d.num_q_heads + 7) / 8));
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(num_seqs) * d.num_q_heads + 15) / 16));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   const void *join = d.head_dim == 64 ? reinterpret_cast<const void *>(&shd::shared_join_kernel<64>)

@@ -18,7 +18,7 @@
 //  * shared_attend_kernel, one persistent CTA per SM: CTA c takes the units
 //    [c n, (c + 1) n) of that axis, so every CTA has the same work whatever
 //    the lengths; an item cut between CTAs leaves a piece in each.
-//  * shared_join_kernel, one warp per (sequence, head): joins the parts.
+//  * shared_join_kernel, a warp per two (sequence, head) rows: joins the parts.
 //
 // The attention runs on tcgen05 for every item, a sequence's few heads
 // included: an M 128 product costs the tensor cores the same whatever its
@@ -127,18 +127,18 @@ struct Args {
   int num_blocks;
   int checked;
   int stall;
-  unsigned long long wait_ns;
+  uint32_t wait_ns;  // limit of every bounded wait
   int32_t *err;
   // workspace
   Axis *axis;
   GroupInfo *groups;
   SeqInfo *seqs;
   CtaStart *starts;
-  float *pre_o;    // [S][Hq][D] prefix parts of uncut items, normalised
-  float *pre_lse;  // [S][Hq], log2 units
-  float *own_o;    // ... own parts
+  float *pre_o;    // prefix parts of uncut items, normalised: tile after tile of [D / 4][rows][4]
+  float *pre_lse;  // ... their log-sum-exps, log2 units
+  float *own_o;    // own parts, [S][Hq][D]
   float *own_lse;
-  float *cut_o;    // [ctas][2][slot_rows][D] pieces of cut items
+  float *cut_o;    // pieces of cut items, [ctas][2][D / 4][slot_rows][4]
   float *cut_lse;
 };
 
@@ -147,8 +147,11 @@ struct Args {
 constexpr int PLAN_THREADS = 512;
 constexpr int PLAN_CAP = 512;  // sequences / groups planned in shared memory
 
+// n / d, in one place: a 64-bit division is some 100 instructions
+static __device__ __noinline__ long long divide(long long n, long long d) { return n / d; }
+
 // Exclusive prefix sum over the CTA's threads; *total gets the sum.
-__device__ __forceinline__ long long scan_exclusive(long long v, long long *total, long long *s_warp) {
+static __device__ __noinline__ long long scan_exclusive(long long v, long long *total, long long *s_warp) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long incl = v;
 #pragma unroll
@@ -160,7 +163,7 @@ __device__ __forceinline__ long long scan_exclusive(long long v, long long *tota
   if (lane == 31) s_warp[warp] = incl;
   __syncthreads();
   long long before = 0, sum = 0;
-#pragma unroll
+#pragma unroll 4
   for (int i = 0; i < PLAN_THREADS / 32; ++i) {
     const long long x = s_warp[i];
     if (i < warp) before += x;
@@ -178,6 +181,7 @@ __host__ __device__ __forceinline__ int item_units(int nb) { return nb > 0 ? nb 
 template <class T>
 __device__ __forceinline__ int find_base(const T *v, int n, long long u) {
   int lo = 0, hi = n - 1;
+#pragma unroll 1
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (v[mid].base <= u)
@@ -199,6 +203,7 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
   const int cap = a.max_blocks * 16;
   SeqInfo *seqs = S <= PLAN_CAP ? s_seqs : a.seqs;
   GroupInfo *groups = G <= PLAN_CAP ? s_groups : a.groups;
+#pragma unroll 1
   for (int s = tid; s < S; s += PLAN_THREADS) {
     int L = __ldg(a.context_lens + s);
     if (a.checked) L = checked_len(L, cap, a.err, nullptr);
@@ -209,6 +214,7 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
   }
   __syncthreads();
   // one warp per group: its sequences, and how much of the prefix they read
+#pragma unroll 1
   for (int j = warp; j < G; j += PLAN_THREADS / 32) {
     const int r0 = __ldg(a.group_start + j), r1 = __ldg(a.group_start + j + 1);
     int P = __ldg(a.prefix_lens + j);
@@ -218,6 +224,7 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
     P = min(max(P, 0), cap) & ~15;
     if (s1 - s0 < 2) P = 0;  // nobody to share with
     int mine = -1, row = 0;
+#pragma unroll 1
     for (int s = s0 + lane; s < s1; s += 32) {
       const int n = min(seqs[s].len, P);
       if (n > mine) {
@@ -246,6 +253,7 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
   __syncthreads();
   // places on the axis: prefix items, then own parts
   long long at = 0;
+#pragma unroll 1
   for (int j0 = 0; j0 < G; j0 += PLAN_THREADS) {
     const int j = j0 + tid;
     const long long v = j < G ? static_cast<long long>(item_units(groups[j].nb)) * groups[j].tiles * a.num_kv : 0;
@@ -255,6 +263,7 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
     at += sum;
   }
   const long long own = at;  // first unit of the own parts
+#pragma unroll 1
   for (int s0 = 0; s0 < S; s0 += PLAN_THREADS) {
     const int s = s0 + tid;
     const int nb = s < S ? max(0, ((seqs[s].len + 15) >> 4) - seqs[s].fb) : 0;
@@ -267,29 +276,29 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
     at += sum;
   }
   const long long U = at;
-  const long long per = max((U + a.ctas - 1) / a.ctas, static_cast<long long>(kMinUnits));
+  const long long per = max(divide(U + a.ctas - 1, a.ctas), static_cast<long long>(kMinUnits));
   if (tid == 0) *a.axis = Axis{U, per};
   __syncthreads();
   // each CTA's first item
+#pragma unroll 1
   for (int c = tid; c < a.ctas; c += PLAN_THREADS) {
     const long long u = c * per;
     CtaStart st = {2, 0, 0, 0};
-    if (u < own) {
-      const int j = find_base(groups, G, u);
-      const long long r = u - groups[j].base;
-      const int n = item_units(groups[j].nb);
-      st = CtaStart{0, j, static_cast<int>(r / n), static_cast<int>(r % n)};
-    } else if (u < U) {
-      const int s = find_base(seqs, S, u);
-      const long long r = u - seqs[s].base;
-      const int n = item_units(seqs[s].nb);
-      st = CtaStart{1, s, static_cast<int>(r / n), static_cast<int>(r % n)};
+    if (u < U) {
+      st.kind = u < own ? 0 : 1;
+      st.idx = st.kind == 0 ? find_base(groups, G, u) : find_base(seqs, S, u);
+      const int n = item_units(st.kind == 0 ? groups[st.idx].nb : seqs[st.idx].nb);
+      const long long r = u - (st.kind == 0 ? groups[st.idx].base : seqs[st.idx].base);
+      st.sub = static_cast<int>(divide(r, n));
+      st.off = static_cast<int>(r - static_cast<long long>(st.sub) * n);
     }
     a.starts[c] = st;
   }
   if (S <= PLAN_CAP)
+#pragma unroll 1
     for (int s = tid; s < S; s += PLAN_THREADS) a.seqs[s] = s_seqs[s];
   if (G <= PLAN_CAP)
+#pragma unroll 1
     for (int j = tid; j < G; j += PLAN_THREADS) a.groups[j] = s_groups[j];
 }
 
@@ -309,7 +318,7 @@ struct __align__(16) Item {
   int key0;    // position of the piece's first token
   int kend;    // keys from here on are not the piece's
   int nblk;    // blocks of the piece
-  int table;   // sequence whose block table is read
+  int lo;      // first block, counted from the item's
   int to;
   int slot;    // kToCut: the slot
   int prefix;  // 1: rows have limits of their own (their lengths)
@@ -317,6 +326,22 @@ struct __align__(16) Item {
 };
 
 constexpr int NIQ = 4;  // items in flight between the roles
+
+// Waits until the phase of `bar` with the given parity has completed; false
+// if that does not happen within limit_ns (at most 2^31).  Short on purpose:
+// it is in the kernel some forty times, and the roles share the SM's
+// instruction caches.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, uint32_t limit_ns) {
+  const uint32_t addr = smem_u32(bar);
+  uint32_t t0 = 0, t1 = 0;
+#pragma unroll 1
+  for (bool first = true; !mbar_test(addr, parity); first = false) {
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t1));
+    if (first) t0 = t1;
+    if (t1 - t0 > limit_ns) return false;
+  }
+  return true;
+}
 
 template <int D_, int KVT_>
 struct Cfg {
@@ -458,6 +483,7 @@ __device__ bool copy_piece(const Args &a, uint8_t *smem, Bars<C> &bar, const int
                            uint32_t &fill, uint64_t pol, int lane) {
   TableWindow tw;
   tw.begin(a, table, nblk, lane);
+#pragma unroll 1
   for (int b = 0; b < nblk; b += BPT) {
     const int n = min(BPT, nblk - b);
     const int tile = tw.at(a, b, lane & (BPT - 1), lane) * a.num_kv + kvh;  // (block, kv head)
@@ -473,10 +499,10 @@ __device__ bool copy_piece(const Args &a, uint8_t *smem, Bars<C> &bar, const int
           tma_load_4d(smem + to + off, map, 0, 0, 0, tile * 2, full, pol);
       }
     };
-    if (!mbar_wait(&bar.lk_empty[st], ph, a.wait_ns)) return false;
+    if (!wait(&bar.lk_empty[st], ph, a.wait_ns)) return false;
     copy(C::OFF_LK, &a.kmap, &bar.lk_full[st]);
-    if (!mbar_wait(&bar.lv_empty[st], ph, a.wait_ns)) {
-      mbar_wait(&bar.lk_full[st], ph ^ 1, a.wait_ns);  // the K copies just issued land
+    if (!wait(&bar.lv_empty[st], ph, a.wait_ns)) {
+      wait(&bar.lk_full[st], ph ^ 1, a.wait_ns);  // the K copies just issued land
       return false;
     }
     copy(C::OFF_LV, &a.vmap, &bar.lv_full[st]);
@@ -488,109 +514,113 @@ __device__ bool copy_piece(const Args &a, uint8_t *smem, Bars<C> &bar, const int
 // After a failed wait: the copies already issued land before the CTA exits.
 template <class C>
 __device__ void drain_copies(const Args &a, Bars<C> &bar, uint32_t fill) {
+#pragma unroll 1
   for (uint32_t i = fill > C::NL ? fill - C::NL : 0; i < fill; ++i) {
-    mbar_wait(&bar.lk_full[i % C::NL], (i / C::NL) & 1, a.wait_ns);
-    mbar_wait(&bar.lv_full[i % C::NL], (i / C::NL) & 1, a.wait_ns);
+    wait(&bar.lk_full[i % C::NL], (i / C::NL) & 1, a.wait_ns);
+    wait(&bar.lv_full[i % C::NL], (i / C::NL) & 1, a.wait_ns);
   }
 }
 
 // Warp 1: the CTA's items, and their copies.
 template <class C>
 __device__ bool walk(const Args &a, uint8_t *smem, Bars<C> &bar, Item *iq, int lane) {
+  if (a.stall) return true;  // test hook: nothing is issued, every wait runs out
   const int me = blockIdx.x;
   const Axis ax = *a.axis;
   const long long b0 = me * ax.per, b1 = min(b0 + ax.per, ax.units);
   const uint64_t pol = l2_evict_first_policy();
   uint32_t fill = 0, posted = 0;
+  long long left = b1 - b0;
+  CtaStart st = a.starts[me];
+  if (left <= 0) st.kind = 2;
+  int kind = -1, items = 0, nb = 0, fb = 0, first = 0, n = 1, tile_seqs = 1, kend = 0, row = 0, whole_to = 0;
+  const int32_t *table = nullptr;
   bool ok = true;
-  auto post = [&](const Item &it) {
-    const uint32_t st = posted % NIQ, ph = (posted / NIQ) & 1;
-    if (!mbar_wait(&bar.iq_empty[st], ph ^ 1, a.wait_ns)) return false;
-    if (lane == 0) {
-      iq[st] = it;
-      mbar_arrive(&bar.iq_full[st]);
-    }
-    __syncwarp();
-    ++posted;
-    return true;
-  };
-  if (a.stall) return true;
-  if (b0 < b1) {
-    const CtaStart st = a.starts[me];
-    int kind = st.kind, idx = st.idx, sub = st.sub, off = st.off;
-    long long left = b1 - b0;
-    while (kind < 2 && ok) {
-      // the group's or sequence's items, from `sub` on
-      Item it = {};
-      int items, nb, kend, fb = 0, first = 0, n = 1, tile_seqs = 1, whole_to = kToPre;
-      if (kind == 0) {
-        const GroupInfo q = a.groups[idx];
-        items = q.tiles * a.num_kv;
-        nb = q.nb;
-        first = q.first;
-        n = q.n;
-        tile_seqs = q.tile_seqs;
-        kend = q.kend;
-        it.table = q.row;
-        it.prefix = 1;
-      } else {
-        const SeqInfo q = a.seqs[idx];
-        items = a.num_kv;
-        nb = q.nb;
-        fb = q.fb;
-        first = idx;
-        kend = q.len;
-        it.table = idx;
-        whole_to = q.fb == 0 ? kToOut : kToOwn;
-      }
-      const int32_t *table = a.block_tables + static_cast<int64_t>(it.table) * a.max_blocks + fb;
-      for (; sub < items && ok && left > 0; ++sub, off = 0) {
-        const int t0 = kind == 0 ? sub / a.num_kv * tile_seqs : 0;
-        it.kvh = kind == 0 ? sub % a.num_kv : sub;
-        it.seq0 = first + t0;
-        it.rows = min(tile_seqs, n - t0) * a.g;
-        // the part of the item's units in this CTA's range, and its blocks
-        const int size = item_units(nb);
-        const int take = static_cast<int>(min(static_cast<long long>(size - off), left));
-        const int lo = max(off - kItemUnits, 0);
-        it.nblk = max(off + take - kItemUnits, 0) - lo;
-        it.key0 = (fb + lo) * 16;
-        it.kend = min(kend, it.key0 + it.nblk * 16);  // a cut piece ends before the item
-        const bool whole = it.nblk == nb;
-        it.to = whole ? whole_to : kToCut;
-        // a cut item that begins inside this CTA's range is its last one
-        it.slot = me * 2 + (off == 0 && left < b1 - b0 ? 1 : 0);
-        left -= take;
-        if (it.nblk > 0)
-          ok = post(it) && copy_piece<C>(a, smem, bar, table + lo, it.nblk, it.kvh, fill, pol, lane);
-      }
-      if (!ok || left == 0) break;
-      // the next group with a prefix, after the last one the sequences with
-      // an own part; the ones without blocks are passed over 32 at a time
-      sub = 0;
-      ++idx;
-      auto next = [&](int count, auto blocks) {
-        while (idx < count) {
-          const unsigned some = __ballot_sync(0xffffffffu, idx + lane < count && blocks(idx + lane) > 0);
-          if (some) {
-            idx += __ffs(some) - 1;
-            return true;
-          }
-          idx += 32;
+  Item it = {};
+#pragma unroll 1
+  while (ok && !it.end) {
+    if (left <= 0 || st.kind == 2) {
+      it.end = 1;
+    } else {
+      if (kind < 0) {  // a group or sequence begins
+        kind = st.kind;
+        if (kind == 0) {
+          const GroupInfo &q = a.groups[st.idx];
+          items = q.tiles * a.num_kv;
+          nb = q.nb;
+          fb = 0;
+          first = q.first;
+          n = q.n;
+          tile_seqs = q.tile_seqs;
+          kend = q.kend;
+          row = q.row;
+          whole_to = kToPre;
+        } else {
+          const SeqInfo &q = a.seqs[st.idx];
+          items = a.num_kv;
+          nb = q.nb;
+          fb = q.fb;
+          first = row = st.idx;
+          n = tile_seqs = 1;
+          kend = q.len;
+          whole_to = q.fb == 0 ? kToOut : kToOwn;
         }
-        return false;
-      };
-      if (kind == 0 && !next(a.num_groups, [&](int j) { return a.groups[j].nb; })) {
-        kind = 1;
-        idx = 0;
+        table = a.block_tables + static_cast<int64_t>(row) * a.max_blocks + fb;
       }
-      if (kind == 1 && !next(a.num_seqs, [&](int s) { return a.seqs[s].nb; })) kind = 2;
+      const int tile = st.sub / a.num_kv;
+      it.kvh = st.sub - tile * a.num_kv;
+      it.seq0 = first + tile * tile_seqs;
+      it.rows = min(tile_seqs, n - tile * tile_seqs) * a.g;
+      it.prefix = kind == 0;
+      // the part of the item's units in this CTA's range, and its blocks
+      const int size = item_units(nb);
+      const int take = static_cast<int>(min(static_cast<long long>(size - st.off), left));
+      const int lo = max(st.off - kItemUnits, 0);
+      it.nblk = max(st.off + take - kItemUnits, 0) - lo;
+      it.key0 = (fb + lo) * 16;
+      it.kend = min(kend, it.key0 + it.nblk * 16);  // a cut piece ends before the item
+      it.lo = lo;
+      it.to = it.nblk == nb ? whole_to : kToCut;
+      // a cut item that begins inside this CTA's range is its last one
+      it.slot = me * 2 + (st.off == 0 && left < b1 - b0 ? 1 : 0);
+      left -= take;
+      st.off = 0;
+      ++st.sub;
     }
-  }
-  if (ok) {
-    Item it = {};
-    it.end = 1;
-    ok = post(it);
+    if (it.end || it.nblk > 0) {
+      const uint32_t at = posted % NIQ;
+      ok = wait(&bar.iq_empty[at], ((posted / NIQ) & 1) ^ 1, a.wait_ns);
+      if (!ok) break;
+      if (lane == 0) {
+        iq[at] = it;
+        mbar_arrive(&bar.iq_full[at]);
+      }
+      __syncwarp();
+      ++posted;
+      if (it.end) break;
+      ok = copy_piece<C>(a, smem, bar, table + it.lo, it.nblk, it.kvh, fill, pol, lane);
+    }
+    if (st.sub == items && left > 0) {
+      // the next group with a prefix, after the last one the sequences with
+      // an own part; the ones without work are passed over 32 at a time
+      st.sub = 0;
+      kind = -1;
+      ++st.idx;
+#pragma unroll 1
+      for (;;) {
+        const int count = st.kind == 0 ? a.num_groups : a.num_seqs, i = st.idx + lane;
+        const int work = i >= count ? 0 : st.kind == 0 ? a.groups[i].nb : a.seqs[i].nb;
+        const unsigned some = __ballot_sync(0xffffffffu, work > 0);
+        if (some) {
+          st.idx += __ffs(some) - 1;
+          break;
+        }
+        st.idx += 32;
+        if (st.idx < count) continue;
+        st.idx = 0;
+        if (++st.kind == 2) break;
+      }
+    }
   }
   if (!ok) drain_copies<C>(a, bar, fill);
   return ok;
@@ -601,7 +631,7 @@ template <class C>
 __device__ __forceinline__ bool take_item(const Args &a, Bars<C> &bar, const Item *iq, uint32_t &taken, Item &it,
                                           int lane) {
   const uint32_t st = taken % NIQ;
-  if (!mbar_wait(&bar.iq_full[st], (taken / NIQ) & 1, a.wait_ns)) return false;
+  if (!wait(&bar.iq_full[st], (taken / NIQ) & 1, a.wait_ns)) return false;
   it = iq[st];
   __syncwarp();
   if (lane == 0) mbar_arrive(&bar.iq_empty[st]);
@@ -618,13 +648,14 @@ __device__ bool load_q(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *i
   uint32_t taken = 0;
   QSlots qs;
   Item it;
+#pragma unroll 1
   for (;;) {
     if (!take_item<C>(a, bar, iq, taken, it, lane)) return false;
     if (it.end) return true;
     qs.next(it.rows);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (qs.uses_slot(i) && !mbar_wait(&bar.q_empty[i], qs.parity(i) ^ 1, a.wait_ns)) return false;
+      if (qs.uses_slot(i) && !wait(&bar.q_empty[i], qs.parity(i) ^ 1, a.wait_ns)) return false;
     uint8_t *base = smem + C::OFF_Q + qs.slot * (C::QB / 2);
     const int half = qs.big ? C::QHALF : C::QHALF / 2;
     float big = 0.f;
@@ -635,8 +666,9 @@ __device__ bool load_q(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *i
     const uint16_t *src0 = a.q + (static_cast<int64_t>(it.seq0) * a.num_q + it.kvh * a.g) * C::D + ch * 8;
     uint8_t *dst0 = base + (ch >> 3) * half;
     const int64_t seq_stride = static_cast<int64_t>(a.num_q) * C::D;
+#pragma unroll 1
     while (R < it.rows) {
-      constexpr int ILP = 8;
+      constexpr int ILP = 4;
       uint4 x[ILP];
       int at[ILP];
 #pragma unroll
@@ -649,6 +681,7 @@ __device__ bool load_q(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *i
           if (at[k] >= 0) cp_async16(dst0 + at[k], src, true);
         }
         R += RPI;
+#pragma unroll 1
         for (hd += RPI; hd >= a.g; hd -= a.g) ++sq;
       }
       if constexpr (C::KV8) {
@@ -695,17 +728,19 @@ __device__ bool widen(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq
   const int x0 = ((2 * (c & 3)) ^ r7) << 4, x1 = ((2 * (c & 3) + 1) ^ r7) << 4;
   uint32_t taken = 0, step = 0;
   Item it;
+#pragma unroll 1
   for (;;) {
     if (!take_item<C>(a, bar, iq, taken, it, lane)) return false;
     if (it.end) return true;
+#pragma unroll 1
     for (int b = 0; b < it.nblk; b += BPT, ++step) {
       const int rows = min(BPT, it.nblk - b) * 16;
       const int keep = it.kend - (it.key0 + b * 16);  // rows of the piece's keys
       const uint32_t ls = step % C::NL, lp = (step / C::NL) & 1, ts = step % C::NT, tp = ((step / C::NT) & 1) ^ 1;
 #pragma unroll 1
       for (int v = 0; v < 2; ++v) {
-        if (!mbar_wait(v ? &bar.lv_full[ls] : &bar.lk_full[ls], lp, a.wait_ns)) return false;
-        if (!mbar_wait(v ? &bar.v_empty[ts] : &bar.k_empty[ts], tp, a.wait_ns)) return false;
+        if (!wait(v ? &bar.lv_full[ls] : &bar.lk_full[ls], lp, a.wait_ns)) return false;
+        if (!wait(v ? &bar.v_empty[ts] : &bar.k_empty[ts], tp, a.wait_ns)) return false;
         const uint8_t *src = smem + (v ? C::OFF_LV : C::OFF_LK) + ls * C::LB + ct * 16;
         uint8_t *dst = smem + (v ? C::OFF_V : C::OFF_K) + ts * C::TB + put;
         const int zero = v ? keep : KT;  // rows from here on become zero
@@ -742,8 +777,38 @@ __device__ bool widen(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq
   }
 }
 
-// One product of 8 or 16 K-steps is issued from descriptors that differ by
-// constants, so that the one issuing thread keeps the tensor pipe fed.
+// Score scale of a kv head, log2 units.
+__device__ __forceinline__ float score_scale(const Args &a, int kvh) {
+  return a.k_scales ? a.qscale0 * __ldg(a.k_scales + kvh) : a.qscale;
+}
+
+// The products, from descriptors split in halves: along a tile only the low
+// word changes (the start address), by constants, so that the one issuing
+// thread takes few instructions per product and the tensor pipe stays fed.
+constexpr uint32_t desc_high(uint32_t sbo) {  // stride, version, 128-byte swizzle
+  return ((sbo >> 4) & 0x3FFFu) | (1u << 14) | (2u << 29);
+}
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t lbo) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) & 0x3FFFu) << 16;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                       uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                       bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "mov.b64 db, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
 
 // Warp 0, one thread: the scores, S[k % 2] = Q K^T of step k, once the step's
 // K has landed and P V of step k - 2 has read the P that lay there.
@@ -753,31 +818,35 @@ __device__ bool issue_qk(const Args &a, uint32_t sbase, uint32_t tmem, Bars<C> &
   uint64_t *k_full = C::KV8 ? bar.k_full : bar.lk_full, *k_empty = C::KV8 ? bar.k_empty : bar.lk_empty;
   uint32_t taken = 0, k = 0;
   QSlots qs;
+#pragma unroll 1
   for (;;) {
     const uint32_t st = taken % NIQ;
-    if (!mbar_wait(&bar.iq_full[st], (taken / NIQ) & 1, a.wait_ns)) return false;
-    const int end = iq[st].end, rows = iq[st].rows, nblk = iq[st].nblk;
+    if (!wait(&bar.iq_full[st], (taken / NIQ) & 1, a.wait_ns)) return false;
+    const int end = iq[st].end, rows = iq[st].rows, nblk = iq[st].nblk, kvh = iq[st].kvh;
     mbar_arrive(&bar.iq_empty[st]);
     ++taken;
     if (end) return true;
     qs.next(rows);
+    // the softmax takes maxima of the scores as they come, so a negative
+    // scale's sign goes into the product (bit 13 negates A)
+    const uint32_t idesc = C::IDESC_QK | (score_scale(a, kvh) < 0.f ? 1u << 13 : 0u);
     const uint32_t qhalf = qs.big ? C::QHALF : C::QHALF / 2;
     // row 0 of the slot is lane first_lane of the product
-    const uint64_t qd =
-        umma_desc_sw128(sbase + C::OFF_Q + qs.slot * (C::QB / 2) - first_lane(rows, taken - 1) * 128, 16, 1024);
+    const uint32_t qd = desc_low(sbase + C::OFF_Q + qs.slot * (C::QB / 2) - first_lane(rows, taken - 1) * 128, 16);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (qs.uses_slot(i) && !mbar_wait(&bar.q_full[i], qs.parity(i), a.wait_ns)) return false;
+      if (qs.uses_slot(i) && !wait(&bar.q_full[i], qs.parity(i), a.wait_ns)) return false;
+#pragma unroll 1
     for (int b = 0; b < nblk; b += BPT, ++k) {
-      if (!mbar_wait(&bar.p_empty[k & 1], ((k >> 1) & 1) ^ 1, a.wait_ns)) return false;
-      if (!mbar_wait(&k_full[k % C::NT], (k / C::NT) & 1, a.wait_ns)) return false;
+      if (!wait(&bar.p_empty[k & 1], ((k >> 1) & 1) ^ 1, a.wait_ns)) return false;
+      if (!wait(&k_full[k % C::NT], (k / C::NT) & 1, a.wait_ns)) return false;
       tc_fence_after_sync();
-      const uint64_t kd = umma_desc_sw128(sbase + C::OFF_K + (k % C::NT) * C::TB, 16, C::GB);
+      const uint32_t kd = desc_low(sbase + C::OFF_K + (k % C::NT) * C::TB, 16);
       const uint32_t s = tmem + C::S_COL + (k & 1) * KT;
 #pragma unroll
       for (int kk = 0; kk < C::D / 16; ++kk)
-        umma_bf16_ss(s, qd + (((kk >> 2) * qhalf + (kk & 3) * 32) >> 4), kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
-                     C::IDESC_QK, kk > 0 ? 1u : 0u);
+        mma_ss(s, qd + (kk & 3) * 2 + (kk >> 2) * (qhalf >> 4), desc_high(1024),
+               kd + ((kk >> 2) * 1024 + (kk & 3) * 32) / 16, desc_high(C::GB), idesc, kk > 0);
       umma_commit(is_narrow(rows) ? &bar.sn_full[(taken - 1) & 3][k & 1] : &bar.sw_full[k & 1]);
       umma_commit(&k_empty[k % C::NT]);
     }
@@ -798,9 +867,10 @@ __device__ bool issue_pv(const Args &a, uint32_t sbase, uint32_t tmem, Bars<C> &
   // bit 2 * narrow + buffer is the parity of its next phase
   uint32_t p_par = 0, o_par = 0;
   uint32_t used = 0, was = 0;  // bit = buffer: it has held an item; that was a narrow one
+#pragma unroll 1
   for (;;) {
     const uint32_t st = taken % NIQ;
-    if (!mbar_wait(&bar.iq_full[st], (taken / NIQ) & 1, a.wait_ns)) return false;
+    if (!wait(&bar.iq_full[st], (taken / NIQ) & 1, a.wait_ns)) return false;
     const int end = iq[st].end, nblk = iq[st].nblk, nar = is_narrow(iq[st].rows);
     mbar_arrive(&bar.iq_empty[st]);
     const uint32_t item = taken++;
@@ -810,31 +880,29 @@ __device__ bool issue_pv(const Args &a, uint32_t sbase, uint32_t tmem, Bars<C> &
     // the item's first product overwrites the output of the item two before
     if ((used >> ob) & 1) {
       const int kind = (was >> ob) & 1, i = 2 * kind + ob;
-      if (!mbar_wait(&bar.o_empty[kind][ob], (o_par >> i) & 1, a.wait_ns)) return false;
+      if (!wait(&bar.o_empty[kind][ob], (o_par >> i) & 1, a.wait_ns)) return false;
       o_par ^= 1u << i;
     }
     used |= 1u << ob;
     was = (was & ~(1u << ob)) | (static_cast<uint32_t>(nar) << ob);
+#pragma unroll 1
     for (int b = 0; b < nblk; b += BPT, ++k) {
-      if (!mbar_wait(&v_full[k % C::NT], (k / C::NT) & 1, a.wait_ns)) return false;
+      if (!wait(&v_full[k % C::NT], (k / C::NT) & 1, a.wait_ns)) return false;
       const int i = 2 * nar + (k & 1);
-      if (!mbar_wait_hint(&bar.p_full[nar][k & 1], (p_par >> i) & 1, a.wait_ns)) return false;
+      if (!wait(&bar.p_full[nar][k & 1], (p_par >> i) & 1, a.wait_ns)) return false;
       p_par ^= 1u << i;
       tc_fence_after_sync();
-      const uint64_t vd = umma_desc_sw128(sbase + C::OFF_V + (k % C::NT) * C::TB, 1024, C::GB);
+      const uint32_t vd = desc_low(sbase + C::OFF_V + (k % C::NT) * C::TB, 1024);
       const uint32_t p = tmem + C::S_COL + (k & 1) * KT;
       // keys 16 kk .. 16 kk + 15: hi at +0, lo at +16 of their 32-column chunk
-      auto block = [&](int kk) {
-        const uint64_t bd = vd + kk * (2 * C::GB >> 4);
-        const uint32_t ap = p + (kk >> 1) * 32 + (kk & 1) * 8;
-        umma_bf16_ts(o, ap, bd, C::IDESC_PV, (kk > 0 || b > 0) ? 1u : 0u);
-        umma_bf16_ts(o, ap + 16, bd, C::IDESC_PV, 1u);
-      };
-      if (nblk - b >= BPT) {
+      // (unrolled: rolled, the issue bounds a long prefix)
+      const int n = nblk - b;
 #pragma unroll
-        for (int kk = 0; kk < BPT; ++kk) block(kk);
-      } else {
-        for (int kk = 0; kk < nblk - b; ++kk) block(kk);
+      for (int kk = 0; kk < BPT; ++kk) {
+        if (kk >= n) break;
+        const uint32_t bd = vd + kk * (2 * C::GB / 16), ap = p + (kk >> 1) * 32 + (kk & 1) * 8;
+        mma_ts(o, ap, bd, desc_high(C::GB), C::IDESC_PV, kk > 0 || b > 0);
+        mma_ts(o, ap + 16, bd, desc_high(C::GB), C::IDESC_PV, true);
       }
       umma_commit(&v_empty[k % C::NT]);
       umma_commit(&bar.p_empty[k & 1]);
@@ -897,74 +965,51 @@ struct Softmax {
       lsum += xch[(h ^ 1) * MAXROWS + row];
     }
     if (is_narrow(it.rows)) {
-      ok = mbar_wait(&bar.on_full[warp & 3], on, a.wait_ns) && ok;
+      ok = wait(&bar.on_full[warp & 3], on, a.wait_ns) && ok;
       on ^= 1;
     } else {
-      ok = mbar_wait(&bar.ow_full[ob], (ow >> ob) & 1, a.wait_ns) && ok;
+      ok = wait(&bar.ow_full[ob], (ow >> ob) & 1, a.wait_ns) && ok;
       ow ^= 1u << ob;
     }
     if (mine && ok) {
       tc_fence_after_sync();
+      // outputs and own parts are rows; prefix parts and pieces are
+      // [4 columns][row of the tile], so that a wide tile's lanes write
+      // consecutive 16 bytes
       const int sq = live ? r / a.g : 0;
       const int64_t orow = static_cast<int64_t>(it.seq0 + sq) * a.num_q + it.kvh * a.g + (r - sq * a.g);
-      const int64_t srow = static_cast<int64_t>(it.slot) * a.slot_rows + r;
-      float *dst = it.to == kToCut ? a.cut_o + srow * D
-                                   : (it.to == kToOut ? a.out : it.to == kToPre ? a.pre_o : a.own_o) + orow * D;
+      float *o_dst = (it.to == kToOut ? a.out : a.own_o) + orow * D;
+      float *l_dst = it.to == kToOut ? (a.lse ? a.lse + orow : nullptr) : a.own_lse + orow;
+      int64_t stride = 4;
+      if (it.to == kToCut) {
+        o_dst = a.cut_o + static_cast<int64_t>(it.slot) * a.slot_rows * D + 4 * r;
+        l_dst = a.cut_lse + static_cast<int64_t>(it.slot) * a.slot_rows + r;
+        stride = 4 * a.slot_rows;
+      } else if (it.to == kToPre) {
+        const int64_t at = static_cast<int64_t>(it.seq0) * a.num_q + static_cast<int64_t>(it.kvh) * it.rows;
+        o_dst = a.pre_o + at * D + 4 * r;
+        l_dst = a.pre_lse + at + r;
+        stride = 4 * it.rows;
+      }
       // no key (a sequence shorter than the piece's first one): nothing to weigh
       const bool none = lsum == 0.f;
       float inv = none ? 0.f : 1.f / lsum;
       if (it.to == kToOut) inv *= a.v_scales ? __ldg(a.v_scales + it.kvh) : a.vscale;
-      if (live && h == 0) {
+      if (live && h == 0 && l_dst) {
         const float ls = none ? -INFINITY : m + log2f(lsum) - C::PB;
-        if (it.to == kToCut)
-          a.cut_lse[srow] = ls;
-        else if (it.to != kToOut)
-          (it.to == kToPre ? a.pre_lse : a.own_lse)[orow] = ls;
-        else if (a.lse)
-          a.lse[orow] = ls * kLn2;
-      }
-      // rows of a quad of lanes change places with its column chunks, so that
-      // a store writes 64 consecutive bytes of each of eight rows
-      const int q = lane & 3;
-      float *qdst[4];
-      bool qlive[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int src = (lane & ~3) | j;
-        qdst[j] = reinterpret_cast<float *>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), src));
-        qlive[j] = __shfl_sync(0xffffffffu, static_cast<int>(live), src) != 0;
+        *l_dst = it.to == kToOut ? ls * kLn2 : ls;
       }
 #pragma unroll 1
       for (int c0 = h * (D / 2); c0 < (h + 1) * (D / 2); c0 += 16) {
         float o[16];
         tmem_ld16(trow + C::O_COL + ob * D + c0, o);
+        if (live) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = none ? 0.f : o[i] * inv;
-        // 4 x 4 transpose of float4s over the quad, in two exchanges
-#pragma unroll
-        for (int bit = 1; bit < 4; bit <<= 1) {
-          const bool up = (q & bit) != 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (j & bit) continue;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float give = up ? o[4 * j + e] : o[4 * (j | bit) + e];
-              const float got = __shfl_xor_sync(0xffffffffu, give, bit);
-              if (up)
-                o[4 * j + e] = got;
-              else
-                o[4 * (j | bit) + e] = got;
-            }
-          }
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<float4 *>(o_dst + (c0 + i) / 4 * stride) =
+                none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                     : make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
         }
-        // o[4 j ..] is now column chunk q of the quad's row j
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (qlive[j])
-            *reinterpret_cast<float4 *>(qdst[j] + c0 + 4 * q) =
-                make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
       }
     }
     tc_fence_before_sync();
@@ -975,6 +1020,7 @@ struct Softmax {
   __device__ bool run(const Item *iq) {
     uint64_t *v_full = C::KV8 ? bar.v_full : bar.lv_full, *v_empty = C::KV8 ? bar.v_empty : bar.lv_empty;
     uint32_t taken = 0, k = 0;
+#pragma unroll 1
     for (;;) {
       Item it;
       const bool got = take_item<C>(a, bar, iq, taken, it, lane);
@@ -994,31 +1040,30 @@ struct Softmax {
       // comes: nothing reads theirs)
       int lim = 0x7fffffff;
       if (live) lim = it.prefix ? min(it.kend, a.seqs[it.seq0 + r / a.g].len) : it.kend;
-      float qsc = a.k_scales ? a.qscale0 * __ldg(a.k_scales + it.kvh) : a.qscale;
-      // the maximum is taken of the scores as they are, so a scale that is not
-      // positive goes into them first (and masked scores never meet a 0)
-      const float sgn = qsc < 0.f ? -1.f : 0.f;
-      const bool turn = !(qsc > 0.f);
-      if (turn) qsc = qsc < 0.f ? -qsc : 1.f;
+      // (a negative scale's sign is in the scores; a zero one must not meet
+      // the -inf of a masked score as a zero)
+      const float qsc = fmaxf(fabsf(score_scale(a, it.kvh)), 1e-37f);
       float m = -INFINITY, l = 0.f;
+#pragma unroll 1
       for (int b = 0; b < it.nblk; b += BPT, ++k) {
         const int n = min(BPT, it.nblk - b);
         const int key0 = it.key0 + b * 16;
         bool there;
         if (nar) {
-          there = mbar_wait_hint(&bar.sn_full[warp & 3][k & 1], (sn >> (k & 1)) & 1, a.wait_ns);
+          there = wait(&bar.sn_full[warp & 3][k & 1], (sn >> (k & 1)) & 1, a.wait_ns);
           sn ^= 1u << (k & 1);
         } else {
-          there = mbar_wait_hint(&bar.sw_full[k & 1], (sw >> (k & 1)) & 1, a.wait_ns);
+          there = wait(&bar.sw_full[k & 1], (sw >> (k & 1)) & 1, a.wait_ns);
           sw ^= 1u << (k & 1);
         }
         tc_fence_after_sync();
         if (!C::KV8 && it.kend < key0 + n * 16) {
           // V rows past the item's keys may hold anything (0 * NaN is NaN)
-          there = there && mbar_wait(&v_full[k % C::NT], (k / C::NT) & 1, a.wait_ns);
+          there = there && wait(&v_full[k % C::NT], (k / C::NT) & 1, a.wait_ns);
           const int keep = it.kend - key0;
           const int threads = nar ? 64 : 256, me = nar ? h * 32 + lane : static_cast<int>(threadIdx.x) - 128;
           uint8_t *v = smem + C::OFF_V + (k % C::NT) * C::TB;
+#pragma unroll 1
           for (int i = me; there && i < (n * 16 - keep) * C::HALVES * 8; i += threads) {
             const int rr = keep + i / (C::HALVES * 8), c = i % (C::HALVES * 8);
             *reinterpret_cast<uint4 *>(v + (rr >> 3) * C::GB + (c >> 3) * 1024 + (rr & 7) * 128 + (c & 7) * 16) =
@@ -1027,7 +1072,7 @@ struct Softmax {
           fence_proxy_async_smem();
         }
         if (!named_bar_and(pair, 64, there && ok)) return false;
-        if (mine) step(k, key0, b > 0, lim, live, qsc, turn, sgn, num, v_empty, m, l);
+        if (mine) step(k, key0, b > 0, lim, live, qsc, num, v_empty, m, l);
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.p_full[nar][k & 1]);
@@ -1037,19 +1082,14 @@ struct Softmax {
   }
 
   // One step's scores (in tensor memory) to P over them; m and l follow.
-  __device__ __forceinline__ void step(uint32_t k, int key0, bool later, int lim, bool live, float qsc, bool turn,
-                                       float sgn, uint32_t num, uint64_t *v_empty, float &m, float &l) {
+  __device__ __forceinline__ void step(uint32_t k, int key0, bool later, int lim, bool live, float qsc,
+                                       uint32_t num, uint64_t *v_empty, float &m, float &l) {
     const uint32_t scol = trow + C::S_COL + (k & 1) * KT + 64 * h;
     const int kh = key0 + 64 * h;
-    // 32 scores as the softmax takes them: a scale that is not positive
-    // applied, keys past the row's limit out
+    // 32 scores, keys past the row's limit out
     auto load = [&](int c, uint32_t(&x)[32]) {
       tmem_ld32_async(scol + 32 * c, x);
       tmem_wait_ld(x);
-      if (turn) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * sgn);
-      }
       if (kh + 32 * c + 32 > lim) {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
@@ -1079,7 +1119,7 @@ struct Softmax {
     if (__any_sync(0xffffffffu, raise && m != -INFINITY)) {
       // rare: this half of O's columns takes the new maximum; the product of
       // the step before, which releases its V tile, is through
-      if (later) ok = mbar_wait(&v_empty[(k - 1) % C::NT], ((k - 1) / C::NT) & 1, a.wait_ns) && ok;
+      if (later) ok = wait(&v_empty[(k - 1) % C::NT], ((k - 1) / C::NT) & 1, a.wait_ns) && ok;
       tc_fence_after_sync();
       const float f = (raise && m != -INFINITY) ? exp2f(m - mx) : 1.f;
       l *= f;
@@ -1154,6 +1194,7 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
       mbar_init(&bar.q_empty[i], 1);
       mbar_init(&bar.sw_full[i], 1);
       mbar_init(&bar.ow_full[i], 1);
+#pragma unroll 1
       for (int nar = 0; nar < 2; ++nar) {
         mbar_init(&bar.p_full[nar][i], nar ? 2 : 8);
         mbar_init(&bar.o_empty[nar][i], nar ? 2 : 8);
@@ -1206,7 +1247,7 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
   // every product issued completes before the tensor memory is given back
   if ((warp == 0 || warp == 2) && lane == 0) {
     umma_commit(&bar.drain[warp >> 1]);
-    mbar_wait(&bar.drain[warp >> 1], 0, a.wait_ns);
+    wait(&bar.drain[warp >> 1], 0, a.wait_ns);
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -1221,104 +1262,129 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
 // u / n for the axis (32-bit where it fits)
 __device__ __forceinline__ int axis_cta(long long u, const Axis &x) {
   if (x.units < 0x7fffffffLL) return static_cast<int>(static_cast<unsigned>(u) / static_cast<unsigned>(x.per));
-  return static_cast<int>(u / x.per);
+  return static_cast<int>(divide(u, x.per));
 }
 
-// One warp per (sequence, head): the parts' pieces by log-sum-exp weights.
-// Rows that the attention wrote itself (one uncut part) are left alone.
+// Two rows (sequence, head) per warp, a row on the lanes of one parity, 16
+// bytes of it a lane: two neighbouring rows of a tile fill a 32-byte sector of
+// its [4 columns][row] parts.  Each row's pieces are weighed by their
+// log-sum-exps.  Rows that the attention wrote itself (one uncut part) are
+// left alone.
 template <int D>
 __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant__ Args a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
-  if (row >= static_cast<int64_t>(a.num_seqs) * a.num_q) return;
   const int lane = threadIdx.x & 31;
-  const int s = static_cast<int>(row / a.num_q), h = static_cast<int>(row - static_cast<int64_t>(s) * a.num_q);
-  const int kvh = h / a.g;
+  const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_q;
+  int64_t row = (static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5)) * 2 + (lane & 1);
+  // every lane stays for the shuffles
+  bool mine = row < rows;
+  if (!mine) row = rows - 1;
+  const int c0 = lane >> 1;  // this lane's columns: 4 (c0 + 16 j)
+  constexpr int NJ = D / 64;
+  const int s = static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(a.num_q));
+  const int h = static_cast<int>(row - static_cast<int64_t>(s) * a.num_q), kvh = h / a.g, hg = h - kvh * a.g;
   const SeqInfo q = a.seqs[s];
   const Axis ax = *a.axis;
-  constexpr int EPL = D / 32;  // elements of a lane
-  using V = typename std::conditional<EPL == 4, float4, float2>::type;
-  V *out = reinterpret_cast<V *>(a.out + row * D) + lane;
   // the pieces of the prefix part and of the own part: piece i of a part is
   // CTA c1 + i's slot (1 where the item begins inside that CTA's range), or
   // the part's own place if one CTA holds all its blocks
-  int p_c1 = 0, p_n = 0, p_s0 = 0, p_r = 0, o_c1 = 0, o_n = 0, o_s0 = 0;
-  bool p_whole = false, o_whole = false;
-  auto pieces = [&](long long u0, int nb, int &c1, int &np, int &s0, bool &whole) {
+  auto pieces = [&](long long u0, int nb, int &c1, int &np, int &s0) {
     c1 = axis_cta(u0, ax);
     if ((c1 + 1) * ax.per - u0 <= kItemUnits) ++c1;  // that CTA's range holds none of its blocks
     np = axis_cta(u0 + item_units(nb) - 1, ax) - c1 + 1;
-    whole = np == 1;
     s0 = u0 > c1 * ax.per;
   };
+  int p_c1 = 0, p_n = 0, p_s0 = 0, p_r = 0, p_rows = 1, o_c1 = 0, o_n = 0, o_s0 = 0;
+  int64_t p_at = 0;  // the prefix part's tile in pre_o / pre_lse
   if (q.fb > 0 && q.len > 0) {
     const GroupInfo gi = a.groups[q.group];
-    const int i = s - gi.first, tile = i / gi.tile_seqs;
-    pieces(gi.base + static_cast<long long>(tile * a.num_kv + kvh) * item_units(gi.nb), gi.nb, p_c1, p_n, p_s0, p_whole);
-    p_r = (i - tile * gi.tile_seqs) * a.g + h % a.g;
+    const int i = s - gi.first, tile = i / gi.tile_seqs, t0 = tile * gi.tile_seqs;
+    pieces(gi.base + static_cast<long long>(tile * a.num_kv + kvh) * item_units(gi.nb), gi.nb, p_c1, p_n, p_s0);
+    p_r = (i - t0) * a.g + hg;
+    p_rows = min(gi.tile_seqs, gi.n - t0) * a.g;
+    p_at = static_cast<int64_t>(gi.first + t0) * a.num_q + static_cast<int64_t>(kvh) * p_rows;
   }
-  if (q.nb > 0) pieces(q.base + static_cast<long long>(kvh) * item_units(q.nb), q.nb, o_c1, o_n, o_s0, o_whole);
-  if (q.fb == 0 && o_whole) return;
-  const int n = p_n + o_n;
-  // piece i's output row and log-sum-exp
-  auto piece = [&](int i, const float *&o, const float *&x) {
+  if (q.nb > 0) pieces(q.base + static_cast<long long>(kvh) * item_units(q.nb), q.nb, o_c1, o_n, o_s0);
+  if (q.fb == 0 && o_n == 1) mine = false;
+  const int n = mine ? p_n + o_n : 0;
+  // where piece i's log-sum-exp and columns 0 .. 3 are, and the distance to the next columns
+  auto piece = [&](int i, const float *&x, const float *&o) -> int {
     const bool pre = i < p_n;
-    if (pre ? p_whole : o_whole) {
-      o = (pre ? a.pre_o : a.own_o) + row * D;
-      x = (pre ? a.pre_lse : a.own_lse) + row;
-      return;
+    if (pre && p_n == 1) {
+      x = a.pre_lse + p_at + p_r;
+      o = a.pre_o + p_at * D + 4 * p_r;
+      return 4 * p_rows;
+    }
+    if (!pre && o_n == 1) {
+      x = a.own_lse + row;
+      o = a.own_o + row * D;
+      return 4;
     }
     const int k = pre ? i : i - p_n;
-    const int64_t slot = static_cast<int64_t>((pre ? p_c1 : o_c1) + k) * 2 + (k == 0 ? (pre ? p_s0 : o_s0) : 0);
-    const int64_t at = slot * a.slot_rows + (pre ? p_r : h % a.g);
-    o = a.cut_o + at * D;
-    x = a.cut_lse + at;
+    const int64_t slot =
+        (static_cast<int64_t>((pre ? p_c1 : o_c1) + k) * 2 + (k == 0 ? (pre ? p_s0 : o_s0) : 0)) * a.slot_rows;
+    const int r = pre ? p_r : hg;
+    x = a.cut_lse + slot + r;
+    o = a.cut_o + slot * D + 4 * r;
+    return 4 * a.slot_rows;
   };
-  float M = -INFINITY, W = 0.f, acc[EPL];
+  // 16 pieces at a time, each fetched by one of the row's lanes: their
+  // log-sum-exps first, then their columns by all the lanes
+  float M = -INFINITY, W = 0.f;
+  float4 acc[NJ];
 #pragma unroll
-  for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    // 32 pieces' log-sum-exps at once, a lane each
-    const float *po = a.out, *px = nullptr;
-    float x = -INFINITY;
-    if (i0 + lane < n) {
-      piece(i0 + lane, po, px);
-      x = __ldcg(px);
+  for (int j = 0; j < NJ; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int most = max(n, __shfl_xor_sync(0xffffffffu, n, 1));
+#pragma unroll 1
+  for (int i0 = 0; i0 < most; i0 += 16) {
+    const float *x = nullptr, *o = a.pre_o;
+    int stride = 0;
+    float v = -INFINITY;
+    if (i0 + c0 < n) {
+      stride = piece(i0 + c0, x, o);
+      v = __ldcg(x);
     }
-    float mn = fmaxf(M, x);
+    float mn = fmaxf(M, v);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-    const float f = M == mn ? 1.f : exp2f(M - mn);  // 0 for the first pieces
-    const float w = x == -INFINITY ? 0.f : exp2f(x - mn);  // a NaN stays one
+    for (int b = 2; b < 32; b <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, b));
+    const float f = M == mn ? 1.f : exp2f(M - mn);
+    const float w = v == -INFINITY ? 0.f : exp2f(v - mn);  // a NaN stays one
+    M = mn;
     float ws = w;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
+    for (int b = 2; b < 32; b <<= 1) ws += __shfl_xor_sync(0xffffffffu, ws, b);
     W = W * f + ws;
-    M = mn;
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) acc[e] *= f;
-    const int m = min(32, n - i0);
+    for (int j = 0; j < NJ; ++j) acc[j] = make_float4(acc[j].x * f, acc[j].y * f, acc[j].z * f, acc[j].w * f);
+    const int m = min(16, most - i0);
 #pragma unroll 4
     for (int i = 0; i < m; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const int from = 2 * i + (lane & 1);
+      const float wi = __shfl_sync(0xffffffffu, w, from);
       const float *oi = reinterpret_cast<const float *>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(po), i));
-      const V v = __ldcg(reinterpret_cast<const V *>(oi) + lane);
-      const float *vf = reinterpret_cast<const float *>(&v);
-      if (wi != 0.f) {
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), from));
+      const int64_t st = __shfl_sync(0xffffffffu, stride, from);
+      // (past a row's pieces: the workspace's first element, with no weight)
 #pragma unroll
-        for (int e = 0; e < EPL; ++e) acc[e] += wi * vf[e];
+      for (int j = 0; j < NJ; ++j) {
+        const float4 y = __ldcg(reinterpret_cast<const float4 *>(oi + (c0 + 16 * j) * st));
+        if (wi != 0.f) {
+          acc[j].x += wi * y.x;
+          acc[j].y += wi * y.y;
+          acc[j].z += wi * y.z;
+          acc[j].w += wi * y.w;
+        }
       }
     }
   }
+  if (!mine) return;
   const float inv = W == 0.f ? 0.f : (a.v_scales ? __ldg(a.v_scales + kvh) : a.vscale) / W;
-  V r;
-  float *rf = reinterpret_cast<float *>(&r);
 #pragma unroll
-  for (int e = 0; e < EPL; ++e) rf[e] = acc[e] * inv;
-  *out = r;
-  if (a.lse && lane == 0) a.lse[row] = W == 0.f ? -INFINITY : (M + log2f(W)) * kLn2;
+  for (int j = 0; j < NJ; ++j)
+    *reinterpret_cast<float4 *>(a.out + row * D + 4 * (c0 + 16 * j)) =
+        make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv);
+  if (a.lse && c0 == 0) a.lse[row] = W == 0.f ? -INFINITY : (M + log2f(W)) * kLn2;
 }
 
 // The attention kernel for a descriptor (pa_shared_16.cu, pa_shared_8.cu).
