@@ -327,20 +327,22 @@ struct __align__(16) Item {
 
 constexpr int NIQ = 4;  // items in flight between the roles
 
-// Waits until the phase of `bar` with the given parity has completed; false
-// if that does not happen within limit_ns (at most 2^31).  Short on purpose:
-// it is in the kernel some forty times, and the roles share the SM's
-// instruction caches.
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, uint32_t limit_ns) {
-  const uint32_t addr = smem_u32(bar);
-  uint32_t t0 = 0, t1 = 0;
-#pragma unroll 1
-  for (bool first = true; !mbar_test(addr, parity); first = false) {
+// Waits, with a whole warp, until the phase of `bar` with the given parity has
+// completed; false (for all its lanes) if that does not happen within
+// limit_ns (at most 2^31).  Its loop is not inlined: it is waited some forty
+// times in the kernel, and the roles share the SM's instruction caches.
+static __device__ __noinline__ bool wait_on(uint32_t addr, uint32_t parity, uint32_t limit_ns) {
+  uint32_t t0, t1;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t0));
+  while (!__all_sync(0xffffffffu, mbar_test(addr, parity))) {
     asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t1));
-    if (first) t0 = t1;
-    if (t1 - t0 > limit_ns) return false;
+    if (__any_sync(0xffffffffu, t1 - t0 > limit_ns)) return false;
   }
   return true;
+}
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, uint32_t limit_ns) {
+  const uint32_t addr = smem_u32(bar);
+  return __all_sync(0xffffffffu, mbar_test(addr, parity)) || wait_on(addr, parity, limit_ns);
 }
 
 template <int D_, int KVT_>
@@ -658,52 +660,38 @@ __device__ bool load_q(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *i
       if (qs.uses_slot(i) && !wait(&bar.q_empty[i], qs.parity(i) ^ 1, a.wait_ns)) return false;
     uint8_t *base = smem + C::OFF_Q + qs.slot * (C::QB / 2);
     const int half = qs.big ? C::QHALF : C::QHALF / 2;
-    float big = 0.f;
-    // a lane keeps its 16-byte column chunk; its rows are RPI apart
-    constexpr int RPI = 32 / CH;
-    const int ch = lane % CH;
-    int R = lane / CH, sq = R / a.g, hd = R - sq * a.g;
-    const uint16_t *src0 = a.q + (static_cast<int64_t>(it.seq0) * a.num_q + it.kvh * a.g) * C::D + ch * 8;
-    uint8_t *dst0 = base + (ch >> 3) * half;
-    const int64_t seq_stride = static_cast<int64_t>(a.num_q) * C::D;
+    // a sequence's g rows lie together: g x CH chunks of 16 bytes
+    const int chunks = a.g * CH;
+    const uint16_t *src = a.q + (static_cast<int64_t>(it.seq0) * a.num_q + it.kvh * a.g) * C::D;
+    auto place = [&](int R, int ch) {
+      return reinterpret_cast<uint4 *>(base + (ch >> 3) * half + R * 128 + (((ch & 7) ^ (R & 7)) << 4));
+    };
 #pragma unroll 1
-    while (R < it.rows) {
-      constexpr int ILP = 4;
-      uint4 x[ILP];
-      int at[ILP];
-#pragma unroll
-      for (int k = 0; k < ILP; ++k) {
-        const uint16_t *src = src0 + sq * seq_stride + hd * C::D;
-        at[k] = R < it.rows ? R * 128 + (((ch & 7) ^ (R & 7)) << 4) : -1;
-        if constexpr (C::KV8) {
-          if (at[k] >= 0) x[k] = __ldg(reinterpret_cast<const uint4 *>(src));
-        } else {
-          if (at[k] >= 0) cp_async16(dst0 + at[k], src, true);
-        }
-        R += RPI;
+    for (int R0 = 0; R0 < it.rows; R0 += a.g, src += static_cast<int64_t>(a.num_q) * C::D)
 #pragma unroll 1
-        for (hd += RPI; hd >= a.g; hd -= a.g) ++sq;
-      }
-      if constexpr (C::KV8) {
-#pragma unroll
-        for (int k = 0; k < ILP; ++k) {
-          if (at[k] < 0) continue;
-          const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-          uint32_t o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float f0 = bf16lo(w[e]), f1 = bf16hi(w[e]);
-            const float f = fmaxf(fabsf(f0), fabsf(f1));
-            if (f <= FLT_MAX) big = fmaxf(big, f);
-            o[e] = pack_f16x2(f0, f1);
-          }
-          *reinterpret_cast<uint4 *>(dst0 + at[k]) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-      }
-    }
-    if (C::KV8 && big >= 65520.f) report_error(a.err, nullptr, kErrFp16Range);
+      for (int j = lane; j < chunks; j += 32) cp_async16(place(R0 + j / CH, j % CH), src + j * 8, true);
     cp_async_commit();
     cp_async_wait<0>();
+    if constexpr (C::KV8) {
+      __syncwarp();
+      float big = 0.f;
+#pragma unroll 4
+      for (int j = lane; j < it.rows * CH; j += 32) {
+        uint4 *p = place(j / CH, j % CH);
+        const uint4 x = *p;
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float f0 = bf16lo(w[e]), f1 = bf16hi(w[e]);
+          const float f = fmaxf(fabsf(f0), fabsf(f1));
+          if (f <= FLT_MAX) big = fmaxf(big, f);
+          o[e] = pack_f16x2(f0, f1);
+        }
+        *p = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      if (big >= 65520.f) report_error(a.err, nullptr, kErrFp16Range);
+    }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0)
@@ -810,56 +798,72 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, ui
       : "memory");
 }
 
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+// The value of lane 0, which the compiler may keep in a uniform register: the
+// products' operands have to be in those, and descriptors that only differ by
+// constants then cost one instruction each.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // Warp 0, one thread: the scores, S[k % 2] = Q K^T of step k, once the step's
 // K has landed and P V of step k - 2 has read the P that lay there.
 template <class C>
-__device__ bool issue_qk(const Args &a, uint32_t sbase, uint32_t tmem, Bars<C> &bar, const Item *iq) {
+__device__ bool issue_qk(const Args &a, uint32_t sbase, uint32_t tmem, Bars<C> &bar, const Item *iq, int lane) {
   // 16-bit caches: the landed tiles feed the products
   uint64_t *k_full = C::KV8 ? bar.k_full : bar.lk_full, *k_empty = C::KV8 ? bar.k_empty : bar.lk_empty;
   uint32_t taken = 0, k = 0;
   QSlots qs;
-#pragma unroll 1
+  Item it;
   for (;;) {
-    const uint32_t st = taken % NIQ;
-    if (!wait(&bar.iq_full[st], (taken / NIQ) & 1, a.wait_ns)) return false;
-    const int end = iq[st].end, rows = iq[st].rows, nblk = iq[st].nblk, kvh = iq[st].kvh;
-    mbar_arrive(&bar.iq_empty[st]);
-    ++taken;
-    if (end) return true;
-    qs.next(rows);
+    if (!take_item<C>(a, bar, iq, taken, it, lane)) return false;
+    if (it.end) return true;
+    qs.next(it.rows);
     // the softmax takes maxima of the scores as they come, so a negative
     // scale's sign goes into the product (bit 13 negates A)
-    const uint32_t idesc = C::IDESC_QK | (score_scale(a, kvh) < 0.f ? 1u << 13 : 0u);
+    const uint32_t idesc = uniform(C::IDESC_QK | (score_scale(a, it.kvh) < 0.f ? 1u << 13 : 0u));
     const uint32_t qhalf = qs.big ? C::QHALF : C::QHALF / 2;
     // row 0 of the slot is lane first_lane of the product
-    const uint32_t qd = desc_low(sbase + C::OFF_Q + qs.slot * (C::QB / 2) - first_lane(rows, taken - 1) * 128, 16);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (qs.uses_slot(i) && !wait(&bar.q_full[i], qs.parity(i), a.wait_ns)) return false;
+    const uint32_t qd0 = uniform(
+        desc_low(sbase + C::OFF_Q + qs.slot * (C::QB / 2) - first_lane(it.rows, taken - 1) * 128, 16));
+    const uint32_t qd1 = uniform(qd0 + (qhalf >> 4));  // the second column half
+    if (qs.uses_slot(0) && !wait(&bar.q_full[0], qs.parity(0), a.wait_ns)) return false;
+    if (qs.uses_slot(1) && !wait(&bar.q_full[1], qs.parity(1), a.wait_ns)) return false;
+    uint64_t *s_full = is_narrow(it.rows) ? bar.sn_full[(taken - 1) & 3] : bar.sw_full;
 #pragma unroll 1
-    for (int b = 0; b < nblk; b += BPT, ++k) {
+    for (int b = 0; b < it.nblk; b += BPT, ++k) {
       if (!wait(&bar.p_empty[k & 1], ((k >> 1) & 1) ^ 1, a.wait_ns)) return false;
       if (!wait(&k_full[k % C::NT], (k / C::NT) & 1, a.wait_ns)) return false;
       tc_fence_after_sync();
-      const uint32_t kd = desc_low(sbase + C::OFF_K + (k % C::NT) * C::TB, 16);
-      const uint32_t s = tmem + C::S_COL + (k & 1) * KT;
+      const uint32_t kd = uniform(desc_low(sbase + C::OFF_K + (k % C::NT) * C::TB, 16));
+      const uint32_t s = uniform(tmem + C::S_COL + (k & 1) * KT);
+      if (elect_one()) {
 #pragma unroll
-      for (int kk = 0; kk < C::D / 16; ++kk)
-        mma_ss(s, qd + (kk & 3) * 2 + (kk >> 2) * (qhalf >> 4), desc_high(1024),
-               kd + ((kk >> 2) * 1024 + (kk & 3) * 32) / 16, desc_high(C::GB), idesc, kk > 0);
-      umma_commit(is_narrow(rows) ? &bar.sn_full[(taken - 1) & 3][k & 1] : &bar.sw_full[k & 1]);
-      umma_commit(&k_empty[k % C::NT]);
+        for (int kk = 0; kk < C::D / 16; ++kk)
+          mma_ss(s, (kk < 4 ? qd0 : qd1) + (kk & 3) * 2, desc_high(1024),
+                 kd + ((kk >> 2) * 1024 + (kk & 3) * 32) / 16, desc_high(C::GB), idesc, kk > 0);
+        umma_commit(&s_full[k & 1]);
+        umma_commit(&k_empty[k % C::NT]);
+      }
+      __syncwarp();
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (qs.uses_slot(i)) umma_commit(&bar.q_empty[i]);
+    if (elect_one()) {
+      if (qs.uses_slot(0)) umma_commit(&bar.q_empty[0]);
+      if (qs.uses_slot(1)) umma_commit(&bar.q_empty[1]);
+    }
+    __syncwarp();
     qs.done();
   }
 }
 
 // Warp 2, one thread: O += P V of every step, hi and lo.
 template <class C>
-__device__ bool issue_pv(const Args &a, uint32_t sbase, uint32_t tmem, Bars<C> &bar, const Item *iq) {
+__device__ bool issue_pv(const Args &a, uint32_t sbase, uint32_t tmem, Bars<C> &bar, const Item *iq, int lane) {
   uint64_t *v_full = C::KV8 ? bar.v_full : bar.lv_full, *v_empty = C::KV8 ? bar.v_empty : bar.lv_empty;
   uint32_t taken = 0, k = 0;
   // the barriers of P and of O count the warps that work on the item, two for
@@ -867,16 +871,12 @@ __device__ bool issue_pv(const Args &a, uint32_t sbase, uint32_t tmem, Bars<C> &
   // bit 2 * narrow + buffer is the parity of its next phase
   uint32_t p_par = 0, o_par = 0;
   uint32_t used = 0, was = 0;  // bit = buffer: it has held an item; that was a narrow one
-#pragma unroll 1
+  Item it;
   for (;;) {
-    const uint32_t st = taken % NIQ;
-    if (!wait(&bar.iq_full[st], (taken / NIQ) & 1, a.wait_ns)) return false;
-    const int end = iq[st].end, nblk = iq[st].nblk, nar = is_narrow(iq[st].rows);
-    mbar_arrive(&bar.iq_empty[st]);
-    const uint32_t item = taken++;
-    if (end) return true;
-    const int ob = item & 1;
-    const uint32_t o = tmem + C::O_COL + ob * C::D;
+    if (!take_item<C>(a, bar, iq, taken, it, lane)) return false;
+    if (it.end) return true;
+    const int nar = is_narrow(it.rows), ob = (taken - 1) & 1;
+    const uint32_t o = uniform(tmem + C::O_COL + ob * C::D);
     // the item's first product overwrites the output of the item two before
     if ((used >> ob) & 1) {
       const int kind = (was >> ob) & 1, i = 2 * kind + ob;
@@ -886,28 +886,31 @@ __device__ bool issue_pv(const Args &a, uint32_t sbase, uint32_t tmem, Bars<C> &
     used |= 1u << ob;
     was = (was & ~(1u << ob)) | (static_cast<uint32_t>(nar) << ob);
 #pragma unroll 1
-    for (int b = 0; b < nblk; b += BPT, ++k) {
+    for (int b = 0; b < it.nblk; b += BPT, ++k) {
       if (!wait(&v_full[k % C::NT], (k / C::NT) & 1, a.wait_ns)) return false;
       const int i = 2 * nar + (k & 1);
       if (!wait(&bar.p_full[nar][k & 1], (p_par >> i) & 1, a.wait_ns)) return false;
       p_par ^= 1u << i;
       tc_fence_after_sync();
-      const uint32_t vd = desc_low(sbase + C::OFF_V + (k % C::NT) * C::TB, 1024);
-      const uint32_t p = tmem + C::S_COL + (k & 1) * KT;
-      // keys 16 kk .. 16 kk + 15: hi at +0, lo at +16 of their 32-column chunk
-      // (unrolled: rolled, the issue bounds a long prefix)
-      const int n = nblk - b;
+      const uint32_t vd = uniform(desc_low(sbase + C::OFF_V + (k % C::NT) * C::TB, 1024));
+      const uint32_t p = uniform(tmem + C::S_COL + (k & 1) * KT);
+      const uint32_t n = uniform(it.nblk - b), more = uniform(b);
+      if (elect_one()) {
+        // keys 16 kk .. 16 kk + 15: hi at +0, lo at +16 of their 32-column chunk
 #pragma unroll
-      for (int kk = 0; kk < BPT; ++kk) {
-        if (kk >= n) break;
-        const uint32_t bd = vd + kk * (2 * C::GB / 16), ap = p + (kk >> 1) * 32 + (kk & 1) * 8;
-        mma_ts(o, ap, bd, desc_high(C::GB), C::IDESC_PV, kk > 0 || b > 0);
-        mma_ts(o, ap + 16, bd, desc_high(C::GB), C::IDESC_PV, true);
+        for (int kk = 0; kk < BPT; ++kk) {
+          if (kk >= static_cast<int>(n)) break;
+          const uint32_t bd = vd + kk * (2 * C::GB / 16), ap = p + (kk >> 1) * 32 + (kk & 1) * 8;
+          mma_ts(o, ap, bd, desc_high(C::GB), C::IDESC_PV, kk > 0 || more != 0);
+          mma_ts(o, ap + 16, bd, desc_high(C::GB), C::IDESC_PV, true);
+        }
+        umma_commit(&v_empty[k % C::NT]);
+        umma_commit(&bar.p_empty[k & 1]);
       }
-      umma_commit(&v_empty[k % C::NT]);
-      umma_commit(&bar.p_empty[k & 1]);
+      __syncwarp();
     }
-    umma_commit(nar ? &bar.on_full[item & 3] : &bar.ow_full[ob]);
+    if (elect_one()) umma_commit(nar ? &bar.on_full[(taken - 1) & 3] : &bar.ow_full[ob]);
+    __syncwarp();
   }
 }
 
@@ -1218,13 +1221,11 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
   asm volatile("griddepcontrol.wait;" ::: "memory");
   bool ok = true;
   if (warp == 0) {
-    if (lane == 0) ok = issue_qk<C>(a, smem_u32(smem), tmem, bar, iq);
-    __syncwarp();
+    ok = issue_qk<C>(a, smem_u32(smem), tmem, bar, iq, lane);
   } else if (warp == 1) {
     ok = walk<C>(a, smem, bar, iq, lane);
   } else if (warp == 2) {
-    if (lane == 0) ok = issue_pv<C>(a, smem_u32(smem), tmem, bar, iq);
-    __syncwarp();
+    ok = issue_pv<C>(a, smem_u32(smem), tmem, bar, iq, lane);
   } else if (warp == 3) {
     ok = load_q<C>(a, smem, bar, iq, lane);
   } else if (warp < 12) {
@@ -1245,8 +1246,9 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
   }
   if (!ok && lane == 0) report_error(a.err, nullptr, kErrWaitTimeout);
   // every product issued completes before the tensor memory is given back
-  if ((warp == 0 || warp == 2) && lane == 0) {
-    umma_commit(&bar.drain[warp >> 1]);
+  if (warp == 0 || warp == 2) {
+    __syncwarp();
+    if (elect_one()) umma_commit(&bar.drain[warp >> 1]);  // the lane that issued them
     wait(&bar.drain[warp >> 1], 0, a.wait_ns);
   }
   tc_fence_before_sync();
