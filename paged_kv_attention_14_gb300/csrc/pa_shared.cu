@@ -105,6 +105,7 @@ cudaError_t launch_shared(const pa_kv_desc &d, float *out, float *lse, const voi
   memset(&a, 0, sizeof a);
   if (!make_map(&a.kmap, k_cache, d) || !make_map(&a.vmap, v_cache, d)) return cudaErrorInvalidValue;
   a.ctas = device_sm_count();
+  a.item_units = b16 ? shd::kItemUnits16 : shd::kItemUnits8;
   const Layout w = layout(d, num_seqs, num_groups, max_group_size, a.ctas);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   a.out = out;
@@ -164,8 +165,8 @@ cudaError_t launch_shared(const pa_kv_desc &d, float *out, float *lse, const voi
   cfg.dynamicSmemBytes = k.smem;
   e = cudaLaunchKernelExC(&cfg, k.fn, args);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(num_seqs) * d.num_q_heads + 15) / 16));
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(num_seqs) * d.num_q_heads + 3) / 4));
+  cfg.blockDim = dim3(64);
   cfg.dynamicSmemBytes = 0;
   const void *join = d.head_dim == 64 ? reinterpret_cast<const void *>(&shd::shared_join_kernel<64>)
                                       : reinterpret_cast<const void *>(&shd::shared_join_kernel<128>);

@@ -31,11 +31,12 @@
 //      products of the next;
 //   1  walks the CTA's part of the axis, publishes its items, copies their
 //      K and V (TMA);
-//   3  Q tiles (two slots, so that items overlap);
+//   3  (16-bit caches) Q tiles, in two slots, so that items overlap;
 //   4-11  softmax, two threads per row (64 keys each), and each item's output;
 //      items of up to 32 rows take one quarter of the lanes each, in turn, so
 //      that four of them can be in their softmax or output at once;
-//   12-15 (8-bit caches) widen the landed bytes to fp16 tiles (exact).
+//   12-15 (8-bit caches) Q tiles, and the landed bytes widened to fp16
+//      tiles (exact).
 // Scores and outputs are double-buffered in tensor memory (S 2 x 128, O 2 x D
 // columns); P overwrites its scores.  Every wait is bounded.
 #pragma once
@@ -62,30 +63,36 @@ constexpr int BPT = KT / 16;     // blocks of a step
 constexpr float kRaise = 8.f;
 // An item costs its blocks and this many more (its Q tile, its first copies'
 // latency, its output), so the axis gives it that many extra units in front.
-constexpr int kItemUnits = 10;
-// a CTA's share is at least one item of one step
-constexpr int kMinUnits = kItemUnits + BPT;
+// Measured best on batches of short own parts behind long prefixes: 6 with
+// 16-bit caches (four groups of 16 on 4096 tokens: 44.9 us with 2, 40.8 with
+// 6, 41.1 with 10), 4 with 8-bit ones, whose wide steps take longer (E4M3
+// batch of 128: 122 us with 2, 106 with 4, 112 with 6).
+constexpr int kItemUnits16 = 6, kItemUnits8 = 4;
 
 // One group's prefix on the axis.
-struct __align__(16) GroupInfo {
+struct __align__(8) GroupInfo {
   long long base;  // first unit
   int first;       // first sequence
   int n;           // sequences
-  int nb;          // blocks of the prefix that some sequence reads (0: nothing shared)
   int kend;        // keys of the prefix that some sequence reads
+  int nb;          // blocks of them (0: nothing shared)
   int tile_seqs;   // sequences of a tile (the last tile may have fewer)
   int tiles;
   int row;         // a sequence whose table holds all of the prefix that is read
-  int pad[3];
+  int P;           // the prefix, whole blocks
 };
-// One sequence's own part.
+// One sequence: its own part, and its place in its group's prefix part.
 struct __align__(16) SeqInfo {
-  long long base;
-  int len;    // tokens
-  int fb;     // first own block
-  int nb;     // own blocks
-  int group;  // its group, -1: none
-  int pad[2];
+  long long base;   // first unit of the own part
+  int len;          // tokens
+  int fb;           // first own block
+  int nb;           // own blocks
+  int group;        // its group, -1: none
+  long long pbase;  // first unit of its tile of the prefix (kv head 0)
+  int pnb;          // blocks of the prefix, 0: none
+  int prow;         // first row in the tile
+  int prows;        // rows of the tile
+  int pseq;         // first sequence of the tile
 };
 // Where a CTA's part of the axis begins.
 struct __align__(16) CtaStart {
@@ -119,6 +126,7 @@ struct Args {
   int tile_seqs;  // sequences a tile may have
   int slot_rows;  // rows of a cut item's slot
   int ctas;       // CTAs that share the axis
+  int item_units;  // units of an item besides its blocks
   float qscale;   // scale * k_scale * log2(e)
   float qscale0;  // scale * log2(e)
   float vscale;
@@ -147,34 +155,48 @@ struct Args {
 constexpr int PLAN_THREADS = 512;
 constexpr int PLAN_CAP = 512;  // sequences / groups planned in shared memory
 
-// n / d, in one place: a 64-bit division is some 100 instructions
-static __device__ __noinline__ long long divide(long long n, long long d) { return n / d; }
-
-// Exclusive prefix sum over the CTA's threads; *total gets the sum.
-static __device__ __noinline__ long long scan_exclusive(long long v, long long *total, long long *s_warp) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long incl = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += t;
-  }
-  __syncthreads();  // s_warp may still be read from the last call
-  if (lane == 31) s_warp[warp] = incl;
-  __syncthreads();
-  long long before = 0, sum = 0;
-#pragma unroll 4
-  for (int i = 0; i < PLAN_THREADS / 32; ++i) {
-    const long long x = s_warp[i];
-    if (i < warp) before += x;
-    sum += x;
-  }
-  *total = sum;
-  return before + incl - v;
+// n / d: 32 bits where they do (a 64-bit division is some 100 instructions)
+static __device__ __noinline__ long long divide64(long long n, long long d) { return n / d; }
+__device__ __forceinline__ long long divide(long long n, long long d) {
+  if (((n | d) >> 31) == 0) return static_cast<unsigned>(n) / static_cast<unsigned>(d);
+  return divide64(n, d);
 }
 
 // Units of an item of nb blocks.
-__host__ __device__ __forceinline__ int item_units(int nb) { return nb > 0 ? nb + kItemUnits : 0; }
+__device__ __forceinline__ int item_units(const Args &a, int nb) { return nb > 0 ? nb + a.item_units : 0; }
+
+// Exclusive prefix sums of two values over the CTA's threads; total gets the sums.
+__device__ __forceinline__ void scan2(long long (&v)[2], long long (&total)[2], long long (*s_warp)[2]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long in[2] = {v[0], v[1]};
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const long long t = __shfl_up_sync(0xffffffffu, in[i], o);
+      if (lane >= o) in[i] += t;
+    }
+  __syncthreads();  // s_warp may still be read from the last call
+  if (lane == 31) {
+    s_warp[warp][0] = in[0];
+    s_warp[warp][1] = in[1];
+  }
+  __syncthreads();
+  long long before[2] = {0, 0}, sum[2] = {0, 0};
+#pragma unroll 4
+  for (int w = 0; w < PLAN_THREADS / 32; ++w)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const long long x = s_warp[w][i];
+      if (w < warp) before[i] += x;
+      sum[i] += x;
+    }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    total[i] = sum[i];
+    v[i] = before[i] + in[i] - v[i];
+  }
+}
 
 // The last entry whose base is <= u (entries without work share the base of
 // the next one, so it is the entry that holds unit u).
@@ -192,91 +214,91 @@ __device__ __forceinline__ int find_base(const T *v, int n, long long u) {
   return lo;
 }
 
+// The plan, by one CTA: a thread per group and per sequence (in rounds of
+// PLAN_THREADS).  Up to PLAN_CAP of each are worked on in shared memory.
 static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const __grid_constant__ Args a) {
-  __shared__ long long s_warp[PLAN_THREADS / 32];
+  __shared__ long long s_warp[PLAN_THREADS / 32][2];
   __shared__ SeqInfo s_seqs[PLAN_CAP];
   __shared__ GroupInfo s_groups[PLAN_CAP];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x;
   const int S = a.num_seqs, G = a.num_groups;
   const int cap = a.max_blocks * 16;
-  SeqInfo *seqs = S <= PLAN_CAP ? s_seqs : a.seqs;
-  GroupInfo *groups = G <= PLAN_CAP ? s_groups : a.groups;
+  const bool small = S <= PLAN_CAP && G <= PLAN_CAP;
+  SeqInfo *seqs = small ? s_seqs : a.seqs;
+  GroupInfo *groups = small ? s_groups : a.groups;
+  // the first round's lengths are in flight beside the groups'
+  int len0 = tid < S ? __ldg(a.context_lens + tid) : 0;
+#pragma unroll 1
+  for (int j = tid; j < G; j += PLAN_THREADS) {
+    const int r0 = __ldg(a.group_start + j), r1 = __ldg(a.group_start + j + 1), r2 = __ldg(a.prefix_lens + j);
+    // whatever the arrays hold, no access leaves the batch
+    GroupInfo q = {};
+    q.first = min(max(r0, 0), S);
+    q.n = min(max(r1, q.first), S) - q.first;
+    if (a.checked && (r0 != q.first || r1 != q.first + q.n || r2 < 0 || r2 > cap))
+      report_error(a.err, nullptr, kErrBadIndex);
+    q.P = q.n < 2 ? 0 : min(max(r2, 0), cap) & ~15;  // a group of one shares with nobody
+    q.row = 0x7fffffff;
+    // tiles of equal numbers of sequences
+    const int t = max(1, (q.n + a.tile_seqs - 1) / a.tile_seqs);
+    q.tile_seqs = max(1, (q.n + t - 1) / t);
+    q.tiles = (q.n + q.tile_seqs - 1) / q.tile_seqs;
+    groups[j] = q;
+  }
+  __syncthreads();
+  // each sequence's group (a binary search over the first sequences), and the
+  // longest part of each prefix that a sequence reads
 #pragma unroll 1
   for (int s = tid; s < S; s += PLAN_THREADS) {
-    int L = __ldg(a.context_lens + s);
+    int L = s == tid ? len0 : __ldg(a.context_lens + s);
     if (a.checked) L = checked_len(L, cap, a.err, nullptr);
     SeqInfo q = {};
     q.len = max(L, 0);
-    q.group = -1;
+    int lo = 0, hi = G - 1;
+#pragma unroll 1
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (groups[mid].first <= s)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    q.group = G > 0 && s >= groups[lo].first && s < groups[lo].first + groups[lo].n ? lo : -1;
+    if (q.group >= 0 && groups[lo].P > 0) {
+      q.fb = groups[lo].P >> 4;
+      atomicMax(&groups[lo].kend, min(q.len, groups[lo].P));
+    }
+    q.nb = max(0, ((q.len + 15) >> 4) - q.fb);
     seqs[s] = q;
   }
   __syncthreads();
-  // one warp per group: its sequences, and how much of the prefix they read
 #pragma unroll 1
-  for (int j = warp; j < G; j += PLAN_THREADS / 32) {
-    const int r0 = __ldg(a.group_start + j), r1 = __ldg(a.group_start + j + 1);
-    int P = __ldg(a.prefix_lens + j);
-    // whatever the arrays hold, no access leaves the batch
-    const int s0 = min(max(r0, 0), S), s1 = min(max(r1, s0), S);
-    if (a.checked && lane == 0 && (r0 != s0 || r1 != s1 || P < 0 || P > cap)) report_error(a.err, nullptr, kErrBadIndex);
-    P = min(max(P, 0), cap) & ~15;
-    if (s1 - s0 < 2) P = 0;  // nobody to share with
-    int mine = -1, row = 0;
-#pragma unroll 1
-    for (int s = s0 + lane; s < s1; s += 32) {
-      const int n = min(seqs[s].len, P);
-      if (n > mine) {
-        mine = n;
-        row = s;
-      }
-      seqs[s].fb = P >> 4;
-      seqs[s].group = j;
-    }
-    const int best = __reduce_max_sync(0xffffffffu, mine);
-    row = __reduce_min_sync(0xffffffffu, mine == best ? row : 0x7fffffff);
-    if (lane == 0) {
-      GroupInfo q = {};
-      q.row = row;
-      q.first = s0;
-      q.n = s1 - s0;
-      q.kend = max(best, 0);
-      q.nb = (q.kend + 15) >> 4;
-      // tiles of equal numbers of sequences
-      q.tiles = max(1, (q.n + a.tile_seqs - 1) / a.tile_seqs);
-      q.tile_seqs = max(1, (q.n + q.tiles - 1) / q.tiles);
-      q.tiles = (q.n + q.tile_seqs - 1) / q.tile_seqs;
-      groups[j] = q;
-    }
+  for (int s = tid; s < S; s += PLAN_THREADS) {
+    const SeqInfo &q = seqs[s];
+    if (q.fb > 0 && min(q.len, q.fb * 16) == groups[q.group].kend) atomicMin(&groups[q.group].row, s);
   }
-  __syncthreads();
   // places on the axis: prefix items, then own parts
-  long long at = 0;
+  long long at[2] = {0, 0};
 #pragma unroll 1
-  for (int j0 = 0; j0 < G; j0 += PLAN_THREADS) {
-    const int j = j0 + tid;
-    const long long v = j < G ? static_cast<long long>(item_units(groups[j].nb)) * groups[j].tiles * a.num_kv : 0;
-    long long sum;
-    const long long e = scan_exclusive(v, &sum, s_warp);
-    if (j < G) groups[j].base = at + e;
-    at += sum;
-  }
-  const long long own = at;  // first unit of the own parts
-#pragma unroll 1
-  for (int s0 = 0; s0 < S; s0 += PLAN_THREADS) {
-    const int s = s0 + tid;
-    const int nb = s < S ? max(0, ((seqs[s].len + 15) >> 4) - seqs[s].fb) : 0;
-    long long sum;
-    const long long e = scan_exclusive(static_cast<long long>(item_units(nb)) * a.num_kv, &sum, s_warp);
-    if (s < S) {
-      seqs[s].nb = nb;
-      seqs[s].base = at + e;
+  for (int i0 = 0; i0 < max(S, G); i0 += PLAN_THREADS) {
+    const int i = i0 + tid;
+    long long v[2] = {0, 0}, sum[2];
+    if (i < G) {
+      const int nb = (groups[i].kend + 15) >> 4;
+      groups[i].nb = nb;
+      v[0] = static_cast<long long>(item_units(a, nb)) * (groups[i].tiles * a.num_kv);
     }
-    at += sum;
+    if (i < S) v[1] = static_cast<long long>(item_units(a, seqs[i].nb)) * a.num_kv;
+    scan2(v, sum, s_warp);
+    if (i < G) groups[i].base = at[0] + v[0];
+    if (i < S) seqs[i].base = at[1] + v[1];
+    at[0] += sum[0];
+    at[1] += sum[1];
   }
-  const long long U = at;
-  const long long per = max(divide(U + a.ctas - 1, a.ctas), static_cast<long long>(kMinUnits));
+  const long long own = at[0], U = at[0] + at[1];  // the own parts' first unit, and the end
+  const long long per = max(divide(U + a.ctas - 1, a.ctas), static_cast<long long>(a.item_units + BPT));
   if (tid == 0) *a.axis = Axis{U, per};
   __syncthreads();
   // each CTA's first item
@@ -286,18 +308,31 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
     CtaStart st = {2, 0, 0, 0};
     if (u < U) {
       st.kind = u < own ? 0 : 1;
-      st.idx = st.kind == 0 ? find_base(groups, G, u) : find_base(seqs, S, u);
-      const int n = item_units(st.kind == 0 ? groups[st.idx].nb : seqs[st.idx].nb);
-      const long long r = u - (st.kind == 0 ? groups[st.idx].base : seqs[st.idx].base);
+      st.idx = st.kind == 0 ? find_base(groups, G, u) : find_base(seqs, S, u - own);
+      const int n = item_units(a, st.kind == 0 ? groups[st.idx].nb : seqs[st.idx].nb);
+      const long long r = st.kind == 0 ? u - groups[st.idx].base : u - own - seqs[st.idx].base;
       st.sub = static_cast<int>(divide(r, n));
       st.off = static_cast<int>(r - static_cast<long long>(st.sub) * n);
     }
     a.starts[c] = st;
   }
-  if (S <= PLAN_CAP)
+  if (!small) __syncthreads();  // the searches above read what is completed below
 #pragma unroll 1
-    for (int s = tid; s < S; s += PLAN_THREADS) a.seqs[s] = s_seqs[s];
-  if (G <= PLAN_CAP)
+  for (int s = tid; s < S; s += PLAN_THREADS) {
+    SeqInfo q = seqs[s];
+    q.base += own;
+    if (q.fb > 0) {
+      const GroupInfo &gi = groups[q.group];
+      const int i = s - gi.first, tile = i / gi.tile_seqs, t0 = tile * gi.tile_seqs;
+      q.pnb = q.len > 0 ? gi.nb : 0;
+      q.pbase = gi.base + static_cast<long long>(tile * a.num_kv) * item_units(a, gi.nb);
+      q.prow = (i - t0) * a.g;
+      q.prows = min(gi.tile_seqs, gi.n - t0) * a.g;
+      q.pseq = gi.first + t0;
+    }
+    a.seqs[s] = q;
+  }
+  if (small)
 #pragma unroll 1
     for (int j = tid; j < G; j += PLAN_THREADS) a.groups[j] = s_groups[j];
 }
@@ -575,10 +610,10 @@ __device__ bool walk(const Args &a, uint8_t *smem, Bars<C> &bar, Item *iq, int l
       it.rows = min(tile_seqs, n - tile * tile_seqs) * a.g;
       it.prefix = kind == 0;
       // the part of the item's units in this CTA's range, and its blocks
-      const int size = item_units(nb);
+      const int size = item_units(a, nb);
       const int take = static_cast<int>(min(static_cast<long long>(size - st.off), left));
-      const int lo = max(st.off - kItemUnits, 0);
-      it.nblk = max(st.off + take - kItemUnits, 0) - lo;
+      const int lo = max(st.off - a.item_units, 0);
+      it.nblk = max(st.off + take - a.item_units, 0) - lo;
       it.key0 = (fb + lo) * 16;
       it.kend = min(kend, it.key0 + it.nblk * 16);  // a cut piece ends before the item
       it.lo = lo;
@@ -641,12 +676,20 @@ __device__ __forceinline__ bool take_item(const Args &a, Bars<C> &bar, const Ite
   return true;
 }
 
-// Warp 3: Q tiles, [half][row][128 B] with the 128-byte swizzle.  With an
-// 8-bit cache the bf16 queries become fp16 (a finite |q| beyond fp16 does
-// not fit and is reported).
+// Where a Q tile's 16-byte column chunk `ch` lies: [half][row][128 B] with the
+// 128-byte swizzle; row R of it at + R * 128, chunk ch & 7 XORed with R & 7.
+template <class C>
+__device__ __forceinline__ uint8_t *q_column(uint8_t *smem, const QSlots &qs, int ch) {
+  return smem + C::OFF_Q + qs.slot * (C::QB / 2) + (ch >> 3) * (qs.big ? C::QHALF : C::QHALF / 2);
+}
+__device__ __forceinline__ int q_row(int R, int ch) { return R * 128 + (((ch & 7) ^ (R & 7)) << 4); }
+
+// Warp 3 (16-bit caches): Q tiles by asynchronous copies.
 template <class C>
 __device__ bool load_q(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq, int lane) {
-  constexpr int CH = C::D / 8;  // 16-byte chunks of a row
+  constexpr int CH = C::D / 8;    // 16-byte chunks of a row
+  constexpr int RPI = 32 / CH;    // rows a warp copies at once
+  const int ch = lane % CH;       // a lane keeps its column chunk
   uint32_t taken = 0;
   QSlots qs;
   Item it;
@@ -655,53 +698,27 @@ __device__ bool load_q(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *i
     if (!take_item<C>(a, bar, iq, taken, it, lane)) return false;
     if (it.end) return true;
     qs.next(it.rows);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (qs.uses_slot(i) && !wait(&bar.q_empty[i], qs.parity(i) ^ 1, a.wait_ns)) return false;
-    uint8_t *base = smem + C::OFF_Q + qs.slot * (C::QB / 2);
-    const int half = qs.big ? C::QHALF : C::QHALF / 2;
-    // a sequence's g rows lie together: g x CH chunks of 16 bytes
-    const int chunks = a.g * CH;
-    const uint16_t *src = a.q + (static_cast<int64_t>(it.seq0) * a.num_q + it.kvh * a.g) * C::D;
-    auto place = [&](int R, int ch) {
-      return reinterpret_cast<uint4 *>(base + (ch >> 3) * half + R * 128 + (((ch & 7) ^ (R & 7)) << 4));
-    };
+    if (qs.uses_slot(0) && !wait(&bar.q_empty[0], qs.parity(0) ^ 1, a.wait_ns)) return false;
+    if (qs.uses_slot(1) && !wait(&bar.q_empty[1], qs.parity(1) ^ 1, a.wait_ns)) return false;
+    uint8_t *col = q_column<C>(smem, qs, ch);
+    const uint16_t *src = a.q + (static_cast<int64_t>(it.seq0) * a.num_q + it.kvh * a.g) * C::D + ch * 8;
 #pragma unroll 1
     for (int R0 = 0; R0 < it.rows; R0 += a.g, src += static_cast<int64_t>(a.num_q) * C::D)
-#pragma unroll 1
-      for (int j = lane; j < chunks; j += 32) cp_async16(place(R0 + j / CH, j % CH), src + j * 8, true);
+#pragma unroll 2
+      for (int r = lane / CH; r < a.g; r += RPI) cp_async16(col + q_row(R0 + r, ch), src + r * C::D, true);
     cp_async_commit();
     cp_async_wait<0>();
-    if constexpr (C::KV8) {
-      __syncwarp();
-      float big = 0.f;
-#pragma unroll 4
-      for (int j = lane; j < it.rows * CH; j += 32) {
-        uint4 *p = place(j / CH, j % CH);
-        const uint4 x = *p;
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        uint32_t o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float f0 = bf16lo(w[e]), f1 = bf16hi(w[e]);
-          const float f = fmaxf(fabsf(f0), fabsf(f1));
-          if (f <= FLT_MAX) big = fmaxf(big, f);
-          o[e] = pack_f16x2(f0, f1);
-        }
-        *p = make_uint4(o[0], o[1], o[2], o[3]);
-      }
-      if (big >= 65520.f) report_error(a.err, nullptr, kErrFp16Range);
-    }
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0)
-      for (int i = 0; i < 2; ++i)
-        if (qs.uses_slot(i)) mbar_arrive(&bar.q_full[i]);
+    if (lane == 0) {
+      if (qs.uses_slot(0)) mbar_arrive(&bar.q_full[0]);
+      if (qs.uses_slot(1)) mbar_arrive(&bar.q_full[1]);
+    }
     qs.done();
   }
 }
 
-// Warps 12-15 (8-bit caches): landed bytes to fp16 tiles, exact; V rows past
+// Warps 12-15 (8-bit caches): Q tiles in fp16, landed bytes to fp16 tiles, exact; V rows past
 // the piece's keys zeroed (they may hold anything, and 0 * NaN is NaN).  A
 // thread keeps its 16-byte column chunk and its row modulo 8, and with them
 // its places in the swizzled tile, over all its rows.
@@ -715,11 +732,66 @@ __device__ bool widen(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq
   const int put = (r0 >> 3) * C::GB + (c >> 2) * 1024 + r7 * 128;
   const int x0 = ((2 * (c & 3)) ^ r7) << 4, x1 = ((2 * (c & 3) + 1) ^ r7) << 4;
   uint32_t taken = 0, step = 0;
+  QSlots qs;
   Item it;
 #pragma unroll 1
   for (;;) {
     if (!take_item<C>(a, bar, iq, taken, it, lane)) return false;
     if (it.end) return true;
+    // the item's Q tile: bf16 queries become fp16 (a finite |q| beyond fp16
+    // does not fit and is reported)
+    qs.next(it.rows);
+    if (qs.uses_slot(0) && !wait(&bar.q_empty[0], qs.parity(0) ^ 1, a.wait_ns)) return false;
+    if (qs.uses_slot(1) && !wait(&bar.q_empty[1], qs.parity(1) ^ 1, a.wait_ns)) return false;
+    {
+      constexpr int QCH = C::D / 8, RPI = C::NCONV * 32 / QCH;
+      const int ch = ct % QCH;
+      uint8_t *col = q_column<C>(smem, qs, ch);
+      const uint16_t *src = a.q + (static_cast<int64_t>(it.seq0) * a.num_q + it.kvh * a.g) * C::D + ch * 8;
+      int R = ct / QCH, sq = R / a.g, hd = R - sq * a.g;
+      float big = 0.f;
+#pragma unroll 1
+      while (R < it.rows) {
+        constexpr int ILP = 4;
+        uint4 x[ILP];
+        int at[ILP];
+#pragma unroll
+        for (int k = 0; k < ILP; ++k) {
+          at[k] = R < it.rows ? q_row(R, ch) : -1;
+          if (at[k] >= 0)
+            x[k] = __ldg(reinterpret_cast<const uint4 *>(src + (static_cast<int64_t>(sq) * a.num_q + hd) * C::D));
+          R += RPI;
+          hd += RPI;
+#pragma unroll 1
+          while (hd >= a.g) {
+            hd -= a.g;
+            ++sq;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < ILP; ++k) {
+          if (at[k] < 0) continue;
+          const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float f0 = bf16lo(w[e]), f1 = bf16hi(w[e]);
+            const float f = fmaxf(fabsf(f0), fabsf(f1));
+            if (f <= FLT_MAX) big = fmaxf(big, f);
+            o[e] = pack_f16x2(f0, f1);
+          }
+          *reinterpret_cast<uint4 *>(col + at[k]) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+      if (big >= 65520.f) report_error(a.err, nullptr, kErrFp16Range);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (qs.uses_slot(0)) mbar_arrive(&bar.q_full[0]);
+        if (qs.uses_slot(1)) mbar_arrive(&bar.q_full[1]);
+      }
+      qs.done();
+    }
 #pragma unroll 1
     for (int b = 0; b < it.nblk; b += BPT, ++step) {
       const int rows = min(BPT, it.nblk - b) * 16;
@@ -1178,7 +1250,7 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
   if (threadIdx.x == 0) {
     for (int i = 0; i < NIQ; ++i) {
       mbar_init(&bar.iq_full[i], 1);
-      mbar_init(&bar.iq_empty[i], 1 + 1 + 1 + 8 + C::NCONV);  // the warps that take items
+      mbar_init(&bar.iq_empty[i], C::KV8 ? 1 + 1 + 8 + C::NCONV : 1 + 1 + 1 + 8);  // the warps that take items
     }
     for (int i = 0; i < C::NL; ++i) {
       mbar_init(&bar.lk_full[i], 1);
@@ -1193,7 +1265,7 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
       mbar_init(&bar.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar.q_full[i], 1);
+      mbar_init(&bar.q_full[i], C::KV8 ? C::NCONV : 1);
       mbar_init(&bar.q_empty[i], 1);
       mbar_init(&bar.sw_full[i], 1);
       mbar_init(&bar.ow_full[i], 1);
@@ -1227,7 +1299,7 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
   } else if (warp == 2) {
     ok = issue_pv<C>(a, smem_u32(smem), tmem, bar, iq, lane);
   } else if (warp == 3) {
-    ok = load_q<C>(a, smem, bar, iq, lane);
+    if constexpr (!C::KV8) ok = load_q<C>(a, smem, bar, iq, lane);
   } else if (warp < 12) {
     const int h = (warp - 4) >> 2;
     Softmax<C> sm{a,
@@ -1261,11 +1333,7 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
 
 // --------------------------------------------------------------------- join
 
-// u / n for the axis (32-bit where it fits)
-__device__ __forceinline__ int axis_cta(long long u, const Axis &x) {
-  if (x.units < 0x7fffffffLL) return static_cast<int>(static_cast<unsigned>(u) / static_cast<unsigned>(x.per));
-  return static_cast<int>(divide(u, x.per));
-}
+__device__ __forceinline__ int axis_cta(long long u, const Axis &x) { return static_cast<int>(divide(u, x.per)); }
 
 // Two rows (sequence, head) per warp, a row on the lanes of one parity, 16
 // bytes of it a lane: two neighbouring rows of a tile fill a 32-byte sector of
@@ -1273,7 +1341,7 @@ __device__ __forceinline__ int axis_cta(long long u, const Axis &x) {
 // log-sum-exps.  Rows that the attention wrote itself (one uncut part) are
 // left alone.
 template <int D>
-__global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(64) shared_join_kernel(const __grid_constant__ Args a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
@@ -1293,21 +1361,16 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
   // the part's own place if one CTA holds all its blocks
   auto pieces = [&](long long u0, int nb, int &c1, int &np, int &s0) {
     c1 = axis_cta(u0, ax);
-    if ((c1 + 1) * ax.per - u0 <= kItemUnits) ++c1;  // that CTA's range holds none of its blocks
-    np = axis_cta(u0 + item_units(nb) - 1, ax) - c1 + 1;
+    if ((c1 + 1) * ax.per - u0 <= a.item_units) ++c1;  // that CTA's range holds none of its blocks
+    np = axis_cta(u0 + item_units(a, nb) - 1, ax) - c1 + 1;
     s0 = u0 > c1 * ax.per;
   };
-  int p_c1 = 0, p_n = 0, p_s0 = 0, p_r = 0, p_rows = 1, o_c1 = 0, o_n = 0, o_s0 = 0;
-  int64_t p_at = 0;  // the prefix part's tile in pre_o / pre_lse
-  if (q.fb > 0 && q.len > 0) {
-    const GroupInfo gi = a.groups[q.group];
-    const int i = s - gi.first, tile = i / gi.tile_seqs, t0 = tile * gi.tile_seqs;
-    pieces(gi.base + static_cast<long long>(tile * a.num_kv + kvh) * item_units(gi.nb), gi.nb, p_c1, p_n, p_s0);
-    p_r = (i - t0) * a.g + hg;
-    p_rows = min(gi.tile_seqs, gi.n - t0) * a.g;
-    p_at = static_cast<int64_t>(gi.first + t0) * a.num_q + static_cast<int64_t>(kvh) * p_rows;
-  }
-  if (q.nb > 0) pieces(q.base + static_cast<long long>(kvh) * item_units(q.nb), q.nb, o_c1, o_n, o_s0);
+  int p_c1 = 0, p_n = 0, p_s0 = 0, o_c1 = 0, o_n = 0, o_s0 = 0;
+  const int p_r = q.prow + hg;
+  // the prefix part's tile in pre_o / pre_lse
+  const int64_t p_at = static_cast<int64_t>(q.pseq) * a.num_q + static_cast<int64_t>(kvh) * q.prows;
+  if (q.pnb > 0) pieces(q.pbase + static_cast<long long>(kvh) * item_units(a, q.pnb), q.pnb, p_c1, p_n, p_s0);
+  if (q.nb > 0) pieces(q.base + static_cast<long long>(kvh) * item_units(a, q.nb), q.nb, o_c1, o_n, o_s0);
   if (q.fb == 0 && o_n == 1) mine = false;
   const int n = mine ? p_n + o_n : 0;
   // where piece i's log-sum-exp and columns 0 .. 3 are, and the distance to the next columns
@@ -1316,7 +1379,7 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
     if (pre && p_n == 1) {
       x = a.pre_lse + p_at + p_r;
       o = a.pre_o + p_at * D + 4 * p_r;
-      return 4 * p_rows;
+      return 4 * q.prows;
     }
     if (!pre && o_n == 1) {
       x = a.own_lse + row;
