@@ -1403,13 +1403,12 @@ __global__ void __launch_bounds__(64) shared_join_kernel(const __grid_constant__
   const int most = max(n, __shfl_xor_sync(0xffffffffu, n, 1));
 #pragma unroll 1
   for (int i0 = 0; i0 < most; i0 += 16) {
+    // (past the row's pieces: its first one again, with no weight)
     const float *x = nullptr, *o = a.pre_o;
     int stride = 0;
     float v = -INFINITY;
-    if (i0 + c0 < n) {
-      stride = piece(i0 + c0, x, o);
-      v = __ldcg(x);
-    }
+    if (n > 0) stride = piece(i0 + c0 < n ? i0 + c0 : 0, x, o);
+    if (i0 + c0 < n) v = __ldcg(x);
     float mn = fmaxf(M, v);
 #pragma unroll
     for (int b = 2; b < 32; b <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, b));
@@ -1423,32 +1422,31 @@ __global__ void __launch_bounds__(64) shared_join_kernel(const __grid_constant__
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[j] = make_float4(acc[j].x * f, acc[j].y * f, acc[j].z * f, acc[j].w * f);
     const int m = min(16, most - i0);
-#pragma unroll 4
+    // no branch on the weights: the loads of eight pieces are in flight at once
+#pragma unroll 8
     for (int i = 0; i < m; ++i) {
       const int from = 2 * i + (lane & 1);
       const float wi = __shfl_sync(0xffffffffu, w, from);
       const float *oi = reinterpret_cast<const float *>(
           __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), from));
       const int64_t st = __shfl_sync(0xffffffffu, stride, from);
-      // (past a row's pieces: the workspace's first element, with no weight)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         const float4 y = __ldcg(reinterpret_cast<const float4 *>(oi + (c0 + 16 * j) * st));
-        if (wi != 0.f) {
-          acc[j].x += wi * y.x;
-          acc[j].y += wi * y.y;
-          acc[j].z += wi * y.z;
-          acc[j].w += wi * y.w;
-        }
+        acc[j].x += wi * y.x;
+        acc[j].y += wi * y.y;
+        acc[j].z += wi * y.z;
+        acc[j].w += wi * y.w;
       }
     }
   }
   if (!mine) return;
-  const float inv = W == 0.f ? 0.f : (a.v_scales ? __ldg(a.v_scales + kvh) : a.vscale) / W;
+  const float inv = (a.v_scales ? __ldg(a.v_scales + kvh) : a.vscale) / W;
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
     *reinterpret_cast<float4 *>(a.out + row * D + 4 * (c0 + 16 * j)) =
-        make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv);
+        W == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                 : make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv);
   if (a.lse && c0 == 0) a.lse[row] = W == 0.f ? -INFINITY : (M + log2f(W)) * kLn2;
 }
 
