@@ -73,16 +73,17 @@ Layout layout(const pa_kv_desc &d, int32_t num_seqs, int32_t num_groups, int32_t
     at += up256(bytes);
     return x;
   };
+  // (the parts first: the join counts their places from cut_o)
+  w.cut_o = take(cut * d.head_dim * 4);
+  w.pre_o = take(rows * d.head_dim * 4);
+  w.own_o = take(rows * d.head_dim * 4);
+  w.cut_lse = take(cut * 4);
+  w.pre_lse = take(rows * 4);
+  w.own_lse = take(rows * 4);
   w.axis = take(sizeof(shd::Axis));
   w.groups = take(sizeof(shd::GroupInfo) * num_groups);
   w.seqs = take(sizeof(shd::SeqInfo) * num_seqs);
   w.starts = take(sizeof(shd::CtaStart) * ctas);
-  w.pre_o = take(rows * d.head_dim * 4);
-  w.pre_lse = take(rows * 4);
-  w.own_o = take(rows * d.head_dim * 4);
-  w.own_lse = take(rows * 4);
-  w.cut_o = take(cut * d.head_dim * 4);
-  w.cut_lse = take(cut * 4);
   w.total = at;
   return w;
 }

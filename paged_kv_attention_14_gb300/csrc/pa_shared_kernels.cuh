@@ -1333,111 +1333,124 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
 
 // --------------------------------------------------------------------- join
 
-__device__ __forceinline__ int axis_cta(long long u, const Axis &x) { return static_cast<int>(divide(u, x.per)); }
+// The CTA that holds unit u of the axis (called, not inlined: the join runs
+// once per launch, and what it costs most is fetching its instructions)
+static __device__ __noinline__ int axis_cta(long long u, long long per) { return static_cast<int>(divide(u, per)); }
 
 // Two rows (sequence, head) per warp, a row on the lanes of one parity, 16
 // bytes of it a lane: two neighbouring rows of a tile fill a 32-byte sector of
 // its [4 columns][row] parts.  Each row's pieces are weighed by their
 // log-sum-exps.  Rows that the attention wrote itself (one uncut part) are
-// left alone.
+// left alone.  Places in the workspace are counted in 16 bytes from cut_o.
 template <int D>
 __global__ void __launch_bounds__(64) shared_join_kernel(const __grid_constant__ Args a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_q;
-  int64_t row = (static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5)) * 2 + (lane & 1);
+  int64_t row = (static_cast<int64_t>(blockIdx.x) * 2 + (threadIdx.x >> 5)) * 2 + (lane & 1);
   // every lane stays for the shuffles
   bool mine = row < rows;
   if (!mine) row = rows - 1;
   const int c0 = lane >> 1;  // this lane's columns: 4 (c0 + 16 j)
-  constexpr int NJ = D / 64;
-  const int s = static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(a.num_q));
-  const int h = static_cast<int>(row - static_cast<int64_t>(s) * a.num_q), kvh = h / a.g, hg = h - kvh * a.g;
+  constexpr int NJ = D / 64, C4 = D / 4;
+  const uint32_t s = static_cast<uint32_t>(row) / static_cast<uint32_t>(a.num_q);
+  const int h = static_cast<int>(static_cast<uint32_t>(row) - s * a.num_q), kvh = h / a.g, hg = h - kvh * a.g;
   const SeqInfo q = a.seqs[s];
-  const Axis ax = *a.axis;
-  // the pieces of the prefix part and of the own part: piece i of a part is
-  // CTA c1 + i's slot (1 where the item begins inside that CTA's range), or
-  // the part's own place if one CTA holds all its blocks
-  auto pieces = [&](long long u0, int nb, int &c1, int &np, int &s0) {
-    c1 = axis_cta(u0, ax);
-    if ((c1 + 1) * ax.per - u0 <= a.item_units) ++c1;  // that CTA's range holds none of its blocks
-    np = axis_cta(u0 + item_units(a, nb) - 1, ax) - c1 + 1;
-    s0 = u0 > c1 * ax.per;
-  };
-  int p_c1 = 0, p_n = 0, p_s0 = 0, o_c1 = 0, o_n = 0, o_s0 = 0;
-  const int p_r = q.prow + hg;
-  // the prefix part's tile in pre_o / pre_lse
-  const int64_t p_at = static_cast<int64_t>(q.pseq) * a.num_q + static_cast<int64_t>(kvh) * q.prows;
-  if (q.pnb > 0) pieces(q.pbase + static_cast<long long>(kvh) * item_units(a, q.pnb), q.pnb, p_c1, p_n, p_s0);
-  if (q.nb > 0) pieces(q.base + static_cast<long long>(kvh) * item_units(a, q.nb), q.nb, o_c1, o_n, o_s0);
-  if (q.fb == 0 && o_n == 1) mine = false;
-  const int n = mine ? p_n + o_n : 0;
-  // where piece i's log-sum-exp and columns 0 .. 3 are, and the distance to the next columns
-  auto piece = [&](int i, const float *&x, const float *&o) -> int {
-    const bool pre = i < p_n;
-    if (pre && p_n == 1) {
-      x = a.pre_lse + p_at + p_r;
-      o = a.pre_o + p_at * D + 4 * p_r;
-      return 4 * q.prows;
+  const long long per = a.axis->per;
+  // the pieces of the prefix part (0) and of the own part (1): piece i of a
+  // part is CTA c1 + i's slot (1 where the item begins inside that CTA's
+  // range), or the part's own place if one CTA holds all its blocks
+  int c1[2] = {0, 0}, np[2] = {0, 0}, s0[2] = {0, 0};
+#pragma unroll 1
+  for (int p = 0; p < 2; ++p) {
+    const int nb = p ? q.nb : q.pnb;
+    if (nb == 0) continue;
+    const int n = item_units(a, nb);
+    const long long u0 = (p ? q.base : q.pbase) + static_cast<long long>(kvh) * n;
+    int c = axis_cta(u0, per);
+    if ((c + 1) * per - u0 <= a.item_units) ++c;  // that CTA's range holds none of its blocks
+    const int m = axis_cta(u0 + n - 1, per) - c + 1, in = u0 > c * per;
+    if (p) {
+      c1[1] = c;
+      np[1] = m;
+      s0[1] = in;
+    } else {
+      c1[0] = c;
+      np[0] = m;
+      s0[0] = in;
     }
-    if (!pre && o_n == 1) {
-      x = a.own_lse + row;
-      o = a.own_o + row * D;
-      return 4;
-    }
-    const int k = pre ? i : i - p_n;
-    const int64_t slot =
-        (static_cast<int64_t>((pre ? p_c1 : o_c1) + k) * 2 + (k == 0 ? (pre ? p_s0 : o_s0) : 0)) * a.slot_rows;
-    const int r = pre ? p_r : hg;
-    x = a.cut_lse + slot + r;
-    o = a.cut_o + slot * D + 4 * r;
-    return 4 * a.slot_rows;
-  };
-  // 16 pieces at a time, each fetched by one of the row's lanes: their
-  // log-sum-exps first, then their columns by all the lanes
+  }
+  if (q.fb == 0 && np[1] == 1) mine = false;
+  const int n = mine ? np[0] + np[1] : 0;
+  const float4 *base = reinterpret_cast<const float4 *>(a.cut_o);
+  const int64_t p_at = static_cast<int64_t>(q.pseq) * a.num_q + static_cast<int64_t>(kvh) * q.prows;  // its tile
   float M = -INFINITY, W = 0.f;
   float4 acc[NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
   const int most = max(n, __shfl_xor_sync(0xffffffffu, n, 1));
+  // 16 pieces at a time, each fetched by one of the row's lanes: their
+  // log-sum-exps first, then their columns by all the lanes
 #pragma unroll 1
   for (int i0 = 0; i0 < most; i0 += 16) {
     // (past the row's pieces: its first one again, with no weight)
-    const float *x = nullptr, *o = a.pre_o;
-    int stride = 0;
+    const bool there = i0 + c0 < n;
+    const int i = there ? i0 + c0 : 0;
+    const bool pre = i < np[0];
+    int at = 0, stride = 0;
     float v = -INFINITY;
-    if (n > 0) stride = piece(i0 + c0 < n ? i0 + c0 : 0, x, o);
-    if (i0 + c0 < n) v = __ldcg(x);
+    if (n > 0) {
+      const float *x;
+      if (pre ? np[0] == 1 : np[1] == 1) {
+        const int64_t r = pre ? p_at : row;
+        at = static_cast<int>(reinterpret_cast<const float4 *>(pre ? a.pre_o : a.own_o) - base) +
+             static_cast<int>(r) * C4 + (pre ? q.prow + hg : 0);
+        stride = pre ? q.prows : 1;
+        x = (pre ? a.pre_lse + q.prow + hg : a.own_lse) + r;
+      } else {
+        const int k = pre ? i : i - np[0], r = pre ? q.prow + hg : hg;
+        const int slot = ((c1[pre ? 0 : 1] + k) * 2 + (k == 0 ? s0[pre ? 0 : 1] : 0)) * a.slot_rows;
+        at = slot * C4 + r;
+        stride = a.slot_rows;
+        x = a.cut_lse + slot + r;
+      }
+      if (there) v = __ldcg(x);
+    }
     float mn = fmaxf(M, v);
-#pragma unroll
+#pragma unroll 1
     for (int b = 2; b < 32; b <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, b));
-    const float f = M == mn ? 1.f : exp2f(M - mn);
-    const float w = v == -INFINITY ? 0.f : exp2f(v - mn);  // a NaN stays one
+    const float f = M == mn ? 1.f : ex2_approx(M - mn);
+    const float w = v == -INFINITY ? 0.f : ex2_approx(v - mn);  // a NaN stays one
     M = mn;
     float ws = w;
-#pragma unroll
+#pragma unroll 1
     for (int b = 2; b < 32; b <<= 1) ws += __shfl_xor_sync(0xffffffffu, ws, b);
     W = W * f + ws;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[j] = make_float4(acc[j].x * f, acc[j].y * f, acc[j].z * f, acc[j].w * f);
-    const int m = min(16, most - i0);
-    // no branch on the weights: the loads of eight pieces are in flight at once
-#pragma unroll 8
-    for (int i = 0; i < m; ++i) {
-      const int from = 2 * i + (lane & 1);
-      const float wi = __shfl_sync(0xffffffffu, w, from);
-      const float *oi = reinterpret_cast<const float *>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), from));
-      const int64_t st = __shfl_sync(0xffffffffu, stride, from);
+    // eight pieces' loads in flight at once
+#pragma unroll 1
+    for (int i8 = 0; i8 < min(16, most - i0); i8 += 8) {
+      float4 y[8][NJ];
+      float wi[8];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const float4 y = __ldcg(reinterpret_cast<const float4 *>(oi + (c0 + 16 * j) * st));
-        acc[j].x += wi * y.x;
-        acc[j].y += wi * y.y;
-        acc[j].z += wi * y.z;
-        acc[j].w += wi * y.w;
+      for (int k = 0; k < 8; ++k) {
+        const int from = 2 * (i8 + k) + (lane & 1);
+        wi[k] = __shfl_sync(0xffffffffu, w, from);
+        const int ai = __shfl_sync(0xffffffffu, at, from), st = __shfl_sync(0xffffffffu, stride, from);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) y[k][j] = __ldcg(base + ai + (c0 + 16 * j) * st);
       }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          acc[j].x += wi[k] * y[k][j].x;
+          acc[j].y += wi[k] * y[k][j].y;
+          acc[j].z += wi[k] * y[k][j].z;
+          acc[j].w += wi[k] * y[k][j].w;
+        }
     }
   }
   if (!mine) return;
