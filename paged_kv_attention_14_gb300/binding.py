@@ -80,6 +80,7 @@ class PaKvDesc(ctypes.Structure):
 
 class PaRopeDesc(ctypes.Structure):
     """``pa_rope_desc`` of include/pa.h (field order and types must match)."""
+    _keep = (None, None, None)  # the tensors whose addresses it holds (make_rope)
     _fields_ = [
         ("cos_sin", ctypes.c_void_p),
         ("max_position", ctypes.c_int32),
@@ -104,6 +105,8 @@ _lib = None
 def load(path: Optional[str] = None):
     """Load the library (once).  Raises if it is missing."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -291,42 +294,42 @@ def make_rope(cos_sin: torch.Tensor, rotary_dim: int = 0, interleaved: bool = Fa
     return r
 
 
-def _check_rope(desc: PaKvDesc, rope: PaRopeDesc):
+def _check_rope(desc: PaKvDesc, rope: PaRopeDesc, act: torch.dtype, d: int):
     """The norm weights against the descriptor: the activation type, one per dim of a head."""
-    act = _act(desc)
-    for t, name in zip(getattr(rope, "_keep", (None,) * 3)[1:], ("q_weight", "k_weight")):
-        if t is not None and (t.dtype not in act or t.shape[0] != desc.head_dim):
-            raise ValueError(f"{name} must hold head_dim elements of {act[0]}")
+    for t in rope._keep[1:]:
+        if t is not None and (t.dtype != act or t.shape[0] != d):
+            raise ValueError(f"q_weight and k_weight must hold head_dim elements of {act}")
 
 
-def _rows(t: Optional[torch.Tensor], desc: PaKvDesc, heads: int, tokens: int, name: str, dense: bool = False):
+def _rows(t: Optional[torch.Tensor], act: torch.dtype, tokens: int, heads: int, d: int, name: str,
+          dense: bool = False):
     """(address, elements from one token to the next) of ``[tokens, heads,
-    head_dim]`` activations whose tokens may lie apart (a slice of a
-    projection's output); (None, 0) for None."""
+    d]`` activations whose tokens may lie apart (a slice of a projection's
+    output); (None, 0) for None."""
     if t is None:
         return None, 0
-    if t.dtype not in _act(desc):
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {_act(desc)[0]}")
+    if t.dtype != act:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {act}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    d = desc.head_dim
-    if tuple(t.shape) != (tokens, heads, d):
+    if t.shape != (tokens, heads, d):
         raise ValueError(f"{name} must be [{tokens}, {heads}, {d}], got {list(t.shape)}")
     st, sh, se = t.stride()
     if tokens == 1:
         st = heads * d  # of one token any stride will do
-    if se != 1 or (heads > 1 and sh != d) or (dense and st != heads * d):
+    if se != 1 or (sh != d and heads > 1) or (dense and st != heads * d):
         raise ValueError(f"{name} must be contiguous" + ("" if dense else " within each token"))
     return t.data_ptr(), st
 
 
-def _one_device(stream, *tensors):
-    """The launches go to the current device: every tensor has to be there."""
-    dev = torch.cuda.current_device()
+def _launch_stream(stream, *tensors) -> int:
+    """The stream's handle.  The launches go to the current device: every
+    tensor has to be there."""
+    dev = torch._C._cuda_getDevice()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
-    return _stream(stream)
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def pa_qk_norm_rope(desc: PaKvDesc, rope: PaRopeDesc, q_out, k_out, q, k, positions, stream=None):
@@ -334,15 +337,16 @@ def pa_qk_norm_rope(desc: PaKvDesc, rope: PaRopeDesc, q_out, k_out, q, k, positi
     ``[T, Hkv, D]`` -> k_out (either pair may be None).  The inputs may be
     slices of one projection's output, the outputs are dense; an output may
     be its own input.  ``positions``: int32 ``[T]``."""
-    T = int(positions.shape[0])
-    _check_rope(desc, rope)
-    qp, qs = _rows(q, desc, desc.num_q_heads, T, "q")
-    kp, ks = _rows(k, desc, desc.num_kv_heads, T, "k")
-    qo, _ = _rows(q_out, desc, desc.num_q_heads, T, "q_out", dense=True)
-    ko, _ = _rows(k_out, desc, desc.num_kv_heads, T, "k_out", dense=True)
+    act, = _act(desc)
+    T, hq, hkv, d = positions.shape[0], desc.num_q_heads, desc.num_kv_heads, desc.head_dim
+    _check_rope(desc, rope, act, d)
+    qp, qs = _rows(q, act, T, hq, d, "q")
+    kp, ks = _rows(k, act, T, hkv, d, "k")
+    qo, _ = _rows(q_out, act, T, hq, d, "q_out", True)
+    ko, _ = _rows(k_out, act, T, hkv, d, "k_out", True)
+    st = _launch_stream(stream, positions, q, k, q_out, k_out, *rope._keep)
     _check(load().pa_qk_norm_rope(ctypes.byref(desc), ctypes.byref(rope), qo, ko, qp, qs, kp, ks,
-                                  _ptr(positions, _I32, "positions"), T,
-                                  _one_device(stream, positions, q, k, q_out, k_out, *getattr(rope, "_keep", ()))))
+                                  _ptr(positions, _I32, "positions"), T, st))
 
 
 def pa_rope_cache_write(desc: PaKvDesc, rope: PaRopeDesc, q_out, q, k, v, positions, k_cache, v_cache, slot_mapping,
@@ -350,27 +354,30 @@ def pa_rope_cache_write(desc: PaKvDesc, rope: PaRopeDesc, q_out, q, k, v, positi
     """pa_qk_norm_rope with k and v ``[T, Hkv, D]`` going to their cache slots:
     q -> q_out (both may be None), k normed and rotated, v as it is, both
     written at ``slot_mapping`` (int64 ``[T]``, negative: no row)."""
-    T = int(slot_mapping.shape[0])
-    _check_rope(desc, rope)
+    act, = _act(desc)
+    T, hq, hkv, d = slot_mapping.shape[0], desc.num_q_heads, desc.num_kv_heads, desc.head_dim
+    _check_rope(desc, rope, act, d)
     if positions.shape[0] != T:
         raise ValueError("positions and slot_mapping must have one entry per token")
-    qp, qs = _rows(q, desc, desc.num_q_heads, T, "q")
-    kp, ks = _rows(k, desc, desc.num_kv_heads, T, "k")
-    vp, vs = _rows(v, desc, desc.num_kv_heads, T, "v")
-    qo, _ = _rows(q_out, desc, desc.num_q_heads, T, "q_out", dense=True)
+    qp, qs = _rows(q, act, T, hq, d, "q")
+    kp, ks = _rows(k, act, T, hkv, d, "k")
+    vp, vs = _rows(v, act, T, hkv, d, "v")
+    qo, _ = _rows(q_out, act, T, hq, d, "q_out", True)
+    st = _launch_stream(stream, positions, q, k, v, q_out, k_cache, v_cache, slot_mapping, *rope._keep)
     _check(load().pa_rope_cache_write(ctypes.byref(desc), ctypes.byref(rope), qo, qp, qs, kp, ks, vp, vs,
                                       _ptr(positions, _I32, "positions"), _cache_ptr(k_cache, desc, "k_cache"),
                                       _cache_ptr(v_cache, desc, "v_cache"), _ptr(slot_mapping, _I64, "slot_mapping"),
-                                      T, _one_device(stream, positions, q, k, v, q_out, k_cache, v_cache,
-                                                     slot_mapping, *getattr(rope, "_keep", ()))))
+                                      T, st))
+
+
+#: element types a cache tensor of each descriptor type may have
+_CACHE_OF = {PA_KV_BF16: (torch.bfloat16,), PA_KV_F16: (torch.float16,),
+             PA_KV_FP8_E4M3: (torch.uint8, torch.float8_e4m3fn), PA_KV_FP8_E5M2: (torch.uint8, torch.float8_e5m2)}
 
 
 def _cache_ptr(t, desc: PaKvDesc, name: str):
     """The address of a cache of the descriptor's type and size."""
-    want = {PA_KV_BF16: (torch.bfloat16,), PA_KV_F16: (torch.float16,),
-            PA_KV_FP8_E4M3: (torch.uint8, torch.float8_e4m3fn),
-            PA_KV_FP8_E5M2: (torch.uint8, torch.float8_e5m2)}[desc.kv_dtype]
-    p = _ptr(t, want, name)
+    p = _ptr(t, _CACHE_OF[desc.kv_dtype], name)
     if t.numel() != desc.num_blocks * desc.num_kv_heads * 16 * desc.head_dim:
         raise ValueError(f"{name} must be [num_blocks, num_kv_heads, 16, head_dim]")
     return p
@@ -446,12 +453,12 @@ def pa_decode_shared(desc: PaKvDesc, out, q, k_cache, v_cache, block_tables, con
     S, G = int(context_lens.shape[0]), int(prefix_lens.shape[0])
     if group_start.shape[0] != G + 1:
         raise ValueError("group_start must have one entry more than prefix_lens")
-    heads = (S, desc.num_q_heads)
-    if tuple(q.shape) != (*heads, desc.head_dim) or out.shape != q.shape or block_tables.shape[0] != S or \
-            (lse is not None and tuple(lse.shape) != heads):
+    hq = desc.num_q_heads
+    if q.shape != (S, hq, desc.head_dim) or out.shape != q.shape or block_tables.shape[0] != S or \
+            (lse is not None and lse.shape != (S, hq)):
         raise ValueError("q and out must be [S, Hq, D], lse [S, Hq] and block_tables [S, max_blocks]")
-    st = _one_device(stream, q, k_cache, v_cache, block_tables, context_lens, group_start, prefix_lens, workspace,
-                     *(t for t in (out, lse) if t is not None and t.is_cuda))
+    st = _launch_stream(stream, q, k_cache, v_cache, block_tables, context_lens, group_start, prefix_lens, workspace,
+                        out if out.is_cuda else None, lse if lse is not None and lse.is_cuda else None)
     _check(load().pa_decode_shared(ctypes.byref(desc), _ptr(out, _F32, "out", host_ok=True),
                                    _ptr(lse, _F32, "lse", allow_none=True, host_ok=True), _ptr(q, _act(desc), "q"),
                                    _cache_ptr(k_cache, desc, "k_cache"), _cache_ptr(v_cache, desc, "v_cache"),

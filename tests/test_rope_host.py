@@ -95,12 +95,11 @@ def test_cache_write_arguments(lib, bad):
 
 def test_binding_refuses_what_it_would_misread():
     """Wrong shapes, strides, types and devices raise before the library is called."""
-    d = _desc()
     cpu = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
-        B._rows(cpu, d, 4, 3, "q")
+        B._rows(cpu, torch.bfloat16, 3, 4, 64, "q")
     with pytest.raises(TypeError, match="dtype"):
-        B._rows(cpu.half(), d, 4, 3, "q")
+        B._rows(cpu.half(), torch.bfloat16, 3, 4, 64, "q")
     with pytest.raises(ValueError, match="CUDA"):
         B.make_rope(torch.zeros(8, 64))
     with pytest.raises(ValueError, match="max_position"):
