@@ -20,10 +20,9 @@
 // Layout: a row belongs to D / 16 neighbouring lanes, each holding two
 // 16-byte chunks that rotate with each other (half split: chunk l and chunk
 // l + rd / 16), so a rotation never leaves its lane and the norm takes
-// log2(D / 16) shuffles.  A lane's HPT rows are consecutive heads of one
-// token: they share the lane's cosines, sines and position, and their loads
-// are all in flight before the first use.
+// log2(D / 16) shuffles.
 #include "pa_device.cuh"
+#include "pa_host_cache.h"
 #include "pa_internal.h"
 
 namespace pa {
@@ -49,10 +48,9 @@ struct RopeArgs {
   float k_scale, v_scale, eps;
   int num_q, num_kv;  // query heads (0: no queries), kv heads (0: no keys)
   int heads;          // rows of a token: num_q + num_kv (+ num_kv values)
-  int slices;         // ceil(heads / HPT)
   int max_position;
   int rd;
-  int64_t total;      // tokens * slices
+  int64_t total;      // rows (few tokens), tokens (many)
   int64_t num_slots;
   int checked;
   int32_t *err;
@@ -89,12 +87,136 @@ __device__ __forceinline__ uint2 encode8(const float (&f)[8], float s) {
   return make_uint2(r[0], r[1]);
 }
 
-// KVT: the cache type (its activation type is fp16 for kKvF16, else bf16);
-// APPEND: keys and values go to the cache.
-template <int D, int KVT, bool APPEND, bool INTER, int HPT>
+// A lane's share of a row: two chunks of 8 elements that rotate with each
+// other, ca and cb, and for half split the 8 frequencies they share, for
+// interleaved 4 of each.
+template <int D, bool INTER>
+struct Lane {
+  static constexpr int LPR = D / 16;  // lanes of a row
+  int ca, cb;
+  bool rot;  // half split: lanes past rd / 16 hold unrotated dims
+  __device__ __forceinline__ Lane(int l, int rd) {
+    const int nr = rd / 16;
+    rot = INTER || l < nr;
+    ca = INTER ? l : (l < nr ? l : 2 * l);
+    cb = INTER ? l + LPR : (l < nr ? l + nr : 2 * l + 1);
+  }
+  // the cosines and sines of a table row (1 and 0 past rd)
+  __device__ __forceinline__ void angles(const float *row, int rd, float (&cs)[8], float (&sn)[8]) const {
+    auto four = [&](float *dst, const float *src) { *reinterpret_cast<float4 *>(dst) = *reinterpret_cast<const float4 *>(src); };
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      cs[i] = 1.f;
+      sn[i] = 0.f;
+    }
+    if constexpr (INTER) {
+      if (ca * 8 < rd) {
+        four(cs, row + ca * 4);
+        four(sn, row + rd / 2 + ca * 4);
+      }
+      if (cb * 8 < rd) {
+        four(cs + 4, row + cb * 4);
+        four(sn + 4, row + rd / 2 + cb * 4);
+      }
+    } else if (rot) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        four(cs + i, row + ca * 8 + i);
+        four(sn + i, row + rd / 2 + ca * 8 + i);
+      }
+    }
+  }
+  __device__ __forceinline__ void rotate(float (&fa)[8], float (&fb)[8], const float (&cs)[8],
+                                         const float (&sn)[8]) const {
+    if constexpr (INTER) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float a0 = fa[2 * e], a1 = fa[2 * e + 1], b0 = fb[2 * e], b1 = fb[2 * e + 1];
+        fa[2 * e] = a0 * cs[e] - a1 * sn[e];
+        fa[2 * e + 1] = a1 * cs[e] + a0 * sn[e];
+        fb[2 * e] = b0 * cs[4 + e] - b1 * sn[4 + e];
+        fb[2 * e + 1] = b1 * cs[4 + e] + b0 * sn[4 + e];
+      }
+    } else if (rot) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x0 = fa[e], x1 = fb[e];
+        fa[e] = x0 * cs[e] - x1 * sn[e];
+        fb[e] = x1 * cs[e] + x0 * sn[e];
+      }
+    }
+  }
+};
+
+// rsqrt(mean square + eps) of a row over its lanes (all of the warp's lanes call it)
+template <int D>
+__device__ __forceinline__ float row_rsqrt(const float (&fa)[8], const float (&fb)[8], float eps) {
+  float ss = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) ss += fa[e] * fa[e] + fb[e] * fb[e];
+#pragma unroll
+  for (int o = 1; o < D / 16; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  return rsqrtf(ss * (1.f / D) + eps);
+}
+
+// A finished row to where it goes: q_out or k_out, or the cache row of the
+// token's slot (values as they came, xa and xb).
+template <int D, int KVT, bool APPEND>
+__device__ __forceinline__ void store_row(const RopeArgs &a, int64_t token, int h, int64_t slot, int ca, int cb,
+                                          const float (&fa)[8], const float (&fb)[8], const uint4 &xa,
+                                          const uint4 &xb) {
+  constexpr int ACT = KVT == kKvF16 ? kKvF16 : kKvBf16;
+  const bool is_q = h < a.num_q, is_v = APPEND && h >= a.num_q + a.num_kv;
+  if (!APPEND || is_q) {
+    uint16_t *dst = is_q ? a.q_out + (token * a.num_q + h) * D : a.k_out + (token * a.num_kv + h - a.num_q) * D;
+    reinterpret_cast<uint4 *>(dst)[ca] = pack8<ACT>(fa);
+    reinterpret_cast<uint4 *>(dst)[cb] = pack8<ACT>(fb);
+  } else if (slot >= 0) {
+    // cache row (slot / 16, kv head, slot % 16) of [num_blocks][num_kv_heads][16][D]
+    const int kvh = h - a.num_q - (is_v ? a.num_kv : 0);
+    const int64_t row = ((slot >> 4) * a.num_kv + kvh) * 16 + (slot & 15);
+    uint8_t *cache = is_v ? a.v_cache : a.k_cache;
+    if constexpr (kv16(KVT)) {
+      uint4 *dst = reinterpret_cast<uint4 *>(cache + row * (2 * D));
+      dst[ca] = is_v ? xa : pack8<ACT>(fa);  // values: bit copies
+      dst[cb] = is_v ? xb : pack8<ACT>(fb);
+    } else {
+      const float *hs = is_v ? a.v_scales : a.k_scales;
+      const float s = hs ? __ldg(hs + kvh) : (is_v ? a.v_scale : a.k_scale);
+      uint2 *dst = reinterpret_cast<uint2 *>(cache + row * D);
+      dst[ca] = encode8<KVT>(fa, s);
+      dst[cb] = encode8<KVT>(fb, s);
+    }
+  }
+}
+
+// A token's position, and its cache slot (-1: none); with checked indices
+// one out of range is reported and replaced by 0 or -1.
+__device__ __forceinline__ int position_of(const RopeArgs &a, int64_t token, bool report) {
+  const int pos = __ldg(a.positions + token);
+  if (a.checked && (pos < 0 || pos >= a.max_position)) {
+    if (report) report_error(a.err, nullptr, kErrBadIndex);
+    return 0;
+  }
+  return pos;
+}
+__device__ __forceinline__ int64_t slot_of(const RopeArgs &a, int64_t token, bool report) {
+  const int64_t slot = __ldg(a.slots + token);
+  if (a.checked && slot >= a.num_slots) {
+    if (report) report_error(a.err, nullptr, kErrBadIndex);
+    return -1;
+  }
+  return slot;
+}
+
+// The kernel of few tokens: a row per D / 16 lanes, one pass.  One token's
+// 40 rows take 2.1 us in a captured graph, the launch; 128 tokens of 48 heads
+// 2.9 us.  KVT: the cache type (its activation type is fp16 for kKvF16, else
+// bf16); APPEND: keys and values go to the cache.
+template <int D, int KVT, bool APPEND, bool INTER>
 __global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a) {
   constexpr int ACT = KVT == kKvF16 ? kKvF16 : kKvBf16;
-  constexpr int LPR = D / 16;  // lanes of a row
+  constexpr int LPR = D / 16;
   // a programmatic dependent launched after this one waits for these writes;
   // this one waits for the writes of the kernel before it
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -103,167 +225,233 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a) {
   const int l = threadIdx.x % LPR;
   // every lane stays for the shuffles; lanes past the end touch no memory
   const bool live = unit < a.total;
-  const int64_t token = live ? unit / a.slices : 0;
-  const int h0 = live ? static_cast<int>(unit - token * a.slices) * HPT : 0;
-  // this lane's chunks of 8 elements: ca and cb rotate with each other
-  const int nr = a.rd / 16;
-  const bool rot = INTER || l < nr;  // half split: lanes nr .. hold unrotated dims
-  const int ca = INTER ? l : (l < nr ? l : 2 * l);
-  const int cb = INTER ? l + LPR : (l < nr ? l + nr : 2 * l + 1);
-
-  // ---- every load first
-  uint4 xa[HPT], xb[HPT];
-#pragma unroll
-  for (int i = 0; i < HPT; ++i) {
-    const int h = h0 + i;
-    xa[i] = xb[i] = make_uint4(0, 0, 0, 0);
-    if (live && h < a.heads) {
-      const uint16_t *src;
-      if (h < a.num_q)
-        src = a.q + token * a.q_stride + static_cast<int64_t>(h) * D;
-      else if (!APPEND || h < a.num_q + a.num_kv)
-        src = a.k + token * a.k_stride + static_cast<int64_t>(h - a.num_q) * D;
-      else
-        src = a.v + token * a.v_stride + static_cast<int64_t>(h - a.num_q - a.num_kv) * D;
-      xa[i] = *reinterpret_cast<const uint4 *>(src + ca * 8);
-      xb[i] = *reinterpret_cast<const uint4 *>(src + cb * 8);
-    }
-  }
-  // cosines and sines: half split, 8 frequencies shared by both chunks;
-  // interleaved, 4 of each chunk (1 and 0 past rd)
+  const int64_t token = !live             ? 0
+                        : a.total >> 32 ? unit / a.heads
+                                        : static_cast<uint32_t>(unit) / static_cast<uint32_t>(a.heads);
+  const int h = live ? static_cast<int>(unit - token * a.heads) : 0;
+  const Lane<D, INTER> ln(l, a.rd);
+  const bool is_q = h < a.num_q, is_v = APPEND && h >= a.num_q + a.num_kv;
+  uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
   float cs[8], sn[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    cs[i] = 1.f;
-    sn[i] = 0.f;
-  }
   int64_t slot = -1;
   if (live) {
-    int pos = __ldg(a.positions + token);
-    if (a.checked && (pos < 0 || pos >= a.max_position)) {
-      if (l == 0) report_error(a.err, nullptr, kErrBadIndex);
-      pos = 0;
-    }
-    const float *row = a.table + static_cast<int64_t>(pos) * a.rd;
-    if constexpr (INTER) {
-      if (ca * 8 < a.rd) {
-        *reinterpret_cast<float4 *>(cs) = __ldg(reinterpret_cast<const float4 *>(row + ca * 4));
-        *reinterpret_cast<float4 *>(sn) = __ldg(reinterpret_cast<const float4 *>(row + a.rd / 2 + ca * 4));
-      }
-      if (cb * 8 < a.rd) {
-        *reinterpret_cast<float4 *>(cs + 4) = __ldg(reinterpret_cast<const float4 *>(row + cb * 4));
-        *reinterpret_cast<float4 *>(sn + 4) = __ldg(reinterpret_cast<const float4 *>(row + a.rd / 2 + cb * 4));
-      }
-    } else if (rot) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        *reinterpret_cast<float4 *>(cs + 4 * i) = __ldg(reinterpret_cast<const float4 *>(row + ca * 8) + i);
-        *reinterpret_cast<float4 *>(sn + 4 * i) = __ldg(reinterpret_cast<const float4 *>(row + a.rd / 2 + ca * 8) + i);
-      }
-    }
-    if constexpr (APPEND) {
-      slot = __ldg(a.slots + token);
-      if (a.checked && slot >= a.num_slots) {
-        if (l == 0) report_error(a.err, nullptr, kErrBadIndex);
-        slot = -1;
-      }
-    }
+    const uint16_t *src = is_q  ? a.q + token * a.q_stride + static_cast<int64_t>(h) * D
+                          : is_v ? a.v + token * a.v_stride + static_cast<int64_t>(h - a.num_q - a.num_kv) * D
+                                 : a.k + token * a.k_stride + static_cast<int64_t>(h - a.num_q) * D;
+    xa = reinterpret_cast<const uint4 *>(src)[ln.ca];
+    xb = reinterpret_cast<const uint4 *>(src)[ln.cb];
+    ln.angles(a.table + static_cast<int64_t>(position_of(a, token, l == 0)) * a.rd, a.rd, cs, sn);
+    if constexpr (APPEND) slot = slot_of(a, token, l == 0);
   }
-
-#pragma unroll
-  for (int i = 0; i < HPT; ++i) {
-    const int h = h0 + i;
-    const bool is_q = h < a.num_q;
-    const bool is_v = APPEND && h >= a.num_q + a.num_kv;
-    float fa[8], fb[8];
-    unpack8<ACT>(xa[i], fa);
-    unpack8<ACT>(xb[i], fb);
+  float fa[8], fb[8];
+  unpack8<ACT>(xa, fa);
+  unpack8<ACT>(xb, fb);
+  if (a.q_weight != nullptr || a.k_weight != nullptr) {  // the same for every lane: all reach the shuffles
+    const float r = row_rsqrt<D>(fa, fb, a.eps);
     const uint16_t *w = is_q ? a.q_weight : a.k_weight;
-    if (a.q_weight != nullptr || a.k_weight != nullptr) {  // the same for every lane: all reach the shuffles
-      float ss = 0.f;
+    if (w != nullptr && !is_v) {
+      float wa[8], wb[8];
+      unpack8<ACT>(__ldg(reinterpret_cast<const uint4 *>(w) + ln.ca), wa);
+      unpack8<ACT>(__ldg(reinterpret_cast<const uint4 *>(w) + ln.cb), wb);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss += fa[e] * fa[e] + fb[e] * fb[e];
-#pragma unroll
-      for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (w != nullptr && !is_v) {
-        const float r = rsqrtf(ss * (1.f / D) + a.eps);
-        float wa[8], wb[8];
-        unpack8<ACT>(__ldg(reinterpret_cast<const uint4 *>(w) + ca), wa);
-        unpack8<ACT>(__ldg(reinterpret_cast<const uint4 *>(w) + cb), wb);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          fa[e] *= r * wa[e];
-          fb[e] *= r * wb[e];
-        }
+      for (int e = 0; e < 8; ++e) {
+        fa[e] *= r * wa[e];
+        fb[e] *= r * wb[e];
       }
     }
-    if (!live || h >= a.heads) continue;
-    if (!is_v) {
-      if constexpr (INTER) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float a0 = fa[2 * e], a1 = fa[2 * e + 1], b0 = fb[2 * e], b1 = fb[2 * e + 1];
-          fa[2 * e] = a0 * cs[e] - a1 * sn[e];
-          fa[2 * e + 1] = a1 * cs[e] + a0 * sn[e];
-          fb[2 * e] = b0 * cs[4 + e] - b1 * sn[4 + e];
-          fb[2 * e + 1] = b1 * cs[4 + e] + b0 * sn[4 + e];
-        }
-      } else if (rot) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float x0 = fa[e], x1 = fb[e];
-          fa[e] = x0 * cs[e] - x1 * sn[e];
-          fb[e] = x1 * cs[e] + x0 * sn[e];
-        }
+  }
+  if (!live) return;
+  if (!is_v) ln.rotate(fa, fb, cs, sn);
+  store_row<D, KVT, APPEND>(a, token, h, slot, ln.ca, ln.cb, fa, fb, xa, xb);
+}
+
+// The kernel of many tokens, one persistent CTA per SM: a producer warp brings
+// the tokens' rows (one bulk copy each of its queries, keys and values, which
+// lie together) and their table rows into a ring of stages, 16 warps work
+// through a stage's rows, so that some 150 KB per SM are in flight whatever
+// registers the arithmetic takes.  16381 tokens of 32 q / 8 kv heads with
+// norms: the kernel above 89.4 us (3,840 GB/s), this one TBD.
+constexpr int kStreamWarps = 16;
+
+struct StreamPlan {
+  int tokens;      // of a stage
+  int stages;
+  int token_bytes; // a token's rows and table row
+  int blocks;      // stages of work
+  unsigned long long wait_ns;
+};
+
+template <int D, int KVT, bool APPEND, bool INTER>
+__global__ void __launch_bounds__((kStreamWarps + 1) * 32, 1) rope_stream_kernel(const RopeArgs a, const StreamPlan p) {
+  constexpr int ACT = KVT == kKvF16 ? kKvF16 : kKvBf16;
+  constexpr int LPR = D / 16;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ uint64_t full[16], empty[16];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kStreamWarps);
+    }
+    fence_mbar_init();
+  }
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int row_bytes = D * 2, q_bytes = a.num_q * row_bytes, kv_bytes = a.num_kv * row_bytes;
+  const int tab_at = a.heads * row_bytes;  // a token: q, k (and v) rows, then its table row
+  const int64_t num_tokens = a.total;
+  int st = 0;
+  uint32_t par = 0;
+  if (warp == kStreamWarps) {
+    // ---- producer: a lane per (token, part)
+    bool ok = true;
+    int issued = 0;
+    for (int b = blockIdx.x; b < p.blocks; b += gridDim.x) {
+      const int64_t t0 = static_cast<int64_t>(b) * p.tokens;
+      const int n = static_cast<int>(min(static_cast<int64_t>(p.tokens), num_tokens - t0));
+      const int i = lane >> 2, part = lane & 3;  // up to 8 tokens x (q, k, v, table)
+      int pos = 0;
+      if (i < n && part == 3) pos = position_of(a, t0 + i, true);
+      if (!mbar_wait(&empty[st], par ^ 1, p.wait_ns)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&full[st], n * p.token_bytes);
+      __syncwarp();
+      if (i < n) {
+        uint8_t *dst = ring + static_cast<size_t>(st) * p.tokens * p.token_bytes + i * p.token_bytes;
+        const int64_t t = t0 + i;
+        if (part == 0 && q_bytes) bulk_g2s(dst, a.q + t * a.q_stride, q_bytes, &full[st]);
+        if (part == 1 && kv_bytes) bulk_g2s(dst + q_bytes, a.k + t * a.k_stride, kv_bytes, &full[st]);
+        if (APPEND && part == 2) bulk_g2s(dst + q_bytes + kv_bytes, a.v + t * a.v_stride, kv_bytes, &full[st]);
+        if (part == 3) bulk_g2s(dst + tab_at, a.table + static_cast<int64_t>(pos) * a.rd, a.rd * 4, &full[st]);
+      }
+      ++issued;
+      if (++st == p.stages) {
+        st = 0;
+        par ^= 1;
       }
     }
-    if (!APPEND || is_q) {
-      uint16_t *dst = is_q ? a.q_out + (token * a.num_q + h) * D : a.k_out + (token * a.num_kv + h - a.num_q) * D;
-      reinterpret_cast<uint4 *>(dst)[ca] = pack8<ACT>(fa);
-      reinterpret_cast<uint4 *>(dst)[cb] = pack8<ACT>(fb);
-    } else if (slot >= 0) {
-      // cache row (slot / 16, kv head, slot % 16) of [num_blocks][num_kv_heads][16][D]
-      const int kvh = h - a.num_q - (is_v ? a.num_kv : 0);
-      const int64_t row = ((slot >> 4) * a.num_kv + kvh) * 16 + (slot & 15);
-      uint8_t *cache = is_v ? a.v_cache : a.k_cache;
-      if constexpr (kv16(KVT)) {
-        uint4 *dst = reinterpret_cast<uint4 *>(cache + row * (2 * D));
-        dst[ca] = is_v ? xa[i] : pack8<ACT>(fa);  // values: bit copies
-        dst[cb] = is_v ? xb[i] : pack8<ACT>(fb);
-      } else {
-        const float *hs = is_v ? a.v_scales : a.k_scales;
-        const float s = hs ? __ldg(hs + kvh) : (is_v ? a.v_scale : a.k_scale);
-        uint2 *dst = reinterpret_cast<uint2 *>(cache + row * D);
-        dst[ca] = encode8<KVT>(fa, s);
-        dst[cb] = encode8<KVT>(fb, s);
+    if (!ok) {
+      if (lane == 0) report_error(a.err, nullptr, kErrWaitTimeout);
+      // the copies already issued land before the CTA can exit
+      for (int k = 1; k <= min(issued, p.stages); ++k) {
+        const int s2 = st - k < 0 ? st - k + p.stages : st - k;
+        mbar_wait(&full[s2], st - k < 0 ? par ^ 1 : par, p.wait_ns);
       }
+    }
+    return;
+  }
+  // ---- consumers: a lane keeps its chunks, and with them its norm weights
+  const int l = threadIdx.x % LPR;
+  const Lane<D, INTER> ln(l, a.rd);
+  constexpr int ROWS = kStreamWarps * 32 / LPR;  // rows at once
+  for (int b = blockIdx.x; b < p.blocks; b += gridDim.x) {
+    const int64_t t0 = static_cast<int64_t>(b) * p.tokens;
+    const int n = static_cast<int>(min(static_cast<int64_t>(p.tokens), num_tokens - t0));
+    if (!mbar_wait(&full[st], par, p.wait_ns)) {
+      if (lane == 0) report_error(a.err, nullptr, kErrWaitTimeout);
+      return;
+    }
+    const uint8_t *stage = ring + static_cast<size_t>(st) * p.tokens * p.token_bytes;
+    const int rows = n * a.heads;
+    int i = (threadIdx.x / LPR) / a.heads, h = (threadIdx.x / LPR) - i * a.heads;
+    // (whole warps go round: every lane reaches the shuffles)
+    for (int r0 = (warp * 32) / LPR; r0 < rows; r0 += ROWS) {
+      const bool live = i < n;
+      const bool is_q = h < a.num_q, is_v = APPEND && h >= a.num_q + a.num_kv;
+      uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
+      const uint8_t *tok = stage + i * p.token_bytes;
+      if (live) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(tok + h * row_bytes);
+        xa = src[ln.ca];
+        xb = src[ln.cb];
+      }
+      float fa[8], fb[8];
+      unpack8<ACT>(xa, fa);
+      unpack8<ACT>(xb, fb);
+      if (a.q_weight != nullptr || a.k_weight != nullptr) {
+        const float r = row_rsqrt<D>(fa, fb, a.eps);
+        const uint16_t *w = is_q ? a.q_weight : a.k_weight;
+        if (w != nullptr && !is_v) {
+          float wa[8], wb[8];
+          unpack8<ACT>(__ldg(reinterpret_cast<const uint4 *>(w) + ln.ca), wa);
+          unpack8<ACT>(__ldg(reinterpret_cast<const uint4 *>(w) + ln.cb), wb);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            fa[e] *= r * wa[e];
+            fb[e] *= r * wb[e];
+          }
+        }
+      }
+      if (live) {
+        if (!is_v) {
+          float cs[8], sn[8];
+          ln.angles(reinterpret_cast<const float *>(tok + tab_at), a.rd, cs, sn);
+          ln.rotate(fa, fb, cs, sn);
+        }
+        int64_t slot = -1;
+        if (APPEND && !is_q) slot = slot_of(a, t0 + i, l == 0);
+        store_row<D, KVT, APPEND>(a, t0 + i, h, slot, ln.ca, ln.cb, fa, fb, xa, xb);
+      }
+      for (h += ROWS; h >= a.heads; h -= a.heads) ++i;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[st]);
+    if (++st == p.stages) {
+      st = 0;
+      par ^= 1;
     }
   }
 }
 
-using RopeKernel = void (*)(const RopeArgs);
+// The kernels of a call: of few and of many tokens.
+struct RopeKernels {
+  void (*few)(const RopeArgs);
+  void (*many)(const RopeArgs, const StreamPlan);
+};
 
-template <int D, int KVT, bool APPEND, int HPT>
-RopeKernel pick_inter(bool inter) {
-  return inter ? &rope_kernel<D, KVT, APPEND, true, HPT> : &rope_kernel<D, KVT, APPEND, false, HPT>;
+template <int D, int KVT, bool APPEND>
+RopeKernels pick_inter(bool inter) {
+  if (inter) return {&rope_kernel<D, KVT, APPEND, true>, &rope_stream_kernel<D, KVT, APPEND, true>};
+  return {&rope_kernel<D, KVT, APPEND, false>, &rope_stream_kernel<D, KVT, APPEND, false>};
 }
 
-template <int KVT, bool APPEND, int HPT>
-RopeKernel pick_dim(int d, bool inter) {
-  return d == 64 ? pick_inter<64, KVT, APPEND, HPT>(inter) : pick_inter<128, KVT, APPEND, HPT>(inter);
+template <int KVT, bool APPEND>
+RopeKernels pick_dim(int d, bool inter) {
+  return d == 64 ? pick_inter<64, KVT, APPEND>(inter) : pick_inter<128, KVT, APPEND>(inter);
 }
 
-template <int HPT>
-RopeKernel pick(const pa_kv_desc &d, bool append, bool inter) {
+RopeKernels pick(const pa_kv_desc &d, bool append, bool inter) {
   if (!append)  // the cache type only gives the activation type
-    return d.kv_dtype == PA_KV_F16 ? pick_dim<kKvF16, false, HPT>(d.head_dim, inter)
-                                   : pick_dim<kKvBf16, false, HPT>(d.head_dim, inter);
+    return d.kv_dtype == PA_KV_F16 ? pick_dim<kKvF16, false>(d.head_dim, inter)
+                                   : pick_dim<kKvBf16, false>(d.head_dim, inter);
   switch (d.kv_dtype) {
-    case PA_KV_F16: return pick_dim<kKvF16, true, HPT>(d.head_dim, inter);
-    case PA_KV_FP8_E4M3: return pick_dim<kKvFp8, true, HPT>(d.head_dim, inter);
-    case PA_KV_FP8_E5M2: return pick_dim<kKvE5M2, true, HPT>(d.head_dim, inter);
-    default: return pick_dim<kKvBf16, true, HPT>(d.head_dim, inter);
+    case PA_KV_F16: return pick_dim<kKvF16, true>(d.head_dim, inter);
+    case PA_KV_FP8_E4M3: return pick_dim<kKvFp8, true>(d.head_dim, inter);
+    case PA_KV_FP8_E5M2: return pick_dim<kKvE5M2, true>(d.head_dim, inter);
+    default: return pick_dim<kKvBf16, true>(d.head_dim, inter);
   }
+}
+
+// Many tokens: enough rows for a few rounds of the SMs' 16 warps, and a token
+// that leaves room for three stages (see kStreamRows).
+constexpr int64_t kStreamRows = 16384;
+
+bool plan_stream(const RopeArgs &a, int head_dim, int64_t num_tokens, StreamPlan *p) {
+  if (num_tokens * a.heads < kStreamRows) return false;
+  p->token_bytes = a.heads * head_dim * 2 + a.rd * 4;
+  const int room = 216 * 1024;
+  p->tokens = 49152 / p->token_bytes;
+  p->tokens = p->tokens < 1 ? 1 : p->tokens > 8 ? 8 : p->tokens;
+  p->stages = room / (p->tokens * p->token_bytes);
+  p->stages = p->stages > 16 ? 16 : p->stages;
+  const int64_t blocks = (num_tokens + p->tokens - 1) / p->tokens;
+  if (p->stages < 3 || blocks > 0x7fffffff) return false;
+  p->blocks = static_cast<int>(blocks);
+  p->wait_ns = test_hooks().wait_ns;
+  return true;
 }
 
 }  // namespace
@@ -302,22 +490,34 @@ cudaError_t launch_rope(const pa_kv_desc &d, const pa_rope_desc &r, void *q_out,
   a.num_slots = static_cast<int64_t>(d.num_blocks) * d.block_size;
   a.checked = d.check_indices;
   a.err = d.error_word;
-  const int hpt = 1;
-  a.slices = (a.heads + hpt - 1) / hpt;
-  a.total = static_cast<int64_t>(num_tokens) * a.slices;
-  const int threads = 256;
-  const int64_t blocks = (a.total * (d.head_dim / 16) + threads - 1) / threads;
+  const RopeKernels kern = pick(d, append, r.interleaved != 0);
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  const RopeKernel kern = pick<1>(d, append, r.interleaved != 0);
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  StreamPlan p;
+  if (plan_stream(a, d.head_dim, num_tokens, &p)) {
+    const size_t smem = static_cast<size_t>(p.stages) * p.tokens * p.token_bytes;
+    // (the limit is set for the largest ring once, not for every size)
+    if (prepare_kernel(reinterpret_cast<const void *>(kern.many), (kStreamWarps + 1) * 32, 216 * 1024) < 1)
+      return cudaErrorInvalidConfiguration;
+    a.total = num_tokens;
+    const int sms = device_sm_count();
+    cfg.gridDim = dim3(p.blocks < sms ? p.blocks : sms);
+    cfg.blockDim = dim3((kStreamWarps + 1) * 32);
+    cfg.dynamicSmemBytes = smem;
+    return cudaLaunchKernelEx(&cfg, kern.many, a, p);
+  }
+  a.total = static_cast<int64_t>(num_tokens) * a.heads;
+  const int threads = 256;
+  const int64_t blocks = (a.total * (d.head_dim / 16) + threads - 1) / threads;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(threads);
+  return cudaLaunchKernelEx(&cfg, kern.few, a);
 }
 
 }  // namespace pa
