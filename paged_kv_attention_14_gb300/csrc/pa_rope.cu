@@ -211,7 +211,7 @@ __device__ __forceinline__ int64_t slot_of(const RopeArgs &a, int64_t token, boo
 
 // The kernel of few tokens: a row per D / 16 lanes, one pass.  One token's
 // 40 rows take 2.1 us in a captured graph, the launch; 128 tokens of 48 heads
-// 2.9 us.  KVT: the cache type (its activation type is fp16 for kKvF16, else
+// 2.8 us.  KVT: the cache type (its activation type is fp16 for kKvF16, else
 // bf16); APPEND: keys and values go to the cache.
 template <int D, int KVT, bool APPEND, bool INTER>
 __global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a) {
@@ -267,11 +267,14 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a) {
 
 // The kernel of many tokens, one persistent CTA per SM: a producer warp brings
 // the tokens' rows (one bulk copy each of its queries, keys and values, which
-// lie together) and their table rows into a ring of stages, 16 warps work
-// through a stage's rows, so that some 150 KB per SM are in flight whatever
+// lie together) and their table rows into a ring of stages, and 20 warps work
+// through a stage's rows, so that some 200 KB per SM are in flight whatever
 // registers the arithmetic takes.  16381 tokens of 32 q / 8 kv heads with
-// norms: the kernel above 89.4 us (3,840 GB/s), this one TBD.
-constexpr int kStreamWarps = 16;
+// norms: the kernel above 77.8 us, this one 57.4 us (5,990 GB/s, 90% of the
+// measured copy rate) with 20 warps, 63.5 with 16, 60.3 with 28.  8192 tokens
+// of 40 q / 8 kv heads into an E4M3 cache: 55.3 and 42.6 us; there the exact
+// divisions by the scale still show.
+constexpr int kStreamWarps = 20;
 
 struct StreamPlan {
   int tokens;      // of a stage
@@ -435,16 +438,20 @@ RopeKernels pick(const pa_kv_desc &d, bool append, bool inter) {
   }
 }
 
-// Many tokens: enough rows for a few rounds of the SMs' 16 warps, and a token
-// that leaves room for three stages (see kStreamRows).
-constexpr int64_t kStreamRows = 16384;
+// The kernel of many tokens is taken from this many bytes of rows on.  2048
+// tokens of 48 heads (25 MB): 13.3 us against 13.9 us; 1024 (13 MB): 8.3
+// against 6.4 us.
+constexpr int64_t kStreamBytes = 20 << 20;
 
 bool plan_stream(const RopeArgs &a, int head_dim, int64_t num_tokens, StreamPlan *p) {
-  if (num_tokens * a.heads < kStreamRows) return false;
+  if (num_tokens * a.heads * head_dim * 2 < kStreamBytes) return false;
   p->token_bytes = a.heads * head_dim * 2 + a.rd * 4;
   const int room = 216 * 1024;
   p->tokens = 49152 / p->token_bytes;
   p->tokens = p->tokens < 1 ? 1 : p->tokens > 8 ? 8 : p->tokens;
+  // a stage's rows have to occupy the warps (8 tokens of 8 heads of 64: 12.5
+  // us against 4.0 us for 8000 tokens)
+  if (p->tokens * a.heads < kStreamWarps * 32 / (head_dim / 16)) return false;
   p->stages = room / (p->tokens * p->token_bytes);
   p->stages = p->stages > 16 ? 16 : p->stages;
   const int64_t blocks = (num_tokens + p->tokens - 1) / p->tokens;

@@ -150,6 +150,61 @@ def test_cache_write(T, hq, hkv, D, rd, kv, norm):
     assert torch.equal(kc[keep], kc0[keep])
 
 
+@pytest.mark.parametrize("kv", [B.PA_KV_BF16, B.PA_KV_F16, B.PA_KV_FP8_E4M3, B.PA_KV_FP8_E5M2])
+@pytest.mark.parametrize("T,hq,hkv,D,rd,inter,norm", [
+    (2701, 32, 8, 128, 128, False, "qk"), (1803, 40, 8, 128, 64, True, "q"), (5003, 24, 6, 64, 64, False, "k"),
+    (700, 128, 8, 128, 16, False, ""), (400, 256, 16, 128, 128, False, "qk")])
+def test_many_tokens(T, hq, hkv, D, rd, inter, norm, kv):
+    """Batches of 20 MB of rows and more, read through the ring of stages: an
+    odd last stage, packed and dense inputs, padding, one token per stage."""
+    c = Case(T, hq, hkv, D, rd, inter, norm, kv, seed=21, packed=T % 2 == 1)
+    qo, ko = c.outs()
+    B.pa_qk_norm_rope(c.desc, c.rope, qo, ko, c.q, c.k, c.pos)
+    c.check(qo, c.q, c.qw, "q")
+    c.check(ko, c.k, c.kw, "k")
+    slots = c.slots.clone()
+    slots[::5] = -1
+    kc0, vc0 = c.caches()
+    kc, vc, kc2, vc2 = kc0.clone(), vc0.clone(), kc0.clone(), vc0.clone()
+    q2 = torch.empty_like(qo)
+    c.write(kc, vc, q2, slots)
+    assert torch.equal(q2, qo)
+    # the kernel of few tokens writes the same bits
+    for lo in range(0, T, 64):
+        part = slice(lo, lo + 64)
+        B.pa_rope_cache_write(c.desc, c.rope, q2[part], c.q[part], c.k[part], c.v[part], c.pos[part], kc2, vc2,
+                              slots[part])
+    assert torch.equal(q2, qo)
+    assert torch.equal(kc.view(torch.uint8), kc2.view(torch.uint8))
+    assert torch.equal(vc.view(torch.uint8), vc2.view(torch.uint8))
+    # in place
+    q3, k3 = c.q.contiguous().clone(), c.k.contiguous().clone()
+    B.pa_qk_norm_rope(c.desc, c.rope, q3, k3, q3, k3, c.pos)
+    assert torch.equal(q3, qo) and torch.equal(k3, ko)
+
+
+def test_many_tokens_checked():
+    ew = torch.zeros(1, dtype=torch.int32, device=DEV)
+    c = Case(2500, 32, 8, 128, 128, False, "qk", error_word=ew, check_indices=True)
+    kc0, vc0 = c.caches()
+    kc, vc, qo = kc0.clone(), vc0.clone(), c.outs()[0]
+    c.write(kc, vc, qo)
+    assert int(ew) == 0
+    c.pos[1000], c.pos[2499] = -5, MAXP
+    slots = c.slots.clone()
+    slots[7] = c.nb * 16 + 3
+    kc2, vc2, qo2 = kc0.clone(), vc0.clone(), torch.empty_like(qo)
+    c.write(kc2, vc2, qo2, slots)
+    assert int(ew) == B.PA_DEVERR_BAD_INDEX
+    keep = torch.ones(2500, dtype=torch.bool, device=DEV)
+    keep[1000] = keep[2499] = False
+    assert torch.equal(qo2[keep], qo[keep])
+    keep[7] = False
+    at = c.slots[keep]
+    assert torch.equal(kc2[at // 16, :, at % 16], kc[at // 16, :, at % 16])
+    assert torch.equal(kc2[c.slots[7] // 16, :, c.slots[7] % 16], kc0[c.slots[7] // 16, :, c.slots[7] % 16])
+
+
 @pytest.mark.parametrize("kv", [B.PA_KV_FP8_E4M3, B.PA_KV_FP8_E5M2])
 def test_per_head_scales(kv):
     c = Case(40, 8, 4, 128, 128, False, "qk", kv, seed=9)
