@@ -166,7 +166,7 @@ cudaError_t launch_shared(const pa_kv_desc &d, float *out, float *lse, const voi
   cfg.dynamicSmemBytes = k.smem;
   e = cudaLaunchKernelExC(&cfg, k.fn, args);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(num_seqs) * d.num_q_heads + 3) / 4));
+  cfg.gridDim = dim3(static_cast<unsigned>(num_seqs), static_cast<unsigned>((d.num_q_heads + 1) / 2 * (d.head_dim / 64) + 1) / 2);
   cfg.blockDim = dim3(64);
   cfg.dynamicSmemBytes = 0;
   const void *join = d.head_dim == 64 ? reinterpret_cast<const void *>(&shd::shared_join_kernel<64>)

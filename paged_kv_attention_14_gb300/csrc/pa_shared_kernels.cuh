@@ -105,6 +105,8 @@ struct __align__(16) CtaStart {
 struct __align__(16) Axis {
   long long units;  // U
   long long per;    // units of a CTA
+  uint32_t magic;   // floor(2^32 / per), 0 if U does not fit 32 bits
+  uint32_t pad[3];
 };
 
 struct Args {
@@ -299,7 +301,10 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
   }
   const long long own = at[0], U = at[0] + at[1];  // the own parts' first unit, and the end
   const long long per = max(divide(U + a.ctas - 1, a.ctas), static_cast<long long>(a.item_units + BPT));
-  if (tid == 0) *a.axis = Axis{U, per};
+  if (tid == 0) {
+    const uint32_t magic = U >> 32 ? 0u : static_cast<uint32_t>(divide64(1LL << 32, per));
+    *a.axis = Axis{U, per, magic, {0, 0, 0}};
+  }
   __syncthreads();
   // each CTA's first item
 #pragma unroll 1
@@ -1333,70 +1338,65 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
 
 // --------------------------------------------------------------------- join
 
-// The CTA that holds unit u of the axis (called, not inlined: the join runs
-// once per launch, and what it costs most is fetching its instructions)
-static __device__ __noinline__ int axis_cta(long long u, long long per) { return static_cast<int>(divide(u, per)); }
+// The CTA that holds unit u of the axis.  With 32 bits the product's high word
+// is the quotient or one less.
+__device__ __forceinline__ int axis_cta(long long u, const Axis &x) {
+  if (x.magic == 0) return static_cast<int>(divide64(u, x.per));
+  const uint32_t n = static_cast<uint32_t>(u), d = static_cast<uint32_t>(x.per), q = __umulhi(n, x.magic);
+  return static_cast<int>(q + (n - q * d >= d ? 1u : 0u));
+}
 
-// Two rows (sequence, head) per warp, a row on the lanes of one parity, 16
-// bytes of it a lane: two neighbouring rows of a tile fill a 32-byte sector of
-// its [4 columns][row] parts.  Each row's pieces are weighed by their
-// log-sum-exps.  Rows that the attention wrote itself (one uncut part) are
-// left alone.  Places in the workspace are counted in 16 bytes from cut_o.
+// 64 columns of two rows (sequence, head) per warp, a row on the lanes of one
+// parity, 16 bytes of it a lane: two neighbouring rows of a tile fill a
+// 32-byte sector of its [4 columns][row] parts.  Each row's pieces are weighed
+// by their log-sum-exps.  Rows that the attention wrote itself (one uncut
+// part) are left alone.  What bounds it is latency, so the loads come in two
+// dependent rounds: the sequence's record, then 16 pieces' log-sum-exps and
+// columns at once.  Places in the workspace are counted in 16 bytes from cut_o.
 template <int D>
 __global__ void __launch_bounds__(64) shared_join_kernel(const __grid_constant__ Args a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_q;
-  int64_t row = (static_cast<int64_t>(blockIdx.x) * 2 + (threadIdx.x >> 5)) * 2 + (lane & 1);
+  const int s = blockIdx.x;
+  constexpr int C4 = D / 4, PARTS = D / 64;  // warps of a pair of rows
+  const int w0 = blockIdx.y * 2 + (threadIdx.x >> 5);
+  int h = w0 / PARTS * 2 + (lane & 1);
   // every lane stays for the shuffles
-  bool mine = row < rows;
-  if (!mine) row = rows - 1;
-  const int c0 = lane >> 1;  // this lane's columns: 4 (c0 + 16 j)
-  constexpr int NJ = D / 64, C4 = D / 4;
-  const uint32_t s = static_cast<uint32_t>(row) / static_cast<uint32_t>(a.num_q);
-  const int h = static_cast<int>(static_cast<uint32_t>(row) - s * a.num_q), kvh = h / a.g, hg = h - kvh * a.g;
+  bool mine = h < a.num_q;
+  if (!mine) h = a.num_q - 1;
+  const int64_t row = static_cast<int64_t>(s) * a.num_q + h;
+  const int l = lane >> 1, c0 = l + 16 * (w0 % PARTS);  // this lane's columns: 4 c0 ..
   const SeqInfo q = a.seqs[s];
-  const long long per = a.axis->per;
+  const Axis ax = *a.axis;
+  const int kvh = static_cast<int>(static_cast<uint32_t>(h) / static_cast<uint32_t>(a.g)), hg = h - kvh * a.g;
   // the pieces of the prefix part (0) and of the own part (1): piece i of a
   // part is CTA c1 + i's slot (1 where the item begins inside that CTA's
   // range), or the part's own place if one CTA holds all its blocks
-  int c1[2] = {0, 0}, np[2] = {0, 0}, s0[2] = {0, 0};
-#pragma unroll 1
+  int c1[2], np[2], s0[2];
+#pragma unroll
   for (int p = 0; p < 2; ++p) {
-    const int nb = p ? q.nb : q.pnb;
-    if (nb == 0) continue;
-    const int n = item_units(a, nb);
+    const int nb = p ? q.nb : q.pnb, n = nb + a.item_units;
     const long long u0 = (p ? q.base : q.pbase) + static_cast<long long>(kvh) * n;
-    int c = axis_cta(u0, per);
-    if ((c + 1) * per - u0 <= a.item_units) ++c;  // that CTA's range holds none of its blocks
-    const int m = axis_cta(u0 + n - 1, per) - c + 1, in = u0 > c * per;
-    if (p) {
-      c1[1] = c;
-      np[1] = m;
-      s0[1] = in;
-    } else {
-      c1[0] = c;
-      np[0] = m;
-      s0[0] = in;
-    }
+    int c = axis_cta(u0, ax);
+    if ((c + 1) * ax.per - u0 <= a.item_units) ++c;  // that CTA's range holds none of its blocks
+    c1[p] = c;
+    np[p] = nb > 0 ? axis_cta(u0 + n - 1, ax) - c + 1 : 0;
+    s0[p] = u0 > c * ax.per;
   }
   if (q.fb == 0 && np[1] == 1) mine = false;
   const int n = mine ? np[0] + np[1] : 0;
   const float4 *base = reinterpret_cast<const float4 *>(a.cut_o);
   const int64_t p_at = static_cast<int64_t>(q.pseq) * a.num_q + static_cast<int64_t>(kvh) * q.prows;  // its tile
   float M = -INFINITY, W = 0.f;
-  float4 acc[NJ];
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   const int most = max(n, __shfl_xor_sync(0xffffffffu, n, 1));
-  // 16 pieces at a time, each fetched by one of the row's lanes: their
-  // log-sum-exps first, then their columns by all the lanes
 #pragma unroll 1
   for (int i0 = 0; i0 < most; i0 += 16) {
-    // (past the row's pieces: its first one again, with no weight)
-    const bool there = i0 + c0 < n;
-    const int i = there ? i0 + c0 : 0;
+    // each of a row's 16 lanes finds a piece's place (past the row's pieces:
+    // the first one's again, with no weight)
+    const bool there = i0 + l < n;
+    const int i = there ? i0 + l : 0;
     const bool pre = i < np[0];
     int at = 0, stride = 0;
     float v = -INFINITY;
@@ -1417,49 +1417,40 @@ __global__ void __launch_bounds__(64) shared_join_kernel(const __grid_constant__
       }
       if (there) v = __ldcg(x);
     }
+    // all the pieces' columns
+    float4 y[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int from = 2 * k + (lane & 1);
+      const int ai = __shfl_sync(0xffffffffu, at, from), st = __shfl_sync(0xffffffffu, stride, from);
+      y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i0 + k < most) y[k] = __ldcg(base + ai + c0 * st);
+    }
     float mn = fmaxf(M, v);
-#pragma unroll 1
+#pragma unroll
     for (int b = 2; b < 32; b <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, b));
     const float f = M == mn ? 1.f : ex2_approx(M - mn);
     const float w = v == -INFINITY ? 0.f : ex2_approx(v - mn);  // a NaN stays one
     M = mn;
     float ws = w;
-#pragma unroll 1
+#pragma unroll
     for (int b = 2; b < 32; b <<= 1) ws += __shfl_xor_sync(0xffffffffu, ws, b);
     W = W * f + ws;
+    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[j] = make_float4(acc[j].x * f, acc[j].y * f, acc[j].z * f, acc[j].w * f);
-    // eight pieces' loads in flight at once
-#pragma unroll 1
-    for (int i8 = 0; i8 < min(16, most - i0); i8 += 8) {
-      float4 y[8][NJ];
-      float wi[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int from = 2 * (i8 + k) + (lane & 1);
-        wi[k] = __shfl_sync(0xffffffffu, w, from);
-        const int ai = __shfl_sync(0xffffffffu, at, from), st = __shfl_sync(0xffffffffu, stride, from);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) y[k][j] = __ldcg(base + ai + (c0 + 16 * j) * st);
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          acc[j].x += wi[k] * y[k][j].x;
-          acc[j].y += wi[k] * y[k][j].y;
-          acc[j].z += wi[k] * y[k][j].z;
-          acc[j].w += wi[k] * y[k][j].w;
-        }
+    for (int k = 0; k < 16; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, 2 * k + (lane & 1));
+      acc.x += wk * y[k].x;
+      acc.y += wk * y[k].y;
+      acc.z += wk * y[k].z;
+      acc.w += wk * y[k].w;
     }
   }
   if (!mine) return;
   const float inv = (a.v_scales ? __ldg(a.v_scales + kvh) : a.vscale) / W;
-#pragma unroll
-  for (int j = 0; j < NJ; ++j)
-    *reinterpret_cast<float4 *>(a.out + row * D + 4 * (c0 + 16 * j)) =
-        W == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                 : make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv);
+  *reinterpret_cast<float4 *>(a.out + row * D + 4 * c0) =
+      W == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+               : make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
   if (a.lse && c0 == 0) a.lse[row] = W == 0.f ? -INFINITY : (M + log2f(W)) * kLn2;
 }
 
