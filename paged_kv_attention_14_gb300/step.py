@@ -9,6 +9,12 @@ Batching Loop" in the "vllm.cpp ARCHITECTURE OVERVIEW" figure of "Building
 and Deploying vllm.cpp ..."; chunked prefill in the Engine core bullet of the
 vllm.cpp repository's "What's implemented").
 
+A step may also start from a layer's projections (``MixedStep.projected``):
+the norm of each head, the rotation and the cache write of all new tokens are
+then one launch (``pa_rope_cache_write``).  A decode batch whose sequences
+share prefixes may name its groups; its attention then reads each shared
+prefix once for its group (``pa_decode_shared``).
+
 This module only orders the library's calls on CUDA streams; every step of
 the computation runs in the library's kernels.  Decode and prefill read
 disjoint outputs and only read the cache, so after the write they may run
@@ -58,14 +64,20 @@ class MixedStep:
     pa_mixed_attention_append launch: the caller's new rows are then the
     decode sequences' tokens in sequence order followed by the prefill
     chunks' tokens in query order, and every chunk starts at a block
-    boundary."""
+    boundary.
+
+    With a ``shared_workspace`` (binding.decode_shared_workspace) a step may
+    be given ``groups``, (group_start, prefix_lens, max_group_size,
+    max_prefix_len) of binding.pa_decode_shared, and then runs its decode as
+    that call: beside the prefill in "streams" mode, before it otherwise."""
 
     MODES = ("fused", "streams", "serial")
 
     def __init__(self, desc: B.PaKvDesc, k_cache, v_cache, scale: float, *, decode_out=None, decode_lse=None,
                  workspace=None, max_context_len_decode: int = 0, prefill_out=None, prefill_lse=None,
                  max_q_len: int = 0, max_context_len_prefill: int = 0, mode: str = "fused",
-                 prefill_workspace=None, decode_append: bool = False, write_in_step: bool = False):
+                 prefill_workspace=None, decode_append: bool = False, write_in_step: bool = False,
+                 shared_workspace=None):
         if mode not in self.MODES:
             raise ValueError(f"mode must be one of {self.MODES}")
         self.desc = desc
@@ -76,6 +88,7 @@ class MixedStep:
         self.prefill_out, self.prefill_lse = prefill_out, prefill_lse
         self.max_q_len, self.max_context_len_prefill = int(max_q_len), int(max_context_len_prefill)
         self.prefill_workspace = prefill_workspace
+        self.shared_workspace = shared_workspace
         self.decode_append = bool(decode_append) and decode_out is not None and prefill_out is None
         self.write_in_step = bool(write_in_step)
         self._balanced = {}  # (prefill sequences, table width) -> the balanced prefill runs
@@ -99,6 +112,13 @@ class MixedStep:
     def decode(self, q, block_tables, context_lens, stream=None):
         B.pa_decode(self.desc, self.decode_out, q, self.k_cache, self.v_cache, block_tables, context_lens,
                     self.max_context_len_decode, self.scale, self.workspace, lse=self.decode_lse, stream=stream)
+
+    def decode_shared(self, q, block_tables, context_lens, groups, stream=None):
+        if self.shared_workspace is None:
+            raise ValueError("a step with groups needs a shared_workspace (binding.decode_shared_workspace)")
+        B.pa_decode_shared(self.desc, self.decode_out, q, self.k_cache, self.v_cache, block_tables, context_lens,
+                           self.max_context_len_decode, *groups, self.scale, self.shared_workspace,
+                           lse=self.decode_lse, stream=stream)
 
     def prefill(self, q, query_start_loc, block_tables, context_lens, stream=None):
         if self.prefill_workspace is not None:
@@ -138,15 +158,20 @@ class MixedStep:
             pf = (self.prefill_out, *pf_args, self.max_q_len, self.max_context_len_prefill, self.prefill_lse)
         return dec, pf
 
-    def attend(self, dec_args, pf_args):
+    def attend(self, dec_args, pf_args, groups=None):
         """Decode and prefill after a cache write already issued on the current stream."""
-        if self.mode == "fused" and self.prefill_balanced(pf_args):
+        if groups is None:
+            decode = self.decode
+        else:
+            def decode(q, block_tables, context_lens):
+                self.decode_shared(q, block_tables, context_lens, groups)
+        if self.mode == "fused" and groups is None and self.prefill_balanced(pf_args):
             # a few long prefill chunks: the balanced kernel on every SM, after the decode
             if dec_args is not None and self.decode_out is not None:
-                self.decode(*dec_args)
+                decode(*dec_args)
             self.prefill(*pf_args)
             return
-        if self.mode == "fused":
+        if self.mode == "fused" and groups is None:
             B.pa_mixed_attention(self.desc, self.k_cache, self.v_cache, self.scale, self.workspace,
                                  *self._mixed_parts(dec_args, pf_args))
             return
@@ -155,19 +180,45 @@ class MixedStep:
             self.ev_written.record(main)
             self.side.wait_event(self.ev_written)
             with torch.cuda.stream(self.side):
-                self.decode(*dec_args)
+                decode(*dec_args)
             self.ev_decoded.record(self.side)
             self.prefill(*pf_args)
             main.wait_event(self.ev_decoded)
             return
         if dec_args is not None and self.decode_out is not None:
-            self.decode(*dec_args)
+            decode(*dec_args)
         if pf_args is not None and self.prefill_out is not None:
             self.prefill(*pf_args)
 
-    def __call__(self, k_new, v_new, slot_mapping, dec_args=None, pf_args=None):
+    def projected(self, rope, q_rot, q, k, v, positions, slot_mapping, dec_args=None, pf_args=None, groups=None):
+        """One step from a layer's projections.  q [T, Hq, D], k and v
+        [T, Hkv, D] (views into one projection, say) of all new tokens: the
+        decode sequences' in sequence order, then the prefill chunks' in query
+        order.  They are normed and rotated by ``rope`` (binding.make_rope) at
+        ``positions`` [T]; q goes to ``q_rot`` [T, Hq, D], k and v into the
+        cache at ``slot_mapping`` [T] (a negative slot: not written).  dec_args:
+        (block_tables, context_lens); pf_args: (query_start_loc, block_tables,
+        context_lens)."""
+        n = 0
+        if dec_args is not None and self.decode_out is not None:
+            n = int(dec_args[1].shape[0])
+            if n > q.shape[0]:
+                raise ValueError(f"q has {q.shape[0]} rows for {n} decode sequences")
+            dec_args = (q_rot[:n], *dec_args)
+        if pf_args is not None and self.prefill_out is not None:
+            pf_args = (q_rot[n:], *pf_args)
+        B.pa_rope_cache_write(self.desc, rope, q_rot, q, k, v, positions, self.k_cache, self.v_cache, slot_mapping)
+        self.attend(dec_args, pf_args, groups)
+
+    def __call__(self, k_new, v_new, slot_mapping, dec_args=None, pf_args=None, groups=None):
         """dec_args: (q, block_tables, context_lens); pf_args: (q, query_start_loc,
-        block_tables, context_lens)."""
+        block_tables, context_lens); groups: the decode sequences' shared
+        prefixes (above)."""
+        if groups is not None:
+            if slot_mapping is not None and slot_mapping.numel() > 0:
+                B.pa_cache_write(self.desc, k_new, v_new, self.k_cache, self.v_cache, slot_mapping)
+            self.attend(dec_args, pf_args, groups)
+            return
         if self.decode_append and dec_args is not None and k_new is not None and \
                 k_new.shape[0] == dec_args[2].shape[0]:
             q, block_tables, context_lens = dec_args

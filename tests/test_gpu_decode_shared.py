@@ -16,7 +16,7 @@ import oracle
 import pa_helpers as H
 from paged_kv_attention_14_gb300 import binding as B
 from paged_kv_attention_14_gb300 import workloads as W
-from paged_kv_attention_14_gb300.step import GraphedStep
+from paged_kv_attention_14_gb300.step import GraphedStep, MixedStep
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -293,6 +293,39 @@ def test_graph_replay_with_other_lengths_and_two_streams_at_once():
     assert torch.equal(outs[1], want) and torch.equal(outs[2], want)
 
 
+@pytest.mark.parametrize("kv", [W.KV_BF16, W.KV_F16, W.KV_FP8])
+@pytest.mark.parametrize("scale", [-0.08, -1e-3, 0.0, 1e-39])
+def test_scales_of_either_sign_and_zero(scale, kv):
+    """Wide and narrow items.  A zero scale weighs every key alike."""
+    b = W.shared_prefix_decode(819, [24, 2], [528, 64], [37 * i % 90 + 1 for i in range(26)], 32, 8, 128, kv_dtype=kv,
+                               device=DEV)
+    b.scale = scale
+    _check(b, *_run(b, H.gpu_caches(b)), ocaches=H.oracle_caches(b), rows=[0, 5, 23, 24, 25])
+
+
+@pytest.mark.parametrize("kv", [W.KV_BF16, W.KV_FP8])
+@pytest.mark.parametrize("pairs,singles", [(256, 0), (256, 1), (600, 137)])
+def test_many_sequences_and_groups(pairs, singles, kv):
+    """More sequences, or groups, than one CTA plans from shared memory (512)."""
+    S = 2 * pairs + singles
+    b = W.shared_prefix_decode(820 + S, [2] * pairs + [1] * singles, [16 * (j % 4) for j in range(pairs)] + [0] * singles,
+                               [13 * i % 37 + 1 for i in range(S)], 8, 2, 128, kv_dtype=kv, device=DEV)
+    gs, pre, _, _ = _args(b)
+    out, lse = _run(b, H.gpu_caches(b))
+    _check(b, out, lse, ocaches=H.oracle_caches(b))
+    # the singles in no group: the same
+    out, lse = _run(b, H.gpu_caches(b), gs=gs[:pairs + 1], pre=pre[:pairs], max_group=2)
+    _check(b, out, lse, ocaches=H.oracle_caches(b))
+
+
+def test_many_empty_groups():
+    """700 groups of which only every tenth has sequences."""
+    b = W.shared_prefix_decode(821, [3] * 70, [48] * 70, [7 * i % 50 + 1 for i in range(210)], 8, 2, 64, device=DEV)
+    gs = torch.tensor([3 * ((i + 9) // 10) for i in range(701)], dtype=torch.int32, device=DEV)
+    pre = torch.full((700,), 48, dtype=torch.int32, device=DEV)
+    _check(b, *_run(b, H.gpu_caches(b), gs=gs, pre=pre))
+
+
 def test_output_in_pinned_host_memory():
     b = W.shared_prefix_decode(815, [4, 1], [64, 0], [9, 50, 1, 16, 33], 32, 8, 128, device=DEV)
     caches = H.gpu_caches(b)
@@ -355,3 +388,63 @@ def test_rotated_append_then_shared_decode():
                                 b.k_pool.cpu(), b.v_pool.cpu())
     assert np.array_equal(kc.view(torch.int16).cpu().numpy().view(np.uint16), ok)
     _check(b, out, lse, ocaches=(oracle.KV_BF16, ok, ov))
+
+
+@pytest.mark.parametrize("mode", ["fused", "streams", "serial"])
+@pytest.mark.parametrize("grouped", [True, False])
+def test_a_step_from_projections(mode, grouped):
+    """MixedStep.projected: decode sequences and prefill chunks, captured and replayed with other inputs."""
+    b = W.shared_prefix_decode(822, [5, 2], [160, 48], [9, 50, 1, 16, 33, 17, 100], 32, 8, 128, device=DEV)
+    p = W.random_prefill(823, [70, 1, 40], [70, 33, 100], 32, 8, 128, device=DEV, poison=True)
+    S, Tq, Hq, Hkv, D = 7, 111, 32, 8, 128
+    # one pool: the chunks' blocks behind the decode sequences'
+    kc, vc = (torch.cat([getattr(b, n), getattr(p, n)]) for n in ("k_pool", "v_pool"))
+    ptab = torch.where(p.block_tables_prefill >= 0, p.block_tables_prefill + b.num_blocks, p.block_tables_prefill)
+    d = B.make_desc(kc.shape[0], Hkv, Hq, D)
+    gs, pre, mg, mp = _args(b)
+    table = B.rope_table(512, D, 1e6, DEV)
+    rope = B.make_rope(table)
+    maxL = b.block_tables_decode.shape[1] * 16
+    n = b.context_lens_decode - 1
+    qsl, plen = p.query_start_loc.cpu(), p.context_lens_prefill.cpu()
+    pos = torch.cat([n.cpu()] + [torch.arange(int(plen[i]) - int(qsl[i + 1] - qsl[i]), int(plen[i])) for i in range(3)])
+    rows = torch.cat([b.block_tables_decode.cpu().gather(1, (n.cpu().long() // 16)[:, None])[:, 0]] + [
+        ptab.cpu()[i, pos[S + int(qsl[i]):S + int(qsl[i + 1])].long() // 16] for i in range(3)])
+    pos = pos.to(torch.int32)
+    slots = (rows.long() * 16 + pos.long() % 16).to(DEV)
+    pos = pos.to(DEV)
+    qkv = torch.zeros(S + Tq, (Hq + 2 * Hkv) * D, dtype=torch.bfloat16, device=DEV)
+    q, k, v = (qkv[:, lo * D:hi * D].view(-1, hi - lo, D) for lo, hi in ((0, Hq), (Hq, Hq + Hkv), (Hq + Hkv, 48)))
+    ws = B.mixed_workspace(d, S, maxL, DEV)
+    out, lse = torch.empty(S, Hq, D, device=DEV), torch.empty(S, Hq, device=DEV)
+    pout, plse = torch.empty(Tq, Hq, D, device=DEV), torch.empty(Tq, Hq, device=DEV)
+    step = MixedStep(d, kc, vc, b.scale, decode_out=out, decode_lse=lse, workspace=ws, max_context_len_decode=maxL,
+                     prefill_out=pout, prefill_lse=plse, max_q_len=70, max_context_len_prefill=100, mode=mode,
+                     shared_workspace=B.decode_shared_workspace(d, S, 2, mg) if grouped else None)
+    q_rot = torch.empty(S + Tq, Hq, D, dtype=torch.bfloat16, device=DEV)
+    groups = (gs, pre, mg, mp) if grouped else None
+
+    def issue():
+        step.projected(rope, q_rot, q, k, v, pos, slots, (b.block_tables_decode, b.context_lens_decode),
+                       (p.query_start_loc, ptab, p.context_lens_prefill), groups)
+
+    graph = GraphedStep(issue)
+    before = kc.cpu(), vc.cpu()
+    qkv.copy_(torch.randn(qkv.shape, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16))
+    graph()
+    k_rot = torch.empty(S + Tq, Hkv, D, dtype=torch.bfloat16, device=DEV)
+    want_q = torch.empty_like(q_rot)
+    B.pa_qk_norm_rope(d, rope, want_q, k_rot, q, k, pos)
+    assert torch.equal(want_q, q_rot)
+    ok, ov = oracle.cache_write(oracle.KV_BF16, 16, Hkv, D, k_rot.cpu(), v.contiguous().cpu(), slots.cpu(), *before)
+    assert np.array_equal(kc.view(torch.int16).cpu().numpy().view(np.uint16), ok)
+    b.q_decode = q_rot[:S]
+    b.num_blocks = kc.shape[0]
+    _check(b, out, lse, ocaches=(oracle.KV_BF16, ok, ov))
+    o, x = oracle.prefill(oracle.KV_BF16, 16, Hkv, Hq, D, q_rot[S:].cpu(), qsl, ok, ov, ptab.cpu(), plen, b.scale)
+    H.assert_close(pout.reshape(-1, D), o.reshape(-1, D), TOL, "prefill out")
+    H.assert_close(plse.reshape(-1), x.reshape(-1), LSE_TOL, "prefill lse")
+    if grouped:
+        step.shared_workspace = None
+        with pytest.raises(ValueError, match="shared_workspace"):
+            issue()
