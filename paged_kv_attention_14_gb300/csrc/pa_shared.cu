@@ -19,18 +19,11 @@ int tile_seqs_of(const pa_kv_desc &d, int32_t max_group_size) {
   return max_group_size < 1 ? 1 : max_group_size > cap ? cap : max_group_size;
 }
 
-// The cache as TMA sees it.  8-bit: rows of (block, kv head, token) triples, a
-// box is the 16 rows of one block and kv head as they are (they are widened).
-// 16-bit: the rows in groups of 8, each row in halves of 64 columns, a box is
-// a block's two groups as [group][half][8 rows][128 B] (128-byte swizzle),
-// one copy of 4 KB at head_dim 128 where plain rows would take one per half.
-bool make_map(CUtensorMap *map, const void *base, const pa_kv_desc &d) {
-  const bool kv8 = d.kv_dtype == PA_KV_FP8_E4M3 || d.kv_dtype == PA_KV_FP8_E5M2;
-  using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                     const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
-                                     CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                     CUtensorMapFloatOOBfill);
-  static EncodeTiledFn enc = [] {
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled() {
+  static const EncodeTiledFn enc = [] {
     void *p = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
@@ -38,6 +31,17 @@ bool make_map(CUtensorMap *map, const void *base, const pa_kv_desc &d) {
       p = nullptr;
     return reinterpret_cast<EncodeTiledFn>(p);
   }();
+  return enc;
+}
+
+// The cache as TMA sees it.  8-bit: rows of (block, kv head, token) triples, a
+// box is the 16 rows of one block and kv head as they are (they are widened).
+// 16-bit: the rows in groups of 8, each row in halves of 64 columns, a box is
+// a block's two groups as [group][half][8 rows][128 B] (128-byte swizzle),
+// one copy of 4 KB at head_dim 128 where plain rows would take one per half.
+bool make_map(CUtensorMap *map, const void *base, const pa_kv_desc &d) {
+  const bool kv8 = d.kv_dtype == PA_KV_FP8_E4M3 || d.kv_dtype == PA_KV_FP8_E5M2;
+  const EncodeTiledFn enc = encode_tiled();
   if (!enc) return false;
   thread_local MapCache<> cache;
   const MapKey key = map_key(base, d.num_blocks, d.num_kv_heads, d.head_dim, kv8);
@@ -61,6 +65,19 @@ bool make_map(CUtensorMap *map, const void *base, const pa_kv_desc &d) {
   if (r != CUDA_SUCCESS) return false;
   cache.put(key, *map);
   return true;
+}
+
+// Q: rows as [sequence][half][head][64 columns], a box is a half of one kv
+// head's rows of a sequence.
+bool make_q_map(CUtensorMap *map, const void *q, const pa_kv_desc &d, int32_t num_seqs) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t D = d.head_dim, Hq = d.num_q_heads;
+  const cuuint64_t dims[4] = {64, Hq, D / 64, static_cast<cuuint64_t>(num_seqs)}, strides[3] = {D * 2, 128, Hq * D * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(Hq / d.num_kv_heads), 1, 1}, estr[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(q), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 Layout layout(const pa_kv_desc &d, int32_t num_seqs, int32_t num_groups, int32_t max_group_size, int ctas) {
@@ -104,14 +121,16 @@ cudaError_t launch_shared(const pa_kv_desc &d, float *out, float *lse, const voi
   if (prepare_kernel(k.fn, k.threads, k.smem) < 1) return cudaErrorInvalidConfiguration;
   shd::Args a;
   memset(&a, 0, sizeof a);
-  if (!make_map(&a.kmap, k_cache, d) || !make_map(&a.vmap, v_cache, d)) return cudaErrorInvalidValue;
+  if (!make_map(&a.kmap, k_cache, d) || !make_map(&a.vmap, v_cache, d) ||
+      !make_q_map(&a.qmap, q, d, num_seqs))
+    return cudaErrorInvalidValue;
   a.ctas = device_sm_count();
-  a.item_units = b16 ? shd::kItemUnits16 : shd::kItemUnits8;
+  a.narrow_units = b16 ? shd::kNarrowUnits16 : shd::kNarrowUnits8;
+  a.wide_units = shd::kWideUnits;
   const Layout w = layout(d, num_seqs, num_groups, max_group_size, a.ctas);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   a.out = out;
   a.lse = lse;
-  a.q = static_cast<const uint16_t *>(q);
   a.block_tables = block_tables;
   a.context_lens = context_lens;
   a.group_start = group_start;
@@ -122,6 +141,7 @@ cudaError_t launch_shared(const pa_kv_desc &d, float *out, float *lse, const voi
   a.num_kv = d.num_kv_heads;
   a.num_q = d.num_q_heads;
   a.g = d.num_q_heads / d.num_kv_heads;
+  a.own_units = shd::is_narrow(a.g) ? a.narrow_units : a.wide_units;
   a.tile_seqs = tile_seqs_of(d, max_group_size);
   a.slot_rows = a.tile_seqs * a.g;
   const float ks = (!b16 && d.k_scale != 0.f) ? d.k_scale : 1.f;

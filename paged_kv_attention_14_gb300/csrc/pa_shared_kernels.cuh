@@ -62,12 +62,15 @@ constexpr int BPT = KT / 16;     // blocks of a step
 // more than this (log2 units), so that O is rarely rescaled
 constexpr float kRaise = 8.f;
 // An item costs its blocks and this many more (its Q tile, its first copies'
-// latency, its output), so the axis gives it that many extra units in front.
-// Measured best on batches of short own parts behind long prefixes: 6 with
-// 16-bit caches (four groups of 16 on 4096 tokens: 44.9 us with 2, 40.8 with
-// 6, 41.1 with 10), 4 with 8-bit ones, whose wide steps take longer (E4M3
-// batch of 128: 122 us with 2, 106 with 4, 112 with 6).
-constexpr int kItemUnits16 = 6, kItemUnits8 = 4;
+// latency, its output), so the axis gives it that many extra units in front;
+// a wide item, which all eight softmax warps finish together, far more than a
+// narrow one.  Measured, wide items' 4 / 10 / 16 / 24 / 32: an E4M3 batch with
+// 16 short wide items among long ones 100.3 / 95.7 / 87.1 / 85.2 / 87.9 us,
+// 64 sequences on one prompt of 16384 tokens (16-bit, from 6) 49.1 / 48.8 /
+// 48.4 / 46.9 / 47.9 us; narrow ones' 4 / 6 / 8 / 10: four groups of 16 on
+// 4096 tokens (16-bit) 39.4 / 37.3 / 36.3 / 38.0 us, the E4M3 batch 85.2 /
+// 84.2 / 86.3 / 87.9 us.
+constexpr int kNarrowUnits16 = 8, kNarrowUnits8 = 6, kWideUnits = 24;
 
 // One group's prefix on the axis.
 struct __align__(8) GroupInfo {
@@ -80,6 +83,7 @@ struct __align__(8) GroupInfo {
   int tiles;
   int row;         // a sequence whose table holds all of the prefix that is read
   int P;           // the prefix, whole blocks
+  int extra;       // units of an item besides its blocks
 };
 // One sequence: its own part, and its place in its group's prefix part.
 struct __align__(16) SeqInfo {
@@ -90,8 +94,9 @@ struct __align__(16) SeqInfo {
   int group;        // its group, -1: none
   long long pbase;  // first unit of its tile of the prefix (kv head 0)
   int pnb;          // blocks of the prefix, 0: none
-  int prow;         // first row in the tile
-  int prows;        // rows of the tile
+  short prow;       // first row in the tile
+  short prows;      // rows of the tile
+  int pextra;       // units of its items besides their blocks
   int pseq;         // first sequence of the tile
 };
 // Where a CTA's part of the axis begins.
@@ -112,9 +117,9 @@ struct __align__(16) Axis {
 struct Args {
   CUtensorMap kmap;
   CUtensorMap vmap;
+  CUtensorMap qmap;
   float *out;
   float *lse;
-  const uint16_t *q;
   const int32_t *block_tables;
   const int32_t *context_lens;
   const int32_t *group_start;
@@ -128,7 +133,7 @@ struct Args {
   int tile_seqs;  // sequences a tile may have
   int slot_rows;  // rows of a cut item's slot
   int ctas;       // CTAs that share the axis
-  int item_units;  // units of an item besides its blocks
+  int narrow_units, wide_units, own_units;  // units of an item besides its blocks
   float qscale;   // scale * k_scale * log2(e)
   float qscale0;  // scale * log2(e)
   float vscale;
@@ -164,8 +169,13 @@ __device__ __forceinline__ long long divide(long long n, long long d) {
   return divide64(n, d);
 }
 
+// A tile of at most 32 rows needs one quarter of the TMEM lanes, and so only
+// the two softmax warps of that quarter.  Such narrow items take the quarters
+// in turn, so that four of them can be in their softmax or output at once.
+__host__ __device__ __forceinline__ bool is_narrow(int rows) { return rows <= 32; }
+
 // Units of an item of nb blocks.
-__device__ __forceinline__ int item_units(const Args &a, int nb) { return nb > 0 ? nb + a.item_units : 0; }
+__device__ __forceinline__ int item_units(int nb, int extra) { return nb > 0 ? nb + extra : 0; }
 
 // Exclusive prefix sums of two values over the CTA's threads; total gets the sums.
 __device__ __forceinline__ void scan2(long long (&v)[2], long long (&total)[2], long long (*s_warp)[2]) {
@@ -247,6 +257,7 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
     const int t = max(1, (q.n + a.tile_seqs - 1) / a.tile_seqs);
     q.tile_seqs = max(1, (q.n + t - 1) / t);
     q.tiles = (q.n + q.tile_seqs - 1) / q.tile_seqs;
+    q.extra = is_narrow(q.tile_seqs * a.g) ? a.narrow_units : a.wide_units;
     groups[j] = q;
   }
   __syncthreads();
@@ -290,9 +301,9 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
     if (i < G) {
       const int nb = (groups[i].kend + 15) >> 4;
       groups[i].nb = nb;
-      v[0] = static_cast<long long>(item_units(a, nb)) * (groups[i].tiles * a.num_kv);
+      v[0] = static_cast<long long>(item_units(nb, groups[i].extra)) * (groups[i].tiles * a.num_kv);
     }
-    if (i < S) v[1] = static_cast<long long>(item_units(a, seqs[i].nb)) * a.num_kv;
+    if (i < S) v[1] = static_cast<long long>(item_units(seqs[i].nb, a.own_units)) * a.num_kv;
     scan2(v, sum, s_warp);
     if (i < G) groups[i].base = at[0] + v[0];
     if (i < S) seqs[i].base = at[1] + v[1];
@@ -300,7 +311,7 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
     at[1] += sum[1];
   }
   const long long own = at[0], U = at[0] + at[1];  // the own parts' first unit, and the end
-  const long long per = max(divide(U + a.ctas - 1, a.ctas), static_cast<long long>(a.item_units + BPT));
+  const long long per = max(divide(U + a.ctas - 1, a.ctas), static_cast<long long>((is_narrow(a.slot_rows) ? a.narrow_units : a.wide_units) + BPT));
   if (tid == 0) {
     const uint32_t magic = U >> 32 ? 0u : static_cast<uint32_t>(divide64(1LL << 32, per));
     *a.axis = Axis{U, per, magic, {0, 0, 0}};
@@ -314,7 +325,8 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
     if (u < U) {
       st.kind = u < own ? 0 : 1;
       st.idx = st.kind == 0 ? find_base(groups, G, u) : find_base(seqs, S, u - own);
-      const int n = item_units(a, st.kind == 0 ? groups[st.idx].nb : seqs[st.idx].nb);
+      const int n = st.kind == 0 ? item_units(groups[st.idx].nb, groups[st.idx].extra)
+                                 : item_units(seqs[st.idx].nb, a.own_units);
       const long long r = st.kind == 0 ? u - groups[st.idx].base : u - own - seqs[st.idx].base;
       st.sub = static_cast<int>(divide(r, n));
       st.off = static_cast<int>(r - static_cast<long long>(st.sub) * n);
@@ -330,9 +342,10 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
       const GroupInfo &gi = groups[q.group];
       const int i = s - gi.first, tile = i / gi.tile_seqs, t0 = tile * gi.tile_seqs;
       q.pnb = q.len > 0 ? gi.nb : 0;
-      q.pbase = gi.base + static_cast<long long>(tile * a.num_kv) * item_units(a, gi.nb);
-      q.prow = (i - t0) * a.g;
-      q.prows = min(gi.tile_seqs, gi.n - t0) * a.g;
+      q.pbase = gi.base + static_cast<long long>(tile * a.num_kv) * item_units(gi.nb, gi.extra);
+      q.prow = static_cast<short>((i - t0) * a.g);
+      q.prows = static_cast<short>(min(gi.tile_seqs, gi.n - t0) * a.g);
+      q.pextra = gi.extra;
       q.pseq = gi.first + t0;
     }
     a.seqs[s] = q;
@@ -438,7 +451,7 @@ struct Bars {
   uint64_t lk_full[C::NL], lk_empty[C::NL], lv_full[C::NL], lv_empty[C::NL];  // landed copies
   static constexpr int NW = C::KV8 ? C::NT : 1;
   uint64_t k_full[NW], k_empty[NW], v_full[NW], v_empty[NW];  // 8-bit: widened tiles
-  uint64_t q_full[2], q_empty[2], p_empty[2];
+  uint64_t q_land[2], q_full[2], q_empty[2], p_empty[2];  // q_land: Q's copies; q_full: ... in fp16 (8-bit caches)
   uint64_t sw_full[2], sn_full[4][2];    // scores of wide items, of narrow ones by quarter; [buffer]
   uint64_t ow_full[2], on_full[4];       // outputs (a quarter's items all use one buffer)
   uint64_t p_full[2][2], o_empty[2][2];  // [narrow][buffer]
@@ -446,10 +459,6 @@ struct Bars {
   uint32_t tmem;
 };
 
-// A tile of at most 32 rows needs one quarter of the TMEM lanes, and so only
-// the two softmax warps of that quarter.  Such narrow items take the quarters
-// in turn, so that four of them can be in their softmax or output at once.
-__device__ __forceinline__ bool is_narrow(int rows) { return rows <= 32; }
 // First lane of item number `item` of the CTA
 __device__ __forceinline__ int first_lane(int rows, uint32_t item) {
   return is_narrow(rows) ? static_cast<int>(item & 3) * 32 : 0;
@@ -518,6 +527,13 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int x, 
       : "memory");
 }
 
+// An L2 policy that keeps what is read: every CTA on a tile reads its queries.
+__device__ __forceinline__ uint64_t l2_evict_last_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
 // The copies of a piece's K and V blocks into the landing slots, a step at a
 // time; `fill` counts the slots of each filled so far.
 template <class C>
@@ -575,7 +591,7 @@ __device__ bool walk(const Args &a, uint8_t *smem, Bars<C> &bar, Item *iq, int l
   long long left = b1 - b0;
   CtaStart st = a.starts[me];
   if (left <= 0) st.kind = 2;
-  int kind = -1, items = 0, nb = 0, fb = 0, first = 0, n = 1, tile_seqs = 1, kend = 0, row = 0, whole_to = 0;
+  int kind = -1, items = 0, nb = 0, extra = 0, fb = 0, first = 0, n = 1, tile_seqs = 1, kend = 0, row = 0, whole_to = 0;
   const int32_t *table = nullptr;
   bool ok = true;
   Item it = {};
@@ -590,6 +606,7 @@ __device__ bool walk(const Args &a, uint8_t *smem, Bars<C> &bar, Item *iq, int l
           const GroupInfo &q = a.groups[st.idx];
           items = q.tiles * a.num_kv;
           nb = q.nb;
+          extra = q.extra;
           fb = 0;
           first = q.first;
           n = q.n;
@@ -601,6 +618,7 @@ __device__ bool walk(const Args &a, uint8_t *smem, Bars<C> &bar, Item *iq, int l
           const SeqInfo &q = a.seqs[st.idx];
           items = a.num_kv;
           nb = q.nb;
+          extra = a.own_units;
           fb = q.fb;
           first = row = st.idx;
           n = tile_seqs = 1;
@@ -615,10 +633,10 @@ __device__ bool walk(const Args &a, uint8_t *smem, Bars<C> &bar, Item *iq, int l
       it.rows = min(tile_seqs, n - tile * tile_seqs) * a.g;
       it.prefix = kind == 0;
       // the part of the item's units in this CTA's range, and its blocks
-      const int size = item_units(a, nb);
+      const int size = nb + extra;
       const int take = static_cast<int>(min(static_cast<long long>(size - st.off), left));
-      const int lo = max(st.off - a.item_units, 0);
-      it.nblk = max(st.off + take - a.item_units, 0) - lo;
+      const int lo = max(st.off - extra, 0);
+      it.nblk = max(st.off + take - extra, 0) - lo;
       it.key0 = (fb + lo) * 16;
       it.kend = min(kend, it.key0 + it.nblk * 16);  // a cut piece ends before the item
       it.lo = lo;
@@ -681,52 +699,49 @@ __device__ __forceinline__ bool take_item(const Args &a, Bars<C> &bar, const Ite
   return true;
 }
 
-// Where a Q tile's 16-byte column chunk `ch` lies: [half][row][128 B] with the
-// 128-byte swizzle; row R of it at + R * 128, chunk ch & 7 XORed with R & 7.
-template <class C>
-__device__ __forceinline__ uint8_t *q_column(uint8_t *smem, const QSlots &qs, int ch) {
-  return smem + C::OFF_Q + qs.slot * (C::QB / 2) + (ch >> 3) * (qs.big ? C::QHALF : C::QHALF / 2);
-}
-__device__ __forceinline__ int q_row(int R, int ch) { return R * 128 + (((ch & 7) ^ (R & 7)) << 4); }
-
-// Warp 3 (16-bit caches): Q tiles by asynchronous copies.
+// Warp 3: Q tiles, [half][row][128 B] with the 128-byte swizzle, a copy per
+// sequence and half (its g rows of the kv head).
 template <class C>
 __device__ bool load_q(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq, int lane) {
-  constexpr int CH = C::D / 8;    // 16-byte chunks of a row
-  constexpr int RPI = 32 / CH;    // rows a warp copies at once
-  const int ch = lane % CH;       // a lane keeps its column chunk
+  const uint64_t pol = l2_evict_last_policy();
   uint32_t taken = 0;
   QSlots qs;
   Item it;
+  bool ok = true;
 #pragma unroll 1
   for (;;) {
-    if (!take_item<C>(a, bar, iq, taken, it, lane)) return false;
-    if (it.end) return true;
+    ok = take_item<C>(a, bar, iq, taken, it, lane);
+    if (!ok || it.end) break;
     qs.next(it.rows);
-    if (qs.uses_slot(0) && !wait(&bar.q_empty[0], qs.parity(0) ^ 1, a.wait_ns)) return false;
-    if (qs.uses_slot(1) && !wait(&bar.q_empty[1], qs.parity(1) ^ 1, a.wait_ns)) return false;
-    uint8_t *col = q_column<C>(smem, qs, ch);
-    const uint16_t *src = a.q + (static_cast<int64_t>(it.seq0) * a.num_q + it.kvh * a.g) * C::D + ch * 8;
-#pragma unroll 1
-    for (int R0 = 0; R0 < it.rows; R0 += a.g, src += static_cast<int64_t>(a.num_q) * C::D)
-#pragma unroll 2
-      for (int r = lane / CH; r < a.g; r += RPI) cp_async16(col + q_row(R0 + r, ch), src + r * C::D, true);
-    cp_async_commit();
-    cp_async_wait<0>();
-    fence_proxy_async_smem();
-    __syncwarp();
+    ok = (!qs.uses_slot(0) || wait(&bar.q_empty[0], qs.parity(0) ^ 1, a.wait_ns)) &&
+         (!qs.uses_slot(1) || wait(&bar.q_empty[1], qs.parity(1) ^ 1, a.wait_ns));
+    if (!ok) break;
     if (lane == 0) {
-      if (qs.uses_slot(0)) mbar_arrive(&bar.q_full[0]);
-      if (qs.uses_slot(1)) mbar_arrive(&bar.q_full[1]);
+      mbar_arrive_expect_tx(&bar.q_land[qs.slot], it.rows * C::HALVES * 128);
+      if (qs.big) mbar_arrive(&bar.q_land[1]);
     }
+    __syncwarp();
+    const uint32_t half = qs.big ? C::QHALF : C::QHALF / 2;
+    uint8_t *to = smem + C::OFF_Q + qs.slot * (C::QB / 2) + (lane % C::HALVES) * half;
+#pragma unroll 1
+    for (int s = lane / C::HALVES; s * a.g < it.rows; s += 32 / C::HALVES)
+      tma_load_4d(to + s * a.g * 128, &a.qmap, 0, it.kvh * a.g, lane % C::HALVES, it.seq0 + s, &bar.q_land[qs.slot], pol);
+    __syncwarp();
     qs.done();
   }
+  // the copies land before the CTA exits, whatever became of the others
+  wait(&bar.q_land[0], qs.parity(0) ^ 1, a.wait_ns);
+  wait(&bar.q_land[1], qs.parity(1) ^ 1, a.wait_ns);
+  return ok;
 }
 
-// Warps 12-15 (8-bit caches): Q tiles in fp16, landed bytes to fp16 tiles, exact; V rows past
+// Warps 12-15 (8-bit caches): Q tiles to fp16, in place (a finite |q| beyond
+// fp16 does not fit and is reported); landed bytes to fp16 tiles, exact; V rows past
 // the piece's keys zeroed (they may hold anything, and 0 * NaN is NaN).  A
 // thread keeps its 16-byte column chunk and its row modulo 8, and with them
-// its places in the swizzled tile, over all its rows.
+// its places in the swizzled tile, over all its rows.  Of the two 16-byte
+// stores the threads of the second column half begin with the other one:
+// equal places of the halves lie in the same banks.
 template <class C>
 __device__ bool widen(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq, int ct, int lane) {
   constexpr int CPR = C::D / 16;                  // 16-byte chunks of a row of bytes
@@ -735,7 +750,8 @@ __device__ bool widen(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq
   constexpr int PER = KT / RSTEP;
   const int c = ct % CPR, r0 = ct / CPR, r7 = r0 & 7;
   const int put = (r0 >> 3) * C::GB + (c >> 2) * 1024 + r7 * 128;
-  const int x0 = ((2 * (c & 3)) ^ r7) << 4, x1 = ((2 * (c & 3) + 1) ^ r7) << 4;
+  const bool swap = (c & 4) != 0;
+  const int x0 = ((2 * (c & 3) + swap) ^ r7) << 4, x1 = ((2 * (c & 3) + !swap) ^ r7) << 4;
   uint32_t taken = 0, step = 0;
   QSlots qs;
   Item it;
@@ -743,50 +759,28 @@ __device__ bool widen(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq
   for (;;) {
     if (!take_item<C>(a, bar, iq, taken, it, lane)) return false;
     if (it.end) return true;
-    // the item's Q tile: bf16 queries become fp16 (a finite |q| beyond fp16
-    // does not fit and is reported)
     qs.next(it.rows);
-    if (qs.uses_slot(0) && !wait(&bar.q_empty[0], qs.parity(0) ^ 1, a.wait_ns)) return false;
-    if (qs.uses_slot(1) && !wait(&bar.q_empty[1], qs.parity(1) ^ 1, a.wait_ns)) return false;
+    if (qs.uses_slot(0) && !wait(&bar.q_land[0], qs.parity(0), a.wait_ns)) return false;
+    if (qs.uses_slot(1) && !wait(&bar.q_land[1], qs.parity(1), a.wait_ns)) return false;
     {
-      constexpr int QCH = C::D / 8, RPI = C::NCONV * 32 / QCH;
-      const int ch = ct % QCH;
-      uint8_t *col = q_column<C>(smem, qs, ch);
-      const uint16_t *src = a.q + (static_cast<int64_t>(it.seq0) * a.num_q + it.kvh * a.g) * C::D + ch * 8;
-      int R = ct / QCH, sq = R / a.g, hd = R - sq * a.g;
+      constexpr int CH = C::D / 8, RPI = C::NCONV * 32 / CH;  // 16-byte chunks of a row; rows at once
+      const int half = qs.big ? C::QHALF : C::QHALF / 2;
+      uint8_t *at = smem + C::OFF_Q + qs.slot * (C::QB / 2) + (ct % CH >> 3) * half + (ct % CH & 7) * 16;
       float big = 0.f;
-#pragma unroll 1
-      while (R < it.rows) {
-        constexpr int ILP = 4;
-        uint4 x[ILP];
-        int at[ILP];
+#pragma unroll 2
+      for (int R = ct / CH; R < it.rows; R += RPI) {
+        uint4 *p = reinterpret_cast<uint4 *>(at + R * 128);  // (any order: the swizzle stays as it is)
+        const uint4 x = *p;
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t o[4];
 #pragma unroll
-        for (int k = 0; k < ILP; ++k) {
-          at[k] = R < it.rows ? q_row(R, ch) : -1;
-          if (at[k] >= 0)
-            x[k] = __ldg(reinterpret_cast<const uint4 *>(src + (static_cast<int64_t>(sq) * a.num_q + hd) * C::D));
-          R += RPI;
-          hd += RPI;
-#pragma unroll 1
-          while (hd >= a.g) {
-            hd -= a.g;
-            ++sq;
-          }
+        for (int e = 0; e < 4; ++e) {
+          const float f0 = bf16lo(w[e]), f1 = bf16hi(w[e]);
+          const float f = fmaxf(fabsf(f0), fabsf(f1));
+          if (f <= FLT_MAX) big = fmaxf(big, f);
+          o[e] = pack_f16x2(f0, f1);
         }
-#pragma unroll
-        for (int k = 0; k < ILP; ++k) {
-          if (at[k] < 0) continue;
-          const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-          uint32_t o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float f0 = bf16lo(w[e]), f1 = bf16hi(w[e]);
-            const float f = fmaxf(fabsf(f0), fabsf(f1));
-            if (f <= FLT_MAX) big = fmaxf(big, f);
-            o[e] = pack_f16x2(f0, f1);
-          }
-          *reinterpret_cast<uint4 *>(col + at[k]) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
+        *p = make_uint4(o[0], o[1], o[2], o[3]);
       }
       if (big >= 65520.f) report_error(a.err, nullptr, kErrFp16Range);
       fence_proxy_async_smem();
@@ -804,8 +798,8 @@ __device__ bool widen(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq
       const uint32_t ls = step % C::NL, lp = (step / C::NL) & 1, ts = step % C::NT, tp = ((step / C::NT) & 1) ^ 1;
 #pragma unroll 1
       for (int v = 0; v < 2; ++v) {
-        if (!wait(v ? &bar.lv_full[ls] : &bar.lk_full[ls], lp, a.wait_ns)) return false;
         if (!wait(v ? &bar.v_empty[ts] : &bar.k_empty[ts], tp, a.wait_ns)) return false;
+        if (!wait(v ? &bar.lv_full[ls] : &bar.lk_full[ls], lp, a.wait_ns)) return false;
         const uint8_t *src = smem + (v ? C::OFF_LV : C::OFF_LK) + ls * C::LB + ct * 16;
         uint8_t *dst = smem + (v ? C::OFF_V : C::OFF_K) + ts * C::TB + put;
         const int zero = v ? keep : KT;  // rows from here on become zero
@@ -818,7 +812,8 @@ __device__ bool widen(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq
           for (int k = 0; k < ILP; ++k) x[k] = *reinterpret_cast<const uint4 *>(src + (k0 + k) * RSTEP * C::D);
 #pragma unroll
           for (int k = 0; k < ILP; ++k) {
-            uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            uint32_t w[4] = {swap ? x[k].z : x[k].x, swap ? x[k].w : x[k].y, swap ? x[k].x : x[k].z,
+                             swap ? x[k].y : x[k].w};
             if (r0 + (k0 + k) * RSTEP >= zero) w[0] = w[1] = w[2] = w[3] = 0;  // the byte 0 is +0
             uint32_t o[8];
 #pragma unroll
@@ -894,6 +889,7 @@ template <class C>
 __device__ bool issue_qk(const Args &a, uint32_t sbase, uint32_t tmem, Bars<C> &bar, const Item *iq, int lane) {
   // 16-bit caches: the landed tiles feed the products
   uint64_t *k_full = C::KV8 ? bar.k_full : bar.lk_full, *k_empty = C::KV8 ? bar.k_empty : bar.lk_empty;
+  uint64_t *q_full = C::KV8 ? bar.q_full : bar.q_land;
   uint32_t taken = 0, k = 0;
   QSlots qs;
   Item it;
@@ -909,8 +905,8 @@ __device__ bool issue_qk(const Args &a, uint32_t sbase, uint32_t tmem, Bars<C> &
     const uint32_t qd0 = uniform(
         desc_low(sbase + C::OFF_Q + qs.slot * (C::QB / 2) - first_lane(it.rows, taken - 1) * 128, 16));
     const uint32_t qd1 = uniform(qd0 + (qhalf >> 4));  // the second column half
-    if (qs.uses_slot(0) && !wait(&bar.q_full[0], qs.parity(0), a.wait_ns)) return false;
-    if (qs.uses_slot(1) && !wait(&bar.q_full[1], qs.parity(1), a.wait_ns)) return false;
+    if (qs.uses_slot(0) && !wait(&q_full[0], qs.parity(0), a.wait_ns)) return false;
+    if (qs.uses_slot(1) && !wait(&q_full[1], qs.parity(1), a.wait_ns)) return false;
     uint64_t *s_full = is_narrow(it.rows) ? bar.sn_full[(taken - 1) & 3] : bar.sw_full;
 #pragma unroll 1
     for (int b = 0; b < it.nblk; b += BPT, ++k) {
@@ -1255,7 +1251,7 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
   if (threadIdx.x == 0) {
     for (int i = 0; i < NIQ; ++i) {
       mbar_init(&bar.iq_full[i], 1);
-      mbar_init(&bar.iq_empty[i], C::KV8 ? 1 + 1 + 8 + C::NCONV : 1 + 1 + 1 + 8);  // the warps that take items
+      mbar_init(&bar.iq_empty[i], 1 + 1 + 1 + 8 + C::NCONV);  // the warps that take items
     }
     for (int i = 0; i < C::NL; ++i) {
       mbar_init(&bar.lk_full[i], 1);
@@ -1270,6 +1266,7 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
       mbar_init(&bar.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.q_land[i], 1);
       mbar_init(&bar.q_full[i], C::KV8 ? C::NCONV : 1);
       mbar_init(&bar.q_empty[i], 1);
       mbar_init(&bar.sw_full[i], 1);
@@ -1304,7 +1301,7 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
   } else if (warp == 2) {
     ok = issue_pv<C>(a, smem_u32(smem), tmem, bar, iq, lane);
   } else if (warp == 3) {
-    if constexpr (!C::KV8) ok = load_q<C>(a, smem, bar, iq, lane);
+    ok = load_q<C>(a, smem, bar, iq, lane);
   } else if (warp < 12) {
     const int h = (warp - 4) >> 2;
     Softmax<C> sm{a,
@@ -1376,10 +1373,10 @@ __global__ void __launch_bounds__(64) shared_join_kernel(const __grid_constant__
   int c1[2], np[2], s0[2];
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
-    const int nb = p ? q.nb : q.pnb, n = nb + a.item_units;
+    const int nb = p ? q.nb : q.pnb, extra = p ? a.own_units : q.pextra, n = nb + extra;
     const long long u0 = (p ? q.base : q.pbase) + static_cast<long long>(kvh) * n;
     int c = axis_cta(u0, ax);
-    if ((c + 1) * ax.per - u0 <= a.item_units) ++c;  // that CTA's range holds none of its blocks
+    if ((c + 1) * ax.per - u0 <= extra) ++c;  // that CTA's range holds none of its blocks
     c1[p] = c;
     np[p] = nb > 0 ? axis_cta(u0 + n - 1, ax) - c + 1 : 0;
     s0[p] = u0 > c * ax.per;

@@ -347,6 +347,43 @@ def test_queries_beyond_fp16_of_an_8bit_cache_are_reported():
     assert int(ew) == B.PA_DEVERR_FP16_RANGE
 
 
+@pytest.mark.parametrize("kv", [W.KV_FP8, W.KV_FP8_E5M2])
+def test_every_finite_byte_of_an_8bit_cache(kv):
+    """K and V of all the type's finite values, its subnormals among them.
+    With the largest one, m, the scale is 1 / (4 m): the bytes' mean magnitude
+    is some 0.13 m (E4M3; E5M2: less), so scale * sum |q k| is about 3, less
+    than the tolerance's 7.  The output is compared in units of m."""
+    b = W.shared_prefix_decode(824, [3, 1], [256, 0], [9, 300, 1, 40], 8, 2, 128, kv_dtype=kv, device=DEV, poison=False)
+    t = torch.float8_e4m3fn if kv == W.KV_FP8 else torch.float8_e5m2
+    val = torch.arange(256, dtype=torch.uint8).view(t).float()
+    finite = torch.isfinite(val)
+    top = float(val[finite].max())
+    good = torch.arange(256, dtype=torch.uint8)[finite]
+    g = torch.Generator().manual_seed(9)
+    kc, vc = (good[torch.randint(0, len(good), tuple(b.k_pool.shape), generator=g)] for _ in range(2))
+    b.k_scale, b.v_scale, b.scale = 1.0, 1.0, 0.25 / top
+    out, lse = _run(b, (kc.to(DEV), vc.to(DEV)))
+    code = H.oracle_caches(b)[0]
+    o, x = H.oracle_decode(b, ocaches=(code, kc.numpy(), vc.numpy()))
+    H.assert_close(out / top, o / top, TOL, "out")
+    H.assert_close(lse, x, LSE_TOL, "lse")
+
+
+@pytest.mark.parametrize("kv", [W.KV_FP8, W.KV_FP8_E5M2])
+def test_nan_bytes_of_an_8bit_cache_reach_their_readers_only(kv):
+    b = W.shared_prefix_decode(825, [3, 1], [256, 0], [9, 300, 1, 40], 8, 2, 128, kv_dtype=kv, device=DEV, poison=False)
+    caches = H.gpu_caches(b)
+    good, _ = _run(b, caches)
+    blk = int(b.block_tables_decode[1, 17])  # of sequence 1's own part
+    for which, byte in ((0, 0x7F), (1, 0xFF)):
+        c = [x.clone() for x in caches]
+        c[which][blk, 1, 3, 77] = byte
+        out, _ = _run(b, c)
+        bad = torch.zeros(4, 8, 128, dtype=torch.bool, device=DEV)
+        bad[1, 4:, slice(None) if which == 0 else 77] = True
+        assert torch.isnan(out[bad]).all() and torch.equal(out[~bad], good[~bad])
+
+
 def test_misuse_of_the_binding_is_refused():
     b = W.shared_prefix_decode(817, [3], [32], [5, 6, 7], 8, 2, 128, device=DEV)
     caches = H.gpu_caches(b)
