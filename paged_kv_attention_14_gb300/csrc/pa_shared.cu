@@ -68,13 +68,13 @@ bool make_map(CUtensorMap *map, const void *base, const pa_kv_desc &d) {
 }
 
 // Q: rows as [sequence][half][head][64 columns], a box is a half of one kv
-// head's rows of a sequence.
-bool make_q_map(CUtensorMap *map, const void *q, const pa_kv_desc &d, int32_t num_seqs) {
+// head's rows of `seqs` sequences, [sequence][head][128 B].
+bool make_q_map(CUtensorMap *map, const void *q, const pa_kv_desc &d, int32_t num_seqs, uint32_t seqs) {
   const EncodeTiledFn enc = encode_tiled();
   if (!enc) return false;
   const cuuint64_t D = d.head_dim, Hq = d.num_q_heads;
   const cuuint64_t dims[4] = {64, Hq, D / 64, static_cast<cuuint64_t>(num_seqs)}, strides[3] = {D * 2, 128, Hq * D * 2};
-  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(Hq / d.num_kv_heads), 1, 1}, estr[4] = {1, 1, 1, 1};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(Hq / d.num_kv_heads), 1, seqs}, estr[4] = {1, 1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(q), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -121,8 +121,10 @@ cudaError_t launch_shared(const pa_kv_desc &d, float *out, float *lse, const voi
   if (prepare_kernel(k.fn, k.threads, k.smem) < 1) return cudaErrorInvalidConfiguration;
   shd::Args a;
   memset(&a, 0, sizeof a);
+  const int seqs = tile_seqs_of(d, max_group_size);
   if (!make_map(&a.kmap, k_cache, d) || !make_map(&a.vmap, v_cache, d) ||
-      !make_q_map(&a.qmap, q, d, num_seqs))
+      !make_q_map(&a.qmap, q, d, num_seqs, 1) ||
+      (seqs >= shd::kQBox && !make_q_map(&a.qmap_box, q, d, num_seqs, shd::kQBox)))
     return cudaErrorInvalidValue;
   a.ctas = device_sm_count();
   a.narrow_units = b16 ? shd::kNarrowUnits16 : shd::kNarrowUnits8;
@@ -142,7 +144,7 @@ cudaError_t launch_shared(const pa_kv_desc &d, float *out, float *lse, const voi
   a.num_q = d.num_q_heads;
   a.g = d.num_q_heads / d.num_kv_heads;
   a.own_units = shd::is_narrow(a.g) ? a.narrow_units : a.wide_units;
-  a.tile_seqs = tile_seqs_of(d, max_group_size);
+  a.tile_seqs = seqs;
   a.slot_rows = a.tile_seqs * a.g;
   const float ks = (!b16 && d.k_scale != 0.f) ? d.k_scale : 1.f;
   a.qscale = scale * ks * shd::kLog2e;

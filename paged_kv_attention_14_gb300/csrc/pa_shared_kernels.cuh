@@ -72,6 +72,8 @@ constexpr float kRaise = 8.f;
 // 84.2 / 86.3 / 87.9 us.
 constexpr int kNarrowUnits16 = 8, kNarrowUnits8 = 6, kWideUnits = 24;
 
+constexpr int kQBox = 8;
+
 // One group's prefix on the axis.
 struct __align__(8) GroupInfo {
   long long base;  // first unit
@@ -117,7 +119,8 @@ struct __align__(16) Axis {
 struct Args {
   CUtensorMap kmap;
   CUtensorMap vmap;
-  CUtensorMap qmap;
+  CUtensorMap qmap;      // queries: a box is one sequence's rows of a kv head, half of their columns,
+  CUtensorMap qmap_box;  // or those of kQBox sequences
   float *out;
   float *lse;
   const int32_t *block_tables;
@@ -699,8 +702,9 @@ __device__ __forceinline__ bool take_item(const Args &a, Bars<C> &bar, const Ite
   return true;
 }
 
-// Warp 3: Q tiles, [half][row][128 B] with the 128-byte swizzle, a copy per
-// sequence and half (its g rows of the kv head).
+// Warp 3: Q tiles, [half][row][128 B] with the 128-byte swizzle.  A copy is
+// one half of kQBox sequences' rows of the kv head; what is left over goes one
+// sequence at a time (a copy takes some 90 cycles to issue).
 template <class C>
 __device__ bool load_q(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq, int lane) {
   const uint64_t pol = l2_evict_last_policy();
@@ -723,9 +727,13 @@ __device__ bool load_q(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *i
     __syncwarp();
     const uint32_t half = qs.big ? C::QHALF : C::QHALF / 2;
     uint8_t *to = smem + C::OFF_Q + qs.slot * (C::QB / 2) + (lane % C::HALVES) * half;
+    const int n = it.rows / a.g, boxes = n / kQBox;  // sequences
 #pragma unroll 1
-    for (int s = lane / C::HALVES; s * a.g < it.rows; s += 32 / C::HALVES)
-      tma_load_4d(to + s * a.g * 128, &a.qmap, 0, it.kvh * a.g, lane % C::HALVES, it.seq0 + s, &bar.q_land[qs.slot], pol);
+    for (int i = lane / C::HALVES; i < boxes + n % kQBox; i += 32 / C::HALVES) {
+      const int s = i < boxes ? i * kQBox : boxes * kQBox + i - boxes;
+      tma_load_4d(to + s * a.g * 128, i < boxes ? &a.qmap_box : &a.qmap, 0, it.kvh * a.g, lane % C::HALVES, it.seq0 + s,
+                  &bar.q_land[qs.slot], pol);
+    }
     __syncwarp();
     qs.done();
   }
@@ -802,7 +810,6 @@ __device__ bool widen(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq
         if (!wait(v ? &bar.lv_full[ls] : &bar.lk_full[ls], lp, a.wait_ns)) return false;
         const uint8_t *src = smem + (v ? C::OFF_LV : C::OFF_LK) + ls * C::LB + ct * 16;
         uint8_t *dst = smem + (v ? C::OFF_V : C::OFF_K) + ts * C::TB + put;
-        const int zero = v ? keep : KT;  // rows from here on become zero
         constexpr int ILP = PER < 4 ? PER : 4;
 #pragma unroll 1
         for (int k0 = 0; k0 < PER; k0 += ILP) {
@@ -812,9 +819,8 @@ __device__ bool widen(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq
           for (int k = 0; k < ILP; ++k) x[k] = *reinterpret_cast<const uint4 *>(src + (k0 + k) * RSTEP * C::D);
 #pragma unroll
           for (int k = 0; k < ILP; ++k) {
-            uint32_t w[4] = {swap ? x[k].z : x[k].x, swap ? x[k].w : x[k].y, swap ? x[k].x : x[k].z,
-                             swap ? x[k].y : x[k].w};
-            if (r0 + (k0 + k) * RSTEP >= zero) w[0] = w[1] = w[2] = w[3] = 0;  // the byte 0 is +0
+            const uint32_t w[4] = {swap ? x[k].z : x[k].x, swap ? x[k].w : x[k].y, swap ? x[k].x : x[k].z,
+                                   swap ? x[k].y : x[k].w};
             uint32_t o[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -824,6 +830,14 @@ __device__ bool widen(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *iq
             uint8_t *row = dst + (k0 + k) * (RSTEP / 8) * C::GB;
             *reinterpret_cast<uint4 *>(row + x0) = make_uint4(o[0], o[1], o[2], o[3]);
             *reinterpret_cast<uint4 *>(row + x1) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        }
+        if (v && keep < rows) {
+#pragma unroll 1
+          for (int r = keep + (r0 - keep & RSTEP - 1); r < rows; r += RSTEP) {
+            uint8_t *row = dst + (r - r0) / 8 * C::GB;
+            *reinterpret_cast<uint4 *>(row + x0) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(row + x1) = make_uint4(0, 0, 0, 0);
           }
         }
         fence_proxy_async_smem();
@@ -1287,6 +1301,9 @@ __global__ void __launch_bounds__(Cfg<D, KVT>::NTHREADS, 1) shared_attend_kernel
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc(&bar.tmem, C::TMEM_COLS);
+  // the maps are fetched while the plan is still made
+  if (warp == 1 && lane < (a.tile_seqs < kQBox ? 3 : 4))
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a.kmap + lane)) : "memory");
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
