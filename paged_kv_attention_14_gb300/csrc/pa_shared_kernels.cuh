@@ -31,14 +31,31 @@
 //      products of the next;
 //   1  walks the CTA's part of the axis, publishes its items, copies their
 //      K and V (TMA);
-//   3  (16-bit caches) Q tiles, in two slots, so that items overlap;
+//   3  Q tiles (TMA), in two slots, so that items overlap;
 //   4-11  softmax, two threads per row (64 keys each), and each item's output;
 //      items of up to 32 rows take one quarter of the lanes each, in turn, so
 //      that four of them can be in their softmax or output at once;
-//   12-15 (8-bit caches) Q tiles, and the landed bytes widened to fp16
-//      tiles (exact).
+//   12-15 (8-bit caches) widen the landed Q and bytes to fp16 tiles (exact).
 // Scores and outputs are double-buffered in tensor memory (S 2 x 128, O 2 x D
 // columns); P overwrites its scores.  Every wait is bounded.
+//
+// Measured, us a call in a captured graph (in brackets what the bytes take at
+// the measured HBM rate, 6.69 TB/s), 32 / 8 heads of 128, bf16:
+//   8 sequences on one document of 131072 tokens     96.2 (81.0)
+//   four groups of 16 on 4096 tokens, own 16-511     35.2 (20.8)
+//   64 sequences on 16384 tokens, own 16-511         45.2 (21.4)
+//   E4M3, 40 / 8 heads, 128 sequences, own 1-1000    82.5 (23.0)
+// What bounds it: the document, HBM (79.5% of its peak rate inside the
+// attention kernel), the rest is the chain of three launches: 3.6 us of plan,
+// 8 to 12 of join.  Wide tiles, the softmax: 1,900 of the 2,150 cycles a step
+// takes, on the two warps of a scheduler.  8-bit caches, shared memory: per
+// 128 keys the products read 128 KB (Q, K, and V twice), the widening reads 32
+// and writes 64, the copies write 32, together 2,050 cycles of a step's 2,700
+// at 128 bytes a cycle; the conversion itself costs nothing (byte moves in its
+// place: no change), and two warps for K with two for V took 20% longer.
+// Short items, the latency of one step after another (narrow ones some 2,300
+// cycles a step) and instruction fetch: the roles run different code at once,
+// so their loops are short and the waits' slow path is one function.
 #pragma once
 
 #include <cuda.h>
@@ -72,7 +89,7 @@ constexpr float kRaise = 8.f;
 // 84.2 / 86.3 / 87.9 us.
 constexpr int kNarrowUnits16 = 8, kNarrowUnits8 = 6, kWideUnits = 24;
 
-constexpr int kQBox = 8;
+constexpr int kQBox = 8;  // sequences of a copy of queries
 
 // One group's prefix on the axis.
 struct __align__(8) GroupInfo {
@@ -1431,14 +1448,17 @@ __global__ void __launch_bounds__(64) shared_join_kernel(const __grid_constant__
       }
       if (there) v = __ldcg(x);
     }
-    // all the pieces' columns
+    // all the pieces' columns, four pieces to a branch
     float4 y[16];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int from = 2 * k + (lane & 1);
-      const int ai = __shfl_sync(0xffffffffu, at, from), st = __shfl_sync(0xffffffffu, stride, from);
-      y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i0 + k < most) y[k] = __ldcg(base + ai + c0 * st);
+    for (int k0 = 0; k0 < 16; k0 += 4) {
+      if (i0 + k0 >= most) break;
+#pragma unroll
+      for (int k = k0; k < k0 + 4; ++k) {
+        const int from = 2 * k + (lane & 1);
+        const int ai = __shfl_sync(0xffffffffu, at, from), st = __shfl_sync(0xffffffffu, stride, from);
+        y[k] = __ldcg(base + ai + c0 * st);
+      }
     }
     float mn = fmaxf(M, v);
 #pragma unroll
@@ -1452,12 +1472,16 @@ __global__ void __launch_bounds__(64) shared_join_kernel(const __grid_constant__
     W = W * f + ws;
     acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float wk = __shfl_sync(0xffffffffu, w, 2 * k + (lane & 1));
-      acc.x += wk * y[k].x;
-      acc.y += wk * y[k].y;
-      acc.z += wk * y[k].z;
-      acc.w += wk * y[k].w;
+    for (int k0 = 0; k0 < 16; k0 += 4) {
+      if (i0 + k0 >= most) break;
+#pragma unroll
+      for (int k = k0; k < k0 + 4; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, 2 * k + (lane & 1));
+        acc.x += wk * y[k].x;
+        acc.y += wk * y[k].y;
+        acc.z += wk * y[k].z;
+        acc.w += wk * y[k].w;
+      }
     }
   }
   if (!mine) return;
