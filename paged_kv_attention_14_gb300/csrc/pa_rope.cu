@@ -190,15 +190,14 @@ __device__ __forceinline__ void store_row(const RopeArgs &a, int64_t token, int 
   }
 }
 
-// A token's position, and its cache slot (-1: none); with checked indices
-// one out of range is reported and replaced by 0 or -1.
+// A token's position (0 in place of one out of range: a padding token's may
+// be anything), and its cache slot (-1: none; with checked indices also for
+// one out of range).  Checked, both are reported.
 __device__ __forceinline__ int position_of(const RopeArgs &a, int64_t token, bool report) {
   const int pos = __ldg(a.positions + token);
-  if (a.checked && (pos < 0 || pos >= a.max_position)) {
-    if (report) report_error(a.err, nullptr, kErrBadIndex);
-    return 0;
-  }
-  return pos;
+  if (static_cast<uint32_t>(pos) < static_cast<uint32_t>(a.max_position)) return pos;
+  if (a.checked && report) report_error(a.err, nullptr, kErrBadIndex);
+  return 0;
 }
 __device__ __forceinline__ int64_t slot_of(const RopeArgs &a, int64_t token, bool report) {
   const int64_t slot = __ldg(a.slots + token);

@@ -284,6 +284,21 @@ def test_checked_positions_and_slots_are_reported_and_skipped():
     c.pos.copy_(good)
 
 
+@pytest.mark.parametrize("tokens", [8, 4096])
+def test_padding_positions_take_position_0(tokens):
+    """Unchecked positions outside the table (padding tokens') read nothing outside it; both kernels."""
+    c = Case(tokens, 32, 8, 128, 128, False, "qk")
+    outside = torch.arange(tokens, device=DEV) % 5 == 3
+    c.pos[outside] = 0
+    want_q, want_k = c.outs()
+    B.pa_qk_norm_rope(c.desc, c.rope, want_q, want_k, c.q, c.k, c.pos)
+    c.pos[outside] = torch.tensor([-1, MAXP, 2**31 - 1, -2**31], dtype=torch.int32, device=DEV).repeat(tokens)[
+        :int(outside.sum())]
+    qo, ko = c.outs()
+    B.pa_qk_norm_rope(c.desc, c.rope, qo, ko, c.q, c.k, c.pos)
+    assert torch.equal(qo, want_q) and torch.equal(ko, want_k)
+
+
 def test_other_stream_and_graph_replay():
     c = Case(50, 32, 8, 128, 128, False, "qk", seed=11)
     want_q, _ = c.outs()
