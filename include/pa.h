@@ -250,7 +250,8 @@ PA_API pa_status pa_cache_write(const pa_kv_desc *desc, const void *k, const voi
  *                  sines, of position p.  A scaled rotation (any long-context
  *                  scheme) is a table with its angles (and its magnitude
  *                  factor) in it.
- *   max_position : rows of cos_sin; positions lie in [0, max_position).
+ *   max_position : rows of cos_sin; positions lie in [0, max_position) (one out
+ *                  of range takes position 0's angles).
  *   rotary_dim   : dims of a head that rotate, the first ones; a multiple of
  *                  16, at most head_dim; 0 means head_dim.
  *   interleaved  : 0: dim i rotates with dim i + rotary_dim / 2; 1: dim 2 i
@@ -292,8 +293,8 @@ typedef struct {
  *   positions    : int32 [num_tokens]
  * Either side may be left out (q and q_out, or k and k_out, both NULL).
  * Uses desc's heads, head_dim, kv_dtype (for the activation type),
- * error_word and check_indices (a position out of range is reported and
- * position 0 used).  num_tokens == 0 enqueues nothing and returns PA_OK.
+ * error_word and check_indices (a position out of range is reported).
+ * num_tokens == 0 enqueues nothing and returns PA_OK.
  */
 PA_API pa_status pa_qk_norm_rope(const pa_kv_desc *desc, const pa_rope_desc *rope, void *q_out, void *k_out,
                                  const void *q, int64_t q_stride, const void *k, int64_t k_stride,
@@ -606,7 +607,8 @@ PA_API size_t pa_decode_shared_workspace_size(const pa_kv_desc *desc, int32_t nu
  * reported and clamped; without it they are clamped in silence).  Errors on
  * the device are reported in desc->error_word only.
  * PA_ERR_UNSUPPORTED: local attention, decode_impl PA_DECODE_SIMT, more than
- * 65535 sequences or groups, a cache of more than 2^31 rows.
+ * 65535 sequences or groups, a cache of more than 2^31 rows, a batch whose
+ * workspace would pass 32 GB.
  */
 PA_API pa_status pa_decode_shared(const pa_kv_desc *desc, float *out, float *lse, const void *q, const void *k_cache,
                                   const void *v_cache, const int32_t *block_tables, int32_t max_blocks_per_seq,

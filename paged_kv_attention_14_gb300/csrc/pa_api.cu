@@ -348,6 +348,10 @@ static pa_status check_shared(const pa_kv_desc *desc, int32_t num_seqs, int32_t 
     return fail(PA_ERR_UNSUPPORTED, "pa_decode_shared runs on the tensor cores (decode_impl AUTO or MMA)%s");
   if (static_cast<int64_t>(desc->num_blocks) * desc->num_kv_heads * 16 > 0x7fffffffLL)
     return fail(PA_ERR_UNSUPPORTED, "pa_decode_shared addresses at most 2^31 cache rows%s");
+  // its parts' places are counted in 16 bytes, in 32 bits
+  if (num_seqs > 0 &&
+      pa::shared_workspace_bytes(*desc, num_seqs, num_groups, max_group_size) > (size_t{1} << 31) * 16 - 16)
+    return fail(PA_ERR_UNSUPPORTED, "pa_decode_shared's workspace would pass 32 GB%s");
   return PA_OK;
 }
 

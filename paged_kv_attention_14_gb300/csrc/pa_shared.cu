@@ -43,28 +43,20 @@ bool make_map(CUtensorMap *map, const void *base, const pa_kv_desc &d) {
   const bool kv8 = d.kv_dtype == PA_KV_FP8_E4M3 || d.kv_dtype == PA_KV_FP8_E5M2;
   const EncodeTiledFn enc = encode_tiled();
   if (!enc) return false;
-  thread_local MapCache<> cache;
-  const MapKey key = map_key(base, d.num_blocks, d.num_kv_heads, d.head_dim, kv8);
-  if (cache.find(key, map)) return true;
   const cuuint64_t D = d.head_dim, rows = static_cast<cuuint64_t>(d.num_blocks) * d.num_kv_heads * 16;
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r;
   if (kv8) {
     const cuuint64_t dims[2] = {D, rows}, strides[1] = {D};
     const cuuint32_t box[2] = {static_cast<cuuint32_t>(D), 16};
-    r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  } else {
-    const cuuint64_t dims[4] = {64, 8, D / 64, rows / 8}, strides[3] = {D * 2, 128, D * 16};
-    const cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(D / 64), 2};
-    r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   }
-  if (r != CUDA_SUCCESS) return false;
-  cache.put(key, *map);
-  return true;
+  const cuuint64_t dims[4] = {64, 8, D / 64, rows / 8}, strides[3] = {D * 2, 128, D * 16};
+  const cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(D / 64), 2};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Q: rows as [sequence][half][head][64 columns], a box is a half of one kv
@@ -143,7 +135,6 @@ cudaError_t launch_shared(const pa_kv_desc &d, float *out, float *lse, const voi
   a.num_kv = d.num_kv_heads;
   a.num_q = d.num_q_heads;
   a.g = d.num_q_heads / d.num_kv_heads;
-  a.own_units = shd::is_narrow(a.g) ? a.narrow_units : a.wide_units;
   a.tile_seqs = seqs;
   a.slot_rows = a.tile_seqs * a.g;
   const float ks = (!b16 && d.k_scale != 0.f) ? d.k_scale : 1.f;

@@ -153,7 +153,7 @@ struct Args {
   int tile_seqs;  // sequences a tile may have
   int slot_rows;  // rows of a cut item's slot
   int ctas;       // CTAs that share the axis
-  int narrow_units, wide_units, own_units;  // units of an item besides its blocks
+  int narrow_units, wide_units;  // units of an item besides its blocks (own parts: narrow ones)
   float qscale;   // scale * k_scale * log2(e)
   float qscale0;  // scale * log2(e)
   float vscale;
@@ -288,7 +288,7 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
     int L = s == tid ? len0 : __ldg(a.context_lens + s);
     if (a.checked) L = checked_len(L, cap, a.err, nullptr);
     SeqInfo q = {};
-    q.len = max(L, 0);
+    q.len = min(max(L, 0), cap);
     int lo = 0, hi = G - 1;
 #pragma unroll 1
     while (lo < hi) {
@@ -323,7 +323,7 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
       groups[i].nb = nb;
       v[0] = static_cast<long long>(item_units(nb, groups[i].extra)) * (groups[i].tiles * a.num_kv);
     }
-    if (i < S) v[1] = static_cast<long long>(item_units(seqs[i].nb, a.own_units)) * a.num_kv;
+    if (i < S) v[1] = static_cast<long long>(item_units(seqs[i].nb, a.narrow_units)) * a.num_kv;
     scan2(v, sum, s_warp);
     if (i < G) groups[i].base = at[0] + v[0];
     if (i < S) seqs[i].base = at[1] + v[1];
@@ -346,7 +346,7 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
       st.kind = u < own ? 0 : 1;
       st.idx = st.kind == 0 ? find_base(groups, G, u) : find_base(seqs, S, u - own);
       const int n = st.kind == 0 ? item_units(groups[st.idx].nb, groups[st.idx].extra)
-                                 : item_units(seqs[st.idx].nb, a.own_units);
+                                 : item_units(seqs[st.idx].nb, a.narrow_units);
       const long long r = st.kind == 0 ? u - groups[st.idx].base : u - own - seqs[st.idx].base;
       st.sub = static_cast<int>(divide(r, n));
       st.off = static_cast<int>(r - static_cast<long long>(st.sub) * n);
@@ -638,7 +638,7 @@ __device__ bool walk(const Args &a, uint8_t *smem, Bars<C> &bar, Item *iq, int l
           const SeqInfo &q = a.seqs[st.idx];
           items = a.num_kv;
           nb = q.nb;
-          extra = a.own_units;
+          extra = a.narrow_units;
           fb = q.fb;
           first = row = st.idx;
           n = tile_seqs = 1;
@@ -1407,7 +1407,7 @@ __global__ void __launch_bounds__(64) shared_join_kernel(const __grid_constant__
   int c1[2], np[2], s0[2];
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
-    const int nb = p ? q.nb : q.pnb, extra = p ? a.own_units : q.pextra, n = nb + extra;
+    const int nb = p ? q.nb : q.pnb, extra = p ? a.narrow_units : q.pextra, n = nb + extra;
     const long long u0 = (p ? q.base : q.pbase) + static_cast<long long>(kvh) * n;
     int c = axis_cta(u0, ax);
     if ((c + 1) * ax.per - u0 <= extra) ++c;  // that CTA's range holds none of its blocks

@@ -244,6 +244,15 @@ def test_checked_indices_are_reported_and_stay_inside():
         assert int(ew) & B.PA_DEVERR_BAD_INDEX, what
 
 
+def test_lengths_past_the_table_end_at_it():
+    b = W.shared_prefix_decode(826, [3], [64], [48, 48, 33], 8, 2, 128, device=DEV, poison=False)
+    b.context_lens_decode = torch.full_like(b.context_lens_decode, b.block_tables_decode.shape[1] * 16)
+    want = _run(b, H.gpu_caches(b))
+    b.context_lens_decode = b.context_lens_decode + torch.tensor([1, 1000, 2**31 - 1 - 200], dtype=torch.int32, device=DEV)
+    out = _run(b, H.gpu_caches(b))
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
 def test_a_stalled_pipeline_is_reported_and_the_next_call_is_right():
     ew = torch.zeros(1, dtype=torch.int32, device=DEV)
     b = W.shared_prefix_decode(813, [20, 3], [512, 32], [9] * 23, 32, 8, 128, device=DEV)

@@ -67,6 +67,14 @@ def test_descriptor(lib, field, value, status):
     assert _call(lib, None) == B.PA_ERR_INVALID_ARG
 
 
+def test_a_workspace_past_32_bits_of_places_is_refused(lib):
+    d = _desc(num_kv_heads=64, num_q_heads=1024, head_dim=128)
+    # two parts of 1024 heads x 128 x 4 bytes a sequence
+    assert lib.pa_decode_shared_workspace_size(ctypes.byref(d), 32000, 1, 2) > 32000 * (1 << 20)
+    assert lib.pa_decode_shared_workspace_size(ctypes.byref(d), 33000, 1, 2) == 0
+    assert _call(lib, d, S=33000) == B.PA_ERR_UNSUPPORTED and "32 GB" in B.last_error()
+
+
 def test_workspace_size(lib):
     d = ctypes.byref(_desc())
     size = lib.pa_decode_shared_workspace_size
