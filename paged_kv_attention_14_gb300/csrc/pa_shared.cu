@@ -10,7 +10,7 @@ namespace {
 constexpr size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct Layout {
-  size_t axis, groups, seqs, starts, pre_o, pre_lse, own_o, own_lse, cut_o, cut_lse, total;
+  size_t axis, groups, seqs, starts, pre_o, pre_lse, own_o, own_lse, cut_o, cut_lse, sums, total;
 };
 
 // Sequences of a tile: what the largest group needs, up to the kernel's rows
@@ -93,6 +93,7 @@ Layout layout(const pa_kv_desc &d, int32_t num_seqs, int32_t num_groups, int32_t
   w.groups = take(sizeof(shd::GroupInfo) * num_groups);
   w.seqs = take(sizeof(shd::SeqInfo) * num_seqs);
   w.starts = take(sizeof(shd::CtaStart) * ctas);
+  w.sums = take(static_cast<size_t>(ctas) * shd::MAXROWS * d.head_dim * 4);
   w.total = at;
   return w;
 }
@@ -159,6 +160,7 @@ cudaError_t launch_shared(const pa_kv_desc &d, float *out, float *lse, const voi
   a.own_lse = reinterpret_cast<float *>(ws + w.own_lse);
   a.cut_o = reinterpret_cast<float *>(ws + w.cut_o);
   a.cut_lse = reinterpret_cast<float *>(ws + w.cut_lse);
+  a.sums = reinterpret_cast<float *>(ws + w.sums);
 
   // each launch overlaps the tail of the one before it (programmatic
   // dependent launch); every kernel waits for that one's writes first

@@ -41,10 +41,10 @@
 //
 // Measured, us a call in a captured graph (in brackets what the bytes take at
 // the measured HBM rate, 6.69 TB/s), 32 / 8 heads of 128, bf16:
-//   8 sequences on one document of 131072 tokens     96.2 (81.0)
-//   four groups of 16 on 4096 tokens, own 16-511     35.2 (20.8)
-//   64 sequences on 16384 tokens, own 16-511         45.2 (21.4)
-//   E4M3, 40 / 8 heads, 128 sequences, own 1-1000    82.5 (23.0)
+//   8 sequences on one document of 131072 tokens    100.1 (81.0)
+//   four groups of 16 on 4096 tokens, own 16-511     36.7 (20.8)
+//   64 sequences on 16384 tokens, own 16-511         46.9 (21.4)
+//   E4M3, 40 / 8 heads, 128 sequences, own 1-1000    88.9 (23.0)
 // What bounds it: the document, HBM (79.5% of its peak rate inside the
 // attention kernel), the rest is the chain of three launches: 3.6 us of plan,
 // 8 to 12 of join.  Wide tiles, the softmax: 1,900 of the 2,150 cycles a step
@@ -175,6 +175,7 @@ struct Args {
   float *own_lse;
   float *cut_o;    // pieces of cut items, [ctas][2][D / 4][slot_rows][4]
   float *cut_lse;
+  float *sums;     // O's sums over the chains of steps so far, [ctas][D / 4][MAXROWS][4]
 };
 
 // ------------------------------------------------------------------ planning
@@ -399,6 +400,15 @@ struct __align__(16) Item {
 };
 
 constexpr int NIQ = 4;  // items in flight between the roles
+// A product adds to O with its sum truncated, not rounded, so that O loses
+// half a unit of its last place on average with every product, always towards
+// zero.  After a chain of this many steps O goes to sums in the workspace,
+// whose additions round, and starts again.  Relative error of a prefix of
+// 131072 tokens, in pieces of some 108 steps, against 64 bits (and us a call):
+// 1.6e-5 without chains (97.8), 7.1e-6 with 24 (99.3), 5.1e-6 with 16
+// (100.1), 3.4e-6 with 8 (101.2); 64 sequences on 16384 tokens, pieces of some
+// 20 steps: 7.3e-6 without (44.9), 4.7e-6 with 16 (46.9), 3.3e-6 with 8 (49.4).
+constexpr int kChain = 16;
 
 // Waits, with a whole warp, until the phase of `bar` with the given parity has
 // completed; false (for all its lanes) if that does not happen within
@@ -998,7 +1008,7 @@ __device__ bool issue_pv(const Args &a, uint32_t sbase, uint32_t tmem, Bars<C> &
       tc_fence_after_sync();
       const uint32_t vd = uniform(desc_low(sbase + C::OFF_V + (k % C::NT) * C::TB, 1024));
       const uint32_t p = uniform(tmem + C::S_COL + (k & 1) * KT);
-      const uint32_t n = uniform(it.nblk - b), more = uniform(b);
+      const uint32_t n = uniform(it.nblk - b), more = uniform(b / BPT % kChain);
       if (elect_one()) {
         // keys 16 kk .. 16 kk + 15: hi at +0, lo at +16 of their 32-column chunk
 #pragma unroll
@@ -1058,8 +1068,38 @@ struct Softmax {
   uint32_t sw = 0, sn = 0;  // scores: bit = buffer
   uint32_t ow = 0, on = 0;  // outputs: bit = buffer; bit 0
 
+  // This thread's columns c .. c + 3 of the item's sum over the chains before
+  // the current one.
+  __device__ __forceinline__ float4 *sum_at(int c) const {
+    uint32_t at = blockIdx.x * (D / 4) * MAXROWS + threadIdx.x % MAXROWS;  // (threadIdx.x % 128: the row)
+    asm volatile("" : "+r"(at));  // not kept in a register from here to there
+    return reinterpret_cast<float4 *>(a.sums) + at + c / 4 * MAXROWS;
+  }
+
+  // The end of a chain, the steps before k: O goes to the sums.  No other
+  // thread adds to this one's, so they are taken in order.
+  __device__ __forceinline__ void flush(uint32_t k, uint32_t num, bool live, bool first, uint64_t *v_empty) {
+    ok = wait(&v_empty[(k - 1) % C::NT], ((k - 1) / C::NT) & 1, a.wait_ns) && ok;
+    tc_fence_after_sync();
+#pragma unroll 1
+    for (int c0 = h * (D / 2); c0 < (h + 1) * (D / 2); c0 += 16) {
+      float o[16];
+      tmem_ld16(trow + C::O_COL + (num & 1) * D + c0, o);
+      if (live) {
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          const float4 x = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          if (first)
+            __stcg(sum_at(c0 + i), x);
+          else
+            atomicAdd(sum_at(c0 + i), x);
+        }
+      }
+    }
+  }
+
   // An item's output, once its last product is through.
-  __device__ __forceinline__ void finish(const Item &it, uint32_t num, float m, float l) {
+  __device__ __forceinline__ void finish(const Item &it, uint32_t num, bool chains, float m, float l) {
     const int ob = num & 1;
     const int r = row - first_lane(it.rows, num);  // row of the tile
     const bool live = r >= 0 && r < it.rows;
@@ -1111,6 +1151,16 @@ struct Softmax {
         float o[16];
         tmem_ld16(trow + C::O_COL + ob * D + c0, o);
         if (live) {
+          if (chains) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              const float4 x = __ldcg(sum_at(c0 + i));
+              o[i] += x.x;
+              o[i + 1] += x.y;
+              o[i + 2] += x.z;
+              o[i + 3] += x.w;
+            }
+          }
 #pragma unroll
           for (int i = 0; i < 16; i += 4)
             *reinterpret_cast<float4 *>(o_dst + (c0 + i) / 4 * stride) =
@@ -1179,17 +1229,20 @@ struct Softmax {
           fence_proxy_async_smem();
         }
         if (!named_bar_and(pair, 64, there && ok)) return false;
-        if (mine) step(k, key0, b > 0, lim, live, qsc, num, v_empty, m, l);
+        if (mine) {
+          step(k, key0, b / BPT, lim, live, qsc, num, v_empty, m, l);
+          if (b > 0 && b / BPT % kChain == 0) flush(k, num, live, b / BPT == kChain, v_empty);
+        }
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.p_full[nar][k & 1]);
       }
-      finish(it, num, m, l);
+      finish(it, num, steps > kChain, m, l);
     }
   }
 
   // One step's scores (in tensor memory) to P over them; m and l follow.
-  __device__ __forceinline__ void step(uint32_t k, int key0, bool later, int lim, bool live, float qsc,
+  __device__ __forceinline__ void step(uint32_t k, int key0, int done, int lim, bool live, float qsc,
                                        uint32_t num, uint64_t *v_empty, float &m, float &l) {
     const uint32_t scol = trow + C::S_COL + (k & 1) * KT + 64 * h;
     const int kh = key0 + 64 * h;
@@ -1226,7 +1279,7 @@ struct Softmax {
     if (__any_sync(0xffffffffu, raise && m != -INFINITY)) {
       // rare: this half of O's columns takes the new maximum; the product of
       // the step before, which releases its V tile, is through
-      if (later) ok = wait(&v_empty[(k - 1) % C::NT], ((k - 1) / C::NT) & 1, a.wait_ns) && ok;
+      if (done) ok = wait(&v_empty[(k - 1) % C::NT], ((k - 1) / C::NT) & 1, a.wait_ns) && ok;
       tc_fence_after_sync();
       const float f = (raise && m != -INFINITY) ? exp2f(m - mx) : 1.f;
       l *= f;
@@ -1237,6 +1290,13 @@ struct Softmax {
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] *= f;
         tmem_st32(trow + C::O_COL + (num & 1) * D + c0, o);
+      }
+      if (done > kChain) {  // and its sums
+#pragma unroll 1
+        for (int c = h * (D / 2); c < (h + 1) * (D / 2); c += 4) {
+          const float4 x = __ldcg(sum_at(c));
+          __stcg(sum_at(c), make_float4(x.x * f, x.y * f, x.z * f, x.w * f));
+        }
       }
     }
     if (raise) m = mx;

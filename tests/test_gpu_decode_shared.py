@@ -99,6 +99,37 @@ def test_two_sequences_on_a_very_long_prefix():
     _check(b, *_run(b, H.gpu_caches(b)))
 
 
+def test_the_error_does_not_grow_with_the_prefix():
+    """131072 tokens, some 108 steps of 128 keys in a piece.  A product adds to
+    the output truncated: half of 2^-23 |O| is lost on average, 0.72 of that
+    over a binade, towards zero every time.  The output of a chain of 16 steps
+    (256 products) grows as a random walk does, so the chain loses
+    256 * 2/3 * 0.72 * 2^-24 = 7.3e-6 of its end value; P's pairs add 2^-18
+    at most, independent from key to key: 1e-5 in the 2-norm.  (Without chains
+    the same sum over 1728 products is 4.9e-5.)"""
+    b = W.shared_prefix_decode(827, [8], [131072], [20, 60, 100, 140, 180, 220, 260, 300], 32, 8, 128, device=DEV)
+    out, _ = _run(b, H.gpu_caches(b))
+    o, _ = H.oracle_decode(b, pairs=[(3, h) for h in range(32)])
+    e = out[3].double().cpu().numpy() - o.reshape(32, 128)
+    assert np.linalg.norm(e) <= 1e-5 * np.linalg.norm(o)
+
+
+def test_rising_scores_over_many_chains():
+    """Row maxima that rise by more than the raise threshold again and again,
+    also between chains, so that the sums are scaled."""
+    b = W.shared_prefix_decode(828, [3], [65536], [5, 6, 7], 8, 8, 64, device=DEV, poison=False)
+    b.q_decode.zero_()
+    b.q_decode[:, :, 0] = 1
+    kc = b.k_pool.clone()
+    kc[..., 0] = 0
+    # the score in log2 units goes up by 12 every 4096 tokens, scattered below by the other columns' zeros
+    up = torch.arange(4096, device=DEV) // 256 * (12 * 0.6931471805599453 / b.scale)
+    kc[b.block_tables_decode[0, :4096].long(), :, :, 0] = up.to(kc.dtype)[:, None, None]
+    b.k_pool = kc
+    # scores up to 125 (130 of the derivation's 7.4 units are 18 times as many)
+    _check(b, *_run(b, (kc, b.v_pool)), scale_tol=18.0)
+
+
 def test_no_groups_is_a_plain_decode():
     b = W.shared_prefix_decode(803, [3, 2], [64, 32], [1, 40, 7, 300, 16], 32, 8, 128, device=DEV)
     none = torch.zeros(0, dtype=torch.int32, device=DEV)
