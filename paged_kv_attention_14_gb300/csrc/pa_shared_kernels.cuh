@@ -45,14 +45,15 @@
 //   four groups of 16 on 4096 tokens, own 16-511     36.7 (20.8)
 //   64 sequences on 16384 tokens, own 16-511         46.9 (21.4)
 //   E4M3, 40 / 8 heads, 128 sequences, own 1-1000    88.9 (23.0)
-// What bounds it: the document, HBM (79.5% of its peak rate inside the
-// attention kernel), the rest is the chain of three launches: 3.6 us of plan,
-// 8 to 12 of join.  Wide tiles, the softmax: 1,900 of the 2,150 cycles a step
+// What bounds it: the document, HBM (75% of its peak rate inside the attention
+// kernel), the rest is the chain of three launches: 3.6 us of plan, 5 to 10
+// of join.  Wide tiles, the softmax: 1,900 of the 2,150 cycles a step
 // takes, on the two warps of a scheduler.  8-bit caches, shared memory: per
 // 128 keys the products read 128 KB (Q, K, and V twice), the widening reads 32
 // and writes 64, the copies write 32, together 2,050 cycles of a step's 2,700
-// at 128 bytes a cycle; the conversion itself costs nothing (byte moves in its
-// place: no change), and two warps for K with two for V took 20% longer.
+// at 128 bytes a cycle; the conversion itself costs nothing (E5M2 by byte
+// moves instead: no change), nor does its order (two warps for K and two for
+// V: 88.4 us).
 // Short items, the latency of one step after another (narrow ones some 2,300
 // cycles a step) and instruction fetch: the roles run different code at once,
 // so their loops are short and the waits' slow path is one function.
