@@ -258,7 +258,7 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x;
   const int S = a.num_seqs, G = a.num_groups;
-  const int cap = a.max_blocks * 16;
+  const int cap = min(a.max_blocks, 0x7ffffff) * 16;
   const bool small = S <= PLAN_CAP && G <= PLAN_CAP;
   SeqInfo *seqs = small ? s_seqs : a.seqs;
   GroupInfo *groups = small ? s_groups : a.groups;

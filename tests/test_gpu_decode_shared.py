@@ -366,6 +366,46 @@ def test_many_empty_groups():
     _check(b, *_run(b, H.gpu_caches(b), gs=gs, pre=pre))
 
 
+@pytest.mark.parametrize("max_group", [0, 1, 8, 1000])
+def test_any_largest_group_size(max_group):
+    """A bound below the largest group, and far above the batch."""
+    b = W.shared_prefix_decode(829, [2, 1], [48, 0], [5, 40, 17], 8, 2, 128, device=DEV)
+    _check(b, *_run(b, H.gpu_caches(b), max_group=max_group))
+
+
+def test_the_largest_batch():
+    """65535 sequences in 21845 groups of three; sampled rows, and the same rows as a batch of their own."""
+    n = 21845
+    b = W.shared_prefix_decode(830, [3] * n, [16 * (j % 3) for j in range(n)], [7 * i % 23 + 1 for i in range(3 * n)], 4, 2,
+                               64, device=DEV)
+    out, lse = _run(b, H.gpu_caches(b))
+    _check(b, out, lse, rows=[0, 1, 2, 3, 511, 512, 513, 32767, 32768, 65531, 65532, 65533, 65534])
+    ref = torch.empty_like(out)
+    d = H.desc_of(b)
+    B.pa_decode(d, ref, b.q_decode, *H.gpu_caches(b), b.block_tables_decode, b.context_lens_decode,
+                b.max_context_len_decode(), b.scale, B.decode_workspace(d, 3 * n, b.max_context_len_decode()))
+    torch.cuda.synchronize()
+    assert float((out - ref).abs().max()) <= 2 * TOL
+
+
+def test_one_stream_takes_batches_of_different_shapes_through_one_workspace():
+    """Calls in a row, each with its own lengths and sizes, not waited for in between."""
+    bs = [W.shared_prefix_decode(831 + i, g, p, s, 32, 8, 128, device=DEV) for i, (g, p, s) in enumerate([
+        ([9, 7], [160, 1040], list(range(1, 17))), ([1], [0], [700]), ([40], [4096], [3 * i % 70 + 1 for i in range(40)])])]
+    ws = B.decode_shared_workspace(H.desc_of(bs[2]), 40, 2, 40)
+    outs = []
+    for b in bs + bs[::-1]:
+        gs, pre, mg, mp = _args(b)
+        o = torch.empty_like(b.q_decode, dtype=torch.float32)
+        B.pa_decode_shared(H.desc_of(b), o, b.q_decode, b.k_pool, b.v_pool, b.block_tables_decode, b.context_lens_decode,
+                           b.block_tables_decode.shape[1] * 16, gs, pre, mg, mp, b.scale, ws)
+        outs.append(o)
+    torch.cuda.synchronize()
+    for i, b in enumerate(bs):
+        assert torch.equal(outs[i], outs[5 - i])
+        _check(b, outs[i], _run(b, H.gpu_caches(b))[1])
+
+
 def test_output_in_pinned_host_memory():
     b = W.shared_prefix_decode(815, [4, 1], [64, 0], [9, 50, 1, 16, 33], 32, 8, 128, device=DEV)
     caches = H.gpu_caches(b)
