@@ -254,6 +254,7 @@ def _act(desc) -> tuple:
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 _I64 = (torch.int64,)
+_U8 = (torch.uint8,)
 
 
 def pa_cache_write(desc: PaKvDesc, k, v, k_cache, v_cache, slot_mapping, stream=None):
@@ -310,10 +311,12 @@ def _rows(t: Optional[torch.Tensor], act: torch.dtype, tokens: int, heads: int, 
         return None, 0
     if t.dtype != act:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {act}")
-    if not t.is_cuda:
+    if t.get_device() < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.shape != (tokens, heads, d):
         raise ValueError(f"{name} must be [{tokens}, {heads}, {d}], got {list(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), heads * d
     st, sh, se = t.stride()
     if tokens == 1:
         st = heads * d  # of one token any stride will do
@@ -330,6 +333,14 @@ def _launch_stream(stream, *tensors) -> int:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _at(t, dtypes, name: str, dev: int):
+    """The address of a tensor that has to be on the current device ``dev``."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _ptr(t, dtypes, name)
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
 def pa_qk_norm_rope(desc: PaKvDesc, rope: PaRopeDesc, q_out, k_out, q, k, positions, stream=None):
@@ -363,11 +374,14 @@ def pa_rope_cache_write(desc: PaKvDesc, rope: PaRopeDesc, q_out, q, k, v, positi
     kp, ks = _rows(k, act, T, hkv, d, "k")
     vp, vs = _rows(v, act, T, hkv, d, "v")
     qo, _ = _rows(q_out, act, T, hq, d, "q_out", True)
-    st = _launch_stream(stream, positions, q, k, v, q_out, k_cache, v_cache, slot_mapping, *rope._keep)
+    if kp is None or vp is None:
+        raise ValueError("k and v are required")
+    st = _launch_stream(stream, q, k, v, q_out, *rope._keep)
+    dev = k.get_device()
     _check(load().pa_rope_cache_write(ctypes.byref(desc), ctypes.byref(rope), qo, qp, qs, kp, ks, vp, vs,
-                                      _ptr(positions, _I32, "positions"), _cache_ptr(k_cache, desc, "k_cache"),
-                                      _cache_ptr(v_cache, desc, "v_cache"), _ptr(slot_mapping, _I64, "slot_mapping"),
-                                      T, st))
+                                      _at(positions, _I32, "positions", dev), _cache_at(k_cache, desc, "k_cache", dev),
+                                      _cache_at(v_cache, desc, "v_cache", dev),
+                                      _at(slot_mapping, _I64, "slot_mapping", dev), T, st))
 
 
 #: element types a cache tensor of each descriptor type may have
@@ -375,9 +389,9 @@ _CACHE_OF = {PA_KV_BF16: (torch.bfloat16,), PA_KV_F16: (torch.float16,),
              PA_KV_FP8_E4M3: (torch.uint8, torch.float8_e4m3fn), PA_KV_FP8_E5M2: (torch.uint8, torch.float8_e5m2)}
 
 
-def _cache_ptr(t, desc: PaKvDesc, name: str):
-    """The address of a cache of the descriptor's type and size."""
-    p = _ptr(t, _CACHE_OF[desc.kv_dtype], name)
+def _cache_at(t, desc: PaKvDesc, name: str, dev: int):
+    """The address of a cache of the descriptor's type and size on the current device."""
+    p = _at(t, _CACHE_OF[desc.kv_dtype], name, dev)
     if t.numel() != desc.num_blocks * desc.num_kv_heads * 16 * desc.head_dim:
         raise ValueError(f"{name} must be [num_blocks, num_kv_heads, 16, head_dim]")
     return p
@@ -457,16 +471,18 @@ def pa_decode_shared(desc: PaKvDesc, out, q, k_cache, v_cache, block_tables, con
     if q.shape != (S, hq, desc.head_dim) or out.shape != q.shape or block_tables.shape[0] != S or \
             (lse is not None and lse.shape != (S, hq)):
         raise ValueError("q and out must be [S, Hq, D], lse [S, Hq] and block_tables [S, max_blocks]")
-    st = _launch_stream(stream, q, k_cache, v_cache, block_tables, context_lens, group_start, prefix_lens, workspace,
-                        out if out.is_cuda else None, lse if lse is not None and lse.is_cuda else None)
-    _check(load().pa_decode_shared(ctypes.byref(desc), _ptr(out, _F32, "out", host_ok=True),
-                                   _ptr(lse, _F32, "lse", allow_none=True, host_ok=True), _ptr(q, _act(desc), "q"),
-                                   _cache_ptr(k_cache, desc, "k_cache"), _cache_ptr(v_cache, desc, "v_cache"),
-                                   _ptr(block_tables, _I32, "block_tables"), int(block_tables.shape[1]),
-                                   _ptr(context_lens, _I32, "context_lens"), S, int(max_context_len),
-                                   _ptr(group_start, _I32, "group_start"), _ptr(prefix_lens, _I32, "prefix_lens"), G,
-                                   int(max_group_size), int(max_prefix_len), float(scale),
-                                   _ptr(workspace, (torch.uint8,), "workspace"), workspace.numel(), st))
+    dev = torch._C._cuda_getDevice()
+    host = [_ptr(t, _F32, n, allow_none=True, host_ok=True) if t is None or not t.is_cuda else _at(t, _F32, n, dev)
+            for t, n in ((out, "out"), (lse, "lse"))]
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    _check(load().pa_decode_shared(ctypes.byref(desc), host[0], host[1], _at(q, _act(desc), "q", dev),
+                                   _cache_at(k_cache, desc, "k_cache", dev), _cache_at(v_cache, desc, "v_cache", dev),
+                                   _at(block_tables, _I32, "block_tables", dev), block_tables.shape[1],
+                                   _at(context_lens, _I32, "context_lens", dev), S, int(max_context_len),
+                                   _at(group_start, _I32, "group_start", dev),
+                                   _at(prefix_lens, _I32, "prefix_lens", dev), G, int(max_group_size),
+                                   int(max_prefix_len), float(scale), _at(workspace, _U8, "workspace", dev),
+                                   workspace.numel(), st))
 
 
 def pa_decode_static(desc: PaKvDesc, out, q, k_cache, v_cache, block_tables, context_lens,

@@ -338,3 +338,5 @@ def test_misuse_of_the_binding_is_refused():
         c.write(kc[:-1], vc, qo)
     with pytest.raises(ValueError, match="one entry"):
         c.write(kc, vc, qo, c.slots[:-1])
+    with pytest.raises(ValueError, match="k and v"):
+        B.pa_rope_cache_write(c.desc, c.rope, qo, c.q, None, c.v, c.pos, kc, vc, c.slots)
