@@ -771,8 +771,10 @@ __device__ bool load_q(const Args &a, uint8_t *smem, Bars<C> &bar, const Item *i
   return ok;
 }
 
-// Warps 12-15 (8-bit caches): Q tiles to fp16, in place (a finite |q| beyond
-// fp16 does not fit and is reported); landed bytes to fp16 tiles, exact; V rows past
+// Warps 12-15 (8-bit caches): Q tiles to fp16, in place (both operands of a
+// product have one type, and bytes fit fp16; bf16's 8 bits fit too, off by
+// 2^-25 at most below 2^-14, and a finite |q| beyond fp16 does not fit and is
+// reported); landed bytes to fp16 tiles, exact; V rows past
 // the piece's keys zeroed (they may hold anything, and 0 * NaN is NaN).  A
 // thread keeps its 16-byte column chunk and its row modulo 8, and with them
 // its places in the swizzled tile, over all its rows.  Of the two 16-byte
