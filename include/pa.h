@@ -592,9 +592,9 @@ PA_API size_t pa_decode_shared_workspace_size(const pa_kv_desc *desc, int32_t nu
  *   prefix_lens : int32 [num_groups]: the block-table rows of group j's
  *                 sequences name the same blocks for their first
  *                 prefix_lens[j] tokens.  A prefix is used in whole blocks
- *                 (rounded down); a sequence may be shorter than its group's
- *                 prefix or empty, and attends its own context_lens[s] tokens
- *                 all the same.
+ *                 (rounded down).  A sequence may be empty or end before its
+ *                 group's prefix does: it attends its own context_lens[s]
+ *                 tokens and no others, by itself.
  *   max_group_size : the largest group (host value).  It sizes the tiles and
  *                 the workspace; larger groups in group_start still give
  *                 right results.

@@ -7,7 +7,9 @@
 // the sum is cut at P_j: the queries of all the group's sequences attend the
 // prefix together, each sequence attends its own rest, and the parts (each
 // normalised by its own sum, with its log-sum-exp) are joined by weights
-// 2^(lse_p - max lse).
+// 2^(lse_p - max lse).  A sequence with L_s < P_j attends all its tokens as its
+// own: in a product a weight of 0 does not keep out a V row that is not finite,
+// so a row of a prefix item has to read all of the item's keys.
 //
 // Three launches:
 //  * shared_plan_kernel (one CTA) turns the lengths into a list of items --
@@ -97,11 +99,10 @@ struct __align__(8) GroupInfo {
   long long base;  // first unit
   int first;       // first sequence
   int n;           // sequences
-  int kend;        // keys of the prefix that some sequence reads
-  int nb;          // blocks of them (0: nothing shared)
+  int nb;          // blocks of the prefix (0: nobody reads it)
   int tile_seqs;   // sequences of a tile (the last tile may have fewer)
   int tiles;
-  int row;         // a sequence whose table holds all of the prefix that is read
+  int row;         // the first sequence that holds the whole prefix
   int P;           // the prefix, whole blocks
   int extra;       // units of an item besides its blocks
 };
@@ -283,8 +284,8 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
     groups[j] = q;
   }
   __syncthreads();
-  // each sequence's group (a binary search over the first sequences), and the
-  // longest part of each prefix that a sequence reads
+  // each sequence's group (a binary search over the first sequences), and
+  // whether it holds the group's whole prefix
 #pragma unroll 1
   for (int s = tid; s < S; s += PLAN_THREADS) {
     int L = s == tid ? len0 : __ldg(a.context_lens + s);
@@ -301,19 +302,14 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
         hi = mid - 1;
     }
     q.group = G > 0 && s >= groups[lo].first && s < groups[lo].first + groups[lo].n ? lo : -1;
-    if (q.group >= 0 && groups[lo].P > 0) {
+    if (q.group >= 0 && groups[lo].P > 0 && q.len >= groups[lo].P) {
       q.fb = groups[lo].P >> 4;
-      atomicMax(&groups[lo].kend, min(q.len, groups[lo].P));
+      atomicMin(&groups[lo].row, s);
     }
     q.nb = max(0, ((q.len + 15) >> 4) - q.fb);
     seqs[s] = q;
   }
   __syncthreads();
-#pragma unroll 1
-  for (int s = tid; s < S; s += PLAN_THREADS) {
-    const SeqInfo &q = seqs[s];
-    if (q.fb > 0 && min(q.len, q.fb * 16) == groups[q.group].kend) atomicMin(&groups[q.group].row, s);
-  }
   // places on the axis: prefix items, then own parts
   long long at[2] = {0, 0};
 #pragma unroll 1
@@ -321,7 +317,7 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
     const int i = i0 + tid;
     long long v[2] = {0, 0}, sum[2];
     if (i < G) {
-      const int nb = (groups[i].kend + 15) >> 4;
+      const int nb = groups[i].row != 0x7fffffff ? groups[i].P >> 4 : 0;
       groups[i].nb = nb;
       v[0] = static_cast<long long>(item_units(nb, groups[i].extra)) * (groups[i].tiles * a.num_kv);
     }
@@ -363,7 +359,7 @@ static __global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const 
     if (q.fb > 0) {
       const GroupInfo &gi = groups[q.group];
       const int i = s - gi.first, tile = i / gi.tile_seqs, t0 = tile * gi.tile_seqs;
-      q.pnb = q.len > 0 ? gi.nb : 0;
+      q.pnb = gi.nb;
       q.pbase = gi.base + static_cast<long long>(tile * a.num_kv) * item_units(gi.nb, gi.extra);
       q.prow = static_cast<short>((i - t0) * a.g);
       q.prows = static_cast<short>(min(gi.tile_seqs, gi.n - t0) * a.g);
@@ -396,8 +392,7 @@ struct __align__(16) Item {
   int lo;      // first block, counted from the item's
   int to;
   int slot;    // kToCut: the slot
-  int prefix;  // 1: rows have limits of their own (their lengths)
-  int pad;
+  int pad[2];
 };
 
 constexpr int NIQ = 4;  // items in flight between the roles
@@ -642,7 +637,7 @@ __device__ bool walk(const Args &a, uint8_t *smem, Bars<C> &bar, Item *iq, int l
           first = q.first;
           n = q.n;
           tile_seqs = q.tile_seqs;
-          kend = q.kend;
+          kend = q.nb * 16;
           row = q.row;
           whole_to = kToPre;
         } else {
@@ -662,7 +657,6 @@ __device__ bool walk(const Args &a, uint8_t *smem, Bars<C> &bar, Item *iq, int l
       it.kvh = st.sub - tile * a.num_kv;
       it.seq0 = first + tile * tile_seqs;
       it.rows = min(tile_seqs, n - tile * tile_seqs) * a.g;
-      it.prefix = kind == 0;
       // the part of the item's units in this CTA's range, and its blocks
       const int size = nb + extra;
       const int take = static_cast<int>(min(static_cast<long long>(size - st.off), left));
@@ -1141,7 +1135,7 @@ struct Softmax {
         l_dst = a.pre_lse + at + r;
         stride = 4 * it.rows;
       }
-      // no key (a sequence shorter than the piece's first one): nothing to weigh
+      // (no key has a weight: scores of -inf throughout)
       const bool none = lsum == 0.f;
       float inv = none ? 0.f : 1.f / lsum;
       if (it.to == kToOut) inv *= a.v_scales ? __ldg(a.v_scales + it.kvh) : a.vscale;
@@ -1196,10 +1190,9 @@ struct Softmax {
         k += steps;
         continue;
       }
-      // keys from here on are not the row's (rows of no sequence take what
-      // comes: nothing reads theirs)
-      int lim = 0x7fffffff;
-      if (live) lim = it.prefix ? min(it.kend, a.seqs[it.seq0 + r / a.g].len) : it.kend;
+      // keys from here on are no row's (those of a sequence that does not hold
+      // the whole prefix, in its group's tile, are computed and read by nobody)
+      const int lim = it.kend;
       // (a negative scale's sign is in the scores; a zero one must not meet
       // the -inf of a masked score as a zero)
       const float qsc = fmaxf(fabsf(score_scale(a, it.kvh)), 1e-37f);
@@ -1249,7 +1242,7 @@ struct Softmax {
                                        uint32_t num, uint64_t *v_empty, float &m, float &l) {
     const uint32_t scol = trow + C::S_COL + (k & 1) * KT + 64 * h;
     const int kh = key0 + 64 * h;
-    // 32 scores, keys past the row's limit out
+    // 32 scores, keys past the item's last out
     auto load = [&](int c, uint32_t(&x)[32]) {
       tmem_ld32_async(scol + 32 * c, x);
       tmem_wait_ld(x);
