@@ -322,6 +322,8 @@ def _rows(t: Optional[torch.Tensor], act: torch.dtype, tokens: int, heads: int, 
         st = heads * d  # of one token any stride will do
     if se != 1 or (sh != d and heads > 1) or (dense and st != heads * d):
         raise ValueError(f"{name} must be contiguous" + ("" if dense else " within each token"))
+    if st < heads * d:  # 0, a broadcast token, would be read as dense rows
+        raise ValueError(f"{name}'s token stride {st} is less than its {heads} x {d} elements")
     return t.data_ptr(), st
 
 
