@@ -1190,9 +1190,6 @@ struct Softmax {
         k += steps;
         continue;
       }
-      // keys from here on are no row's (those of a sequence that does not hold
-      // the whole prefix, in its group's tile, are computed and read by nobody)
-      const int lim = it.kend;
       // (a negative scale's sign is in the scores; a zero one must not meet
       // the -inf of a masked score as a zero)
       const float qsc = fmaxf(fabsf(score_scale(a, it.kvh)), 1e-37f);
@@ -1226,7 +1223,8 @@ struct Softmax {
         }
         if (!named_bar_and(pair, 64, there && ok)) return false;
         if (mine) {
-          step(k, key0, b / BPT, lim, live, qsc, num, v_empty, m, l);
+          // (counted from the step's first key: positions end at the end of 32 bits)
+          step(k, it.kend - key0, b / BPT, live, qsc, num, v_empty, m, l);
           if (b > 0 && b / BPT % kChain == 0) flush(k, num, live, b / BPT == kChain, v_empty);
         }
         tc_fence_before_sync();
@@ -1237,19 +1235,21 @@ struct Softmax {
     }
   }
 
-  // One step's scores (in tensor memory) to P over them; m and l follow.
-  __device__ __forceinline__ void step(uint32_t k, int key0, int done, int lim, bool live, float qsc,
-                                       uint32_t num, uint64_t *v_empty, float &m, float &l) {
+  // One step's scores (in tensor memory) to P over them; m and l follow.  The
+  // keys from `keys` on are no row's.  (Rows of a sequence that does not hold the
+  // whole prefix, in its group's tile, are computed, and read by nobody.)
+  __device__ __forceinline__ void step(uint32_t k, int keys, int done, bool live, float qsc, uint32_t num,
+                                       uint64_t *v_empty, float &m, float &l) {
     const uint32_t scol = trow + C::S_COL + (k & 1) * KT + 64 * h;
-    const int kh = key0 + 64 * h;
+    const int mine = keys - 64 * h;
     // 32 scores, keys past the item's last out
     auto load = [&](int c, uint32_t(&x)[32]) {
       tmem_ld32_async(scol + 32 * c, x);
       tmem_wait_ld(x);
-      if (kh + 32 * c + 32 > lim) {
+      if (32 * c + 32 > mine) {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-          if (kh + 32 * c + i >= lim) x[i] = __float_as_uint(-INFINITY);
+          if (32 * c + i >= mine) x[i] = __float_as_uint(-INFINITY);
       }
     };
     uint32_t sc[32];
