@@ -251,7 +251,8 @@ PA_API pa_status pa_cache_write(const pa_kv_desc *desc, const void *k, const voi
  *                  scheme) is a table with its angles (and its magnitude
  *                  factor) in it.
  *   max_position : rows of cos_sin; positions lie in [0, max_position) (one out
- *                  of range takes position 0's angles).
+ *                  of range takes position 0's angles, and is reported with
+ *                  check_indices unless its token is padding).
  *   rotary_dim   : dims of a head that rotate, the first ones; a multiple of
  *                  16, at most head_dim; 0 means head_dim.
  *   interleaved  : 0: dim i rotates with dim i + rotary_dim / 2; 1: dim 2 i
@@ -309,7 +310,8 @@ PA_API pa_status pa_qk_norm_rope(const pa_kv_desc *desc, const pa_rope_desc *rop
  *                  from one token to the next (a multiple of 8, 0: dense);
  *                  neither normed nor rotated.
  *   slot_mapping : as in pa_cache_write; a token with a negative slot (padding)
- *                  writes no cache row, its query is computed all the same.
+ *                  writes no cache row, its query is computed all the same;
+ *                  its position may hold anything (see max_position).
  * A 16-bit cache receives what pa_qk_norm_rope followed by pa_cache_write
  * stores, bit for bit.  An 8-bit cache receives the keys encoded from their
  * fp32 values (pa_cache_write's encoding, without the rounding to 16 bits

@@ -190,13 +190,15 @@ __device__ __forceinline__ void store_row(const RopeArgs &a, int64_t token, int 
   }
 }
 
-// A token's position (0 in place of one out of range: a padding token's may
-// be anything), and its cache slot (-1: none; with checked indices also for
-// one out of range).  Checked, both are reported.
+// A token's position (0 in place of one out of range), and its cache slot
+// (-1: none; with checked indices also for one out of range).  Checked, both
+// are reported, but for the position of a padding token (one with a negative
+// slot), which may be anything.
+template <bool APPEND>
 __device__ __forceinline__ int position_of(const RopeArgs &a, int64_t token, bool report) {
   const int pos = __ldg(a.positions + token);
   if (static_cast<uint32_t>(pos) < static_cast<uint32_t>(a.max_position)) return pos;
-  if (a.checked && report) report_error(a.err, nullptr, kErrBadIndex);
+  if (a.checked && report && !(APPEND && __ldg(a.slots + token) < 0)) report_error(a.err, nullptr, kErrBadIndex);
   return 0;
 }
 __device__ __forceinline__ int64_t slot_of(const RopeArgs &a, int64_t token, bool report) {
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a) {
                                  : a.k + token * a.k_stride + static_cast<int64_t>(h - a.num_q) * D;
     xa = reinterpret_cast<const uint4 *>(src)[ln.ca];
     xb = reinterpret_cast<const uint4 *>(src)[ln.cb];
-    ln.angles(a.table + static_cast<int64_t>(position_of(a, token, l == 0)) * a.rd, a.rd, cs, sn);
+    ln.angles(a.table + static_cast<int64_t>(position_of<APPEND>(a, token, l == 0)) * a.rd, a.rd, cs, sn);
     if constexpr (APPEND) slot = slot_of(a, token, l == 0);
   }
   float fa[8], fb[8];
@@ -314,7 +316,7 @@ __global__ void __launch_bounds__((kStreamWarps + 1) * 32, 1) rope_stream_kernel
       const int n = static_cast<int>(min(static_cast<int64_t>(p.tokens), num_tokens - t0));
       const int i = lane >> 2, part = lane & 3;  // up to 8 tokens x (q, k, v, table)
       int pos = 0;
-      if (i < n && part == 3) pos = position_of(a, t0 + i, true);
+      if (i < n && part == 3) pos = position_of<APPEND>(a, t0 + i, true);
       if (!mbar_wait(&empty[st], par ^ 1, p.wait_ns)) {
         ok = false;
         break;
