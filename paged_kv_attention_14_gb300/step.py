@@ -213,8 +213,11 @@ class MixedStep:
     def __call__(self, k_new, v_new, slot_mapping, dec_args=None, pf_args=None, groups=None):
         """dec_args: (q, block_tables, context_lens); pf_args: (q, query_start_loc,
         block_tables, context_lens); groups: the decode sequences' shared
-        prefixes (above)."""
+        prefixes (above); such a step writes its new rows at ``slot_mapping``
+        whatever ``decode_append`` and ``write_in_step`` say."""
         if groups is not None:
+            if slot_mapping is None and k_new is not None:  # (the shared decode does not append)
+                raise ValueError("a step with groups needs a slot_mapping for its new rows")
             if slot_mapping is not None and slot_mapping.numel() > 0:
                 B.pa_cache_write(self.desc, k_new, v_new, self.k_cache, self.v_cache, slot_mapping)
             self.attend(dec_args, pf_args, groups)
