@@ -200,7 +200,7 @@ class MixedStep:
         (block_tables, context_lens); pf_args: (query_start_loc, block_tables,
         context_lens)."""
         n = 0
-        if dec_args is not None and self.decode_out is not None:
+        if dec_args is not None:  # (also for a step without decode outputs: their rows are there)
             n = int(dec_args[1].shape[0])
             if n > q.shape[0]:
                 raise ValueError(f"q has {q.shape[0]} rows for {n} decode sequences")

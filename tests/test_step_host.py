@@ -64,3 +64,19 @@ def test_groups_without_slots_for_the_new_rows_are_refused(calls, append):
 def test_groups_without_new_rows_only_attend(calls):
     _step()(None, None, None, _decode_args(), groups=GROUPS)
     assert [c[0] for c in calls] == ["pa_decode_shared"]
+
+
+@pytest.mark.parametrize("decode", [True, False])
+def test_the_chunks_queries_follow_the_decode_sequences(calls, decode):
+    """q_rot holds the decode sequences' rows first, also for a step without decode outputs."""
+    T = S + 5
+    q_rot = torch.arange(T * HQ * D, dtype=torch.float32).to(torch.bfloat16).view(T, HQ, D)
+    q = torch.zeros_like(q_rot)
+    kv = torch.zeros(T, HKV, D, dtype=torch.bfloat16)
+    _, tables, lens = _decode_args()
+    pf = (torch.tensor([0, 5], dtype=torch.int32), torch.zeros(1, 4, dtype=torch.int32), torch.tensor([5], dtype=torch.int32))
+    _step(decode=decode, prefill=True).projected(None, q_rot, q, kv, kv, torch.zeros(T, dtype=torch.int32),
+                                                 torch.arange(T), (tables, lens), pf)
+    assert [c[0] for c in calls] == ["pa_rope_cache_write"] + ["pa_decode"] * decode + ["pa_prefill_chunk"]
+    rows = calls[-1][1][2]
+    assert rows.data_ptr() == q_rot[S:].data_ptr() and rows.shape[0] == 5
