@@ -131,7 +131,8 @@ typedef enum {
                                     65536, beyond its fp16 products; the rows
                                     using it are wrong: use
                                     PA_PREFILL_TCGEN05_PAIR (V) or
-                                    PA_PREFILL_MMA_SYNC                       */
+                                    PA_PREFILL_MMA_SYNC.  pa_decode_shared
+                                    with an 8-bit cache: such a q value       */
 #define PA_DEVERR_REFCOUNT 8     /* pa_release_blocks met a page with no owner
                                     left; that entry was left untouched        */
 
@@ -582,8 +583,10 @@ PA_API size_t pa_decode_shared_workspace_size(const pa_kv_desc *desc, int32_t nu
 
 /*
  * pa_decode for a batch whose sequences share prefixes: the same arguments
- * and the same results (up to fp32 rounding), with each shared prefix read
- * once for all the sequences of its group instead of once per sequence
+ * and the same results (up to rounding: weights as pairs of 16-bit values, sums
+ * in fp32), with each shared prefix read once for all the sequences of its group
+ * instead of once per sequence (from device memory; an SM takes 128 / (query
+ * heads per kv head) sequences at a time)
  * ("Zero-Copy Cache Hits" of "1. Technical Mechanics of the Radix Cache" bind
  * the sequences of a prefix hit to the same pages).  One call does what
  * pa_prefix_attention, pa_decode over the own parts and pa_merge_partials do
@@ -603,8 +606,9 @@ PA_API size_t pa_decode_shared_workspace_size(const pa_kv_desc *desc, int32_t nu
  *   max_prefix_len : an upper bound of prefix_lens (host value).
  *   workspace   : pa_decode_shared_workspace_size() bytes, 16-byte aligned.
  * num_groups == 0 is a plain decode.  out and lse may be pinned host memory,
- * as in pa_decode.  With an 8-bit cache the queries are used in fp16: a finite
- * |q| >= 65520 sets PA_DEVERR_FP16_RANGE in desc->error_word.  With
+ * as in pa_decode.  With an 8-bit cache the queries are used in fp16, as in
+ * pa_decode (below 2^-14 they are off by up to 2^-25): a finite |q| >= 65520 sets
+ * PA_DEVERR_FP16_RANGE in desc->error_word.  With
  * check_indices the group arrays are checked too (values out of range are
  * reported and clamped; without it they are clamped in silence).  Errors on
  * the device are reported in desc->error_word only.

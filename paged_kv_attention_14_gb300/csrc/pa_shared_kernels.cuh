@@ -25,7 +25,8 @@
 // The attention runs on tcgen05 for every item, a sequence's few heads
 // included: an M 128 product costs the tensor cores the same whatever its
 // live rows, 24 products of K 16 per 128 keys (8 for Q K^T, 16 for P V with P
-// as a hi + lo pair) -- about 1,900 cycles, less than the 2,850 in which the
+// as a hi + lo pair) -- about 1,500 cycles (the tensor pipe's active time over
+// the steps of 64 sequences on 16384 tokens), less than the 2,850 in which the
 // SM's share of the measured HBM rate brings those 128 keys (64 KB of bf16).
 // Roles (warps) of the attend kernel:
 //   0  issues Q K^T (one thread), one step ahead of
@@ -43,22 +44,41 @@
 //
 // Measured, us a call in a captured graph (in brackets what the bytes take at
 // the measured HBM rate, 6.69 TB/s), 32 / 8 heads of 128, bf16:
-//   8 sequences on one document of 131072 tokens    100.1 (81.0)
-//   four groups of 16 on 4096 tokens, own 16-511     36.7 (20.8)
-//   64 sequences on 16384 tokens, own 16-511         46.9 (21.4)
-//   E4M3, 40 / 8 heads, 128 sequences, own 1-1000    88.9 (23.0)
-// What bounds it: the document, HBM (75% of its peak rate inside the attention
-// kernel), the rest is the chain of three launches: 3.6 us of plan, 5 to 10
-// of join.  Wide tiles, the softmax: 1,900 of the 2,150 cycles a step
-// takes, on the two warps of a scheduler.  8-bit caches, shared memory: per
-// 128 keys the products read 128 KB (Q, K, and V twice), the widening reads 32
-// and writes 64, the copies write 32, together 2,050 cycles of a step's 2,700
-// at 128 bytes a cycle; the conversion itself costs nothing (E5M2 by byte
-// moves instead: no change), nor does its order (two warps for K and two for
-// V: 88.4 us).
-// Short items, the latency of one step after another (narrow ones some 2,300
-// cycles a step) and instruction fetch: the roles run different code at once,
-// so their loops are short and the waits' slow path is one function.
+//   8 sequences on one document of 131072 tokens     97.3 (81.0)
+//   four groups of 16 on 4096 tokens, own 16-511     36.9 (20.8)
+//   64 sequences on 16384 tokens, own 16-511         47.5 (21.4)
+//   E4M3, 40 / 8 heads, 128 sequences, own 1-1000    84.6 (23.0)
+// What bounds it, from the clock read at the roles' phases (1.9 GHz):
+//  * the document, HBM (75% of its peak rate inside the attention kernel); the
+//    rest is the chain of three launches, 3.6 us of plan and 5 to 10 of join.
+//  * 64 sequences on one prompt, the softmax: the 85 SMs with the prefix take 24
+//    or 25 steps of 2,200 cycles, 1,810 of them from a step's scores to its P,
+//    55,000 of the kernel's 72,000 cycles.  6,500 go by before the first product
+//    (the plan is read, the first copies land, code is fetched cold), 4,000 in
+//    the flush of the sums (kChain), 5,700 in the output.  The SMs with own
+//    parts are done after 20 to 30 of the 38.8 us: a block weighs the same on
+//    the axis in an item of either kind.
+//  * the E4M3 batch, the latency of a step: 39 to 46 steps an SM, one every
+//    2,970 cycles.  Two are in flight (two score buffers), each for some 5,900
+//    from its Q K^T to the end of its P V, 2,400 of them in the softmax where a
+//    16-bit cache's narrow items take 1,870: shared memory is busy.  Per 128
+//    keys the products read 128 KB (Q, K, and V twice), the widening reads 32
+//    and writes 64, the copies write 32, together 2,050 cycles at 128 bytes a
+//    cycle.  The conversion itself costs nothing (E5M2 by byte moves instead:
+//    no change), nor does its order (two warps for K and two for V: the same).
+//  * short items, the same latency (16-bit narrow ones some 2,300 cycles a step)
+//    and instruction fetch: the roles run different code at once, so their loops
+//    are short and the waits' slow path is one function.
+//
+// Fewer bits than fp32, and why.  The products take 16-bit operands.  P as one
+// such value would leave 2^-8 (bf16) or 2^-11 (fp16) of each weight; the pair
+// leaves 2^-16 or 2^-22 and costs a second product, which the tensor cores have
+// room for; a third part would cost as much again.  Queries of an 8-bit cache
+// become fp16 (see widen).  Exponentials are ex2.approx, 2^-22.  O loses to the
+// products' truncation (see kChain).  Error against 64 bits, relative in the
+// 2-norm, and that of fp32 PyTorch operations: document 5.1e-6 (6.5e-6), one
+// prompt 4.7e-6 (2.3e-6), four groups 4.6e-6 (1.2e-6), E4M3 batch 2.5e-6
+// (8.6e-7), four sequences of some 30 tokens 2.1e-6 (1.1e-7).
 #pragma once
 
 #include <cuda.h>
@@ -86,7 +106,8 @@ constexpr float kRaise = 8.f;
 // 64 sequences on one prompt of 16384 tokens (16-bit, from 6) 49.1 / 48.8 /
 // 48.4 / 46.9 / 47.9 us; narrow ones' 4 / 6 / 8 / 10: four groups of 16 on
 // 4096 tokens (16-bit) 39.4 / 37.3 / 36.3 / 38.0 us, the E4M3 batch 85.2 /
-// 84.2 / 86.3 / 87.9 us.
+// 84.2 / 86.3 / 87.9 us.  (All at head_dim 128; own parts weigh as narrow items,
+// and a tile as its group's fullest one.)
 constexpr int kNarrowUnits16 = 8, kNarrowUnits8 = 6, kWideUnits = 24;
 
 constexpr int kQBox = 8;  // sequences of a copy of queries
@@ -209,7 +230,7 @@ constexpr int NIQ = 4;  // items in flight between the roles
 // half a unit of its last place on average with every product, always towards
 // zero.  After a chain of this many steps O goes to sums in the workspace,
 // whose additions round, and starts again.  Relative error of a prefix of
-// 131072 tokens, in pieces of some 108 steps, against 64 bits (and us a call):
+// 131072 tokens, in pieces of some 55 steps, against 64 bits (and us a call):
 // 1.6e-5 without chains (97.8), 7.1e-6 with 24 (99.3), 5.1e-6 with 16
 // (100.1), 3.4e-6 with 8 (101.2); 64 sequences on 16384 tokens, pieces of some
 // 20 steps: 7.3e-6 without (44.9), 4.7e-6 with 16 (46.9), 3.3e-6 with 8 (49.4).
