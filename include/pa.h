@@ -91,7 +91,8 @@ extern "C" {
  *    pa_mixed_attention_append.
  *    Added without a new version (nothing before them changed):
  *    pa_rope_desc, pa_qk_norm_rope, pa_rope_cache_write,
- *    pa_decode_shared_workspace_size, pa_decode_shared. */
+ *    pa_decode_shared_workspace_size, pa_decode_shared, PA_KV_INT4,
+ *    PA_KV_INT4_F16, pa_widen_blocks. */
 #define PA_ABI_VERSION 4
 
 /* Symbols of the shared library; everything else in it stays hidden. */
@@ -116,10 +117,33 @@ typedef enum {
   PA_KV_BF16 = 0,     /* bf16 K/V, bit copies of the written values          */
   PA_KV_FP8_E4M3 = 1, /* OCP E4M3 bytes, fp32 scales per tensor or kv head */
   PA_KV_FP8_E5M2 = 2, /* OCP E5M2 bytes, fp32 scales per tensor or kv head */
-  PA_KV_F16 = 3       /* fp16 K/V of an fp16 model: q and the written rows
+  PA_KV_F16 = 3,      /* fp16 K/V of an fp16 model: q and the written rows
                          are fp16 too; bit copies ("Block-Paged KV Cache
                          (FP8/FP16)")                                      */
+  PA_KV_INT4 = 16,    /* (types below 8 bits count from 16) 4-bit codes with a scale and a minimum per 64 dims
+                         (below); q and the written rows are bf16          */
+  PA_KV_INT4_F16 = 17 /* the same cache of an fp16 model: q and the written
+                         rows are fp16                                     */
 } pa_kv_dtype;
+
+/*
+ * The 4-bit cache (PA_KV_INT4, PA_KV_INT4_F16).  Each of k_cache and v_cache
+ * is [num_blocks][num_kv_heads][PA_INT4_TILE_BYTES(head_dim)] bytes; the tile
+ * of a block and kv head holds
+ *   uint8 codes[16][head_dim / 2]        the code of an even dim in the low half
+ *   fp16  pairs[16][head_dim / 64][2]    (scale, minimum) of each 64 dims
+ * of its 16 rows.  A dim reads as scale * code + minimum.  pa_cache_write
+ * stores, for the 64 dims x of a group, minimum = fp16(min x), scale =
+ * fp16((max x - min x) / 15) and codes clamp(rint((x - minimum) * (1 / scale)),
+ * 0, 15), in fp32 arithmetic rounded to nearest even; a group with a value
+ * that is not finite, or whose scale or minimum passes fp16 (reported as
+ * PA_DEVERR_FP16_RANGE), reads as NaN.
+ * Calls that take it: pa_cache_write, pa_decode, pa_decode_static,
+ * pa_decode_workspace_size, pa_widen_blocks, pa_copy_blocks, pa_bind_blocks,
+ * pa_release_blocks, and pa_qk_norm_rope, which takes its activation type; the
+ * others return PA_ERR_UNSUPPORTED.
+ */
+#define PA_INT4_TILE_BYTES(head_dim) (9 * (head_dim))
 
 /* Bits the kernels OR into an error word (see "Failures on the device"). */
 #define PA_DEVERR_WAIT_TIMEOUT 1 /* a bounded wait ran out; outputs incomplete */
@@ -636,6 +660,24 @@ PA_API pa_status pa_decode_shared(const pa_kv_desc *desc, float *out, float *lse
  */
 PA_API pa_status pa_copy_blocks(const pa_kv_desc *desc, void *k_cache, void *v_cache, const int32_t *src_blocks,
                                 const int32_t *dst_blocks, int32_t num_pairs, pa_stream_t stream);
+
+/*
+ * Pages of a 4-bit cache to 16 bits: for every i < num_pairs, block
+ * dst_blocks[i] of k_out and v_out receives the values of block src_blocks[i]
+ * of k_cache and v_cache (every kv head and slot), each scale * code + minimum
+ * rounded once to the activation type.  k_out and v_out are caches of
+ * num_out_blocks blocks in that type (PA_KV_BF16; PA_KV_F16 for
+ * PA_KV_INT4_F16), so a chunk that follows a 4-bit prefix is attended by
+ * pa_prefill_chunk over the widened pages.  A src may repeat.
+ *   src_blocks : int32 [num_pairs] in [0, num_blocks); dst_blocks : int32
+ *                [num_pairs] in [0, num_out_blocks), no dst twice.
+ * Outputs must not overlap the 4-bit cache.  With check_indices a pair naming a
+ * block outside either cache is skipped and reported.  num_pairs == 0 enqueues
+ * nothing and returns PA_OK.
+ */
+PA_API pa_status pa_widen_blocks(const pa_kv_desc *desc, const void *k_cache, const void *v_cache,
+                                 const int32_t *src_blocks, void *k_out, void *v_out, const int32_t *dst_blocks,
+                                 int32_t num_out_blocks, int32_t num_pairs, pa_stream_t stream);
 
 /*
  * Prefix-cache page bookkeeping on the device ("1. Technical Mechanics of

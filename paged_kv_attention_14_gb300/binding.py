@@ -29,6 +29,8 @@ PA_KV_BF16 = 0
 PA_KV_FP8_E4M3 = 1
 PA_KV_FP8_E5M2 = 2
 PA_KV_F16 = 3
+PA_KV_INT4 = 16
+PA_KV_INT4_F16 = 17
 
 PA_DECODE_AUTO = 0
 PA_DECODE_SIMT = 1
@@ -53,7 +55,7 @@ EXPORTED = ("pa_abi_version", "pa_last_error", "pa_cache_write", "pa_decode_work
             "pa_mixed_workspace_size", "pa_mixed_attention", "pa_prefill_workspace_size",
             "pa_prefill_chunk_balanced", "pa_test_prefill_schedule", "pa_prefill_balanced_chosen",
             "pa_decode_append", "pa_mixed_attention_append", "pa_qk_norm_rope", "pa_rope_cache_write",
-            "pa_decode_shared_workspace_size", "pa_decode_shared")
+            "pa_decode_shared_workspace_size", "pa_decode_shared", "pa_widen_blocks")
 
 
 class PaKvDesc(ctypes.Structure):
@@ -149,6 +151,8 @@ def load(path: Optional[str] = None):
         lib.pa_prefix_attention.restype = ctypes.c_int
         lib.pa_copy_blocks.argtypes = [D, P, P, P, P, I32, P]
         lib.pa_copy_blocks.restype = ctypes.c_int
+        lib.pa_widen_blocks.argtypes = [D, P, P, P, P, P, P, I32, I32, P]
+        lib.pa_widen_blocks.restype = ctypes.c_int
         lib.pa_merge_partials.argtypes = [P, P, P, P, P, I32, I32, I32, I32, P]
         lib.pa_merge_partials.restype = ctypes.c_int
         lib.pa_decode_static.argtypes = [D, P, P, P, P, P, P, I32, P, I32, I32, F, P]
@@ -249,8 +253,9 @@ _F16 = (torch.float16,)
 
 
 def _act(desc) -> tuple:
-    """Element type of q and of new K/V rows: fp16 with an fp16 cache, else bf16."""
-    return _F16 if desc.kv_dtype == PA_KV_F16 else _BF16
+    """Element type of q and of new K/V rows: that of a 16-bit cache, fp16 with
+    PA_KV_INT4_F16, else bf16."""
+    return _F16 if desc.kv_dtype in (PA_KV_F16, PA_KV_INT4_F16) else _BF16
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 _I64 = (torch.int64,)
@@ -388,15 +393,50 @@ def pa_rope_cache_write(desc: PaKvDesc, rope: PaRopeDesc, q_out, q, k, v, positi
 
 #: element types a cache tensor of each descriptor type may have
 _CACHE_OF = {PA_KV_BF16: (torch.bfloat16,), PA_KV_F16: (torch.float16,),
-             PA_KV_FP8_E4M3: (torch.uint8, torch.float8_e4m3fn), PA_KV_FP8_E5M2: (torch.uint8, torch.float8_e5m2)}
+             PA_KV_FP8_E4M3: (torch.uint8, torch.float8_e4m3fn), PA_KV_FP8_E5M2: (torch.uint8, torch.float8_e5m2),
+             PA_KV_INT4: (torch.uint8,), PA_KV_INT4_F16: (torch.uint8,)}
 
 
 def _cache_at(t, desc: PaKvDesc, name: str, dev: int):
     """The address of a cache of the descriptor's type and size on the current device."""
     p = _at(t, _CACHE_OF[desc.kv_dtype], name, dev)
-    if t.numel() != desc.num_blocks * desc.num_kv_heads * 16 * desc.head_dim:
+    if desc.kv_dtype in (PA_KV_INT4, PA_KV_INT4_F16):
+        if t.numel() != desc.num_blocks * desc.num_kv_heads * int4_tile_bytes(desc.head_dim):
+            raise ValueError(f"{name} must be [num_blocks, num_kv_heads, int4_tile_bytes(head_dim)]")
+    elif t.numel() != desc.num_blocks * desc.num_kv_heads * 16 * desc.head_dim:
         raise ValueError(f"{name} must be [num_blocks, num_kv_heads, 16, head_dim]")
     return p
+
+
+def int4_tile_bytes(head_dim: int) -> int:
+    """Bytes of one (block, kv head) of a 4-bit cache: 16 rows of codes and of (scale, minimum) pairs."""
+    return 9 * head_dim
+
+
+def int4_cache(num_blocks: int, num_kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
+    """A K or V cache of PA_KV_INT4 / PA_KV_INT4_F16, every row reading as zeros."""
+    return torch.zeros((num_blocks, num_kv_heads, int4_tile_bytes(head_dim)), dtype=torch.uint8,
+                       device=device or "cuda")
+
+
+def pa_widen_blocks(desc: PaKvDesc, k_cache, v_cache, src_blocks, k_out, v_out, dst_blocks, stream=None):
+    """Blocks src_blocks[i] of a 4-bit cache to blocks dst_blocks[i] of k_out and
+    v_out ``[num_out_blocks, Hkv, 16, D]`` in the activation type (int32 block ids)."""
+    act, = _act(desc)
+    n, d = src_blocks.shape[0], desc.head_dim
+    if dst_blocks.shape[0] != n:
+        raise ValueError("src_blocks and dst_blocks must have one entry per pair")
+    if desc.kv_dtype not in (PA_KV_INT4, PA_KV_INT4_F16):
+        raise ValueError("pa_widen_blocks reads a 4-bit cache (PA_KV_INT4, PA_KV_INT4_F16)")
+    st = _launch_stream(stream, k_cache)
+    dev = k_cache.get_device()
+    ko, vo = _at(k_out, (act,), "k_out", dev), _at(v_out, (act,), "v_out", dev)
+    nb = k_out.shape[0]
+    if k_out.shape != (nb, desc.num_kv_heads, 16, d) or v_out.shape != k_out.shape:
+        raise ValueError("k_out and v_out must be [num_out_blocks, num_kv_heads, 16, head_dim]")
+    _check(load().pa_widen_blocks(ctypes.byref(desc), _cache_at(k_cache, desc, "k_cache", dev),
+                                  _cache_at(v_cache, desc, "v_cache", dev), _at(src_blocks, _I32, "src_blocks", dev),
+                                  ko, vo, _at(dst_blocks, _I32, "dst_blocks", dev), nb, n, st))
 
 
 def pa_decode_workspace_size(desc: PaKvDesc, num_seqs: int, max_context_len: int) -> int:

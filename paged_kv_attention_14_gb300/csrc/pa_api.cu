@@ -30,7 +30,10 @@ pa_status ok() {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-pa_status check_desc(const pa_kv_desc *d) {
+bool is_int4(const pa_kv_desc &d) { return d.kv_dtype == PA_KV_INT4 || d.kv_dtype == PA_KV_INT4_F16; }
+
+// int4: whether the call takes a 4-bit cache
+pa_status check_desc(const pa_kv_desc *d, bool int4 = false) {
   if (!d) return fail(PA_ERR_INVALID_ARG, "desc is NULL%s");
   if (d->block_size != 16) return fail(PA_ERR_UNSUPPORTED, "block_size must be 16%s");
   if (d->head_dim != 64 && d->head_dim != 128)
@@ -42,8 +45,11 @@ pa_status check_desc(const pa_kv_desc *d) {
   if (d->num_q_heads / d->num_kv_heads > 16)
     return fail(PA_ERR_UNSUPPORTED, "group size num_q_heads / num_kv_heads must be <= 16%s");
   if (d->kv_dtype != PA_KV_BF16 && d->kv_dtype != PA_KV_FP8_E4M3 && d->kv_dtype != PA_KV_FP8_E5M2 &&
-      d->kv_dtype != PA_KV_F16)
-    return fail(PA_ERR_INVALID_ARG, "kv_dtype must be PA_KV_BF16, PA_KV_F16, PA_KV_FP8_E4M3 or PA_KV_FP8_E5M2%s");
+      d->kv_dtype != PA_KV_F16 && !is_int4(*d))
+    return fail(PA_ERR_INVALID_ARG, "kv_dtype must be PA_KV_BF16, PA_KV_F16, PA_KV_FP8_E4M3, PA_KV_FP8_E5M2, "
+                                    "PA_KV_INT4 or PA_KV_INT4_F16%s");
+  if (!int4 && is_int4(*d))
+    return fail(PA_ERR_UNSUPPORTED, "this call takes no 4-bit cache (widen its pages with pa_widen_blocks)%s");
   if (d->num_blocks < 0) return fail(PA_ERR_INVALID_ARG, "num_blocks must be >= 0%s");
   if (d->sliding_window < 0 || d->attention_chunk < 0)
     return fail(PA_ERR_INVALID_ARG, "sliding_window and attention_chunk must be >= 0%s");
@@ -125,7 +131,7 @@ pa_status validate_decode(const pa_kv_desc *desc, const float *out, const float 
                           const void *k_cache, const void *v_cache, const int32_t *block_tables,
                           int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
                           int32_t max_context_len, float scale, DecodePlan *plan) {
-  pa_status st = check_desc(desc);
+  pa_status st = check_desc(desc, true);
   if (st != PA_OK) return st;
   if (num_seqs < 0) return fail(PA_ERR_INVALID_ARG, "num_seqs must be >= 0%s");
   if (num_seqs == 0) return PA_OK;
@@ -187,7 +193,7 @@ const char *pa_last_error(void) { return g_last_error; }
 pa_status pa_cache_write(const pa_kv_desc *desc, const void *k, const void *v, void *k_cache,
                          void *v_cache, const int64_t *slot_mapping, int32_t num_tokens,
                          pa_stream_t stream) {
-  pa_status st = check_desc(desc);
+  pa_status st = check_desc(desc, true);
   if (st != PA_OK) return st;
   if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens must be >= 0%s");
   if (num_tokens == 0) return ok();
@@ -197,15 +203,17 @@ pa_status pa_cache_write(const pa_kv_desc *desc, const void *k, const void *v, v
     return fail(PA_ERR_INVALID_ARG, "k, v, k_cache and v_cache must be 16-byte aligned%s");
   if (!aligned16(slot_mapping) && (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
     return fail(PA_ERR_INVALID_ARG, "slot_mapping must be 8-byte aligned%s");
-  const cudaError_t e = pa::launch_cache_write(*desc, k, v, k_cache, v_cache, slot_mapping,
-                                               num_tokens, reinterpret_cast<cudaStream_t>(stream));
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      is_int4(*desc) ? pa::launch_int4_write(*desc, k, v, k_cache, v_cache, slot_mapping, num_tokens, s)
+                     : pa::launch_cache_write(*desc, k, v, k_cache, v_cache, slot_mapping, num_tokens, s);
   return e == cudaSuccess ? ok() : cuda_fail(e);
 }
 
 pa_status pa_qk_norm_rope(const pa_kv_desc *desc, const pa_rope_desc *rope, void *q_out, void *k_out, const void *q,
                           int64_t q_stride, const void *k, int64_t k_stride, const int32_t *positions,
                           int32_t num_tokens, pa_stream_t stream) {
-  pa_status st = check_desc(desc);
+  pa_status st = check_desc(desc, true);
   if (st != PA_OK) return st;
   if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens must be >= 0%s");
   if (num_tokens == 0) return ok();
@@ -246,7 +254,7 @@ pa_status pa_rope_cache_write(const pa_kv_desc *desc, const pa_rope_desc *rope, 
 
 size_t pa_decode_workspace_size(const pa_kv_desc *desc, int32_t num_seqs, int32_t max_context_len) {
   (void)max_context_len;
-  if (check_desc(desc) != PA_OK || num_seqs < 0) return 0;
+  if (check_desc(desc, true) != PA_OK || num_seqs < 0) return 0;
   pa::DecodePlan plan;
   const char *why = "";
   if (pa::plan_decode(*desc, num_seqs, &plan, &why) != PA_OK) {
@@ -578,7 +586,7 @@ pa_status pa_prefix_attention(const pa_kv_desc *desc, float *out, float *lse, co
 
 pa_status pa_copy_blocks(const pa_kv_desc *desc, void *k_cache, void *v_cache, const int32_t *src_blocks,
                          const int32_t *dst_blocks, int32_t num_pairs, pa_stream_t stream) {
-  pa_status st = check_desc(desc);
+  pa_status st = check_desc(desc, true);
   if (st != PA_OK) return st;
   if (num_pairs < 0) return fail(PA_ERR_INVALID_ARG, "num_pairs must be >= 0%s");
   if (num_pairs == 0) return ok();
@@ -593,10 +601,32 @@ pa_status pa_copy_blocks(const pa_kv_desc *desc, void *k_cache, void *v_cache, c
   return e == cudaSuccess ? ok() : cuda_fail(e);
 }
 
+pa_status pa_widen_blocks(const pa_kv_desc *desc, const void *k_cache, const void *v_cache, const int32_t *src_blocks,
+                          void *k_out, void *v_out, const int32_t *dst_blocks, int32_t num_out_blocks,
+                          int32_t num_pairs, pa_stream_t stream) {
+  pa_status st = check_desc(desc, true);
+  if (st != PA_OK) return st;
+  if (!is_int4(*desc))
+    return fail(PA_ERR_INVALID_ARG, "pa_widen_blocks reads a 4-bit cache (PA_KV_INT4, PA_KV_INT4_F16)%s");
+  if (num_pairs < 0 || num_out_blocks < 0)
+    return fail(PA_ERR_INVALID_ARG, "num_pairs and num_out_blocks must be >= 0%s");
+  if (num_pairs == 0) return ok();
+  if (!k_cache || !v_cache || !src_blocks || !k_out || !v_out || !dst_blocks)
+    return fail(PA_ERR_INVALID_ARG,
+                "k_cache, v_cache, src_blocks, k_out, v_out and dst_blocks must be non-NULL%s");
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out))
+    return fail(PA_ERR_INVALID_ARG, "k_cache, v_cache, k_out and v_out must be 16-byte aligned%s");
+  if ((reinterpret_cast<uintptr_t>(src_blocks) & 3u) || (reinterpret_cast<uintptr_t>(dst_blocks) & 3u))
+    return fail(PA_ERR_INVALID_ARG, "src_blocks and dst_blocks must be 4-byte aligned%s");
+  const cudaError_t e = pa::launch_int4_widen(*desc, k_cache, v_cache, src_blocks, k_out, v_out, dst_blocks,
+                                              num_out_blocks, num_pairs, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e);
+}
+
 pa_status pa_bind_blocks(const pa_kv_desc *desc, int32_t *block_tables, int32_t max_blocks_per_seq,
                          int32_t num_table_rows, const int32_t *seq_rows, const int32_t *hit_start,
                          const int32_t *hit_blocks, int32_t num_seqs, int32_t *refcounts, pa_stream_t stream) {
-  pa_status st = check_desc(desc);
+  pa_status st = check_desc(desc, true);
   if (st != PA_OK) return st;
   if (num_seqs < 0 || num_table_rows < 0) return fail(PA_ERR_INVALID_ARG, "num_seqs and num_table_rows must be >= 0%s");
   if (num_seqs == 0) return ok();
@@ -618,7 +648,7 @@ pa_status pa_release_blocks(const pa_kv_desc *desc, int32_t *block_tables, int32
                             int32_t num_table_rows, const int32_t *seq_rows, const int32_t *block_counts,
                             int32_t num_seqs, int32_t *refcounts, int32_t *free_list, int32_t *free_count,
                             pa_stream_t stream) {
-  pa_status st = check_desc(desc);
+  pa_status st = check_desc(desc, true);
   if (st != PA_OK) return st;
   if (num_seqs < 0 || num_table_rows < 0) return fail(PA_ERR_INVALID_ARG, "num_seqs and num_table_rows must be >= 0%s");
   if (num_seqs == 0) return ok();

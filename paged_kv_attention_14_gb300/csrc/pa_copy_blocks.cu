@@ -12,6 +12,7 @@
 // coalesced 16-byte accesses.  With checked indices a pair naming a block
 // outside the cache is skipped and reported.
 #include "pa_device.cuh"
+#include "pa_int4.cuh"
 #include "pa_internal.h"
 
 namespace pa {
@@ -42,8 +43,10 @@ __global__ void __launch_bounds__(256) copy_blocks_kernel(uint4 *__restrict__ k_
 
 cudaError_t launch_copy_blocks(const pa_kv_desc &d, void *k_cache, void *v_cache, const int32_t *src_blocks,
                                const int32_t *dst_blocks, int32_t num_pairs, cudaStream_t stream) {
+  const bool int4 = d.kv_dtype == PA_KV_INT4 || d.kv_dtype == PA_KV_INT4_F16;
   const int esz = (d.kv_dtype == PA_KV_BF16 || d.kv_dtype == PA_KV_F16) ? 2 : 1;
-  const int64_t block_bytes = static_cast<int64_t>(d.num_kv_heads) * d.block_size * d.head_dim * esz;
+  const int64_t block_bytes = static_cast<int64_t>(d.num_kv_heads) *
+                              (int4 ? i4::tile_bytes(d.head_dim) : d.block_size * d.head_dim * esz);
   const int64_t vecs = block_bytes / 16;
   const int64_t total = vecs * num_pairs;
   const int threads = 256;

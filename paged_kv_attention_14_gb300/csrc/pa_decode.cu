@@ -127,6 +127,7 @@ bool make_cache_map(CUtensorMap *map, const void *base, const pa_kv_desc &d, con
 int device_sm_count() { return device_info().sm_count; }
 
 pa_status plan_decode(const pa_kv_desc &d, int32_t num_seqs, DecodePlan *plan, const char **why) {
+  if (d.kv_dtype == PA_KV_INT4 || d.kv_dtype == PA_KV_INT4_F16) return plan_int4_decode(d, plan, why);
   const int g = d.num_q_heads / d.num_kv_heads;
   const int impl = resolve_impl(d);
   if (impl != PA_DECODE_SIMT && impl != PA_DECODE_MMA) {
@@ -153,6 +154,8 @@ pa_status plan_decode(const pa_kv_desc &d, int32_t num_seqs, DecodePlan *plan, c
   plan->num_ctas = device_info().sm_count * occ;
   plan->workspace_bytes =
       dec::ws_layout(num_seqs, plan->num_groups, plan->num_ctas, k.slot_heads, d.head_dim).total;
+  // the error word's 256 bytes, then one counter per sequence and kv head at most
+  plan->zero_bytes = 256 + sizeof(int32_t) * static_cast<size_t>(num_seqs) * d.num_kv_heads;
   return PA_OK;
 }
 
@@ -212,6 +215,9 @@ cudaError_t launch_decode(const pa_kv_desc &d, const DecodePlan &plan, float *ou
                           const int32_t *block_tables, int32_t max_blocks_per_seq,
                           const int32_t *context_lens, int32_t num_seqs, float scale,
                           void *workspace, cudaStream_t stream, const void *k_new, const void *v_new) {
+  if (d.kv_dtype == PA_KV_INT4 || d.kv_dtype == PA_KV_INT4_F16)
+    return launch_int4_decode(d, plan, out, lse, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
+                              num_seqs, scale, workspace, stream);
   const KernelInfo k = kernel_for(d, plan.impl);
   dec::DecodeArgs a;
   if (!dec::make_decode_args(d, plan, out, lse, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,

@@ -82,9 +82,8 @@ PA_API pa_status pa_decode_static(const pa_kv_desc *desc, float *out, float *lse
   cudaError_t e = scratch_address(&scratch);
   if (e != cudaSuccess) return static_fail(PA_ERR_CUDA, cudaGetErrorString(e));
   // The array keeps the previous call's contents: its error word and merge
-  // counters (the first 256 bytes plus one int32 per sequence and kv head)
-  // must start at zero, the rest is rewritten by every launch.
-  const size_t head = 256 + sizeof(int32_t) * static_cast<size_t>(num_seqs) * desc->num_kv_heads;
+  // counters must start at zero, the rest is rewritten by every launch.
+  const size_t head = plan.zero_bytes;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   e = cudaMemsetAsync(scratch, 0, head < plan.workspace_bytes ? head : plan.workspace_bytes, s);
   if (e != cudaSuccess) return static_fail(PA_ERR_CUDA, cudaGetErrorString(e));

@@ -1,0 +1,208 @@
+// pa_int4_pages.cu -- rows into a 4-bit cache, and its pages back to 16 bits.
+//
+// A group of 64 dims x of a row is stored as m = fp16(min x), s = fp16((max x
+// - min x) / 15) and codes n = clamp(rint((x - m) * (1 / s)), 0, 15), 1 / s
+// being the correctly rounded fp32 reciprocal; it reads as s n + m.  s = 0 (all
+// dims alike) stores n = 0.  A group with a value that is not finite, or whose
+// minimum or scale passes fp16, stores NaN for both and reads as NaN.
+#include "pa_int4.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+
+namespace {
+
+template <bool F16>
+struct Act2;
+template <>
+struct Act2<true> {
+  using T = __half2;
+  static __device__ float2 f(T x) { return __half22float2(x); }
+};
+template <>
+struct Act2<false> {
+  using T = __nv_bfloat162;
+  static __device__ float2 f(T x) { return __bfloat1622float2(x); }
+};
+
+// The codes (8 bytes) of 16 dims of a group held by four neighbouring lanes,
+// and the group's (scale, minimum) pair.  range: the group's values are finite
+// but pass fp16.
+template <bool F16>
+__device__ __forceinline__ uint2 encode16(const uint4 &a, const uint4 &b, uint32_t &pair, bool &range) {
+  using A = Act2<F16>;
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  typename A::T x[8], lo, hi;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const typename A::T *>(&w[i]);
+  lo = hi = x[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    lo = __hmin2_nan(lo, x[i]);
+    hi = __hmax2_nan(hi, x[i]);
+  }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    lo = __hmin2_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = __hmax2_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  const float2 l2 = A::f(lo), h2 = A::f(hi);
+  const bool nan = l2.x != l2.x || l2.y != l2.y || h2.x != h2.x || h2.y != h2.y;
+  const float mn = fminf(l2.x, l2.y), mx = fmaxf(h2.x, h2.y);
+  __half s16 = __float2half_rn(__fdiv_rn(mx - mn, 15.f)), m16 = __float2half_rn(mn);
+  const bool ok = !nan && fabsf(__half2float(s16)) <= 65504.f && fabsf(__half2float(m16)) <= 65504.f;
+  range = !ok && !nan && fabsf(mn) <= 3.4e38f && fabsf(mx) <= 3.4e38f;
+  if (!ok) s16 = m16 = __ushort_as_half(0x7fff);
+  pair = static_cast<uint32_t>(__half_as_ushort(s16)) | (static_cast<uint32_t>(__half_as_ushort(m16)) << 16);
+  const float s = __half2float(s16), m = __half2float(m16);
+  const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+  uint32_t c[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float2 f = A::f(x[i / 2]);
+    // rounded to the nearest even whole number by the addition of 1.5 * 2^23;
+    // fmaxf takes the 0 of a NaN
+    const float t = fminf(fmaxf(__fmul_rn((i & 1 ? f.y : f.x) - m, r), 0.f), 15.f);
+    c[i / 8] |= (__float_as_uint(t + 12582912.f) & 15u) << (4 * (i % 8));
+  }
+  return make_uint2(c[0], c[1]);
+}
+
+// One thread moves 16 dims of K and of V: 32 bytes read, 8 bytes of codes
+// written; the first of a group's four threads writes its pair.  Bound by the
+// rows' bytes (2 (2 D + 9 D / 16) per token and kv head); the arithmetic, about
+// 9 instructions a dim, is half of what the SMs issue in that time.
+template <bool F16>
+__global__ void __launch_bounds__(256) int4_write_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v,
+                                                         uint8_t *__restrict__ k_cache, uint8_t *__restrict__ v_cache,
+                                                         const int64_t *__restrict__ slot_mapping, int64_t total,
+                                                         int num_kv_heads, int d, int64_t num_slots, int checked,
+                                                         int32_t *err) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int parts = d / 16;
+  const int64_t row = i / parts;  // token * num_kv_heads + head
+  const int part = static_cast<int>(i - row * parts);
+  int64_t slot = -1;
+  if (i < total) slot = __ldg(slot_mapping + row / num_kv_heads);
+  if (checked && slot >= num_slots) {
+    if (part == 0) report_error(err, nullptr, kErrBadIndex);
+    slot = -1;
+  }
+  // a group's four lanes share a row, so they all have work or none has; the
+  // shuffles take all lanes of the warp
+  const bool live = slot >= 0;
+  const uint4 z = make_uint4(0, 0, 0, 0);
+  const uint4 k0 = live ? __ldg(k + 2 * i) : z, k1 = live ? __ldg(k + 2 * i + 1) : z;
+  const uint4 v0 = live ? __ldg(v + 2 * i) : z, v1 = live ? __ldg(v + 2 * i + 1) : z;
+  uint32_t kp, vp;
+  bool kr, vr;
+  const uint2 kc = encode16<F16>(k0, k1, kp, kr);
+  const uint2 vc = encode16<F16>(v0, v1, vp, vr);
+  if (!live) return;
+  const int64_t tile = ((slot >> 4) * num_kv_heads + row % num_kv_heads) * i4::tile_bytes(d);
+  const int off = static_cast<int>(slot & 15);
+  const int64_t at = tile + off * (d / 2) + part * 8;
+  *reinterpret_cast<uint2 *>(k_cache + at) = kc;
+  *reinterpret_cast<uint2 *>(v_cache + at) = vc;
+  if ((part & 3) == 0) {
+    const int64_t pat = tile + i4::code_bytes(d) + (off * i4::groups(d) + part / 4) * 4;
+    *reinterpret_cast<uint32_t *>(k_cache + pat) = kp;
+    *reinterpret_cast<uint32_t *>(v_cache + pat) = vp;
+    if (kr || vr) report_error(err, nullptr, kErrFp16Range);
+  }
+}
+
+// Eight dims (one word of codes) as s n + m, rounded once to the activation type.
+template <bool F16>
+__device__ __forceinline__ uint4 widen8dims(uint32_t w, uint32_t pair) {
+  const float s = f16lo(pair), m = f16hi(pair);
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // 2^23 + n, less 2^23: n as an fp32 number
+    const float a = __uint_as_float(0x4B000000u | ((w >> (8 * i)) & 15u)) - 8388608.f;
+    const float b = __uint_as_float(0x4B000000u | ((w >> (8 * i + 4)) & 15u)) - 8388608.f;
+    r[i] = F16 ? pack_f16x2(fmaf(s, a, m), fmaf(s, b, m)) : pack_bf16x2(fmaf(s, a, m), fmaf(s, b, m));
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// One warp widens one tile (a page of a kv head) of K or V: every lane has D /
+// 16 words of codes in flight and stores 16 bytes for each, neighbouring lanes
+// neighbouring bytes.  Bound by the bytes (9 D read, 32 D written a tile).
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) int4_widen_kernel(const uint8_t *__restrict__ k_cache,
+                                                         const uint8_t *__restrict__ v_cache,
+                                                         const int32_t *__restrict__ src_blocks,
+                                                         uint8_t *__restrict__ k_out, uint8_t *__restrict__ v_out,
+                                                         const int32_t *__restrict__ dst_blocks, int64_t tiles,
+                                                         int num_kv_heads, int num_blocks, int num_out_blocks,
+                                                         int checked, int32_t *err) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr int kWords = D / 16;  // per lane: 16 rows of D / 8 words
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x / 32);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32; i < tiles; i += warps) {
+    // tile order: page, K or V, kv head
+    const int64_t pair = i / (2 * num_kv_heads);
+    const int r = static_cast<int>(i - pair * 2 * num_kv_heads);
+    const bool is_v = r >= num_kv_heads;
+    const int head = is_v ? r - num_kv_heads : r;
+    const int sb = __ldg(src_blocks + pair), db = __ldg(dst_blocks + pair);
+    if (checked && (sb < 0 || sb >= num_blocks || db < 0 || db >= num_out_blocks)) {
+      if (r == 0 && lane == 0) report_error(err, nullptr, kErrBadIndex);
+      continue;
+    }
+    const uint8_t *src =
+        (is_v ? v_cache : k_cache) + (static_cast<int64_t>(sb) * num_kv_heads + head) * i4::tile_bytes(D);
+    uint8_t *dst = (is_v ? v_out : k_out) + (static_cast<int64_t>(db) * num_kv_heads + head) * (32 * D);
+    const uint32_t *codes = reinterpret_cast<const uint32_t *>(src);
+    const uint32_t *pairs = reinterpret_cast<const uint32_t *>(src + i4::code_bytes(D));
+    uint32_t w[kWords], p[kWords];
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) {
+      const int at = j * 32 + lane;  // word of the tile: eight dims, a 64-dim group has eight words
+      w[j] = __ldg(codes + at);
+      p[j] = __ldg(pairs + at / 8);
+    }
+#pragma unroll
+    for (int j = 0; j < kWords; ++j)
+      *reinterpret_cast<uint4 *>(dst + (j * 32 + lane) * 16) = widen8dims<F16>(w[j], p[j]);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_int4_write(const pa_kv_desc &d, const void *k, const void *v, void *k_cache, void *v_cache,
+                              const int64_t *slot_mapping, int32_t num_tokens, cudaStream_t stream) {
+  const int64_t total = static_cast<int64_t>(num_tokens) * d.num_kv_heads * (d.head_dim / 16);
+  const int threads = 256;
+  const int64_t blocks = (total + threads - 1) / threads;
+  auto kern = d.kv_dtype == PA_KV_INT4_F16 ? &int4_write_kernel<true> : &int4_write_kernel<false>;
+  kern<<<static_cast<unsigned>(blocks), threads, 0, stream>>>(
+      static_cast<const uint4 *>(k), static_cast<const uint4 *>(v), static_cast<uint8_t *>(k_cache),
+      static_cast<uint8_t *>(v_cache), slot_mapping, total, d.num_kv_heads, d.head_dim,
+      static_cast<int64_t>(d.num_blocks) * 16, d.check_indices, d.error_word);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_int4_widen(const pa_kv_desc &d, const void *k_cache, const void *v_cache,
+                              const int32_t *src_blocks, void *k_out, void *v_out, const int32_t *dst_blocks,
+                              int32_t num_out_blocks, int32_t num_pairs, cudaStream_t stream) {
+  const bool f16 = d.kv_dtype == PA_KV_INT4_F16;
+  const int64_t tiles = static_cast<int64_t>(num_pairs) * d.num_kv_heads * 2;
+  const int threads = 256;
+  const int64_t want = (tiles + threads / 32 - 1) / (threads / 32);
+  const int64_t cap = static_cast<int64_t>(device_sm_count()) * 8;
+  const unsigned blocks = static_cast<unsigned>(want < cap ? want : cap);
+  auto kern = d.head_dim == 128 ? (f16 ? &int4_widen_kernel<128, true> : &int4_widen_kernel<128, false>)
+                                : (f16 ? &int4_widen_kernel<64, true> : &int4_widen_kernel<64, false>);
+  kern<<<blocks, threads, 0, stream>>>(static_cast<const uint8_t *>(k_cache), static_cast<const uint8_t *>(v_cache),
+                                       src_blocks, static_cast<uint8_t *>(k_out), static_cast<uint8_t *>(v_out),
+                                       dst_blocks, tiles, d.num_kv_heads, d.num_blocks, num_out_blocks,
+                                       d.check_indices, d.error_word);
+  return cudaGetLastError();
+}
+
+}  // namespace pa

@@ -21,6 +21,14 @@ cudaError_t launch_rope(const pa_kv_desc &d, const pa_rope_desc &r, void *q_out,
                         const int32_t *positions, void *k_cache, void *v_cache, const int64_t *slot_mapping,
                         int32_t num_tokens, cudaStream_t stream);
 
+// A 4-bit cache: rows into it, its pages to 16 bits, and its decode
+// (pa_int4_pages.cu, pa_int4_decode.cu).
+cudaError_t launch_int4_write(const pa_kv_desc &d, const void *k, const void *v, void *k_cache, void *v_cache,
+                              const int64_t *slot_mapping, int32_t num_tokens, cudaStream_t stream);
+cudaError_t launch_int4_widen(const pa_kv_desc &d, const void *k_cache, const void *v_cache,
+                              const int32_t *src_blocks, void *k_out, void *v_out, const int32_t *dst_blocks,
+                              int32_t num_out_blocks, int32_t num_pairs, cudaStream_t stream);
+
 cudaError_t launch_merge(float *out, float *lse_out, const float *part_o, const float *part_lse,
                          const int32_t *num_parts, int32_t num_seqs, int32_t num_heads,
                          int32_t max_parts, int32_t head_dim, cudaStream_t stream);
@@ -32,7 +40,14 @@ struct DecodePlan {
   int num_groups;  // kv head groups per sequence (segments per sequence)
   int num_ctas;    // persistent grid size
   size_t workspace_bytes;
+  size_t zero_bytes;  // of its start, which must be zero before a call (error word, counters)
 };
+
+pa_status plan_int4_decode(const pa_kv_desc &d, DecodePlan *plan, const char **why);
+cudaError_t launch_int4_decode(const pa_kv_desc &d, const DecodePlan &plan, float *out, float *lse, const void *q,
+                               const void *k_cache, const void *v_cache, const int32_t *block_tables,
+                               int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs, float scale,
+                               void *workspace, cudaStream_t stream);
 
 // Fills `plan` for the descriptor; returns PA_OK or an error with a message.
 pa_status plan_decode(const pa_kv_desc &d, int32_t num_seqs, DecodePlan *plan, const char **why);

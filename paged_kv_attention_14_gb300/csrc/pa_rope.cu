@@ -429,8 +429,9 @@ RopeKernels pick_dim(int d, bool inter) {
 
 RopeKernels pick(const pa_kv_desc &d, bool append, bool inter) {
   if (!append)  // the cache type only gives the activation type
-    return d.kv_dtype == PA_KV_F16 ? pick_dim<kKvF16, false>(d.head_dim, inter)
-                                   : pick_dim<kKvBf16, false>(d.head_dim, inter);
+    return d.kv_dtype == PA_KV_F16 || d.kv_dtype == PA_KV_INT4_F16
+               ? pick_dim<kKvF16, false>(d.head_dim, inter)
+               : pick_dim<kKvBf16, false>(d.head_dim, inter);
   switch (d.kv_dtype) {
     case PA_KV_F16: return pick_dim<kKvF16, true>(d.head_dim, inter);
     case PA_KV_FP8_E4M3: return pick_dim<kKvFp8, true>(d.head_dim, inter);
