@@ -26,7 +26,7 @@
 // pair of fp16 (22 bits): rows 8..15 of the operand are the lo halves of rows
 // 0..7 (more than 8 query heads per kv head: a second product).
 //
-// The sums of the tensor cores round towards zero, so they run for 16 stages at
+// The sums of the tensor cores round towards zero, so they run for 8 stages at
 // most and are then added to fp32 registers.
 #include <cuda.h>
 
@@ -38,10 +38,8 @@ namespace pa {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kMinUnits = 4;   // units a warp gets at least, where there are few
-constexpr int kFan = 16;       // pieces joined in one step
-constexpr int kFlush = 16;     // stages between additions to the fp32 sums
+constexpr int kMinUnits = 12;  // units a CTA gets at least, where there are few
+constexpr int kFlush = 8;      // stages between additions to the fp32 sums
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -55,29 +53,62 @@ struct Args {
   int window, chunk;
   int32_t *err, *user_err;
   int checked, num_blocks, f16;
-  int32_t *count1, *count2;  // pieces arrived: [2 workers] and [workers]
-  float2 *slot_ml;           // [2 workers][g]: reference exponent, sum
-  float *slot_o;             // [2 workers][g][D]
+  int32_t *count;   // [CTAs]: pieces arrived of what begins in a CTA and goes on
+  float2 *slot_ml;  // [2 warps][g]: reference exponent, sum
+  float *slot_o;    // [2 warps][g][D]
 };
 
-template <int D>
+template <int D, int NQ>
 struct Cfg {
+  static constexpr int W = NQ == 16 ? 8 : 12;  // warps: as many as the registers allow
   static constexpr int TB = i4::tile_bytes(D);
   static constexpr int STAGE = 4 * TB;  // K and V of two blocks
-  static constexpr int NST = D == 128 ? 6 : 8;
+  static constexpr int NST = D == 64 ? 8 : W == 8 ? 6 : 4;
   static constexpr int RING = NST * STAGE;
-  static constexpr int SMEM = kWarps * RING;
+  static constexpr int SMEM = W * RING;
   static constexpr int NG = D / 64;
 };
 
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+__device__ __forceinline__ uint32_t lds32(const uint8_t *a) { return *reinterpret_cast<const uint32_t *>(a); }
+__device__ __forceinline__ uint2 lds64(const uint8_t *a) { return *reinterpret_cast<const uint2 *>(a); }
+// the pairs of a row: one word a group
+template <int NG>
+__device__ __forceinline__ void load_pairs(const uint8_t *at, uint32_t (&w)[2]) {
+  if constexpr (NG == 2) {
+    const uint2 u = lds64(at);
+    w[0] = u.x;
+    w[1] = u.y;
+  } else {
+    w[0] = lds32(at);
+  }
+}
+// D = A(16x16, row) * B(16x8, col) + C, f16 inputs, fp32 accumulate; free to
+// be scheduled (a function of its operands)
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// ... with C = 0
+__device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                     uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// the halves of an fp16 pair in fp32
+__device__ __forceinline__ float2 halves(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2 *>(&u)); }
+// (x & mask) ^ flip
+__device__ __forceinline__ uint32_t and_xor(uint32_t x, uint32_t mask, uint32_t flip) {
   uint32_t r;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(a));
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(x), "r"(mask), "r"(flip));
   return r;
 }
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 r;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+// an 8 x 8 matrix of 16-bit values, one row's pair a lane, transposed
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src) {
@@ -110,65 +141,130 @@ __device__ __forceinline__ Span span_of(const Args &a, int raw) {
   return s;
 }
 
-// Joins n pieces of one (sequence, kv head), slot_of(i) in turn; to the outputs
-// of query row `row0` on (final) or to slot `to`.
+// Joins n pieces of one query row, slot_of(i) in turn: lane i holds a piece's
+// reference and sum, the pieces' dims come sixteen at a time.  To out / lse
+// (given the row's place), or to slot `to` (out NULL).
 template <int D, typename F>
-__device__ __forceinline__ void join(const Args &a, int n, F slot_of, int64_t row0, bool final, int to) {
-  constexpr int LPR = D / 4;  // lanes per row, 4 dims each
+__device__ __forceinline__ void join_row(const Args &a, int n, F slot_of, int r, float *out, float *lse, int to) {
+  constexpr int LPR = D / 4;       // lanes per piece of a row, 4 dims each
+  constexpr int PPL = 32 / LPR;    // pieces at a time
   const int lane = threadIdx.x & 31;
-  const int c = (lane % LPR) * 4;
-  for (int r = lane / LPR; r < a.g; r += 32 / LPR) {
-    float ref = -INFINITY;
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) ref = fmaxf(ref, __ldcg(&a.slot_ml[static_cast<int64_t>(slot_of(i)) * a.g + r].x));
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-      const int64_t at = static_cast<int64_t>(slot_of(i)) * a.g + r;
-      const float2 ml = __ldcg(&a.slot_ml[at]);
-      const float4 x = __ldcg(reinterpret_cast<const float4 *>(a.slot_o + at * D + c));
-      const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - ref);
-      l = fmaf(w, ml.y, l);
-      o.x = fmaf(w, x.x, o.x);
-      o.y = fmaf(w, x.y, o.y);
-      o.z = fmaf(w, x.z, o.z);
-      o.w = fmaf(w, x.w, o.w);
+  const int c = (lane % LPR) * 4, sub = lane / LPR;
+  float ref = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int base = 0; base < n; base += 32) {
+    const int m = min(32, n - base);
+    const int slot = slot_of(base + min(lane, m - 1));
+    const float2 ml =
+        lane < m ? __ldcg(&a.slot_ml[static_cast<int64_t>(slot) * a.g + r]) : make_float2(-INFINITY, 0.f);
+    const float nref = fmaxf(ref, warp_max_xor(ml.x, 1, 32));
+    const float w = ml.x == -INFINITY ? 0.f * ml.y : ex2_approx(ml.x - nref);
+    const float keep = ref == -INFINITY ? 0.f : ex2_approx(ref - nref);
+    float add = w * ml.y;
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) add += __shfl_xor_sync(0xffffffffu, add, k);
+    l = l * keep + add;
+    ref = nref;
+    o.x *= keep;
+    o.y *= keep;
+    o.z *= keep;
+    o.w *= keep;
+    for (int i0 = 0; i0 < m; i0 += 16) {
+      float4 x[16 / PPL];
+      float f[16 / PPL];
+#pragma unroll
+      for (int i = 0; i < 16 / PPL; ++i) {
+        const int at = min(i0 + i * PPL + sub, m - 1);
+        const int from = __shfl_sync(0xffffffffu, slot, at);
+        f[i] = __shfl_sync(0xffffffffu, w, at);
+        if (i0 + i * PPL + sub >= m) f[i] = 0.f;
+        x[i] = i0 + i * PPL + sub < m
+                   ? __ldcg(reinterpret_cast<const float4 *>(a.slot_o + (static_cast<int64_t>(from) * a.g + r) * D + c))
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < 16 / PPL; ++i) {
+        o.x = fmaf(f[i], x[i].x, o.x);
+        o.y = fmaf(f[i], x[i].y, o.y);
+        o.z = fmaf(f[i], x[i].z, o.z);
+        o.w = fmaf(f[i], x[i].w, o.w);
+      }
     }
-    if (final) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      *reinterpret_cast<float4 *>(a.out + (row0 + r) * D + c) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-      if (a.lse && c == 0) a.lse[row0 + r] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+  }
+  if constexpr (PPL == 2) {
+    o.x += __shfl_xor_sync(0xffffffffu, o.x, 16);
+    o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
+    o.z += __shfl_xor_sync(0xffffffffu, o.z, 16);
+    o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
+  }
+  if (sub != 0) return;
+  if (out) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<float4 *>(out + c) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    if (lse && c == 0) *lse = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+  } else {
+    const int64_t at = static_cast<int64_t>(to) * a.g + r;
+    *reinterpret_cast<float4 *>(a.slot_o + at * D + c) = o;
+    if (c == 0) a.slot_ml[at] = make_float2(ref, l);
+  }
+}
+
+// A (sequence, kv head) of which a warp holds a piece.
+struct Piece {
+  long long seg;  // its first unit
+  int64_t row0;   // its first query row
+  int nb;         // its units; 0: no piece
+};
+
+// How the units are dealt out: CTA c of `ctas` has [first(c), first(c + 1)),
+// its warp w of `warps` an equal part of that.  (total = each * ctas + rest;
+// a CTA's part is below 2^27: of 2^31 tokens.)
+struct Deal {
+  long long each;
+  int rest, ctas, warps;
+  __device__ __forceinline__ Deal(long long total, int ctas_, int warps_) : ctas(ctas_), warps(warps_) {
+    if (total < 0x7fffffffLL) {
+      const int n = static_cast<int>(total), e = n / ctas;
+      each = e;
+      rest = n - e * ctas;
     } else {
-      const int64_t at = static_cast<int64_t>(to) * a.g + r;
-      *reinterpret_cast<float4 *>(a.slot_o + at * D + c) = o;
-      if (c == 0) a.slot_ml[at] = make_float2(ref, l);
+      each = total / ctas;
+      rest = static_cast<int>(total - each * ctas);
     }
   }
-}
-
-// Counts a piece whose data all lanes have written; true for the last of n.
-__device__ __forceinline__ bool last_of(int32_t *counter, int n) {
-  __threadfence();
-  __syncwarp();
-  int last = 0;
-  if ((threadIdx.x & 31) == 0) {
-    last = atom_add_acq_rel_gpu(counter, 1) == n - 1;
-    if (last) st_relaxed_gpu(counter, 0);
+  __device__ __forceinline__ long long first(int c) const { return each * c + rest * c / ctas; }
+  __device__ __forceinline__ long long first(int c, int w) const {
+    const long long c0 = first(c);
+    return c0 + static_cast<unsigned>(static_cast<int>(first(c + 1) - c0) * w) / static_cast<unsigned>(warps);
   }
-  last = __shfl_sync(0xffffffffu, last, 0);
-  __threadfence();
-  return last != 0;
-}
+  // the CTA and the warp that have unit u: from CTA c on downwards, upwards
+  __device__ __forceinline__ int down(int c, long long u) const {
+    while (first(c) > u) --c;
+    return c;
+  }
+  __device__ __forceinline__ int up(int c, long long u) const {
+    while (first(c + 1) <= u) ++c;
+    return c;
+  }
+  __device__ __forceinline__ int warp_of(int c, long long u) const {
+    const long long c0 = first(c);
+    const unsigned n = static_cast<unsigned>(first(c + 1) - c0), at = static_cast<unsigned>(u - c0);
+    return static_cast<int>(((at + 1) * warps - 1) / n);
+  }
+};
 
-template <int D, bool WIDE>
-__global__ void __launch_bounds__(kWarps * 32, 1) int4_decode_kernel(const Args a) {
-  using C = Cfg<D>;
-  constexpr int NG = C::NG, NST = C::NST, TB = C::TB;
-  constexpr int NR = WIDE ? 2 : 1;  // query rows a lane holds: lane / 4, and 8 more
+// NQ: query columns of the products of weights and values (4, 8 or 16).
+template <int D, int NQ>
+__global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(const Args a) {
+  using C = Cfg<D, NQ>;
+  constexpr int NG = C::NG, NST = C::NST, TB = C::TB, kWarps = C::W;
+  constexpr int NR = NQ == 16 ? 2 : 1;  // eights of queries
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long pre[kWarps * 32];
   __shared__ long long warp_sum[kWarps];
+  __shared__ Piece pieces[2 * kWarps];  // of each warp: one that began before its range, one that goes on behind it
+  __shared__ long long starts[kWarps + 1];  // of the warps' ranges
+  __shared__ int joins[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gq = lane >> 2, t = lane & 3;
 
@@ -209,21 +305,25 @@ __global__ void __launch_bounds__(kWarps * 32, 1) int4_decode_kernel(const Args 
   }
 
   // --- this warp's range of units [u0, u1)
-  const long long all = static_cast<long long>(gridDim.x) * kWarps;
+  if (total == 0) return;
   const long long want = (total + kMinUnits - 1) / kMinUnits;
-  const long long workers = want < all ? want : all;
-  const int wk = warp * gridDim.x + blockIdx.x;
-  if (wk >= workers) return;
-  const long long u0 = total * wk / workers, u1 = total * (wk + 1) / workers;
+  const Deal deal(total, static_cast<int>(want < gridDim.x ? want : gridDim.x), kWarps);
+  const int cta = blockIdx.x;
+  if (cta >= deal.ctas) return;
+  const long long u0 = deal.first(cta, warp), u1 = deal.first(cta, warp + 1);
+  if (lane < 2) pieces[2 * warp + lane].nb = 0;
+  if (lane == 0) starts[warp] = u0;
+  if (tid == 0) starts[kWarps] = deal.first(cta + 1);
 
+  if (u0 < u1) {  // (not indented: the whole of the warp's work)
   // --- the sequence of its first unit
   int s0;
   long long at0;  // units before it
   {
     int i = 0;
 #pragma unroll
-    for (int step = kWarps * 16; step > 0; step >>= 1)
-      if (pre[i + step] <= u0) i += step;
+    for (int step = 256; step > 0; step >>= 1)
+      if (i + step < kWarps * 32 && pre[i + step] <= u0) i += step;
     s0 = i * cs;
     at0 = pre[i];
     for (;; s0 += 32) {
@@ -243,12 +343,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) int4_decode_kernel(const Args 
         break;
       }
       at0 += __shfl_sync(0xffffffffu, incl, 31);
-      if (s0 + 32 >= a.num_seqs) return;  // lengths changed under way: nothing to do
+      if (s0 + 32 >= a.num_seqs) break;  // (not reached: u0 < total)
     }
   }
 
   // --- the fetching side: where it stands
-  const uint32_t ring = smem_u32(smem) + warp * C::RING;
+  const uint8_t *const ring = smem + warp * C::RING;
+  const uint32_t ring_at = smem_u32(ring);
   int fs = s0, fh, fb;  // sequence, kv head, block of the (sequence, kv head)
   Span fsp = span_of(a, __ldg(a.lens + fs));
   {
@@ -257,7 +358,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) int4_decode_kernel(const Args 
     fb = static_cast<int>(off - static_cast<long long>(fh) * fsp.nb);
   }
   int next_len = fs + 1 < a.num_seqs ? __ldg(a.lens + fs + 1) : 0;
-  long long fu = u0;
+  int fleft = static_cast<int>(u1 - u0);  // units to fetch
   int fslot = 0;
   // a window of 32 entries of the sequence's table, one per lane, and the next
   int win = 0, win_s = -1, win_b = 0, nxt = 0, nxt_s = -1, nxt_b = 0;
@@ -272,9 +373,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) int4_decode_kernel(const Args 
   const int my_dst = staged<D>(lane / (D / 32), (lane % (D / 32)) * 16);
   constexpr int PC = D / 16;  // 16-byte chunks of a tile's pairs
   const int pt = lane / PC;   // the tile whose pairs this lane copies: block pt / 2, K or V
-  const int64_t head_stride = TB, block_stride = static_cast<int64_t>(a.hkv) * TB;
+  const int my_pair_dst = pt * TB + i4::code_bytes(D) + (lane % PC) * 16;
+  const uint8_t *const my_k = a.kc + lane * 16, *const my_v = a.vc + lane * 16;
+  const uint8_t *const my_pair = (pt & 1 ? a.vc : a.kc) + i4::code_bytes(D) + (lane % PC) * 16;
+  const int64_t block_stride = static_cast<int64_t>(a.hkv) * TB;
   auto fetch = [&]() {
-    if (fu < u1) {
+    if (fleft > 0) {
       if (!(win_s == fs && fb >= win_b && fb < win_b + 32)) {
         win = nxt_s == fs && nxt_b == fb ? nxt : entries(fs, fsp, fb);
         win_s = fs;
@@ -290,36 +394,33 @@ __global__ void __launch_bounds__(kWarps * 32, 1) int4_decode_kernel(const Args 
           nxt = nxt_s < a.num_seqs ? entries(nxt_s, span_of(a, next_len), 0) : 0;
         }
       }
-      const bool two = fb + 1 < fsp.nb && fu + 1 < u1;
+      const bool two = fb + 1 < fsp.nb && fleft > 1;
       const int id0 = __shfl_sync(0xffffffffu, win, (fb - win_b) & 31);
       const int id1 = __shfl_sync(0xffffffffu, win, (fb - win_b + 1) & 31);
-      const uint32_t dst = ring + fslot * C::STAGE;
-      const int64_t o0 = id0 * block_stride + fh * head_stride, o1 = id1 * block_stride + fh * head_stride;
+      const uint32_t dst = ring_at + fslot * C::STAGE;
+      const int64_t o0 = id0 * block_stride + fh * TB, o1 = id1 * block_stride + fh * TB;
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
-        copy16(dst + my_dst + i * 512, a.kc + o0 + lane * 16 + i * 512);
-        copy16(dst + TB + my_dst + i * 512, a.vc + o0 + lane * 16 + i * 512);
+        copy16(dst + my_dst + i * 512, my_k + o0 + i * 512);
+        copy16(dst + TB + my_dst + i * 512, my_v + o0 + i * 512);
       }
       if (two) {
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
-          copy16(dst + 2 * TB + my_dst + i * 512, a.kc + o1 + lane * 16 + i * 512);
-          copy16(dst + 3 * TB + my_dst + i * 512, a.vc + o1 + lane * 16 + i * 512);
+          copy16(dst + 2 * TB + my_dst + i * 512, my_k + o1 + i * 512);
+          copy16(dst + 3 * TB + my_dst + i * 512, my_v + o1 + i * 512);
         }
       }
-      if (pt < (two ? 4 : 2)) {
-        const int off = i4::code_bytes(D) + (lane % PC) * 16;
-        copy16(dst + pt * TB + off, (pt & 1 ? a.vc : a.kc) + (pt & 2 ? o1 : o0) + off);
-      }
+      if (pt < (two ? 4 : 2)) copy16(dst + my_pair_dst, my_pair + (pt & 2 ? o1 : o0));
       fslot = fslot + 1 == NST ? 0 : fslot + 1;
       const int n = two ? 2 : 1;
-      fu += n;
+      fleft -= n;
       fb += n;
-      if (fb == fsp.nb && fu < u1) {
+      if (fb == fsp.nb && fleft > 0) {
         fb = 0;
         if (++fh == a.hkv) {
           fh = 0;
-          do {  // the next sequence with tokens (fu < u1: there is one)
+          do {  // the next sequence with tokens (units are left: there is one)
             ++fs;
             fsp = span_of(a, next_len);
             next_len = fs + 1 < a.num_seqs ? __ldg(a.lens + fs + 1) : 0;
@@ -336,15 +437,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) int4_decode_kernel(const Args 
 
   // --- addresses of a lane's operands in a staged tile
   const int krow = (gq >> 1) + 4 * (gq & 1);
-  int kat[NG], vat[2][NG];  // vat[i & 1] for row t + 4 i
-#pragma unroll
-  for (int p = 0; p < NG; ++p) {
-    kat[p] = staged<D>(krow, 32 * p + 8 * t);
-    vat[0][p] = staged<D>(t, 32 * p + 4 * gq);
-    vat[1][p] = staged<D>(t + 4, 32 * p + 4 * gq);
-  }
-  constexpr int ROW8 = 8 * (D / 2);  // eight rows further
+  const int kat = staged<D>(krow, 8 * t);                                    // group 1: ^ 32
+  const int vat0 = staged<D>(t, 4 * gq), vat1 = staged<D>(t + 4, 4 * gq);  // rows t + 4 i: i even, odd
+  constexpr int ROW8 = 8 * (D / 2);                                          // eight rows further
 
+  const float low = t < 2 ? 0.f : -1.f;
+  const float flip = gq & 1 ? -1.f : 1.f, flip15 = gq & 1 ? 15.f : 0.f;
   int cslot = 0;
   long long cu = u0;
 #pragma unroll 1
@@ -352,21 +450,23 @@ __global__ void __launch_bounds__(kWarps * 32, 1) int4_decode_kernel(const Args 
     // --- one (sequence, kv head), or this warp's part of it
     const long long seg = cu - cb;
     const int b_end = static_cast<int>(min(static_cast<long long>(csp.nb), cb + (u1 - cu)));
+    cu += b_end - cb;
     const int64_t row0 = static_cast<int64_t>(cseq) * a.hq + ch * a.g;
 
+    // per lane: its part of query gq's dims, and the rest of queries 2 t, 2 t + 1
     uint32_t qf[NR][D / 16][2];
-    float cs_[NR], cm[NR][NG], M[NR], l[NR], mz[NR][NG];
+    float cs_[NR][2], cm[NR][NG][2], M[NR][2], l[NR][2], mz[NR][NG][2];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      const bool has = gq + 8 * r < a.g;
+      const int query = (NQ == 4 ? gq & 3 : gq) + 8 * r;
       uint4 raw[NG][2];
       float amax = 0.f, sum[NG];
 #pragma unroll
       for (int p = 0; p < NG; ++p)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          raw[p][j] = has ? __ldg(reinterpret_cast<const uint4 *>(a.q + (row0 + gq + 8 * r) * D + 64 * p + 16 * t) + j)
-                          : make_uint4(0, 0, 0, 0);
+          raw[p][j] = query < a.g ? __ldg(reinterpret_cast<const uint4 *>(a.q + (row0 + query) * D + 64 * p + 16 * t) + j)
+                                  : make_uint4(0, 0, 0, 0);
       float f[NG][16];
 #pragma unroll
       for (int p = 0; p < NG; ++p) {
@@ -402,44 +502,51 @@ __global__ void __launch_bounds__(kWarps * 32, 1) int4_decode_kernel(const Args 
           qf[r][p * 4 + 2 * w + 1][0] = pack_f16x2(x[2] * down, x[6] * down);
           qf[r][p * 4 + 2 * w + 1][1] = pack_f16x2(x[3] * (down * 0.0625f), x[7] * (down * 0.0625f));
         }
-      cs_[r] = a.qscale * __uint_as_float(static_cast<uint32_t>(127 + 24 + e) << 23);
+      const float cq = a.qscale * __uint_as_float(static_cast<uint32_t>(127 + 24 + e) << 23);
 #pragma unroll
-      for (int p = 0; p < NG; ++p) {
-        cm[r][p] = a.qscale * sum[p];
-        mz[r][p] = 0.f;
+      for (int c = 0; c < 2; ++c) {
+        cs_[r][c] = __shfl_sync(0xffffffffu, cq, 8 * t + 4 * c);
+#pragma unroll
+        for (int p = 0; p < NG; ++p) {
+          cm[r][p][c] = a.qscale * __shfl_sync(0xffffffffu, sum[p], 8 * t + 4 * c);
+          mz[r][p][c] = 0.f;
+        }
+        M[r][c] = -INFINITY;
+        l[r][c] = 0.f;
       }
-      M[r] = -INFINITY;
-      l[r] = 0.f;
     }
     // weights are 2^(x - M + kexp): kexp keeps weight * scale within fp16
     float kexp = 60.f, kap = 1152921504606846976.f;  // 2^60
-    float acc[NG][8][4], sum[NR][NG][8][2];
+    float shift[NR][2], high[NR][2];                 // kexp - M, and the score that raises M
 #pragma unroll
-    for (int p = 0; p < NG; ++p)
+    for (int r = 0; r < NR; ++r)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[p][j][i] = 0.f;
-#pragma unroll
-        for (int r = 0; r < NR; ++r) sum[r][p][j][0] = sum[r][p][j][1] = 0.f;
+      for (int c = 0; c < 2; ++c) {
+        shift[r][c] = kexp;
+        high[r][c] = -INFINITY;
       }
-    auto flush = [&](const float (&alpha)[NR]) {
+    float acc[NR][NG][4][4], sum[NR][NG][4][4];  // [queries 0..7, 8..15][group][16 dims]
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
 #pragma unroll
       for (int p = 0; p < NG; ++p)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if constexpr (WIDE) {
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+          for (int i = 0; i < 4; ++i) acc[r][p][j][i] = sum[r][p][j][i] = 0.f;
+    // the tensor cores' sums to the fp32 sums
+    auto flush = [&]() {
 #pragma unroll
-              for (int c = 0; c < 2; ++c) sum[r][p][j][c] = (sum[r][p][j][c] + acc[p][j][2 * r + c]) * alpha[r];
-          } else {
+      for (int r = 0; r < NR; ++r)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) sum[0][p][j][c] = (sum[0][p][j][c] + (acc[p][j][c] + acc[p][j][2 + c])) * alpha[0];
-          }
+        for (int p = 0; p < NG; ++p)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[p][j][i] = 0.f;
-        }
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              sum[r][p][j][i] += acc[r][p][j][i];
+              acc[r][p][j][i] = 0.f;
+            }
     };
 
     int since = 0;
@@ -449,266 +556,232 @@ __global__ void __launch_bounds__(kWarps * 32, 1) int4_decode_kernel(const Args 
       __syncwarp();
       fetch();
       const int n = b_end - cb < 2 ? 1 : 2;
-      const uint32_t st = ring + cslot * C::STAGE;
-      const int pos0 = (csp.b0 + cb) * 16;
-      const bool edge = n < 2 || pos0 < csp.first || pos0 + 32 > csp.len;
+      const uint8_t *const st = ring + cslot * C::STAGE;
+#pragma unroll 1
+      for (int tt = 0; tt < n; ++tt) {
+        const uint8_t *const kt = st + 2 * tt * TB, *const vt = kt + TB;
+        const int pos0 = (csp.b0 + cb + tt) * 16;
 
-      // scores: x[r][tile][i] of token t + 4 i
-      float x[NR][2][4];
-      float ks[2][4][NG], km[2][4][NG];
-#pragma unroll
-      for (int tt = 0; tt < 2; ++tt) {
-        const uint32_t kt = st + 2 * tt * TB;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t pa_ = kt + i4::code_bytes(D) + (t + 4 * i) * (4 * NG);
-          uint32_t w[2];
-          if constexpr (NG == 2) {
-            const uint2 u = lds64(pa_);
-            w[0] = u.x;
-            w[1] = u.y;
-          } else {
-            w[0] = lds32(pa_);
-          }
+        // scores: x[r][i][c] of token krow + 8 i and query 2 t + c (+ 8 r)
+        float x[NR][2][2];
+        {
+          float s[NR][NG][4];
 #pragma unroll
           for (int p = 0; p < NG; ++p) {
-            ks[tt][i][p] = f16lo(w[p]);
-            km[tt][i][p] = f16hi(w[p]);
-          }
-        }
-        float s[2][NG][4];
+            const uint2 k0 = lds64(kt + (kat ^ (32 * p))), k8 = lds64(kt + (kat ^ (32 * p)) + ROW8);
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+            for (int h = 0; h < 4; ++h) {
+              const uint32_t u = (h < 2 ? k0.x : k0.y) >> (h & 1 ? 8 : 0), v = (h < 2 ? k8.x : k8.y) >> (h & 1 ? 8 : 0);
+              const uint32_t a0 = u & 0x000F000Fu, a1 = v & 0x000F000Fu, a2 = u & 0x00F000F0u, a3 = v & 0x00F000F0u;
 #pragma unroll
-          for (int p = 0; p < NG; ++p) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[nt][p][i] = 0.f;
-            const uint2 w = lds64(kt + kat[p] + nt * ROW8);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t u = h ? w.y : w.x, u8 = u >> 8;
-              const uint32_t *qa = qf[0][p * 4 + 2 * h], *qb = qf[0][p * 4 + 2 * h + 1];
-              const uint32_t *ra = qf[NR - 1][p * 4 + 2 * h], *rb = qf[NR - 1][p * 4 + 2 * h + 1];
-              mma_f16_16816(s[nt][p], qa[0], WIDE ? ra[0] : 0u, qa[1], WIDE ? ra[1] : 0u, u & 0x000F000Fu,
-                            u & 0x00F000F0u);
-              mma_f16_16816(s[nt][p], qb[0], WIDE ? rb[0] : 0u, qb[1], WIDE ? rb[1] : 0u, u8 & 0x000F000Fu,
-                            u8 & 0x00F000F0u);
+              for (int r = 0; r < NR; ++r) {
+                if (h == 0)
+                  mma0(s[r][p], a0, a1, a2, a3, qf[r][p * 4 + h][0], qf[r][p * 4 + h][1]);
+                else
+                  mma(s[r][p], a0, a1, a2, a3, qf[r][p * 4 + h][0], qf[r][p * 4 + h][1]);
+              }
             }
           }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t w[2];
+            load_pairs<NG>(kt + i4::code_bytes(D) + (krow + 8 * i) * (4 * NG), w);
+            const float2 g0 = halves(w[0]), g1 = halves(w[NG - 1]);  // scale, minimum
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                float y = s[r][0][2 * i + c] * g0.x, z = g0.y * cm[r][0][c];
+                if constexpr (NG == 2) {
+                  y = fmaf(s[r][NG - 1][2 * i + c], g1.x, y);
+                  z = fmaf(g1.y, cm[r][NG - 1][c], z);
+                }
+                x[r][i][c] = fmaf(y, cs_[r][c], z);
+              }
+          }
+        }
+
+        // the values' scales and minima; masked tokens have neither.  Every
+        // second token's weight is negated and its code taken from 15, s n + m
+        // = (m + 15 s) - s (15 - n): codes are never negative, and without this
+        // the two sums, of codes and of minima, would grow far past their
+        // difference.
+        float vs[2][NG], vm[2][NG];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t w[2];
+          load_pairs<NG>(vt + i4::code_bytes(D) + (krow + 8 * i) * (4 * NG), w);
+#pragma unroll
+          for (int p = 0; p < NG; ++p) {
+            const float2 g = halves(w[p]);
+            vs[i][p] = g.x;
+            vm[i][p] = fmaf(flip15, g.x, g.y);
+          }
+        }
+        if (pos0 < csp.first || pos0 + 16 > csp.len) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int pos = pos0 + krow + 8 * i;
+            if (pos < csp.first || pos >= csp.len) {
+#pragma unroll
+              for (int r = 0; r < NR; ++r) x[r][i][0] = x[r][i][1] = -INFINITY;
+#pragma unroll
+              for (int p = 0; p < NG; ++p) vs[i][p] = vm[i][p] = 0.f;
+            }
+          }
+        }
+
+        // the running maximum is raised only when a score passes it by 2^8,
+        // and kexp lowered only when a scale needs it: a vote, no shuffles
+        float smax = fmaxf(vs[0][0], vs[1][0]);
+        if constexpr (NG == 2) smax = fmax3(smax, vs[0][NG - 1], vs[1][NG - 1]);
+        bool raise = smax * kap > 128.f;
 #pragma unroll
         for (int r = 0; r < NR; ++r)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float y = s[i >> 1][0][2 * r + (i & 1)] * ks[tt][i][0], z = km[tt][i][0] * cm[r][0];
-            if constexpr (NG == 2) {
-              y = fmaf(s[i >> 1][NG - 1][2 * r + (i & 1)], ks[tt][i][NG - 1], y);
-              z = fmaf(km[tt][i][NG - 1], cm[r][NG - 1], z);
+          for (int c = 0; c < 2; ++c) raise |= fmaxf(x[r][0][c], x[r][1][c]) > high[r][c];
+        if (__any_sync(0xffffffffu, raise)) {
+          smax = warp_max_xor(smax, 1, 32);
+          float nk = kexp;
+          if (smax * kap > 128.f) {
+            int e = static_cast<int>(__float_as_uint(smax) >> 23) - 127;  // smax in [2^e, 2^(e + 1))
+            e = e > 16 ? 16 : e;
+            nk = static_cast<float>(4 - e);
+            kap = __uint_as_float(static_cast<uint32_t>(127 + 4 - e) << 23);
+          }
+          flush();
+          since = 0;
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float m = fmaxf(M[r][c], warp_max_xor(fmaxf(x[r][0][c], x[r][1][c]), 4, 32));
+              const float alpha = M[r][c] == -INFINITY ? 0.f : ex2_approx((M[r][c] - m) + (nk - kexp));
+              M[r][c] = m;
+              shift[r][c] = nk - (m == -INFINITY ? 0.f : m);
+              high[r][c] = m + 8.f;
+              l[r][c] *= alpha;
+#pragma unroll
+              for (int p = 0; p < NG; ++p) {
+                mz[r][p][c] *= alpha;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  sum[r][p][j][c] *= alpha;
+                  sum[r][p][j][2 + c] *= alpha;
+                }
+              }
             }
-            x[r][tt][i] = fmaf(y, cs_[r], z);
-          }
-      }
-
-      // the values' scales and minima; masked tokens have neither
-      float vs[2][4][NG], vm[2][4][NG];
-#pragma unroll
-      for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t pa_ = st + (2 * tt + 1) * TB + i4::code_bytes(D) + (t + 4 * i) * (4 * NG);
-          uint32_t w[2];
-          if constexpr (NG == 2) {
-            const uint2 u = lds64(pa_);
-            w[0] = u.x;
-            w[1] = u.y;
-          } else {
-            w[0] = lds32(pa_);
-          }
-#pragma unroll
-          for (int p = 0; p < NG; ++p) {
-            vs[tt][i][p] = f16lo(w[p]);
-            vm[tt][i][p] = f16hi(w[p]);
-          }
+          kexp = nk;
         }
-      if (edge) {
-#pragma unroll
-        for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int pos = pos0 + 16 * tt + t + 4 * i;
-            if (pos < csp.first || pos >= csp.len || tt >= n) {
-#pragma unroll
-              for (int r = 0; r < NR; ++r) x[r][tt][i] = -INFINITY;
-#pragma unroll
-              for (int p = 0; p < NG; ++p) vs[tt][i][p] = vm[tt][i][p] = 0.f;
-            }
-          }
-      }
 
-      // the running maximum is raised only when a score passes it by 2^8, and
-      // kexp lowered only when a scale needs it: a vote, no shuffles
-      float smax = 0.f, xmax[NR];
-      bool raise = false;
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        xmax[r] = fmaxf(fmax3(x[r][0][0], x[r][0][1], x[r][0][2]), fmax3(x[r][0][3], x[r][1][0], x[r][1][1]));
-        xmax[r] = fmax3(xmax[r], x[r][1][2], x[r][1][3]);
-        raise |= xmax[r] > M[r] + 8.f;
-      }
-#pragma unroll
-      for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int p = 0; p < NG; ++p) smax = fmaxf(smax, vs[tt][i][p]);
-      raise |= smax * kap > 128.f;
-      if (__any_sync(0xffffffffu, raise)) {
-        float alpha[NR];
-        smax = warp_max_xor(smax, 1, 32);
-        float nk = kexp;
-        if (smax * kap > 128.f) {
-          int e = static_cast<int>(__float_as_uint(smax) >> 23) - 127;  // smax in [2^e, 2^(e + 1))
-          e = e > 16 ? 16 : e;
-          nk = static_cast<float>(4 - e);
-          kap = __uint_as_float(static_cast<uint32_t>(127 + 4 - e) << 23);
-        }
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const float m = fmaxf(M[r], warp_max_xor(xmax[r], 1, 4));
-          alpha[r] = M[r] == -INFINITY ? 0.f : ex2_approx((M[r] - m) + (nk - kexp));
-          M[r] = m;
-          l[r] *= alpha[r];
-#pragma unroll
-          for (int p = 0; p < NG; ++p) mz[r][p] *= alpha[r];
-        }
-        kexp = nk;
-        flush(alpha);
-        since = 0;
-      }
-      float shift[NR];
-#pragma unroll
-      for (int r = 0; r < NR; ++r) shift[r] = kexp - (M[r] == -INFINITY ? 0.f : M[r]);
-
-#pragma unroll
-      for (int tt = 0; tt < 2; ++tt) {
+        // weights times scales as hi + lo, turned into operands (token pairs of
+        // a query) by 8 x 8 transposes
         uint32_t hi[NR][NG][2], lo[NR][NG][2];
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-          float w[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            w[i] = ex2_approx(x[r][tt][i] + shift[r]);
-            l[r] += w[i];
+          for (int i = 0; i < 2; ++i) {
+            const float w0 = ex2_approx(x[r][i][0] + shift[r][0]), w1 = ex2_approx(x[r][i][1] + shift[r][1]);
+            l[r][0] += w0;
+            l[r][1] += w1;
 #pragma unroll
-            for (int p = 0; p < NG; ++p) mz[r][p] = fmaf(w[i], vm[tt][i][p], mz[r][p]);
-          }
-#pragma unroll
-          for (int p = 0; p < NG; ++p)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float y0 = w[2 * j] * vs[tt][2 * j][p], y1 = w[2 * j + 1] * vs[tt][2 * j + 1][p];
-              hi[r][p][j] = pack_f16x2(y0, y1);
-              lo[r][p][j] = pack_f16x2(y0 - f16lo(hi[r][p][j]), y1 - f16hi(hi[r][p][j]));
+            for (int p = 0; p < NG; ++p) {
+              mz[r][p][0] = fmaf(w0, vm[i][p], mz[r][p][0]);
+              mz[r][p][1] = fmaf(w1, vm[i][p], mz[r][p][1]);
+              const float sv = vs[i][p] * flip;
+              const float y0 = w0 * sv, y1 = w1 * sv;
+              const uint32_t h = pack_f16x2(y0, y1);
+              const float2 hf = halves(h);
+              if constexpr (NQ == 4) {  // the lo halves in the columns of queries 4..7 (y - 0 h is y)
+                hi[r][p][i] = transposed(pack_f16x2(fmaf(low, hf.x, y0), fmaf(low, hf.y, y1)));
+              } else {
+                hi[r][p][i] = transposed(h);
+                lo[r][p][i] = transposed(pack_f16x2(y0 - hf.x, y1 - hf.y));
+              }
             }
+          }
         }
-        const uint32_t vt = st + (2 * tt + 1) * TB;
 #pragma unroll
         for (int p = 0; p < NG; ++p) {
-          const uint32_t w0 = lds32(vt + vat[0][p]), w1 = lds32(vt + vat[1][p]);
-          const uint32_t w2 = lds32(vt + vat[0][p] + ROW8), w3 = lds32(vt + vat[1][p] + ROW8);
+          const uint32_t w0 = lds32(vt + (vat0 ^ (32 * p))), w1 = lds32(vt + (vat1 ^ (32 * p)));
+          const uint32_t w2 = lds32(vt + (vat0 ^ (32 * p)) + ROW8), w3 = lds32(vt + (vat1 ^ (32 * p)) + ROW8);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t b0 = __byte_perm(w0, w1, h ? 0x7632 : 0x5410);
             uint32_t b1 = __byte_perm(w2, w3, h ? 0x7632 : 0x5410);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t mask = j & 1 ? 0x00F000F0u : 0x000F000Fu;
-              if (j == 2) {
-                b0 >>= 8;
-                b1 >>= 8;
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t v0 = and_xor(b0, 0x000F000Fu, 0x000F0000u), v1 = and_xor(b0, 0x00F000F0u, 0x00F00000u);
+              const uint32_t v2 = and_xor(b1, 0x000F000Fu, 0x000F0000u), v3 = and_xor(b1, 0x00F000F0u, 0x00F00000u);
+#pragma unroll
+              for (int r = 0; r < NR; ++r) {
+                mma(acc[r][p][2 * h + j], v0, v1, v2, v3, hi[r][p][0], hi[r][p][1]);
+                if constexpr (NQ != 4) mma(acc[r][p][2 * h + j], v0, v1, v2, v3, lo[r][p][0], lo[r][p][1]);
               }
-              if constexpr (WIDE) {
-                mma_f16_16816(acc[p][4 * h + j], hi[0][p][0], hi[1][p][0], hi[0][p][1], hi[1][p][1], b0 & mask,
-                              b1 & mask);
-                mma_f16_16816(acc[p][4 * h + j], lo[0][p][0], lo[1][p][0], lo[0][p][1], lo[1][p][1], b0 & mask,
-                              b1 & mask);
-              } else {
-                mma_f16_16816(acc[p][4 * h + j], hi[0][p][0], lo[0][p][0], hi[0][p][1], lo[0][p][1], b0 & mask,
-                              b1 & mask);
-              }
+              b0 >>= 8;
+              b1 >>= 8;
             }
           }
         }
       }
       cslot = cslot + 1 == NST ? 0 : cslot + 1;
       cb += n;
-      cu += n;
       if (++since == kFlush) {
-        float one[NR];
-#pragma unroll
-        for (int r = 0; r < NR; ++r) one[r] = 1.f;
-        flush(one);
+        flush();
         since = 0;
       }
     }
 
-    // --- the end of the piece: to the outputs, or to a slot and perhaps the join
-    {
-      float one[NR];
-#pragma unroll
-      for (int r = 0; r < NR; ++r) one[r] = 1.f;
-      flush(one);
-    }
+    // --- the end of the piece: to the outputs, or to a slot for the join
+    flush();
     const bool whole = seg >= u0 && seg + csp.nb <= u1;
-    const int slot = 2 * wk + (seg >= u0 ? 1 : 0);
+    const int slot = 2 * (cta * kWarps + warp) + (seg >= u0 ? 1 : 0);
+    float *dst = whole ? a.out + row0 * D : a.slot_o + static_cast<int64_t>(slot) * a.g * D;
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    for (int r = 0; r < NR; ++r)
 #pragma unroll
-      for (int p = 0; p < NG; ++p) {
-        mz[r][p] += __shfl_xor_sync(0xffffffffu, mz[r][p], 1);
-        mz[r][p] += __shfl_xor_sync(0xffffffffu, mz[r][p], 2);
-      }
-      const int row = gq + 8 * r;
-      if (row < a.g) {
-        const float ref = M[r] == -INFINITY ? -INFINITY : M[r] - kexp;
-        const float inv = !whole ? 1.f : l[r] == 0.f ? 0.f : 1.f / l[r];
-        float *dst = whole ? a.out + (row0 + row) * D : a.slot_o + (static_cast<int64_t>(slot) * a.g + row) * D;
+      for (int c = 0; c < 2; ++c) {
+        const int query = 2 * t + c + 8 * r;
+        const bool has = query < a.g && (NQ != 4 || t < 2);
+        float lsum = l[r][c], z[NG];
 #pragma unroll
-        for (int p = 0; p < NG; ++p)
+        for (int o = 4; o < 32; o <<= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+        for (int p = 0; p < NG; ++p) {
+          z[p] = mz[r][p][c];
 #pragma unroll
-            for (int j = 0; j < 8; j += 4) {
-              // 2^24 for the codes' place in fp16, a sixteenth of it for the odd dims
-              float4 o;
-              o.x = fmaf(sum[r][p][j][c], 16777216.f, mz[r][p]) * inv;
-              o.y = fmaf(sum[r][p][j + 1][c], 1048576.f, mz[r][p]) * inv;
-              o.z = fmaf(sum[r][p][j + 2][c], 16777216.f, mz[r][p]) * inv;
-              o.w = fmaf(sum[r][p][j + 3][c], 1048576.f, mz[r][p]) * inv;
-              *reinterpret_cast<float4 *>(dst + 64 * p + 16 * t + 8 * c + j) = o;
-            }
-        if (t == 0) {
+          for (int o = 4; o < 32; o <<= 1) z[p] += __shfl_xor_sync(0xffffffffu, z[p], o);
+        }
+        const float ref = M[r][c] == -INFINITY ? -INFINITY : M[r][c] - kexp;
+        const float inv = !whole ? 1.f : lsum == 0.f ? 0.f : 1.f / lsum;
+        if (gq == 0 && has) {
           if (!whole)
-            a.slot_ml[static_cast<int64_t>(slot) * a.g + row] = make_float2(ref, l[r]);
+            a.slot_ml[static_cast<int64_t>(slot) * a.g + query] = make_float2(ref, lsum);
           else if (a.lse)
-            a.lse[row0 + row] = l[r] == 0.f ? -INFINITY : (ref + log2f(l[r])) * kLn2;
+            a.lse[row0 + query] = lsum == 0.f ? -INFINITY : (ref + log2f(lsum)) * kLn2;
+        }
+#pragma unroll
+        for (int p = 0; p < NG; ++p) {
+          // 2^24 for the codes' place in fp16, a sixteenth of it for the odd dims
+          float o[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float e = sum[r][p][j][c], f = sum[r][p][j][2 + c];
+            if constexpr (NQ == 4) {  // the lo halves, from the columns of queries 4..7
+              e += __shfl_xor_sync(0xffffffffu, e, 2);
+              f += __shfl_xor_sync(0xffffffffu, f, 2);
+            }
+            o[2 * j] = fmaf(e, 16777216.f, z[p]) * inv;
+            o[2 * j + 1] = fmaf(f, 1048576.f, z[p]) * inv;
+          }
+          if (has) {
+            float4 *to = reinterpret_cast<float4 *>(dst + query * D + 64 * p + 8 * gq);
+            to[0] = make_float4(o[0], o[1], o[2], o[3]);
+            to[1] = make_float4(o[4], o[5], o[6], o[7]);
+          }
         }
       }
-    }
-    if (!whole) {
-      // the workers of this (sequence, kv head) are wa .. wz
-      const int wa = static_cast<int>(((seg + 1) * workers - 1) / total);
-      const int wz = static_cast<int>(((seg + csp.nb) * workers - 1) / total);
-      auto slot_of_worker = [wa](int w) { return 2 * w + (w == wa ? 1 : 0); };
-      const int first = max(wa, wk / kFan * kFan), n1 = min(wz, wk / kFan * kFan + kFan - 1) - first + 1;
-      const int n2 = wz / kFan - wa / kFan + 1;
-      bool on = n1 == 1 || last_of(a.count1 + slot_of_worker(first), n1);
-      if (on && n1 > 1)
-        join<D>(a, n1, [&](int i) { return slot_of_worker(first + i); }, row0, n2 == 1, slot_of_worker(first));
-      if (on && n2 > 1 && last_of(a.count2 + wa, n2))
-        join<D>(a, n2, [&](int i) { return slot_of_worker(max(wa, (wa / kFan + i) * kFan)); }, row0, true, 0);
-    }
+    if (!whole && lane == 0) pieces[2 * warp + (seg >= u0 ? 1 : 0)] = Piece{seg, row0, csp.nb};
 
     if (cb == csp.nb && cu < u1) {
       cb = 0;
@@ -722,30 +795,97 @@ __global__ void __launch_bounds__(kWarps * 32, 1) int4_decode_kernel(const Args 
     }
   }
   cp_async_wait<0>();
+  }  // u0 < u1
+
+  // --- pieces of this CTA's warps joined, a query row a warp
+  __syncthreads();
+  const long long c0 = starts[0], c1 = starts[kWarps];
+  const int slot0 = 2 * cta * kWarps;
+  for (int k = 0; k < 2 * kWarps; ++k) {
+    const Piece pc = pieces[k];
+    const int w = k >> 1;
+    // the first piece here of its (sequence, kv head)
+    if (pc.nb == 0 || starts[w] > (pc.seg > c0 ? pc.seg : c0)) continue;
+    const long long end = pc.seg + pc.nb;
+    // its further pieces: the first of the warps that follow (a warp without
+    // units, of a CTA with fewer units than warps, has none)
+    unsigned held = 0;
+    for (int x = w + 1; x < kWarps && starts[x] < end; ++x) held |= (pieces[2 * x].nb > 0 ? 1u : 0u) << x;
+    const int n = 1 + __popc(held);
+    if (n == 1) continue;  // a CTA's only piece goes on elsewhere: it lies in its slot
+    const bool here = pc.seg >= c0 && end <= c1;
+    auto slot_of = [&](int i) {
+      unsigned m = held;
+      for (int j = 1; j < i; ++j) m &= m - 1;
+      return slot0 + (i == 0 ? k : 2 * (__ffs(m) - 1));
+    };
+    for (int r = (warp + kWarps - w) % kWarps; r < a.g; r += kWarps)
+      join_row<D>(a, n, slot_of, r, here ? a.out + (pc.row0 + r) * D : nullptr,
+                  here && a.lse ? a.lse + pc.row0 + r : nullptr, slot0 + k);
+  }
+
+  // --- and what goes beyond this CTA, by the CTA that finishes its last piece
+  __threadfence();
+  __syncthreads();
+  if (tid < 2) {
+    joins[tid] = -1;
+    // tid 0: what began before this CTA; tid 1: what begins here and goes on
+    for (int k = 0; k < 2 * kWarps; ++k) {
+      const Piece pc = pieces[k];
+      if (pc.nb == 0 || (tid == 0 ? pc.seg >= c0 : pc.seg < c0 || pc.seg + pc.nb <= c1)) continue;
+      const int ca = deal.down(cta, pc.seg), cz = deal.up(cta, pc.seg + pc.nb - 1);
+      if (atom_add_acq_rel_gpu(a.count + ca, 1) == cz - ca) {
+        st_relaxed_gpu(a.count + ca, 0);
+        joins[tid] = k;
+      }
+      break;
+    }
+    __threadfence();
+  }
+  __syncthreads();
+  for (int j = 0; j < 2; ++j) {
+    if (joins[j] < 0) continue;
+    const Piece pc = pieces[joins[j]];
+    const int ca = deal.down(cta, pc.seg), cz = deal.up(cta, pc.seg + pc.nb - 1);
+    auto slot_of = [&](int i) {
+      const int c = ca + i;
+      return i == 0 ? 2 * (c * kWarps + deal.warp_of(c, pc.seg)) + 1
+                    : 2 * (c * kWarps + deal.warp_of(c, deal.first(c)));
+    };
+    for (int r = warp; r < a.g; r += kWarps)
+      join_row<D>(a, cz - ca + 1, slot_of, r, a.out + (pc.row0 + r) * D, a.lse ? a.lse + pc.row0 + r : nullptr, 0);
+  }
 }
 
-using Kernel = void (*)(const Args);
+struct Kernel {
+  const void *fn;
+  int warps, smem;
+};
 
-Kernel kernel_of(const pa_kv_desc &d, size_t *smem) {
-  const bool wide = d.num_q_heads / d.num_kv_heads > 8;
-  if (d.head_dim == 128) {
-    *smem = Cfg<128>::SMEM;
-    return wide ? &int4_decode_kernel<128, true> : &int4_decode_kernel<128, false>;
-  }
-  *smem = Cfg<64>::SMEM;
-  return wide ? &int4_decode_kernel<64, true> : &int4_decode_kernel<64, false>;
+template <int D, int NQ>
+Kernel kernel_for() {
+  return {reinterpret_cast<const void *>(&int4_decode_kernel<D, NQ>), Cfg<D, NQ>::W, Cfg<D, NQ>::SMEM};
+}
+
+template <int D>
+Kernel kernel_of_dim(int g) {
+  return g <= 4 ? kernel_for<D, 4>() : g <= 8 ? kernel_for<D, 8>() : kernel_for<D, 16>();
+}
+
+Kernel kernel_of(const pa_kv_desc &d) {
+  const int g = d.num_q_heads / d.num_kv_heads;
+  return d.head_dim == 128 ? kernel_of_dim<128>(g) : kernel_of_dim<64>(g);
 }
 
 struct Layout {
-  size_t count1, count2, ml, o, total;
+  size_t count, ml, o, total;
 };
 
-Layout layout(int ctas, int g, int d) {
-  const size_t workers = static_cast<size_t>(ctas) * kWarps;
+Layout layout(int ctas, int warps, int g, int d) {
+  const size_t workers = static_cast<size_t>(ctas) * warps;
   Layout w;
-  w.count1 = 256;
-  w.count2 = w.count1 + 2 * workers * sizeof(int32_t);
-  w.ml = (w.count2 + workers * sizeof(int32_t) + 255) / 256 * 256;
+  w.count = 256;
+  w.ml = (w.count + ctas * sizeof(int32_t) + 255) / 256 * 256;
   w.o = (w.ml + 2 * workers * g * sizeof(float2) + 255) / 256 * 256;
   w.total = w.o + 2 * workers * g * d * sizeof(float);
   return w;
@@ -758,9 +898,8 @@ pa_status plan_int4_decode(const pa_kv_desc &d, DecodePlan *plan, const char **w
     *why = "a 4-bit cache is decoded on the tensor cores (decode_impl AUTO or MMA)";
     return PA_ERR_UNSUPPORTED;
   }
-  size_t smem = 0;
-  const Kernel fn = kernel_of(d, &smem);
-  const int occ = prepare_kernel(reinterpret_cast<const void *>(fn), kWarps * 32, smem);
+  const Kernel k = kernel_of(d);
+  const int occ = prepare_kernel(k.fn, k.warps * 32, k.smem);
   if (occ < 1) {
     *why = "the decode kernel does not fit on this device";
     return PA_ERR_CUDA;
@@ -769,7 +908,7 @@ pa_status plan_int4_decode(const pa_kv_desc &d, DecodePlan *plan, const char **w
   plan->slot_heads = d.num_q_heads / d.num_kv_heads;
   plan->num_groups = d.num_kv_heads;
   plan->num_ctas = device_sm_count();
-  const Layout w = layout(plan->num_ctas, plan->slot_heads, d.head_dim);
+  const Layout w = layout(plan->num_ctas, k.warps, plan->slot_heads, d.head_dim);
   plan->workspace_bytes = w.total;
   plan->zero_bytes = w.ml;
   return PA_OK;
@@ -779,9 +918,8 @@ cudaError_t launch_int4_decode(const pa_kv_desc &d, const DecodePlan &plan, floa
                                const void *k_cache, const void *v_cache, const int32_t *block_tables,
                                int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs, float scale,
                                void *workspace, cudaStream_t stream) {
-  size_t smem = 0;
-  const Kernel fn = kernel_of(d, &smem);
-  const Layout w = layout(plan.num_ctas, plan.slot_heads, d.head_dim);
+  const Kernel k = kernel_of(d);
+  const Layout w = layout(plan.num_ctas, k.warps, plan.slot_heads, d.head_dim);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   Args a;
   a.out = out;
@@ -804,8 +942,7 @@ cudaError_t launch_int4_decode(const pa_kv_desc &d, const DecodePlan &plan, floa
   a.checked = d.check_indices;
   a.num_blocks = d.num_blocks;
   a.f16 = d.kv_dtype == PA_KV_INT4_F16;
-  a.count1 = reinterpret_cast<int32_t *>(ws + w.count1);
-  a.count2 = reinterpret_cast<int32_t *>(ws + w.count2);
+  a.count = reinterpret_cast<int32_t *>(ws + w.count);
   a.slot_ml = reinterpret_cast<float2 *>(ws + w.ml);
   a.slot_o = reinterpret_cast<float *>(ws + w.o);
   // programmatic dependent launch: it waits for the preceding kernel's writes
@@ -815,13 +952,13 @@ cudaError_t launch_int4_decode(const pa_kv_desc &d, const DecodePlan &plan, floa
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(plan.num_ctas);
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(k.warps * 32);
+  cfg.dynamicSmemBytes = k.smem;
   cfg.stream = stream;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
   void *args[] = {&a};
-  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(fn), args);
+  return cudaLaunchKernelExC(&cfg, k.fn, args);
 }
 
 }  // namespace pa
