@@ -92,7 +92,7 @@ extern "C" {
  *    Added without a new version (nothing before them changed):
  *    pa_rope_desc, pa_qk_norm_rope, pa_rope_cache_write,
  *    pa_decode_shared_workspace_size, pa_decode_shared, PA_KV_INT4,
- *    PA_KV_INT4_F16, pa_widen_blocks. */
+ *    PA_KV_INT4_F16, pa_widen_blocks, pa_prompt_attention. */
 #define PA_ABI_VERSION 4
 
 /* Symbols of the shared library; everything else in it stays hidden. */
@@ -140,8 +140,8 @@ typedef enum {
  * PA_DEVERR_FP16_RANGE), reads as NaN.
  * Calls that take it: pa_cache_write, pa_decode, pa_decode_static,
  * pa_decode_workspace_size, pa_widen_blocks, pa_copy_blocks, pa_bind_blocks,
- * pa_release_blocks, and pa_qk_norm_rope, which takes its activation type; the
- * others return PA_ERR_UNSUPPORTED.
+ * pa_release_blocks, and pa_qk_norm_rope and pa_prompt_attention, which take
+ * its activation type; the others return PA_ERR_UNSUPPORTED.
  */
 #define PA_INT4_TILE_BYTES(head_dim) (9 * (head_dim))
 
@@ -400,6 +400,39 @@ PA_API pa_status pa_prefill_chunk(const pa_kv_desc *desc, float *out, float *lse
                            int32_t max_blocks_per_seq, const int32_t *context_lens,
                            int32_t num_seqs, int32_t max_q_len, int32_t max_context_len,
                            float scale, pa_stream_t stream);
+
+/*
+ * Causal attention of whole prompts from their own rows, without a cache: the
+ * first pass over prompts that bring all their tokens at once, before (or
+ * beside) the write of their keys and values to any cache.  Prompt s owns the
+ * packed rows [query_start_loc[s], query_start_loc[s+1]) of q, k, v and out;
+ * its token i attends its tokens [0, i] (local attention: from the first
+ * one that the descriptor's sliding_window and attention_chunk leave).
+ *   out[i][h] = sum_j softmax_j(scale * q[i][h] . k[j][h / g]) v[j][h / g]
+ *   q    : [num_tokens][num_q_heads][head_dim], k, v : [num_tokens]
+ *          [num_kv_heads][head_dim], in the activation type (bf16; fp16 with
+ *          PA_KV_F16 and PA_KV_INT4_F16), the heads of a token contiguous;
+ *          q_stride, k_stride, v_stride elements from one token to the next (a
+ *          multiple of 8, 0: dense), so that all may lie inside one
+ *          projection's output.  16-byte aligned.
+ *   out  : [num_tokens][num_q_heads][head_dim], dense, in the activation type;
+ *          it must not overlap the inputs.
+ *   lse  : optional [num_tokens][num_q_heads] fp32, natural log.
+ *   query_start_loc : int32 [num_seqs + 1], non-decreasing, within [0,
+ *          num_tokens].  Rows outside every prompt are not written.
+ *   max_q_len : an upper bound of the prompts' lengths (host value).
+ * Scores and sums in fp32, the weights rounded to the activation type for the
+ * product with v, one rounding of the result.  A row of v that is not finite
+ * reaches the tokens that see it and no others.
+ * Uses desc's heads, head_dim, kv_dtype (for the activation type), local
+ * attention, error_word and check_indices (query_start_loc out of range or
+ * order, or a prompt longer than max_q_len, is reported and that prompt left
+ * out or cut).  num_seqs, num_tokens or max_q_len == 0 enqueues nothing.
+ */
+PA_API pa_status pa_prompt_attention(const pa_kv_desc *desc, void *out, float *lse, const void *q, int64_t q_stride,
+                                     const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                     const int32_t *query_start_loc, int32_t num_seqs, int32_t num_tokens,
+                                     int32_t max_q_len, float scale, pa_stream_t stream);
 
 /*
  * A decode step's cache write and decode attention in one launch: the decode

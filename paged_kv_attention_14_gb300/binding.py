@@ -55,7 +55,7 @@ EXPORTED = ("pa_abi_version", "pa_last_error", "pa_cache_write", "pa_decode_work
             "pa_mixed_workspace_size", "pa_mixed_attention", "pa_prefill_workspace_size",
             "pa_prefill_chunk_balanced", "pa_test_prefill_schedule", "pa_prefill_balanced_chosen",
             "pa_decode_append", "pa_mixed_attention_append", "pa_qk_norm_rope", "pa_rope_cache_write",
-            "pa_decode_shared_workspace_size", "pa_decode_shared", "pa_widen_blocks")
+            "pa_decode_shared_workspace_size", "pa_decode_shared", "pa_widen_blocks", "pa_prompt_attention")
 
 
 class PaKvDesc(ctypes.Structure):
@@ -153,6 +153,8 @@ def load(path: Optional[str] = None):
         lib.pa_copy_blocks.restype = ctypes.c_int
         lib.pa_widen_blocks.argtypes = [D, P, P, P, P, P, P, I32, I32, P]
         lib.pa_widen_blocks.restype = ctypes.c_int
+        lib.pa_prompt_attention.argtypes = [D, P, P, P, I64, P, I64, P, I64, P, I32, I32, I32, F, P]
+        lib.pa_prompt_attention.restype = ctypes.c_int
         lib.pa_merge_partials.argtypes = [P, P, P, P, P, I32, I32, I32, I32, P]
         lib.pa_merge_partials.restype = ctypes.c_int
         lib.pa_decode_static.argtypes = [D, P, P, P, P, P, P, I32, P, I32, I32, F, P]
@@ -609,6 +611,29 @@ def pa_prefill_chunk(desc: PaKvDesc, out, q, query_start_loc, k_cache, v_cache, 
                                    _ptr(block_tables, _I32, "block_tables"), int(block_tables.shape[1]),
                                    _ptr(context_lens, _I32, "context_lens"), S, int(max_q_len),
                                    int(max_context_len), float(scale), _stream(stream)))
+
+
+def pa_prompt_attention(desc: PaKvDesc, out, q, k, v, query_start_loc, max_q_len: int, scale: float, lse=None,
+                        stream=None):
+    """Causal attention of packed prompts from their rows: q ``[T, Hq, D]``, k
+    and v ``[T, Hkv, D]`` (slices of one projection's output, say) -> out ``[T,
+    Hq, D]``, dense, in the activation type (lse ``[T, Hq]`` fp32).
+    ``query_start_loc``: int32 ``[S + 1]``."""
+    act, = _act(desc)
+    T, hq, hkv, d = q.shape[0], desc.num_q_heads, desc.num_kv_heads, desc.head_dim
+    qp, qs = _rows(q, act, T, hq, d, "q")
+    kp, ks = _rows(k, act, T, hkv, d, "k")
+    vp, vs = _rows(v, act, T, hkv, d, "v")
+    op, _ = _rows(out, act, T, hq, d, "out", True)
+    if op is None or kp is None or vp is None:
+        raise ValueError("out, q, k and v are required")
+    if lse is not None and lse.shape != (T, hq):
+        raise ValueError(f"lse must be [{T}, {hq}], got {list(lse.shape)}")
+    st = _launch_stream(stream, q, k, v, out, lse, query_start_loc)
+    dev = q.get_device()
+    _check(load().pa_prompt_attention(ctypes.byref(desc), op, None if lse is None else _at(lse, _F32, "lse", dev), qp,
+                                      qs, kp, ks, vp, vs, _at(query_start_loc, _I32, "query_start_loc", dev),
+                                      query_start_loc.shape[0] - 1, T, int(max_q_len), float(scale), st))
 
 
 def pa_prefill_workspace_size(desc: PaKvDesc, num_seqs: int, max_q_len: int) -> int:

@@ -601,6 +601,41 @@ pa_status pa_copy_blocks(const pa_kv_desc *desc, void *k_cache, void *v_cache, c
   return e == cudaSuccess ? ok() : cuda_fail(e);
 }
 
+pa_status pa_prompt_attention(const pa_kv_desc *desc, void *out, float *lse, const void *q, int64_t q_stride,
+                              const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                              const int32_t *query_start_loc, int32_t num_seqs, int32_t num_tokens, int32_t max_q_len,
+                              float scale, pa_stream_t stream) {
+  pa_status st = check_desc(desc, true);
+  if (st != PA_OK) return st;
+  if (num_seqs < 0 || num_tokens < 0 || max_q_len < 0)
+    return fail(PA_ERR_INVALID_ARG, "num_seqs, num_tokens and max_q_len must be >= 0%s");
+  if (num_seqs == 0 || num_tokens == 0 || max_q_len == 0) return ok();
+  if (max_q_len > num_tokens) return fail(PA_ERR_INVALID_ARG, "max_q_len must be at most num_tokens%s");
+  if (!out || !q || !k || !v || !query_start_loc)
+    return fail(PA_ERR_INVALID_ARG, "out, q, k, v and query_start_loc must be non-NULL%s");
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k) || !aligned16(v))
+    return fail(PA_ERR_INVALID_ARG, "out, q, k and v must be 16-byte aligned%s");
+  if ((reinterpret_cast<uintptr_t>(query_start_loc) & 3u) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return fail(PA_ERR_INVALID_ARG, "query_start_loc and lse must be 4-byte aligned%s");
+  const int64_t dq = static_cast<int64_t>(desc->num_q_heads) * desc->head_dim;
+  const int64_t dk = static_cast<int64_t>(desc->num_kv_heads) * desc->head_dim;
+  const int64_t far = int64_t{1} << 38;  // a tensor map's strides, in bytes, stay below 2^40
+  if ((q_stride != 0 && (q_stride < dq || q_stride % 8 != 0 || q_stride > far)) ||
+      (k_stride != 0 && (k_stride < dk || k_stride % 8 != 0 || k_stride > far)) ||
+      (v_stride != 0 && (v_stride < dk || v_stride % 8 != 0 || v_stride > far)))
+    return fail(PA_ERR_INVALID_ARG,
+                "token strides must be 0 or multiples of 8 elements that cover a token's heads, at most 2^38%s");
+  if (!(scale == scale)) return fail(PA_ERR_INVALID_ARG, "scale is NaN%s");
+  // a CTA per (up to 128 rows, kv head), at most twice as many places
+  const int64_t tokens = 128 / (desc->num_q_heads / desc->num_kv_heads);
+  if ((num_tokens / tokens + num_seqs) * desc->num_kv_heads > 0x3fffffff)
+    return fail(PA_ERR_UNSUPPORTED, "too many tokens and heads for one call%s");
+  const cudaError_t e =
+      pa::launch_prompt(*desc, out, lse, q, q_stride, k, k_stride, v, v_stride, query_start_loc, num_seqs, num_tokens,
+                        max_q_len, scale, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e);
+}
+
 pa_status pa_widen_blocks(const pa_kv_desc *desc, const void *k_cache, const void *v_cache, const int32_t *src_blocks,
                           void *k_out, void *v_out, const int32_t *dst_blocks, int32_t num_out_blocks,
                           int32_t num_pairs, pa_stream_t stream) {

@@ -29,6 +29,12 @@ cudaError_t launch_int4_widen(const pa_kv_desc &d, const void *k_cache, const vo
                               const int32_t *src_blocks, void *k_out, void *v_out, const int32_t *dst_blocks,
                               int32_t num_out_blocks, int32_t num_pairs, cudaStream_t stream);
 
+// Causal attention of packed prompts from their own rows (pa_prompt.cu); a
+// stride of 0 means dense rows.
+cudaError_t launch_prompt(const pa_kv_desc &d, void *out, float *lse, const void *q, int64_t q_stride, const void *k,
+                          int64_t k_stride, const void *v, int64_t v_stride, const int32_t *query_start_loc,
+                          int32_t num_seqs, int32_t num_tokens, int32_t max_q_len, float scale, cudaStream_t stream);
+
 cudaError_t launch_merge(float *out, float *lse_out, const float *part_o, const float *part_lse,
                          const int32_t *num_parts, int32_t num_seqs, int32_t num_heads,
                          int32_t max_parts, int32_t head_dim, cudaStream_t stream);

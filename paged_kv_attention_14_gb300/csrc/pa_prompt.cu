@@ -1,0 +1,649 @@
+// pa_prompt.cu -- causal attention of whole prompts from their own rows.
+//
+//   out_i = sum_{j <= i} softmax_j(scale q_i . k_j) v_j   within each prompt,
+// prompts of different lengths packed one behind another, query head h using kv
+// head h / g; sliding-window and chunked-local layers start at a later key.
+//
+// Work.  An item is up to 256 rows of one (prompt, kv head): the query tokens
+// times the g heads that share the kv head, in two tiles of 128 rows (128 / g
+// tokens each), so that every K / V tile of 128 keys feeds two products.  An item
+// is a CTA: warp 0 issues the products, warp 1 the copies (TMA, straight from
+// the strided rows), warps 2-3 look over the V tiles that some row sees only in
+// part, and a warpgroup per tile does the softmax, one row a thread.
+//
+// Per K tile and query tile: S = Q K^T into 128 columns of tensor memory; the
+// softmax writes P, in the activation type, over them; O += P V takes P from
+// tensor memory.  The tensor cores work on one tile while the other's softmax
+// runs.  The running maximum is raised only when it grows by 2^8 (O is then
+// rescaled in tensor memory), sums are fp32 of the unrounded weights.  P in 16
+// bits is off by half a step of the type that the output is rounded to as well.
+//
+// A weight of zero does not cancel an infinity or a NaN: in the V tiles that
+// some row sees in part, rows behind the keys in use are zeroed, and a row with
+// a value that is not finite is zeroed and noted; the epilogue adds it to
+// the queries that do see it, in fp32.
+//
+// Bounded by the tensor cores: 4 D flops a (query head, key) pair.
+#include <cuda.h>
+
+#include "pa_device.cuh"
+#include "pa_host_cache.h"
+#include "pa_internal.h"
+
+namespace pa {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int KT = 128;                  // keys of a tile
+constexpr float kRaise = 8.f;            // log2 units the maximum may be behind
+constexpr int kNoted = 32;               // partly seen tiles with a mask of their own
+
+struct Args {
+  CUtensorMap qmap, kmap, vmap;
+  void *out;
+  float *lse;
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t *starts;
+  int num_seqs, num_tokens, max_q_len, hq, hkv, g;
+  int rt;            // tokens of a tile: 128 / g
+  int tiles;         // items of a prompt of the longest length (by position), 0: items packed
+  int packed;        // ... and then their number
+  float scale2;      // scale * log2(e)
+  float qs, mul;     // its magnitude (1 for 0), and the factor (1, -1, 0) that is left
+  int window, chunk;
+  int32_t *err;
+  int checked, stall;
+  unsigned long long wait_ns;
+};
+
+template <int D, int NQT>
+struct Cfg {
+  static constexpr int HALVES = D / 64;
+  static constexpr int HALF = 128 * 128;  // bytes of 128 rows of 64 dims
+  static constexpr int TILE = HALVES * HALF;
+  static constexpr int NSK = NQT == 2 ? (D == 128 ? 3 : 4) : (D == 128 ? 1 : 2);
+  static constexpr int NSV = NQT == 2 ? (D == 128 ? 2 : 4) : (D == 128 ? 1 : 2);
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = OFF_Q + NQT * TILE;
+  static constexpr int OFF_V = OFF_K + NSK * TILE;
+  static constexpr int OFF_NOTE = OFF_V + NSV * TILE;  // [kNoted][4] masks
+  static constexpr int OFF_BAR = OFF_NOTE + kNoted * 16;
+  static constexpr int SMEM = OFF_BAR + 256 + 1024;  // alignment slack
+  static constexpr int THREADS = 128 + NQT * 128;
+  static constexpr uint32_t COLS = NQT * 256;  // tensor memory: S of each tile, then O
+  static constexpr uint32_t O_COL = NQT * KT;
+  // barriers
+  static constexpr int Q_FULL = 0, K_FULL = 1, K_EMPTY = K_FULL + NSK, V_FULL = K_EMPTY + NSK,
+                       V_EMPTY = V_FULL + NSV, V_OK = V_EMPTY + NSV, S_FULL = V_OK + NSV, P_FULL = S_FULL + NQT,
+                       DRAIN = P_FULL + NQT, NBAR = DRAIN + 1;
+  static_assert(NBAR * 8 + 32 <= 256 && SMEM <= 232448, "shared memory");
+};
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  return F16 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+}
+template <bool F16>
+__device__ __forceinline__ float val(uint16_t x) {
+  return F16 ? __half2float(__ushort_as_half(x)) : __uint_as_float(static_cast<uint32_t>(x) << 16);
+}
+
+// The item of a CTA; all lanes of the calling warp.  False: none.
+struct Item {
+  int start, len;  // the prompt's first token, its tokens
+  int p0;          // the item's first query
+  int head;        // kv head
+};
+template <int NQT>
+__device__ __forceinline__ bool find_item(const Args &a, Item &it) {
+  const int lane = threadIdx.x & 31, qt = NQT * a.rt;
+  int b = blockIdx.x;
+  it.head = b % a.hkv;
+  b /= a.hkv;
+  int s, tile;
+  if (a.tiles > 0) {  // the longest key ranges of all prompts first
+    s = b % a.num_seqs;
+    tile = a.tiles - 1 - b / a.num_seqs;
+  } else {
+    // items are numbered so that prompt s begins at start(s) / qt + s: room
+    // for all of its items, and no sums over the prompts before it
+    const int i = a.packed - 1 - b;
+    int lo = 0, n = a.num_seqs;
+    while (n > 1) {
+      const int step = (n + 31) / 32;
+      const int x = lo + lane * step;
+      const bool in = lane * step < n && __ldg(a.starts + x) / qt + x <= i;
+      const int c = __popc(__ballot_sync(0xffffffffu, in));
+      const int skip = (c > 0 ? c - 1 : 0) * step;
+      lo += skip;
+      n = min(step, n - skip);
+    }
+    s = lo;
+    tile = i - (__ldg(a.starts + s) / qt + s);
+  }
+  it.start = __ldg(a.starts + s);
+  int end = __ldg(a.starts + s + 1);
+  if (a.checked) {
+    if (it.start < 0 || end < it.start || end > a.num_tokens) return false;  // (reported by CTA 0)
+  }
+  it.len = end - it.start;
+  if (tile < 0 || tile >= (it.len + qt - 1) / qt) return false;
+  it.p0 = tile * qt;
+  return true;
+}
+
+template <int R>
+__device__ __forceinline__ void set_registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void set_registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+// Adds the noted V rows (zeroed in the products) that query `pos` sees to 32
+// dims of its output, from dim c0 on.
+template <int D, bool F16>
+__device__ __noinline__ void add_noted(const Args &a, const uint32_t *notes, const Item &it, int pos, int head, int first,
+                                       int j0, int n_iter, int seen_by_all_lo, int seen_by_all_hi, float lse2, int c0,
+                                       float *o) {
+  const uint16_t *q = a.q + static_cast<int64_t>(it.start + pos) * a.q_stride + head * D;
+  int e = 0;
+  for (int jj = 0; jj < n_iter; ++jj) {
+    const int k0 = (j0 + jj) * KT;
+    if (k0 >= seen_by_all_lo && k0 + KT <= seen_by_all_hi) continue;
+    for (int i = 0; i < KT; ++i) {
+      const int key = k0 + i;
+      if (key < first || key > pos) continue;
+      if (e < kNoted && !(notes[e * 4 + (i >> 5)] >> (i & 31) & 1u)) continue;
+      const uint16_t *k = a.k + static_cast<int64_t>(it.start + key) * a.k_stride + it.head * D;
+      const uint16_t *v = a.v + static_cast<int64_t>(it.start + key) * a.v_stride + it.head * D;
+      bool noted = false;
+      float x = 0.f;
+      for (int d = 0; d < D; ++d) {
+        noted |= !(fabsf(val<F16>(v[d])) <= 3.4e38f);
+        x = fmaf(val<F16>(q[d]), val<F16>(k[d]), x);
+      }
+      if (!noted) continue;
+      const float p = exp2f(x * a.scale2 - lse2);
+      for (int d = 0; d < 32; ++d) o[d] = fmaf(p, val<F16>(v[c0 + d]), o[d]);
+    }
+    ++e;
+  }
+}
+
+template <int D, bool F16, int NQT>
+__global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt_kernel(const __grid_constant__ Args a) {
+  using C = Cfg<D, NQT>;
+  constexpr int KVT = F16 ? kKvF16 : kKvBf16;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (a.checked && blockIdx.x == 0)
+    for (int s = threadIdx.x; s < a.num_seqs; s += C::THREADS) {
+      const int b = __ldg(a.starts + s), e = __ldg(a.starts + s + 1);
+      if (b < 0 || e < b || e > a.num_tokens || e - b > a.max_q_len) report_error(a.err, nullptr, kErrBadIndex);
+    }
+  Item it;
+  if (!find_item<NQT>(a, it)) return;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + C::NBAR);
+  volatile int *s_abort = reinterpret_cast<int *>(tmem_slot + 1);
+  int *s_noted = reinterpret_cast<int *>(tmem_slot + 2);
+  int *s_last = reinterpret_cast<int *>(tmem_slot + 3);  // K, V tiles whose copies were issued; Q's
+  uint32_t *notes = reinterpret_cast<uint32_t *>(smem + C::OFF_NOTE);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+
+  const int nq = min(NQT * a.rt, it.len - it.p0);  // queries
+  const int nt = NQT == 1 || nq <= a.rt ? 1 : 2;   // tiles
+  const int p1 = it.p0 + nq - 1;
+  const int kv_end = p1 + 1;
+  const int j0 = local_first_key(it.p0, a.window, a.chunk) / KT;
+  const int n_iter = (kv_end + KT - 1) / KT - j0;
+  // keys that every query of the item sees
+  const int all_lo = local_first_key(p1, a.window, a.chunk), all_hi = it.p0 + 1;
+
+  if (tid == 0) {
+    for (int i = 0; i < C::NSK; ++i) {
+      mbar_init(&bar[C::K_FULL + i], 1);
+      mbar_init(&bar[C::K_EMPTY + i], 1);
+    }
+    for (int i = 0; i < C::NSV; ++i) {
+      mbar_init(&bar[C::V_FULL + i], 1);
+      mbar_init(&bar[C::V_EMPTY + i], 1);
+      mbar_init(&bar[C::V_OK + i], 2);
+    }
+    for (int t = 0; t < NQT; ++t) {
+      mbar_init(&bar[C::S_FULL + t], 1);
+      mbar_init(&bar[C::P_FULL + t], 4);
+    }
+    mbar_init(&bar[C::Q_FULL], 1);
+    mbar_init(&bar[C::DRAIN], 1);
+    *s_abort = 0;
+    *s_noted = 0;
+    s_last[0] = s_last[1] = -1;
+    s_last[2] = 0;
+    fence_mbar_init();
+  }
+  for (int i = tid; i < kNoted * 4; i += C::THREADS) notes[i] = 0;
+  if (warp == 0) tmem_alloc(tmem_slot, C::COLS);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  bool ok = true;
+
+  if (warp < 4) {
+    set_registers_down<NQT == 2 ? 88 : 56>();
+    if (warp == 1) {
+      // ------------------------------------------------------- copies
+      if (lane == 0 && !a.stall) {
+        const uint64_t pol = l2_evict_first_policy();
+        uint64_t keep;
+        asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
+        mbar_arrive_expect_tx(&bar[C::Q_FULL], nt * C::HALVES * a.rt * a.g * 128);
+        for (int t = 0; t < nt; ++t)
+          for (int h = 0; h < C::HALVES; ++h)
+            tma_load_3d(smem + C::OFF_Q + t * C::TILE + h * C::HALF, &a.qmap, h * 64, it.head * a.g,
+                        it.start + it.p0 + t * a.rt, &bar[C::Q_FULL], pol);
+        s_last[2] = 1;
+        for (int jj = 0; jj < n_iter && ok; ++jj) {
+          const int row = it.start + (j0 + jj) * KT;
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {  // K, V
+            const int ns = part ? C::NSV : C::NSK, st = jj % ns;
+            const int full = (part ? C::V_FULL : C::K_FULL) + st, empty = (part ? C::V_EMPTY : C::K_EMPTY) + st;
+            if (jj >= ns && !mbar_wait(&bar[empty], ((jj / ns) - 1) & 1, a.wait_ns)) {
+              ok = false;
+              break;
+            }
+            if (*s_abort) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&bar[full], C::TILE);
+            for (int h = 0; h < C::HALVES; ++h)
+              tma_load_3d(smem + (part ? C::OFF_V : C::OFF_K) + st * C::TILE + h * C::HALF, part ? &a.vmap : &a.kmap,
+                          h * 64, it.head, row, &bar[full], keep);
+            s_last[part] = jj;
+          }
+        }
+        if (!ok) *s_abort = 1;
+      }
+    } else if (warp == 0) {
+      // ----------------------------------------------------- products
+      if (lane == 0) {
+        constexpr uint32_t IQK = umma_idesc_bf16(128, KT, false, false, F16);
+        constexpr uint32_t IPV = umma_idesc_bf16(128, D, false, true, F16);
+        auto qk = [&](int t, int jj) {
+          const uint32_t qb = sbase + C::OFF_Q + t * C::TILE, kb = sbase + C::OFF_K + (jj % C::NSK) * C::TILE;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16_ss(tmem + t * KT, umma_desc_sw128(qb + (kk >> 2) * C::HALF + (kk & 3) * 32, 16, 1024),
+                         umma_desc_sw128(kb + (kk >> 2) * C::HALF + (kk & 3) * 32, 16, 1024), IQK, kk > 0 ? 1u : 0u);
+        };
+        auto pv = [&](int t, int jj) {
+          const uint32_t vb = sbase + C::OFF_V + (jj % C::NSV) * C::TILE;
+#pragma unroll
+          for (int kk = 0; kk < KT / 16; ++kk)
+            umma_bf16_ts(tmem + C::O_COL + t * D, tmem + t * KT + (kk >> 1) * 32 + (kk & 1) * 8,
+                         umma_desc_sw128(vb + kk * 2048, C::HALF, 1024), IPV, jj > 0 || kk > 0 ? 1u : 0u);
+        };
+        ok = mbar_wait(&bar[C::Q_FULL], 0, a.wait_ns) && mbar_wait(&bar[C::K_FULL], 0, a.wait_ns);
+        if (ok) {
+          tc_fence_after_sync();
+          for (int t = 0; t < nt; ++t) {
+            qk(t, 0);
+            umma_commit(&bar[C::S_FULL + t]);
+          }
+          if (n_iter > 1 && C::NSK == 1) umma_commit(&bar[C::K_EMPTY]);  // the only slot: K may follow at once
+          ok = mbar_wait(&bar[C::V_OK], 0, a.wait_ns);
+        }
+        for (int jj = 0; jj < n_iter && ok; ++jj) {
+          const bool next = jj + 1 < n_iter;
+          for (int t = 0; t < nt; ++t) {
+            if (!mbar_wait_hint(&bar[C::P_FULL + t], jj & 1, a.wait_ns)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+            pv(t, jj);
+            if (t == nt - 1) {
+              umma_commit(&bar[C::V_EMPTY + jj % C::NSV]);  // V of tile jj is done with
+              if (next && C::NSV > 1 &&
+                  !mbar_wait(&bar[C::V_OK + (jj + 1) % C::NSV], ((jj + 1) / C::NSV) & 1, a.wait_ns)) {
+                ok = false;
+                break;
+              }
+            }
+            if (next) {
+              if (t == 0 && !mbar_wait(&bar[C::K_FULL + (jj + 1) % C::NSK], ((jj + 1) / C::NSK) & 1, a.wait_ns)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after_sync();
+              qk(t, jj + 1);
+            }
+            // S of tile jj + 1 is there and P V of tile jj is done
+            umma_commit(&bar[C::S_FULL + t]);
+            if (t == nt - 1) {
+              if (C::NSK == 1 && jj + 2 < n_iter) umma_commit(&bar[C::K_EMPTY]);
+              if (next && C::NSV == 1 && !mbar_wait(&bar[C::V_OK], (jj + 1) & 1, a.wait_ns)) {
+                ok = false;
+                break;
+              }
+            }
+            if (C::NSK > 1 && t == 0) umma_commit(&bar[C::K_EMPTY + jj % C::NSK]);  // (a tile ago: both QKs are issued)
+          }
+        }
+        if (!ok) *s_abort = 1;
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------- V tiles looked over
+      const int ct = tid - 64;
+      int e = 0;  // partly seen tiles so far
+      for (int jj = 0; jj < n_iter; ++jj) {
+        const int st = jj % C::NSV, k0 = (j0 + jj) * KT;
+        if (!mbar_wait(&bar[C::V_FULL + st], (jj / C::NSV) & 1, a.wait_ns)) {
+          ok = false;
+          break;
+        }
+        if (k0 < all_lo || k0 + KT > all_hi) {
+          uint8_t *vt = smem + C::OFF_V + st * C::TILE;
+#pragma unroll 1
+          for (int r = ct; r < KT; r += 64) {
+            const bool drop = k0 + r >= kv_end;
+            uint32_t bad = 0;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+              const uint4 x = *reinterpret_cast<const uint4 *>(vt + (c >> 3) * C::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+              // an exponent of all ones carries into the sign's place
+              const uint32_t m = F16 ? 0x7C007C00u : 0x7F807F80u, one = F16 ? 0x04000400u : 0x00800080u;
+              bad |= ((x.x & m) + one) | ((x.y & m) + one) | ((x.z & m) + one) | ((x.w & m) + one);
+            }
+            bad &= 0x80008000u;
+            if (drop || bad) {
+              for (int c = 0; c < D / 8; ++c)
+                *reinterpret_cast<uint4 *>(vt + (c >> 3) * C::HALF + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+              if (!drop) {
+                if (e < kNoted) atomicOr(&notes[e * 4 + (r >> 5)], 1u << (r & 31));
+                *s_noted = 1;
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          ++e;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[C::V_OK + st]);
+      }
+      if (!ok && lane == 0) *s_abort = 1;
+    }
+  } else {
+    // --------------------------------------------------------- softmax
+    set_registers_up<NQT == 2 ? 208 : 200>();
+    const int t = (warp - 4) >> 2, r = tid - 128 - t * 128;  // tile, row
+    if (t < nt) {
+      const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      const int tok = r / a.g, pos = min(it.p0 + t * a.rt + tok, p1);
+      const bool live = tok < a.rt && it.p0 + t * a.rt + tok <= p1;
+      const int first = local_first_key(pos, a.window, a.chunk);
+      // keys that every row of this tile sees
+      const int t_hi = it.p0 + t * a.rt, t_lo = local_first_key(min(t_hi + a.rt - 1, p1), a.window, a.chunk);
+      float ms = -INFINITY;  // the reference maximum, scaled
+      float lsum = 0.f;
+      for (int jj = 0; jj < n_iter; ++jj) {
+        const int k0 = (j0 + jj) * KT;
+        if (!mbar_wait(&bar[C::S_FULL + t], jj & 1, a.wait_ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32_async(trow + t * KT + c * 32, s[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
+        if (a.mul != 1.f) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[c][i] = __float_as_uint(__uint_as_float(s[c][i]) * a.mul);
+        }
+        if (k0 + KT > t_hi + 1 || k0 < t_lo) {
+          const int hi = pos - k0, lo = first - k0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (c * 32 + i > hi || c * 32 + i < lo) s[c][i] = 0xff800000u;  // -inf
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float m4[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t *x = &s[c][8 * k];
+            m4[k] = fmax3(fmax3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2])),
+                          fmax3(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5])),
+                          fmaxf(__uint_as_float(x[6]), __uint_as_float(x[7])));
+          }
+          mx[c] = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
+        }
+        const float mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * a.qs;
+        if (__any_sync(0xffffffffu, mt > ms + kRaise)) {
+          const float nm = fmaxf(ms, mt);
+          const float alpha = ms == -INFINITY ? 0.f : ex2_approx(ms - nm);
+          ms = nm;
+          lsum *= alpha;
+          if (jj > 0) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float o[32];
+              tmem_ld32(trow + C::O_COL + t * D + c, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= alpha;
+              tmem_st32(trow + C::O_COL + t * D + c, o);
+            }
+          }
+        }
+        const float ref = ms == -INFINITY ? 0.f : ms;
+        const uint64_t q2 = f2_pack(a.qs, a.qs), r2 = f2_pack(-ref, -ref);
+        uint64_t l2[2] = {0, 0};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t p[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 y = f2_unpack(
+                f2_fma(f2_pack(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), q2, r2));
+            const float e0 = ex2_approx(y.x), e1 = ex2_approx(y.y);
+            l2[i & 1] = f2_add(l2[i & 1], f2_pack(e0, e1));
+            p[i] = pack16x2<KVT>(e0, e1);
+          }
+          tmem_st16_async(trow + t * KT + c * 32, p);
+        }
+        tmem_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[C::P_FULL + t]);
+        const float2 la = f2_unpack(f2_add(l2[0], l2[1]));
+        lsum += la.x + la.y;
+      }
+      // the last products
+      if (ok && !mbar_wait(&bar[C::S_FULL + t], n_iter & 1, a.wait_ns)) ok = false;
+      if (ok) {
+        tc_fence_after_sync();
+        const float inv = lsum == 0.f ? 0.f : 1.f / lsum;  // (a NaN stays one)
+        const float lse2 = lsum == 0.f ? -INFINITY : ms + log2f(lsum);
+        const int head = it.head * a.g + (r - tok * a.g);
+        const int64_t row = static_cast<int64_t>(it.start + it.p0 + t * a.rt + tok) * a.hq + head;
+        uint8_t *dst = static_cast<uint8_t *>(a.out) + row * (D * 2);
+        const bool noted = *reinterpret_cast<volatile int *>(s_noted) != 0;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(trow + C::O_COL + t * D + c, o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= inv;
+          if (live) {
+            if (noted)
+              add_noted<D, F16>(a, notes, it, pos, head, first, j0, n_iter, all_lo, all_hi, lse2, c, o);
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              *reinterpret_cast<uint4 *>(dst + (c + i) * 2) =
+                  make_uint4(pack2<F16>(o[i], o[i + 1]), pack2<F16>(o[i + 2], o[i + 3]), pack2<F16>(o[i + 4], o[i + 5]),
+                             pack2<F16>(o[i + 6], o[i + 7]));
+          }
+        }
+        if (live && a.lse) a.lse[row] = lse2 * kLn2;
+      }
+      if (!ok && lane == 0) *s_abort = 1;
+    }
+  }
+
+  // --- the end: copies in flight land, products complete, then the memory goes
+  tc_fence_before_sync();
+  __syncthreads();
+  if (*s_abort) {
+    if (tid == 0) report_error(a.err, nullptr, kErrWaitTimeout);
+    if (warp == 1 && lane == 0) {
+      if (s_last[2]) mbar_wait(&bar[C::Q_FULL], 0, a.wait_ns);
+      for (int j = max(0, s_last[0] - C::NSK + 1); j <= s_last[0]; ++j)
+        mbar_wait(&bar[C::K_FULL + j % C::NSK], (j / C::NSK) & 1, a.wait_ns);
+      for (int j = max(0, s_last[1] - C::NSV + 1); j <= s_last[1]; ++j)
+        mbar_wait(&bar[C::V_FULL + j % C::NSV], (j / C::NSV) & 1, a.wait_ns);
+    }
+  }
+  if (warp == 0 && lane == 0) {
+    umma_commit(&bar[C::DRAIN]);
+    mbar_wait(&bar[C::DRAIN], 0, a.wait_ns);
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 0) tmem_dealloc(tmem, C::COLS);
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled() {
+  static EncodeTiledFn fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  return fn;
+}
+
+// Rows [tokens][heads][d], `stride` elements from token to token, box {64
+// dims, `heads_box` heads, `tokens_box` tokens}; behind the last token zeros.
+bool make_rows_map(CUtensorMap *map, const void *base, bool f16, int tokens, int heads, int d, int64_t stride,
+                   int heads_box, int tokens_box) {
+  thread_local MapCache<24> cache;
+  const MapKey key = map_key(base, f16, tokens, heads, d, stride, heads_box, tokens_box);
+  if (cache.find(key, map)) return true;
+  EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads_box), static_cast<cuuint32_t>(tokens_box)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  if (enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base),
+          dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return false;
+  cache.put(key, *map);
+  return true;
+}
+
+template <int D, bool F16, int NQT>
+cudaError_t launch(Args &a, int max_q_len, cudaStream_t stream) {
+  using C = Cfg<D, NQT>;
+  const void *fn = reinterpret_cast<const void *>(&prompt_kernel<D, F16, NQT>);
+  if (prepare_kernel(fn, C::THREADS, C::SMEM) < 1) return cudaErrorInvalidConfiguration;
+  const int qt = NQT * a.rt;
+  // by position, the longest key ranges first, unless that leaves too many
+  // CTAs without an item (prompts much shorter than the longest)
+  const int64_t by_pos = (static_cast<int64_t>(max_q_len) + qt - 1) / qt * a.num_seqs;
+  const int64_t packed = a.num_tokens / qt + static_cast<int64_t>(a.num_seqs);
+  a.tiles = by_pos <= 2 * packed ? (max_q_len + qt - 1) / qt : 0;
+  a.packed = static_cast<int>(packed);
+  const int64_t items = (a.tiles ? by_pos : packed) * a.hkv;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(items));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  void *args[] = {&a};
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+template <int D, bool F16>
+cudaError_t launch_tiles(Args &a, int max_q_len, cudaStream_t stream) {
+  // prompts of one tile: a smaller CTA, two to an SM
+  return max_q_len <= a.rt ? launch<D, F16, 1>(a, max_q_len, stream) : launch<D, F16, 2>(a, max_q_len, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt(const pa_kv_desc &d, void *out, float *lse, const void *q, int64_t q_stride, const void *k,
+                          int64_t k_stride, const void *v, int64_t v_stride, const int32_t *query_start_loc,
+                          int32_t num_seqs, int32_t num_tokens, int32_t max_q_len, float scale, cudaStream_t stream) {
+  Args a;
+  memset(&a, 0, sizeof a);
+  const bool f16 = d.kv_dtype == PA_KV_F16 || d.kv_dtype == PA_KV_INT4_F16;
+  const int D = d.head_dim;
+  a.g = d.num_q_heads / d.num_kv_heads;
+  a.rt = 128 / a.g;
+  a.q_stride = q_stride ? q_stride : static_cast<int64_t>(d.num_q_heads) * D;
+  a.k_stride = k_stride ? k_stride : static_cast<int64_t>(d.num_kv_heads) * D;
+  a.v_stride = v_stride ? v_stride : static_cast<int64_t>(d.num_kv_heads) * D;
+  if (!make_rows_map(&a.qmap, q, f16, num_tokens, d.num_q_heads, D, a.q_stride, a.g, a.rt) ||
+      !make_rows_map(&a.kmap, k, f16, num_tokens, d.num_kv_heads, D, a.k_stride, 1, KT) ||
+      !make_rows_map(&a.vmap, v, f16, num_tokens, d.num_kv_heads, D, a.v_stride, 1, KT))
+    return cudaErrorInvalidValue;
+  a.out = out;
+  a.lse = lse;
+  a.q = static_cast<const uint16_t *>(q);
+  a.k = static_cast<const uint16_t *>(k);
+  a.v = static_cast<const uint16_t *>(v);
+  a.starts = query_start_loc;
+  a.num_seqs = num_seqs;
+  a.num_tokens = num_tokens;
+  a.max_q_len = max_q_len;
+  a.hq = d.num_q_heads;
+  a.hkv = d.num_kv_heads;
+  a.scale2 = scale * kLog2e;
+  a.qs = scale == 0.f ? 1.f : fabsf(a.scale2);
+  a.mul = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
+  a.window = d.sliding_window;
+  a.chunk = d.attention_chunk;
+  a.err = d.error_word;
+  a.checked = d.check_indices;
+  const TestHooks hooks = test_hooks();
+  a.stall = hooks.stall;
+  a.wait_ns = hooks.wait_ns;
+  if (D == 128) return f16 ? launch_tiles<128, true>(a, max_q_len, stream) : launch_tiles<128, false>(a, max_q_len, stream);
+  return f16 ? launch_tiles<64, true>(a, max_q_len, stream) : launch_tiles<64, false>(a, max_q_len, stream);
+}
+
+}  // namespace pa
