@@ -78,7 +78,7 @@ struct Cfg {
   // barriers
   static constexpr int Q_FULL = 0, K_FULL = 1, K_EMPTY = K_FULL + NSK, V_FULL = K_EMPTY + NSK,
                        V_EMPTY = V_FULL + NSV, V_OK = V_EMPTY + NSV, S_FULL = V_OK + NSV, P_FULL = S_FULL + NQT,
-                       DRAIN = P_FULL + NQT, NBAR = DRAIN + 1;
+                       P_REST = P_FULL + NQT, DRAIN = P_REST + NQT, NBAR = DRAIN + 1;
   static_assert(NBAR * 8 + 32 <= 256 && SMEM <= 232448, "shared memory");
 };
 
@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
     for (int t = 0; t < NQT; ++t) {
       mbar_init(&bar[C::S_FULL + t], 1);
       mbar_init(&bar[C::P_FULL + t], 4);
+      mbar_init(&bar[C::P_REST + t], 4);
     }
     mbar_init(&bar[C::Q_FULL], 1);
     mbar_init(&bar[C::DRAIN], 1);
@@ -276,72 +277,110 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
       }
     } else if (warp == 0) {
       // ----------------------------------------------------- products
-      if (lane == 0) {
-        constexpr uint32_t IQK = umma_idesc_bf16(128, KT, false, false, F16);
-        constexpr uint32_t IPV = umma_idesc_bf16(128, D, false, true, F16);
-        auto qk = [&](int t, int jj) {
-          const uint32_t qb = sbase + C::OFF_Q + t * C::TILE, kb = sbase + C::OFF_K + (jj % C::NSK) * C::TILE;
+      // the warp stays together, so that the operands are in uniform registers
+      // and a product is one instruction: with a lane's own registers the
+      // issuing took 105 and 80 cycles a product and 300 between the tiles
+      constexpr uint32_t IQK = umma_idesc_bf16(128, KT, false, false, F16);
+      constexpr uint32_t IPV = umma_idesc_bf16(128, D, false, true, F16);
+      const uint32_t q_lo = uniform(desc_low(sbase + C::OFF_Q, 16)), k_lo = uniform(desc_low(sbase + C::OFF_K, 16));
+      const uint32_t v_lo = uniform(desc_low(sbase + C::OFF_V, C::HALF));
+      const uint32_t tm = uniform(tmem);
+      auto qk = [&](int t, int stage) {
+        const uint32_t qd = uniform(q_lo + t * (C::TILE >> 4)), kd = uniform(k_lo + stage * (C::TILE >> 4));
+        const uint32_t s = uniform(tm + t * KT);
+        if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_bf16_ss(tmem + t * KT, umma_desc_sw128(qb + (kk >> 2) * C::HALF + (kk & 3) * 32, 16, 1024),
-                         umma_desc_sw128(kb + (kk >> 2) * C::HALF + (kk & 3) * 32, 16, 1024), IQK, kk > 0 ? 1u : 0u);
-        };
-        auto pv = [&](int t, int jj) {
-          const uint32_t vb = sbase + C::OFF_V + (jj % C::NSV) * C::TILE;
-#pragma unroll
-          for (int kk = 0; kk < KT / 16; ++kk)
-            umma_bf16_ts(tmem + C::O_COL + t * D, tmem + t * KT + (kk >> 1) * 32 + (kk & 1) * 8,
-                         umma_desc_sw128(vb + kk * 2048, C::HALF, 1024), IPV, jj > 0 || kk > 0 ? 1u : 0u);
-        };
-        ok = mbar_wait(&bar[C::Q_FULL], 0, a.wait_ns) && mbar_wait(&bar[C::K_FULL], 0, a.wait_ns);
-        if (ok) {
-          tc_fence_after_sync();
-          for (int t = 0; t < nt; ++t) {
-            qk(t, 0);
-            umma_commit(&bar[C::S_FULL + t]);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4;
+            mma_ss(s, qd + off, desc_high(1024), kd + off, desc_high(1024), IQK, kk > 0);
           }
-          if (n_iter > 1 && C::NSK == 1) umma_commit(&bar[C::K_EMPTY]);  // the only slot: K may follow at once
-          ok = mbar_wait(&bar[C::V_OK], 0, a.wait_ns);
         }
-        for (int jj = 0; jj < n_iter && ok; ++jj) {
-          const bool next = jj + 1 < n_iter;
-          for (int t = 0; t < nt; ++t) {
-            if (!mbar_wait_hint(&bar[C::P_FULL + t], jj & 1, a.wait_ns)) {
+        __syncwarp();
+      };
+      auto pv = [&](int t, int stage, int half, bool more) {
+        const uint32_t vd = uniform(v_lo + stage * (C::TILE >> 4)), p = uniform(tm + t * KT);
+        const uint32_t o = uniform(tm + C::O_COL + t * D), acc = uniform(more ? 1u : 0u);
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int kk = half * 4 + i;
+            mma_ts(o, p + (kk >> 1) * 32 + (kk & 1) * 8, vd + kk * (2048 >> 4), desc_high(1024), IPV,
+                   kk > 0 || acc != 0);
+          }
+        }
+        __syncwarp();
+      };
+      auto commit = [&](int b) {
+        if (elect_one()) umma_commit(&bar[b]);
+        __syncwarp();
+      };
+      ok = mbar_wait(&bar[C::Q_FULL], 0, a.wait_ns) && mbar_wait(&bar[C::K_FULL], 0, a.wait_ns);
+      if (ok) {
+        tc_fence_after_sync();
+        for (int t = 0; t < nt; ++t) {
+          qk(t, 0);
+          commit(C::S_FULL + t);
+        }
+        if (n_iter > 1 && C::NSK == 1) commit(C::K_EMPTY);  // the only slot: K may follow at once
+        ok = mbar_wait(&bar[C::V_OK], 0, a.wait_ns);
+      }
+      // stages and parities of tile jj (V) and jj + 1 (K, V)
+      int vs = 0, ks1 = 1 % C::NSK, vs1 = 1 % C::NSV;
+      uint32_t kpar1 = 1 / C::NSK, vpar1 = 1 / C::NSV;
+      for (int jj = 0; jj < n_iter && ok; ++jj) {
+        const bool next = jj + 1 < n_iter;
+#pragma unroll 1
+        for (int t = 0; t < nt; ++t) {
+          if (!mbar_wait_hint(&bar[C::P_FULL + t], jj & 1, a.wait_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          pv(t, vs, 0, jj > 0);
+          if (!mbar_wait_hint(&bar[C::P_REST + t], jj & 1, a.wait_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          pv(t, vs, 1, true);
+          if (t == nt - 1) {
+            commit(C::V_EMPTY + vs);  // V of tile jj is done with
+            if (next && C::NSV > 1 && !mbar_wait(&bar[C::V_OK + vs1], vpar1 & 1, a.wait_ns)) {
+              ok = false;
+              break;
+            }
+          }
+          if (next) {
+            if (t == 0 && !mbar_wait(&bar[C::K_FULL + ks1], kpar1 & 1, a.wait_ns)) {
               ok = false;
               break;
             }
             tc_fence_after_sync();
-            pv(t, jj);
-            if (t == nt - 1) {
-              umma_commit(&bar[C::V_EMPTY + jj % C::NSV]);  // V of tile jj is done with
-              if (next && C::NSV > 1 &&
-                  !mbar_wait(&bar[C::V_OK + (jj + 1) % C::NSV], ((jj + 1) / C::NSV) & 1, a.wait_ns)) {
-                ok = false;
-                break;
-              }
+            qk(t, ks1);
+          }
+          // S of tile jj + 1 is there and P V of tile jj is done
+          commit(C::S_FULL + t);
+          if (t == nt - 1) {
+            // K of tile jj + 1 is done with
+            if (jj + 1 + C::NSK < n_iter) commit(C::K_EMPTY + ks1);
+            if (next && C::NSV == 1 && !mbar_wait(&bar[C::V_OK], vpar1 & 1, a.wait_ns)) {
+              ok = false;
+              break;
             }
-            if (next) {
-              if (t == 0 && !mbar_wait(&bar[C::K_FULL + (jj + 1) % C::NSK], ((jj + 1) / C::NSK) & 1, a.wait_ns)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after_sync();
-              qk(t, jj + 1);
-            }
-            // S of tile jj + 1 is there and P V of tile jj is done
-            umma_commit(&bar[C::S_FULL + t]);
-            if (t == nt - 1) {
-              if (C::NSK == 1 && jj + 2 < n_iter) umma_commit(&bar[C::K_EMPTY]);
-              if (next && C::NSV == 1 && !mbar_wait(&bar[C::V_OK], (jj + 1) & 1, a.wait_ns)) {
-                ok = false;
-                break;
-              }
-            }
-            if (C::NSK > 1 && t == 0) umma_commit(&bar[C::K_EMPTY + jj % C::NSK]);  // (a tile ago: both QKs are issued)
           }
         }
-        if (!ok) *s_abort = 1;
+        if (jj == 0 && C::NSK > 1 && C::NSK < n_iter) commit(C::K_EMPTY);  // and of tile 0
+        vs = vs1;
+        if (++vs1 == C::NSV) {
+          vs1 = 0;
+          ++vpar1;
+        }
+        if (++ks1 == C::NSK) {
+          ks1 = 0;
+          ++kpar1;
+        }
       }
+      if (!ok && lane == 0) *s_abort = 1;
       __syncwarp();
     } else {
       // ------------------------------------------------- V tiles looked over
@@ -468,11 +507,13 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
             p[i] = pack16x2<KVT>(e0, e1);
           }
           tmem_st16_async(trow + t * KT + c * 32, p);
+          if (c & 1) {  // the first 64 keys' products need not wait for the rest
+            tmem_wait_st();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[(c == 1 ? C::P_FULL : C::P_REST) + t]);
+          }
         }
-        tmem_wait_st();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[C::P_FULL + t]);
         const float2 la = f2_unpack(f2_add(l2[0], l2[1]));
         lsum += la.x + la.y;
       }
@@ -521,11 +562,11 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
         mbar_wait(&bar[C::V_FULL + j % C::NSV], (j / C::NSV) & 1, a.wait_ns);
     }
   }
-  if (warp == 0 && lane == 0) {
-    umma_commit(&bar[C::DRAIN]);
+  if (warp == 0) {
+    if (elect_one()) umma_commit(&bar[C::DRAIN]);  // the lane that issued the products
+    __syncwarp();
     mbar_wait(&bar[C::DRAIN], 0, a.wait_ns);
   }
-  __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
