@@ -6,10 +6,13 @@
 //
 // Work.  An item is up to 256 rows of one (prompt, kv head): the query tokens
 // times the g heads that share the kv head, in two tiles of 128 rows (128 / g
-// tokens each), so that every K / V tile of 128 keys feeds two products.  An item
-// is a CTA: warp 0 issues the products, warp 1 the copies (TMA, straight from
-// the strided rows), warps 2-3 look over the V tiles that some row sees only in
-// part, and a warpgroup per tile does the softmax, one row a thread.
+// tokens each), so that every K / V tile of 128 keys feeds two products.  A CTA
+// per SM runs its items through one pipeline: warp 0 issues the products, warp 1
+// the copies (TMA, straight from the strided rows, into the next item while the
+// last one's products run), warps 2-3 look over the V tiles that some row sees
+// only in part, and a warpgroup per tile does the softmax, one row a thread.
+// Items go to the CTAs in rows, longest key ranges first, every second row
+// backwards.
 //
 // Per K tile and query tile: S = Q K^T into 128 columns of tensor memory; the
 // softmax writes P, in the activation type, over them; O += P V takes P from
@@ -51,6 +54,7 @@ struct Args {
   int rt;            // tokens of a tile: 128 / g
   int tiles;         // items of a prompt of the longest length (by position), 0: items packed
   int packed;        // ... and then their number
+  int items;         // places for items of all kv heads
   float scale2;      // scale * log2(e)
   float qs, mul;     // its magnitude (1 for 0), and the factor (1, -1, 0) that is left
   int window, chunk;
@@ -64,22 +68,26 @@ struct Cfg {
   static constexpr int HALVES = D / 64;
   static constexpr int HALF = 128 * 128;  // bytes of 128 rows of 64 dims
   static constexpr int TILE = HALVES * HALF;
-  static constexpr int NSK = NQT == 2 ? (D == 128 ? 3 : 4) : (D == 128 ? 1 : 2);
-  static constexpr int NSV = NQT == 2 ? (D == 128 ? 2 : 4) : (D == 128 ? 1 : 2);
+  static constexpr int NSK = NQT == 2 ? (D == 128 ? 2 : 4) : (D == 128 ? 1 : 2);
+  static constexpr int NSV = NSK;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = OFF_Q + NQT * TILE;
   static constexpr int OFF_V = OFF_K + NSK * TILE;
-  static constexpr int OFF_NOTE = OFF_V + NSV * TILE;  // [kNoted][4] masks
-  static constexpr int OFF_BAR = OFF_NOTE + kNoted * 16;
-  static constexpr int SMEM = OFF_BAR + 256 + 1024;  // alignment slack
+  // 32 rows of a softmax warp on their way out: all dims, or 32 of them at a time
+  static constexpr int STAGE_ROW = NQT == 2 ? 128 : 64;
+  static constexpr int OFF_STAGE = OFF_V + NSV * TILE;
+  static constexpr int OFF_NOTE = OFF_STAGE + NQT * 4 * 32 * STAGE_ROW;  // [2][kNoted][4] masks
+  static constexpr int OFF_BAR = OFF_NOTE + 2 * kNoted * 16;
+  static constexpr int SMEM = OFF_BAR + 384 + 1024;  // alignment slack
   static constexpr int THREADS = 128 + NQT * 128;
   static constexpr uint32_t COLS = NQT * 256;  // tensor memory: S of each tile, then O
   static constexpr uint32_t O_COL = NQT * KT;
   // barriers
-  static constexpr int Q_FULL = 0, K_FULL = 1, K_EMPTY = K_FULL + NSK, V_FULL = K_EMPTY + NSK,
+  static constexpr int Q_FULL = 0, Q_EMPTY = 1, K_FULL = 2, K_EMPTY = K_FULL + NSK, V_FULL = K_EMPTY + NSK,
                        V_EMPTY = V_FULL + NSV, V_OK = V_EMPTY + NSV, S_FULL = V_OK + NSV, P_FULL = S_FULL + NQT,
-                       P_REST = P_FULL + NQT, DRAIN = P_REST + NQT, NBAR = DRAIN + 1;
-  static_assert(NBAR * 8 + 32 <= 256 && SMEM <= 232448, "shared memory");
+                       P_REST = P_FULL + NQT, O_FULL = P_REST + NQT, NOTED = O_FULL + NQT, DRAIN = NOTED + 2,
+                       NBAR = DRAIN + 1;
+  static_assert(NBAR * 8 + 32 <= 384 && SMEM <= (NQT == 2 ? 232448 : 115 * 1024), "shared memory");
 };
 
 template <bool F16>
@@ -91,16 +99,19 @@ __device__ __forceinline__ float val(uint16_t x) {
   return F16 ? __half2float(__ushort_as_half(x)) : __uint_as_float(static_cast<uint32_t>(x) << 16);
 }
 
-// The item of a CTA; all lanes of the calling warp.  False: none.
+// An item.
 struct Item {
-  int start, len;  // the prompt's first token, its tokens
-  int p0;          // the item's first query
-  int head;        // kv head
+  int start, len;        // the prompt's first token, its tokens
+  int p0, p1;            // the item's first and last query
+  int head;              // kv head
+  int nt;                // tiles
+  int j0, n_iter;        // tiles of keys
+  int all_lo, all_hi;    // keys that all of its queries see
 };
+// The item at place b; all lanes of the calling warp.  False: none.
 template <int NQT>
-__device__ __forceinline__ bool find_item(const Args &a, Item &it) {
+__device__ __forceinline__ bool find_item(const Args &a, int b, Item &it) {
   const int lane = threadIdx.x & 31, qt = NQT * a.rt;
-  int b = blockIdx.x;
   it.head = b % a.hkv;
   b /= a.hkv;
   int s, tile;
@@ -132,7 +143,20 @@ __device__ __forceinline__ bool find_item(const Args &a, Item &it) {
   it.len = end - it.start;
   if (tile < 0 || tile >= (it.len + qt - 1) / qt) return false;
   it.p0 = tile * qt;
+  it.p1 = min(it.p0 + qt, it.len) - 1;
+  it.nt = it.p1 - it.p0 < a.rt ? 1 : NQT;
+  it.j0 = local_first_key(it.p0, a.window, a.chunk) / KT;
+  it.n_iter = it.p1 / KT + 1 - it.j0;
+  it.all_lo = local_first_key(it.p1, a.window, a.chunk);
+  it.all_hi = it.p0 + 1;
   return true;
+}
+
+// The place of this CTA's i-th item: rows of a place per CTA, every second one
+// backwards.
+__device__ __forceinline__ int place(int i) {
+  const int c = blockIdx.x, n = gridDim.x;
+  return i * n + (i & 1 ? n - 1 - c : c);
 }
 
 template <int R>
@@ -148,13 +172,12 @@ __device__ __forceinline__ void set_registers_up() {
 // dims of its output, from dim c0 on.
 template <int D, bool F16>
 __device__ __noinline__ void add_noted(const Args &a, const uint32_t *notes, const Item &it, int pos, int head, int first,
-                                       int j0, int n_iter, int seen_by_all_lo, int seen_by_all_hi, float lse2, int c0,
-                                       float *o) {
+                                       float lse2, int c0, float *o) {
   const uint16_t *q = a.q + static_cast<int64_t>(it.start + pos) * a.q_stride + head * D;
   int e = 0;
-  for (int jj = 0; jj < n_iter; ++jj) {
-    const int k0 = (j0 + jj) * KT;
-    if (k0 >= seen_by_all_lo && k0 + KT <= seen_by_all_hi) continue;
+  for (int jj = 0; jj < it.n_iter; ++jj) {
+    const int k0 = (it.j0 + jj) * KT;
+    if (k0 >= it.all_lo && k0 + KT <= it.all_hi) continue;
     for (int i = 0; i < KT; ++i) {
       const int key = k0 + i;
       if (key < first || key > pos) continue;
@@ -179,34 +202,22 @@ template <int D, bool F16, int NQT>
 __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt_kernel(const __grid_constant__ Args a) {
   using C = Cfg<D, NQT>;
   constexpr int KVT = F16 ? kKvF16 : kKvBf16;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (a.checked && blockIdx.x == 0)
-    for (int s = threadIdx.x; s < a.num_seqs; s += C::THREADS) {
-      const int b = __ldg(a.starts + s), e = __ldg(a.starts + s + 1);
-      if (b < 0 || e < b || e > a.num_tokens || e - b > a.max_q_len) report_error(a.err, nullptr, kErrBadIndex);
-    }
-  Item it;
-  if (!find_item<NQT>(a, it)) return;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + C::NBAR);
   volatile int *s_abort = reinterpret_cast<int *>(tmem_slot + 1);
-  int *s_noted = reinterpret_cast<int *>(tmem_slot + 2);
-  int *s_last = reinterpret_cast<int *>(tmem_slot + 3);  // K, V tiles whose copies were issued; Q's
+  int *s_noted = reinterpret_cast<int *>(tmem_slot + 2);  // [2]
+  int *s_last = reinterpret_cast<int *>(tmem_slot + 4);   // K and V tiles and Qs whose copies were issued
   uint32_t *notes = reinterpret_cast<uint32_t *>(smem + C::OFF_NOTE);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
-  const int nq = min(NQT * a.rt, it.len - it.p0);  // queries
-  const int nt = NQT == 1 || nq <= a.rt ? 1 : 2;   // tiles
-  const int p1 = it.p0 + nq - 1;
-  const int kv_end = p1 + 1;
-  const int j0 = local_first_key(it.p0, a.window, a.chunk) / KT;
-  const int n_iter = (kv_end + KT - 1) / KT - j0;
-  // keys that every query of the item sees
-  const int all_lo = local_first_key(p1, a.window, a.chunk), all_hi = it.p0 + 1;
-
+  if (tid == 32) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a.qmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a.kmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a.vmap)) : "memory");
+  }
   if (tid == 0) {
     for (int i = 0; i < C::NSK; ++i) {
       mbar_init(&bar[C::K_FULL + i], 1);
@@ -221,59 +232,71 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
       mbar_init(&bar[C::S_FULL + t], 1);
       mbar_init(&bar[C::P_FULL + t], 4);
       mbar_init(&bar[C::P_REST + t], 4);
+      mbar_init(&bar[C::O_FULL + t], 1);
     }
     mbar_init(&bar[C::Q_FULL], 1);
+    mbar_init(&bar[C::Q_EMPTY], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&bar[C::NOTED + i], NQT * 4);
     mbar_init(&bar[C::DRAIN], 1);
     *s_abort = 0;
-    *s_noted = 0;
-    s_last[0] = s_last[1] = -1;
-    s_last[2] = 0;
+    s_noted[0] = s_noted[1] = 0;
+    s_last[0] = s_last[1] = s_last[2] = 0;
     fence_mbar_init();
   }
-  for (int i = tid; i < kNoted * 4; i += C::THREADS) notes[i] = 0;
+  for (int i = tid; i < 2 * kNoted * 4; i += C::THREADS) notes[i] = 0;
   if (warp == 0) tmem_alloc(tmem_slot, C::COLS);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  // the tensor memory of a kernel before this one is free by now, its results
+  // are there after this
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (a.checked && blockIdx.x == 0)
+    for (int s = tid; s < a.num_seqs; s += C::THREADS) {
+      const int b = __ldg(a.starts + s), e = __ldg(a.starts + s + 1);
+      if (b < 0 || e < b || e > a.num_tokens || e - b > a.max_q_len) report_error(a.err, nullptr, kErrBadIndex);
+    }
   bool ok = true;
+  Item it;
 
   if (warp < 4) {
     set_registers_down<NQT == 2 ? 88 : 56>();
     if (warp == 1) {
       // ------------------------------------------------------- copies
-      if (lane == 0 && !a.stall) {
-        const uint64_t pol = l2_evict_first_policy();
-        uint64_t keep;
-        asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
-        mbar_arrive_expect_tx(&bar[C::Q_FULL], nt * C::HALVES * a.rt * a.g * 128);
-        for (int t = 0; t < nt; ++t)
-          for (int h = 0; h < C::HALVES; ++h)
-            tma_load_3d(smem + C::OFF_Q + t * C::TILE + h * C::HALF, &a.qmap, h * 64, it.head * a.g,
-                        it.start + it.p0 + t * a.rt, &bar[C::Q_FULL], pol);
-        s_last[2] = 1;
-        for (int jj = 0; jj < n_iter && ok; ++jj) {
-          const int row = it.start + (j0 + jj) * KT;
+      const uint64_t pol = l2_evict_first_policy();
+      uint64_t keep;
+      asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
+      int nq = 0, nk = 0;  // Qs, K (and V) tiles so far
+      for (int i = 0; i * gridDim.x < static_cast<unsigned>(a.items) && ok && !a.stall; ++i) {
+        const int b = place(i);
+        if (b >= a.items || !find_item<NQT>(a, b, it)) continue;
+        if (nq > 0 && !mbar_wait(&bar[C::Q_EMPTY], (nq - 1) & 1, a.wait_ns)) ok = false;
+        if (ok && lane == 0) {
+          mbar_arrive_expect_tx(&bar[C::Q_FULL], it.nt * C::HALVES * a.rt * a.g * 128);
+          for (int t = 0; t < it.nt; ++t)
+            for (int h = 0; h < C::HALVES; ++h)
+              tma_load_3d(smem + C::OFF_Q + t * C::TILE + h * C::HALF, &a.qmap, h * 64, it.head * a.g,
+                          it.start + it.p0 + t * a.rt, &bar[C::Q_FULL], pol);
+          s_last[2] = nq + 1;
+        }
+        ++nq;
+        for (int jj = 0; jj < it.n_iter && ok; ++jj, ++nk) {
+          const int row = it.start + (it.j0 + jj) * KT, st = nk % C::NSK, use = nk / C::NSK;
 #pragma unroll
           for (int part = 0; part < 2; ++part) {  // K, V
-            const int ns = part ? C::NSV : C::NSK, st = jj % ns;
             const int full = (part ? C::V_FULL : C::K_FULL) + st, empty = (part ? C::V_EMPTY : C::K_EMPTY) + st;
-            if (jj >= ns && !mbar_wait(&bar[empty], ((jj / ns) - 1) & 1, a.wait_ns)) {
-              ok = false;
-              break;
+            if (ok && use > 0 && !mbar_wait(&bar[empty], (use - 1) & 1, a.wait_ns)) ok = false;
+            if (*s_abort) ok = false;
+            if (ok && lane == 0) {
+              mbar_arrive_expect_tx(&bar[full], C::TILE);
+              for (int h = 0; h < C::HALVES; ++h)
+                tma_load_3d(smem + (part ? C::OFF_V : C::OFF_K) + st * C::TILE + h * C::HALF, part ? &a.vmap : &a.kmap,
+                            h * 64, it.head, row, &bar[full], keep);
+              s_last[part] = nk + 1;
             }
-            if (*s_abort) {
-              ok = false;
-              break;
-            }
-            mbar_arrive_expect_tx(&bar[full], C::TILE);
-            for (int h = 0; h < C::HALVES; ++h)
-              tma_load_3d(smem + (part ? C::OFF_V : C::OFF_K) + st * C::TILE + h * C::HALF, part ? &a.vmap : &a.kmap,
-                          h * 64, it.head, row, &bar[full], keep);
-            s_last[part] = jj;
           }
         }
-        if (!ok) *s_abort = 1;
       }
     } else if (warp == 0) {
       // ----------------------------------------------------- products
@@ -314,251 +337,311 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
         if (elect_one()) umma_commit(&bar[b]);
         __syncwarp();
       };
-      ok = mbar_wait(&bar[C::Q_FULL], 0, a.wait_ns) && mbar_wait(&bar[C::K_FULL], 0, a.wait_ns);
-      if (ok) {
+      uint32_t nq = 0, p_par[2] = {0, 0};
+      int vs = 0, ks = 0;  // stages of the next V and K tile, and their parities
+      uint32_t v_par = 0, k_par = 0;
+      for (int i = 0; i * gridDim.x < static_cast<unsigned>(a.items) && ok; ++i) {
+        const int b = place(i);
+        if (b >= a.items || !find_item<NQT>(a, b, it)) continue;
+        const int nt = it.nt, n_iter = it.n_iter;
+        // S of a key tile, both query tiles; then its K is done with
+        auto k_done = [&](bool last) {
+          commit(C::K_EMPTY + ks);
+          if (last) commit(C::Q_EMPTY);
+          if (++ks == C::NSK) {
+            ks = 0;
+            k_par ^= 1;
+          }
+        };
+        ok = mbar_wait(&bar[C::Q_FULL], nq & 1, a.wait_ns) && mbar_wait(&bar[C::K_FULL + ks], k_par, a.wait_ns);
+        ++nq;
+        if (!ok) break;
         tc_fence_after_sync();
         for (int t = 0; t < nt; ++t) {
-          qk(t, 0);
+          qk(t, ks);
           commit(C::S_FULL + t);
         }
-        if (n_iter > 1 && C::NSK == 1) commit(C::K_EMPTY);  // the only slot: K may follow at once
-        ok = mbar_wait(&bar[C::V_OK], 0, a.wait_ns);
-      }
-      // stages and parities of tile jj (V) and jj + 1 (K, V)
-      int vs = 0, ks1 = 1 % C::NSK, vs1 = 1 % C::NSV;
-      uint32_t kpar1 = 1 / C::NSK, vpar1 = 1 / C::NSV;
-      for (int jj = 0; jj < n_iter && ok; ++jj) {
-        const bool next = jj + 1 < n_iter;
-#pragma unroll 1
-        for (int t = 0; t < nt; ++t) {
-          if (!mbar_wait_hint(&bar[C::P_FULL + t], jj & 1, a.wait_ns)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          pv(t, vs, 0, jj > 0);
-          if (!mbar_wait_hint(&bar[C::P_REST + t], jj & 1, a.wait_ns)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          pv(t, vs, 1, true);
-          if (t == nt - 1) {
-            commit(C::V_EMPTY + vs);  // V of tile jj is done with
-            if (next && C::NSV > 1 && !mbar_wait(&bar[C::V_OK + vs1], vpar1 & 1, a.wait_ns)) {
+        k_done(n_iter == 1);
+        for (int jj = 0; jj < n_iter && ok; ++jj) {
+          const bool next = jj + 1 < n_iter;
+          ok = mbar_wait(&bar[C::V_OK + vs], v_par, a.wait_ns);
+#pragma unroll
+          for (int t = 0; t < NQT; ++t) {
+            if (t >= nt || !ok) continue;
+            if (!mbar_wait_hint(&bar[C::P_FULL + t], p_par[t], a.wait_ns)) {
               ok = false;
-              break;
-            }
-          }
-          if (next) {
-            if (t == 0 && !mbar_wait(&bar[C::K_FULL + ks1], kpar1 & 1, a.wait_ns)) {
-              ok = false;
-              break;
+              continue;
             }
             tc_fence_after_sync();
-            qk(t, ks1);
-          }
-          // S of tile jj + 1 is there and P V of tile jj is done
-          commit(C::S_FULL + t);
-          if (t == nt - 1) {
-            // K of tile jj + 1 is done with
-            if (jj + 1 + C::NSK < n_iter) commit(C::K_EMPTY + ks1);
-            if (next && C::NSV == 1 && !mbar_wait(&bar[C::V_OK], vpar1 & 1, a.wait_ns)) {
+            pv(t, vs, 0, jj > 0);
+            if (!mbar_wait_hint(&bar[C::P_REST + t], p_par[t], a.wait_ns)) {
               ok = false;
-              break;
+              continue;
+            }
+            p_par[t] ^= 1;
+            tc_fence_after_sync();
+            pv(t, vs, 1, true);
+            if (t == nt - 1) commit(C::V_EMPTY + vs);
+            if (next) {
+              if (t == 0 && !mbar_wait(&bar[C::K_FULL + ks], k_par, a.wait_ns)) {
+                ok = false;
+                continue;
+              }
+              tc_fence_after_sync();
+              qk(t, ks);
+              commit(C::S_FULL + t);  // S of the next key tile is there, and P V of this one done
+            } else {
+              commit(C::O_FULL + t);
             }
           }
-        }
-        if (jj == 0 && C::NSK > 1 && C::NSK < n_iter) commit(C::K_EMPTY);  // and of tile 0
-        vs = vs1;
-        if (++vs1 == C::NSV) {
-          vs1 = 0;
-          ++vpar1;
-        }
-        if (++ks1 == C::NSK) {
-          ks1 = 0;
-          ++kpar1;
+          if (next && ok) k_done(jj + 2 == n_iter);
+          if (++vs == C::NSV) {
+            vs = 0;
+            v_par ^= 1;
+          }
         }
       }
-      if (!ok && lane == 0) *s_abort = 1;
-      __syncwarp();
     } else {
       // ------------------------------------------------- V tiles looked over
       const int ct = tid - 64;
-      int e = 0;  // partly seen tiles so far
-      for (int jj = 0; jj < n_iter; ++jj) {
-        const int st = jj % C::NSV, k0 = (j0 + jj) * KT;
-        if (!mbar_wait(&bar[C::V_FULL + st], (jj / C::NSV) & 1, a.wait_ns)) {
-          ok = false;
-          break;
+      int nv = 0, n_items = 0;
+      for (int i = 0; i * gridDim.x < static_cast<unsigned>(a.items) && ok; ++i) {
+        const int b = place(i);
+        if (b >= a.items || !find_item<NQT>(a, b, it)) continue;
+        const int buf = n_items & 1;
+        uint32_t *note = notes + buf * kNoted * 4;
+        // the notes of the item before the last are read
+        if (n_items >= 2) {
+          if (!mbar_wait(&bar[C::NOTED + buf], ((n_items >> 1) - 1) & 1, a.wait_ns)) {
+            ok = false;
+            break;
+          }
+          if (*reinterpret_cast<volatile int *>(&s_noted[buf])) {
+            named_bar_sync(1, 64);  // both warps have seen it
+            for (int x = ct; x < kNoted * 4; x += 64) note[x] = 0;
+            s_noted[buf] = 0;
+            named_bar_sync(1, 64);
+          }
         }
-        if (k0 < all_lo || k0 + KT > all_hi) {
-          uint8_t *vt = smem + C::OFF_V + st * C::TILE;
+        ++n_items;
+        int e = 0;  // partly seen tiles so far
+        for (int jj = 0; jj < it.n_iter; ++jj, ++nv) {
+          const int st = nv % C::NSV, k0 = (it.j0 + jj) * KT;
+          if (!mbar_wait(&bar[C::V_FULL + st], (nv / C::NSV) & 1, a.wait_ns)) {
+            ok = false;
+            break;
+          }
+          if (k0 < it.all_lo || k0 + KT > it.all_hi) {
+            uint8_t *vt = smem + C::OFF_V + st * C::TILE;
 #pragma unroll 1
-          for (int r = ct; r < KT; r += 64) {
-            const bool drop = k0 + r >= kv_end;
-            uint32_t bad = 0;
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-              const uint4 x = *reinterpret_cast<const uint4 *>(vt + (c >> 3) * C::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-              // an exponent of all ones carries into the sign's place
-              const uint32_t m = F16 ? 0x7C007C00u : 0x7F807F80u, one = F16 ? 0x04000400u : 0x00800080u;
-              bad |= ((x.x & m) + one) | ((x.y & m) + one) | ((x.z & m) + one) | ((x.w & m) + one);
-            }
-            bad &= 0x80008000u;
-            if (drop || bad) {
-              for (int c = 0; c < D / 8; ++c)
-                *reinterpret_cast<uint4 *>(vt + (c >> 3) * C::HALF + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+            for (int r = ct; r < KT; r += 64) {
+              const bool drop = k0 + r > it.p1;
+              uint32_t bad = 0;
               if (!drop) {
-                if (e < kNoted) atomicOr(&notes[e * 4 + (r >> 5)], 1u << (r & 31));
-                *s_noted = 1;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                  const uint4 x =
+                      *reinterpret_cast<const uint4 *>(vt + (c >> 3) * C::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+                  // an exponent of all ones carries into the sign's place
+                  const uint32_t m = F16 ? 0x7C007C00u : 0x7F807F80u, one = F16 ? 0x04000400u : 0x00800080u;
+                  bad |= ((x.x & m) + one) | ((x.y & m) + one) | ((x.z & m) + one) | ((x.w & m) + one);
+                }
+                bad &= 0x80008000u;
+              }
+              if (drop || bad) {
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c)
+                  *reinterpret_cast<uint4 *>(vt + (c >> 3) * C::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+                      make_uint4(0, 0, 0, 0);
+                if (!drop) {
+                  if (e < kNoted) atomicOr(&note[e * 4 + (r >> 5)], 1u << (r & 31));
+                  *reinterpret_cast<volatile int *>(&s_noted[buf]) = 1;
+                }
               }
             }
+            fence_proxy_async_smem();
+            ++e;
           }
-          fence_proxy_async_smem();
-          ++e;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar[C::V_OK + st]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[C::V_OK + st]);
       }
-      if (!ok && lane == 0) *s_abort = 1;
     }
   } else {
     // --------------------------------------------------------- softmax
     set_registers_up<NQT == 2 ? 208 : 200>();
     const int t = (warp - 4) >> 2, r = tid - 128 - t * 128;  // tile, row
-    if (t < nt) {
-      const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-      const int tok = r / a.g, pos = min(it.p0 + t * a.rt + tok, p1);
-      const bool live = tok < a.rt && it.p0 + t * a.rt + tok <= p1;
-      const int first = local_first_key(pos, a.window, a.chunk);
-      // keys that every row of this tile sees
-      const int t_hi = it.p0 + t * a.rt, t_lo = local_first_key(min(t_hi + a.rt - 1, p1), a.window, a.chunk);
-      float ms = -INFINITY;  // the reference maximum, scaled
-      float lsum = 0.f;
-      for (int jj = 0; jj < n_iter; ++jj) {
-        const int k0 = (j0 + jj) * KT;
-        if (!mbar_wait(&bar[C::S_FULL + t], jj & 1, a.wait_ns)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after_sync();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_async(trow + t * KT + c * 32, s[c]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
-        if (a.mul != 1.f) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s[c][i] = __float_as_uint(__uint_as_float(s[c][i]) * a.mul);
-        }
-        if (k0 + KT > t_hi + 1 || k0 < t_lo) {
-          const int hi = pos - k0, lo = first - k0;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c * 32 + i > hi || c * 32 + i < lo) s[c][i] = 0xff800000u;  // -inf
-        }
-        float mx[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float m4[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t *x = &s[c][8 * k];
-            m4[k] = fmax3(fmax3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2])),
-                          fmax3(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5])),
-                          fmaxf(__uint_as_float(x[6]), __uint_as_float(x[7])));
+    const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const int tok = r / a.g, sub = r - tok * a.g;
+    uint8_t *stage = smem + C::OFF_STAGE + (warp - 4) * 32 * C::STAGE_ROW;
+    uint32_t s_par = 0, o_par = 0;
+    int n_items = 0;
+    for (int i = 0; i * gridDim.x < static_cast<unsigned>(a.items) && ok; ++i) {
+      const int b = place(i);
+      if (b >= a.items || !find_item<NQT>(a, b, it)) continue;
+      const int buf = n_items++ & 1;
+      if (t < it.nt) {
+        const int pos = min(it.p0 + t * a.rt + tok, it.p1);
+        const int first = local_first_key(pos, a.window, a.chunk);
+        // keys that every row of this warp sees
+        const int w_hi = __reduce_min_sync(0xffffffffu, pos), w_lo = __reduce_max_sync(0xffffffffu, first);
+        float ms = -INFINITY;  // the reference maximum, scaled
+        float lsum = 0.f;
+        for (int jj = 0; jj < it.n_iter; ++jj) {
+          const int k0 = (it.j0 + jj) * KT;
+          if (!mbar_wait(&bar[C::S_FULL + t], s_par, a.wait_ns)) {
+            ok = false;
+            break;
           }
-          mx[c] = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
-        }
-        const float mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * a.qs;
-        if (__any_sync(0xffffffffu, mt > ms + kRaise)) {
-          const float nm = fmaxf(ms, mt);
-          const float alpha = ms == -INFINITY ? 0.f : ex2_approx(ms - nm);
-          ms = nm;
-          lsum *= alpha;
-          if (jj > 0) {
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              float o[32];
-              tmem_ld32(trow + C::O_COL + t * D + c, o);
+          s_par ^= 1;
+          tc_fence_after_sync();
+          uint32_t s[4][32];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= alpha;
-              tmem_st32(trow + C::O_COL + t * D + c, o);
+          for (int c = 0; c < 4; ++c) tmem_ld32_async(trow + t * KT + c * 32, s[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
+          if (a.mul != 1.f) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int x = 0; x < 32; ++x) s[c][x] = __float_as_uint(__uint_as_float(s[c][x]) * a.mul);
+          }
+          if (k0 + KT > w_hi + 1 || k0 < w_lo) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int c0 = k0 + c * 32;
+              if (c0 + 31 > w_hi) {  // some row's last key is before the chunk's end
+                const int hi = pos - c0;
+#pragma unroll
+                for (int x = 0; x < 32; ++x) s[c][x] = x > hi ? 0xff800000u : s[c][x];  // -inf
+              }
+              if (c0 < w_lo) {
+                const int lo = first - c0;
+#pragma unroll
+                for (int x = 0; x < 32; ++x) s[c][x] = x < lo ? 0xff800000u : s[c][x];
+              }
             }
           }
-        }
-        const float ref = ms == -INFINITY ? 0.f : ms;
-        const uint64_t q2 = f2_pack(a.qs, a.qs), r2 = f2_pack(-ref, -ref);
-        uint64_t l2[2] = {0, 0};
+          float mx[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t p[16];
+          for (int c = 0; c < 4; ++c) {
+            float m4[4];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 y = f2_unpack(
-                f2_fma(f2_pack(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), q2, r2));
-            const float e0 = ex2_approx(y.x), e1 = ex2_approx(y.y);
-            l2[i & 1] = f2_add(l2[i & 1], f2_pack(e0, e1));
-            p[i] = pack16x2<KVT>(e0, e1);
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t *x = &s[c][8 * k];
+              m4[k] = fmax3(fmax3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2])),
+                            fmax3(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5])),
+                            fmaxf(__uint_as_float(x[6]), __uint_as_float(x[7])));
+            }
+            mx[c] = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
           }
-          tmem_st16_async(trow + t * KT + c * 32, p);
-          if (c & 1) {  // the first 64 keys' products need not wait for the rest
-            tmem_wait_st();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[(c == 1 ? C::P_FULL : C::P_REST) + t]);
+          const float mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * a.qs;
+          if (__any_sync(0xffffffffu, mt > ms + kRaise)) {
+            const float nm = fmaxf(ms, mt);
+            const float alpha = ms == -INFINITY ? 0.f : ex2_approx(ms - nm);
+            ms = nm;
+            lsum *= alpha;
+            if (jj > 0) {
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tmem_ld32(trow + C::O_COL + t * D + c, o);
+#pragma unroll
+                for (int x = 0; x < 32; ++x) o[x] *= alpha;
+                tmem_st32(trow + C::O_COL + t * D + c, o);
+              }
+            }
           }
+          const float ref = ms == -INFINITY ? 0.f : ms;
+          const uint64_t q2 = f2_pack(a.qs, a.qs), r2 = f2_pack(-ref, -ref);
+          uint64_t l2[2] = {0, 0};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t p[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              const float2 y = f2_unpack(
+                  f2_fma(f2_pack(__uint_as_float(s[c][2 * x]), __uint_as_float(s[c][2 * x + 1])), q2, r2));
+              const float e0 = ex2_approx(y.x), e1 = ex2_approx(y.y);
+              l2[x & 1] = f2_add(l2[x & 1], f2_pack(e0, e1));
+              p[x] = pack16x2<KVT>(e0, e1);
+            }
+            tmem_st16_async(trow + t * KT + c * 32, p);
+            if (c & 1) {  // the first 64 keys' products need not wait for the rest
+              tmem_wait_st();
+              tc_fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bar[(c == 1 ? C::P_FULL : C::P_REST) + t]);
+            }
+          }
+          const float2 la = f2_unpack(f2_add(l2[0], l2[1]));
+          lsum += la.x + la.y;
         }
-        const float2 la = f2_unpack(f2_add(l2[0], l2[1]));
-        lsum += la.x + la.y;
-      }
-      // the last products
-      if (ok && !mbar_wait(&bar[C::S_FULL + t], n_iter & 1, a.wait_ns)) ok = false;
-      if (ok) {
+        // the last products are done: out, through shared memory, so that a
+        // warp's stores cover whole rows (a row a thread was 16 bytes of 32
+        // rows a store: 64 lines each, 6000 cycles an item)
+        if (ok && !mbar_wait(&bar[C::O_FULL + t], o_par, a.wait_ns)) ok = false;
+        o_par ^= 1;
+        if (!ok) break;
         tc_fence_after_sync();
         const float inv = lsum == 0.f ? 0.f : 1.f / lsum;  // (a NaN stays one)
         const float lse2 = lsum == 0.f ? -INFINITY : ms + log2f(lsum);
-        const int head = it.head * a.g + (r - tok * a.g);
-        const int64_t row = static_cast<int64_t>(it.start + it.p0 + t * a.rt + tok) * a.hq + head;
-        uint8_t *dst = static_cast<uint8_t *>(a.out) + row * (D * 2);
-        const bool noted = *reinterpret_cast<volatile int *>(s_noted) != 0;
+        const int tok0 = it.start + it.p0 + t * a.rt;
+        const int left = min(a.rt, it.p1 + 1 - (it.p0 + t * a.rt)) * a.g;  // rows in use
+        const int head = it.head * a.g + sub;
+        const bool noted = *reinterpret_cast<volatile int *>(&s_noted[buf]) != 0;
+        if (r < left && a.lse) a.lse[static_cast<int64_t>(tok0 + tok) * a.hq + head] = lse2 * kLn2;
+        constexpr int PART = C::STAGE_ROW / 2;            // dims staged at a time
+        constexpr int LPR = C::STAGE_ROW / 16;            // lanes of a staged row
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float o[32];
-          tmem_ld32(trow + C::O_COL + t * D + c, o);
+        for (int c0 = 0; c0 < D; c0 += PART) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= inv;
-          if (live) {
-            if (noted)
-              add_noted<D, F16>(a, notes, it, pos, head, first, j0, n_iter, all_lo, all_hi, lse2, c, o);
+          for (int h = 0; h < PART / 32; ++h) {
+            float o[32];
+            tmem_ld32(trow + C::O_COL + t * D + c0 + h * 32, o);
 #pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              *reinterpret_cast<uint4 *>(dst + (c + i) * 2) =
-                  make_uint4(pack2<F16>(o[i], o[i + 1]), pack2<F16>(o[i + 2], o[i + 3]), pack2<F16>(o[i + 4], o[i + 5]),
-                             pack2<F16>(o[i + 6], o[i + 7]));
+            for (int x = 0; x < 32; ++x) o[x] *= inv;
+            if (noted && r < left)
+              add_noted<D, F16>(a, notes + buf * kNoted * 4, it, pos, head, first, lse2, c0 + h * 32, o);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              *reinterpret_cast<uint4 *>(stage + lane * C::STAGE_ROW + (((h * 4 + x) ^ (lane & (LPR - 1))) << 4)) =
+                  make_uint4(pack2<F16>(o[8 * x], o[8 * x + 1]), pack2<F16>(o[8 * x + 2], o[8 * x + 3]),
+                             pack2<F16>(o[8 * x + 4], o[8 * x + 5]), pack2<F16>(o[8 * x + 6], o[8 * x + 7]));
           }
+          __syncwarp();
+          const int row0 = (warp & 3) * 32;
+#pragma unroll
+          for (int x = 0; x < LPR; ++x) {
+            const int rr = x * (32 / LPR) + lane / LPR, ch = lane % LPR;
+            const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * C::STAGE_ROW + ((ch ^ (rr & (LPR - 1))) << 4));
+            const int q = row0 + rr;
+            if (q < left) {
+              const int qtok = q / a.g;
+              const int64_t at = (static_cast<int64_t>(tok0 + qtok) * a.hq + it.head * a.g + (q - qtok * a.g)) * D + c0;
+              *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.out) + at * 2 + ch * 16) = v;
+            }
+          }
+          __syncwarp();
         }
-        if (live && a.lse) a.lse[row] = lse2 * kLn2;
       }
-      if (!ok && lane == 0) *s_abort = 1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[C::NOTED + buf]);
     }
   }
+  if (!ok) *s_abort = 1;
 
   // --- the end: copies in flight land, products complete, then the memory goes
+  __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
   if (*s_abort) {
     if (tid == 0) report_error(a.err, nullptr, kErrWaitTimeout);
-    if (warp == 1 && lane == 0) {
-      if (s_last[2]) mbar_wait(&bar[C::Q_FULL], 0, a.wait_ns);
-      for (int j = max(0, s_last[0] - C::NSK + 1); j <= s_last[0]; ++j)
+    if (warp == 1) {
+      if (s_last[2] > 0) mbar_wait(&bar[C::Q_FULL], (s_last[2] - 1) & 1, a.wait_ns);
+      for (int j = max(0, s_last[0] - C::NSK); j < s_last[0]; ++j)
         mbar_wait(&bar[C::K_FULL + j % C::NSK], (j / C::NSK) & 1, a.wait_ns);
-      for (int j = max(0, s_last[1] - C::NSV + 1); j <= s_last[1]; ++j)
+      for (int j = max(0, s_last[1] - C::NSV); j < s_last[1]; ++j)
         mbar_wait(&bar[C::V_FULL + j % C::NSV], (j / C::NSV) & 1, a.wait_ns);
     }
   }
@@ -623,12 +706,13 @@ cudaError_t launch(Args &a, int max_q_len, cudaStream_t stream) {
   const int64_t packed = a.num_tokens / qt + static_cast<int64_t>(a.num_seqs);
   a.tiles = by_pos <= 2 * packed ? (max_q_len + qt - 1) / qt : 0;
   a.packed = static_cast<int>(packed);
-  const int64_t items = (a.tiles ? by_pos : packed) * a.hkv;
+  a.items = static_cast<int>((a.tiles ? by_pos : packed) * a.hkv);
+  const int ctas = device_sm_count() * (NQT == 2 ? 1 : 2);
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(items));
+  cfg.gridDim = dim3(static_cast<unsigned>(a.items < ctas ? a.items : ctas));
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
