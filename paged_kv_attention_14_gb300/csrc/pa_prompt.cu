@@ -42,6 +42,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int KT = 128;                  // keys of a tile
 constexpr float kRaise = 8.f;            // log2 units the maximum may be behind
 constexpr int kNoted = 32;               // partly seen tiles with a mask of their own
+constexpr int kAhead = 4;                // items found before they are needed
 
 struct Args {
   CUtensorMap qmap, kmap, vmap;
@@ -78,15 +79,16 @@ struct Cfg {
   static constexpr int OFF_STAGE = OFF_V + NSV * TILE;
   static constexpr int OFF_NOTE = OFF_STAGE + NQT * 4 * 32 * STAGE_ROW;  // [2][kNoted][4] masks
   static constexpr int OFF_BAR = OFF_NOTE + 2 * kNoted * 16;
-  static constexpr int SMEM = OFF_BAR + 384 + 1024;  // alignment slack
+  static constexpr int OFF_ITEM = OFF_BAR + 384;
+  static constexpr int SMEM = OFF_ITEM + kAhead * 64 + 1024;  // alignment slack
   static constexpr int THREADS = 128 + NQT * 128;
   static constexpr uint32_t COLS = NQT * 256;  // tensor memory: S of each tile, then O
   static constexpr uint32_t O_COL = NQT * KT;
   // barriers
   static constexpr int Q_FULL = 0, Q_EMPTY = 1, K_FULL = 2, K_EMPTY = K_FULL + NSK, V_FULL = K_EMPTY + NSK,
                        V_EMPTY = V_FULL + NSV, V_OK = V_EMPTY + NSV, S_FULL = V_OK + NSV, P_FULL = S_FULL + NQT,
-                       P_REST = P_FULL + NQT, O_FULL = P_REST + NQT, NOTED = O_FULL + NQT, DRAIN = NOTED + 2,
-                       NBAR = DRAIN + 1;
+                       P_REST = P_FULL + NQT, O_FULL = P_REST + NQT, NOTED = O_FULL + NQT, I_FULL = NOTED + 2,
+                       I_EMPTY = I_FULL + kAhead, DRAIN = I_EMPTY + kAhead, NBAR = DRAIN + 1;
   static_assert(NBAR * 8 + 32 <= 384 && SMEM <= (NQT == 2 ? 232448 : 115 * 1024), "shared memory");
 };
 
@@ -108,6 +110,8 @@ struct Item {
   int j0, n_iter;        // tiles of keys
   int all_lo, all_hi;    // keys that all of its queries see
 };
+static_assert(sizeof(Item) <= 64, "an item's place in shared memory");
+
 // The item at place b; all lanes of the calling warp.  False: none.
 template <int NQT>
 __device__ __forceinline__ bool find_item(const Args &a, int b, Item &it) {
@@ -168,33 +172,48 @@ __device__ __forceinline__ void set_registers_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-// Adds the noted V rows (zeroed in the products) that query `pos` sees to 32
-// dims of its output, from dim c0 on.
+// The outputs of a row (a lane of tensor memory, live or not; the whole warp
+// calls it) of an item with noted V rows: the products' sums, and the noted rows
+// that its query sees.
 template <int D, bool F16>
-__device__ __noinline__ void add_noted(const Args &a, const uint32_t *notes, const Item &it, int pos, int head, int first,
-                                       float lse2, int c0, float *o) {
+__device__ __noinline__ void store_noted(const Args &a, const uint32_t *notes, const Item &it, int pos, int head,
+                                         int first, bool live, float inv, float lse2, uint32_t o_at) {
   const uint16_t *q = a.q + static_cast<int64_t>(it.start + pos) * a.q_stride + head * D;
-  int e = 0;
-  for (int jj = 0; jj < it.n_iter; ++jj) {
-    const int k0 = (it.j0 + jj) * KT;
-    if (k0 >= it.all_lo && k0 + KT <= it.all_hi) continue;
-    for (int i = 0; i < KT; ++i) {
-      const int key = k0 + i;
-      if (key < first || key > pos) continue;
-      if (e < kNoted && !(notes[e * 4 + (i >> 5)] >> (i & 31) & 1u)) continue;
-      const uint16_t *k = a.k + static_cast<int64_t>(it.start + key) * a.k_stride + it.head * D;
-      const uint16_t *v = a.v + static_cast<int64_t>(it.start + key) * a.v_stride + it.head * D;
-      bool noted = false;
-      float x = 0.f;
-      for (int d = 0; d < D; ++d) {
-        noted |= !(fabsf(val<F16>(v[d])) <= 3.4e38f);
-        x = fmaf(val<F16>(q[d]), val<F16>(k[d]), x);
+  uint8_t *out = static_cast<uint8_t *>(a.out) + (static_cast<int64_t>(it.start + pos) * a.hq + head) * (D * 2);
+#pragma unroll 1
+  for (int c0 = 0; c0 < D; c0 += 32) {
+    float o[32];
+    tmem_ld32(o_at + c0, o);
+#pragma unroll
+    for (int x = 0; x < 32; ++x) o[x] *= inv;
+    int e = 0;
+    for (int jj = 0; jj < it.n_iter; ++jj) {
+      const int k0 = (it.j0 + jj) * KT;
+      if (k0 >= it.all_lo && k0 + KT <= it.all_hi) continue;
+      for (int i = 0; i < KT; ++i) {
+        const int key = k0 + i;
+        if (!live || key < first || key > pos) continue;
+        if (e < kNoted && !(notes[e * 4 + (i >> 5)] >> (i & 31) & 1u)) continue;
+        const uint16_t *k = a.k + static_cast<int64_t>(it.start + key) * a.k_stride + it.head * D;
+        const uint16_t *v = a.v + static_cast<int64_t>(it.start + key) * a.v_stride + it.head * D;
+        bool noted = false;
+        float x = 0.f;
+        for (int d = 0; d < D; ++d) {
+          noted |= !(fabsf(val<F16>(v[d])) <= 3.4e38f);
+          x = fmaf(val<F16>(q[d]), val<F16>(k[d]), x);
+        }
+        if (!noted) continue;
+        const float p = exp2f(x * a.scale2 - lse2);
+#pragma unroll
+        for (int d = 0; d < 32; ++d) o[d] = fmaf(p, val<F16>(v[c0 + d]), o[d]);
       }
-      if (!noted) continue;
-      const float p = exp2f(x * a.scale2 - lse2);
-      for (int d = 0; d < 32; ++d) o[d] = fmaf(p, val<F16>(v[c0 + d]), o[d]);
+      ++e;
     }
-    ++e;
+    __syncwarp();
+    if (live)
+#pragma unroll
+      for (int x = 0; x < 32; x += 2)
+        *reinterpret_cast<uint32_t *>(out + (c0 + x) * 2) = pack2<F16>(o[x], o[x + 1]);
   }
 }
 
@@ -237,6 +256,10 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
     mbar_init(&bar[C::Q_FULL], 1);
     mbar_init(&bar[C::Q_EMPTY], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&bar[C::NOTED + i], NQT * 4);
+    for (int i = 0; i < kAhead; ++i) {
+      mbar_init(&bar[C::I_FULL + i], 1);
+      mbar_init(&bar[C::I_EMPTY + i], 3 + NQT * 4);
+    }
     mbar_init(&bar[C::DRAIN], 1);
     *s_abort = 0;
     s_noted[0] = s_noted[1] = 0;
@@ -259,6 +282,21 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
     }
   bool ok = true;
   Item it;
+  int n_items = 0;
+  const Item *ring = reinterpret_cast<const Item *>(smem + C::OFF_ITEM);  // 64 bytes apart
+  // the next item that the copying warp found; false: no more, or a wait ran out
+  auto next_item = [&]() {
+    const int st = n_items % kAhead;
+    if (!mbar_wait(&bar[C::I_FULL + st], (n_items / kAhead) & 1, a.wait_ns)) {
+      ok = false;
+      return false;
+    }
+    it = *reinterpret_cast<const Item *>(reinterpret_cast<const uint8_t *>(ring) + st * 64);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[C::I_EMPTY + st]);
+    ++n_items;
+    return it.nt > 0;
+  };
 
   if (warp < 4) {
     set_registers_down<NQT == 2 ? 88 : 56>();
@@ -268,9 +306,21 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
       uint64_t keep;
       asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
       int nq = 0, nk = 0;  // Qs, K (and V) tiles so far
-      for (int i = 0; i * gridDim.x < static_cast<unsigned>(a.items) && ok && !a.stall; ++i) {
+      // hands an item (nt 0: the end) to the other warps
+      auto publish = [&]() {
+        const int st = n_items % kAhead, use = n_items / kAhead;
+        if (use > 0 && !mbar_wait(&bar[C::I_EMPTY + st], (use - 1) & 1, a.wait_ns)) ok = false;
+        if (ok && lane == 0) {
+          *reinterpret_cast<Item *>(smem + C::OFF_ITEM + st * 64) = it;
+          mbar_arrive(&bar[C::I_FULL + st]);
+        }
+        ++n_items;
+      };
+      for (int i = 0; i * gridDim.x < static_cast<unsigned>(a.items) && ok; ++i) {
         const int b = place(i);
         if (b >= a.items || !find_item<NQT>(a, b, it)) continue;
+        publish();
+        if (a.stall) continue;
         if (nq > 0 && !mbar_wait(&bar[C::Q_EMPTY], (nq - 1) & 1, a.wait_ns)) ok = false;
         if (ok && lane == 0) {
           mbar_arrive_expect_tx(&bar[C::Q_FULL], it.nt * C::HALVES * a.rt * a.g * 128);
@@ -298,6 +348,8 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
           }
         }
       }
+      it.nt = 0;
+      if (ok) publish();
     } else if (warp == 0) {
       // ----------------------------------------------------- products
       // the warp stays together, so that the operands are in uniform registers
@@ -340,9 +392,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
       uint32_t nq = 0, p_par[2] = {0, 0};
       int vs = 0, ks = 0;  // stages of the next V and K tile, and their parities
       uint32_t v_par = 0, k_par = 0;
-      for (int i = 0; i * gridDim.x < static_cast<unsigned>(a.items) && ok; ++i) {
-        const int b = place(i);
-        if (b >= a.items || !find_item<NQT>(a, b, it)) continue;
+      while (ok && next_item()) {
         const int nt = it.nt, n_iter = it.n_iter;
         // S of a key tile, both query tiles; then its K is done with
         auto k_done = [&](bool last) {
@@ -404,15 +454,13 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
     } else {
       // ------------------------------------------------- V tiles looked over
       const int ct = tid - 64;
-      int nv = 0, n_items = 0;
-      for (int i = 0; i * gridDim.x < static_cast<unsigned>(a.items) && ok; ++i) {
-        const int b = place(i);
-        if (b >= a.items || !find_item<NQT>(a, b, it)) continue;
-        const int buf = n_items & 1;
+      int nv = 0;
+      while (ok && next_item()) {
+        const int buf = (n_items - 1) & 1;
         uint32_t *note = notes + buf * kNoted * 4;
         // the notes of the item before the last are read
-        if (n_items >= 2) {
-          if (!mbar_wait(&bar[C::NOTED + buf], ((n_items >> 1) - 1) & 1, a.wait_ns)) {
+        if (n_items > 2) {
+          if (!mbar_wait(&bar[C::NOTED + buf], (((n_items - 1) >> 1) - 1) & 1, a.wait_ns)) {
             ok = false;
             break;
           }
@@ -423,7 +471,6 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
             named_bar_sync(1, 64);
           }
         }
-        ++n_items;
         int e = 0;  // partly seen tiles so far
         for (int jj = 0; jj < it.n_iter; ++jj, ++nv) {
           const int st = nv % C::NSV, k0 = (it.j0 + jj) * KT;
@@ -474,12 +521,10 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
     const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const int tok = r / a.g, sub = r - tok * a.g;
     uint8_t *stage = smem + C::OFF_STAGE + (warp - 4) * 32 * C::STAGE_ROW;
+    const unsigned g_inv = (65536 + a.g - 1) / a.g;  // x / g = x * g_inv >> 16 for x < 128
     uint32_t s_par = 0, o_par = 0;
-    int n_items = 0;
-    for (int i = 0; i * gridDim.x < static_cast<unsigned>(a.items) && ok; ++i) {
-      const int b = place(i);
-      if (b >= a.items || !find_item<NQT>(a, b, it)) continue;
-      const int buf = n_items++ & 1;
+    while (ok && next_item()) {
+      const int buf = (n_items - 1) & 1;
       if (t < it.nt) {
         const int pos = min(it.p0 + t * a.rt + tok, it.p1);
         const int first = local_first_key(pos, a.window, a.chunk);
@@ -589,40 +634,42 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
         const int tok0 = it.start + it.p0 + t * a.rt;
         const int left = min(a.rt, it.p1 + 1 - (it.p0 + t * a.rt)) * a.g;  // rows in use
         const int head = it.head * a.g + sub;
-        const bool noted = *reinterpret_cast<volatile int *>(&s_noted[buf]) != 0;
         if (r < left && a.lse) a.lse[static_cast<int64_t>(tok0 + tok) * a.hq + head] = lse2 * kLn2;
-        constexpr int PART = C::STAGE_ROW / 2;            // dims staged at a time
-        constexpr int LPR = C::STAGE_ROW / 16;            // lanes of a staged row
+        if (*reinterpret_cast<volatile int *>(&s_noted[buf]) != 0) {
+          store_noted<D, F16>(a, notes + buf * kNoted * 4, it, pos, head, first, r < left, inv, lse2,
+                              trow + C::O_COL + t * D);
+        } else {
+          constexpr int PART = C::STAGE_ROW / 2;  // dims staged at a time
+          constexpr int LPR = C::STAGE_ROW / 16;  // lanes of a staged row
+          uint8_t *out = static_cast<uint8_t *>(a.out) + (static_cast<int64_t>(tok0) * a.hq + it.head * a.g) * (D * 2);
 #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += PART) {
+          for (int c0 = 0; c0 < D; c0 += PART) {
 #pragma unroll
-          for (int h = 0; h < PART / 32; ++h) {
-            float o[32];
-            tmem_ld32(trow + C::O_COL + t * D + c0 + h * 32, o);
+            for (int h = 0; h < PART / 32; ++h) {
+              float o[32];
+              tmem_ld32(trow + C::O_COL + t * D + c0 + h * 32, o);
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] *= inv;
-            if (noted && r < left)
-              add_noted<D, F16>(a, notes + buf * kNoted * 4, it, pos, head, first, lse2, c0 + h * 32, o);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              *reinterpret_cast<uint4 *>(stage + lane * C::STAGE_ROW + (((h * 4 + x) ^ (lane & (LPR - 1))) << 4)) =
-                  make_uint4(pack2<F16>(o[8 * x], o[8 * x + 1]), pack2<F16>(o[8 * x + 2], o[8 * x + 3]),
-                             pack2<F16>(o[8 * x + 4], o[8 * x + 5]), pack2<F16>(o[8 * x + 6], o[8 * x + 7]));
-          }
-          __syncwarp();
-          const int row0 = (warp & 3) * 32;
-#pragma unroll
-          for (int x = 0; x < LPR; ++x) {
-            const int rr = x * (32 / LPR) + lane / LPR, ch = lane % LPR;
-            const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * C::STAGE_ROW + ((ch ^ (rr & (LPR - 1))) << 4));
-            const int q = row0 + rr;
-            if (q < left) {
-              const int qtok = q / a.g;
-              const int64_t at = (static_cast<int64_t>(tok0 + qtok) * a.hq + it.head * a.g + (q - qtok * a.g)) * D + c0;
-              *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.out) + at * 2 + ch * 16) = v;
+              for (int x = 0; x < 4; ++x)
+                *reinterpret_cast<uint4 *>(stage + lane * C::STAGE_ROW + (((h * 4 + x) ^ (lane & (LPR - 1))) << 4)) =
+                    make_uint4(pack2<F16>(o[8 * x] * inv, o[8 * x + 1] * inv),
+                               pack2<F16>(o[8 * x + 2] * inv, o[8 * x + 3] * inv),
+                               pack2<F16>(o[8 * x + 4] * inv, o[8 * x + 5] * inv),
+                               pack2<F16>(o[8 * x + 6] * inv, o[8 * x + 7] * inv));
             }
+            __syncwarp();
+            const int ch = lane % LPR;
+#pragma unroll
+            for (int x = 0; x < LPR; ++x) {
+              const int rr = x * (32 / LPR) + lane / LPR, q = (warp & 3) * 32 + rr;
+              const uint4 v =
+                  *reinterpret_cast<const uint4 *>(stage + rr * C::STAGE_ROW + ((ch ^ (rr & (LPR - 1))) << 4));
+              const int qtok = static_cast<int>(q * g_inv >> 16);
+              if (q < left)
+                *reinterpret_cast<uint4 *>(out + (static_cast<int64_t>(qtok) * a.hq + (q - qtok * a.g)) * (D * 2) +
+                                           c0 * 2 + ch * 16) = v;
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
       }
       __syncwarp();
