@@ -26,8 +26,8 @@
 // pair of fp16 (22 bits): rows 8..15 of the operand are the lo halves of rows
 // 0..7 (more than 8 query heads per kv head: a second product).
 //
-// The sums of the tensor cores round towards zero, so they run for 8 stages at
-// most and are then added to fp32 registers.
+// The sums of the tensor cores round towards zero, so they run over one stage
+// and are then added to fp32 registers.
 #include <cuda.h>
 
 #include "pa_host_cache.h"
@@ -39,7 +39,6 @@ namespace pa {
 namespace {
 
 constexpr int kMinUnits = 12;  // units a CTA gets at least, where there are few
-constexpr int kFlush = 8;      // stages between additions to the fp32 sums
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -54,18 +53,22 @@ struct Args {
   int32_t *err, *user_err;
   int checked, num_blocks, f16;
   int32_t *count;   // [CTAs]: pieces arrived of what begins in a CTA and goes on
-  float2 *slot_ml;  // [2 warps][g]: reference exponent, sum
-  float *slot_o;    // [2 warps][g][D]
+  // what a CTA has of a (sequence, kv head) that began before it, and of one
+  // that goes on behind it
+  float2 *slot_ml;  // [CTAs][2][g]: reference exponent, sum
+  float *slot_o;    // [CTAs][2][g][D]
 };
 
 template <int D, int NQ>
 struct Cfg {
-  static constexpr int W = NQ == 16 ? 8 : 12;  // warps: as many as the registers allow
+  static constexpr int W = 8;  // warps
   static constexpr int TB = i4::tile_bytes(D);
   static constexpr int STAGE = 4 * TB;  // K and V of two blocks
-  static constexpr int NST = D == 64 ? 8 : W == 8 ? 6 : 4;
+  static constexpr int NST = D == 64 ? 8 : NQ == 4 ? 5 : NQ == 8 ? 4 : 2;
   static constexpr int RING = NST * STAGE;
-  static constexpr int SMEM = W * RING;
+  static constexpr int OFF_ML = W * RING;                       // the pieces of the CTA's warps, two each:
+  static constexpr int OFF_O = OFF_ML + 2 * W * NQ * 8;        // [2 W][g] reference exponent, sum, and
+  static constexpr int SMEM = OFF_O + 2 * W * NQ * D * 4;      // [2 W][g][D]
   static constexpr int NG = D / 64;
 };
 
@@ -141,72 +144,53 @@ __device__ __forceinline__ Span span_of(const Args &a, int raw) {
   return s;
 }
 
-// Joins n pieces of one query row, slot_of(i) in turn: lane i holds a piece's
-// reference and sum, the pieces' dims come sixteen at a time.  To out / lse
-// (given the row's place), or to slot `to` (out NULL).
-template <int D, typename F>
-__device__ __forceinline__ void join_row(const Args &a, int n, F slot_of, int r, float *out, float *lse, int to) {
-  constexpr int LPR = D / 4;       // lanes per piece of a row, 4 dims each
-  constexpr int PPL = 32 / LPR;    // pieces at a time
-  const int lane = threadIdx.x & 31;
-  const int c = (lane % LPR) * 4, sub = lane / LPR;
-  float ref = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int base = 0; base < n; base += 32) {
-    const int m = min(32, n - base);
-    const int slot = slot_of(base + min(lane, m - 1));
-    const float2 ml =
-        lane < m ? __ldcg(&a.slot_ml[static_cast<int64_t>(slot) * a.g + r]) : make_float2(-INFINITY, 0.f);
-    const float nref = fmaxf(ref, warp_max_xor(ml.x, 1, 32));
-    const float w = ml.x == -INFINITY ? 0.f * ml.y : ex2_approx(ml.x - nref);
-    const float keep = ref == -INFINITY ? 0.f : ex2_approx(ref - nref);
-    float add = w * ml.y;
+// D / 32 dims of a row: a lane's part.
+template <int D>
+struct Part {
+  float x[D / 32];
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1) add += __shfl_xor_sync(0xffffffffu, add, k);
-    l = l * keep + add;
-    ref = nref;
-    o.x *= keep;
-    o.y *= keep;
-    o.z *= keep;
-    o.w *= keep;
-    for (int i0 = 0; i0 < m; i0 += 16) {
-      float4 x[16 / PPL];
-      float f[16 / PPL];
-#pragma unroll
-      for (int i = 0; i < 16 / PPL; ++i) {
-        const int at = min(i0 + i * PPL + sub, m - 1);
-        const int from = __shfl_sync(0xffffffffu, slot, at);
-        f[i] = __shfl_sync(0xffffffffu, w, at);
-        if (i0 + i * PPL + sub >= m) f[i] = 0.f;
-        x[i] = i0 + i * PPL + sub < m
-                   ? __ldcg(reinterpret_cast<const float4 *>(a.slot_o + (static_cast<int64_t>(from) * a.g + r) * D + c))
-                   : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-      for (int i = 0; i < 16 / PPL; ++i) {
-        o.x = fmaf(f[i], x[i].x, o.x);
-        o.y = fmaf(f[i], x[i].y, o.y);
-        o.z = fmaf(f[i], x[i].z, o.z);
-        o.w = fmaf(f[i], x[i].w, o.w);
-      }
+    for (int i = 0; i < D / 32; ++i) x[i] = 0.f;
+  }
+  __device__ __forceinline__ void load(const float *p) {
+    if constexpr (D == 128) {
+      const float4 v = *reinterpret_cast<const float4 *>(p);
+      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2 *>(p);
+      x[0] = v.x, x[1] = v.y;
     }
   }
-  if constexpr (PPL == 2) {
-    o.x += __shfl_xor_sync(0xffffffffu, o.x, 16);
-    o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
-    o.z += __shfl_xor_sync(0xffffffffu, o.z, 16);
-    o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
+  __device__ __forceinline__ void load_l2(const float *p) {
+    if constexpr (D == 128) {
+      const float4 v = __ldcg(reinterpret_cast<const float4 *>(p));
+      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+      const float2 v = __ldcg(reinterpret_cast<const float2 *>(p));
+      x[0] = v.x, x[1] = v.y;
+    }
   }
-  if (sub != 0) return;
-  if (out) {
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    *reinterpret_cast<float4 *>(out + c) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-    if (lse && c == 0) *lse = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
-  } else {
-    const int64_t at = static_cast<int64_t>(to) * a.g + r;
-    *reinterpret_cast<float4 *>(a.slot_o + at * D + c) = o;
-    if (c == 0) a.slot_ml[at] = make_float2(ref, l);
+  __device__ __forceinline__ void store(float *p, float f) const {
+    if constexpr (D == 128)
+      *reinterpret_cast<float4 *>(p) = make_float4(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
+    else
+      *reinterpret_cast<float2 *>(p) = make_float2(x[0] * f, x[1] * f);
   }
+  __device__ __forceinline__ void add(float w, const Part &o) {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) x[i] = fmaf(w, o.x[i], x[i]);
+  }
+};
+
+// A joined row (its reference, sum and dims) to the outputs.
+template <int D>
+__device__ __forceinline__ void store_row(const Args &a, int64_t row, float ref, float l, const Part<D> &o) {
+  const int lane = threadIdx.x & 31;
+  o.store(a.out + row * D + lane * (D / 32), l == 0.f ? 0.f : 1.f / l);
+  if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+}
+__device__ __forceinline__ float weight_of(float2 ml, float ref) {
+  return ml.x == -INFINITY ? 0.f * ml.y : ex2_approx(ml.x - ref);  // (a NaN stays one)
 }
 
 // A (sequence, kv head) of which a warp holds a piece.
@@ -214,6 +198,12 @@ struct Piece {
   long long seg;  // its first unit
   int64_t row0;   // its first query row
   int nb;         // its units; 0: no piece
+};
+
+// A (sequence, kv head) cut between n CTAs from CTA ca on, which this one joins;
+// one of its pieces here (-1: nothing to join).
+struct Join {
+  int piece, ca, n;
 };
 
 // How the units are dealt out: CTA c of `ctas` has [first(c), first(c + 1)),
@@ -237,19 +227,11 @@ struct Deal {
     const long long c0 = first(c);
     return c0 + static_cast<unsigned>(static_cast<int>(first(c + 1) - c0) * w) / static_cast<unsigned>(warps);
   }
-  // the CTA and the warp that have unit u: from CTA c on downwards, upwards
-  __device__ __forceinline__ int down(int c, long long u) const {
-    while (first(c) > u) --c;
-    return c;
-  }
-  __device__ __forceinline__ int up(int c, long long u) const {
-    while (first(c + 1) <= u) ++c;
-    return c;
-  }
-  __device__ __forceinline__ int warp_of(int c, long long u) const {
-    const long long c0 = first(c);
-    const unsigned n = static_cast<unsigned>(first(c + 1) - c0), at = static_cast<unsigned>(u - c0);
-    return static_cast<int>(((at + 1) * warps - 1) / n);
+  // the CTA that has unit u
+  __device__ __forceinline__ int cta_of(long long u) const {
+    const long long total = each * ctas + rest, x = (u + 1) * ctas - 1;
+    if (total * ctas < 0xffffffffLL) return static_cast<int>(static_cast<unsigned>(x) / static_cast<unsigned>(total));
+    return static_cast<int>(x / total);
   }
 };
 
@@ -264,7 +246,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
   __shared__ long long warp_sum[kWarps];
   __shared__ Piece pieces[2 * kWarps];  // of each warp: one that began before its range, one that goes on behind it
   __shared__ long long starts[kWarps + 1];  // of the warps' ranges
-  __shared__ int joins[2];
+  __shared__ Join joins[2];
+  float2 *const part_ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
+  float *const part_o = reinterpret_cast<float *>(smem + C::OFF_O);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gq = lane >> 2, t = lane & 3;
 
@@ -326,7 +310,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
       if (i + step < kWarps * 32 && pre[i + step] <= u0) i += step;
     s0 = i * cs;
     at0 = pre[i];
-    for (;; s0 += 32) {
+    for (; cs > 1; s0 += 32) {  // (cs 1: a sequence a thread, it is the one)
       const int s = s0 + lane;
       long long incl = s < a.num_seqs ? static_cast<long long>(span_of(a, __ldg(a.lens + s)).nb) * a.hkv : 0;
 #pragma unroll
@@ -525,7 +509,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
         shift[r][c] = kexp;
         high[r][c] = -INFINITY;
       }
-    float acc[NR][NG][4][4], sum[NR][NG][4][4];  // [queries 0..7, 8..15][group][16 dims]
+    float sum[NR][NG][4][4];  // [queries 0..7, 8..15][group][16 dims]
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -533,23 +517,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[r][p][j][i] = sum[r][p][j][i] = 0.f;
-    // the tensor cores' sums to the fp32 sums
-    auto flush = [&]() {
-#pragma unroll
-      for (int r = 0; r < NR; ++r)
-#pragma unroll
-        for (int p = 0; p < NG; ++p)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              sum[r][p][j][i] += acc[r][p][j][i];
-              acc[r][p][j][i] = 0.f;
-            }
-    };
-
-    int since = 0;
+          for (int i = 0; i < 4; ++i) sum[r][p][j][i] = 0.f;
 #pragma unroll 1
     while (cb < b_end) {
       cp_async_wait<NST - 2>();
@@ -557,138 +525,149 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
       fetch();
       const int n = b_end - cb < 2 ? 1 : 2;
       const uint8_t *const st = ring + cslot * C::STAGE;
-#pragma unroll 1
-      for (int tt = 0; tt < n; ++tt) {
-        const uint8_t *const kt = st + 2 * tt * TB, *const vt = kt + TB;
-        const int pos0 = (csp.b0 + cb + tt) * 16;
+      // Both blocks of the stage in step (where there is one only, the other's
+      // tokens are masked).
+      const int pos0 = (csp.b0 + cb) * 16;
 
-        // scores: x[r][i][c] of token krow + 8 i and query 2 t + c (+ 8 r)
-        float x[NR][2][2];
-        {
-          float s[NR][NG][4];
+      // scores: x[r][tt][i][c] of token krow + 8 i and query 2 t + c (+ 8 r)
+      float x[NR][2][2][2];
 #pragma unroll
-          for (int p = 0; p < NG; ++p) {
-            const uint2 k0 = lds64(kt + (kat ^ (32 * p))), k8 = lds64(kt + (kat ^ (32 * p)) + ROW8);
+      for (int tt = 0; tt < 2; ++tt) {
+        const uint8_t *const kt = st + 2 * tt * TB;
+        float s[NR][NG][4];
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              const uint32_t u = (h < 2 ? k0.x : k0.y) >> (h & 1 ? 8 : 0), v = (h < 2 ? k8.x : k8.y) >> (h & 1 ? 8 : 0);
-              const uint32_t a0 = u & 0x000F000Fu, a1 = v & 0x000F000Fu, a2 = u & 0x00F000F0u, a3 = v & 0x00F000F0u;
+        for (int p = 0; p < NG; ++p) {
+          const uint2 k0 = lds64(kt + (kat ^ (32 * p))), k8 = lds64(kt + (kat ^ (32 * p)) + ROW8);
 #pragma unroll
-              for (int r = 0; r < NR; ++r) {
-                if (h == 0)
-                  mma0(s[r][p], a0, a1, a2, a3, qf[r][p * 4 + h][0], qf[r][p * 4 + h][1]);
-                else
-                  mma(s[r][p], a0, a1, a2, a3, qf[r][p * 4 + h][0], qf[r][p * 4 + h][1]);
-              }
+          for (int h = 0; h < 4; ++h) {
+            const uint32_t u = (h < 2 ? k0.x : k0.y) >> (h & 1 ? 8 : 0), v = (h < 2 ? k8.x : k8.y) >> (h & 1 ? 8 : 0);
+            const uint32_t a0 = u & 0x000F000Fu, a1 = v & 0x000F000Fu, a2 = u & 0x00F000F0u, a3 = v & 0x00F000F0u;
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+              if (h == 0)
+                mma0(s[r][p], a0, a1, a2, a3, qf[r][p * 4 + h][0], qf[r][p * 4 + h][1]);
+              else
+                mma(s[r][p], a0, a1, a2, a3, qf[r][p * 4 + h][0], qf[r][p * 4 + h][1]);
             }
           }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t w[2];
-            load_pairs<NG>(kt + i4::code_bytes(D) + (krow + 8 * i) * (4 * NG), w);
-            const float2 g0 = halves(w[0]), g1 = halves(w[NG - 1]);  // scale, minimum
-#pragma unroll
-            for (int r = 0; r < NR; ++r)
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                float y = s[r][0][2 * i + c] * g0.x, z = g0.y * cm[r][0][c];
-                if constexpr (NG == 2) {
-                  y = fmaf(s[r][NG - 1][2 * i + c], g1.x, y);
-                  z = fmaf(g1.y, cm[r][NG - 1][c], z);
-                }
-                x[r][i][c] = fmaf(y, cs_[r][c], z);
-              }
-          }
         }
-
-        // the values' scales and minima; masked tokens have neither.  Every
-        // second token's weight is negated and its code taken from 15, s n + m
-        // = (m + 15 s) - s (15 - n): codes are never negative, and without this
-        // the two sums, of codes and of minima, would grow far past their
-        // difference.
-        float vs[2][NG], vm[2][NG];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           uint32_t w[2];
-          load_pairs<NG>(vt + i4::code_bytes(D) + (krow + 8 * i) * (4 * NG), w);
-#pragma unroll
-          for (int p = 0; p < NG; ++p) {
-            const float2 g = halves(w[p]);
-            vs[i][p] = g.x;
-            vm[i][p] = fmaf(flip15, g.x, g.y);
-          }
-        }
-        if (pos0 < csp.first || pos0 + 16 > csp.len) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int pos = pos0 + krow + 8 * i;
-            if (pos < csp.first || pos >= csp.len) {
-#pragma unroll
-              for (int r = 0; r < NR; ++r) x[r][i][0] = x[r][i][1] = -INFINITY;
-#pragma unroll
-              for (int p = 0; p < NG; ++p) vs[i][p] = vm[i][p] = 0.f;
-            }
-          }
-        }
-
-        // the running maximum is raised only when a score passes it by 2^8,
-        // and kexp lowered only when a scale needs it: a vote, no shuffles
-        float smax = fmaxf(vs[0][0], vs[1][0]);
-        if constexpr (NG == 2) smax = fmax3(smax, vs[0][NG - 1], vs[1][NG - 1]);
-        bool raise = smax * kap > 128.f;
-#pragma unroll
-        for (int r = 0; r < NR; ++r)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) raise |= fmaxf(x[r][0][c], x[r][1][c]) > high[r][c];
-        if (__any_sync(0xffffffffu, raise)) {
-          smax = warp_max_xor(smax, 1, 32);
-          float nk = kexp;
-          if (smax * kap > 128.f) {
-            int e = static_cast<int>(__float_as_uint(smax) >> 23) - 127;  // smax in [2^e, 2^(e + 1))
-            e = e > 16 ? 16 : e;
-            nk = static_cast<float>(4 - e);
-            kap = __uint_as_float(static_cast<uint32_t>(127 + 4 - e) << 23);
-          }
-          flush();
-          since = 0;
+          load_pairs<NG>(kt + i4::code_bytes(D) + (krow + 8 * i) * (4 * NG), w);
+          const float2 g0 = halves(w[0]), g1 = halves(w[NG - 1]);  // scale, minimum
 #pragma unroll
           for (int r = 0; r < NR; ++r)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const float m = fmaxf(M[r][c], warp_max_xor(fmaxf(x[r][0][c], x[r][1][c]), 4, 32));
-              const float alpha = M[r][c] == -INFINITY ? 0.f : ex2_approx((M[r][c] - m) + (nk - kexp));
-              M[r][c] = m;
-              shift[r][c] = nk - (m == -INFINITY ? 0.f : m);
-              high[r][c] = m + 8.f;
-              l[r][c] *= alpha;
+              float y = s[r][0][2 * i + c] * g0.x, z = g0.y * cm[r][0][c];
+              if constexpr (NG == 2) {
+                y = fmaf(s[r][NG - 1][2 * i + c], g1.x, y);
+                z = fmaf(g1.y, cm[r][NG - 1][c], z);
+              }
+              x[r][tt][i][c] = fmaf(y, cs_[r][c], z);
+            }
+        }
+      }
+
+      // the values' scales and minima; masked tokens have neither.  Every
+      // second token's weight is negated and its code taken from 15, s n + m =
+      // (m + 15 s) - s (15 - n): codes are never negative, and without this the
+      // two sums, of codes and of minima, would grow far past their difference.
+      float vs[2][2][NG], vm[2][2][NG];
 #pragma unroll
-              for (int p = 0; p < NG; ++p) {
-                mz[r][p][c] *= alpha;
+      for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  sum[r][p][j][c] *= alpha;
-                  sum[r][p][j][2 + c] *= alpha;
-                }
+        for (int i = 0; i < 2; ++i) {
+          uint32_t w[2];
+          load_pairs<NG>(st + (2 * tt + 1) * TB + i4::code_bytes(D) + (krow + 8 * i) * (4 * NG), w);
+#pragma unroll
+          for (int p = 0; p < NG; ++p) {
+            const float2 g = halves(w[p]);
+            vs[tt][i][p] = g.x;
+            vm[tt][i][p] = fmaf(flip15, g.x, g.y);
+          }
+        }
+      if (n < 2 || pos0 < csp.first || pos0 + 32 > csp.len) {
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int pos = pos0 + 16 * tt + krow + 8 * i;
+            if (tt >= n || pos < csp.first || pos >= csp.len) {
+#pragma unroll
+              for (int r = 0; r < NR; ++r) x[r][tt][i][0] = x[r][tt][i][1] = -INFINITY;
+#pragma unroll
+              for (int p = 0; p < NG; ++p) vs[tt][i][p] = vm[tt][i][p] = 0.f;
+            }
+          }
+      }
+
+      // the running maximum is raised only when a score passes it by 2^8, and
+      // kexp lowered only when a scale needs it: a vote, no shuffles
+      float smax = fmaxf(fmax3(vs[0][0][0], vs[0][1][0], vs[1][0][0]), vs[1][1][0]);
+      if constexpr (NG == 2)
+        smax = fmax3(fmax3(smax, vs[0][0][NG - 1], vs[0][1][NG - 1]), vs[1][0][NG - 1], vs[1][1][NG - 1]);
+      bool raise = smax * kap > 128.f;
+      float xmax[NR][2];
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          xmax[r][c] = fmaxf(fmax3(x[r][0][0][c], x[r][0][1][c], x[r][1][0][c]), x[r][1][1][c]);
+          raise |= xmax[r][c] > high[r][c];
+        }
+      if (__any_sync(0xffffffffu, raise)) {
+        smax = warp_max_xor(smax, 1, 32);
+        float nk = kexp;
+        if (smax * kap > 128.f) {
+          int e = static_cast<int>(__float_as_uint(smax) >> 23) - 127;  // smax in [2^e, 2^(e + 1))
+          e = e > 16 ? 16 : e;
+          nk = static_cast<float>(4 - e);
+          kap = __uint_as_float(static_cast<uint32_t>(127 + 4 - e) << 23);
+        }
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float m = fmaxf(M[r][c], warp_max_xor(xmax[r][c], 4, 32));
+            const float alpha = M[r][c] == -INFINITY ? 0.f : ex2_approx((M[r][c] - m) + (nk - kexp));
+            M[r][c] = m;
+            shift[r][c] = nk - (m == -INFINITY ? 0.f : m);
+            high[r][c] = m + 8.f;
+            l[r][c] *= alpha;
+#pragma unroll
+            for (int p = 0; p < NG; ++p) {
+              mz[r][p][c] *= alpha;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                sum[r][p][j][c] *= alpha;
+                sum[r][p][j][2 + c] *= alpha;
               }
             }
-          kexp = nk;
-        }
+          }
+        kexp = nk;
+      }
 
+      float acc[NR][NG][4][4];  // the stage's products
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt) {
+        const uint8_t *const vt = st + (2 * tt + 1) * TB;
         // weights times scales as hi + lo, turned into operands (token pairs of
         // a query) by 8 x 8 transposes
         uint32_t hi[NR][NG][2], lo[NR][NG][2];
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
+        for (int r = 0; r < NR; ++r)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float w0 = ex2_approx(x[r][i][0] + shift[r][0]), w1 = ex2_approx(x[r][i][1] + shift[r][1]);
+            const float w0 = ex2_approx(x[r][tt][i][0] + shift[r][0]), w1 = ex2_approx(x[r][tt][i][1] + shift[r][1]);
             l[r][0] += w0;
             l[r][1] += w1;
 #pragma unroll
             for (int p = 0; p < NG; ++p) {
-              mz[r][p][0] = fmaf(w0, vm[i][p], mz[r][p][0]);
-              mz[r][p][1] = fmaf(w1, vm[i][p], mz[r][p][1]);
-              const float sv = vs[i][p] * flip;
+              mz[r][p][0] = fmaf(w0, vm[tt][i][p], mz[r][p][0]);
+              mz[r][p][1] = fmaf(w1, vm[tt][i][p], mz[r][p][1]);
+              const float sv = vs[tt][i][p] * flip;
               const float y0 = w0 * sv, y1 = w1 * sv;
               const uint32_t h = pack_f16x2(y0, y1);
               const float2 hf = halves(h);
@@ -700,7 +679,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
               }
             }
           }
-        }
 #pragma unroll
         for (int p = 0; p < NG; ++p) {
           const uint32_t w0 = lds32(vt + (vat0 ^ (32 * p))), w1 = lds32(vt + (vat1 ^ (32 * p)));
@@ -715,7 +693,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
               const uint32_t v2 = and_xor(b1, 0x000F000Fu, 0x000F0000u), v3 = and_xor(b1, 0x00F000F0u, 0x00F00000u);
 #pragma unroll
               for (int r = 0; r < NR; ++r) {
-                mma(acc[r][p][2 * h + j], v0, v1, v2, v3, hi[r][p][0], hi[r][p][1]);
+                if (tt == 0)
+                  mma0(acc[r][p][2 * h + j], v0, v1, v2, v3, hi[r][p][0], hi[r][p][1]);
+                else
+                  mma(acc[r][p][2 * h + j], v0, v1, v2, v3, hi[r][p][0], hi[r][p][1]);
                 if constexpr (NQ != 4) mma(acc[r][p][2 * h + j], v0, v1, v2, v3, lo[r][p][0], lo[r][p][1]);
               }
               b0 >>= 8;
@@ -724,19 +705,22 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
           }
         }
       }
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int p = 0; p < NG; ++p)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[r][p][j][i] += acc[r][p][j][i];
       cslot = cslot + 1 == NST ? 0 : cslot + 1;
       cb += n;
-      if (++since == kFlush) {
-        flush();
-        since = 0;
-      }
     }
 
     // --- the end of the piece: to the outputs, or to a slot for the join
-    flush();
     const bool whole = seg >= u0 && seg + csp.nb <= u1;
-    const int slot = 2 * (cta * kWarps + warp) + (seg >= u0 ? 1 : 0);
-    float *dst = whole ? a.out + row0 * D : a.slot_o + static_cast<int64_t>(slot) * a.g * D;
+    const int slot = 2 * warp + (seg >= u0 ? 1 : 0);
+    float *dst = whole ? a.out + row0 * D : part_o + slot * a.g * D;
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -756,7 +740,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
         const float inv = !whole ? 1.f : lsum == 0.f ? 0.f : 1.f / lsum;
         if (gq == 0 && has) {
           if (!whole)
-            a.slot_ml[static_cast<int64_t>(slot) * a.g + query] = make_float2(ref, lsum);
+            part_ml[slot * a.g + query] = make_float2(ref, lsum);
           else if (a.lse)
             a.lse[row0 + query] = lsum == 0.f ? -INFINITY : (ref + log2f(lsum)) * kLn2;
         }
@@ -781,7 +765,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
           }
         }
       }
-    if (!whole && lane == 0) pieces[2 * warp + (seg >= u0 ? 1 : 0)] = Piece{seg, row0, csp.nb};
+    if (!whole && lane == 0) pieces[slot] = Piece{seg, row0, csp.nb};
 
     if (cb == csp.nb && cu < u1) {
       cb = 0;
@@ -800,60 +784,108 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
   // --- pieces of this CTA's warps joined, a query row a warp
   __syncthreads();
   const long long c0 = starts[0], c1 = starts[kWarps];
-  const int slot0 = 2 * cta * kWarps;
   for (int k = 0; k < 2 * kWarps; ++k) {
     const Piece pc = pieces[k];
     const int w = k >> 1;
     // the first piece here of its (sequence, kv head)
     if (pc.nb == 0 || starts[w] > (pc.seg > c0 ? pc.seg : c0)) continue;
     const long long end = pc.seg + pc.nb;
-    // its further pieces: the first of the warps that follow (a warp without
-    // units, of a CTA with fewer units than warps, has none)
-    unsigned held = 0;
-    for (int x = w + 1; x < kWarps && starts[x] < end; ++x) held |= (pieces[2 * x].nb > 0 ? 1u : 0u) << x;
-    const int n = 1 + __popc(held);
-    if (n == 1) continue;  // a CTA's only piece goes on elsewhere: it lies in its slot
     const bool here = pc.seg >= c0 && end <= c1;
-    auto slot_of = [&](int i) {
-      unsigned m = held;
-      for (int j = 1; j < i; ++j) m &= m - 1;
-      return slot0 + (i == 0 ? k : 2 * (__ffs(m) - 1));
-    };
-    for (int r = (warp + kWarps - w) % kWarps; r < a.g; r += kWarps)
-      join_row<D>(a, n, slot_of, r, here ? a.out + (pc.row0 + r) * D : nullptr,
-                  here && a.lse ? a.lse + pc.row0 + r : nullptr, slot0 + k);
+    for (int r = (warp + kWarps - w) % kWarps; r < a.g; r += kWarps) {
+      // its further pieces: the first of the warps that follow (a warp without
+      // units, of a CTA with fewer units than warps, has none)
+      float ref = part_ml[k * a.g + r].x;
+      for (int x = w + 1; x < kWarps && starts[x] < end; ++x)
+        if (pieces[2 * x].nb > 0) ref = fmaxf(ref, part_ml[2 * x * a.g + r].x);
+      float l = 0.f;
+      Part<D> o;
+      o.clear();
+      for (int x = w; x < kWarps && (x == w || starts[x] < end); ++x) {
+        const int slot = x == w ? k : 2 * x;
+        if (pieces[slot].nb == 0) continue;
+        const float2 ml = part_ml[slot * a.g + r];
+        const float f = weight_of(ml, ref);
+        Part<D> v;
+        v.load(part_o + (slot * a.g + r) * D + lane * (D / 32));
+        l = fmaf(f, ml.y, l);
+        o.add(f, v);
+      }
+      if (here) {
+        store_row<D>(a, pc.row0 + r, ref, l, o);
+      } else {
+        const int64_t at = (2 * static_cast<int64_t>(cta) + (pc.seg >= c0 ? 1 : 0)) * a.g + r;
+        o.store(a.slot_o + at * D + lane * (D / 32), 1.f);
+        if (lane == 0) a.slot_ml[at] = make_float2(ref, l);
+      }
+    }
   }
 
-  // --- and what goes beyond this CTA, by the CTA that finishes its last piece
+  // --- and what goes beyond this CTA, by the CTA that finishes its last piece.
+  // Lane 0 of warp 0: what began before this CTA; lane 1: what begins here and
+  // goes on.
+  int mine = -1, ca = 0, n = 0;
+  if (warp == 0) {
+    const Piece pc = pieces[lane < 2 * kWarps ? lane : 0];
+    const bool held = lane < 2 * kWarps && pc.nb > 0;
+    const unsigned before = __ballot_sync(0xffffffffu, held && pc.seg < c0);
+    const unsigned behind = __ballot_sync(0xffffffffu, held && pc.seg >= c0 && pc.seg + pc.nb > c1);
+    mine = lane < 2 ? __ffs(lane == 0 ? before : behind) - 1 : -1;
+    if (mine >= 0) {
+      ca = deal.cta_of(pieces[mine].seg);
+      n = deal.cta_of(pieces[mine].seg + pieces[mine].nb - 1) - ca + 1;
+    }
+  }
   __threadfence();
   __syncthreads();
   if (tid < 2) {
-    joins[tid] = -1;
-    // tid 0: what began before this CTA; tid 1: what begins here and goes on
-    for (int k = 0; k < 2 * kWarps; ++k) {
-      const Piece pc = pieces[k];
-      if (pc.nb == 0 || (tid == 0 ? pc.seg >= c0 : pc.seg < c0 || pc.seg + pc.nb <= c1)) continue;
-      const int ca = deal.down(cta, pc.seg), cz = deal.up(cta, pc.seg + pc.nb - 1);
-      if (atom_add_acq_rel_gpu(a.count + ca, 1) == cz - ca) {
-        st_relaxed_gpu(a.count + ca, 0);
-        joins[tid] = k;
-      }
-      break;
+    if (mine >= 0 && atom_add_acq_rel_gpu(a.count + ca, 1) == n - 1) {
+      st_relaxed_gpu(a.count + ca, 0);
+      __threadfence();
+    } else {
+      mine = -1;
     }
-    __threadfence();
+    joins[tid] = Join{mine, ca, n};
   }
   __syncthreads();
   for (int j = 0; j < 2; ++j) {
-    if (joins[j] < 0) continue;
-    const Piece pc = pieces[joins[j]];
-    const int ca = deal.down(cta, pc.seg), cz = deal.up(cta, pc.seg + pc.nb - 1);
-    auto slot_of = [&](int i) {
-      const int c = ca + i;
-      return i == 0 ? 2 * (c * kWarps + deal.warp_of(c, pc.seg)) + 1
-                    : 2 * (c * kWarps + deal.warp_of(c, deal.first(c)));
-    };
-    for (int r = warp; r < a.g; r += kWarps)
-      join_row<D>(a, cz - ca + 1, slot_of, r, a.out + (pc.row0 + r) * D, a.lse ? a.lse + pc.row0 + r : nullptr, 0);
+    const Join jn = joins[j];
+    if (jn.piece < 0) continue;
+    // slots, in the order of the units: the second of CTA ca, the first of those behind
+    auto slot_of = [&](int i) { return 2 * static_cast<int64_t>(jn.ca + i) + (i == 0 ? 1 : 0); };
+    for (int r = warp; r < a.g; r += kWarps) {
+      float ref = -INFINITY, l = 0.f;
+      Part<D> o;
+      o.clear();
+      for (int base = 0; base < jn.n; base += 32) {
+        // a lane's piece's reference and sum; the dims come eight pieces at a time
+        const int m = min(32, jn.n - base);
+        const float2 ml = lane < m ? __ldcg(&a.slot_ml[slot_of(base + lane) * a.g + r]) : make_float2(-INFINITY, 0.f);
+        const float up = fmaxf(ref, warp_max_xor(ml.x, 1, 32));
+        const float f = weight_of(ml, up), keep = ref == -INFINITY ? 0.f : ex2_approx(ref - up);
+        ref = up;
+        l *= keep;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) o.x[i] *= keep;
+        for (int i0 = 0; i0 < m; i0 += 8) {
+          Part<D> v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (i0 + i < m)
+              v[i].load_l2(a.slot_o + (slot_of(base + i0 + i) * a.g + r) * D + lane * (D / 32));
+            else
+              v[i].clear();
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int at = (i0 + i) & 31;  // (lanes from m on have weight and sum 0)
+            const float w = __shfl_sync(0xffffffffu, f, at);
+            l = fmaf(w, __shfl_sync(0xffffffffu, ml.y, at), l);
+            o.add(w, v[i]);
+          }
+        }
+      }
+      store_row<D>(a, pieces[jn.piece].row0 + r, ref, l, o);
+    }
   }
 }
 
@@ -881,13 +913,13 @@ struct Layout {
   size_t count, ml, o, total;
 };
 
-Layout layout(int ctas, int warps, int g, int d) {
-  const size_t workers = static_cast<size_t>(ctas) * warps;
+Layout layout(int ctas, int g, int d) {
+  const size_t slots = 2 * static_cast<size_t>(ctas);
   Layout w;
   w.count = 256;
   w.ml = (w.count + ctas * sizeof(int32_t) + 255) / 256 * 256;
-  w.o = (w.ml + 2 * workers * g * sizeof(float2) + 255) / 256 * 256;
-  w.total = w.o + 2 * workers * g * d * sizeof(float);
+  w.o = (w.ml + slots * g * sizeof(float2) + 255) / 256 * 256;
+  w.total = w.o + slots * g * d * sizeof(float);
   return w;
 }
 
@@ -908,7 +940,7 @@ pa_status plan_int4_decode(const pa_kv_desc &d, DecodePlan *plan, const char **w
   plan->slot_heads = d.num_q_heads / d.num_kv_heads;
   plan->num_groups = d.num_kv_heads;
   plan->num_ctas = device_sm_count();
-  const Layout w = layout(plan->num_ctas, k.warps, plan->slot_heads, d.head_dim);
+  const Layout w = layout(plan->num_ctas, plan->slot_heads, d.head_dim);
   plan->workspace_bytes = w.total;
   plan->zero_bytes = w.ml;
   return PA_OK;
@@ -919,7 +951,7 @@ cudaError_t launch_int4_decode(const pa_kv_desc &d, const DecodePlan &plan, floa
                                int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs, float scale,
                                void *workspace, cudaStream_t stream) {
   const Kernel k = kernel_of(d);
-  const Layout w = layout(plan.num_ctas, k.warps, plan.slot_heads, d.head_dim);
+  const Layout w = layout(plan.num_ctas, plan.slot_heads, d.head_dim);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   Args a;
   a.out = out;
