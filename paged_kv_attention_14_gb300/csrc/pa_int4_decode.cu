@@ -280,24 +280,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
     __syncthreads();
   }
 
-  // --- sequences without tokens
-  for (int s = blockIdx.x * kWarps + warp; s < a.num_seqs; s += gridDim.x * kWarps) {
-    if (span_of(a, __ldg(a.lens + s)).nb > 0) continue;
-    for (int i = lane; i < a.hq * D; i += 32) a.out[static_cast<int64_t>(s) * a.hq * D + i] = 0.f;
-    if (a.lse)
-      for (int i = lane; i < a.hq; i += 32) a.lse[static_cast<int64_t>(s) * a.hq + i] = -INFINITY;
-  }
-
   // --- this warp's range of units [u0, u1)
-  if (total == 0) return;
   const long long want = (total + kMinUnits - 1) / kMinUnits;
-  const Deal deal(total, static_cast<int>(want < gridDim.x ? want : gridDim.x), kWarps);
+  const Deal deal(total, static_cast<int>(want < 1 ? 1 : want < gridDim.x ? want : gridDim.x), kWarps);
   const int cta = blockIdx.x;
-  if (cta >= deal.ctas) return;
-  const long long u0 = deal.first(cta, warp), u1 = deal.first(cta, warp + 1);
+  const bool idle = cta >= deal.ctas || total == 0;
+  const long long u0 = idle ? 0 : deal.first(cta, warp), u1 = idle ? 0 : deal.first(cta, warp + 1);
   if (lane < 2) pieces[2 * warp + lane].nb = 0;
   if (lane == 0) starts[warp] = u0;
-  if (tid == 0) starts[kWarps] = deal.first(cta + 1);
+  if (tid == 0) starts[kWarps] = idle ? 0 : deal.first(cta + 1);
 
   if (u0 < u1) {  // (not indented: the whole of the warp's work)
   // --- the sequence of its first unit
@@ -781,39 +772,68 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
   cp_async_wait<0>();
   }  // u0 < u1
 
+  // --- sequences without tokens
+#pragma unroll 1
+  for (int s = blockIdx.x * kWarps + warp; s < a.num_seqs; s += gridDim.x * kWarps) {
+    if (span_of(a, __ldg(a.lens + s)).nb > 0) continue;
+    for (int i = lane; i < a.hq * D; i += 32) a.out[static_cast<int64_t>(s) * a.hq * D + i] = 0.f;
+    if (a.lse)
+      for (int i = lane; i < a.hq; i += 32) a.lse[static_cast<int64_t>(s) * a.hq + i] = -INFINITY;
+  }
+  if (idle) return;
+
   // --- pieces of this CTA's warps joined, a query row a warp
   __syncthreads();
   const long long c0 = starts[0], c1 = starts[kWarps];
-  for (int k = 0; k < 2 * kWarps; ++k) {
-    const Piece pc = pieces[k];
-    const int w = k >> 1;
-    // the first piece here of its (sequence, kv head)
-    if (pc.nb == 0 || starts[w] > (pc.seg > c0 ? pc.seg : c0)) continue;
-    const long long end = pc.seg + pc.nb;
-    const bool here = pc.seg >= c0 && end <= c1;
-    for (int r = (warp + kWarps - w) % kWarps; r < a.g; r += kWarps) {
-      // its further pieces: the first of the warps that follow (a warp without
-      // units, of a CTA with fewer units than warps, has none)
-      float ref = part_ml[k * a.g + r].x;
-      for (int x = w + 1; x < kWarps && starts[x] < end; ++x)
-        if (pieces[2 * x].nb > 0) ref = fmaxf(ref, part_ml[2 * x * a.g + r].x);
-      float l = 0.f;
+  static_assert(2 * kWarps <= 32, "a lane a piece");
+  // lane k: piece k; whether it is the first here of its (sequence, kv head),
+  // and the warps (bits) that have its further pieces
+  Piece pc = pieces[lane < 2 * kWarps ? lane : 0];
+  if (lane >= 2 * kWarps) pc.nb = 0;
+  const long long end = pc.seg + pc.nb;
+  const bool lead = pc.nb > 0 && starts[lane >> 1] <= (pc.seg > c0 ? pc.seg : c0);
+  const bool here = pc.seg >= c0 && end <= c1;
+  const unsigned has0 = __ballot_sync(0xffffffffu, pc.nb > 0);  // bit 2 w: warp w has a piece that began before it
+  unsigned more = 0;
+#pragma unroll 1  // (code that runs once is paid for by its length: it comes from memory)
+  for (int x = 1; x < kWarps; ++x)
+    more |= (x > lane >> 1 && starts[x] < end && (has0 >> (2 * x) & 1u)) ? 1u << x : 0u;
+  unsigned todo = __ballot_sync(0xffffffffu, lead);
+  for (int item = 0; todo; todo &= todo - 1) {
+    const int k = __ffs(todo) - 1, w = k >> 1;
+    const unsigned in = __shfl_sync(0xffffffffu, more, k) | 1u << w;
+    const bool out = __shfl_sync(0xffffffffu, here, k);
+    const bool second = __shfl_sync(0xffffffffu, pc.seg >= c0, k);
+    const int64_t row0 = __shfl_sync(0xffffffffu, pc.row0, k);
+#pragma unroll 1
+    for (int r = 0; r < a.g; ++r, ++item) {
+      if (item % kWarps != warp) continue;
+      // lane x: warp x's piece
+      const bool mine = lane < kWarps && (in >> lane & 1u);
+      const int slot = lane == w ? k : 2 * lane;
+      const float2 ml = mine ? part_ml[slot * a.g + r] : make_float2(-INFINITY, 0.f);
+      float ref = ml.x;
+#pragma unroll 1
+      for (int o = 1; o < kWarps; o <<= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
+      ref = __shfl_sync(0xffffffffu, ref, 0);
+      const float f = weight_of(ml, ref);
+      float l = f * ml.y;
+#pragma unroll 1
+      for (int o = 1; o < kWarps; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
       Part<D> o;
       o.clear();
-      for (int x = w; x < kWarps && (x == w || starts[x] < end); ++x) {
-        const int slot = x == w ? k : 2 * x;
-        if (pieces[slot].nb == 0) continue;
-        const float2 ml = part_ml[slot * a.g + r];
-        const float f = weight_of(ml, ref);
+#pragma unroll 1
+      for (unsigned left = in; left; left &= left - 1) {
+        const int x = __ffs(left) - 1;
         Part<D> v;
-        v.load(part_o + (slot * a.g + r) * D + lane * (D / 32));
-        l = fmaf(f, ml.y, l);
-        o.add(f, v);
+        v.load(part_o + ((x == w ? k : 2 * x) * a.g + r) * D + lane * (D / 32));
+        o.add(__shfl_sync(0xffffffffu, f, x), v);
       }
-      if (here) {
-        store_row<D>(a, pc.row0 + r, ref, l, o);
+      l = __shfl_sync(0xffffffffu, l, 0);
+      if (out) {
+        store_row<D>(a, row0 + r, ref, l, o);
       } else {
-        const int64_t at = (2 * static_cast<int64_t>(cta) + (pc.seg >= c0 ? 1 : 0)) * a.g + r;
+        const int64_t at = (2 * static_cast<int64_t>(cta) + (second ? 1 : 0)) * a.g + r;
         o.store(a.slot_o + at * D + lane * (D / 32), 1.f);
         if (lane == 0) a.slot_ml[at] = make_float2(ref, l);
       }
@@ -825,10 +845,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
   // goes on.
   int mine = -1, ca = 0, n = 0;
   if (warp == 0) {
-    const Piece pc = pieces[lane < 2 * kWarps ? lane : 0];
-    const bool held = lane < 2 * kWarps && pc.nb > 0;
-    const unsigned before = __ballot_sync(0xffffffffu, held && pc.seg < c0);
-    const unsigned behind = __ballot_sync(0xffffffffu, held && pc.seg >= c0 && pc.seg + pc.nb > c1);
+    const unsigned before = __ballot_sync(0xffffffffu, pc.nb > 0 && pc.seg < c0);
+    const unsigned behind = __ballot_sync(0xffffffffu, pc.nb > 0 && pc.seg >= c0 && end > c1);
     mine = lane < 2 ? __ffs(lane == 0 ? before : behind) - 1 : -1;
     if (mine >= 0) {
       ca = deal.cta_of(pieces[mine].seg);
@@ -847,17 +865,19 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
     joins[tid] = Join{mine, ca, n};
   }
   __syncthreads();
+#pragma unroll 1
   for (int j = 0; j < 2; ++j) {
     const Join jn = joins[j];
     if (jn.piece < 0) continue;
     // slots, in the order of the units: the second of CTA ca, the first of those behind
     auto slot_of = [&](int i) { return 2 * static_cast<int64_t>(jn.ca + i) + (i == 0 ? 1 : 0); };
+#pragma unroll 1
     for (int r = warp; r < a.g; r += kWarps) {
       float ref = -INFINITY, l = 0.f;
       Part<D> o;
       o.clear();
       for (int base = 0; base < jn.n; base += 32) {
-        // a lane's piece's reference and sum; the dims come eight pieces at a time
+        // a lane's piece's reference and sum; the dims come four pieces at a time
         const int m = min(32, jn.n - base);
         const float2 ml = lane < m ? __ldcg(&a.slot_ml[slot_of(base + lane) * a.g + r]) : make_float2(-INFINITY, 0.f);
         const float up = fmaxf(ref, warp_max_xor(ml.x, 1, 32));
@@ -866,17 +886,18 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
         l *= keep;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) o.x[i] *= keep;
-        for (int i0 = 0; i0 < m; i0 += 8) {
-          Part<D> v[8];
+#pragma unroll 1
+        for (int i0 = 0; i0 < m; i0 += 4) {
+          Part<D> v[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 4; ++i) {
             if (i0 + i < m)
               v[i].load_l2(a.slot_o + (slot_of(base + i0 + i) * a.g + r) * D + lane * (D / 32));
             else
               v[i].clear();
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 4; ++i) {
             const int at = (i0 + i) & 31;  // (lanes from m on have weight and sum 0)
             const float w = __shfl_sync(0xffffffffu, f, at);
             l = fmaf(w, __shfl_sync(0xffffffffu, ml.y, at), l);
