@@ -250,6 +250,7 @@ def _stream(stream) -> Optional[int]:
 
 
 _CACHE = (torch.bfloat16, torch.float16, torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)
+_INT4 = (PA_KV_INT4, PA_KV_INT4_F16)
 _BF16 = (torch.bfloat16,)
 _F16 = (torch.float16,)
 
@@ -265,8 +266,19 @@ _U8 = (torch.uint8,)
 
 
 def pa_cache_write(desc: PaKvDesc, k, v, k_cache, v_cache, slot_mapping, stream=None):
-    """Scatter k, v ``[T, Hkv, D]`` bf16 into the caches at ``slot_mapping`` (int64 [T])."""
+    """Scatter k, v ``[T, Hkv, D]`` bf16 (fp16 with PA_KV_F16 and PA_KV_INT4_F16)
+    into the caches at ``slot_mapping`` (int64 [T])."""
     T = int(slot_mapping.shape[0])
+    if desc.kv_dtype in _INT4:
+        act = _act(desc)
+        if k.shape != (T, desc.num_kv_heads, desc.head_dim) or v.shape != k.shape:
+            raise ValueError(f"k and v must be [{T}, {desc.num_kv_heads}, {desc.head_dim}]")
+        dev = torch._C._cuda_getDevice()
+        st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+        _check(load().pa_cache_write(ctypes.byref(desc), _at(k, act, "k", dev), _at(v, act, "v", dev),
+                                     _cache_at(k_cache, desc, "k_cache", dev), _cache_at(v_cache, desc, "v_cache", dev),
+                                     _at(slot_mapping, _I64, "slot_mapping", dev), T, st))
+        return
     _check(load().pa_cache_write(ctypes.byref(desc), _ptr(k, _act(desc), "k"), _ptr(v, _act(desc), "v"),
                                  _ptr(k_cache, _CACHE, "k_cache"), _ptr(v_cache, _CACHE, "v_cache"),
                                  _ptr(slot_mapping, _I64, "slot_mapping"), T, _stream(stream)))
@@ -402,7 +414,7 @@ _CACHE_OF = {PA_KV_BF16: (torch.bfloat16,), PA_KV_F16: (torch.float16,),
 def _cache_at(t, desc: PaKvDesc, name: str, dev: int):
     """The address of a cache of the descriptor's type and size on the current device."""
     p = _at(t, _CACHE_OF[desc.kv_dtype], name, dev)
-    if desc.kv_dtype in (PA_KV_INT4, PA_KV_INT4_F16):
+    if desc.kv_dtype in _INT4:
         if t.numel() != desc.num_blocks * desc.num_kv_heads * int4_tile_bytes(desc.head_dim):
             raise ValueError(f"{name} must be [num_blocks, num_kv_heads, int4_tile_bytes(head_dim)]")
     elif t.numel() != desc.num_blocks * desc.num_kv_heads * 16 * desc.head_dim:
@@ -428,7 +440,7 @@ def pa_widen_blocks(desc: PaKvDesc, k_cache, v_cache, src_blocks, k_out, v_out, 
     n, d = src_blocks.shape[0], desc.head_dim
     if dst_blocks.shape[0] != n:
         raise ValueError("src_blocks and dst_blocks must have one entry per pair")
-    if desc.kv_dtype not in (PA_KV_INT4, PA_KV_INT4_F16):
+    if desc.kv_dtype not in _INT4:
         raise ValueError("pa_widen_blocks reads a 4-bit cache (PA_KV_INT4, PA_KV_INT4_F16)")
     st = _launch_stream(stream, k_cache)
     dev = k_cache.get_device()
@@ -454,12 +466,34 @@ def decode_workspace(desc: PaKvDesc, num_seqs: int, max_context_len: int, device
     return torch.zeros(max(n, 16), dtype=torch.uint8, device=device or "cuda")
 
 
+def _decode_int4(call, desc, out, q, k_cache, v_cache, block_tables, context_lens, max_context_len, scale, lse, stream,
+                 workspace=None):
+    """pa_decode / pa_decode_static over a 4-bit cache."""
+    S, hq = context_lens.shape[0], desc.num_q_heads
+    if q.shape != (S, hq, desc.head_dim) or out.shape != q.shape or block_tables.dim() != 2 or \
+            block_tables.shape[0] != S or (lse is not None and lse.shape != (S, hq)):
+        raise ValueError("q and out must be [S, Hq, D], lse [S, Hq] and block_tables [S, max_blocks]")
+    dev = torch._C._cuda_getDevice()
+    host = [_ptr(t, _F32, n, allow_none=True, host_ok=True) if t is None or not t.is_cuda else _at(t, _F32, n, dev)
+            for t, n in ((out, "out"), (lse, "lse"))]
+    ws = () if workspace is None else (_at(workspace, _U8, "workspace", dev), workspace.numel())
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    _check(call(ctypes.byref(desc), host[0], host[1], _at(q, _act(desc), "q", dev),
+                _cache_at(k_cache, desc, "k_cache", dev), _cache_at(v_cache, desc, "v_cache", dev),
+                _at(block_tables, _I32, "block_tables", dev), block_tables.shape[1],
+                _at(context_lens, _I32, "context_lens", dev), S, int(max_context_len), float(scale), *ws, st))
+
+
 def pa_decode(desc: PaKvDesc, out, q, k_cache, v_cache, block_tables, context_lens,
               max_context_len: int, scale: float, workspace, lse=None, stream=None):
     """Decode attention: q ``[S, Hq, D]`` bf16 -> out ``[S, Hq, D]`` fp32 (lse ``[S, Hq]``).
     ``out`` / ``lse`` may be pinned CPU tensors: the kernel stores the result
     straight into host memory."""
     S = int(context_lens.shape[0])
+    if desc.kv_dtype in _INT4:
+        _decode_int4(load().pa_decode, desc, out, q, k_cache, v_cache, block_tables, context_lens, max_context_len,
+                     scale, lse, stream, workspace)
+        return
     _check(load().pa_decode(ctypes.byref(desc), _ptr(out, _F32, "out", host_ok=True),
                             _ptr(lse, _F32, "lse", allow_none=True, host_ok=True), _ptr(q, _act(desc), "q"),
                             _ptr(k_cache, _CACHE, "k_cache"), _ptr(v_cache, _CACHE, "v_cache"),
@@ -534,6 +568,10 @@ def pa_decode_static(desc: PaKvDesc, out, q, k_cache, v_cache, block_tables, con
     """pa_decode on the library's own fixed-size scratch (no workspace argument,
     for callers that cannot allocate device memory where they decode)."""
     S = int(context_lens.shape[0])
+    if desc.kv_dtype in _INT4:
+        _decode_int4(load().pa_decode_static, desc, out, q, k_cache, v_cache, block_tables, context_lens,
+                     max_context_len, scale, lse, stream)
+        return
     _check(load().pa_decode_static(ctypes.byref(desc), _ptr(out, _F32, "out", host_ok=True),
                                    _ptr(lse, _F32, "lse", allow_none=True, host_ok=True), _ptr(q, _act(desc), "q"),
                                    _ptr(k_cache, _CACHE, "k_cache"), _ptr(v_cache, _CACHE, "v_cache"),
@@ -702,6 +740,9 @@ def prefix_splits(num_groups: int, num_kv_heads: int, q_tiles: int, max_prefix_l
 
 def pa_copy_blocks(desc: PaKvDesc, k_cache, v_cache, src_blocks, dst_blocks, stream=None):
     """Copy-on-write: block dst_blocks[i] of both caches gets block src_blocks[i]."""
+    if desc.kv_dtype in _INT4:  # (the other types' caches are taken as they come)
+        for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+            _cache_at(t, desc, name, torch._C._cuda_getDevice())
     _check(load().pa_copy_blocks(ctypes.byref(desc), _ptr(k_cache, _CACHE, "k_cache"),
                                  _ptr(v_cache, _CACHE, "v_cache"), _ptr(src_blocks, _I32, "src_blocks"),
                                  _ptr(dst_blocks, _I32, "dst_blocks"), int(src_blocks.shape[0]),

@@ -469,7 +469,9 @@ pa_status mixed_call(const pa_kv_desc *desc, float *dec_out, float *dec_lse, con
   // the decode part's checks (and its plan, whose workspace the call uses);
   // with no decode sequence only the descriptor and the plan of an empty batch
   pa::DecodePlan plan;
-  pa_status st = pa::validate_decode(desc, dec_out, dec_lse, dec_q, k_cache, v_cache, dec_block_tables,
+  pa_status st = check_desc(desc);
+  if (st != PA_OK) return st;
+  st = pa::validate_decode(desc, dec_out, dec_lse, dec_q, k_cache, v_cache, dec_block_tables,
                                      dec_max_blocks_per_seq, dec_context_lens, num_dec_seqs, dec_max_context_len,
                                      scale, &plan);
   if (st != PA_OK) return st;

@@ -15,6 +15,11 @@ then one launch (``pa_rope_cache_write``).  A decode batch whose sequences
 share prefixes may name its groups; its attention then reads each shared
 prefix once for its group (``pa_decode_shared``).
 
+Prompts that arrive whole need no cache to be attended (``MixedStep.prompts``):
+their attention works on their own rows (``pa_prompt_attention``) and only
+their keys and values go to the cache, of any type.  Over a 4-bit cache, which
+has no prefill of its own, this is how prompts are served.
+
 This module only orders the library's calls on CUDA streams; every step of
 the computation runs in the library's kernels.  Decode and prefill read
 disjoint outputs and only read the cache, so after the write they may run
@@ -209,6 +214,21 @@ class MixedStep:
             pf_args = (q_rot[n:], *pf_args)
         B.pa_rope_cache_write(self.desc, rope, q_rot, q, k, v, positions, self.k_cache, self.v_cache, slot_mapping)
         self.attend(dec_args, pf_args, groups)
+
+    def prompts(self, out, q, k, v, query_start_loc, max_q_len, slot_mapping=None, lse=None, rope=None, positions=None,
+                q_rot=None, k_rot=None):
+        """Whole prompts: the attention of packed rows q [T, Hq, D], k and v [T,
+        Hkv, D] into ``out`` [T, Hq, D] (the activation type), and their keys
+        and values into the cache at ``slot_mapping`` [T] (None: not written;
+        v is then free to be a slice of a projection's output, else it is
+        dense).  With ``rope`` (binding.make_rope) q and k are normed and rotated
+        at ``positions`` [T] first, into ``q_rot`` and ``k_rot``."""
+        if rope is not None:
+            B.pa_qk_norm_rope(self.desc, rope, q_rot, k_rot, q, k, positions)
+            q, k = q_rot, k_rot
+        if slot_mapping is not None:
+            B.pa_cache_write(self.desc, k, v, self.k_cache, self.v_cache, slot_mapping)
+        B.pa_prompt_attention(self.desc, out, q, k, v, query_start_loc, max_q_len, self.scale, lse=lse)
 
     def __call__(self, k_new, v_new, slot_mapping, dec_args=None, pf_args=None, groups=None):
         """dec_args: (q, block_tables, context_lens); pf_args: (q, query_start_loc,

@@ -370,3 +370,63 @@ def test_steps_over_a_4_bit_cache():
     x = x.masked_fill(torch.arange(L + c)[None, :] > torch.arange(L, L + c)[:, None], -math.inf)
     want = (torch.softmax(x, -1) @ vv[:, None]).reshape(hq, c, d).transpose(0, 1)
     torch.testing.assert_close(got.cpu().double(), want, rtol=0, atol=2e-3)  # pa_prefill_chunk's tolerance
+
+
+def test_prompts_then_steps_over_a_4_bit_cache():
+    """Prompts attended on their own rows and written to a 4-bit cache, then decode steps over it, with the prompts'
+    call and a step each in a graph."""
+    hq, hkv, d, lens = 8, 2, 128, [37, 100, 16]
+    nb, n, T = 40, len(lens), sum(lens)
+    desc = pa.make_desc(nb, hkv, hq, d, pa.PA_KV_INT4)
+    kc, vc = pa.int4_cache(nb, hkv, d), pa.int4_cache(nb, hkv, d)
+    tables = torch.randperm(nb, generator=torch.Generator().manual_seed(2))[:n * 10].view(n, 10).to(torch.int32)
+    slots = torch.cat([tables[s].long()[torch.arange(L) // 16] * 16 + torch.arange(L) % 16 for s, L in enumerate(lens)])
+    g = torch.Generator(device=DEV).manual_seed(3)
+    qkv = torch.randn((T, hq + 2 * hkv, d), generator=g, device=DEV).to(torch.bfloat16)
+    v = qkv[:, hq + hkv:].contiguous()
+    rope = pa.make_rope(pa.rope_table(256, d))
+    pos = torch.cat([torch.arange(L) for L in lens]).to(torch.int32).to(DEV)
+    starts = torch.tensor([0, 37, 137, 153], dtype=torch.int32, device=DEV)
+    q_rot = torch.empty((T, hq, d), dtype=torch.bfloat16, device=DEV)
+    k_rot = torch.empty((T, hkv, d), dtype=torch.bfloat16, device=DEV)
+    out = torch.empty_like(q_rot)
+    dec = torch.zeros((n, hq, d), device=DEV)
+    scale = 1 / math.sqrt(d)
+    step = MixedStep(desc, kc, vc, scale, decode_out=dec, workspace=pa.decode_workspace(desc, n, 160),
+                     max_context_len_decode=160, mode="serial")
+    dslots = slots.to(DEV)
+    graph = GraphedStep(lambda: step.prompts(out, qkv[:, :hq], qkv[:, hq:hq + hkv], v, starts, 100, dslots, rope=rope,
+                                             positions=pos, q_rot=q_rot, k_rot=k_rot))
+    kc.zero_()
+    vc.zero_()
+    graph()
+    at = 0
+    for L in lens:  # the rotated rows' own attention
+        x = q_rot[at:at + L].cpu().double().transpose(0, 1).view(hkv, hq // hkv, L, d)
+        x = x @ k_rot[at:at + L].cpu().double().transpose(0, 1)[:, None].transpose(-1, -2) * scale
+        p = torch.softmax(x.masked_fill(torch.ones(L, L).triu(1).bool(), -math.inf), -1)
+        vv = v[at:at + L].cpu().double().transpose(0, 1)[:, None]
+        want, size = [(p @ y).reshape(hq, L, d).transpose(0, 1) for y in (vv, vv.abs())]
+        off = (out[at:at + L].cpu().double() - want).abs()
+        assert (off <= 2.0 ** -8 * (size + want.abs()) + 2.0 ** -15 * size).all()
+        at += L
+    # the rows in the cache, and steps behind them
+    stored = ref.rows_of(kc.cpu(), d)[slots // 16, :, slots % 16]
+    codes, s, m = ref.quantise(k_rot.cpu())
+    assert torch.equal(stored, (codes.double().unflatten(-1, (-1, 64)) * s.double()[..., None] +
+                                m.double()[..., None]).flatten(-2))
+    now = torch.tensor(lens, dtype=torch.int32)
+    bufs = dict(q=q_rot[:n].clone(), k=k_rot[:n].clone(), v=v[:n].clone(), slots=torch.zeros(n, dtype=torch.int64, device=DEV),
+                tables=tables.to(DEV), lens=now.to(DEV))
+    one = GraphedStep(lambda: step(bufs["k"], bufs["v"], bufs["slots"],
+                                   dec_args=(bufs["q"], bufs["tables"], bufs["lens"])))
+    for i in range(5):
+        bufs["slots"].copy_(tables[torch.arange(n), now.long() // 16].long() * 16 + now.long() % 16)
+        now += 1
+        bufs["lens"].copy_(now)
+        for b in ("q", "k", "v"):
+            bufs[b].copy_(torch.randn(bufs[b].shape, generator=g, device=DEV))
+        one()
+        want, _ = ref.decode(bufs["q"].cpu(), kc.cpu(), vc.cpu(), tables, now, scale)
+        vmax = float(ref.rows_of(vc.cpu(), d).abs().max())
+        torch.testing.assert_close(dec.cpu().double(), want, rtol=0, atol=TOL * vmax)
