@@ -56,22 +56,38 @@ __device__ __forceinline__ uint2 encode16(const uint4 &a, const uint4 &b, uint32
   pair = static_cast<uint32_t>(__half_as_ushort(s16)) | (static_cast<uint32_t>(__half_as_ushort(m16)) << 16);
   const float s = __half2float(s16), m = __half2float(m16);
   const float r = s > 0.f ? __frcp_rn(s) : 0.f;
-  uint32_t c[2] = {0, 0};
+  // rounded to the nearest even whole number by the addition of 1.5 * 2^23, in
+  // pairs; four codes at a time are put together as an fp32 number below 2^16
+  const uint64_t m2 = f2_pack(-m, -m), r2 = f2_pack(r, r);
+  const uint64_t big = f2_pack(12582912.f, 12582912.f), w256 = f2_pack(256.f, 256.f);
+  // the codes grow with x, so its ends say whether any leaves [0, 15] (a
+  // minimum far from 0 is rounded by more than a step); NaN says so too
+  const bool inside = __fmul_rn(mn - m, r) > -0.5f && __fmul_rn(mx - m, r) < 15.5f;
+  uint32_t c[2];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float2 f = A::f(x[i / 2]);
-    // rounded to the nearest even whole number by the addition of 1.5 * 2^23;
-    // fmaxf takes the 0 of a NaN
-    const float t = fminf(fmaxf(__fmul_rn((i & 1 ? f.y : f.x) - m, r), 0.f), 15.f);
-    c[i / 8] |= (__float_as_uint(t + 12582912.f) & 15u) << (4 * (i % 8));
+  for (int h = 0; h < 2; ++h) {
+    uint64_t n[4];  // pairs of codes
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = A::f(x[4 * h + i]);
+      uint64_t t = f2_mul(f2_add(f2_pack(f.x, f.y), m2), r2);
+      if (!inside) {  // (fmaxf takes the 0 of a NaN)
+        const float2 u = f2_unpack(t);
+        t = f2_pack(fminf(fmaxf(u.x, 0.f), 15.f), fminf(fmaxf(u.y, 0.f), 15.f));
+      }
+      n[i] = f2_sub(f2_add(t, big), big);
+    }
+    const float2 lo4 = f2_unpack(f2_fma(n[1], w256, n[0])), hi4 = f2_unpack(f2_fma(n[3], w256, n[2]));
+    const float a4 = fmaf(lo4.y, 16.f, lo4.x) + 8388608.f, b4 = fmaf(hi4.y, 16.f, hi4.x) + 8388608.f;
+    c[h] = __byte_perm(__float_as_uint(a4), __float_as_uint(b4), 0x5410);
   }
   return make_uint2(c[0], c[1]);
 }
 
 // One thread moves 16 dims of K and of V: 32 bytes read, 8 bytes of codes
 // written; the first of a group's four threads writes its pair.  Bound by the
-// rows' bytes (2 (2 D + 9 D / 16) per token and kv head); the arithmetic, about
-// 9 instructions a dim, is half of what the SMs issue in that time.
+// rows' bytes (2 (2 D + 9 D / 16) per token and kv head); the arithmetic is about
+// 4 instructions a dim.
 template <bool F16>
 __global__ void __launch_bounds__(256) int4_write_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v,
                                                          uint8_t *__restrict__ k_cache, uint8_t *__restrict__ v_cache,
