@@ -88,19 +88,21 @@ __device__ __forceinline__ uint2 encode16(const uint4 &a, const uint4 &b, uint32
 // written; the first of a group's four threads writes its pair.  Bound by the
 // rows' bytes (2 (2 D + 9 D / 16) per token and kv head); the arithmetic is about
 // 4 instructions a dim.
-template <bool F16>
+template <int D, bool F16>
 __global__ void __launch_bounds__(256) int4_write_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v,
                                                          uint8_t *__restrict__ k_cache, uint8_t *__restrict__ v_cache,
-                                                         const int64_t *__restrict__ slot_mapping, int64_t total,
-                                                         int num_kv_heads, int d, int64_t num_slots, int checked,
+                                                         const int64_t *__restrict__ slot_mapping, uint32_t rows,
+                                                         uint32_t num_kv_heads, int64_t num_slots, int checked,
                                                          int32_t *err) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int parts = d / 16;
-  const int64_t row = i / parts;  // token * num_kv_heads + head
-  const int part = static_cast<int>(i - row * parts);
+  constexpr int kParts = D / 16;
+  // a row of 2^32 would be one of 550 GB of keys: 32 bits, whose division is short
+  const uint32_t row = blockIdx.x * (256u / kParts) + threadIdx.x / kParts;  // token * num_kv_heads + head
+  const int part = threadIdx.x % kParts;
+  const int64_t i = static_cast<int64_t>(row) * kParts + part;
+  const uint32_t token = row / num_kv_heads, head = row - token * num_kv_heads;
   int64_t slot = -1;
-  if (i < total) slot = __ldg(slot_mapping + row / num_kv_heads);
+  if (row < rows) slot = __ldg(slot_mapping + token);
   if (checked && slot >= num_slots) {
     if (part == 0) report_error(err, nullptr, kErrBadIndex);
     slot = -1;
@@ -116,13 +118,13 @@ __global__ void __launch_bounds__(256) int4_write_kernel(const uint4 *__restrict
   const uint2 kc = encode16<F16>(k0, k1, kp, kr);
   const uint2 vc = encode16<F16>(v0, v1, vp, vr);
   if (!live) return;
-  const int64_t tile = ((slot >> 4) * num_kv_heads + row % num_kv_heads) * i4::tile_bytes(d);
+  const int64_t tile = ((slot >> 4) * num_kv_heads + head) * i4::tile_bytes(D);
   const int off = static_cast<int>(slot & 15);
-  const int64_t at = tile + off * (d / 2) + part * 8;
+  const int64_t at = tile + off * (D / 2) + part * 8;
   *reinterpret_cast<uint2 *>(k_cache + at) = kc;
   *reinterpret_cast<uint2 *>(v_cache + at) = vc;
   if ((part & 3) == 0) {
-    const int64_t pat = tile + i4::code_bytes(d) + (off * i4::groups(d) + part / 4) * 4;
+    const int64_t pat = tile + i4::code_bytes(D) + (off * i4::groups(D) + part / 4) * 4;
     *reinterpret_cast<uint32_t *>(k_cache + pat) = kp;
     *reinterpret_cast<uint32_t *>(v_cache + pat) = vp;
     if (kr || vr) report_error(err, nullptr, kErrFp16Range);
@@ -152,19 +154,19 @@ __global__ void __launch_bounds__(256) int4_widen_kernel(const uint8_t *__restri
                                                          const uint8_t *__restrict__ v_cache,
                                                          const int32_t *__restrict__ src_blocks,
                                                          uint8_t *__restrict__ k_out, uint8_t *__restrict__ v_out,
-                                                         const int32_t *__restrict__ dst_blocks, int64_t tiles,
-                                                         int num_kv_heads, int num_blocks, int num_out_blocks,
+                                                         const int32_t *__restrict__ dst_blocks, uint32_t tiles,
+                                                         uint32_t num_kv_heads, int num_blocks, int num_out_blocks,
                                                          int checked, int32_t *err) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int kWords = D / 16;  // per lane: 16 rows of D / 8 words
   const int lane = threadIdx.x & 31;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x / 32);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32; i < tiles; i += warps) {
+  const uint32_t warps = gridDim.x * (blockDim.x / 32);
+  // (2^31 tiles would be 4 TB of pages)
+  for (uint32_t i = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; i < tiles; i += warps) {
     // tile order: page, K or V, kv head
-    const int64_t pair = i / (2 * num_kv_heads);
-    const int r = static_cast<int>(i - pair * 2 * num_kv_heads);
+    const uint32_t pair = i / (2 * num_kv_heads), r = i - pair * 2 * num_kv_heads;
     const bool is_v = r >= num_kv_heads;
-    const int head = is_v ? r - num_kv_heads : r;
+    const uint32_t head = is_v ? r - num_kv_heads : r;
     const int sb = __ldg(src_blocks + pair), db = __ldg(dst_blocks + pair);
     if (checked && (sb < 0 || sb >= num_blocks || db < 0 || db >= num_out_blocks)) {
       if (r == 0 && lane == 0) report_error(err, nullptr, kErrBadIndex);
@@ -192,14 +194,17 @@ __global__ void __launch_bounds__(256) int4_widen_kernel(const uint8_t *__restri
 
 cudaError_t launch_int4_write(const pa_kv_desc &d, const void *k, const void *v, void *k_cache, void *v_cache,
                               const int64_t *slot_mapping, int32_t num_tokens, cudaStream_t stream) {
-  const int64_t total = static_cast<int64_t>(num_tokens) * d.num_kv_heads * (d.head_dim / 16);
-  const int threads = 256;
-  const int64_t blocks = (total + threads - 1) / threads;
-  auto kern = d.kv_dtype == PA_KV_INT4_F16 ? &int4_write_kernel<true> : &int4_write_kernel<false>;
+  const bool f16 = d.kv_dtype == PA_KV_INT4_F16;
+  const int64_t rows = static_cast<int64_t>(num_tokens) * d.num_kv_heads;
+  const int threads = 256, per_cta = threads / (d.head_dim / 16);
+  const int64_t blocks = (rows + per_cta - 1) / per_cta;
+  if (rows > 0xffffffffLL || blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  auto kern = d.head_dim == 128 ? (f16 ? &int4_write_kernel<128, true> : &int4_write_kernel<128, false>)
+                                : (f16 ? &int4_write_kernel<64, true> : &int4_write_kernel<64, false>);
   kern<<<static_cast<unsigned>(blocks), threads, 0, stream>>>(
       static_cast<const uint4 *>(k), static_cast<const uint4 *>(v), static_cast<uint8_t *>(k_cache),
-      static_cast<uint8_t *>(v_cache), slot_mapping, total, d.num_kv_heads, d.head_dim,
-      static_cast<int64_t>(d.num_blocks) * 16, d.check_indices, d.error_word);
+      static_cast<uint8_t *>(v_cache), slot_mapping, static_cast<uint32_t>(rows),
+      static_cast<uint32_t>(d.num_kv_heads), static_cast<int64_t>(d.num_blocks) * 16, d.check_indices, d.error_word);
   return cudaGetLastError();
 }
 
@@ -208,15 +213,17 @@ cudaError_t launch_int4_widen(const pa_kv_desc &d, const void *k_cache, const vo
                               int32_t num_out_blocks, int32_t num_pairs, cudaStream_t stream) {
   const bool f16 = d.kv_dtype == PA_KV_INT4_F16;
   const int64_t tiles = static_cast<int64_t>(num_pairs) * d.num_kv_heads * 2;
+  if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
   const int threads = 256;
   const int64_t want = (tiles + threads / 32 - 1) / (threads / 32);
-  const int64_t cap = static_cast<int64_t>(device_sm_count()) * 8;
+  const int64_t cap = static_cast<int64_t>(device_sm_count()) * 32;
   const unsigned blocks = static_cast<unsigned>(want < cap ? want : cap);
   auto kern = d.head_dim == 128 ? (f16 ? &int4_widen_kernel<128, true> : &int4_widen_kernel<128, false>)
                                 : (f16 ? &int4_widen_kernel<64, true> : &int4_widen_kernel<64, false>);
   kern<<<blocks, threads, 0, stream>>>(static_cast<const uint8_t *>(k_cache), static_cast<const uint8_t *>(v_cache),
                                        src_blocks, static_cast<uint8_t *>(k_out), static_cast<uint8_t *>(v_out),
-                                       dst_blocks, tiles, d.num_kv_heads, d.num_blocks, num_out_blocks,
+                                       dst_blocks, static_cast<uint32_t>(tiles), static_cast<uint32_t>(d.num_kv_heads),
+                                       d.num_blocks, num_out_blocks,
                                        d.check_indices, d.error_word);
   return cudaGetLastError();
 }
