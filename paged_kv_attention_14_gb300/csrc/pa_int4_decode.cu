@@ -102,12 +102,6 @@ __device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, ui
 }
 // the halves of an fp16 pair in fp32
 __device__ __forceinline__ float2 halves(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2 *>(&u)); }
-// (x & mask) ^ flip
-__device__ __forceinline__ uint32_t and_xor(uint32_t x, uint32_t mask, uint32_t flip) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(x), "r"(mask), "r"(flip));
-  return r;
-}
 // an 8 x 8 matrix of 16-bit values, one row's pair a lane, transposed
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t r;
@@ -417,7 +411,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
   constexpr int ROW8 = 8 * (D / 2);                                          // eight rows further
 
   const float low = t < 2 ? 0.f : -1.f;
-  const float flip = gq & 1 ? -1.f : 1.f, flip15 = gq & 1 ? 15.f : 0.f;
   int cslot = 0;
   long long cu = u0;
 #pragma unroll 1
@@ -561,10 +554,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
         }
       }
 
-      // the values' scales and minima; masked tokens have neither.  Every
-      // second token's weight is negated and its code taken from 15, s n + m =
-      // (m + 15 s) - s (15 - n): codes are never negative, and without this the
-      // two sums, of codes and of minima, would grow far past their difference.
+      // the values' scales and minima; masked tokens have neither.  The weights
+      // of a block's last eight tokens are negated and their codes taken from
+      // 15, s n + m = (m + 15 s) - s (15 - n): codes are never negative, and
+      // without this the two sums, of codes and of minima, would grow far past
+      // their difference (131069 tokens: outputs off by 2e-4 of their norm).
       float vs[2][2][NG], vm[2][2][NG];
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt)
@@ -576,7 +570,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
           for (int p = 0; p < NG; ++p) {
             const float2 g = halves(w[p]);
             vs[tt][i][p] = g.x;
-            vm[tt][i][p] = fmaf(flip15, g.x, g.y);
+            vm[tt][i][p] = i == 0 ? g.y : fmaf(15.f, g.x, g.y);
           }
         }
       if (n < 2 || pos0 < csp.first || pos0 + 32 > csp.len) {
@@ -658,7 +652,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
             for (int p = 0; p < NG; ++p) {
               mz[r][p][0] = fmaf(w0, vm[tt][i][p], mz[r][p][0]);
               mz[r][p][1] = fmaf(w1, vm[tt][i][p], mz[r][p][1]);
-              const float sv = vs[tt][i][p] * flip;
+              const float sv = i == 0 ? vs[tt][i][p] : -vs[tt][i][p];
               const float y0 = w0 * sv, y1 = w1 * sv;
               const uint32_t h = pack_f16x2(y0, y1);
               const float2 hf = halves(h);
@@ -680,8 +674,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
             uint32_t b1 = __byte_perm(w2, w3, h ? 0x7632 : 0x5410);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const uint32_t v0 = and_xor(b0, 0x000F000Fu, 0x000F0000u), v1 = and_xor(b0, 0x00F000F0u, 0x00F00000u);
-              const uint32_t v2 = and_xor(b1, 0x000F000Fu, 0x000F0000u), v3 = and_xor(b1, 0x00F000F0u, 0x00F00000u);
+              const uint32_t v0 = b0 & 0x000F000Fu, v1 = b0 & 0x00F000F0u;
+              const uint32_t v2 = ~b1 & 0x000F000Fu, v3 = ~b1 & 0x00F000F0u;
 #pragma unroll
               for (int r = 0; r < NR; ++r) {
                 if (tt == 0)
