@@ -805,9 +805,9 @@ PA_API pa_status pa_decode_static(const pa_kv_desc *desc, float *out, float *lse
 
 /*
  * Test hook for the failure path (no counterpart on the pages).  While
- * enabled (enable != 0), the producers of the decode, shared decode and
- * tcgen05 prefill kernels launched afterwards issue no copies and signal nothing, so the
- * kernels' bounded waits run out: they report PA_DEVERR_WAIT_TIMEOUT, free
+ * enabled (enable != 0), the producers of the decode, shared decode, tcgen05
+ * prefill and prompt kernels launched afterwards issue no copies and signal nothing (the
+ * 4-bit decode waits for nothing but its own loads), so the kernels' bounded waits run out: they report PA_DEVERR_WAIT_TIMEOUT, free
  * what they hold and return, with nothing in flight.  wait_limit_ns (> 0)
  * replaces the 2 s limit of every bounded wait while enabled, so a test
  * does not wait long.  Process-wide; pass enable = 0 to restore normal

@@ -630,7 +630,7 @@ pa_status pa_prompt_attention(const pa_kv_desc *desc, void *out, float *lse, con
   if (!(scale == scale)) return fail(PA_ERR_INVALID_ARG, "scale is NaN%s");
   // a CTA per (up to 128 rows, kv head), at most twice as many places
   const int64_t tokens = 128 / (desc->num_q_heads / desc->num_kv_heads);
-  if ((num_tokens / tokens + num_seqs) * desc->num_kv_heads > 0x3fffffff)
+  if ((num_tokens / tokens + num_seqs) * desc->num_kv_heads > 0x1fffffff)
     return fail(PA_ERR_UNSUPPORTED, "too many tokens and heads for one call%s");
   const cudaError_t e =
       pa::launch_prompt(*desc, out, lse, q, q_stride, k, k_stride, v, v_stride, query_start_loc, num_seqs, num_tokens,

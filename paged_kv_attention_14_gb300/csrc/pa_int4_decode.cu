@@ -23,8 +23,17 @@
 // (outputs).  The queries are used in fp16, scaled by a power of two so that
 // their largest is in [1, 2): exact for bf16 and fp16 down to 2^-10 of the
 // largest, 2^-21 of it below.  The weights times the scales go in as a hi + lo
-// pair of fp16 (22 bits): rows 8..15 of the operand are the lo halves of rows
-// 0..7 (more than 8 query heads per kv head: a second product).
+// pair of fp16 (22 bits).  Scores are keys (16 rows) times queries (8 columns),
+// outputs are values (16 dims) times weights (8 columns); with up to 4 query
+// heads per kv head the columns of queries 4..7 take the lo halves, with more
+// there is a product for each half.
+//
+// Bounded by instructions: a block of a kv head takes a warp about 320 (codes to
+// operands 90, products 16, weights and scales 130, fetching 30), and the SMs
+// issue every second cycle with the two warps a scheduler that the registers
+// allow.  32 sequences of 8192, 32 / 8 heads of 128: 69.2 us, 4.4 TB/s; 128
+// sequences of 1024 to 8192, 40 heads: 152 us.  Before the first block and
+// after the last a call takes about 9 us.
 //
 // The sums of the tensor cores round towards zero, so they run over one stage
 // and are then added to fp32 registers.

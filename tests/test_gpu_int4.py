@@ -313,6 +313,49 @@ def test_decode_static_and_pinned_outputs():
         b.check()
 
 
+def test_a_cache_past_32_bits():
+    """Rows whose bytes lie past 2^32 are written, widened and attended where they are."""
+    hkv, d, nb = 8, 128, 480_000  # 4.4 GB each
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 10 GB")
+    desc = pa.make_desc(nb, hkv, hkv, d, pa.PA_KV_INT4, check_indices=True)
+    kc, vc = pa.int4_cache(nb, hkv, d), pa.int4_cache(nb, hkv, d)
+    pages = [nb - 1, 3, nb - 7]
+    small = pa.make_desc(3, hkv, hkv, d, pa.PA_KV_INT4)
+    ks, vs = pa.int4_cache(3, hkv, d), pa.int4_cache(3, hkv, d)
+    T = 45
+    k, v = [x.to(DEV) for x in (_rows(T, hkv, d, torch.bfloat16, 1), _rows(T, hkv, d, torch.bfloat16, 2))]
+    i = torch.arange(T, device=DEV)
+    at = torch.tensor(pages, device=DEV)
+    pa.pa_cache_write(desc, k, v, kc, vc, at[i // 16] * 16 + i % 16)
+    pa.pa_cache_write(small, k, v, ks, vs, i)
+    for p, q in enumerate(pages):
+        assert torch.equal(kc[q], ks[p]) and torch.equal(vc[q], vs[p])
+    q = torch.randn((1, hkv, d), device=DEV).to(torch.bfloat16)
+    outs = []
+    for de, c, tab in ((desc, (kc, vc), pages), (small, (ks, vs), [0, 1, 2])):
+        out = torch.zeros((1, hkv, d), device=DEV)
+        pa.pa_decode(de, out, q, *c, torch.tensor([tab], dtype=torch.int32, device=DEV),
+                     torch.tensor([T], dtype=torch.int32, device=DEV), T, 0.1, pa.decode_workspace(de, 1, T))
+        wide = torch.zeros((2, 3, hkv, 16, d), dtype=torch.bfloat16, device=DEV)
+        pa.pa_widen_blocks(de, *c, torch.tensor(tab, dtype=torch.int32, device=DEV), wide[0], wide[1],
+                           torch.arange(3, dtype=torch.int32, device=DEV))
+        outs.append((out, wide))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+def test_two_decodes_at_once():
+    a, b = Batch([3000, 70, 5], 8, 2, 128, pa.PA_KV_INT4, seed=17), Batch([900] * 20, 16, 1, 64, pa.PA_KV_INT4_F16, seed=18)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for x, st in zip((a, b), streams):
+            x.run(stream=st)
+    torch.cuda.synchronize()
+    a.check()
+    b.check()
+
+
 def test_steps_over_a_4_bit_cache():
     """A layer's tokens rotated, written, attended; a chunk behind them over the widened pages."""
     hq, hkv, d, steps, n = 8, 2, 64, 20, 3

@@ -195,6 +195,27 @@ def test_on_another_stream_captured_and_the_same_twice():
     assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
 
 
+def test_two_calls_at_once_and_beside_other_tensor_memory():
+    """Prompts on two streams, of the large and the small kind, and a chunked prefill between them."""
+    big, small = _rows([900, 300], 8, 2, 128, torch.bfloat16, 13), _rows([30] * 90, 8, 2, 128, torch.bfloat16, 14)
+    desc = pa.make_desc(8, 2, 8, 128)
+    outs = [torch.zeros(x[0].shape, dtype=torch.bfloat16, device=DEV) for x in (big, small)]
+    kc, vc = [torch.randn((8, 2, 16, 128), device=DEV).to(torch.bfloat16) for _ in range(2)]
+    pf = torch.zeros((64, 8, 128), device=DEV)
+    pq = small[0][:64].contiguous()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    table, lens, loc = torch.arange(8, dtype=torch.int32, device=DEV)[None], i32(128), i32(0, 64)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for (q, k, v, starts), out, longest, st in zip((big, small), outs, (900, 30), streams):
+            pa.pa_prompt_attention(desc, out, q, k, v, starts, longest, 0.1, stream=st)
+        pa.pa_prefill_chunk(desc, pf, pq, loc, kc, vc, table, lens, 64, 128, 0.1, stream=streams[0])
+    torch.cuda.synchronize()
+    for (q, k, v, _), out, lens in zip((big, small), outs, ([900, 300], [30] * 90)):
+        _check(out, None, _want(q, k, v, lens, 0.1), torch.bfloat16)
+
+
 def test_checked_starts():
     q, k, v, _ = _rows([100], 2, 1, 64, torch.bfloat16, 11)
     out = torch.zeros((100, 2, 64), dtype=torch.bfloat16, device=DEV)
