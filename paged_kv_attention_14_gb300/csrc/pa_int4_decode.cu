@@ -15,6 +15,8 @@
 // another warp.  (Bulk copies issued by one lane: 17% slower.)  A (sequence, kv
 // head) cut between warps is joined by the CTA from pieces in shared memory,
 // one cut between CTAs by the CTA that counts in last, always in the same order.
+// Where all sequences are short the CTAs' ranges end at whole (sequence, kv
+// head)s, so that there is nothing to join between them (kWhole).
 //
 // Codes as operands.  A code of 4 bits in the lowest bits of an fp16 number is
 // the subnormal n 2^-24, exactly; in the next four it is 16 n 2^-24.  So a word
@@ -32,8 +34,8 @@
 // operands 90, products 16, weights and scales 130, fetching 30), and the SMs
 // issue every second cycle with the two warps a scheduler that the registers
 // allow.  32 sequences of 8192, 32 / 8 heads of 128: 69.2 us, 4.4 TB/s; 128
-// sequences of 1024 to 8192, 40 heads: 152 us.  Before the first block and
-// after the last a call takes about 9 us.
+// sequences of 1024 to 8192, 40 heads: 151 us.  Before the first block and
+// after the last a call takes 7 us, 9 where CTAs join.
 //
 // The sums of the tensor cores round towards zero, so they run over one stage
 // and are then added to fp32 registers.
@@ -48,6 +50,7 @@ namespace pa {
 namespace {
 
 constexpr int kMinUnits = 8;  // units a CTA gets at least, where there are few
+constexpr int kWhole = 64;  // blocks of a sequence up to which CTAs get whole (sequence, kv head)s
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -228,10 +231,6 @@ struct Deal {
     }
   }
   __device__ __forceinline__ long long first(int c) const { return each * c + rest * c / ctas; }
-  __device__ __forceinline__ long long first(int c, int w) const {
-    const long long c0 = first(c);
-    return c0 + static_cast<unsigned>(static_cast<int>(first(c + 1) - c0) * w) / static_cast<unsigned>(warps);
-  }
   // the CTA that has unit u
   __device__ __forceinline__ int cta_of(long long u) const {
     const long long total = each * ctas + rest, x = (u + 1) * ctas - 1;
@@ -249,6 +248,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long pre[kWarps * 32];
   __shared__ long long warp_sum[kWarps];
+  __shared__ int warp_longest[kWarps];
+  __shared__ long long bounds[2];
   __shared__ Piece pieces[2 * kWarps];  // of each warp: one that began before its range, one that goes on behind it
   __shared__ long long starts[kWarps + 1];  // of the warps' ranges
   __shared__ Join joins[2];
@@ -262,17 +263,25 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
   // --- the units before each thread's share of the sequences, and all of them
   const int cs = (a.num_seqs + kWarps * 32 - 1) / (kWarps * 32);
   long long total;
+  int longest = 0;
   {
     long long mine = 0;
-    for (int s = tid * cs; s < min((tid + 1) * cs, a.num_seqs); ++s)
-      mine += static_cast<long long>(span_of(a, __ldg(a.lens + s)).nb) * a.hkv;
+    for (int s = tid * cs; s < min((tid + 1) * cs, a.num_seqs); ++s) {
+      const int nb = span_of(a, __ldg(a.lens + s)).nb;
+      mine += static_cast<long long>(nb) * a.hkv;
+      longest = max(longest, nb);
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
-    if (lane == 31) warp_sum[warp] = incl;
+    if (lane == 31) {
+      warp_sum[warp] = incl;
+      warp_longest[warp] = longest;
+    }
     __syncthreads();
     long long base = 0;
     total = 0;
@@ -280,6 +289,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) base += warp_sum[w];
       total += warp_sum[w];
+      longest = max(longest, warp_longest[w]);
     }
     pre[tid] = base + incl - mine;
     __syncthreads();
@@ -290,43 +300,67 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
   const Deal deal(total, static_cast<int>(want < 1 ? 1 : want < gridDim.x ? want : gridDim.x), kWarps);
   const int cta = blockIdx.x;
   const bool idle = cta >= deal.ctas || total == 0;
-  const long long u0 = idle ? 0 : deal.first(cta, warp), u1 = idle ? 0 : deal.first(cta, warp + 1);
-  if (lane < 2) pieces[2 * warp + lane].nb = 0;
-  if (lane == 0) starts[warp] = u0;
-  if (tid == 0) starts[kWarps] = idle ? 0 : deal.first(cta + 1);
-
-  if (u0 < u1) {  // (not indented: the whole of the warp's work)
-  // --- the sequence of its first unit
-  int s0;
-  long long at0;  // units before it
-  {
-    int i = 0;
-#pragma unroll
-    for (int step = 256; step > 0; step >>= 1)
-      if (i + step < kWarps * 32 && pre[i + step] <= u0) i += step;
-    s0 = i * cs;
-    at0 = pre[i];
-    for (; cs > 1; s0 += 32) {  // (cs 1: a sequence a thread, it is the one)
-      const int s = s0 + lane;
-      long long incl = s < a.num_seqs ? static_cast<long long>(span_of(a, __ldg(a.lens + s)).nb) * a.hkv : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
+  const bool whole_only = longest <= kWhole;
+  long long r0 = 0, r1 = 0, u0 = 0, u1 = 0;  // the CTA's units, the warp's
+  int s0 = 0;                                // the sequence of unit u0
+  long long at0 = 0;                         // units before it
+  if (!idle) {
+    if (!whole_only) r0 = deal.first(cta), r1 = deal.first(cta + 1);
+#pragma unroll 1
+    for (int pass = whole_only ? 0 : 1; pass < 2; ++pass) {
+      long long u;  // the unit whose sequence is looked for
+      if (pass == 0) {
+        u = deal.first(cta + (warp & 1));  // (total, for the last CTA's end: its last sequence or one behind it)
+      } else {
+        const unsigned n = static_cast<unsigned>(r1 - r0);
+        u = u0 = r0 + n * warp / kWarps;
+        u1 = r0 + n * (warp + 1) / kWarps;
+        if (u0 >= u1) break;
       }
-      const unsigned over = __ballot_sync(0xffffffffu, at0 + incl > u0);
-      if (over) {
-        const int j = __ffs(over) - 1;
-        const long long before = __shfl_sync(0xffffffffu, incl, j > 0 ? j - 1 : 0);
-        if (j > 0) at0 += before;
-        s0 += j;
-        break;
+      // the last thread whose share begins at u or before it: of every
+      // kWarps-th, then of those from there on
+      int i = (__popc(__ballot_sync(0xffffffffu, pre[lane * kWarps] <= u)) - 1) * kWarps;
+      i += __popc(__ballot_sync(0xffffffffu, lane < kWarps && pre[i + (lane < kWarps ? lane : 0)] <= u)) - 1;
+      s0 = i * cs;
+      at0 = pre[i];
+#pragma unroll 1
+      for (; cs > 1; s0 += 32) {  // (cs 1: a sequence a thread, it is the one)
+        const int s = s0 + lane;
+        long long incl = s < a.num_seqs ? static_cast<long long>(span_of(a, __ldg(a.lens + s)).nb) * a.hkv : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += x;
+        }
+        const unsigned over = __ballot_sync(0xffffffffu, at0 + incl > u);
+        if (over) {
+          const int j = __ffs(over) - 1;
+          const long long before = __shfl_sync(0xffffffffu, incl, j > 0 ? j - 1 : 0);
+          if (j > 0) at0 += before;
+          s0 += j;
+          break;
+        }
+        at0 += __shfl_sync(0xffffffffu, incl, 31);
+        if (s0 + 32 >= a.num_seqs) break;  // (u is the total)
       }
-      at0 += __shfl_sync(0xffffffffu, incl, 31);
-      if (s0 + 32 >= a.num_seqs) break;  // (not reached: u0 < total)
+      if (pass == 0) {
+        // the nearest end of a (sequence, kv head)
+        if (u < total) {
+          const int nb = span_of(a, __ldg(a.lens + s0)).nb, in = static_cast<int>(u - at0) % nb;
+          u += 2 * in < nb ? -in : nb - in;
+        }
+        if (warp < 2 && lane == 0) bounds[warp] = u;
+        __syncthreads();
+        r0 = bounds[0];
+        r1 = bounds[1];
+      }
     }
   }
+  if (lane < 2) pieces[2 * warp + lane].nb = 0;
+  if (lane == 0) starts[warp] = u0;
+  if (tid == 0) starts[kWarps] = r1;
 
+  if (u0 < u1) {  // (not indented: the whole of the warp's work)
   // --- the fetching side: where it stands
   const uint8_t *const ring = smem + warp * C::RING;
   const uint32_t ring_at = smem_u32(ring);
@@ -412,6 +446,25 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
   };
   int cseq = fs, ch = fh, cb = fb;  // the computing side
   Span csp = fsp;
+  // a lane's part of a piece's queries: with one eight of them asked for a
+  // piece ahead, the first before the blocks
+  constexpr bool kAhead = NR == 1;
+  uint4 raw[NR][NG][2];
+  auto ask_queries = [&](int seq, int head) {
+    const int64_t row0 = static_cast<int64_t>(seq) * a.hq + head * a.g;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const int query = (NQ == 4 ? gq & 3 : gq) + 8 * r;
+#pragma unroll
+      for (int p = 0; p < NG; ++p)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          raw[r][p][j] = query < a.g
+                             ? __ldg(reinterpret_cast<const uint4 *>(a.q + (row0 + query) * D + 64 * p + 16 * t) + j)
+                             : make_uint4(0, 0, 0, 0);
+    }
+  };
+  if constexpr (kAhead) ask_queries(cseq, ch);
 #pragma unroll 1
   for (int i = 0; i < NST - 1; ++i) fetch();
 
@@ -432,27 +485,21 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
     cu += b_end - cb;
     const int64_t row0 = static_cast<int64_t>(cseq) * a.hq + ch * a.g;
 
+    if constexpr (!kAhead) ask_queries(cseq, ch);
+
     // per lane: its part of query gq's dims, and the rest of queries 2 t, 2 t + 1
     uint32_t qf[NR][D / 16][2];
     float cs_[NR][2], cm[NR][NG][2], M[NR][2], l[NR][2], mz[NR][NG][2];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      const int query = (NQ == 4 ? gq & 3 : gq) + 8 * r;
-      uint4 raw[NG][2];
       float amax = 0.f, sum[NG];
-#pragma unroll
-      for (int p = 0; p < NG; ++p)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          raw[p][j] = query < a.g ? __ldg(reinterpret_cast<const uint4 *>(a.q + (row0 + query) * D + 64 * p + 16 * t) + j)
-                                  : make_uint4(0, 0, 0, 0);
       float f[NG][16];
 #pragma unroll
       for (int p = 0; p < NG; ++p) {
         sum[p] = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const uint32_t w = j < 4 ? (&raw[p][0].x)[j] : (&raw[p][1].x)[j - 4];
+          const uint32_t w = j < 4 ? (&raw[r][p][0].x)[j] : (&raw[r][p][1].x)[j - 4];
           f[p][2 * j] = a.f16 ? f16lo(w) : bf16lo(w);
           f[p][2 * j + 1] = a.f16 ? f16hi(w) : bf16hi(w);
         }
@@ -493,6 +540,19 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
         M[r][c] = -INFINITY;
         l[r][c] = 0.f;
       }
+    }
+    // the (sequence, kv head) of the next piece
+    int nseq = cseq, nh = ch;
+    Span nsp = csp;
+    if (cu < u1) {
+      if (++nh == a.hkv) {
+        nh = 0;
+        do {
+          ++nseq;
+          nsp = span_of(a, __ldg(a.lens + nseq));
+        } while (nsp.nb == 0 && nseq + 1 < a.num_seqs);
+      }
+      if constexpr (kAhead) ask_queries(nseq, nh);
     }
     // weights are 2^(x - M + kexp): kexp keeps weight * scale within fp16
     float kexp = 60.f, kap = 1152921504606846976.f;  // 2^60
@@ -763,16 +823,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
       }
     if (!whole && lane == 0) pieces[slot] = Piece{seg, row0, csp.nb};
 
-    if (cb == csp.nb && cu < u1) {
-      cb = 0;
-      if (++ch == a.hkv) {
-        ch = 0;
-        do {
-          ++cseq;
-          csp = span_of(a, __ldg(a.lens + cseq));
-        } while (csp.nb == 0 && cseq + 1 < a.num_seqs);
-      }
-    }
+    cseq = nseq;
+    ch = nh;
+    csp = nsp;
+    cb = 0;
   }
   cp_async_wait<0>();
   }  // u0 < u1
@@ -883,6 +937,17 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
         // a lane's piece's reference and sum; the dims come four pieces at a time
         const int m = min(32, jn.n - base);
         const float2 ml = lane < m ? __ldcg(&a.slot_ml[slot_of(base + lane) * a.g + r]) : make_float2(-INFINITY, 0.f);
+        Part<D> v[4];
+        auto ask = [&](int i0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i0 + i < m)
+              v[i].load_l2(a.slot_o + (slot_of(base + i0 + i) * a.g + r) * D + lane * (D / 32));
+            else
+              v[i].clear();
+          }
+        };
+        ask(0);
         const float up = fmaxf(ref, warp_max_xor(ml.x, 1, 32));
         const float f = weight_of(ml, up), keep = ref == -INFINITY ? 0.f : ex2_approx(ref - up);
         ref = up;
@@ -891,14 +956,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
         for (int i = 0; i < D / 32; ++i) o.x[i] *= keep;
 #pragma unroll 1
         for (int i0 = 0; i0 < m; i0 += 4) {
-          Part<D> v[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (i0 + i < m)
-              v[i].load_l2(a.slot_o + (slot_of(base + i0 + i) * a.g + r) * D + lane * (D / 32));
-            else
-              v[i].clear();
-          }
+          if (i0) ask(i0);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int at = (i0 + i) & 31;  // (lanes from m on have weight and sum 0)

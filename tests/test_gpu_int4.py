@@ -217,6 +217,18 @@ def test_decode_of_many_sequences():
     b.check()
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (3, 1, 64), (16, 1, 128), (10, 2, 64)])
+@pytest.mark.parametrize("lens", [[1024] * 24, [1025, 0] + [1024] * 9, [0, 0], [0] * 300 + [700] + [0] * 500 + [33, 0],
+                                  list(range(400)), [64] * 152 + [0], [1] * 513])
+def test_decode_around_what_is_dealt_whole(hq, hkv, d, lens):
+    b = Batch(lens, hq, hkv, d, pa.PA_KV_INT4, seed=6)
+    b.run()
+    b.check()
+    first = b.out.clone()
+    b.run()
+    assert torch.equal(b.out, first)
+
+
 @pytest.mark.parametrize("local", [dict(sliding_window=1), dict(sliding_window=5), dict(sliding_window=100),
                                    dict(attention_chunk=64), dict(attention_chunk=48, sliding_window=20)])
 @pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (16, 1, 64)])
