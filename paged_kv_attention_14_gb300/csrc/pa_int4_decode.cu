@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
   Span fsp = span_of(a, __ldg(a.lens + fs));
   {
     const long long off = u0 - at0;
-    fh = static_cast<int>(off / fsp.nb);
+    fh = total < 0x7fffffff ? static_cast<int>(off) / fsp.nb : static_cast<int>(off / fsp.nb);
     fb = static_cast<int>(off - static_cast<long long>(fh) * fsp.nb);
   }
   int next_len = fs + 1 < a.num_seqs ? __ldg(a.lens + fs + 1) : 0;
@@ -911,6 +911,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
       }
     }
   }
+
+  if (whole_only) return;
 
   // --- and what goes beyond this CTA, by the CTA that finishes its last piece.
   // Lane 0 of warp 0: what began before this CTA; lane 1: what begins here and
