@@ -33,9 +33,9 @@
 // Bounded by instructions: a block of a kv head takes a warp about 320 (codes to
 // operands 90, products 16, weights and scales 130, fetching 30), and the SMs
 // issue every second cycle with the two warps a scheduler that the registers
-// allow.  32 sequences of 8192, 32 / 8 heads of 128: 69.2 us, 4.4 TB/s; 128
-// sequences of 1024 to 8192, 40 heads: 151 us.  Before the first block and
-// after the last a call takes 7 us, 9 where CTAs join.
+// allow.  32 sequences of 8192, 32 / 8 heads of 128: 66.4 us, 4.6 TB/s; 128
+// sequences of 1024 to 8192, 40 heads: 145 us.  The smallest call takes 7.5 us:
+// lengths, tables and blocks one after the other from memory, launch, outputs.
 //
 // The sums of the tensor cores round towards zero, so they run over one stage
 // and are then added to fp32 registers.
@@ -49,8 +49,15 @@ namespace pa {
 
 namespace {
 
-constexpr int kMinUnits = 8;  // units a CTA gets at least, where there are few
-constexpr int kWhole = 64;  // blocks of a sequence up to which CTAs get whole (sequence, kv head)s
+// Units a CTA gets at least, where there are few: with more, warps take two one
+// after the other (5 sequences of 1 to 33 tokens: 7.5 us; 16: 7.8).
+constexpr int kMinUnits = 8;
+// Blocks of the longest sequence up to which CTAs get whole (sequence, kv
+// head)s: joining between CTAs costs about 3 us, a CTA's surplus at most as many
+// blocks.  32 sequences, 32 / 8 heads of 128, whole against cut: of 128 tokens
+// 8.2 us and 11.5, of 1024 15.3 and 17.5, of 2048 23.5 both, of 4096 41.8 and
+// 40.7 (ragged to 4096: 40.1 and 28.1).
+constexpr int kWhole = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -74,7 +81,7 @@ struct Args {
 template <int D, int NQ>
 struct Cfg {
   // warps: what the registers allow without spilling.  64 dims, up to 8 queries:
-  // 12 (128 sequences of 1024 to 8192, 32 / 8 heads: 94 us; 8 warps 106).
+  // 12 (128 sequences of 1024 to 8192, 32 / 8 heads: 94 us; 8 warps 103).
   static constexpr int W = D == 64 && NQ <= 8 ? 12 : 8;
   static constexpr int TB = i4::tile_bytes(D);
   static constexpr int STAGE = 4 * TB;  // K and V of two blocks
@@ -927,7 +934,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
       n = deal.cta_of(pieces[mine].seg + pieces[mine].nb - 1) - ca + 1;
     }
   }
-  __syncthreads();
+  __syncthreads();  // (the CTA's slots: released with the counts below)
   if (tid < 2) {
     if (mine >= 0 && atom_add_acq_rel_gpu(a.count + ca, 1) == n - 1) {
       st_relaxed_gpu(a.count + ca, 0);
