@@ -18,9 +18,9 @@
 // Where all sequences are short the CTAs' ranges end at whole (sequence, kv
 // head)s, so that there is nothing to join between them (kWhole).
 //
-// Codes as operands.  A code of 4 bits in the lowest bits of an fp16 number is
-// the subnormal n 2^-24, exactly; in the next four it is 16 n 2^-24.  So a word
-// of 8 codes becomes four operand registers by a shift and four masks, and the
+// Codes as operands.  A code of 4 bits in bits 2..5 of an fp16 number is the
+// subnormal n 2^-22, exactly; in bits 6..9 it is n 2^-18.  So a word of 8 codes
+// becomes four operand registers by two shifts and four masks, and the
 // powers of two are taken out of the queries (scores) and of the results
 // (outputs).  The queries are used in fp16, scaled by a power of two so that
 // their largest is in [1, 2): exact for bf16 and fp16 down to 2^-10 of the
@@ -30,11 +30,11 @@
 // heads per kv head the columns of queries 4..7 take the lo halves, with more
 // there is a product for each half.
 //
-// Bounded by instructions: a block of a kv head takes a warp about 320 (codes to
-// operands 90, products 16, weights and scales 130, fetching 30), and the SMs
+// Bounded by instructions: a block of a kv head takes a warp about 335 (codes to
+// operands 105, products 16, weights and scales 130, fetching 30), and the SMs
 // issue every second cycle with the two warps a scheduler that the registers
-// allow.  32 sequences of 8192, 32 / 8 heads of 128: 66.4 us, 4.6 TB/s; 128
-// sequences of 1024 to 8192, 40 heads: 145 us.  The smallest call takes 7.5 us:
+// allow.  32 sequences of 8192, 32 / 8 heads of 128: 68.5 us, 4.4 TB/s; 128
+// sequences of 1024 to 8192, 40 heads: 152 us.  The smallest call takes 7.5 us:
 // lengths, tables and blocks one after the other from memory, launch, outputs.
 //
 // The sums of the tensor cores round towards zero, so they run over one stage
@@ -92,6 +92,16 @@ struct Cfg {
   static constexpr int SMEM = OFF_O + 2 * W * NQ * D * 4;      // [2 W][g][D]
   static constexpr int NG = D / 64;
 };
+
+// A word's bytes 0 and 2 (odd: 1 and 3) with their codes where the masks are:
+// even dims n 2^-22, odd dims n 2^-18.  (The tensor cores lose what lies far
+// below an operand's exponent, and a subnormal's counts as 2^-14.  Codes in bits
+// 0..3 and 4..7 need a shift a word less and are 2 to 5% faster, but the outputs'
+// errors, against 64 bits, are then 2.3e-6 to 2.8e-6 instead of 4.6e-7 to 8.7e-7;
+// all codes in bits 6..9: 3.9e-7 to 7.4e-7, 5% slower.)
+constexpr uint32_t kLowCodes = 0x003C003Cu, kHighCodes = 0x03C003C0u;
+constexpr int kCodeExp = 22;
+__device__ __forceinline__ uint32_t place(uint32_t w, int odd) { return odd ? w >> 6 : w << 2; }
 
 __device__ __forceinline__ uint32_t lds32(const uint8_t *a) { return *reinterpret_cast<const uint32_t *>(a); }
 __device__ __forceinline__ uint2 lds64(const uint8_t *a) { return *reinterpret_cast<const uint2 *>(a); }
@@ -535,7 +545,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
           qf[r][p * 4 + 2 * w + 1][0] = pack_f16x2(x[2] * down, x[6] * down);
           qf[r][p * 4 + 2 * w + 1][1] = pack_f16x2(x[3] * (down * 0.0625f), x[7] * (down * 0.0625f));
         }
-      const float cq = a.qscale * __uint_as_float(static_cast<uint32_t>(127 + 24 + e) << 23);
+      const float cq = a.qscale * __uint_as_float(static_cast<uint32_t>(127 + kCodeExp + e) << 23);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         cs_[r][c] = __shfl_sync(0xffffffffu, cq, 8 * t + 4 * c);
@@ -602,8 +612,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
           const uint2 k0 = lds64(kt + (kat ^ (32 * p))), k8 = lds64(kt + (kat ^ (32 * p)) + ROW8);
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
-            const uint32_t u = (h < 2 ? k0.x : k0.y) >> (h & 1 ? 8 : 0), v = (h < 2 ? k8.x : k8.y) >> (h & 1 ? 8 : 0);
-            const uint32_t a0 = u & 0x000F000Fu, a1 = v & 0x000F000Fu, a2 = u & 0x00F000F0u, a3 = v & 0x00F000F0u;
+            const uint32_t u = place(h < 2 ? k0.x : k0.y, h & 1), v = place(h < 2 ? k8.x : k8.y, h & 1);
+            const uint32_t a0 = u & kLowCodes, a1 = v & kLowCodes, a2 = u & kHighCodes, a3 = v & kHighCodes;
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
               if (h == 0)
@@ -748,12 +758,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
           const uint32_t w2 = lds32(vt + (vat0 ^ (32 * p)) + ROW8), w3 = lds32(vt + (vat1 ^ (32 * p)) + ROW8);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            uint32_t b0 = __byte_perm(w0, w1, h ? 0x7632 : 0x5410);
-            uint32_t b1 = __byte_perm(w2, w3, h ? 0x7632 : 0x5410);
+            const uint32_t b0 = __byte_perm(w0, w1, h ? 0x7632 : 0x5410);
+            const uint32_t b1 = __byte_perm(w2, w3, h ? 0x7632 : 0x5410);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const uint32_t v0 = b0 & 0x000F000Fu, v1 = b0 & 0x00F000F0u;
-              const uint32_t v2 = ~b1 & 0x000F000Fu, v3 = ~b1 & 0x00F000F0u;
+              const uint32_t c0 = place(b0, j), c1 = place(b1, j);
+              const uint32_t v0 = c0 & kLowCodes, v1 = c0 & kHighCodes, v2 = ~c1 & kLowCodes, v3 = ~c1 & kHighCodes;
 #pragma unroll
               for (int r = 0; r < NR; ++r) {
                 if (tt == 0)
@@ -762,8 +772,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
                   mma(acc[r][p][2 * h + j], v0, v1, v2, v3, hi[r][p][0], hi[r][p][1]);
                 if constexpr (NQ != 4) mma(acc[r][p][2 * h + j], v0, v1, v2, v3, lo[r][p][0], lo[r][p][1]);
               }
-              b0 >>= 8;
-              b1 >>= 8;
             }
           }
         }
@@ -818,8 +826,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
               e += __shfl_xor_sync(0xffffffffu, e, 2);
               f += __shfl_xor_sync(0xffffffffu, f, 2);
             }
-            o[2 * j] = fmaf(e, 16777216.f, z[p]) * inv;
-            o[2 * j + 1] = fmaf(f, 1048576.f, z[p]) * inv;
+            o[2 * j] = fmaf(e, static_cast<float>(1 << kCodeExp), z[p]) * inv;
+            o[2 * j + 1] = fmaf(f, static_cast<float>(1 << (kCodeExp - 4)), z[p]) * inv;
           }
           if (has) {
             float4 *to = reinterpret_cast<float4 *>(dst + query * D + 64 * p + 8 * gq);
