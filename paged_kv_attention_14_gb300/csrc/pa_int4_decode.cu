@@ -30,7 +30,7 @@
 // heads per kv head the columns of queries 4..7 take the lo halves, with more
 // there is a product for each half.
 //
-// Bounded by instructions: a block of a kv head takes a warp about 335 (codes to
+// Bounded by instructions: a block of a kv head takes a warp about 330 (codes to
 // operands 105, products 16, weights and scales 130, fetching 30), and the SMs
 // issue every second cycle with the two warps a scheduler that the registers
 // allow.  32 sequences of 8192, 32 / 8 heads of 128: 68.5 us, 4.4 TB/s; 128
