@@ -94,7 +94,7 @@ struct Cfg {
                        V_EMPTY = V_FULL + NSV, V_OK = V_EMPTY + NSV, S_FULL = V_OK + NSV, P_FULL = S_FULL + NQT,
                        P_REST = P_FULL + NQT, O_FULL = P_REST + NQT, NOTED = O_FULL + NQT, I_FULL = NOTED + 2,
                        I_EMPTY = I_FULL + kAhead, DRAIN = I_EMPTY + kAhead, NBAR = DRAIN + 1;
-  static_assert(NBAR * 8 + 32 <= 384 && SMEM <= (NQT == 2 ? 232448 : 115 * 1024), "shared memory");
+  static_assert(NBAR * 8 + 36 <= 384 && SMEM <= (NQT == 2 ? 232448 : 115 * 1024), "shared memory");
 };
 
 template <bool F16>
@@ -232,8 +232,8 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + C::NBAR);
   volatile int *s_abort = reinterpret_cast<int *>(tmem_slot + 1);
-  int *s_noted = reinterpret_cast<int *>(tmem_slot + 2);  // [2]
-  int *s_last = reinterpret_cast<int *>(tmem_slot + 4);   // K and V tiles and Qs whose copies were issued
+  int *s_noted = reinterpret_cast<int *>(tmem_slot + 2);  // [2][2]: of each of the warps that look over V
+  int *s_last = reinterpret_cast<int *>(tmem_slot + 6);   // K and V tiles and Qs whose copies were issued
   uint32_t *notes = reinterpret_cast<uint32_t *>(smem + C::OFF_NOTE);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
     }
     mbar_init(&bar[C::DRAIN], 1);
     *s_abort = 0;
-    s_noted[0] = s_noted[1] = 0;
+    for (int i = 0; i < 4; ++i) s_noted[i] = 0;
     s_last[0] = s_last[1] = s_last[2] = 0;
     fence_mbar_init();
   }
@@ -458,23 +458,29 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
       }
     } else {
       // ------------------------------------------------- V tiles looked over
-      const int ct = tid - 64;
+      // Warp 2 has rows 0..31 and 64..95 of a tile, warp 3 the others: each
+      // has words of its own in a tile's mask (w, w + 2) and a flag of its own,
+      // and so never waits for the other, which may be tiles ahead of it or
+      // have given up.
+      const int ct = tid - 64, w = warp - 2;
       int nv = 0;
       while (ok && next_item()) {
         const int buf = (n_items - 1) & 1;
         uint32_t *note = notes + buf * kNoted * 4;
-        // the notes of the item before the last are read
+        volatile int *noted = &s_noted[2 * buf + w];
+        // the notes of the item before the last are read: this warp's are cleared
         if (n_items > 2) {
           if (!mbar_wait(&bar[C::NOTED + buf], (((n_items - 1) >> 1) - 1) & 1, a.wait_ns)) {
             ok = false;
             break;
           }
-          if (*reinterpret_cast<volatile int *>(&s_noted[buf])) {
-            named_bar_sync(1, 64);  // both warps have seen it
-            for (int x = ct; x < kNoted * 4; x += 64) note[x] = 0;
-            s_noted[buf] = 0;
-            named_bar_sync(1, 64);
+          const bool used = *noted != 0;  // (set by lanes of this warp)
+          __syncwarp();
+          if (used) {
+            for (int x = lane; x < kNoted; x += 32) note[x * 4 + w] = note[x * 4 + w + 2] = 0;
+            if (lane == 0) *noted = 0;
           }
+          __syncwarp();
         }
         int e = 0;  // partly seen tiles so far
         for (int jj = 0; jj < it.n_iter; ++jj, ++nv) {
@@ -507,7 +513,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
                       make_uint4(0, 0, 0, 0);
                 if (!drop) {
                   if (e < kNoted) atomicOr(&note[e * 4 + (r >> 5)], 1u << (r & 31));
-                  *reinterpret_cast<volatile int *>(&s_noted[buf]) = 1;
+                  *noted = 1;
                 }
               }
             }
@@ -640,7 +646,8 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
         const int left = min(a.rt, it.p1 + 1 - (it.p0 + t * a.rt)) * a.g;  // rows in use
         const int head = it.head * a.g + sub;
         if (r < left && a.lse) a.lse[static_cast<int64_t>(tok0 + tok) * a.hq + head] = lse2 * kLn2;
-        if (*reinterpret_cast<volatile int *>(&s_noted[buf]) != 0) {
+        volatile int *noted = &s_noted[2 * buf];
+        if ((noted[0] | noted[1]) != 0) {
           store_noted<D, F16>(a, notes + buf * kNoted * 4, it, pos, head, first, r < left, inv, lse2,
                               trow + C::O_COL + t * D);
         } else {
