@@ -683,6 +683,11 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
             __syncwarp();
           }
         }
+      } else if (n_items > 2 && !mbar_wait(&bar[C::NOTED + buf], (((n_items - 1) >> 1) - 1) & 1, a.wait_ns)) {
+        // (a tile without rows here could be items ahead of the other one, and
+        // would count twice for the notes that the other still reads)
+        ok = false;
+        break;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar[C::NOTED + buf]);

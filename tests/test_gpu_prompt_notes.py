@@ -72,3 +72,14 @@ def test_bad_rows_in_some_of_many_items(hq, hkv, d, rows, every):
     n = rows // (hq // hkv)
     lens = [n] * (304 if rows <= 128 else 152)  # four items of each CTA
     _check(lens, hq, hkv, d, _some(lens, hkv, d, every, seed=rows + every))
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(16, 4, 128), (8, 4, 64)])
+def test_bad_rows_in_items_of_one_tile_beside_items_of_two(hq, hkv, d):
+    # most items have rows in their first tile only, the second one's warps have
+    # nothing to do for several items on end
+    g = torch.Generator().manual_seed(d)
+    lens = torch.randint(1, 24, (900,), generator=g).tolist()
+    for s in range(0, 900, 90):
+        lens[s] = 150
+    _check(lens, hq, hkv, d, _some(lens, hkv, d, 2, seed=d), seed=1)
