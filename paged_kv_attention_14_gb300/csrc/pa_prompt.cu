@@ -105,6 +105,19 @@ template <bool F16>
 __device__ __forceinline__ float val(uint16_t x) {
   return F16 ? __half2float(__ushort_as_half(x)) : __uint_as_float(static_cast<uint32_t>(x) << 16);
 }
+// The signs' places of a pair of values: set where one is not finite (an
+// exponent of all ones carries into the sign's place).
+template <bool F16>
+__device__ __forceinline__ uint32_t exponents_full(const uint4 &x) {
+  const uint32_t m = F16 ? 0x7C007C00u : 0x7F807F80u, one = F16 ? 0x04000400u : 0x00800080u;
+  return ((x.x & m) + one) | ((x.y & m) + one) | ((x.z & m) + one) | ((x.w & m) + one);
+}
+// x + a . b of two pairs
+template <bool F16>
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float x) {
+  x = fmaf(val<F16>(static_cast<uint16_t>(a)), val<F16>(static_cast<uint16_t>(b)), x);
+  return fmaf(val<F16>(static_cast<uint16_t>(a >> 16)), val<F16>(static_cast<uint16_t>(b >> 16)), x);
+}
 
 // An item.
 struct Item {
@@ -177,48 +190,87 @@ __device__ __forceinline__ void set_registers_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
 }
 
+// Whether a row of D values (16-byte aligned) has one that is not finite.
+template <int D, bool F16>
+__device__ __forceinline__ bool not_finite(const uint16_t *row) {
+  const uint4 *x = reinterpret_cast<const uint4 *>(row);
+  uint32_t bad = 0;
+#pragma unroll 4
+  for (int c = 0; c < D / 8; ++c) bad |= exponents_full<F16>(__ldg(x + c));
+  return (bad & 0x80008000u) != 0;
+}
+
 // The outputs of a row (a lane of tensor memory, live or not; the whole warp
 // calls it) of an item with noted V rows: the products' sums, and the noted rows
-// that its query sees.
+// that its query sees.  Partly seen tiles past the first kNoted are looked
+// over here, a row a lane: a chunk of 2^20 keys then takes some 10 ms, far from the
+// limit of the waits for this warp, and so does one whose rows are all noted.
 template <int D, bool F16>
 __device__ __noinline__ void store_noted(const Args &a, const uint32_t *notes, const Item &it, int pos, int head,
                                          int first, bool live, float inv, float lse2, uint32_t o_at) {
-  const uint16_t *q = a.q + static_cast<int64_t>(it.start + pos) * a.q_stride + head * D;
+  const int lane = threadIdx.x & 31;
+  const uint4 *q = reinterpret_cast<const uint4 *>(a.q + static_cast<int64_t>(it.start + pos) * a.q_stride + head * D);
   uint8_t *out = static_cast<uint8_t *>(a.out) + (static_cast<int64_t>(it.start + pos) * a.hq + head) * (D * 2);
 #pragma unroll 1
-  for (int c0 = 0; c0 < D; c0 += 32) {
-    float o[32];
-    tmem_ld32(o_at + c0, o);
+  for (int c0 = 0; c0 < D; c0 += 64) {
+    float o[2][32];
+    tmem_ld32(o_at + c0, o[0]);
+    tmem_ld32(o_at + c0 + 32, o[1]);
 #pragma unroll
-    for (int x = 0; x < 32; ++x) o[x] *= inv;
+    for (int x = 0; x < 64; ++x) o[x >> 5][x & 31] *= inv;
     int e = 0;
+#pragma unroll 1
     for (int jj = 0; jj < it.n_iter; ++jj) {
       const int k0 = (it.j0 + jj) * KT;
       if (k0 >= it.all_lo && k0 + KT <= it.all_hi) continue;
-      for (int i = 0; i < KT; ++i) {
-        const int key = k0 + i;
-        if (!live || key < first || key > pos) continue;
-        if (e < kNoted && !(notes[e * 4 + (i >> 5)] >> (i & 31) & 1u)) continue;
-        const uint16_t *k = a.k + static_cast<int64_t>(it.start + key) * a.k_stride + it.head * D;
-        const uint16_t *v = a.v + static_cast<int64_t>(it.start + key) * a.v_stride + it.head * D;
-        bool noted = false;
-        float x = 0.f;
-        for (int d = 0; d < D; ++d) {
-          noted |= !(fabsf(val<F16>(v[d])) <= 3.4e38f);
-          x = fmaf(val<F16>(q[d]), val<F16>(k[d]), x);
+#pragma unroll 1
+      for (int w = 0; w < KT; w += 32) {
+        uint32_t bad;
+        if (e < kNoted) {
+          bad = notes[e * 4 + (w >> 5)];
+        } else {
+          const int key = k0 + w + lane;
+          bad = __ballot_sync(0xffffffffu, key <= it.p1 && not_finite<D, F16>(a.v + static_cast<int64_t>(it.start + key) *
+                                                                                       a.v_stride + it.head * D));
         }
-        if (!noted) continue;
-        const float p = exp2f(x * a.scale2 - lse2);
+#pragma unroll 1
+        for (; bad; bad &= bad - 1) {
+          const int key = k0 + w + __ffs(bad) - 1;
+          if (!live || key < first || key > pos) continue;
+          const uint4 *k =
+              reinterpret_cast<const uint4 *>(a.k + static_cast<int64_t>(it.start + key) * a.k_stride + it.head * D);
+          const uint4 *v = reinterpret_cast<const uint4 *>(a.v + static_cast<int64_t>(it.start + key) * a.v_stride +
+                                                           it.head * D + c0);
+          float x = 0.f;
+#pragma unroll 2
+          for (int d = 0; d < D / 8; ++d) {
+            const uint4 qd = __ldg(q + d), kd = __ldg(k + d);
+            x = dot2<F16>(qd.x, kd.x, x);
+            x = dot2<F16>(qd.y, kd.y, x);
+            x = dot2<F16>(qd.z, kd.z, x);
+            x = dot2<F16>(qd.w, kd.w, x);
+          }
+          const float p = exp2f(x * a.scale2 - lse2);
 #pragma unroll
-        for (int d = 0; d < 32; ++d) o[d] = fmaf(p, val<F16>(v[c0 + d]), o[d]);
+          for (int d = 0; d < 8; ++d) {
+            const uint4 vd = __ldg(v + d);
+            const uint32_t u[4] = {vd.x, vd.y, vd.z, vd.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float *y = &o[d >> 2][(d & 3) * 8 + 2 * i];
+              y[0] = fmaf(p, val<F16>(static_cast<uint16_t>(u[i])), y[0]);
+              y[1] = fmaf(p, val<F16>(static_cast<uint16_t>(u[i] >> 16)), y[1]);
+            }
+          }
+        }
       }
       ++e;
     }
     __syncwarp();
     if (live)
 #pragma unroll
-      for (int x = 0; x < 32; x += 2)
-        *reinterpret_cast<uint32_t *>(out + (c0 + x) * 2) = pack2<F16>(o[x], o[x + 1]);
+      for (int x = 0; x < 64; x += 2)
+        *reinterpret_cast<uint32_t *>(out + (c0 + x) * 2) = pack2<F16>(o[x >> 5][x & 31], o[x >> 5][(x & 31) + 1]);
   }
 }
 
@@ -500,9 +552,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
                 for (int c = 0; c < D / 8; ++c) {
                   const uint4 x =
                       *reinterpret_cast<const uint4 *>(vt + (c >> 3) * C::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-                  // an exponent of all ones carries into the sign's place
-                  const uint32_t m = F16 ? 0x7C007C00u : 0x7F807F80u, one = F16 ? 0x04000400u : 0x00800080u;
-                  bad |= ((x.x & m) + one) | ((x.y & m) + one) | ((x.z & m) + one) | ((x.w & m) + one);
+                  bad |= exponents_full<F16>(x);
                 }
                 bad &= 0x80008000u;
               }

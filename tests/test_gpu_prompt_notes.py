@@ -83,3 +83,41 @@ def test_bad_rows_in_items_of_one_tile_beside_items_of_two(hq, hkv, d):
     for s in range(0, 900, 90):
         lens[s] = 150
     _check(lens, hq, hkv, d, _some(lens, hkv, d, 2, seed=d), seed=1)
+
+
+def _far(chunk, hkv, d, where):
+    """A bad value in each of the tiles `where` (by number) of the first chunk, and one in the second chunk."""
+    return [(128 * t + 5 + 3 * i, i % hkv, (7 * i) % d, float("nan")) for i, t in enumerate(where)] + [(chunk + 9, 0, 1, float("inf"))]
+
+
+@pytest.mark.parametrize("act,hq,hkv,d", [(torch.bfloat16, 8, 2, 128), (torch.float16, 4, 4, 64)])
+def test_bad_rows_in_more_partly_seen_tiles_than_have_masks(act, hq, hkv, d):
+    # the item over the chunks' boundary sees all 41 tiles of the first chunk in part
+    chunk = 40 * 128 + 20
+    _check([3 * 128, chunk + 200], hq, hkv, d,
+           [(384 + t, *rest) for t, *rest in _far(chunk, hkv, d, (0, 31, 33, 40))], act=act, times=2, seed=2,
+           attention_chunk=chunk)
+
+
+@pytest.mark.parametrize("every", [1, 1000])
+def test_a_long_chunk_with_bad_rows_is_within_the_waits_limit(every):
+    # 4 heads of 32768 keys behind the masks; every row of v bad, or a few
+    hq, hkv, d, chunk = 4, 1, 128, 32768 + 100
+    T = chunk + 60
+    q, k, v, starts = _rows([T], hq, hkv, d, torch.bfloat16, 3)
+    v[::every, :, ::2] = v[chunk, :, ::2] = float("nan")
+    out = torch.zeros((T, hq, d), dtype=torch.bfloat16, device=DEV)
+    word = torch.zeros(1, dtype=torch.int32, device=DEV)
+    desc = pa.make_desc(0, hkv, hq, d, attention_chunk=chunk, error_word=word)
+    pa.pa_prompt_attention(desc, out, q, k, v, starts, T, 1 / math.sqrt(d))
+    assert int(word) == 0
+    assert out[:, :, ::2].isnan().all() and torch.isfinite(out[:, :, 1::2]).all()
+    rows = torch.tensor([chunk - 70, chunk - 1, chunk, T - 1], device=DEV)
+    for h in range(hq):
+        x = q[rows, h].double() @ k[:, 0].double().T / math.sqrt(d)
+        j = torch.arange(T, device=DEV)
+        x = x.masked_fill((j > rows[:, None]) | (j < rows[:, None] // chunk * chunk), -math.inf)
+        p, vv = torch.softmax(x, -1), v[:, 0, 1::2].double()
+        o, size = p @ vv, p @ vv.abs()
+        tol = U[torch.bfloat16] * (size + o.abs()) + 2.0 ** -15 * size
+        assert ((out[rows, h, 1::2].double() - o).abs() <= tol).all()
