@@ -351,13 +351,16 @@ PA_API pa_status pa_rope_cache_write(const pa_kv_desc *desc, const pa_rope_desc 
 /*
  * Bytes of scratch that pa_decode needs for num_seqs sequences on the current
  * device.  Zero-fill the workspace once before its first use; it may then be
- * reused by consecutive calls on one stream (each call that completes without
- * error leaves its error word and its merge counters at zero again; the rest
- * holds the last call's partial results).  Calls that overlap on the GPU need
- * separate workspaces.  After a call completes, the first int32 of the
- * workspace holds the PA_DEVERR_* bits it reported; if it is not zero, the
- * merge counters may be left behind too: zero-fill the whole workspace again
- * before its next use.
+ * reused by consecutive calls on one stream: pa_decode, pa_decode_append,
+ * pa_mixed_attention and pa_mixed_attention_append, with any number of
+ * sequences and any cache type, as long as the descriptors have the same
+ * heads and head_dim and the workspace is as large as each call asks.  (Each
+ * call that completes without error leaves its error word and its merge
+ * counters at zero again; the rest holds the last call's partial results.)
+ * Calls that overlap on the GPU need separate workspaces.  After a call
+ * completes, the first int32 of the workspace holds the PA_DEVERR_* bits it
+ * reported; if it is not zero, the merge counters may be left behind too:
+ * zero-fill the whole workspace again before its next use.
  */
 PA_API size_t pa_decode_workspace_size(const pa_kv_desc *desc, int32_t num_seqs, int32_t max_context_len);
 

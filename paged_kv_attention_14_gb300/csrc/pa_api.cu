@@ -451,7 +451,7 @@ size_t pa_mixed_workspace_size(const pa_kv_desc *desc, int32_t num_dec_seqs, int
     fail(PA_ERR_UNSUPPORTED, "%s", why);
     return 0;
   }
-  return pa::mixed_plan(*desc, num_dec_seqs, plan).workspace_bytes;
+  return pa::mixed_plan(plan).workspace_bytes;
 }
 
 namespace {
@@ -497,7 +497,7 @@ pa_status mixed_call(const pa_kv_desc *desc, float *dec_out, float *dec_lse, con
     }
     if (!has_pf) num_new_rows = num_dec_seqs;
   }
-  plan = pa::mixed_plan(*desc, num_dec_seqs, plan);
+  plan = pa::mixed_plan(plan);
   if (!workspace || !aligned16(workspace))
     return fail(PA_ERR_WORKSPACE, "workspace must be non-NULL and 16-byte aligned%s");
   if (workspace_bytes < plan.workspace_bytes)

@@ -143,20 +143,29 @@ pa_status plan_decode(const pa_kv_desc &d, int32_t num_seqs, DecodePlan *plan, c
     return PA_ERR_UNSUPPORTED;
   }
   const KernelInfo k = kernel_for(d, impl);
-  const int occ = prepare_kernel(k.fn, k.threads, k.smem);
+  int occ = prepare_kernel(k.fn, k.threads, k.smem);
   if (occ < 1) {
     *why = "the decode kernel does not fit on this device";
     return PA_ERR_CUDA;
   }
+  const int most = decode_slot_rows(g, d.head_dim) / k.slot_heads;  // (measured: at least the occupancy)
+  occ = occ < most ? occ : most;
   plan->impl = impl;
   plan->slot_heads = k.slot_heads;
   plan->num_groups = d.num_kv_heads / k.hg;
   plan->num_ctas = device_info().sm_count * occ;
-  plan->workspace_bytes =
-      dec::ws_layout(num_seqs, plan->num_groups, plan->num_ctas, k.slot_heads, d.head_dim).total;
-  // the error word's 256 bytes, then one counter per sequence and kv head at most
-  plan->zero_bytes = 256 + sizeof(int32_t) * static_cast<size_t>(num_seqs) * d.num_kv_heads;
+  plan->slots = kWsSlots;
+  plan->counters = kWsSlots + decode_slot_region(device_info().sm_count, g, d.head_dim);
+  plan->workspace_bytes = plan->counters + dec::counter_bytes(num_seqs, plan->num_groups);
+  plan->zero_bytes = 0;
   return PA_OK;
+}
+
+void pack_static_plan(const pa_kv_desc &d, int32_t num_seqs, DecodePlan *plan) {
+  if (d.kv_dtype == PA_KV_INT4 || d.kv_dtype == PA_KV_INT4_F16) return;  // (no counters behind its slots)
+  plan->counters = 256;
+  plan->slots = plan->zero_bytes = plan->counters + dec::counter_bytes(num_seqs, plan->num_groups);
+  plan->workspace_bytes = plan->slots + dec::slot_bytes(plan->num_ctas, plan->slot_heads, d.head_dim);
 }
 
 namespace dec {
@@ -166,7 +175,6 @@ bool make_decode_args(const pa_kv_desc &d, const DecodePlan &plan, float *out, f
                       int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs, float scale,
                       void *workspace, DecodeArgs *ap) {
   const KernelInfo k = kernel_for(d, plan.impl);
-  const dec::WsLayout w = dec::ws_layout(num_seqs, plan.num_groups, plan.num_ctas, plan.slot_heads, d.head_dim);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   DecodeArgs &a = *ap;
   memset(&a, 0, sizeof a);
@@ -202,9 +210,9 @@ bool make_decode_args(const pa_kv_desc &d, const DecodePlan &plan, float *out, f
   const TestHooks hooks = test_hooks();
   a.stall = hooks.stall;
   a.wait_ns = hooks.wait_ns;
-  a.seg_counter = reinterpret_cast<int32_t *>(ws + w.counter_off);
-  a.slot_lse = reinterpret_cast<float *>(ws + w.slot_lse_off);
-  a.slot_o = reinterpret_cast<float *>(ws + w.slot_o_off);
+  a.seg_counter = reinterpret_cast<int32_t *>(ws + plan.counters);
+  a.slot_lse = reinterpret_cast<float *>(ws + plan.slots);
+  a.slot_o = reinterpret_cast<float *>(ws + plan.slots + slot_lse_bytes(plan.num_ctas, plan.slot_heads));
   return true;
 }
 

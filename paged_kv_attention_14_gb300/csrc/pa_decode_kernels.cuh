@@ -167,21 +167,15 @@ __device__ __forceinline__ int seq_len(const DecodeArgs &a, int s) {
 
 constexpr size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Workspace: [0, 4) error word, then the merge counters (one per segment;
-// every merge resets its counter, so they stay zero between launches), slot
-// lse and slot outputs.
-struct WsLayout {
-  size_t counter_off, slot_lse_off, slot_o_off, total;
-};
-
+// The merge counters (one per segment; every merge resets its counter, so they
+// stay zero between launches), and the slots: lse, then outputs.
+inline size_t counter_bytes(int num_seqs, int num_groups) {
+  return align256(sizeof(int32_t) * size_t(num_seqs) * num_groups);
+}
 // slot_heads: query heads of one slot (kv heads per group x padded group size)
-inline WsLayout ws_layout(int num_seqs, int num_groups, int grid, int slot_heads, int d) {
-  WsLayout w;
-  w.counter_off = 256;
-  w.slot_lse_off = w.counter_off + align256(sizeof(int32_t) * size_t(num_seqs) * num_groups);
-  w.slot_o_off = w.slot_lse_off + align256(sizeof(float) * size_t(grid) * 2 * slot_heads);
-  w.total = w.slot_o_off + align256(sizeof(float) * size_t(grid) * 2 * slot_heads * d);
-  return w;
+inline size_t slot_lse_bytes(int grid, int slot_heads) { return align256(sizeof(float) * size_t(grid) * 2 * slot_heads); }
+inline size_t slot_bytes(int grid, int slot_heads, int d) {
+  return slot_lse_bytes(grid, slot_heads) + align256(sizeof(float) * size_t(grid) * 2 * slot_heads * d);
 }
 
 // Output of an empty sequence: zeros and lse = -inf.

@@ -75,6 +75,7 @@ PA_API pa_status pa_decode_static(const pa_kv_desc *desc, float *out, float *lse
     pa::set_last_error("");
     return PA_OK;
   }
+  pa::pack_static_plan(*desc, num_seqs, &plan);
   if (plan.workspace_bytes > kStaticScratchBytes)
     return static_fail(PA_ERR_WORKSPACE,
                        "this batch needs more decode scratch than the 8 MiB static array; use pa_decode");
@@ -83,9 +84,8 @@ PA_API pa_status pa_decode_static(const pa_kv_desc *desc, float *out, float *lse
   if (e != cudaSuccess) return static_fail(PA_ERR_CUDA, cudaGetErrorString(e));
   // The array keeps the previous call's contents: its error word and merge
   // counters must start at zero, the rest is rewritten by every launch.
-  const size_t head = plan.zero_bytes;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  e = cudaMemsetAsync(scratch, 0, head < plan.workspace_bytes ? head : plan.workspace_bytes, s);
+  e = cudaMemsetAsync(scratch, 0, plan.zero_bytes, s);
   if (e != cudaSuccess) return static_fail(PA_ERR_CUDA, cudaGetErrorString(e));
   e = pa::launch_decode(*desc, plan, out, lse, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
                         num_seqs, scale, scratch, s);

@@ -1019,15 +1019,15 @@ Kernel kernel_of(const pa_kv_desc &d) {
   return d.head_dim == 128 ? kernel_of_dim<128>(g) : kernel_of_dim<64>(g);
 }
 
+// Of the workspace: the slots' statistics, their dims, and the end.
 struct Layout {
-  size_t count, ml, o, total;
+  size_t ml, o, total;
 };
 
 Layout layout(int ctas, int g, int d) {
   const size_t slots = 2 * static_cast<size_t>(ctas);
   Layout w;
-  w.count = 256;
-  w.ml = (w.count + ctas * sizeof(int32_t) + 255) / 256 * 256;
+  w.ml = kWsSlots;
   w.o = (w.ml + slots * g * sizeof(float2) + 255) / 256 * 256;
   w.total = w.o + slots * g * d * sizeof(float);
   return w;
@@ -1050,9 +1050,15 @@ pa_status plan_int4_decode(const pa_kv_desc &d, DecodePlan *plan, const char **w
   plan->slot_heads = d.num_q_heads / d.num_kv_heads;
   plan->num_groups = d.num_kv_heads;
   plan->num_ctas = device_sm_count();
+  if (kWsCtaCounters + plan->num_ctas * sizeof(int32_t) > kWsSlots) {
+    *why = "more SMs than the workspace has counters for";
+    return PA_ERR_UNSUPPORTED;
+  }
   const Layout w = layout(plan->num_ctas, plan->slot_heads, d.head_dim);
+  plan->slots = w.ml;
+  plan->counters = kWsCtaCounters;
   plan->workspace_bytes = w.total;
-  plan->zero_bytes = w.ml;
+  plan->zero_bytes = kWsCtaCounters + plan->num_ctas * sizeof(int32_t);
   return PA_OK;
 }
 
@@ -1084,7 +1090,7 @@ cudaError_t launch_int4_decode(const pa_kv_desc &d, const DecodePlan &plan, floa
   a.checked = d.check_indices;
   a.num_blocks = d.num_blocks;
   a.f16 = d.kv_dtype == PA_KV_INT4_F16;
-  a.count = reinterpret_cast<int32_t *>(ws + w.count);
+  a.count = reinterpret_cast<int32_t *>(ws + plan.counters);
   a.slot_ml = reinterpret_cast<float2 *>(ws + w.ml);
   a.slot_o = reinterpret_cast<float *>(ws + w.o);
   // programmatic dependent launch: it waits for the preceding kernel's writes

@@ -45,9 +45,32 @@ struct DecodePlan {
   int slot_heads;  // query heads per partial-result slot of the kernel
   int num_groups;  // kv head groups per sequence (segments per sequence)
   int num_ctas;    // persistent grid size
+  size_t slots, counters;  // where the workspace's partial results and its counters per segment begin
   size_t workspace_bytes;
-  size_t zero_bytes;  // of its start, which must be zero before a call (error word, counters)
+  size_t zero_bytes;  // pa_decode_static: of its scratch, zeroed before each call (error word, counters)
 };
+
+// A decode workspace.  What has to be zero between calls lies where no call
+// that may share the workspace keeps anything else, whatever its number of
+// sequences and its cache type:
+//   [0, 256)             the error word, the mixed step's work counters
+//   [256, kWsSlots)      the 4-bit decode's counters, one per CTA
+//   [kWsSlots, +region)  partial results (anything): room for every decode
+//                        kernel of this group size
+//   behind it            the other kernels' counters, one per segment
+constexpr size_t kWsCtaCounters = 256, kWsSlots = 4096;
+// query heads of a slot: the group size padded
+inline int decode_padded_group(int g) { return g <= 4 ? 4 : g <= 8 ? 8 : 16; }
+// Query heads of a CTA's slots x CTAs an SM, at most.
+inline int decode_slot_rows(int g, int head_dim) { return decode_padded_group(g) * 256 / head_dim; }
+// Two slots of so many rows of head_dim floats per SM, with two floats a row (its
+// statistics) beside them.
+inline size_t decode_slot_region(int sms, int g, int head_dim) {
+  return (static_cast<size_t>(sms) * 2 * decode_slot_rows(g, head_dim) * (head_dim + 2) * sizeof(float) + 511) / 256 * 256;
+}
+// The plan of a decode on scratch that is zeroed before each call: counters
+// first, no room for other kernels.
+void pack_static_plan(const pa_kv_desc &d, int32_t num_seqs, DecodePlan *plan);
 
 pa_status plan_int4_decode(const pa_kv_desc &d, DecodePlan *plan, const char **why);
 cudaError_t launch_int4_decode(const pa_kv_desc &d, const DecodePlan &plan, float *out, float *lse, const void *q,
@@ -101,7 +124,7 @@ pa_status validate_prefill(const pa_kv_desc *desc, const float *out, const float
 pa_status check_mixed(const pa_kv_desc &d, const DecodePlan &plan, const char **why);
 // The decode part's plan in the single-launch step (more partitions than SMs)
 // from pa_decode's plan for the same batch.
-DecodePlan mixed_plan(const pa_kv_desc &d, int32_t num_dec_seqs, const DecodePlan &plan);
+DecodePlan mixed_plan(const DecodePlan &plan);
 cudaError_t launch_mixed(const pa_kv_desc &d, const DecodePlan &plan, float *dec_out, float *dec_lse,
                          const void *dec_q, const int32_t *dec_block_tables, int32_t dec_max_blocks,
                          const int32_t *dec_context_lens, int32_t num_dec_seqs, float *pf_out, float *pf_lse,

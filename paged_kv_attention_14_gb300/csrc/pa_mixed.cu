@@ -166,11 +166,11 @@ extern "C" PA_API int pa_debug_mixed_trace_clear() {
 // extra merges grew the total and the step got slower (141 against 133 us
 // on workload 5's shapes); one it is.
 constexpr int kMixedDecodeSplit = 1;
+static_assert(kMixedDecodeSplit <= 2, "the workspace has room for two CTAs an SM of these kernels");
 
-DecodePlan mixed_plan(const pa_kv_desc &d, int32_t num_dec_seqs, const DecodePlan &plan) {
+DecodePlan mixed_plan(const DecodePlan &plan) {
   DecodePlan p = plan;
   p.num_ctas = plan.num_ctas * kMixedDecodeSplit;
-  p.workspace_bytes = dec::ws_layout(num_dec_seqs, p.num_groups, p.num_ctas, p.slot_heads, d.head_dim).total;
   return p;
 }
 
