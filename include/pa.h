@@ -472,9 +472,10 @@ PA_API pa_status pa_decode_append(const pa_kv_desc *desc, float *out, float *lse
  * Bytes of scratch that pa_prefill_chunk_balanced needs for num_seqs chunks
  * of at most max_q_len queries on the current device (0 if the descriptor is
  * invalid).  Same rules as pa_decode's workspace: zero-fill it once before
- * its first use; consecutive calls on one stream may reuse it (a call that
- * completes without error leaves its error word and its piece counters at
- * zero); calls that overlap on the GPU need separate workspaces.  After a
+ * its first use; consecutive calls on one stream may reuse it, whatever their
+ * chunks, with the same heads and head_dim (a call that completes without
+ * error leaves its error word and its piece counters at zero); calls that
+ * overlap on the GPU, and pa_decode's, need separate workspaces.  After a
  * call completes, its first int32 holds the PA_DEVERR_* bits the balanced
  * kernel reported; if it is not zero, zero-fill the whole workspace again
  * before its next use.

@@ -37,19 +37,20 @@ cudaError_t launch(const pa_kv_desc &d, float *out, float *lse, const void *q, c
 }
 
 // The balanced launch's workspace: the error word, then the items' piece
-// counters (one int32 per (pair, kv head)), then two slots per CTA: the
-// pieces' log-sum-exp and their normalised outputs.  Every part starts on a
-// 256-byte boundary.
+// counters (one int32 per (pair, kv head), with room for the most pairs that it
+// takes, so that no batch's slots lie where another one's counters do), then
+// two slots per CTA: the pieces' log-sum-exp and their normalised outputs.
+// Every part starts on a 256-byte boundary.
 struct SkLayout {
   size_t counters, lse, o, total;
 };
 
 inline size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
-inline SkLayout sk_layout(int head_dim, long long pairs, int num_kv_heads, int G) {
+inline SkLayout sk_layout(int head_dim, int num_kv_heads, int G) {
   SkLayout l;
   l.counters = 256;
-  l.lse = l.counters + round256(static_cast<size_t>(pairs) * num_kv_heads * sizeof(int32_t));
+  l.lse = l.counters + round256(static_cast<size_t>(kPrefillSkMaxPairs) * num_kv_heads * sizeof(int32_t));
   l.o = l.lse + round256(static_cast<size_t>(2) * G * MROWS * sizeof(float));
   l.total = l.o + static_cast<size_t>(2) * G * MROWS * head_dim * sizeof(float);
   return l;
@@ -67,7 +68,7 @@ cudaError_t launch_sk(const pa_kv_desc &d, float *out, float *lse, const void *q
   const int gx = (max_q_len + a.qt - 1) / a.qt;
   if (gx == 0 || num_seqs == 0) return cudaSuccess;
   const int G = device_sm_count();
-  const SkLayout l = sk_layout(D, static_cast<long long>(num_seqs) * gx, d.num_kv_heads, G);
+  const SkLayout l = sk_layout(D, d.num_kv_heads, G);
   uint8_t *w = static_cast<uint8_t *>(workspace);
   a.num_seqs = num_seqs;
   a.gx = gx;
@@ -127,7 +128,7 @@ bool prefill_sk_pays(const pa_kv_desc &d, int32_t num_seqs, int32_t max_q_len, i
 size_t prefill_sk_workspace_bytes(const pa_kv_desc &d, int32_t num_seqs, int32_t max_q_len) {
   // a batch that runs the plain grid needs the error word only
   if (!prefill_sk_applies(d, num_seqs, max_q_len)) return 256;
-  return pftc::sk_layout(d.head_dim, sk_pairs(d, num_seqs, max_q_len), d.num_kv_heads, device_sm_count()).total;
+  return pftc::sk_layout(d.head_dim, d.num_kv_heads, device_sm_count()).total;
 }
 
 cudaError_t launch_prefill_tc_sk(const pa_kv_desc &d, float *out, float *lse, const void *q,

@@ -3,7 +3,7 @@ gives the bits that it gives with a workspace of its own."""
 import pytest
 import torch
 
-from pa_helpers import desc_of, gpu_caches, gpu_decode
+from pa_helpers import desc_of, gpu_caches, gpu_decode, gpu_prefill, prefill_workspace
 from paged_kv_attention_14_gb300 import binding as B
 from paged_kv_attention_14_gb300 import workloads as W
 from test_gpu_int4 import Batch
@@ -71,3 +71,21 @@ def test_a_mixed_step_and_decodes_share_a_workspace():
         torch.testing.assert_close(out, want, rtol=0, atol=2e-3)  # cut at other places than pa_decode's: its tolerance
         assert torch.equal(many(ws)[0], want_many)
         assert torch.equal(four(ws)[0], want4)
+
+
+def test_one_workspace_for_balanced_prefills_of_different_shapes():
+    B.pa_test_prefill_schedule(1)
+    try:
+        bs = [W.random_prefill(20, [64, 200], [3000, 2500], 32, 8, 128, device=DEV, poison=True),
+              W.random_prefill(21, [300] * 12, [900] * 12, 32, 8, 128, device=DEV, poison=True),
+              W.random_prefill(22, [512], [8000], 32, 8, 128, device=DEV, poison=True),
+              W.random_prefill(23, [90] * 40, [400] * 40, 32, 8, 128, kv_dtype=W.KV_FP8, device=DEV, poison=True)]
+        caches = [gpu_caches(b) for b in bs]
+        sizes = [prefill_workspace(b) for b in bs]
+        own = [gpu_prefill(b, caches=c, workspace=w) for b, c, w in zip(bs, caches, sizes)]
+        ws = torch.zeros(max(w.numel() for w in sizes), dtype=torch.uint8, device=DEV)
+        for i in (0, 1, 2, 3, 1, 0, 3, 2, 1):
+            out, lse = gpu_prefill(bs[i], caches=caches[i], workspace=ws)
+            assert torch.equal(out, own[i][0]) and torch.equal(lse, own[i][1]), i
+    finally:
+        B.pa_test_prefill_schedule(0)
