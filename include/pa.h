@@ -132,7 +132,8 @@ typedef enum {
  * of a block and kv head holds
  *   uint8 codes[16][head_dim / 2]        the code of an even dim in the low half
  *   fp16  pairs[16][head_dim / 64][2]    (scale, minimum) of each 64 dims
- * of its 16 rows.  A dim reads as scale * code + minimum.  pa_cache_write
+ * of its 16 rows.  A dim reads as scale * code + minimum (the readers take
+ * finite scales of either sign).  pa_cache_write
  * stores, for the 64 dims x of a group, minimum = fp16(min x), scale =
  * fp16((max x - min x) / 15) and codes clamp(rint((x - minimum) * (1 / scale)),
  * 0, 15), in fp32 arithmetic rounded to nearest even; a group with a value

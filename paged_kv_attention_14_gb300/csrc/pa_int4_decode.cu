@@ -677,10 +677,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
       }
 
       // the running maximum is raised only when a score passes it by 2^8, and
-      // kexp lowered only when a scale needs it: a vote, no shuffles
-      float smax = fmaxf(fmax3(vs[0][0][0], vs[0][1][0], vs[1][0][0]), vs[1][1][0]);
+      // kexp lowered only when a scale needs it: a vote, no shuffles.  (Pages from
+      // elsewhere may have scales of either sign.)
+      auto mag = [&](int tt, int i, int p) { return fabsf(vs[tt][i][p]); };
+      float smax = fmaxf(fmax3(mag(0, 0, 0), mag(0, 1, 0), mag(1, 0, 0)), mag(1, 1, 0));
       if constexpr (NG == 2)
-        smax = fmax3(fmax3(smax, vs[0][0][NG - 1], vs[0][1][NG - 1]), vs[1][0][NG - 1], vs[1][1][NG - 1]);
+        smax = fmax3(fmax3(smax, mag(0, 0, 1), mag(0, 1, 1)), mag(1, 0, 1), mag(1, 1, 1));
       bool raise = smax * kap > 128.f;
       float xmax[NR][2];
 #pragma unroll
