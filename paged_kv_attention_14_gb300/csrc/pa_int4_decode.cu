@@ -25,7 +25,10 @@
 // (outputs).  The queries are used in fp16, scaled by a power of two so that
 // their largest is in [1, 2): exact for bf16 and fp16 down to 2^-10 of the
 // largest, 2^-21 of it below.  The weights times the scales go in as a hi + lo
-// pair of fp16 (22 bits).  Scores are keys (16 rows) times queries (8 columns),
+// pair of fp16, times a power of two per query and group of dims that follows the
+// largest such product so far: 22 bits down to 2^-18 of it, 2^-29 of it below.
+// (One power of two for a warp's piece, from the largest scale, loses groups and
+// tokens of small scales beside large ones, and is 2 to 3% faster.)  Scores are keys (16 rows) times queries (8 columns),
 // outputs are values (16 dims) times weights (8 columns); with up to 4 query
 // heads per kv head the columns of queries 4..7 take the lo halves, with more
 // there is a product for each half.
@@ -214,6 +217,8 @@ __device__ __forceinline__ void store_row(const Args &a, int64_t row, float ref,
   o.store(a.out + row * D + lane * (D / 32), l == 0.f ? 0.f : 1.f / l);
   if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
 }
+constexpr float kNone = 3e38f;  // minus a running maximum that there is not yet
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 __device__ __forceinline__ float weight_of(float2 ml, float ref) {
   return ml.x == -INFINITY ? 0.f * ml.y : ex2_approx(ml.x - ref);  // (a NaN stays one)
 }
@@ -506,7 +511,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
 
     // per lane: its part of query gq's dims, and the rest of queries 2 t, 2 t + 1
     uint32_t qf[NR][D / 16][2];
-    float cs_[NR][2], cm[NR][NG][2], M[NR][2], l[NR][2], mz[NR][NG][2];
+    float cs_[NR][2], cm[NR][NG][2], l[NR][2], mz[NR][NG][2];
+    // Weights are 2^(x - M + k) with the running maximum M: k, per query and group
+    // of dims, brings the largest weight times scale to about 2^4 (in fp16 the
+    // hi + lo pair then has 22 bits down to 2^-18 of that, and 2^-29 of it below).
+    // shift = k - M of group 0; rat = 2^(k - its k) of group 1; lim = 2^(7 - k).
+    float shift[NR][2], lim[NR][2], rat[NR][2];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       float amax = 0.f, sum[NG];
@@ -554,7 +564,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
           cm[r][p][c] = a.qscale * __shfl_sync(0xffffffffu, sum[p], 8 * t + 4 * c);
           mz[r][p][c] = 0.f;
         }
-        M[r][c] = -INFINITY;
+        shift[r][c] = kNone;
+        lim[r][c] = 128.f;
+        rat[r][c] = 1.f;
         l[r][c] = 0.f;
       }
     }
@@ -571,16 +583,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
       }
       if constexpr (kAhead) ask_queries(nseq, nh);
     }
-    // weights are 2^(x - M + kexp): kexp keeps weight * scale within fp16
-    float kexp = 60.f, kap = 1152921504606846976.f;  // 2^60
-    float shift[NR][2], high[NR][2];                 // kexp - M, and the score that raises M
-#pragma unroll
-    for (int r = 0; r < NR; ++r)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        shift[r][c] = kexp;
-        high[r][c] = -INFINITY;
-      }
     float sum[NR][NG][4][4];  // [queries 0..7, 8..15][group][16 dims]
 #pragma unroll
     for (int r = 0; r < NR; ++r)
@@ -676,43 +678,57 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
           }
       }
 
-      // the running maximum is raised only when a score passes it by 2^8, and
-      // kexp lowered only when a scale needs it: a vote, no shuffles.  (Pages from
+      // M and the k are set anew only when a weight passes 2^8 or a product of
+      // weight and scale 2^15: a vote, no shuffles.  (The bound taken here is the
+      // largest weight times the largest scale of a lane's tokens.  Pages from
       // elsewhere may have scales of either sign.)
       auto mag = [&](int tt, int i, int p) { return fabsf(vs[tt][i][p]); };
-      float smax = fmaxf(fmax3(mag(0, 0, 0), mag(0, 1, 0), mag(1, 0, 0)), mag(1, 1, 0));
-      if constexpr (NG == 2)
-        smax = fmax3(fmax3(smax, mag(0, 0, 1), mag(0, 1, 1)), mag(1, 0, 1), mag(1, 1, 1));
-      bool raise = smax * kap > 128.f;
-      float xmax[NR][2];
+      float smax[NG];
+#pragma unroll
+      for (int p = 0; p < NG; ++p) smax[p] = fmaxf(fmax3(mag(0, 0, p), mag(0, 1, p), mag(1, 0, p)), mag(1, 1, p));
+      bool raise = false;
+      float w[NR][2][2][2];
+      auto weigh = [&](int r, int c) {
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) w[r][tt][i][c] = ex2_approx(x[r][tt][i][c] + shift[r][c]);
+      };
 #pragma unroll
       for (int r = 0; r < NR; ++r)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          xmax[r][c] = fmaxf(fmax3(x[r][0][0][c], x[r][0][1][c], x[r][1][0][c]), x[r][1][1][c]);
-          raise |= xmax[r][c] > high[r][c];
+          weigh(r, c);
+          const float u = NG == 2 ? fmax3(smax[0], smax[NG - 1] * rat[r][c], lim[r][c]) : fmaxf(smax[0], lim[r][c]);
+          raise |= fmaxf(fmax3(w[r][0][0][c], w[r][0][1][c], w[r][1][0][c]), w[r][1][1][c]) * u > 32768.f;
         }
       if (__any_sync(0xffffffffu, raise)) {
-        smax = warp_max_xor(smax, 1, 32);
-        float nk = kexp;
-        if (smax * kap > 128.f) {
-          int e = static_cast<int>(__float_as_uint(smax) >> 23) - 127;  // smax in [2^e, 2^(e + 1))
-          e = e > 16 ? 16 : e;
-          nk = static_cast<float>(4 - e);
-          kap = __uint_as_float(static_cast<uint32_t>(127 + 4 - e) << 23);
-        }
 #pragma unroll
         for (int r = 0; r < NR; ++r)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const float m = fmaxf(M[r][c], warp_max_xor(xmax[r][c], 4, 32));
-            const float alpha = M[r][c] == -INFINITY ? 0.f : ex2_approx((M[r][c] - m) + (nk - kexp));
-            M[r][c] = m;
-            shift[r][c] = nk - (m == -INFINITY ? 0.f : m);
-            high[r][c] = m + 8.f;
-            l[r][c] *= alpha;
+            float k[2], n[2];  // of the groups, before and after
+            k[0] = static_cast<float>(134 - static_cast<int>(__float_as_uint(lim[r][c]) >> 23));
+            k[1] = k[0] + static_cast<float>(static_cast<int>(__float_as_uint(rat[r][c]) >> 23) - 127);
+            const float xmax = fmaxf(fmax3(x[r][0][0][c], x[r][0][1][c], x[r][1][0][c]), x[r][1][1][c]);
+            const float m0 = k[0] - shift[r][c], m = fmaxf(m0, warp_max_xor(xmax, 4, 32));
 #pragma unroll
             for (int p = 0; p < NG; ++p) {
+              // the largest weight times scale so far (within one binary place
+              // per raise, from k) and of these tokens, relative to m
+              float top = -INFINITY;
+#pragma unroll
+              for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) top = fmaxf(top, x[r][tt][i][c] + __log2f(mag(tt, i, p)));
+              top = fmaxf(warp_max_xor(top, 4, 32) - m, (m0 - m) + (4.f - k[p]));
+              n[p] = fminf(fmaxf(ceilf(4.f - top), -40.f), 60.f);
+            }
+            const float to = n[0] - m;
+#pragma unroll
+            for (int p = 0; p < NG; ++p) {
+              const float alpha = ex2_approx((to - shift[r][c]) + ((n[p] - n[0]) - (k[p] - k[0])));
+              if (p == 0) l[r][c] *= alpha;
               mz[r][p][c] *= alpha;
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
@@ -720,8 +736,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
                 sum[r][p][j][2 + c] *= alpha;
               }
             }
+            shift[r][c] = to;
+            lim[r][c] = power_of_two(7 - static_cast<int>(n[0]));
+            if constexpr (NG == 2) rat[r][c] = power_of_two(static_cast<int>(n[1] - n[0]));
+            weigh(r, c);
           }
-        kexp = nk;
       }
 
       float acc[NR][NG][4][4];  // the stage's products
@@ -735,15 +754,17 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
         for (int r = 0; r < NR; ++r)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float w0 = ex2_approx(x[r][tt][i][0] + shift[r][0]), w1 = ex2_approx(x[r][tt][i][1] + shift[r][1]);
+            const float w0 = w[r][tt][i][0], w1 = w[r][tt][i][1];
             l[r][0] += w0;
             l[r][1] += w1;
 #pragma unroll
             for (int p = 0; p < NG; ++p) {
-              mz[r][p][0] = fmaf(w0, vm[tt][i][p], mz[r][p][0]);
-              mz[r][p][1] = fmaf(w1, vm[tt][i][p], mz[r][p][1]);
+              const float2 u = p == 0 ? make_float2(w0, w1)
+                                      : f2_unpack(f2_mul(f2_pack(w0, w1), f2_pack(rat[r][0], rat[r][1])));
+              mz[r][p][0] = fmaf(u.x, vm[tt][i][p], mz[r][p][0]);
+              mz[r][p][1] = fmaf(u.y, vm[tt][i][p], mz[r][p][1]);
               const float sv = i == 0 ? vs[tt][i][p] : -vs[tt][i][p];
-              const float y0 = w0 * sv, y1 = w1 * sv;
+              const float y0 = u.x * sv, y1 = u.y * sv;
               const uint32_t h = pack_f16x2(y0, y1);
               const float2 hf = halves(h);
               if constexpr (NQ == 4) {  // the lo halves in the columns of queries 4..7 (y - 0 h is y)
@@ -809,7 +830,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) z[p] += __shfl_xor_sync(0xffffffffu, z[p], o);
         }
-        const float ref = M[r][c] == -INFINITY ? -INFINITY : M[r][c] - kexp;
+        const float ref = shift[r][c] == kNone ? -INFINITY : -shift[r][c];
         const float inv = !whole ? 1.f : lsum == 0.f ? 0.f : 1.f / lsum;
         if (gq == 0 && has) {
           if (!whole)
@@ -819,17 +840,19 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
         }
 #pragma unroll
         for (int p = 0; p < NG; ++p) {
-          // 2^24 for the codes' place in fp16, a sixteenth of it for the odd dims
+          // 2^22 for the codes' place in fp16, a sixteenth of it for the odd dims;
+          // 1 / rat
+          const float by = p == 0 ? inv : inv * __uint_as_float((254u << 23) - __float_as_uint(rat[r][c]));
           float o[8];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            float e = sum[r][p][j][c], f = sum[r][p][j][2 + c];
+            float e = sum[r][p][j][c], d = sum[r][p][j][2 + c];
             if constexpr (NQ == 4) {  // the lo halves, from the columns of queries 4..7
               e += __shfl_xor_sync(0xffffffffu, e, 2);
-              f += __shfl_xor_sync(0xffffffffu, f, 2);
+              d += __shfl_xor_sync(0xffffffffu, d, 2);
             }
-            o[2 * j] = fmaf(e, static_cast<float>(1 << kCodeExp), z[p]) * inv;
-            o[2 * j + 1] = fmaf(f, static_cast<float>(1 << (kCodeExp - 4)), z[p]) * inv;
+            o[2 * j] = fmaf(e, static_cast<float>(1 << kCodeExp), z[p]) * by;
+            o[2 * j + 1] = fmaf(d, static_cast<float>(1 << (kCodeExp - 4)), z[p]) * by;
           }
           if (has) {
             float4 *to = reinterpret_cast<float4 *>(dst + query * D + 64 * p + 8 * gq);

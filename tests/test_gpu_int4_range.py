@@ -43,3 +43,67 @@ def test_scales_of_either_sign(hq, hkv, d, which):
     want, wlse = b.want()
     torch.testing.assert_close(out, want, rtol=0, atol=TOL * b.vmax)
     torch.testing.assert_close(lse, wlse, rtol=0, atol=TOL)
+
+
+def _size(b):
+    """[sequences, heads, groups]: per group of 64 dims, the sum over the tokens of weight x (15 |scale| + |minimum|)."""
+    d, hkv = b.d, b.kc.shape[1]
+    S, hq, _ = b.q.shape
+    size = torch.zeros((S, hq, d // 64), dtype=torch.float64)
+    for s in range(S):
+        L = int(b.lens[s])
+        if L == 0:
+            continue
+        at = b.tables[s, :(L + 15) // 16].long()
+        k = ref.rows_of(b.kc[at], d).permute(1, 0, 2, 3).reshape(hkv, -1, d)[:, :L]
+        p = _pairs(b.vc, d)[at].double().permute(1, 0, 2, 3, 4).reshape(hkv, -1, d // 64, 2)[:, :L].abs()
+        x = b.q[s].double().view(hkv, hq // hkv, d) @ k.transpose(1, 2) * b.scale
+        size[s] = (torch.softmax(x, -1) @ (15 * p[..., 0] + p[..., 1])).reshape(hq, -1)
+    return size
+
+
+def _check(b):
+    """Each group of an output within 5e-5 of the sum of its terms' magnitudes: the weights' 2^-15.5 (test_gpu_int4), and
+    for products of weight and scale far below the largest seen 2^-29 of that for each of at most 2^13 tokens: 2^-16."""
+    out, lse = _run(b)
+    want, wlse = b.want()
+    off = (out - want).abs().unflatten(-1, (-1, 64)).amax(-1)
+    tol = TOL * _size(b)
+    assert (off <= tol).all(), f"off by {float((off / tol.clamp(min=1e-300)).max()):.2f} of the bound"
+    torch.testing.assert_close(lse, wlse, rtol=0, atol=TOL)
+    assert int(b.word) == 0
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (16, 2), (16, 1)])
+@pytest.mark.parametrize("kind", [pa.PA_KV_INT4, pa.PA_KV_INT4_F16])
+@pytest.mark.parametrize("big", [0, 1])
+def test_groups_with_scales_far_apart(hq, hkv, kind, big):
+    b = Batch([700, 33, 2500, 1], hq, hkv, 128, kind, seed=22)
+    p = _pairs(b.vc, 128)
+    p[..., big, :] *= 2.0 ** 13
+    p[..., 1 - big, :] *= 2.0 ** -10
+    _check(b)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (8, 1, 64), (16, 1, 128)])
+@pytest.mark.parametrize("at", [0, 5, 300])
+@pytest.mark.parametrize("low", [-20.0, -1.0])
+def test_a_token_of_large_values_that_hardly_counts(hq, hkv, d, at, low):
+    b = Batch([700, 1100], hq, hkv, d, pa.PA_KV_INT4, seed=23, vscale=1e-3)
+    b.q = b.q.abs()
+    for s in range(2):
+        block, row = int(b.tables[s, at // 16]), at % 16
+        _pairs(b.kc, d)[block, :, row] = torch.tensor([0.0, low]).half()
+        _pairs(b.vc, d)[block, :, row] *= 2.0 ** 20
+    assert torch.isfinite(ref.rows_of(b.vc, d)[b.tables[0, 0]]).all()
+    _check(b)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (8, 1, 64), (16, 1, 128), (4, 4, 64)])
+@pytest.mark.parametrize("lens", [[900, 31, 0, 5], [8000]])
+def test_scales_of_any_size_in_any_order(hq, hkv, d, lens):
+    b = Batch(lens, hq, hkv, d, pa.PA_KV_INT4, seed=24, qscale=4.0)  # (scores of magnitude 20)
+    g = torch.Generator().manual_seed(25)
+    p = _pairs(b.vc, d)
+    p *= torch.exp2(torch.randint(-11, 12, (*p.shape[:-1], 1), generator=g).float()).half()
+    _check(b)
