@@ -424,7 +424,8 @@ PA_API pa_status pa_prefill_chunk(const pa_kv_desc *desc, float *out, float *lse
  *   lse  : optional [num_tokens][num_q_heads] fp32, natural log.
  *   query_start_loc : int32 [num_seqs + 1], non-decreasing, within [0,
  *          num_tokens].  Rows outside every prompt are not written.
- *   max_q_len : an upper bound of the prompts' lengths (host value).
+ *   max_q_len : an upper bound of the prompts' lengths, at most num_tokens
+ *          (host value).
  * Scores and sums in fp32, the weights rounded to the activation type for the
  * product with v, one rounding of the result.  A row of v that is not finite
  * reaches the tokens that see it and no others.

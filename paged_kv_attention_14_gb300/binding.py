@@ -656,7 +656,8 @@ def pa_prompt_attention(desc: PaKvDesc, out, q, k, v, query_start_loc, max_q_len
     """Causal attention of packed prompts from their rows: q ``[T, Hq, D]``, k
     and v ``[T, Hkv, D]`` (slices of one projection's output, say) -> out ``[T,
     Hq, D]``, dense, in the activation type (lse ``[T, Hq]`` fp32).
-    ``query_start_loc``: int32 ``[S + 1]``."""
+    ``query_start_loc``: int32 ``[S + 1]``; ``max_q_len``: any upper bound of the
+    prompts' lengths (a model's longest, say)."""
     act, = _act(desc)
     T, hq, hkv, d = q.shape[0], desc.num_q_heads, desc.num_kv_heads, desc.head_dim
     qp, qs = _rows(q, act, T, hq, d, "q")
@@ -671,7 +672,7 @@ def pa_prompt_attention(desc: PaKvDesc, out, q, k, v, query_start_loc, max_q_len
     dev = q.get_device()
     _check(load().pa_prompt_attention(ctypes.byref(desc), op, None if lse is None else _at(lse, _F32, "lse", dev), qp,
                                       qs, kp, ks, vp, vs, _at(query_start_loc, _I32, "query_start_loc", dev),
-                                      query_start_loc.shape[0] - 1, T, int(max_q_len), float(scale), st))
+                                      query_start_loc.shape[0] - 1, T, min(int(max_q_len), T), float(scale), st))
 
 
 def pa_prefill_workspace_size(desc: PaKvDesc, num_seqs: int, max_q_len: int) -> int:
