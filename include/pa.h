@@ -704,7 +704,8 @@ PA_API pa_status pa_copy_blocks(const pa_kv_desc *desc, void *k_cache, void *v_c
  * Pages of a 4-bit cache to 16 bits: for every i < num_pairs, block
  * dst_blocks[i] of k_out and v_out receives the values of block src_blocks[i]
  * of k_cache and v_cache (every kv head and slot), each scale * code + minimum
- * rounded once to the activation type.  k_out and v_out are caches of
+ * rounded once to the activation type; what passes fp16's largest value by the
+ * scale's rounding becomes that value (PA_KV_INT4_F16).  k_out and v_out are caches of
  * num_out_blocks blocks in that type (PA_KV_BF16; PA_KV_F16 for
  * PA_KV_INT4_F16), so a chunk that follows a 4-bit prefix is attended by
  * pa_prefill_chunk over the widened pages.  A src may repeat.

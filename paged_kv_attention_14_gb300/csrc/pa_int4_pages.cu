@@ -143,6 +143,13 @@ __device__ __forceinline__ uint4 widen8dims(uint32_t w, uint32_t pair) {
     const float a = __uint_as_float(0x4B000000u | ((w >> (8 * i)) & 15u)) - 8388608.f;
     const float b = __uint_as_float(0x4B000000u | ((w >> (8 * i + 4)) & 15u)) - 8388608.f;
     r[i] = F16 ? pack_f16x2(fmaf(s, a, m), fmaf(s, b, m)) : pack_bf16x2(fmaf(s, a, m), fmaf(s, b, m));
+    if constexpr (F16) {
+      // the scale's rounding may carry the top of a group past fp16's largest
+      __half2 h = *reinterpret_cast<const __half2 *>(&r[i]);
+      const __half2 top = __half2half2(__ushort_as_half(0x7BFF));
+      h = __hmax2_nan(__hmin2_nan(h, top), __hneg2(top));
+      r[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
   }
   return make_uint4(r[0], r[1], r[2], r[3]);
 }

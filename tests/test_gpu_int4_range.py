@@ -107,3 +107,21 @@ def test_scales_of_any_size_in_any_order(hq, hkv, d, lens):
     p = _pairs(b.vc, d)
     p *= torch.exp2(torch.randint(-11, 12, (*p.shape[:-1], 1), generator=g).float()).half()
     _check(b)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_widened_fp16_pages_of_the_largest_values_stay_finite(d):
+    # 65504 + 65504 in 15 steps: the scale rounds to 8736, the top reads as 65536
+    x = torch.zeros((2, 1, 16, d), dtype=torch.float16)
+    x[..., 0::64], x[..., 1::64], x[..., 2::64] = -65504.0, 65504.0, 100.0
+    x[1] = -x[1]
+    x[1, 0, 3, 5] = float("nan")
+    cache = ref.cache_of(x)
+    assert ref.rows_of(cache, d).nan_to_num(0.0).max() == 65536.0
+    ids = torch.arange(2, dtype=torch.int32, device=DEV)
+    ko, vo = [torch.zeros((2, 1, 16, d), dtype=torch.float16, device=DEV) for _ in range(2)]
+    pa.pa_widen_blocks(pa.make_desc(2, 1, 1, d, pa.PA_KV_INT4_F16), cache.to(DEV), cache.to(DEV), ids, ko, vo, ids)
+    want = ref.rows_of(cache, d).clamp(-65504.0, 65504.0).half()  # (a NaN stays one)
+    for got in (ko.cpu(), vo.cpu()):
+        assert torch.equal(got.isnan(), want.isnan()) and bool(want.isnan().any())
+        assert torch.equal(got.nan_to_num(0.0), want.nan_to_num(0.0))
