@@ -27,7 +27,7 @@
  *   block_tables     : int32 [num_seqs][max_blocks_per_seq], physical block
  *                      id of each logical block of each sequence
  *   context_lens     : int32 [num_seqs], KV tokens of each sequence including
- *                      the ones written this step
+ *                      the ones written this step (at most 2^31 - 16)
  *   slot_mapping     : int64 [num_tokens], slot = block * block_size + offset;
  *                      a negative slot means "skip this token"
  * Query head h attends kv head h / (num_q_heads / num_kv_heads).

@@ -160,7 +160,7 @@ __device__ __forceinline__ void report(const DecodeArgs &a, int bits) { report_e
 // capacity (and reported when outside it).
 __device__ __forceinline__ int seq_len(const DecodeArgs &a, int s) {
   const int L = __ldg(a.context_lens + s);
-  return a.checked ? checked_len(L, a.max_blocks_per_seq * 16, a.err, a.user_err) : L;
+  return a.checked ? checked_len(L, table_tokens(a.max_blocks_per_seq), a.err, a.user_err) : L;
 }
 
 // ---------------------------------------------------------------- workspace

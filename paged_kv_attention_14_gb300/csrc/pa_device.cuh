@@ -61,6 +61,9 @@ __device__ __forceinline__ int checked_block(int phys, int num_blocks, int32_t *
   return phys;
 }
 
+// The tokens that a table of so many blocks holds; lengths end at 2^31 - 16.
+__device__ __forceinline__ int table_tokens(int blocks) { return min(blocks, 0x7ffffff) * 16; }
+
 // Checked mode: a context length must lie in [0, max_len] (max_len = the
 // table's max_blocks_per_seq * 16).  A length outside is reported and
 // clamped into the range.

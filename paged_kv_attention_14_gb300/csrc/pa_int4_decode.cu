@@ -161,7 +161,7 @@ struct Span {
 };
 __device__ __forceinline__ Span span_of(const Args &a, int raw) {
   Span s;
-  s.len = a.checked ? checked_len(raw, a.max_blocks * 16, a.err, a.user_err) : raw;
+  s.len = a.checked ? checked_len(raw, table_tokens(a.max_blocks), a.err, a.user_err) : raw;
   if (s.len <= 0) {
     s.len = s.first = s.b0 = s.nb = 0;
     return s;
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::W * 32, 1) int4_decode_kernel(cons
             vm[tt][i][p] = i == 0 ? g.y : fmaf(15.f, g.x, g.y);
           }
         }
-      if (n < 2 || pos0 < csp.first || pos0 + 32 > csp.len) {
+      if (n < 2 || pos0 < csp.first || csp.len - pos0 < 32) {
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt)
 #pragma unroll

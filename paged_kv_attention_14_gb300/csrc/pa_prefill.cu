@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(NW * 32, 1) prefill_kernel(const PrefillArgs a
   if (a.checked) {
     // lengths within the table's capacity; a chunk no longer than its context
     // nor than the launch's query tiles; rows start at a row >= 0
-    L = checked_len(L, a.max_blocks_per_seq * 16, a.err, nullptr);
+    L = checked_len(L, table_tokens(a.max_blocks_per_seq), a.err, nullptr);
     q_len = checked_len(q_len, a.prefix_mode ? static_cast<int>(gridDim.x) * a.qt
                                              : min(L, static_cast<int>(gridDim.x) * a.qt), a.err, nullptr);
     if (qs < 0) {

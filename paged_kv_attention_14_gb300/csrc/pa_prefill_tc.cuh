@@ -196,7 +196,7 @@ __device__ __forceinline__ bool item_range(const Args &a, int s, int split, int 
     // lengths within the table's capacity; a chunk no longer than its context
     // nor than the launch's query tiles; rows start at a row >= 0
     int32_t *e1 = report ? a.err : nullptr, *e2 = report ? a.ws_err : nullptr;
-    r.L = checked_len(r.L, a.max_blocks_per_seq * 16, e1, e2);
+    r.L = checked_len(r.L, table_tokens(a.max_blocks_per_seq), e1, e2);
     r.q_len = checked_len(r.q_len, a.prefix_mode ? gx * a.qt : min(r.L, gx * a.qt), e1, e2);
     if (r.qs < 0) {
       if (report && threadIdx.x == 0) report_error(a.err, a.ws_err, kErrBadIndex);
