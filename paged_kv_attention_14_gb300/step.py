@@ -219,10 +219,11 @@ class MixedStep:
                 q_rot=None, k_rot=None):
         """Whole prompts: the attention of packed rows q [T, Hq, D], k and v [T,
         Hkv, D] into ``out`` [T, Hq, D] (the activation type), and their keys
-        and values into the cache at ``slot_mapping`` [T] (None: not written;
-        v is then free to be a slice of a projection's output, else it is
-        dense).  With ``rope`` (binding.make_rope) q and k are normed and rotated
-        at ``positions`` [T] first, into ``q_rot`` and ``k_rot``."""
+        and values into the cache at ``slot_mapping`` [T] (None: not written).
+        With ``rope`` (binding.make_rope) q and k are normed and rotated at
+        ``positions`` [T] first, into ``q_rot`` and ``k_rot``.  All may be slices
+        of a projection's output, except what the cache write takes: with a
+        ``slot_mapping`` v is dense, and without ``rope`` k as well."""
         if rope is not None:
             B.pa_qk_norm_rope(self.desc, rope, q_rot, k_rot, q, k, positions)
             q, k = q_rot, k_rot

@@ -24,3 +24,25 @@ def test_any_bound_of_the_lengths(longest):
     kc, vc = [torch.zeros((8, hkv, 16, d), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
     MixedStep(desc, kc, vc, 1 / math.sqrt(d)).prompts(again, q, k, v, starts, longest)
     assert torch.equal(again, out)
+
+
+def test_what_a_step_of_prompts_writes_is_dense():
+    lens, hq, hkv, d = [20, 12], 4, 2, 64
+    q, k, v, starts = _rows(lens, hq, hkv, d, torch.bfloat16, 2)  # slices of a projection
+    kc, vc = [torch.zeros((4, hkv, 16, d), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    step = MixedStep(pa.make_desc(4, hkv, hq, d), kc, vc, 0.125)
+    slots = torch.arange(32, device=DEV)
+    out, want = [torch.zeros((32, hq, d), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    for bad in ((k, v.contiguous()), (k.contiguous(), v)):
+        with pytest.raises(ValueError, match="contiguous"):
+            step.prompts(out, q, *bad, starts, 20, slots)
+    step.prompts(want, q, k, v, starts, 20)
+    step.prompts(out, q, k.contiguous(), v.contiguous(), starts, 20, slots)
+    assert torch.equal(out, want)
+    assert torch.equal(kc.transpose(1, 2).reshape(64, hkv, d)[:32], k)
+    # rotated, only v has to be dense
+    rot = [torch.empty((32, h, d), dtype=torch.bfloat16, device=DEV) for h in (hq, hkv)]
+    pos = torch.arange(32, dtype=torch.int32, device=DEV)
+    step.prompts(out, q, k, v.contiguous(), starts, 20, slots, rope=pa.make_rope(pa.rope_table(64, d)), positions=pos,
+                 q_rot=rot[0], k_rot=rot[1])
+    assert torch.equal(kc.transpose(1, 2).reshape(64, hkv, d)[:32], rot[1])
