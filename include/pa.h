@@ -427,12 +427,17 @@ PA_API pa_status pa_prefill_chunk(const pa_kv_desc *desc, float *out, float *lse
  *   max_q_len : an upper bound of the prompts' lengths, at most num_tokens
  *          (host value).
  * Scores and sums in fp32, the weights rounded to the activation type for the
- * product with v, one rounding of the result.  A row of v that is not finite
- * reaches the tokens that see it and no others.
- * Uses desc's heads, head_dim, kv_dtype (for the activation type), local
- * attention, error_word and check_indices (query_start_loc out of range or
- * order, or a prompt longer than max_q_len, is reported and that prompt left
- * out or cut).  num_seqs, num_tokens or max_q_len == 0 enqueues nothing.
+ * product with v, one rounding of the result.  (pa_prefill_chunk keeps 11 bits
+ * of them or a pair.)  With prefill_impl PA_PREFILL_TCGEN05_PAIR or
+ * PA_PREFILL_MMA_SYNC the weights are a hi + lo pair of the activation type,
+ * for more tensor work.  A row of v that is not finite reaches the tokens that
+ * see it and no others.
+ * Uses desc's heads, head_dim, kv_dtype (for the activation type),
+ * prefill_impl (for the weights), local attention, error_word and
+ * check_indices (query_start_loc out of range or order, or a prompt longer than
+ * max_q_len, is reported and that prompt left out or cut; what the others then
+ * get is meaningless too).  num_seqs, num_tokens or max_q_len == 0 enqueues
+ * nothing.
  */
 PA_API pa_status pa_prompt_attention(const pa_kv_desc *desc, void *out, float *lse, const void *q, int64_t q_stride,
                                      const void *k, int64_t k_stride, const void *v, int64_t v_stride,

@@ -657,7 +657,8 @@ def pa_prompt_attention(desc: PaKvDesc, out, q, k, v, query_start_loc, max_q_len
     and v ``[T, Hkv, D]`` (slices of one projection's output, say) -> out ``[T,
     Hq, D]``, dense, in the activation type (lse ``[T, Hq]`` fp32).
     ``query_start_loc``: int32 ``[S + 1]``; ``max_q_len``: any upper bound of the
-    prompts' lengths (a model's longest, say)."""
+    prompts' lengths (a model's longest, say).  ``prefill_impl`` PA_PREFILL_TCGEN05_PAIR
+    or PA_PREFILL_MMA_SYNC of the descriptor: softmax weights as a hi + lo pair."""
     act, = _act(desc)
     T, hq, hkv, d = q.shape[0], desc.num_q_heads, desc.num_kv_heads, desc.head_dim
     qp, qs = _rows(q, act, T, hq, d, "q")

@@ -19,7 +19,12 @@
 // tensor memory.  The tensor cores work on one tile while the other's softmax
 // runs.  The running maximum is raised only when it grows by 2^8 (O is then
 // rescaled in tensor memory), sums are fp32 of the unrounded weights.  P in 16
-// bits is off by half a step of the type that the output is rounded to as well.
+// bits is off by half a step of the type that the output is rounded to as well:
+// outputs are off by 1.3 times what their own rounding costs (16384 tokens, bf16,
+// against 64 bits: 2.1e-3 of their norm, 1.6e-3 with exact weights).  As a hi +
+// lo pair, the low half in the columns of S beside the high half's, P costs
+// nothing more of that but half as many products again: 1.88 ms for 1.26 (five
+// prompts of 256 to 2048: 83 us for 65).  The caller's choice (prefill_impl).
 //
 // A weight of zero does not cancel an infinity or a NaN: in the V tiles that
 // some row sees in part, rows behind the keys in use are zeroed, and a row with
@@ -274,7 +279,8 @@ __device__ __noinline__ void store_noted(const Args &a, const uint32_t *notes, c
   }
 }
 
-template <int D, bool F16, int NQT>
+// PAIR: the weights go to the products as a hi + lo pair.
+template <int D, bool F16, int NQT, bool PAIR>
 __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt_kernel(const __grid_constant__ Args a) {
   using C = Cfg<D, NQT>;
   constexpr int KVT = F16 ? kKvF16 : kKvBf16;
@@ -438,6 +444,8 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
             const int kk = half * 4 + i;
             mma_ts(o, p + (kk >> 1) * 32 + (kk & 1) * 8, vd + kk * (2048 >> 4), desc_high(1024), IPV,
                    kk > 0 || acc != 0);
+            if constexpr (PAIR)
+              mma_ts(o, p + (kk >> 1) * 32 + 16 + (kk & 1) * 8, vd + kk * (2048 >> 4), desc_high(1024), IPV, true);
           }
         }
         __syncwarp();
@@ -663,7 +671,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
           uint64_t l2[2] = {0, 0};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            uint32_t p[16];
+            uint32_t p[16], lo[PAIR ? 16 : 1];
 #pragma unroll
             for (int x = 0; x < 16; ++x) {
               const float2 y = f2_unpack(
@@ -671,8 +679,10 @@ __global__ void __launch_bounds__(Cfg<D, NQT>::THREADS, NQT == 2 ? 1 : 2) prompt
               const float e0 = ex2_approx(y.x), e1 = ex2_approx(y.y);
               l2[x & 1] = f2_add(l2[x & 1], f2_pack(e0, e1));
               p[x] = pack16x2<KVT>(e0, e1);
+              if constexpr (PAIR) lo[x] = pack16x2<KVT>(e0 - lo16<KVT>(p[x]), e1 - hi16<KVT>(p[x]));
             }
             tmem_st16_async(trow + t * KT + c * 32, p);
+            if constexpr (PAIR) tmem_st16_async(trow + t * KT + c * 32 + 16, lo);  // (S is in registers)
             if (c & 1) {  // the first 64 keys' products need not wait for the rest
               tmem_wait_st();
               tc_fence_before_sync();
@@ -808,10 +818,10 @@ bool make_rows_map(CUtensorMap *map, const void *base, bool f16, int tokens, int
   return true;
 }
 
-template <int D, bool F16, int NQT>
+template <int D, bool F16, int NQT, bool PAIR>
 cudaError_t launch(Args &a, int max_q_len, cudaStream_t stream) {
   using C = Cfg<D, NQT>;
-  const void *fn = reinterpret_cast<const void *>(&prompt_kernel<D, F16, NQT>);
+  const void *fn = reinterpret_cast<const void *>(&prompt_kernel<D, F16, NQT, PAIR>);
   if (prepare_kernel(fn, C::THREADS, C::SMEM) < 1) return cudaErrorInvalidConfiguration;
   const int qt = NQT * a.rt;
   // by position, the longest key ranges first, unless that leaves too many
@@ -836,10 +846,16 @@ cudaError_t launch(Args &a, int max_q_len, cudaStream_t stream) {
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
-template <int D, bool F16>
+template <int D, bool F16, bool PAIR>
 cudaError_t launch_tiles(Args &a, int max_q_len, cudaStream_t stream) {
   // prompts of one tile: a smaller CTA, two to an SM
-  return max_q_len <= a.rt ? launch<D, F16, 1>(a, max_q_len, stream) : launch<D, F16, 2>(a, max_q_len, stream);
+  return max_q_len <= a.rt ? launch<D, F16, 1, PAIR>(a, max_q_len, stream)
+                           : launch<D, F16, 2, PAIR>(a, max_q_len, stream);
+}
+
+template <int D, bool F16>
+cudaError_t launch_weights(Args &a, bool pair, int max_q_len, cudaStream_t stream) {
+  return pair ? launch_tiles<D, F16, true>(a, max_q_len, stream) : launch_tiles<D, F16, false>(a, max_q_len, stream);
 }
 
 }  // namespace
@@ -881,8 +897,13 @@ cudaError_t launch_prompt(const pa_kv_desc &d, void *out, float *lse, const void
   const TestHooks hooks = test_hooks();
   a.stall = hooks.stall;
   a.wait_ns = hooks.wait_ns;
-  if (D == 128) return f16 ? launch_tiles<128, true>(a, max_q_len, stream) : launch_tiles<128, false>(a, max_q_len, stream);
-  return f16 ? launch_tiles<64, true>(a, max_q_len, stream) : launch_tiles<64, false>(a, max_q_len, stream);
+  // the settings whose prefill multiplies by a pair too
+  const bool pair = d.prefill_impl == PA_PREFILL_TCGEN05_PAIR || d.prefill_impl == PA_PREFILL_MMA_SYNC;
+  if (D == 128)
+    return f16 ? launch_weights<128, true>(a, pair, max_q_len, stream)
+               : launch_weights<128, false>(a, pair, max_q_len, stream);
+  return f16 ? launch_weights<64, true>(a, pair, max_q_len, stream)
+             : launch_weights<64, false>(a, pair, max_q_len, stream);
 }
 
 }  // namespace pa
