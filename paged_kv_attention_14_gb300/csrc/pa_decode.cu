@@ -56,23 +56,6 @@ KernelInfo kernel_for(const pa_kv_desc &d, int impl) {
   return dec::pick_mma_fp8(d.head_dim, g, hg);
 }
 
-// cuTensorMapEncodeTiled, fetched from the driver through the runtime
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_tiled() {
-  static EncodeTiledFn fn = [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeTiledFn>(p);
-  }();
-  return fn;
-}
-
 // The cache as TMA sees it.  Rows are (block, kv head, token) triples of
 // head_dim elements; one box is the 16 tokens of HG consecutive kv heads of
 // one block.  Rows of 256 bytes (bf16, head_dim 128) are cut into two

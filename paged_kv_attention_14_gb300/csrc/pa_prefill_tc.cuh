@@ -1143,18 +1143,7 @@ inline bool make_map(CUtensorMap *map, const void *base, const pa_kv_desc &d) {
   const CUtensorMapDataType dt = kv8                      ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                  : d.kv_dtype == PA_KV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                            : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                     const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
-                                     CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                     CUtensorMapFloatOOBfill);
-  static EncodeTiledFn enc = [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeTiledFn>(p);
-  }();
+  const EncodeTiledFn enc = encode_tiled();
   if (!enc) return false;
   thread_local MapCache<> cache;  // the last few caches' maps of this thread
   const MapKey key = map_key(base, d.num_blocks, d.num_kv_heads, D, d.kv_dtype);
@@ -1183,18 +1172,7 @@ inline bool make_new_rows_map(CUtensorMap *map, const void *base, int64_t rows, 
   if ((reinterpret_cast<uintptr_t>(base) & 15) != 0 || rows <= 0) return false;
   const CUtensorMapDataType dt =
       d.kv_dtype == PA_KV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                     const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
-                                     CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                     CUtensorMapFloatOOBfill);
-  static EncodeTiledFn enc = [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeTiledFn>(p);
-  }();
+  const EncodeTiledFn enc = encode_tiled();
   if (!enc) return false;
   thread_local MapCache<> cache;
   const MapKey key = map_key(base, rows, d.num_kv_heads, D, d.kv_dtype, -3);
@@ -1221,18 +1199,7 @@ inline bool make_new_rows_map(CUtensorMap *map, const void *base, int64_t rows, 
 template <int D>
 inline bool make_qmap(CUtensorMap *map, const void *q, int num_q_heads, int g) {
   if ((reinterpret_cast<uintptr_t>(q) & 15) != 0 || g <= 0 || MT % g != 0) return false;
-  using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                     const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
-                                     CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                     CUtensorMapFloatOOBfill);
-  static EncodeTiledFn enc = [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeTiledFn>(p);
-  }();
+  const EncodeTiledFn enc = encode_tiled();
   if (!enc) return false;
   thread_local MapCache<> cache;
   const MapKey key = map_key(q, num_q_heads, D, g, -1);
@@ -1256,18 +1223,7 @@ inline bool make_qmap(CUtensorMap *map, const void *q, int num_q_heads, int g) {
 template <int D>
 inline bool make_omap(CUtensorMap *map, const float *out, int num_q_heads, int g) {
   if ((reinterpret_cast<uintptr_t>(out) & 15) != 0 || g <= 0 || MT % g != 0) return false;
-  using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                     const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
-                                     CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                     CUtensorMapFloatOOBfill);
-  static EncodeTiledFn enc = [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeTiledFn>(p);
-  }();
+  const EncodeTiledFn enc = encode_tiled();
   if (!enc) return false;
   thread_local MapCache<> cache;
   const MapKey key = map_key(out, num_q_heads, D, g, -2);

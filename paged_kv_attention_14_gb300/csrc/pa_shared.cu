@@ -337,21 +337,6 @@ int tile_seqs_of(const pa_kv_desc &d, int32_t max_group_size) {
   return max_group_size < 1 ? 1 : max_group_size > cap ? cap : max_group_size;
 }
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_tiled() {
-  static const EncodeTiledFn enc = [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeTiledFn>(p);
-  }();
-  return enc;
-}
-
 // The cache as TMA sees it.  8-bit: rows of (block, kv head, token) triples, a
 // box is the 16 rows of one block and kv head as they are (they are widened).
 // 16-bit: the rows in groups of 8, each row in halves of 64 columns, a box is
