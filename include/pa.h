@@ -139,6 +139,8 @@ typedef enum {
  * 0, 15), in fp32 arithmetic rounded to nearest even; a group with a value
  * that is not finite, or whose scale or minimum passes fp16 (reported as
  * PA_DEVERR_FP16_RANGE), reads as NaN.
+ * The decode takes its queries to 2^-21 of the largest element of their row
+ * (bf16 and fp16 exactly down to 2^-10 of it), of magnitudes below 2^115.
  * Calls that take it: pa_cache_write, pa_decode, pa_decode_static,
  * pa_decode_workspace_size, pa_widen_blocks, pa_copy_blocks, pa_bind_blocks,
  * pa_release_blocks, and pa_qk_norm_rope and pa_prompt_attention, which take

@@ -33,12 +33,16 @@
 // heads per kv head the columns of queries 4..7 take the lo halves, with more
 // there is a product for each half.
 //
-// Bounded by instructions: a block of a kv head takes a warp about 330 (codes to
-// operands 105, products 16, weights and scales 130, fetching 30), and the SMs
-// issue every second cycle with the two warps a scheduler that the registers
-// allow.  32 sequences of 8192, 32 / 8 heads of 128: 68.5 us, 4.4 TB/s; 128
-// sequences of 1024 to 8192, 40 heads: 152 us.  The smallest call takes 7.5 us:
-// lengths, tables and blocks one after the other from memory, launch, outputs.
+// Bounded by latency at two warps a scheduler, which is what the registers allow:
+// a block of a kv head takes a warp about 335 instructions (codes to operands 105,
+// products 16, weights and scales 135, fetching 30), three quarters of what the
+// SMs could issue while its bytes come at the copy rate, and they issue in 54%
+// of the cycles.  32 sequences of 8192, 32 / 8 heads of 128: 70.3 us, 4.3 TB/s; 128
+// sequences of 1024 to 8192, 40 heads: 157 us.  Farthest from the bytes are 9 to
+// 16 query heads a kv head (32 sequences of 4096, 16 / 1 heads: 22.5 us for 2.8):
+// four products an operand, a ring of two stages, no queries asked for ahead.  The
+// smallest call takes 7.4 us: lengths, tables and blocks one after the other from
+// memory, launch, outputs.
 //
 // The sums of the tensor cores round towards zero, so they run over one stage
 // and are then added to fp32 registers.
@@ -83,8 +87,9 @@ struct Args {
 
 template <int D, int NQ>
 struct Cfg {
-  // warps: what the registers allow without spilling.  64 dims, up to 8 queries:
-  // 12 (128 sequences of 1024 to 8192, 32 / 8 heads: 94 us; 8 warps 103).
+  // warps: what the registers allow without spilling (128 dims and more than 8
+  // queries: 12 words of a lane spill).  64 dims, up to 8 queries: 12 (128
+  // sequences of 1024 to 8192, 32 / 8 heads: 89 us; 8 warps about a tenth more).
   static constexpr int W = D == 64 && NQ <= 8 ? 12 : 8;
   static constexpr int TB = i4::tile_bytes(D);
   static constexpr int STAGE = 4 * TB;  // K and V of two blocks

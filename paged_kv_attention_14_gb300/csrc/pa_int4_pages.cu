@@ -86,9 +86,10 @@ __device__ __forceinline__ uint2 encode16(const uint4 &a, const uint4 &b, uint32
 
 // One thread moves 16 dims of K and of V: 32 bytes read, 8 bytes of codes
 // written; the first of a group's four threads writes its pair.  Bound by the
-// rows' bytes (2 (2 D + 9 D / 16) per token and kv head); the arithmetic is about
-// 4 instructions a dim.  16381 tokens of 8 heads of 128: 17.7 us of a floor of
-// 12.8 (86 MB).
+// issue slots: 16 instructions a dim (68.4 million warp instructions for 65536
+// tokens of 8 heads of 128, issued in 82% of the cycles, the ALU busy in 68%), 1.36
+// times the bytes' time (2 (2 D + 9 D / 16) per token and kv head): 68.7 us of a
+// floor of 51.2; 16381 tokens 17.9 of 12.8 (86 MB).
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) int4_write_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v,
                                                          uint8_t *__restrict__ k_cache, uint8_t *__restrict__ v_cache,
