@@ -133,12 +133,11 @@ typedef enum {
  *   uint8 codes[16][head_dim / 2]        the code of an even dim in the low half
  *   fp16  pairs[16][head_dim / 64][2]    (scale, minimum) of each 64 dims
  * of its 16 rows.  A dim reads as scale * code + minimum (the readers take
- * finite scales of either sign).  pa_cache_write
- * stores, for the 64 dims x of a group, minimum = fp16(min x), scale =
- * fp16((max x - min x) / 15) and codes clamp(rint((x - minimum) * (1 / scale)),
- * 0, 15), in fp32 arithmetic rounded to nearest even; a group with a value
- * that is not finite, or whose scale or minimum passes fp16 (reported as
- * PA_DEVERR_FP16_RANGE), reads as NaN.
+ * finite scales of either sign).  pa_cache_write stores, for the 64 dims x of
+ * a group, minimum = fp16(min x), scale = fp16((max x - min x) / 15) and codes
+ * clamp(rint((x - minimum) * (1 / scale)), 0, 15), in fp32 arithmetic rounded
+ * to nearest even; a group with a value that is not finite, or whose scale or
+ * minimum passes fp16 (reported as PA_DEVERR_FP16_RANGE), reads as NaN.
  * The decode takes its queries to 2^-21 of the largest element of their row
  * (bf16 and fp16 exactly down to 2^-10 of it), of magnitudes below 2^115.
  * Calls that take it: pa_cache_write, pa_decode, pa_decode_static,
@@ -712,8 +711,8 @@ PA_API pa_status pa_copy_blocks(const pa_kv_desc *desc, void *k_cache, void *v_c
  * dst_blocks[i] of k_out and v_out receives the values of block src_blocks[i]
  * of k_cache and v_cache (every kv head and slot), each scale * code + minimum
  * rounded once to the activation type; what passes fp16's largest value by the
- * scale's rounding becomes that value (PA_KV_INT4_F16).  k_out and v_out are caches of
- * num_out_blocks blocks in that type (PA_KV_BF16; PA_KV_F16 for
+ * scale's rounding becomes that value (PA_KV_INT4_F16).  k_out and v_out are
+ * caches of num_out_blocks blocks in that type (PA_KV_BF16; PA_KV_F16 for
  * PA_KV_INT4_F16), so a chunk that follows a 4-bit prefix is attended by
  * pa_prefill_chunk over the widened pages.  A src may repeat.
  *   src_blocks : int32 [num_pairs] in [0, num_blocks); dst_blocks : int32

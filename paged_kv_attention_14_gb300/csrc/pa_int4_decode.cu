@@ -28,10 +28,10 @@
 // pair of fp16, times a power of two per query and group of dims that follows the
 // largest such product so far: 22 bits down to 2^-18 of it, 2^-29 of it below.
 // (One power of two for a warp's piece, from the largest scale, loses groups and
-// tokens of small scales beside large ones, and is 2 to 3% faster.)  Scores are keys (16 rows) times queries (8 columns),
-// outputs are values (16 dims) times weights (8 columns); with up to 4 query
-// heads per kv head the columns of queries 4..7 take the lo halves, with more
-// there is a product for each half.
+// tokens of small scales beside large ones, and is 2 to 4% faster.)  Scores are
+// keys (16 rows) times queries (8 columns), outputs are values (16 dims) times
+// weights (8 columns); with up to 4 query heads per kv head the columns of
+// queries 4..7 take the lo halves, with more there is a product for each half.
 //
 // Bounded by latency at two warps a scheduler, which is what the registers allow:
 // a block of a kv head takes a warp about 335 instructions (codes to operands 105,
